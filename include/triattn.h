@@ -450,6 +450,116 @@ triattn_status triattn_trimul_bwd(const triattn_trimul_shape* shape, const void*
                                   void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Transition: the gated feed-forward block of the pair stack, over M rows of
+ * C features (the pairs of z [B, N, N, C], or any other rows):
+ *
+ *   x       = LayerNorm(z; ln_w, ln_b)   over the C features, eps 1e-5
+ *   [a | b] = x W_in                     W_in [C, 2H]
+ *   h       = act(a) * b
+ *   out     = m * (h W_o)                W_o [H, C], m: optional row mask
+ *
+ * act: TRIATTN_ACT_SILU a sigmoid(a), TRIATTN_ACT_SIGMOID sigmoid(a), or
+ * TRIATTN_ACT_GELU a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) / 2.  No
+ * projection biases; the residual update z + out is left to the caller.  A
+ * row whose mask is 0 is left out: its out and dz are 0 and it takes no part
+ * in any gradient, whatever z and d_out hold there (NaN and infinities
+ * included).  The forward keeps nothing for the backward, which computes x, a
+ * and b again.
+ *
+ * Shape: 0 <= M < 2^31; C a multiple of 32 up to 256; H a multiple of 32 up
+ * to 4096; flags 0 or TRIATTN_FLAG_GRADS_BF16 (the backward's parameter
+ * gradients are BF16, one rounding of the FP32 sums, instead of FP32).
+ * Otherwise TRIATTN_ERR_INVALID_ARG (negative M, non-positive C or H,
+ * activation, flags) or TRIATTN_ERR_UNSUPPORTED; the size query returns 0.
+ * With M = 0 the forward does nothing and the backward zeroes the parameter
+ * gradients; z, mask, out, d_out, dz and the workspace may then be NULL.
+ *
+ * Layouts (device pointers, contiguous row-major, 16-byte aligned, the mask
+ * 2-byte aligned; outputs must not overlap inputs):
+ *   z, dz, out, d_out  [M, C] bf16
+ *   mask               optional [M] bf16, multiplicative, finite
+ *   ln_w, ln_b         [C] fp32
+ *   w_in [C, 2H] bf16, w_o [H, C] bf16
+ *   d_ln_w, d_ln_b [C], d_w_in [C, 2H], d_w_o [H, C]  fp32 or bf16 (flags);
+ *                      overwritten, not accumulated
+ *   workspace  triattn_transition_workspace_bytes(shape, backward) bytes,
+ *              256-byte aligned, contents ignored.
+ *
+ * Bitwise reproducible for a fixed shape and device.  Argument errors
+ * return before anything is launched; a failed launch returns
+ * TRIATTN_ERR_CUDA.
+ */
+#define TRIATTN_ACT_SILU 0
+#define TRIATTN_ACT_SIGMOID 1
+#define TRIATTN_ACT_GELU 2
+#define TRIATTN_FLAG_GRADS_BF16 2u
+
+typedef struct {
+  long long M;    /* rows */
+  int C;          /* features */
+  int H;          /* hidden features */
+  int activation; /* TRIATTN_ACT_* */
+  unsigned flags; /* 0 or TRIATTN_FLAG_GRADS_BF16 */
+} triattn_transition_shape;
+
+size_t triattn_transition_workspace_bytes(const triattn_transition_shape* shape, int backward);
+
+/* Forward: writes out. */
+triattn_status triattn_transition_fwd(const triattn_transition_shape* shape, const void* z, const void* mask,
+                                      const float* ln_w, const float* ln_b, const void* w_in, const void* w_o,
+                                      void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward of <out, d_out>: dz (bf16) and the parameter gradients. */
+triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, const void* z, const void* mask,
+                                      const float* ln_w, const float* ln_b, const void* w_in, const void* w_o,
+                                      const void* d_out, void* dz, void* d_ln_w, void* d_ln_b, void* d_w_in,
+                                      void* d_w_o, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Global norm of a list of n gradient tensors, and clipping by it:
+ *
+ *   norm = sqrt(sum of g^2 over every element)  (TRIATTN_NORM_L2), or
+ *          max |g|                              (TRIATTN_NORM_MAX)
+ *   coef = min(1, max_norm / (norm + 1e-6))
+ *   triattn_grad_norm writes norm; triattn_clip_grad_norm also replaces every
+ *   element by g * coef, in place (out NULL), or writes it to out[i] (same
+ *   dtypes and element counts; then the gradients stay as they are).
+ *
+ * `tensors` and `out` are HOST arrays, read before the call returns; their
+ * data are contiguous DEVICE arrays, BF16 or FP32, aligned to their element.
+ * Tensors of 0 elements are skipped (their data may be NULL); n = 0 gives
+ * norm 0.  An element below 2^40 per tensor.  `norm` is one device float,
+ * 4-byte aligned; no call waits for the device.  Squares are added in FP32
+ * per thread and in FP64 above that, in a fixed order: bitwise reproducible.
+ * A NaN element makes norm NaN; a norm that is not finite makes coef NaN or
+ * 0, and the gradients are multiplied by it like any other.  Destinations may
+ * share no byte with one another or with a gradient, nor, in place, the
+ * gradients with one another: TRIATTN_ERR_INVALID_ARG, as for a NULL or
+ * misaligned pointer, a negative count, a norm type that is neither, a
+ * max_norm that is negative or NaN, or an `out` that does not match;
+ * TRIATTN_ERR_UNSUPPORTED for another dtype.  workspace:
+ * triattn_grad_norm_workspace_bytes(n) bytes, 256-byte aligned, contents
+ * ignored.
+ */
+#define TRIATTN_DTYPE_BF16 0
+#define TRIATTN_DTYPE_FP32 1
+#define TRIATTN_NORM_L2 0
+#define TRIATTN_NORM_MAX 1
+
+typedef struct {
+  void* data;      /* device pointer */
+  long long numel; /* elements */
+  int dtype;       /* TRIATTN_DTYPE_* */
+} triattn_tensor;
+
+size_t triattn_grad_norm_workspace_bytes(long long n);
+triattn_status triattn_grad_norm(const triattn_tensor* tensors, long long n, int norm_type, float* norm,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+triattn_status triattn_clip_grad_norm(const triattn_tensor* tensors, const triattn_tensor* out, long long n,
+                                      int norm_type, float max_norm, float* norm, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/*
  * The library's tensor-core GEMM, as used by the multiplicative update and
  * the module (exported so that it can be tested and reused; not one of the
  * method's operations).  Row-major C[M, N] = op(A) op(B): A is [M, K] with

@@ -158,14 +158,16 @@ __device__ __forceinline__ void unpack(const Packed<K>& r, float (&f)[K]) {
 
 // One warp per pair: x = (z - mean) * rstd * gamma + beta (BF16), mean and
 // rstd saved in FP32.  Lane l holds the C / 32 consecutive features from
-// l C / 32; the loads of several pairs are in flight together.
-template <int C>
+// l C / 32; the loads of several pairs are in flight together.  MASKED: a row
+// whose mask is 0 gives x = 0, whatever z holds there.
+template <int C, bool MASKED = false>
 __global__ void __launch_bounds__(256, kLnFwdPerSm) ln_fwd_kernel(const uint16_t* __restrict__ z,
                                                                   const float* __restrict__ gamma,
                                                                   const float* __restrict__ beta,
                                                                   uint16_t* __restrict__ x,
                                                                   float* __restrict__ mean_out,
-                                                                  float* __restrict__ rstd_out, size_t M) {
+                                                                  float* __restrict__ rstd_out, size_t M,
+                                                                  const uint16_t* __restrict__ mask = nullptr) {
   constexpr int kPer = C / 32;
   constexpr int kRows = C <= 128 ? 8 : 4;  // rows a warp has in flight
   const int lane = threadIdx.x & 31;
@@ -198,6 +200,12 @@ __global__ void __launch_bounds__(256, kLnFwdPerSm) ln_fwd_kernel(const uint16_t
       float o[kPer];
 #pragma unroll
       for (int e = 0; e < kPer; ++e) o[e] = (v[e] - mean) * rstd * gm[e] + bt[e];
+      if constexpr (MASKED) {
+        if ((mask[m] & 0x7FFFu) == 0) {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+        }
+      }
       st_bf16<kPer>(x + m * C + c0, o);
       if (lane == 0) {
         mean_out[m] = mean;
@@ -212,8 +220,9 @@ __global__ void __launch_bounds__(256, kLnFwdPerSm) ln_fwd_kernel(const uint16_t
 // over its pairs (fixed grid-stride assignment, ascending); the block adds
 // its 8 warps' sums in warp order and writes one partial row per block.  Lane
 // l holds the C / 32 consecutive features from l C / 32; the loads of
-// several pairs are in flight together.
-template <int C>
+// several pairs are in flight together.  MASKED: a row whose mask is 0 gives
+// dz = 0 and no part of dgamma and dbeta, whatever z and dx hold there.
+template <int C, bool MASKED = false>
 __global__ void __launch_bounds__(256, kLnBwdPerSm) ln_bwd_kernel(const uint16_t* __restrict__ z,
                                                                   const uint16_t* __restrict__ dx,
                                                                   const float* __restrict__ gamma,
@@ -221,7 +230,8 @@ __global__ void __launch_bounds__(256, kLnBwdPerSm) ln_bwd_kernel(const uint16_t
                                                                   const float* __restrict__ rstd_in,
                                                                   uint16_t* __restrict__ dz,
                                                                   float* __restrict__ part_gamma,
-                                                                  float* __restrict__ part_beta, size_t M) {
+                                                                  float* __restrict__ part_beta, size_t M,
+                                                                  const uint16_t* __restrict__ mask = nullptr) {
   constexpr int kPer = C / 32;
   constexpr int kRows = C <= 128 ? 4 : (C <= 192 ? 2 : 1);  // rows a warp has in flight
   __shared__ float red_g[8][C], red_b[8][C];
@@ -249,6 +259,13 @@ __global__ void __launch_bounds__(256, kLnBwdPerSm) ln_bwd_kernel(const uint16_t
     for (int r = 0; r < kRows; ++r) {
       const size_t m = m0 + r * warps;
       if (m >= M) break;  // the same m in every lane
+      if constexpr (MASKED) {
+        if ((mask[m] & 0x7FFFu) == 0) {
+          const float zero[kPer] = {};
+          st_bf16<kPer>(dz + m * C + c0, zero);
+          continue;
+        }
+      }
       const float mean = mu[r], rstd = rs[r];
       float xh[kPer], d[kPer], g[kPer];
       unpack<kPer>(zr[r], xh);

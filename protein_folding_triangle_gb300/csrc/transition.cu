@@ -1,0 +1,388 @@
+// Transition: the gated feed-forward block of the pair stack over M rows of C
+// features, forward and backward.
+//
+//   x = LayerNorm(z; ln_w, ln_b)                    eps 1e-5
+//   [a | b] = x W_in      W_in [C, 2H]              h = act(a) b
+//   out = m (h W_o)       W_o [H, C]                m: optional row mask
+//
+// backward from d_out, with g = m d_out (nothing is kept from the forward:
+// x, a and b are computed again):
+//
+//   dW_o = h^T g    dh = g W_o^T    da = dh b act'(a)    db = dh act(a)
+//   dW_in = x^T [da | db]    dx = [da | db] W_in^T    dz, d_ln_w, d_ln_b from dx
+//
+// A row whose mask is 0 is left out: out and dz are 0 and no gradient takes a
+// part of it, whatever z and d_out hold there (padding may be NaN).
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "kernels.cuh"
+#include "pairops.cuh"
+#include "triattn.h"
+
+namespace triattn {
+namespace {
+
+using namespace pairops;
+
+constexpr int kMaxH = 4096;
+
+// act(a) and act'(a).  Each takes one hardware tanh (absolute error about
+// 2^-11, below the BF16 rounding of h): sigmoid(a) = (1 + tanh(a / 2)) / 2.
+template <int ACT>
+__device__ __forceinline__ float act_fwd(float a) {
+  if constexpr (ACT == TRIATTN_ACT_GELU) {
+    const float u = a * fmaf(0.0356774081f * a, a, 0.7978845608f);  // sqrt(2/pi) (a + 0.044715 a^3)
+    const float ha = 0.5f * a;
+    return fmaf(ha, tanh_approx(u), ha);
+  } else {
+    const float s = fmaf(0.5f, tanh_approx(0.5f * a), 0.5f);
+    return ACT == TRIATTN_ACT_SILU ? a * s : s;
+  }
+}
+template <int ACT>
+__device__ __forceinline__ void act_both(float a, float& f, float& df) {
+  if constexpr (ACT == TRIATTN_ACT_GELU) {
+    const float a2 = a * a;
+    const float t = tanh_approx(a * fmaf(0.0356774081f, a2, 0.7978845608f));
+    const float ht = fmaf(0.5f, t, 0.5f);
+    f = a * ht;
+    df = fmaf(0.5f * a * fmaf(-t, t, 1.f), fmaf(0.1070322243f, a2, 0.7978845608f), ht);
+  } else {
+    const float s = fmaf(0.5f, tanh_approx(0.5f * a), 0.5f);
+    if constexpr (ACT == TRIATTN_ACT_SILU) {
+      f = a * s;
+      df = fmaf(f, 1.f - s, s);
+    } else {
+      f = s;
+      df = s * (1.f - s);
+    }
+  }
+}
+
+__device__ __forceinline__ void unpack8(const uint4 w, float (&f)[8]) {
+  f[0] = bf16lo_to_f32(w.x); f[1] = bf16hi_to_f32(w.x);
+  f[2] = bf16lo_to_f32(w.y); f[3] = bf16hi_to_f32(w.y);
+  f[4] = bf16lo_to_f32(w.z); f[5] = bf16hi_to_f32(w.z);
+  f[6] = bf16lo_to_f32(w.w); f[7] = bf16hi_to_f32(w.w);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ uint4 ld16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void st16(uint16_t* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
+
+// h = act(a) b m, 8 features per thread (P [M, 2H] = a | b, h [M, H]).
+template <int ACT>
+__global__ void __launch_bounds__(256) gate_fwd_kernel(const uint16_t* __restrict__ P,
+                                                       const uint16_t* __restrict__ mask, uint16_t* __restrict__ h,
+                                                       int H, size_t M) {
+  const size_t chunks = H / 8;
+  for (size_t t = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < M * chunks;
+       t += static_cast<size_t>(gridDim.x) * blockDim.x) {
+    const size_t m = t / chunks;
+    const int c0 = 8 * static_cast<int>(t % chunks);
+    float a[8], b[8];
+    unpack8(ld16(P + m * 2 * H + c0), a);
+    unpack8(ld16(P + m * 2 * H + H + c0), b);
+    const float mk = mask != nullptr ? bf16lo_to_f32(mask[m]) : 1.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = act_fwd<ACT>(a[e]) * b[e] * mk;
+    st16(h + m * H + c0, pack8(a));
+  }
+}
+
+// h = act(a) b, and [da | db] over P in place, from dh [M, H].
+template <int ACT>
+__global__ void __launch_bounds__(256) gate_bwd_kernel(uint16_t* __restrict__ P, const uint16_t* __restrict__ dh,
+                                                       uint16_t* __restrict__ h, int H, size_t M) {
+  const size_t chunks = H / 8;
+  for (size_t t = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < M * chunks;
+       t += static_cast<size_t>(gridDim.x) * blockDim.x) {
+    const size_t m = t / chunks;
+    const int c0 = 8 * static_cast<int>(t % chunks);
+    float a[8], b[8], d[8], o[8];
+    unpack8(ld16(P + m * 2 * H + c0), a);
+    unpack8(ld16(P + m * 2 * H + H + c0), b);
+    unpack8(ld16(dh + m * H + c0), d);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float f, df;
+      act_both<ACT>(a[e], f, df);
+      o[e] = f * b[e];
+      a[e] = d[e] * b[e] * df;
+      b[e] = d[e] * f;
+    }
+    st16(h + m * H + c0, pack8(o));
+    st16(P + m * 2 * H + c0, pack8(a));
+    st16(P + m * 2 * H + H + c0, pack8(b));
+  }
+}
+
+// g = m d_out, exactly 0 where m is 0 (8 features per thread).
+__global__ void __launch_bounds__(256) mask_rows_kernel(const uint16_t* __restrict__ d_out,
+                                                        const uint16_t* __restrict__ mask, uint16_t* __restrict__ g,
+                                                        int C, size_t M) {
+  const size_t chunks = C / 8;
+  for (size_t t = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < M * chunks;
+       t += static_cast<size_t>(gridDim.x) * blockDim.x) {
+    const size_t m = t / chunks;
+    const float mk = bf16lo_to_f32(mask[m]);
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (mk != 0.f) {
+      float v[8];
+      unpack8(ld16(d_out + 8 * t), v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= mk;
+      w = pack8(v);
+    }
+    st16(g + 8 * t, w);
+  }
+}
+
+// One warp per output column, as column_sum_kernel, the result FP32 or BF16.
+__global__ void __launch_bounds__(256) ln_param_sum_kernel(const float* __restrict__ pg, const float* __restrict__ pb,
+                                                           int rows, int C, int bf16, void* __restrict__ dgamma,
+                                                           void* __restrict__ dbeta) {
+  const int col = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x & 31;
+  if (col >= 2 * C) return;
+  const float* part = col < C ? pg : pb;
+  void* dst = col < C ? dgamma : dbeta;
+  const int c = col < C ? col : col - C;
+  float s = 0.f;
+  for (int r = lane; r < rows; r += 32) s += part[static_cast<size_t>(r) * C + c];
+  s = warp_sum(s);
+  if (lane != 0) return;
+  if (bf16) static_cast<uint16_t*>(dst)[c] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFFu);
+  else static_cast<float*>(dst)[c] = s;
+}
+
+// ---------------------------------------------------------------- host side
+size_t rup(size_t x) { return (x + 255) / 256 * 256; }
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool al2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+
+struct TrDims {
+  size_t M;
+  int C, H, act;
+  bool bf16;
+};
+TrDims tr_dims(const triattn_transition_shape* s) {
+  return {static_cast<size_t>(s->M), s->C, s->H, s->activation, (s->flags & TRIATTN_FLAG_GRADS_BF16) != 0};
+}
+
+struct TrWs {
+  size_t gemm, x, mean, rstd, P, h, g, dh, dx, pg, pb, total;
+};
+TrWs tr_ws(const TrDims& d, bool bwd) {
+  TrWs w;
+  size_t o = 0;
+  w.gemm = o; o += rup(kGemmWorkspace);
+  w.x = o;    o += rup(d.M * d.C * 2);
+  w.mean = o; o += rup(d.M * 4);
+  w.rstd = o; o += rup(d.M * 4);
+  w.P = o;    o += rup(d.M * d.H * 4);
+  w.h = o;    o += rup(d.M * d.H * 2);
+  w.g = w.dh = w.dx = w.pg = w.pb = o;
+  if (bwd) {
+    w.g = o;  o += rup(d.M * d.C * 2);
+    w.dh = o; o += rup(d.M * d.H * 2);
+    w.dx = o; o += rup(d.M * d.C * 2);
+    w.pg = o; o += rup(static_cast<size_t>(kLnBlocks) * d.C * 4);
+    w.pb = o; o += rup(static_cast<size_t>(kLnBlocks) * d.C * 4);
+  }
+  w.total = o;
+  return w;
+}
+
+triattn_status check_transition(const triattn_transition_shape* s) {
+  if (s == nullptr || s->M < 0 || s->C < 1 || s->H < 1 || (s->flags & ~TRIATTN_FLAG_GRADS_BF16) != 0 ||
+      s->activation < TRIATTN_ACT_SILU || s->activation > TRIATTN_ACT_GELU)
+    return TRIATTN_ERR_INVALID_ARG;
+  if (s->M > 0x7fffffffll || !ln_width_ok(s->C) || s->H % 32 != 0 || s->H > kMaxH) return TRIATTN_ERR_UNSUPPORTED;
+  return TRIATTN_OK;
+}
+
+// f(std::integral_constant<int, V>) for the activations / the row widths.
+template <typename F>
+cudaError_t by_act(int act, F&& f) {
+  switch (act) {
+    case TRIATTN_ACT_SILU: return f(std::integral_constant<int, TRIATTN_ACT_SILU>{});
+    case TRIATTN_ACT_SIGMOID: return f(std::integral_constant<int, TRIATTN_ACT_SIGMOID>{});
+    case TRIATTN_ACT_GELU: return f(std::integral_constant<int, TRIATTN_ACT_GELU>{});
+  }
+  return cudaErrorInvalidValue;
+}
+template <typename F>
+cudaError_t by_c(int C, F&& f) {
+  switch (C) {
+    case 32: return f(std::integral_constant<int, 32>{});
+    case 64: return f(std::integral_constant<int, 64>{});
+    case 96: return f(std::integral_constant<int, 96>{});
+    case 128: return f(std::integral_constant<int, 128>{});
+    case 160: return f(std::integral_constant<int, 160>{});
+    case 192: return f(std::integral_constant<int, 192>{});
+    case 224: return f(std::integral_constant<int, 224>{});
+    case 256: return f(std::integral_constant<int, 256>{});
+  }
+  return cudaErrorInvalidValue;
+}
+
+unsigned grid_for(size_t n) { return static_cast<unsigned>(n / 256 + 1 < 152 * 16 ? n / 256 + 1 : 152 * 16); }
+
+cudaError_t ln_fwd_rows(const TrDims& d, const void* z, const void* mask, const float* ln_w, const float* ln_b,
+                        uint8_t* ws, const TrWs& w, cudaStream_t s) {
+  const uint16_t* zp = static_cast<const uint16_t*>(z);
+  const uint16_t* mk = static_cast<const uint16_t*>(mask);
+  uint16_t* x = reinterpret_cast<uint16_t*>(ws + w.x);
+  float* mean = reinterpret_cast<float*>(ws + w.mean);
+  float* rstd = reinterpret_cast<float*>(ws + w.rstd);
+  return by_c(d.C, [&](auto ic) {
+    constexpr int C = decltype(ic)::value;
+    if (mk != nullptr) ln_fwd_kernel<C, true><<<kLnFwdBlocks, 256, 0, s>>>(zp, ln_w, ln_b, x, mean, rstd, d.M, mk);
+    else ln_fwd_kernel<C><<<kLnFwdBlocks, 256, 0, s>>>(zp, ln_w, ln_b, x, mean, rstd, d.M);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace
+}  // namespace triattn
+
+using namespace triattn;
+
+extern "C" {
+
+size_t triattn_transition_workspace_bytes(const triattn_transition_shape* shape, int backward) {
+  if (check_transition(shape) != TRIATTN_OK) return 0;
+  return tr_ws(tr_dims(shape), backward != 0).total;
+}
+
+triattn_status triattn_transition_fwd(const triattn_transition_shape* shape, const void* z, const void* mask,
+                                      const float* ln_w, const float* ln_b, const void* w_in, const void* w_o,
+                                      void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  const triattn_status st = check_transition(shape);
+  if (st != TRIATTN_OK) return st;
+  if (shape->M == 0) return TRIATTN_OK;
+  const void* req[] = {z, ln_w, ln_b, w_in, w_o, out};
+  for (const void* q : req)
+    if (q == nullptr || !al16(q)) return TRIATTN_ERR_INVALID_ARG;
+  if (mask != nullptr && !al2(mask)) return TRIATTN_ERR_INVALID_ARG;
+  const TrDims d = tr_dims(shape);
+  const TrWs w = tr_ws(d, false);
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < w.total)
+    return TRIATTN_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  void* const gws = ws + w.gemm;
+  const int M = static_cast<int>(d.M);
+  uint16_t* P = reinterpret_cast<uint16_t*>(ws + w.P);
+  uint16_t* h = reinterpret_cast<uint16_t*>(ws + w.h);
+  if (trace_call(kKTrLn, s, [&] { return ln_fwd_rows(d, z, mask, ln_w, ln_b, ws, w, s); }) != cudaSuccess)
+    return TRIATTN_ERR_CUDA;
+  if (gemm_traced(kKTrGemm, gws, s, false, false, M, 2 * d.H, d.C, ws + w.x, d.C, w_in, 2 * d.H, P, 2 * d.H, false) !=
+      TRIATTN_OK)
+    return TRIATTN_ERR_CUDA;
+  if (trace_call(kKTrGate, s, [&] {
+        return by_act(d.act, [&](auto ic) {
+          gate_fwd_kernel<decltype(ic)::value><<<grid_for(d.M * d.H / 8), 256, 0, s>>>(
+              P, static_cast<const uint16_t*>(mask), h, d.H, d.M);
+          return cudaGetLastError();
+        });
+      }) != cudaSuccess)
+    return TRIATTN_ERR_CUDA;
+  return gemm_traced(kKTrGemm, gws, s, false, false, M, d.C, d.H, h, d.H, w_o, d.C, out, d.C, false);
+}
+
+triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, const void* z, const void* mask,
+                                      const float* ln_w, const float* ln_b, const void* w_in, const void* w_o,
+                                      const void* d_out, void* dz, void* d_ln_w, void* d_ln_b, void* d_w_in,
+                                      void* d_w_o, void* workspace, size_t workspace_bytes, void* stream) {
+  const triattn_status st = check_transition(shape);
+  if (st != TRIATTN_OK) return st;
+  const TrDims d = tr_dims(shape);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const void* par[] = {d_ln_w, d_ln_b, d_w_in, d_w_o};
+  for (const void* q : par)
+    if (q == nullptr || !al16(q)) return TRIATTN_ERR_INVALID_ARG;
+  if (d.M == 0) {  // no rows: the gradients are sums of nothing
+    const size_t es = d.bf16 ? 2 : 4;
+    const bool ok = cudaMemsetAsync(d_ln_w, 0, es * d.C, s) == cudaSuccess &&
+                    cudaMemsetAsync(d_ln_b, 0, es * d.C, s) == cudaSuccess &&
+                    cudaMemsetAsync(d_w_in, 0, es * d.C * 2 * d.H, s) == cudaSuccess &&
+                    cudaMemsetAsync(d_w_o, 0, es * d.C * d.H, s) == cudaSuccess;
+    return ok ? TRIATTN_OK : TRIATTN_ERR_CUDA;
+  }
+  const void* req[] = {z, ln_w, ln_b, w_in, w_o, d_out, dz};
+  for (const void* q : req)
+    if (q == nullptr || !al16(q)) return TRIATTN_ERR_INVALID_ARG;
+  if (mask != nullptr && !al2(mask)) return TRIATTN_ERR_INVALID_ARG;
+  const TrWs w = tr_ws(d, true);
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < w.total)
+    return TRIATTN_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  void* const gws = ws + w.gemm;
+  const int M = static_cast<int>(d.M), C = d.C, H = d.H;
+  const uint16_t* mk = static_cast<const uint16_t*>(mask);
+  uint16_t* P = reinterpret_cast<uint16_t*>(ws + w.P);
+  uint16_t* h = reinterpret_cast<uint16_t*>(ws + w.h);
+  uint16_t* dh = reinterpret_cast<uint16_t*>(ws + w.dh);
+  const void* g = d_out;
+  auto gemm = [&](bool ta, bool tb, int m, int n, int k, const void* A, int lda, const void* B, int ldb, void* Cp,
+                  int ldc, bool f32) {
+    return gemm_traced(kKTrGemm, gws, s, ta, tb, m, n, k, A, lda, B, ldb, Cp, ldc, f32) == TRIATTN_OK;
+  };
+  if (trace_call(kKTrLn, s, [&] { return ln_fwd_rows(d, z, mask, ln_w, ln_b, ws, w, s); }) != cudaSuccess)
+    return TRIATTN_ERR_CUDA;
+  if (mk != nullptr) {
+    g = ws + w.g;
+    if (trace_call(kKTrGate, s, [&] {
+          mask_rows_kernel<<<grid_for(d.M * C / 8), 256, 0, s>>>(static_cast<const uint16_t*>(d_out), mk,
+                                                                 reinterpret_cast<uint16_t*>(ws + w.g), C, d.M);
+          return cudaGetLastError();
+        }) != cudaSuccess)
+      return TRIATTN_ERR_CUDA;
+  }
+  if (!gemm(false, false, M, 2 * H, C, ws + w.x, C, w_in, 2 * H, P, 2 * H, false) ||
+      !gemm(false, true, M, H, C, g, C, w_o, C, dh, H, false))
+    return TRIATTN_ERR_CUDA;
+  if (trace_call(kKTrGate, s, [&] {
+        return by_act(d.act, [&](auto ic) {
+          gate_bwd_kernel<decltype(ic)::value><<<grid_for(d.M * H / 8), 256, 0, s>>>(P, dh, h, H, d.M);
+          return cudaGetLastError();
+        });
+      }) != cudaSuccess)
+    return TRIATTN_ERR_CUDA;
+  if (!gemm(true, false, H, C, M, h, H, g, C, d_w_o, C, !d.bf16) ||
+      !gemm(true, false, C, 2 * H, M, ws + w.x, C, P, 2 * H, d_w_in, 2 * H, !d.bf16) ||
+      !gemm(false, true, M, C, 2 * H, P, 2 * H, w_in, 2 * H, ws + w.dx, C, false))
+    return TRIATTN_ERR_CUDA;
+  float* pg = reinterpret_cast<float*>(ws + w.pg);
+  float* pb = reinterpret_cast<float*>(ws + w.pb);
+  if (trace_call(kKTrLnBwd, s, [&] {
+        return by_c(C, [&](auto ic) {
+          constexpr int kC = decltype(ic)::value;
+          const uint16_t* zp = static_cast<const uint16_t*>(z);
+          const uint16_t* dx = reinterpret_cast<const uint16_t*>(ws + w.dx);
+          const float* mean = reinterpret_cast<const float*>(ws + w.mean);
+          const float* rstd = reinterpret_cast<const float*>(ws + w.rstd);
+          uint16_t* dzp = static_cast<uint16_t*>(dz);
+          if (mk != nullptr)
+            ln_bwd_kernel<kC, true><<<kLnBlocks, 256, 0, s>>>(zp, dx, ln_w, mean, rstd, dzp, pg, pb, d.M, mk);
+          else
+            ln_bwd_kernel<kC><<<kLnBlocks, 256, 0, s>>>(zp, dx, ln_w, mean, rstd, dzp, pg, pb, d.M);
+          return cudaGetLastError();
+        });
+      }) != cudaSuccess)
+    return TRIATTN_ERR_CUDA;
+  const cudaError_t e = trace_call(kKTrColSum, s, [&] {
+    ln_param_sum_kernel<<<static_cast<unsigned>((2 * C + 7) / 8), 256, 0, s>>>(pg, pb, kLnBlocks, C, d.bf16 ? 1 : 0,
+                                                                               d_ln_w, d_ln_b);
+    return cudaGetLastError();
+  });
+  return e == cudaSuccess ? TRIATTN_OK : TRIATTN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -177,3 +177,28 @@ def make_trimul_inputs(B: int, N: int, Cz: int, Ch: int, seed: int = 0, pad_frac
         mask = (keep[:, None] * keep[None, :]).expand(B, N, N).contiguous().to(torch.bfloat16)
     return {"z": z, "d_out": d_out, "ln_in_w": ln_in_w, "ln_in_b": ln_in_b, "w_p": w_p, "ln_out_w": ln_out_w,
             "ln_out_b": ln_out_b, "w_o": w_o, "mask": mask}
+
+
+def make_transition_inputs(lead, C: int, H: int, seed: int = 0, drop: float = 0.0) -> dict:
+    """Seeded inputs of the transition over rows of shape ``lead`` (CPU
+    tensors): z and d_out [*lead, C] BF16 (standard normal); LayerNorm scale
+    1 + 0.1 n and shift 0.1 n (FP32); W_in [C, 2H] with entries n / sqrt(C) and
+    W_o [H, C] with entries n / sqrt(H) (BF16).  Draw order: z, d_out, ln_w,
+    ln_b, W_in, W_o, mask.  With ``drop`` > 0 each row is masked (0) with that
+    probability in the multiplicative mask [*lead] (BF16), else the mask is
+    None."""
+    g = torch.Generator(device="cpu")
+    g.manual_seed(int(seed))
+    lead = tuple(lead)
+
+    def normal(shape, scale=1.0):
+        return torch.randn(shape, generator=g, dtype=torch.float32) * scale
+
+    z = normal(lead + (C,)).to(torch.bfloat16)
+    d_out = normal(lead + (C,)).to(torch.bfloat16)
+    ln_w = 1.0 + normal((C,), 0.1)
+    ln_b = normal((C,), 0.1)
+    w_in = normal((C, 2 * H), C ** -0.5).to(torch.bfloat16)
+    w_o = normal((H, C), H ** -0.5).to(torch.bfloat16)
+    mask = (torch.rand(lead, generator=g) >= drop).to(torch.bfloat16) if drop > 0 else None
+    return {"z": z, "d_out": d_out, "ln_w": ln_w, "ln_b": ln_b, "w_in": w_in, "w_o": w_o, "mask": mask}

@@ -38,9 +38,12 @@ EXPORTED = ("triattn_status_string", "triattn_fwd_workspace_bytes", "triattn_bwd
             "triattn_module_workspace_bytes", "tri_attn_module_fwd", "tri_attn_module_bwd",
             "triattn_trimul_ctx_bytes", "triattn_trimul_workspace_bytes", "triattn_trimul_fwd",
             "triattn_trimul_bwd", "triattn_gemm_workspace_bytes", "triattn_gemm", "tri_attn_fwd_strided",
-            "tri_attn_bwd_strided")
+            "tri_attn_bwd_strided", "triattn_transition_workspace_bytes", "triattn_transition_fwd",
+            "triattn_transition_bwd", "triattn_grad_norm_workspace_bytes", "triattn_grad_norm",
+            "triattn_clip_grad_norm")
 
 FLAG_DBIAS_FP32 = 1
+FLAG_GRADS_BF16 = 2
 
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -77,6 +80,17 @@ class TriMulShape(ctypes.Structure):
                 ("direction", ctypes.c_int), ("flags", ctypes.c_uint)]
 
 
+class TransitionShape(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_longlong), ("C", ctypes.c_int), ("H", ctypes.c_int), ("activation", ctypes.c_int),
+                ("flags", ctypes.c_uint)]
+
+
+class Tensor(ctypes.Structure):
+    """triattn_tensor: one gradient of a list (device pointer, elements, dtype)."""
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_longlong), ("dtype", ctypes.c_int)]
+
+
+ACTIVATIONS = {"silu": 0, "sigmoid": 1, "gelu": 2}
 TRIMUL_DIRECTIONS = {"outgoing": 0, "incoming": 1}
 
 
@@ -135,7 +149,20 @@ def _declare(lib):
     lib.triattn_trimul_fwd.restype = ctypes.c_int
     lib.triattn_trimul_bwd.argtypes = [tp] + [vp] * 16 + [ctypes.c_size_t, vp]
     lib.triattn_trimul_bwd.restype = ctypes.c_int
+    rp, gp = ctypes.POINTER(TransitionShape), ctypes.POINTER(Tensor)
+    lib.triattn_transition_workspace_bytes.argtypes = [rp, ctypes.c_int]
+    lib.triattn_transition_workspace_bytes.restype = ctypes.c_size_t
+    lib.triattn_transition_fwd.argtypes = [rp] + [vp] * 8 + [ctypes.c_size_t, vp]
+    lib.triattn_transition_fwd.restype = ctypes.c_int
+    lib.triattn_transition_bwd.argtypes = [rp] + [vp] * 13 + [ctypes.c_size_t, vp]
+    lib.triattn_transition_bwd.restype = ctypes.c_int
     ll = ctypes.c_longlong
+    lib.triattn_grad_norm_workspace_bytes.argtypes = [ll]
+    lib.triattn_grad_norm_workspace_bytes.restype = ctypes.c_size_t
+    lib.triattn_grad_norm.argtypes = [vp, ll, ctypes.c_int, vp, vp, ctypes.c_size_t, vp]
+    lib.triattn_grad_norm.restype = ctypes.c_int
+    lib.triattn_clip_grad_norm.argtypes = [vp, vp, ll, ctypes.c_int, ctypes.c_float, vp, vp, ctypes.c_size_t, vp]
+    lib.triattn_clip_grad_norm.restype = ctypes.c_int
     lib.triattn_gemm_workspace_bytes.argtypes = [ctypes.c_int] * 4
     lib.triattn_gemm_workspace_bytes.restype = ctypes.c_size_t
     lib.triattn_gemm.argtypes = ([ctypes.c_int] * 5 + [vp, ll, vp, ll, vp, ll, ctypes.c_int, ctypes.c_int, ll, ll, ll,
@@ -599,6 +626,177 @@ def triattn_trimul_bwd(z, mask, ln_in_w, w_p, ln_out_w, w_o, ctx, d_out, directi
                                      _stream_ptr(stream))
     _raise(code, "triattn_trimul_bwd")
     return out
+
+
+def _on_stream(device, stream):
+    """Context in which `device` is current and allocations belong to the
+    stream that the call runs on (so a workspace freed at the end of the call
+    is not handed to another stream while its kernels still run)."""
+    return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device))
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def transition_shape(rows: int, C: int, H: int, activation: str = "silu", grads_bf16: bool = False) -> TransitionShape:
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {tuple(ACTIVATIONS)}")
+    return TransitionShape(rows, C, H, ACTIVATIONS[activation], FLAG_GRADS_BF16 if grads_bf16 else 0)
+
+
+def transition_workspace_bytes(rows: int, C: int, H: int, backward: bool = False) -> int:
+    """Workspace of the transition's forward or backward; 0 for an unsupported shape."""
+    s = transition_shape(rows, C, H)
+    return int(load().triattn_transition_workspace_bytes(ctypes.byref(s), int(backward)))
+
+
+def _transition_check(z, mask, ln_w, ln_b, w_in, w_o):
+    if z.dim() < 1 or w_o.dim() != 2:
+        raise ValueError("z must be [..., C] and w_o [H, C]")
+    C, H = z.shape[-1], w_o.shape[0]
+    _check(z, "z", z.shape)
+    _check(ln_w, "ln_w", (C,), torch.float32)
+    _check(ln_b, "ln_b", (C,), torch.float32)
+    _check(w_in, "w_in", (C, 2 * H))
+    _check(w_o, "w_o", (H, C))
+    if mask is not None:
+        _check(mask, "mask", z.shape[:-1])
+    _same_device(z.device, mask=mask, ln_w=ln_w, ln_b=ln_b, w_in=w_in, w_o=w_o)
+    return z.numel() // C if C else 0, C, H
+
+
+def triattn_transition_fwd(z, mask, ln_w, ln_b, w_in, w_o, activation: str = "silu", *, workspace=None, out=None,
+                           stream=None):
+    """Transition (gated feed-forward block) forward over the rows of z
+    [..., C] bf16: out = mask * ((act(a) * b) w_o), [a | b] = LayerNorm(z) w_in.
+    ``mask`` [...] bf16 (1 keeps a row, 0 leaves it out) or None; ``activation``
+    "silu", "sigmoid" or "gelu" (tanh form).  Returns out [..., C] bf16."""
+    M, C, H = _transition_check(z, mask, ln_w, ln_b, w_in, w_o)
+    s = transition_shape(M, C, H, activation)
+    need = int(load().triattn_transition_workspace_bytes(ctypes.byref(s), 0))
+    if need == 0:
+        raise TriAttnError(ERR_UNSUPPORTED, "triattn_transition_fwd")
+    with _on_stream(z.device, stream):
+        workspace = torch.empty(need, dtype=torch.uint8, device=z.device) if workspace is None else workspace
+        out = torch.empty_like(z) if out is None else out
+        _check(out, "out", z.shape)
+        _same_device(z.device, workspace=workspace, out=out)
+        code = load().triattn_transition_fwd(ctypes.byref(s), _ptr(z), _ptr(mask), _ptr(ln_w), _ptr(ln_b), _ptr(w_in),
+                                             _ptr(w_o), _ptr(out), _ptr(workspace), _bytes(workspace),
+                                             _stream_ptr(stream))
+    _raise(code, "triattn_transition_fwd")
+    return out
+
+
+def triattn_transition_bwd(z, mask, ln_w, ln_b, w_in, w_o, d_out, activation: str = "silu", *,
+                           grads_bf16: bool = False, workspace=None, out=None, stream=None):
+    """Backward of <out, d_out>; the forward's intermediates are computed
+    again.  Returns (dz bf16, d_ln_w, d_ln_b, d_w_in, d_w_o), the parameter
+    gradients FP32, or with ``grads_bf16`` BF16 (one rounding of the FP32 sums)."""
+    M, C, H = _transition_check(z, mask, ln_w, ln_b, w_in, w_o)
+    _check(d_out, "d_out", z.shape)
+    s = transition_shape(M, C, H, activation, grads_bf16)
+    need = int(load().triattn_transition_workspace_bytes(ctypes.byref(s), 1))
+    if need == 0:
+        raise TriAttnError(ERR_UNSUPPORTED, "triattn_transition_bwd")
+    dt = torch.bfloat16 if grads_bf16 else torch.float32
+    with _on_stream(z.device, stream):
+        workspace = torch.empty(need, dtype=torch.uint8, device=z.device) if workspace is None else workspace
+        if out is None:
+            kw = dict(dtype=dt, device=z.device)
+            out = (torch.empty_like(z), torch.empty(C, **kw), torch.empty(C, **kw), torch.empty((C, 2 * H), **kw),
+                   torch.empty((H, C), **kw))
+        dz, dlw, dlb, dwi, dwo = out
+        _check(dz, "dz", z.shape)
+        for name, t, shape in (("d_ln_w", dlw, (C,)), ("d_ln_b", dlb, (C,)), ("d_w_in", dwi, (C, 2 * H)),
+                               ("d_w_o", dwo, (H, C))):
+            _check(t, name, shape, dt)
+        _same_device(z.device, d_out=d_out, workspace=workspace, dz=dz, d_ln_w=dlw, d_ln_b=dlb, d_w_in=dwi, d_w_o=dwo)
+        code = load().triattn_transition_bwd(ctypes.byref(s), _ptr(z), _ptr(mask), _ptr(ln_w), _ptr(ln_b), _ptr(w_in),
+                                             _ptr(w_o), _ptr(d_out), _ptr(dz), _ptr(dlw), _ptr(dlb), _ptr(dwi),
+                                             _ptr(dwo), _ptr(workspace), _bytes(workspace), _stream_ptr(stream))
+    _raise(code, "triattn_transition_bwd")
+    return dz, dlw, dlb, dwi, dwo
+
+
+GRAD_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _dense(t) -> bool:
+    """Whether the elements of a strided tensor fill one block of memory, each once."""
+    n = 1
+    for size, stride in sorted(zip(t.shape, t.stride()), key=lambda p: p[1]):
+        if size != 1:
+            if stride != n:
+                return False
+            n *= size
+    return True
+
+
+def _tensor_table(tensors, name, device):
+    table = (Tensor * len(tensors))()
+    for i, t in enumerate(tensors):
+        if t.dtype not in GRAD_DTYPES or t.device != device or t.layout != torch.strided:
+            raise ValueError(f"{name}[{i}] must be a strided bfloat16 or float32 tensor on {device}")
+        if not t.is_contiguous() and t.numel() and not _dense(t):
+            raise ValueError(f"{name}[{i}] must fill one block of memory")
+        table[i] = (t.data_ptr(), t.numel(), GRAD_DTYPES[t.dtype])
+    return table
+
+
+def _grad_call(tensors, norm_type):
+    tensors = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
+    kinds = {2.0: 0, float("inf"): 1}
+    if float(norm_type) not in kinds:
+        raise ValueError("norm_type must be 2 or inf")
+    device = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
+    if device.type != "cuda":
+        raise ValueError("the gradients must be CUDA tensors")
+    return tensors, kinds[float(norm_type)], device
+
+
+def triattn_grad_norm(tensors, norm_type: float = 2.0, *, stream=None):
+    """Norm of all elements of ``tensors`` (BF16 and FP32 CUDA tensors, mixed):
+    2 or inf.  Returns a 0-dim FP32 tensor; nothing waits for the device."""
+    tensors, kind, device = _grad_call(tensors, norm_type)
+    n = len(tensors)
+    table = _tensor_table(tensors, "tensors", device)
+    with _on_stream(device, stream):
+        norm = torch.empty((), dtype=torch.float32, device=device)
+        ws = torch.empty(max(int(load().triattn_grad_norm_workspace_bytes(n)), 16), dtype=torch.uint8, device=device)
+        code = load().triattn_grad_norm(table, n, kind, _ptr(norm), _ptr(ws), _bytes(ws), _stream_ptr(stream))
+    _raise(code, "triattn_grad_norm")
+    return norm
+
+
+def triattn_clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, *, out=None, stream=None):
+    """Scale ``tensors`` (BF16 and FP32 CUDA tensors, mixed) by
+    min(1, max_norm / (norm + 1e-6)), in place, or into ``out`` (a list of
+    tensors of the same shapes, strides and dtypes).  Returns the norm before
+    clipping as a 0-dim FP32 tensor; nothing waits for the device.  A tensor
+    may not be listed twice."""
+    tensors, kind, device = _grad_call(tensors, norm_type)
+    n = len(tensors)
+    table = _tensor_table(tensors, "tensors", device)
+    into = None
+    if out is not None:
+        out = [out] if isinstance(out, torch.Tensor) else list(out)
+        if len(out) != n:
+            raise ValueError(f"out has {len(out)} tensors, expected {n}")
+        into = _tensor_table(out, "out", device)
+        for i, (a, b) in enumerate(zip(tensors, out)):
+            if a.dtype != b.dtype or a.shape != b.shape or a.stride() != b.stride():
+                raise ValueError(f"out[{i}] must have the shape, strides and dtype of tensors[{i}]")
+    with _on_stream(device, stream):
+        norm = torch.empty((), dtype=torch.float32, device=device)
+        ws = torch.empty(max(int(load().triattn_grad_norm_workspace_bytes(n)), 16), dtype=torch.uint8, device=device)
+        code = load().triattn_clip_grad_norm(table, into, n, kind, float(max_norm), _ptr(norm), _ptr(ws), _bytes(ws),
+                                             _stream_ptr(stream))
+    _raise(code, "triattn_clip_grad_norm")
+    return norm
 
 
 def gemm(a, b, *, ta: bool = False, tb: bool = False, out_f32: bool = False, out=None, stream=None):
