@@ -596,6 +596,8 @@ SplitPlan split_plan(int M, int N, int K, int batch, int BN, int sms) {
 
 }  // namespace
 
+void* tensor_map_encoder() { return reinterpret_cast<void*>(gemm_encoder()); }
+
 size_t gemm_splitk_bytes(int M, int N, int K, int batch) {
   const int BN = N > 128 ? 256 : 128;
   const SplitPlan sp = split_plan(M, N, K, batch, BN, gemm_sms());

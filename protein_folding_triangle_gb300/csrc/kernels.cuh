@@ -149,6 +149,14 @@ cudaError_t launch_gemm_heads(bool tb, int M, int N, int K, const void* A, long 
 cudaError_t launch_gate_bwd_proj(int B, long long NN, int Cz, int Ch, const void* x, const void* w_p,
                                  const void* mask, const void* dA, const void* dB, void* dp, long long ldp,
                                  const WaitCtl& wc, cudaStream_t s);
+// The driver's cuTensorMapEncodeTiled (PFN_cuTensorMapEncodeTiled_v12000), or null.
+void* tensor_map_encoder();
+// The transition's fused forward (transition_fwd.cu): whether its rule takes
+// this width, and the launch (arguments as in triattn_transition_fwd).
+bool transition_fwd_fused(int C, int H);
+cudaError_t launch_transition_fwd(long long M, int C, int H, int act, const void* z, const void* mask,
+                                  const float* ln_w, const float* ln_b, const void* w_in, const void* w_o, void* out,
+                                  const WaitCtl& wc, cudaStream_t s);
 // The bounded-wait control of the current device (status word, time limit).
 WaitCtl current_wait_ctl();
 
@@ -157,7 +165,7 @@ enum KernelKind {
   kKFwd = 0, kKPre, kKTrans, kKMain, kKRedDq, kKRedDb, kKMainAtomic, kKFinDq, kKFinDb, kKCombine, kKFwdPrep,
   kKModLnFwd, kKModLayout, kKModGemm, kKModLnBwd, kKModColSum,
   kKTmLnIn, kKTmProj, kKTmGate, kKTmContract, kKTmLnOut, kKTmOutGate, kKTmColSum, kKGemm, kKTmProjGate,
-  kKTrLn, kKTrGemm, kKTrGate, kKTrLnBwd, kKTrColSum, kKGradSum, kKGradScale, kKGradNorm,
+  kKTrLn, kKTrFwd, kKTrGemm, kKTrGate, kKTrLnBwd, kKTrColSum, kKGradSum, kKGradScale, kKGradNorm,
   kKinds
 };
 // Runs `launch` on stream `s`, bracketed by a pair of trace events while

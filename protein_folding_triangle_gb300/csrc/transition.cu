@@ -20,6 +20,7 @@
 
 #include "kernels.cuh"
 #include "pairops.cuh"
+#include "transition.cuh"
 #include "triattn.h"
 
 namespace triattn {
@@ -28,39 +29,6 @@ namespace {
 using namespace pairops;
 
 constexpr int kMaxH = 4096;
-
-// act(a) and act'(a).  Each takes one hardware tanh (absolute error about
-// 2^-11, below the BF16 rounding of h): sigmoid(a) = (1 + tanh(a / 2)) / 2.
-template <int ACT>
-__device__ __forceinline__ float act_fwd(float a) {
-  if constexpr (ACT == TRIATTN_ACT_GELU) {
-    const float u = a * fmaf(0.0356774081f * a, a, 0.7978845608f);  // sqrt(2/pi) (a + 0.044715 a^3)
-    const float ha = 0.5f * a;
-    return fmaf(ha, tanh_approx(u), ha);
-  } else {
-    const float s = fmaf(0.5f, tanh_approx(0.5f * a), 0.5f);
-    return ACT == TRIATTN_ACT_SILU ? a * s : s;
-  }
-}
-template <int ACT>
-__device__ __forceinline__ void act_both(float a, float& f, float& df) {
-  if constexpr (ACT == TRIATTN_ACT_GELU) {
-    const float a2 = a * a;
-    const float t = tanh_approx(a * fmaf(0.0356774081f, a2, 0.7978845608f));
-    const float ht = fmaf(0.5f, t, 0.5f);
-    f = a * ht;
-    df = fmaf(0.5f * a * fmaf(-t, t, 1.f), fmaf(0.1070322243f, a2, 0.7978845608f), ht);
-  } else {
-    const float s = fmaf(0.5f, tanh_approx(0.5f * a), 0.5f);
-    if constexpr (ACT == TRIATTN_ACT_SILU) {
-      f = a * s;
-      df = fmaf(f, 1.f - s, s);
-    } else {
-      f = s;
-      df = s * (1.f - s);
-    }
-  }
-}
 
 __device__ __forceinline__ void unpack8(const uint4 w, float (&f)[8]) {
   f[0] = bf16lo_to_f32(w.x); f[1] = bf16hi_to_f32(w.x);
@@ -180,6 +148,11 @@ struct TrWs {
 TrWs tr_ws(const TrDims& d, bool bwd) {
   TrWs w;
   size_t o = 0;
+  if (!bwd && transition_fwd_fused(d.C, d.H)) {  // the fused forward keeps everything on the chip
+    w.gemm = w.x = w.mean = w.rstd = w.P = w.h = w.g = w.dh = w.dx = w.pg = w.pb = 0;
+    w.total = 256;
+    return w;
+  }
   w.gemm = o; o += rup(kGemmWorkspace);
   w.x = o;    o += rup(d.M * d.C * 2);
   w.mean = o; o += rup(d.M * 4);
@@ -206,16 +179,7 @@ triattn_status check_transition(const triattn_transition_shape* s) {
   return TRIATTN_OK;
 }
 
-// f(std::integral_constant<int, V>) for the activations / the row widths.
-template <typename F>
-cudaError_t by_act(int act, F&& f) {
-  switch (act) {
-    case TRIATTN_ACT_SILU: return f(std::integral_constant<int, TRIATTN_ACT_SILU>{});
-    case TRIATTN_ACT_SIGMOID: return f(std::integral_constant<int, TRIATTN_ACT_SIGMOID>{});
-    case TRIATTN_ACT_GELU: return f(std::integral_constant<int, TRIATTN_ACT_GELU>{});
-  }
-  return cudaErrorInvalidValue;
-}
+// f(std::integral_constant<int, C>) for the row widths.
 template <typename F>
 cudaError_t by_c(int C, F&& f) {
   switch (C) {
@@ -275,6 +239,13 @@ triattn_status triattn_transition_fwd(const triattn_transition_shape* shape, con
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < w.total)
     return TRIATTN_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (transition_fwd_fused(d.C, d.H)) {
+    const cudaError_t e = trace_call(kKTrFwd, s, [&] {
+      return launch_transition_fwd(shape->M, d.C, d.H, d.act, z, mask, ln_w, ln_b, w_in, w_o, out, current_wait_ctl(),
+                                   s);
+    });
+    return e == cudaSuccess ? TRIATTN_OK : TRIATTN_ERR_CUDA;
+  }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   void* const gws = ws + w.gemm;
   const int M = static_cast<int>(d.M);
