@@ -157,6 +157,16 @@ bool transition_fwd_fused(int C, int H);
 cudaError_t launch_transition_fwd(long long M, int C, int H, int act, const void* z, const void* mask,
                                   const float* ln_w, const float* ln_b, const void* w_in, const void* w_o, void* out,
                                   const WaitCtl& wc, cudaStream_t s);
+// The transition's fused backward up to the weight gradients' operands
+// (transition_bwd.cu): dz, and for every row x [M, C], g = m d_out [M, C]
+// (written only with a mask), h [M, H] and [da | db] [M, 2H], all BF16;
+// *parts (at most kTbPartRows) partial rows of d_ln_w and d_ln_b.
+constexpr int kTbPartRows = 152 * 4;
+bool transition_bwd_fused(int C, int H);
+cudaError_t launch_transition_bwd(long long M, int C, int H, int act, const void* z, const void* mask,
+                                  const float* ln_w, const float* ln_b, const void* w_in, const void* w_o,
+                                  const void* d_out, void* dz, void* x, void* g, void* h, void* dab, float* part_g,
+                                  float* part_b, int* parts, const WaitCtl& wc, cudaStream_t s);
 // The bounded-wait control of the current device (status word, time limit).
 WaitCtl current_wait_ctl();
 
@@ -165,7 +175,7 @@ enum KernelKind {
   kKFwd = 0, kKPre, kKTrans, kKMain, kKRedDq, kKRedDb, kKMainAtomic, kKFinDq, kKFinDb, kKCombine, kKFwdPrep,
   kKModLnFwd, kKModLayout, kKModGemm, kKModLnBwd, kKModColSum,
   kKTmLnIn, kKTmProj, kKTmGate, kKTmContract, kKTmLnOut, kKTmOutGate, kKTmColSum, kKGemm, kKTmProjGate,
-  kKTrLn, kKTrFwd, kKTrGemm, kKTrGate, kKTrLnBwd, kKTrColSum, kKGradSum, kKGradScale, kKGradNorm,
+  kKTrLn, kKTrFwd, kKTrBwd, kKTrGemm, kKTrGate, kKTrLnBwd, kKTrColSum, kKGradSum, kKGradScale, kKGradNorm,
   kKinds
 };
 // Runs `launch` on stream `s`, bracketed by a pair of trace events while

@@ -155,6 +155,15 @@ TrWs tr_ws(const TrDims& d, bool bwd) {
   }
   w.gemm = o; o += rup(kGemmWorkspace);
   w.x = o;    o += rup(d.M * d.C * 2);
+  if (bwd && transition_bwd_fused(d.C, d.H)) {
+    w.P = o;  o += rup(d.M * d.H * 4);
+    w.h = o;  o += rup(d.M * d.H * 2);
+    w.g = o;  o += rup(d.M * d.C * 2);
+    w.pg = o; o += rup(static_cast<size_t>(kTbPartRows) * d.C * 4);
+    w.pb = o; o += rup(static_cast<size_t>(kTbPartRows) * d.C * 4);
+    w.mean = w.rstd = w.dh = w.dx = w.total = o;
+    return w;
+  }
   w.mean = o; o += rup(d.M * 4);
   w.rstd = o; o += rup(d.M * 4);
   w.P = o;    o += rup(d.M * d.H * 4);
@@ -305,6 +314,30 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
                   int ldc, bool f32) {
     return gemm_traced(kKTrGemm, gws, s, ta, tb, m, n, k, A, lda, B, ldb, Cp, ldc, f32) == TRIATTN_OK;
   };
+  float* pg = reinterpret_cast<float*>(ws + w.pg);
+  float* pb = reinterpret_cast<float*>(ws + w.pb);
+  int parts = kLnBlocks;
+  // dW_o = h^T g, dW_in = x^T [da | db], and the sums of the LayerNorm's partial rows
+  auto weight_grads = [&]() -> bool {
+    return gemm(true, false, H, C, M, h, H, g, C, d_w_o, C, !d.bf16) &&
+           gemm(true, false, C, 2 * H, M, ws + w.x, C, P, 2 * H, d_w_in, 2 * H, !d.bf16);
+  };
+  auto ln_grads = [&] {
+    return trace_call(kKTrColSum, s, [&] {
+             ln_param_sum_kernel<<<static_cast<unsigned>((2 * C + 7) / 8), 256, 0, s>>>(pg, pb, parts, C,
+                                                                                        d.bf16 ? 1 : 0, d_ln_w, d_ln_b);
+             return cudaGetLastError();
+           }) == cudaSuccess;
+  };
+  if (transition_bwd_fused(C, H)) {
+    if (mk != nullptr) g = ws + w.g;
+    if (trace_call(kKTrBwd, s, [&] {
+          return launch_transition_bwd(shape->M, C, H, d.act, z, mask, ln_w, ln_b, w_in, w_o, d_out, dz, ws + w.x,
+                                       ws + w.g, h, P, pg, pb, &parts, current_wait_ctl(), s);
+        }) != cudaSuccess)
+      return TRIATTN_ERR_CUDA;
+    return weight_grads() && ln_grads() ? TRIATTN_OK : TRIATTN_ERR_CUDA;
+  }
   if (trace_call(kKTrLn, s, [&] { return ln_fwd_rows(d, z, mask, ln_w, ln_b, ws, w, s); }) != cudaSuccess)
     return TRIATTN_ERR_CUDA;
   if (mk != nullptr) {
@@ -326,12 +359,8 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
         });
       }) != cudaSuccess)
     return TRIATTN_ERR_CUDA;
-  if (!gemm(true, false, H, C, M, h, H, g, C, d_w_o, C, !d.bf16) ||
-      !gemm(true, false, C, 2 * H, M, ws + w.x, C, P, 2 * H, d_w_in, 2 * H, !d.bf16) ||
-      !gemm(false, true, M, C, 2 * H, P, 2 * H, w_in, 2 * H, ws + w.dx, C, false))
+  if (!weight_grads() || !gemm(false, true, M, C, 2 * H, P, 2 * H, w_in, 2 * H, ws + w.dx, C, false))
     return TRIATTN_ERR_CUDA;
-  float* pg = reinterpret_cast<float*>(ws + w.pg);
-  float* pb = reinterpret_cast<float*>(ws + w.pb);
   if (trace_call(kKTrLnBwd, s, [&] {
         return by_c(C, [&](auto ic) {
           constexpr int kC = decltype(ic)::value;
@@ -348,12 +377,7 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
         });
       }) != cudaSuccess)
     return TRIATTN_ERR_CUDA;
-  const cudaError_t e = trace_call(kKTrColSum, s, [&] {
-    ln_param_sum_kernel<<<static_cast<unsigned>((2 * C + 7) / 8), 256, 0, s>>>(pg, pb, kLnBlocks, C, d.bf16 ? 1 : 0,
-                                                                               d_ln_w, d_ln_b);
-    return cudaGetLastError();
-  });
-  return e == cudaSuccess ? TRIATTN_OK : TRIATTN_ERR_CUDA;
+  return ln_grads() ? TRIATTN_OK : TRIATTN_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,8 +1,10 @@
-// Activations of the transition, shared by its kernels.
+// Activations and tensor maps of the transition, shared by its kernels.
 #pragma once
+#include <cudaTypedefs.h>
+
 #include <type_traits>
 
-#include "ptx.cuh"
+#include "kernels.cuh"
 #include "triattn.h"
 
 namespace triattn {
@@ -50,6 +52,17 @@ cudaError_t by_act(int act, F&& f) {
     case TRIATTN_ACT_GELU: return f(std::integral_constant<int, TRIATTN_ACT_GELU>{});
   }
   return cudaErrorInvalidValue;
+}
+
+// 3-D BF16 map in boxes of 64 (inner) x box1 x box2, 128-byte swizzle.
+inline bool tf_map(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+                   cuuint32_t box1, cuuint32_t box2) {
+  const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (enc == nullptr) return false;
+  const cuuint32_t box[3] = {64u, box1, box2}, es[3] = {1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace

@@ -21,8 +21,6 @@
 // 2-5 normalise the next tile's rows (thread = row) and drain out; 6-21 the
 // activation, eight warps per stage, so that a chunk's arithmetic may take the
 // time of two chunks' MMAs.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <cstring>
 
@@ -336,16 +334,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
-}
-
-bool tf_map(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
-            cuuint32_t box1, cuuint32_t box2) {
-  const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
-  if (enc == nullptr) return false;
-  const cuuint32_t box[3] = {64u, box1, box2}, es[3] = {1u, 1u, 1u};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int C, int ACT>

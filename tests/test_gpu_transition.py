@@ -341,3 +341,28 @@ def test_refusals_on_device():
     odd = torch.empty(8 * 64 + 4, dtype=torch.bfloat16, device="cuda")[4:].view(8, 64)  # 8-byte aligned
     with pytest.raises(T.TriAttnError):
         T.triattn_transition_fwd(odd, None, lw, lb, wi, wo)
+
+
+@pytest.mark.parametrize("C,H", [(128, 512), (96, 64), (256, 64)])
+def test_tensors_on_16_byte_boundaries(C, H):
+    """Row tensors and the mask that start at odd multiples of 16 (2) bytes give
+    the same bits, written into views aligned the same way."""
+    M = 333
+    x = S.make_transition_inputs((M,), C, H, seed=30, drop=0.2)
+    ref = run_gpu(x)
+    d = to_dev(x)
+
+    def shifted(t, by):
+        buf = torch.empty(t.numel() + 64, dtype=t.dtype, device="cuda")
+        v = buf[by:by + t.numel()].view(t.shape)
+        return v.copy_(t)
+
+    for k in ("z", "d_out", "w_in", "w_o"):
+        d[k] = shifted(d[k], 8)
+    d["ln_w"], d["ln_b"], d["mask"] = shifted(d["ln_w"], 4), shifted(d["ln_b"], 4), shifted(d["mask"], 1)
+    out = T.triattn_transition_fwd(*params(d), out=shifted(ref[0], 8))
+    grads = T.triattn_transition_bwd(*params(d), d["d_out"], out=tuple(
+        shifted(t, 8 if t.dtype == torch.bfloat16 else 4) for t in ref[1:]))
+    torch.cuda.synchronize()
+    for a, b in zip(ref, (out,) + tuple(grads)):
+        assert torch.equal(a, b)
