@@ -431,34 +431,16 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrival on the barrier at the same shared-memory offset in CTA `rank`.
+// Arrival on the barrier at the same shared-memory offset in CTA `rank`.  What
+// it hands over lies in TMEM (ordered by the tcgen05 fences on both sides) or
+// was written by TMA; at cluster scope the release would also wait for every
+// global store of the thread, and the acquire would drop the L1 cache.
 __device__ __forceinline__ void mbar_arrive_cta(uint64_t* bar, uint32_t rank) {
   asm volatile(
       "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n"
-      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar)),
+      " mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar)),
       "r"(rank)
       : "memory");
-}
-// Bounded wait that also acquires what the other CTA's arrivals released.
-static __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, const WaitCtl& wc,
-                                                         volatile int* abort) {
-  const uint64_t t0 = global_timer_ns();
-  for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendHintNs)
-        : "memory");
-    if (ok != 0) return true;
-    if (*abort) return false;
-    if (global_timer_ns() - t0 > wc.limit_ns) {
-      atomicOr(wc.status, kDevTimeout);
-      *abort = 1;
-      return false;
-    }
-  }
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols));

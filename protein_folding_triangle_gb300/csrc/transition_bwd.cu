@@ -208,7 +208,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTbThreads, 1)
       const uint64_t d_ring = smem_desc(smem_u32(s_ring), 16, 1024, 2);
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, wc, abort));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, wc, abort));
       };
       int t = 0, i = 0, slot = 0, phase = 0;  // of the next [a | b]
       int xt = 0, xi = 0, xslot = 0;          // of the next dx

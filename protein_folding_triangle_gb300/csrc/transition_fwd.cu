@@ -14,13 +14,17 @@
 //   [a | b] = x [W_a | W_b] chunk      M = 256, N = 128, A = x in TMEM
 //   h = act(a) b                       registers, BF16 back into TMEM
 //   out += h W_o chunk                 M = 256, N = C, A = h in TMEM
-// h overwrites columns of a that its own warp has read, so two stages of
-// [a | b], out and two x tiles fill the 512 TMEM columns at C = 128.
+// x, out, two stages of h and two of [a | b] fill the 512 TMEM columns at
+// C = 128.  A stage of [a | b] is free for the next chunk but one as soon as
+// the activation has read it, whatever becomes of its h.
 //
-// Warps: 0 loads the weights; 1 (of CTA 0) issues the MMAs of both CTAs;
-// 2-5 normalise the next tile's rows (thread = row) and drain out; 6-21 the
-// activation, eight warps per stage, so that a chunk's arithmetic may take the
-// time of two chunks' MMAs.
+// Warps: 0 loads the weights; 1 and 22 (of CTA 0) issue the MMAs of both CTAs,
+// one the input projections, one the output projection: a wait costs an
+// issuer some 200 clocks even when the phase is complete, and the tensor
+// cores' queue is shorter than that (one issuer for both kept them busy for
+// 60% of the time); 2-5 normalise the next tile's rows (thread = row) and
+// drain out; 6-21 the activation, eight warps per stage, so that a chunk's
+// arithmetic may take the time of two chunks' MMAs.
 #include <algorithm>
 #include <cstring>
 
@@ -30,7 +34,7 @@
 namespace triattn {
 namespace {
 
-constexpr int kTfWarps = 22;
+constexpr int kTfWarps = 23;
 constexpr int kTfThreads = kTfWarps * 32;
 constexpr int kTfMaxChunks = 32;
 constexpr int kTfBarBytes = 2048;  // barriers (under 1 KB), ln_w and ln_b (1 KB)
@@ -40,9 +44,9 @@ struct TfBars {
   uint64_t w_load[kTfMaxChunks];   // a chunk's weights are in this CTA (TMA bytes)
   uint64_t w_ready[kTfMaxChunks];  // ... in both CTAs (CTA 0)
   uint64_t z_full;                 // z tile in shared memory (TMA bytes)
-  uint64_t x_full[2], x_free[2];   // x tile written (CTA 0) / read by its last MMA (both)
-  uint64_t ab_full[2];             // [a | b] of a stage complete (both)
-  uint64_t h_full[2];              // h of a stage written (CTA 0)
+  uint64_t x_full, x_free;         // x tile written (CTA 0) / read by its last MMA (both)
+  uint64_t ab_full[2], ab_free[2]; // [a | b] of a stage complete (both) / read (CTA 0)
+  uint64_t h_full[2], h_free[2];   // h of a stage written (CTA 0) / read (both)
   uint64_t out_full, out_free;     // out complete (both) / drained (CTA 0)
   uint32_t tmem_slot;
   int abort;
@@ -72,7 +76,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
                           const __grid_constant__ CUtensorMap tm_win, const __grid_constant__ CUtensorMap tm_wo,
                           const TfParams p) {
   using L = TfSmem<C>;
-  constexpr uint32_t kX = 0, kOut = C, kAB = 256;  // TMEM columns: x0 x1 (C/2 each), out, two [a | b] stages
+  constexpr uint32_t kX = 0, kOut = 64, kH = 192, kAB = 256;  // TMEM columns; two stages of h (32) and [a | b] (128)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const s_win = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const s_wo = s_win + p.chunks * L::kWin;
@@ -85,6 +89,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int mine = p.tiles > pair ? (p.tiles - 1 - pair) / pairs + 1 : 0;  // tiles of this pair
+  const long long total = static_cast<long long>(mine) * p.chunks;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.chunks; ++i) {
@@ -92,11 +98,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
       mbar_init(&bars->w_ready[i], 2);
     }
     mbar_init(&bars->z_full, 1);
+    mbar_init(&bars->x_full, 8);
+    mbar_init(&bars->x_free, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->x_full[i], 8);
-      mbar_init(&bars->x_free[i], 1);
       mbar_init(&bars->ab_full[i], 1);
+      mbar_init(&bars->ab_free[i], 16);
       mbar_init(&bars->h_full[i], 16);
+      mbar_init(&bars->h_free[i], 1);
     }
     mbar_init(&bars->out_full, 1);
     mbar_init(&bars->out_free, 8);
@@ -128,53 +136,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------ MMA issuer: [a | b]
     if (rank == 0) {
-      constexpr uint32_t id_ab = idesc_bf16_f32(256, 128, 0, 1), id_out = idesc_bf16_f32(256, C, 0, 1);
-      const uint32_t wi = smem_u32(s_win), wo = smem_u32(s_wo);
-      const int mine = p.tiles > pair ? (p.tiles - 1 - pair) / pairs + 1 : 0;
-      const long long total = static_cast<long long>(mine) * p.chunks;
+      constexpr uint32_t id_ab = idesc_bf16_f32(256, 128, 0, 1);
+      const uint64_t d_win = smem_desc(smem_u32(s_win), 64 * 128, 1024, 2);  // an offset of n bytes adds n / 16
       bool ok = true;
-      int at = 0, ai = 0;  // tile and chunk of the next [a | b]
-      long long ag = 0;
-      auto issue_ab = [&]() {
-        const int xb = at & 1;
-        if (ai == 0) ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&bars->x_full[xb], (at >> 1) & 1, wc, abort));
-        if (at == 0) ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&bars->w_ready[ai], 0, wc, abort));
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t st = static_cast<uint32_t>(ag & 1);
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < C / 16; ++k)
-            mma_ts_pair(tmem + kAB + 128 * st, tmem + kX + xb * (C / 2) + 8 * k,
-                        smem_desc(wi + ai * L::kWin + k * 2048, 64 * 128, 1024, 2), id_ab, k > 0 ? 1u : 0u);
-          mma_commit_pair(&bars->ab_full[st]);
-          if (ai == p.chunks - 1) mma_commit_pair(&bars->x_free[xb]);
-        }
-        __syncwarp();
-        ++ag;
-        if (++ai == p.chunks) {
-          ai = 0;
-          ++at;
-        }
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, wc, abort));
       };
-      if (ag < total) issue_ab();
-      if (ok && ag < total) issue_ab();
       int t = 0, i = 0;
-      for (long long g = 0; g < total && ok; ++g) {
+      for (long long g = 0; g < total; ++g) {
         const uint32_t st = static_cast<uint32_t>(g & 1);
-        ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bars->h_full[st], (g >> 1) & 1, wc, abort));
-        if (ok && i == 0 && t > 0)
-          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bars->out_free, (t - 1) & 1, wc, abort));
+        if (g >= 2) wait(&bars->ab_free[st], static_cast<uint32_t>((g >> 1) - 1) & 1);
+        if (i == 0) wait(&bars->x_full, t & 1);
+        if (t == 0) wait(&bars->w_ready[i], 0);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          // K steps 0, 1 of h at columns 0, 8 of the stage, steps 2, 3 at 32, 40
+          const uint64_t w = d_win + i * (L::kWin / 16);
+#pragma unroll
+          for (int k = 0; k < C / 16; ++k)
+            mma_ts_pair(tmem + kAB + 128 * st, tmem + kX + 8 * k, w + k * (2048 / 16), id_ab, k > 0 ? 1u : 0u);
+          mma_commit_pair(&bars->ab_full[st]);
+          if (i == p.chunks - 1) mma_commit_pair(&bars->x_free);
+        }
+        __syncwarp();
+        if (++i == p.chunks) {
+          i = 0;
+          ++t;
+        }
+      }
+    }
+  } else if (warp == kTfWarps - 1) {
+    // ------------------------------------------------------------ MMA issuer: out
+    if (rank == 0) {
+      constexpr uint32_t id_out = idesc_bf16_f32(256, C, 0, 1);
+      const uint64_t d_wo = smem_desc(smem_u32(s_wo), 64 * 128, 1024, 2);
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, wc, abort));
+      };
+      int t = 0, i = 0;
+      for (long long g = 0; g < total; ++g) {
+        const uint32_t st = static_cast<uint32_t>(g & 1);
+        if (t == 0) wait(&bars->w_ready[i], 0);
+        if (i == 0 && t > 0) wait(&bars->out_free, (t - 1) & 1);
+        wait(&bars->h_full[st], (g >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t w = d_wo + i * (L::kWo / 16);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ts_pair(tmem + kOut, tmem + kAB + 128 * st + (k >> 1) * 32 + (k & 1) * 8,
-                        smem_desc(wo + i * L::kWo + k * 2048, 64 * 128, 1024, 2), id_out, (i > 0 || k > 0) ? 1u : 0u);
+            mma_ts_pair(tmem + kOut, tmem + kH + 32 * st + 8 * k, w + k * (2048 / 16), id_out,
+                        (i > 0 || k > 0) ? 1u : 0u);
+          mma_commit_pair(&bars->h_free[st]);
           if (i == p.chunks - 1) mma_commit_pair(&bars->out_full);
         }
         __syncwarp();
@@ -182,8 +198,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
           i = 0;
           ++t;
         }
-        // the stage's h has been read by MMAs issued before: the next [a | b] may follow
-        if (ag < total) issue_ab();
       }
     }
   } else if (warp < 6) {
@@ -198,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
         tma_load_3d(s_z + b * 16384, &tm_z, &bars->z_full, 64 * b, tile * 256 + static_cast<int>(rank) * 128, 0);
     };
     auto z16 = [&](int c) { return reinterpret_cast<uint4*>(s_z + (c >> 3) * 16384 + sw128(r, c & 7)); };
-    // x of local tile u into its TMEM buffer: the row's statistics in two passes
+    // x of local tile u into TMEM once the previous tile's is read: the row's statistics in two passes
     auto normalise = [&](int u) -> bool {
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->z_full, u & 1, wc, abort))) return false;
       float s = 0.f;
@@ -221,8 +235,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
         }
       }
       const float rstd = rsqrtf(q * (1.f / C) + 1e-5f);
-      if (u >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bars->x_free[u & 1], ((u >> 1) - 1) & 1, wc, abort)))
-        return false;
+      if (u > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->x_free, (u - 1) & 1, wc, abort))) return false;
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < C / 8; c += 2) {  // 16 features = 8 columns at a time
@@ -242,15 +255,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
                                                fmaf((bf16hi_to_f32(ws[2 * e + 1]) - mean) * rstd, g.w, b.w));
           }
         }
-        tmem_st8(tmem + lane_addr + kX + (u & 1) * (C / 2) + 4 * c, x);
+        tmem_st8(tmem + lane_addr + kX + 4 * c, x);
       }
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cta(&bars->x_full[u & 1], 0);
+      if (lane == 0) mbar_arrive_cta(&bars->x_full, 0);
       return true;
     };
-    const int mine = p.tiles > pair ? (p.tiles - 1 - pair) / pairs + 1 : 0;
     bool ok = mine > 0;
     if (ok) {
       if (first) load_z(pair);
@@ -304,22 +316,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
   } else {
     // ------------------------------------------------------------ activation
     const int idx = warp - 6, st = idx >> 3, hf = (idx >> 2) & 1, quarter = warp & 3;
-    const uint32_t base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kAB + 128 * st + 32 * hf;
-    const int mine = p.tiles > pair ? (p.tiles - 1 - pair) / pairs + 1 : 0;
-    const long long total = static_cast<long long>(mine) * p.chunks;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t ab = lanes + kAB + 128 * st + 32 * hf, hcol = lanes + kH + 32 * st + 16 * hf;
     for (long long g = st; g < total; g += 2) {
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->ab_full[st], (g >> 1) & 1, wc, abort))) break;
       tc_fence_after();
+      bool ok = true;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         uint32_t a[16], b[16], h[8];
-        tmem_ld16x2_wait(base + 16 * j, a, base + 64 + 16 * j, b);
+        tmem_ld16x2_wait(ab + 16 * j, a, ab + 64 + 16 * j, b);
+        if (j == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cta(&bars->ab_free[st], 0);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           h[e] = pack_bf16x2(act_fwd<ACT>(__uint_as_float(a[2 * e])) * __uint_as_float(b[2 * e]),
                              act_fwd<ACT>(__uint_as_float(a[2 * e + 1])) * __uint_as_float(b[2 * e + 1]));
-        tmem_st8(base + 8 * j, h);  // over columns of a this warp has read
+        if (j == 0 && g >= 2) {  // the out MMAs of the chunk before last have read this stage's h
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->h_free[st], static_cast<uint32_t>((g >> 1) - 1) & 1, wc, abort));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        tmem_st8(hcol + 8 * j, h);
       }
+      if (!ok) break;
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
