@@ -43,6 +43,55 @@ __device__ __forceinline__ void act_both(float a, float& f, float& df) {
   }
 }
 
+// The same for two features at once on packed FP32 pairs, with the product:
+// h = act(a) b.
+template <int ACT>
+__device__ __forceinline__ float2 gate_fwd2(float2 a, float2 b) {
+  const float2 half = make_float2(0.5f, 0.5f);
+  const float2 ha = fmul2(a, half);
+  float2 u = ha, p = fmul2(ha, b);
+  if constexpr (ACT == TRIATTN_ACT_GELU) {
+    const float2 q = ffma2(fmul2(a, a), make_float2(0.0356774081f, 0.0356774081f),
+                           make_float2(0.7978845608f, 0.7978845608f));
+    u = fmul2(a, q);
+  }
+  if constexpr (ACT == TRIATTN_ACT_SIGMOID) p = fmul2(b, half);
+  const float2 t = make_float2(tanh_approx(u.x), tanh_approx(u.y));
+  return ffma2(p, t, p);
+}
+// ... and h, da = d b act'(a), db = d act(a).
+template <int ACT>
+__device__ __forceinline__ void gate_bwd2(float2 a, float2 b, float2 d, float2& h, float2& da, float2& db) {
+  const float2 half = make_float2(0.5f, 0.5f);
+  const float2 ha = fmul2(a, half);
+  float2 f, df;
+  if constexpr (ACT == TRIATTN_ACT_GELU) {
+    const float2 a2 = fmul2(a, a), c1 = make_float2(0.7978845608f, 0.7978845608f);
+    const float2 u = fmul2(a, ffma2(a2, make_float2(0.0356774081f, 0.0356774081f), c1));
+    const float2 t = make_float2(tanh_approx(u.x), tanh_approx(u.y));
+    f = ffma2(ha, t, ha);
+    const float2 w = fmul2(ha, ffma2(a2, make_float2(0.1070322243f, 0.1070322243f), c1));
+    const float2 wt = fmul2(w, t);
+    df = fadd2(ffma2(make_float2(-wt.x, -wt.y), t, w), ffma2(t, half, half));
+  } else {
+    const float2 t = make_float2(tanh_approx(ha.x), tanh_approx(ha.y));
+    const float2 s = ffma2(t, half, half);
+    if constexpr (ACT == TRIATTN_ACT_SILU) {
+      f = ffma2(ha, t, ha);
+      df = fadd2(ffma2(make_float2(-f.x, -f.y), s, f), s);
+    } else {
+      f = s;
+      df = ffma2(make_float2(-s.x, -s.y), s, s);
+    }
+  }
+  h = fmul2(f, b);
+  db = fmul2(d, f);
+  da = fmul2(fmul2(d, b), df);
+}
+__device__ __forceinline__ float2 bf16x2_to_f32x2(uint32_t w) {
+  return make_float2(bf16lo_to_f32(w), bf16hi_to_f32(w));
+}
+
 // f(std::integral_constant<int, ACT>) for the activations.
 template <typename F>
 cudaError_t by_act(int act, F&& f) {
@@ -54,15 +103,23 @@ cudaError_t by_act(int act, F&& f) {
   return cudaErrorInvalidValue;
 }
 
-// 3-D BF16 map in boxes of 64 (inner) x box1 x box2, 128-byte swizzle.
-inline bool tf_map(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
-                   cuuint32_t box1, cuuint32_t box2) {
+// 3-D BF16 maps: boxes of 64 (inner) x box1 x box2 with the 128-byte swizzle,
+// and (tf_map32) boxes of 32 x 32 with the 64-byte swizzle.
+inline bool tf_map_box(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+                       cuuint32_t box0, cuuint32_t box1, cuuint32_t box2, CUtensorMapSwizzle swizzle) {
   const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
   if (enc == nullptr) return false;
-  const cuuint32_t box[3] = {64u, box1, box2}, es[3] = {1u, 1u, 1u};
+  const cuuint32_t box[3] = {box0, box1, box2}, es[3] = {1u, 1u, 1u};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+inline bool tf_map(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+                   cuuint32_t box1, cuuint32_t box2) {
+  return tf_map_box(m, base, dims, strides, 64u, box1, box2, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+inline bool tf_map32(CUtensorMap* m, void* base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2]) {
+  return tf_map_box(m, base, dims, strides, 32u, 32u, 1u, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 }  // namespace

@@ -4,11 +4,11 @@
 //
 // A pair of CTAs (cluster of two, tcgen05 cta_group::2) takes tiles of 256
 // rows, 128 per CTA.  With cta_group::2 each CTA holds one half of the N
-// columns of every B operand, so the pair's shared memory holds all weights
-// and they are loaded once per pair, not once per tile: CTA 0 keeps W_a and
-// columns [0, C/2) of W_o, CTA 1 W_b and columns [C/2, C) (192 KB each at
-// C = 128, H = 512; one CTA alone could not hold them, and streaming them for
-// every 128 rows would take 54 bytes per clock and SM from L2).
+// columns of every B operand: CTA 0 W_a and columns [0, C/2) of W_o, CTA 1 W_b
+// and columns [C/2, C).  W_in is loaded once per pair and stays (128 KB per
+// CTA at C = 128, H = 512; streaming it for every 128 rows would take 36 bytes
+// per clock and SM from L2); W_o, a third of the bytes, comes through a ring
+// of chunks, which leaves room for two z tiles.
 //
 // Per tile and 64-wide hidden chunk i (K = C, then K = 64):
 //   [a | b] = x [W_a | W_b] chunk      M = 256, N = 128, A = x in TMEM
@@ -18,13 +18,14 @@
 // C = 128.  A stage of [a | b] is free for the next chunk but one as soon as
 // the activation has read it, whatever becomes of its h.
 //
-// Warps: 0 loads the weights; 1 and 22 (of CTA 0) issue the MMAs of both CTAs,
+// Warps: 0 loads the weights, 3 tells CTA 0 that this CTA's are in; 1 and 2 (of CTA 0) issue the MMAs of both CTAs,
 // one the input projections, one the output projection: a wait costs an
 // issuer some 200 clocks even when the phase is complete, and the tensor
 // cores' queue is shorter than that (one issuer for both kept them busy for
-// 60% of the time); 2-5 normalise the next tile's rows (thread = row) and
-// drain out; 6-21 the activation, eight warps per stage, so that a chunk's
-// arithmetic may take the time of two chunks' MMAs.
+// 60% of the time); 4-7 normalise the next tile's rows, 8-11 drain out
+// (thread = row for both; one group for both took 10,000 clocks a tile,
+// more than its MMAs); 12-27 the activation, eight warps per stage, so that a
+// chunk's arithmetic may take the time of two chunks' MMAs.
 #include <algorithm>
 #include <cstring>
 
@@ -34,16 +35,21 @@
 namespace triattn {
 namespace {
 
-constexpr int kTfWarps = 23;
-constexpr int kTfThreads = kTfWarps * 32;
+constexpr int kTfThreads = 28 * 32;
+// Registers per thread of the warpgroups (setmaxnreg): seven shares of what
+// the block was launched with (72 each).
+constexpr int kTfRegsIssue = 40, kTfRegsLn = 56, kTfRegsOut = 88, kTfRegsAct = 80;
+constexpr int kTfRegsSum = kTfRegsIssue + kTfRegsLn + kTfRegsOut + 4 * kTfRegsAct;
 constexpr int kTfMaxChunks = 32;
+constexpr int kTfSlots = 3;  // W_o ring
 constexpr int kTfBarBytes = 2048;  // barriers (under 1 KB), ln_w and ln_b (1 KB)
 constexpr int kTfSmemMax = 232448;
 
 struct TfBars {
-  uint64_t w_load[kTfMaxChunks];   // a chunk's weights are in this CTA (TMA bytes)
+  uint64_t w_load[kTfMaxChunks];   // a chunk of W_in is in this CTA (TMA bytes)
   uint64_t w_ready[kTfMaxChunks];  // ... in both CTAs (CTA 0)
-  uint64_t z_full;                 // z tile in shared memory (TMA bytes)
+  uint64_t o_load[kTfSlots], o_ready[kTfSlots], o_empty[kTfSlots];  // the same for W_o's ring; read (both)
+  uint64_t z_full[2];              // z tile in shared memory (TMA bytes)
   uint64_t x_full, x_free;         // x tile written (CTA 0) / read by its last MMA (both)
   uint64_t ab_full[2], ab_free[2]; // [a | b] of a stage complete (both) / read (CTA 0)
   uint64_t h_full[2], h_free[2];   // h of a stage written (CTA 0) / read (both)
@@ -67,7 +73,10 @@ struct TfSmem {
   static constexpr int kZ = kZBoxes * 16384;
   static constexpr int kWin = C * 128;   // one chunk: C rows (K) of 64 columns
   static constexpr int kWo = 64 * 128;   // one chunk: 64 rows (K) of 64 columns, C / 2 of them used
-  static constexpr int bytes(int chunks) { return chunks * (kWin + kWo) + kZ + kTfBarBytes + 1024; }  // + alignment
+  static constexpr int kStg = 4 * 2048;  // out's staging: 32 rows of 32 features per warp
+  static constexpr int bytes(int chunks) {
+    return chunks * kWin + kTfSlots * kWo + 2 * kZ + kStg + kTfBarBytes + 1024;  // + alignment
+  }
 };
 
 template <int C, int ACT>
@@ -80,9 +89,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const s_win = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const s_wo = s_win + p.chunks * L::kWin;
-  uint8_t* const s_z = s_wo + p.chunks * L::kWo;
-  TfBars* const bars = reinterpret_cast<TfBars*>(s_z + L::kZ);
-  float* const s_gam = reinterpret_cast<float*>(s_z + L::kZ + 1024);
+  uint8_t* const s_z = s_wo + kTfSlots * L::kWo;
+  uint8_t* const s_stg = s_z + 2 * L::kZ;
+  TfBars* const bars = reinterpret_cast<TfBars*>(s_stg + L::kStg);
+  float* const s_gam = reinterpret_cast<float*>(s_stg + L::kStg + 1024);
   float* const s_bet = s_gam + C;
   volatile int* abort = &bars->abort;
   const WaitCtl& wc = p.wc;
@@ -97,10 +107,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
       mbar_init(&bars->w_load[i], 1);
       mbar_init(&bars->w_ready[i], 2);
     }
-    mbar_init(&bars->z_full, 1);
+    for (int i = 0; i < kTfSlots; ++i) {
+      mbar_init(&bars->o_load[i], 1);
+      mbar_init(&bars->o_ready[i], 2);
+      mbar_init(&bars->o_empty[i], 1);
+    }
     mbar_init(&bars->x_full, 8);
     mbar_init(&bars->x_free, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->z_full[i], 1);
       mbar_init(&bars->ab_full[i], 1);
       mbar_init(&bars->ab_free[i], 16);
       mbar_init(&bars->h_full[i], 16);
@@ -122,17 +137,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_slot;
 
+  if (warp < 4) regs_dec<kTfRegsIssue>();
   if (warp == 0) {
     // ------------------------------------------------------------ weights
     if (lane == 0) {
-      for (int i = 0; i < p.chunks; ++i) {
-        mbar_expect_tx(&bars->w_load[i], L::kWin + L::kWo);
+      auto load_win = [&](int i) {
+        mbar_expect_tx(&bars->w_load[i], L::kWin);
         tma_load_3d(s_win + i * L::kWin, &tm_win, &bars->w_load[i], 64 * i, static_cast<int>(rank), 0);
-        tma_load_3d(s_wo + i * L::kWo, &tm_wo, &bars->w_load[i], static_cast<int>(rank) * (C / 2), 64 * i, 0);
+      };
+      load_win(0);
+      int slot = 0, phase = 0, i = 0;
+      for (long long g = 0; g < total; ++g) {
+        if (g == 1) {  // behind the first chunk's weights, the rest of W_in
+          for (int k = 1; k < p.chunks; ++k) load_win(k);
+        }
+        if (!mbar_wait(&bars->o_empty[slot], phase ^ 1, wc, abort)) break;
+        mbar_expect_tx(&bars->o_load[slot], L::kWo);
+        tma_load_3d(s_wo + slot * L::kWo, &tm_wo, &bars->o_load[slot], static_cast<int>(rank) * (C / 2), 64 * i, 0);
+        if (++i == p.chunks) i = 0;
+        if (++slot == kTfSlots) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
-      for (int i = 0; i < p.chunks; ++i) {
-        if (!mbar_wait(&bars->w_load[i], 0, wc, abort)) break;
-        mbar_arrive_cta(&bars->w_ready[i], 0);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ weights' arrival, to CTA 0
+    if (lane == 0) {
+      int slot = 0, phase = 0;
+      for (long long g = 0; g < total; ++g) {
+        if (g < p.chunks) {
+          if (!mbar_wait(&bars->w_load[g], 0, wc, abort)) break;
+          mbar_arrive_cta(&bars->w_ready[g], 0);
+        }
+        if (!mbar_wait(&bars->o_load[slot], phase, wc, abort)) break;
+        mbar_arrive_cta(&bars->o_ready[slot], 0);
+        if (++slot == kTfSlots) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
     }
   } else if (warp == 1) {
@@ -167,7 +210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
         }
       }
     }
-  } else if (warp == kTfWarps - 1) {
+  } else if (warp == 2) {
     // ------------------------------------------------------------ MMA issuer: out
     if (rank == 0) {
       constexpr uint32_t id_out = idesc_bf16_f32(256, C, 0, 1);
@@ -176,86 +219,118 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, wc, abort));
       };
-      int t = 0, i = 0;
+      int t = 0, i = 0, slot = 0, phase = 0;
       for (long long g = 0; g < total; ++g) {
         const uint32_t st = static_cast<uint32_t>(g & 1);
-        if (t == 0) wait(&bars->w_ready[i], 0);
+        wait(&bars->o_ready[slot], phase);
         if (i == 0 && t > 0) wait(&bars->out_free, (t - 1) & 1);
         wait(&bars->h_full[st], (g >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t w = d_wo + i * (L::kWo / 16);
+          const uint64_t w = d_wo + slot * (L::kWo / 16);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_ts_pair(tmem + kOut, tmem + kH + 32 * st + 8 * k, w + k * (2048 / 16), id_out,
                         (i > 0 || k > 0) ? 1u : 0u);
           mma_commit_pair(&bars->h_free[st]);
+          mma_commit_pair(&bars->o_empty[slot]);
           if (i == p.chunks - 1) mma_commit_pair(&bars->out_full);
         }
         __syncwarp();
+        if (++slot == kTfSlots) {
+          slot = 0;
+          phase ^= 1;
+        }
         if (++i == p.chunks) {
           i = 0;
           ++t;
         }
       }
     }
-  } else if (warp < 6) {
-    // ------------------------------------------------------------ rows
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------------ x = LayerNorm(z)
+    regs_dec<kTfRegsLn>();
     const int quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-    const bool first = warp == 2 && lane == 0;
-    auto load_z = [&](int tile) {
-      mbar_expect_tx(&bars->z_full, L::kZ);
+    const bool first = warp == 4 && lane == 0;
+    auto load_z = [&](int u) {
+      const int row = (pair + u * pairs) * 256 + static_cast<int>(rank) * 128;
+      uint64_t* const bar = &bars->z_full[u & 1];
+      mbar_expect_tx(bar, L::kZ);
 #pragma unroll
       for (int b = 0; b < L::kZBoxes; ++b)
-        tma_load_3d(s_z + b * 16384, &tm_z, &bars->z_full, 64 * b, tile * 256 + static_cast<int>(rank) * 128, 0);
+        tma_load_3d(s_z + (u & 1) * L::kZ + b * 16384, &tm_z, bar, 64 * b, row, 0);
     };
-    auto z16 = [&](int c) { return reinterpret_cast<uint4*>(s_z + (c >> 3) * 16384 + sw128(r, c & 7)); };
-    // x of local tile u into TMEM once the previous tile's is read: the row's statistics in two passes
     auto normalise = [&](int u) -> bool {
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars->z_full, u & 1, wc, abort))) return false;
-      float s = 0.f;
-#pragma unroll 4
-      for (int c = 0; c < C / 8; ++c) {
-        const uint4 w = *z16(c);
-        s += ((bf16lo_to_f32(w.x) + bf16hi_to_f32(w.x)) + (bf16lo_to_f32(w.y) + bf16hi_to_f32(w.y))) +
-             ((bf16lo_to_f32(w.z) + bf16hi_to_f32(w.z)) + (bf16lo_to_f32(w.w) + bf16hi_to_f32(w.w)));
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->z_full[u & 1], (u >> 1) & 1, wc, abort))) return false;
+      uint8_t* const zt = s_z + (u & 1) * L::kZ;
+      auto z16 = [&](int c) { return reinterpret_cast<uint4*>(zt + (c >> 3) * 16384 + sw128(r, c & 7)); };
+      // Mean and variance in one pass, about the mean k of the row's first 8
+      // features: |k - mean| is at most sqrt((C - 8) / 8) < 4 standard
+      // deviations whatever the row holds, so that the difference below
+      // loses less than a factor of 17 of the FP32 precision.
+      float2 k2;
+      {
+        const uint4 w = *z16(0);
+        k2 = fadd2(fadd2(bf16x2_to_f32x2(w.x), bf16x2_to_f32x2(w.y)),
+                   fadd2(bf16x2_to_f32x2(w.z), bf16x2_to_f32x2(w.w)));
       }
-      const float mean = s * (1.f / C);
-      float q = 0.f;
+      const float k = (k2.x + k2.y) * 0.125f;
+      const float2 nk = make_float2(-k, -k);
+      float2 s2[2], q2[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) s2[e] = q2[e] = make_float2(0.f, 0.f);
 #pragma unroll 4
       for (int c = 0; c < C / 8; ++c) {
         const uint4 w = *z16(c);
         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float a = bf16lo_to_f32(ws[e]) - mean, b = bf16hi_to_f32(ws[e]) - mean;
-          q = fmaf(a, a, fmaf(b, b, q));
+          const float2 d = fadd2(bf16x2_to_f32x2(ws[e]), nk);
+          s2[e & 1] = fadd2(s2[e & 1], d);
+          q2[e & 1] = ffma2(d, d, q2[e & 1]);
         }
       }
-      const float rstd = rsqrtf(q * (1.f / C) + 1e-5f);
+      const float2 ss = fadd2(s2[0], s2[1]), qq = fadd2(q2[0], q2[1]);
+      const float ds = (ss.x + ss.y) * (1.f / C);  // mean - k
+      const float mean = k + ds;
+      const float rstd = rsqrtf(fmaxf(fmaf(-ds, ds, (qq.x + qq.y) * (1.f / C)), 0.f) + 1e-5f);
+      const float2 nm = make_float2(-mean, -mean), rs = make_float2(rstd, rstd);
+      // x over z in shared memory first, so that little is left to do once the
+      // previous tile's x has been read
+#pragma unroll 4
+      for (int c = 0; c < C / 8; ++c) {
+        const uint4 w = *z16(c);
+        uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        const float4* gm = reinterpret_cast<const float4*>(s_gam + 8 * c);
+        const float4* bt = reinterpret_cast<const float4*>(s_bet + 8 * c);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 g = gm[e], b = bt[e];
+          const float2 x0 = ffma2(fmul2(fadd2(bf16x2_to_f32x2(ws[2 * e]), nm), rs), make_float2(g.x, g.y),
+                                  make_float2(b.x, b.y));
+          const float2 x1 = ffma2(fmul2(fadd2(bf16x2_to_f32x2(ws[2 * e + 1]), nm), rs), make_float2(g.z, g.w),
+                                  make_float2(b.z, b.w));
+          ws[2 * e] = pack_bf16x2(x0.x, x0.y);
+          ws[2 * e + 1] = pack_bf16x2(x1.x, x1.y);
+        }
+        *z16(c) = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+      }
       if (u > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->x_free, (u - 1) & 1, wc, abort))) return false;
       tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < C / 8; c += 2) {  // 16 features = 8 columns at a time
-        uint32_t x[8];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+      for (int c = 0; c < C / 8; c += 4) {  // 32 features = 16 columns at a time
+        uint32_t x[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
           const uint4 w = *z16(c + j);
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-          const float4* gm = reinterpret_cast<const float4*>(s_gam + 8 * (c + j));
-          const float4* bt = reinterpret_cast<const float4*>(s_bet + 8 * (c + j));
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float4 g = gm[e], b = bt[e];
-            x[4 * j + 2 * e] = pack_bf16x2(fmaf((bf16lo_to_f32(ws[2 * e]) - mean) * rstd, g.x, b.x),
-                                           fmaf((bf16hi_to_f32(ws[2 * e]) - mean) * rstd, g.y, b.y));
-            x[4 * j + 2 * e + 1] = pack_bf16x2(fmaf((bf16lo_to_f32(ws[2 * e + 1]) - mean) * rstd, g.z, b.z),
-                                               fmaf((bf16hi_to_f32(ws[2 * e + 1]) - mean) * rstd, g.w, b.w));
-          }
+          x[4 * j] = w.x;
+          x[4 * j + 1] = w.y;
+          x[4 * j + 2] = w.z;
+          x[4 * j + 3] = w.w;
         }
-        tmem_st8(tmem + lane_addr + kX + 4 * c, x);
+        tmem_st16(tmem + lane_addr + kX + 4 * c, x);
       }
       tc_wait_st();
       tc_fence_before();
@@ -263,68 +338,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
       if (lane == 0) mbar_arrive_cta(&bars->x_full, 0);
       return true;
     };
-    bool ok = mine > 0;
-    if (ok) {
-      if (first) load_z(pair);
-      ok = normalise(0);
+    if (first && mine > 0) load_z(0);
+    if (first && mine > 1) load_z(1);
+    bool ok = true;
+    for (int u = 0; u < mine; ++u) {  // no warp leaves the loop early: they meet at its barrier
+      ok = ok && normalise(u);
+      fence_proxy_async_smem();
       __syncwarp();
-      named_bar_sync(1, 128);  // every row of the z tile is read
-      if (first && mine > 1) load_z(pair + pairs);
+      named_bar_sync(1, 128);  // every row of the tile is in TMEM
+      if (first && ok && u + 2 < mine) load_z(u + 2);
     }
+  } else if (warp >= 8 && warp < 12) {
+    // ------------------------------------------------------------ out
+    regs_inc<kTfRegsOut>();
+    const int quarter = warp & 3;
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    uint8_t* const stg = s_stg + quarter * 2048;
     for (int u = 0; u < mine; ++u) {
-      // next tile's rows before this tile's out: the issuer is never short of x
-      if (ok && u + 1 < mine) ok = normalise(u + 1);
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->out_full, u & 1, wc, abort));
-      if (ok) {
-        tc_fence_after();
-        const int tile = pair + u * pairs;
-        const long long row = static_cast<long long>(tile) * 256 + rank * 128 + r;
-        const float mk = p.mask != nullptr && row < p.M ? bf16lo_to_f32(p.mask[row]) : 1.f;
-        // the row's part of the z tile is read: out takes its place
-#pragma unroll 1
-        for (int c = 0; c < C; c += 32) {
-          uint32_t v[32];
-          tmem_ld32_wait(tmem + lane_addr + kOut + c, v);
+      const long long row = (static_cast<long long>(pair) + static_cast<long long>(u) * pairs) * 256 + rank * 128 +
+                            quarter * 32 + lane;
+      const bool in = row < p.M;
+      const float mk = p.mask != nullptr && in ? bf16lo_to_f32(p.mask[row]) : 1.f;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->out_full, u & 1, wc, abort))) break;
+      tc_fence_after();
+      // the whole row out of TMEM before anything is stored: the next tile's
+      // first out MMA waits for it
+      uint32_t w[C / 2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t w[4];
+      for (int c = 0; c < C; c += 32) {
+        uint32_t v[32];
+        tmem_ld32_wait(tmem + lane_addr + kOut + c, v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float lo = __uint_as_float(v[8 * j + 2 * e]) * mk, hi = __uint_as_float(v[8 * j + 2 * e + 1]) * mk;
-              w[e] = mk == 0.f ? 0u : pack_bf16x2(lo, hi);  // a row left out is 0 even if it held NaN
-            }
-            *z16(c / 8 + j) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+        for (int e = 0; e < 16; ++e) {
+          const float2 o = fmul2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
+                                 make_float2(mk, mk));
+          w[c / 2 + e] = pack_bf16x2(o.x, o.y);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cta(&bars->out_free, 0);
-        fence_proxy_async_smem();
       }
+      tc_fence_before();
       __syncwarp();
-      named_bar_sync(1, 128);
-      if (first && ok) {
-        const int tile = pair + u * pairs;
+      if (lane == 0) mbar_arrive_cta(&bars->out_free, 0);
+      // 32 features at a time through the warp's staging buffer (64-byte
+      // swizzled rows) and out by TMA, which leaves out rows past the end
 #pragma unroll
-        for (int b = 0; b < L::kZBoxes; ++b)
-          tma_store_3d(&tm_out, s_z + b * 16384, 64 * b, tile * 256 + static_cast<int>(rank) * 128, 0);
-        bulk_wait_read();
-        if (u + 2 < mine) load_z(pair + (u + 2) * pairs);
+      for (int c = 0; c < C / 32; ++c) {
+        if (lane == 0) bulk_wait_read();  // the store before has read the buffer
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = mk == 0.f ? 0u : w[16 * c + 4 * j + e];  // left out: 0 even if it held NaN
+          *reinterpret_cast<uint4*>(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && in) tma_store_3d(&tm_out, stg, 32 * c, static_cast<int>(row), 0);  // lane 0: the first row
       }
     }
-    if (first) bulk_wait_all();
-  } else {
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  } else if (warp >= 12) {
     // ------------------------------------------------------------ activation
-    const int idx = warp - 6, st = idx >> 3, hf = (idx >> 2) & 1, quarter = warp & 3;
+    regs_inc<kTfRegsAct>();
+    const int idx = warp - 12, st = idx >> 3, hf = (idx >> 2) & 1, quarter = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t ab = lanes + kAB + 128 * st + 32 * hf, hcol = lanes + kH + 32 * st + 16 * hf;
     for (long long g = st; g < total; g += 2) {
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->ab_full[st], (g >> 1) & 1, wc, abort))) break;
       tc_fence_after();
-      bool ok = true;
+      // in two halves: all 64 values at once leave the registers no room for
+      // the arithmetic of one to overlap that of the next (175 against 165 us)
+      uint32_t h[16];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        uint32_t a[16], b[16], h[8];
+        uint32_t a[16], b[16];
         tmem_ld16x2_wait(ab + 16 * j, a, ab + 64 + 16 * j, b);
         if (j == 1) {
           tc_fence_before();
@@ -332,17 +420,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
           if (lane == 0) mbar_arrive_cta(&bars->ab_free[st], 0);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          h[e] = pack_bf16x2(act_fwd<ACT>(__uint_as_float(a[2 * e])) * __uint_as_float(b[2 * e]),
-                             act_fwd<ACT>(__uint_as_float(a[2 * e + 1])) * __uint_as_float(b[2 * e + 1]));
-        if (j == 0 && g >= 2) {  // the out MMAs of the chunk before last have read this stage's h
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->h_free[st], static_cast<uint32_t>((g >> 1) - 1) & 1, wc, abort));
-          if (!ok) break;
-          tc_fence_after();
+        for (int e = 0; e < 8; ++e) {
+          const float2 v = gate_fwd2<ACT>(make_float2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1])),
+                                          make_float2(__uint_as_float(b[2 * e]), __uint_as_float(b[2 * e + 1])));
+          h[8 * j + e] = pack_bf16x2(v.x, v.y);
         }
-        tmem_st8(hcol + 8 * j, h);
       }
-      if (!ok) break;
+      // the out MMAs of the chunk before last have read this stage's h
+      if (g >= 2 &&
+          !__all_sync(0xffffffffu, mbar_wait(&bars->h_free[st], static_cast<uint32_t>((g >> 1) - 1) & 1, wc, abort)))
+        break;
+      tc_fence_after();
+      tmem_st16(hcol, h);
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -363,9 +452,13 @@ template <int C, int ACT>
 cudaError_t tf_launch(const CUtensorMap& tz, const CUtensorMap& to, const CUtensorMap& twi, const CUtensorMap& two,
                       const TfParams& p, int grid, cudaStream_t s) {
   const int bytes = TfSmem<C>::bytes(p.chunks);
-  const cudaError_t e = cudaFuncSetAttribute(transition_fwd_kernel<C, ACT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  cudaError_t e = cudaFuncSetAttribute(transition_fwd_kernel<C, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       bytes);
+  cudaFuncAttributes at;
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, transition_fwd_kernel<C, ACT>);
   if (e != cudaSuccess) return e;
+  // a split above the launch's registers would wait for ever
+  if (at.numRegs * (kTfThreads / 128) < kTfRegsSum) return cudaErrorInvalidConfiguration;
   transition_fwd_kernel<C, ACT><<<grid, kTfThreads, bytes, s>>>(tz, to, twi, two, p);
   return cudaGetLastError();
 }
@@ -395,7 +488,7 @@ cudaError_t launch_transition_fwd(long long M, int C, int H, int act, const void
   const cuuint64_t zd[3] = {c, m, 1}, zs[2] = {2 * c, 2 * c * m};
   const cuuint64_t wd[3] = {h, 2, c}, ws[2] = {2 * h, 4 * h};  // the a and b columns apart: past H reads 0
   const cuuint64_t od[3] = {c, h, 1}, os[2] = {2 * c, 2 * c * h};
-  if (!tf_map(&tz, z, zd, zs, 128, 1) || !tf_map(&to, out, zd, zs, 128, 1) ||
+  if (!tf_map(&tz, z, zd, zs, 128, 1) || !tf_map32(&to, out, zd, zs) ||
       !tf_map(&twi, w_in, wd, ws, 1, static_cast<cuuint32_t>(C)) || !tf_map(&two, w_o, od, os, 64, 1))
     return cudaErrorInvalidValue;
   TfParams p;
