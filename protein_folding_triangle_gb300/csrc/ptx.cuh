@@ -472,19 +472,6 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&r)[8]) {
                "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-// 32 bytes at an address that is 16-byte aligned only.
-__device__ __forceinline__ void ld_global_2v4(const void* p, uint32_t (&r)[8]) {
-  asm volatile(
-      "ld.global.v4.b32 {%0, %1, %2, %3}, [%8];\nld.global.v4.b32 {%4, %5, %6, %7}, [%8+16];"
-      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7])
-      : "l"(p)
-      : "memory");
-}
-__device__ __forceinline__ void st_global_2v4(void* p, const uint32_t (&r)[8]) {
-  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};\nst.global.v4.b32 [%0+16], {%5, %6, %7, %8};" ::"l"(p),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
 __device__ __forceinline__ void tmem_ld16x3_wait(uint32_t ta0, uint32_t (&a)[16], uint32_t ta1, uint32_t (&b)[16],
                                                  uint32_t ta2, uint32_t (&c)[16]) {
   asm volatile(

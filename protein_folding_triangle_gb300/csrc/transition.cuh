@@ -92,6 +92,40 @@ __device__ __forceinline__ float2 bf16x2_to_f32x2(uint32_t w) {
   return make_float2(bf16lo_to_f32(w), bf16hi_to_f32(w));
 }
 
+// Mean and 1 / sqrt(variance + eps) of a row of C features held as C / 8
+// chunks of 16 bytes at z16(c), in one pass about the mean k of its first 8
+// features: |k - mean| is at most sqrt((C - 8) / 8) < 4 standard deviations
+// whatever the row holds, so that the difference below loses less than a
+// factor of 17 of the FP32 precision.
+template <int C, typename F>
+__device__ __forceinline__ float2 row_stats(F&& z16) {
+  float k;
+  {
+    const uint4 w = *z16(0);
+    const float2 k2 = fadd2(fadd2(bf16x2_to_f32x2(w.x), bf16x2_to_f32x2(w.y)),
+                            fadd2(bf16x2_to_f32x2(w.z), bf16x2_to_f32x2(w.w)));
+    k = (k2.x + k2.y) * 0.125f;
+  }
+  const float2 nk = make_float2(-k, -k);
+  float2 s2[2], q2[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) s2[e] = q2[e] = make_float2(0.f, 0.f);
+#pragma unroll 4
+  for (int c = 0; c < C / 8; ++c) {
+    const uint4 w = *z16(c);
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 d = fadd2(bf16x2_to_f32x2(ws[e]), nk);
+      s2[e & 1] = fadd2(s2[e & 1], d);
+      q2[e & 1] = ffma2(d, d, q2[e & 1]);
+    }
+  }
+  const float2 ss = fadd2(s2[0], s2[1]), qq = fadd2(q2[0], q2[1]);
+  const float ds = (ss.x + ss.y) * (1.f / C);  // mean - k
+  return make_float2(k + ds, rsqrtf(fmaxf(fmaf(-ds, ds, (qq.x + qq.y) * (1.f / C)), 0.f) + 1e-5f));
+}
+
 // f(std::integral_constant<int, ACT>) for the activations.
 template <typename F>
 cudaError_t by_act(int act, F&& f) {

@@ -266,36 +266,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->z_full[u & 1], (u >> 1) & 1, wc, abort))) return false;
       uint8_t* const zt = s_z + (u & 1) * L::kZ;
       auto z16 = [&](int c) { return reinterpret_cast<uint4*>(zt + (c >> 3) * 16384 + sw128(r, c & 7)); };
-      // Mean and variance in one pass, about the mean k of the row's first 8
-      // features: |k - mean| is at most sqrt((C - 8) / 8) < 4 standard
-      // deviations whatever the row holds, so that the difference below
-      // loses less than a factor of 17 of the FP32 precision.
-      float2 k2;
-      {
-        const uint4 w = *z16(0);
-        k2 = fadd2(fadd2(bf16x2_to_f32x2(w.x), bf16x2_to_f32x2(w.y)),
-                   fadd2(bf16x2_to_f32x2(w.z), bf16x2_to_f32x2(w.w)));
-      }
-      const float k = (k2.x + k2.y) * 0.125f;
-      const float2 nk = make_float2(-k, -k);
-      float2 s2[2], q2[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) s2[e] = q2[e] = make_float2(0.f, 0.f);
-#pragma unroll 4
-      for (int c = 0; c < C / 8; ++c) {
-        const uint4 w = *z16(c);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 d = fadd2(bf16x2_to_f32x2(ws[e]), nk);
-          s2[e & 1] = fadd2(s2[e & 1], d);
-          q2[e & 1] = ffma2(d, d, q2[e & 1]);
-        }
-      }
-      const float2 ss = fadd2(s2[0], s2[1]), qq = fadd2(q2[0], q2[1]);
-      const float ds = (ss.x + ss.y) * (1.f / C);  // mean - k
-      const float mean = k + ds;
-      const float rstd = rsqrtf(fmaxf(fmaf(-ds, ds, (qq.x + qq.y) * (1.f / C)), 0.f) + 1e-5f);
+      const float2 st = row_stats<C>(z16);
+      const float mean = st.x, rstd = st.y;
       const float2 nm = make_float2(-mean, -mean), rs = make_float2(rstd, rstd);
       // x over z in shared memory first, so that little is left to do once the
       // previous tile's x has been read
