@@ -273,12 +273,18 @@ triattn_status gn_check(const triattn_tensor* ts, long long n) {
 struct Span {
   uintptr_t lo, hi;
 };
-// Whether two of the spans share a byte.
-bool gn_overlap(std::vector<Span>& v) {
-  std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
-  for (size_t i = 1; i < v.size(); ++i)
-    if (v[i].lo < v[i - 1].hi) return true;
-  return false;
+// The bytes of every tensor, by address (views of one buffer mostly come in order).
+std::vector<Span> gn_spans(const triattn_tensor* ts, long long n) {
+  std::vector<Span> v;
+  v.reserve(static_cast<size_t>(n));
+  for (long long i = 0; i < n; ++i)
+    if (ts[i].numel > 0) {
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(ts[i].data);
+      v.push_back({lo, lo + static_cast<uintptr_t>(gn_bytes(ts[i]))});
+    }
+  const auto less = [](const Span& a, const Span& b) { return a.lo < b.lo; };
+  if (!std::is_sorted(v.begin(), v.end(), less)) std::sort(v.begin(), v.end(), less);
+  return v;
 }
 
 // Table of tensors [i0, i1); false if their chunks exceed 32 bits.
@@ -410,29 +416,18 @@ triattn_status triattn_clip_grad_norm(const triattn_tensor* tensors, const triat
       if (out[i].numel != tensors[i].numel || out[i].dtype != tensors[i].dtype) return TRIATTN_ERR_INVALID_ARG;
   }
   // Tensors that are written may share no byte with another one: each element
-  // is scaled by one thread, without an order between them.
+  // is scaled by one thread, without an order between them.  Sources may
+  // overlap one another where they are only read.
   try {
-    std::vector<Span> v;
-    v.reserve(static_cast<size_t>(n) * 2);
-    auto add = [&](const triattn_tensor* ts) {
-      for (long long i = 0; i < n; ++i)
-        if (ts[i].numel > 0) {
-          const uintptr_t lo = reinterpret_cast<uintptr_t>(ts[i].data);
-          v.push_back({lo, lo + static_cast<uintptr_t>(gn_bytes(ts[i]))});
-        }
-    };
-    add(out != nullptr ? out : tensors);
-    if (gn_overlap(v)) return TRIATTN_ERR_INVALID_ARG;
-    if (out != nullptr) {  // sources may overlap one another, not a destination
-      const std::vector<Span> dst = v;
-      for (long long i = 0; i < n; ++i) {
-        if (tensors[i].numel == 0) continue;
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(tensors[i].data);
-        const uintptr_t hi = lo + static_cast<uintptr_t>(gn_bytes(tensors[i]));
-        // the first destination that ends above lo (they are disjoint and sorted)
-        const auto it = std::upper_bound(dst.begin(), dst.end(), lo,
-                                         [](uintptr_t a, const Span& b) { return a < b.hi; });
-        if (it != dst.end() && it->lo < hi) return TRIATTN_ERR_INVALID_ARG;
+    std::vector<Span> dst = gn_spans(out != nullptr ? out : tensors, n);
+    for (size_t i = 1; i < dst.size(); ++i)
+      if (dst[i].lo < dst[i - 1].hi) return TRIATTN_ERR_INVALID_ARG;
+    if (out != nullptr) {
+      const std::vector<Span> src = gn_spans(tensors, n);
+      size_t k = 0;  // the first destination that ends above the source's start (they are disjoint)
+      for (const Span& a : src) {
+        while (k < dst.size() && dst[k].hi <= a.lo) ++k;
+        if (k < dst.size() && dst[k].lo < a.hi) return TRIATTN_ERR_INVALID_ARG;
       }
     }
   } catch (const std::bad_alloc&) {

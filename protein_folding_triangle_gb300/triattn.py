@@ -9,10 +9,12 @@ if the shared library is missing or cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 from typing import Optional
 
+import numpy as np
 import torch
 
 from . import build as _build
@@ -628,11 +630,29 @@ def triattn_trimul_bwd(z, mask, ln_in_w, w_p, ln_out_w, w_o, ctx, d_out, directi
     return out
 
 
+class _Here:
+    """A context that changes nothing."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
 def _on_stream(device, stream):
-    """Context in which `device` is current and allocations belong to the
-    stream that the call runs on (so a workspace freed at the end of the call
-    is not handed to another stream while its kernels still run)."""
-    return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device))
+    """(context, stream pointer) of a call on `device`: inside the context the
+    device is current and allocations belong to the stream that the call runs
+    on, so that a workspace freed at the end of the call is not handed to
+    another stream while its kernels still run."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+        if torch.cuda.current_device() == device.index:
+            return _HERE, ctypes.c_void_p(stream.cuda_stream)
+    return torch.cuda.stream(stream), ctypes.c_void_p(stream.cuda_stream)
 
 
 def _same_device(device, **tensors):
@@ -676,17 +696,22 @@ def triattn_transition_fwd(z, mask, ln_w, ln_b, w_in, w_o, activation: str = "si
     "silu", "sigmoid" or "gelu" (tanh form).  Returns out [..., C] bf16."""
     M, C, H = _transition_check(z, mask, ln_w, ln_b, w_in, w_o)
     s = transition_shape(M, C, H, activation)
-    need = int(load().triattn_transition_workspace_bytes(ctypes.byref(s), 0))
+    lib = load()
+    need = lib.triattn_transition_workspace_bytes(ctypes.byref(s), 0)
     if need == 0:
         raise TriAttnError(ERR_UNSUPPORTED, "triattn_transition_fwd")
-    with _on_stream(z.device, stream):
+    here, sp = _on_stream(z.device, stream)
+    with here:
         workspace = torch.empty(need, dtype=torch.uint8, device=z.device) if workspace is None else workspace
-        out = torch.empty_like(z) if out is None else out
-        _check(out, "out", z.shape)
-        _same_device(z.device, workspace=workspace, out=out)
-        code = load().triattn_transition_fwd(ctypes.byref(s), _ptr(z), _ptr(mask), _ptr(ln_w), _ptr(ln_b), _ptr(w_in),
-                                             _ptr(w_o), _ptr(out), _ptr(workspace), _bytes(workspace),
-                                             _stream_ptr(stream))
+        if out is None:
+            out = torch.empty_like(z)
+        else:
+            _check(out, "out", z.shape)
+            _same_device(z.device, out=out)
+        _same_device(z.device, workspace=workspace)
+        code = lib.triattn_transition_fwd(ctypes.byref(s), z.data_ptr(), None if mask is None else mask.data_ptr(),
+                                          ln_w.data_ptr(), ln_b.data_ptr(), w_in.data_ptr(), w_o.data_ptr(),
+                                          out.data_ptr(), workspace.data_ptr(), _bytes(workspace), sp)
     _raise(code, "triattn_transition_fwd")
     return out
 
@@ -699,30 +724,38 @@ def triattn_transition_bwd(z, mask, ln_w, ln_b, w_in, w_o, d_out, activation: st
     M, C, H = _transition_check(z, mask, ln_w, ln_b, w_in, w_o)
     _check(d_out, "d_out", z.shape)
     s = transition_shape(M, C, H, activation, grads_bf16)
-    need = int(load().triattn_transition_workspace_bytes(ctypes.byref(s), 1))
+    lib = load()
+    need = lib.triattn_transition_workspace_bytes(ctypes.byref(s), 1)
     if need == 0:
         raise TriAttnError(ERR_UNSUPPORTED, "triattn_transition_bwd")
     dt = torch.bfloat16 if grads_bf16 else torch.float32
-    with _on_stream(z.device, stream):
+    here, sp = _on_stream(z.device, stream)
+    with here:
         workspace = torch.empty(need, dtype=torch.uint8, device=z.device) if workspace is None else workspace
         if out is None:
             kw = dict(dtype=dt, device=z.device)
             out = (torch.empty_like(z), torch.empty(C, **kw), torch.empty(C, **kw), torch.empty((C, 2 * H), **kw),
                    torch.empty((H, C), **kw))
-        dz, dlw, dlb, dwi, dwo = out
-        _check(dz, "dz", z.shape)
-        for name, t, shape in (("d_ln_w", dlw, (C,)), ("d_ln_b", dlb, (C,)), ("d_w_in", dwi, (C, 2 * H)),
-                               ("d_w_o", dwo, (H, C))):
-            _check(t, name, shape, dt)
-        _same_device(z.device, d_out=d_out, workspace=workspace, dz=dz, d_ln_w=dlw, d_ln_b=dlb, d_w_in=dwi, d_w_o=dwo)
-        code = load().triattn_transition_bwd(ctypes.byref(s), _ptr(z), _ptr(mask), _ptr(ln_w), _ptr(ln_b), _ptr(w_in),
-                                             _ptr(w_o), _ptr(d_out), _ptr(dz), _ptr(dlw), _ptr(dlb), _ptr(dwi),
-                                             _ptr(dwo), _ptr(workspace), _bytes(workspace), _stream_ptr(stream))
+            dz, dlw, dlb, dwi, dwo = out
+        else:
+            dz, dlw, dlb, dwi, dwo = out
+            _check(dz, "dz", z.shape)
+            for name, t, shape in (("d_ln_w", dlw, (C,)), ("d_ln_b", dlb, (C,)), ("d_w_in", dwi, (C, 2 * H)),
+                                   ("d_w_o", dwo, (H, C))):
+                _check(t, name, shape, dt)
+            _same_device(z.device, dz=dz, d_ln_w=dlw, d_ln_b=dlb, d_w_in=dwi, d_w_o=dwo)
+        _same_device(z.device, d_out=d_out, workspace=workspace)
+        code = lib.triattn_transition_bwd(ctypes.byref(s), z.data_ptr(), None if mask is None else mask.data_ptr(),
+                                          ln_w.data_ptr(), ln_b.data_ptr(), w_in.data_ptr(), w_o.data_ptr(),
+                                          d_out.data_ptr(), dz.data_ptr(), dlw.data_ptr(), dlb.data_ptr(),
+                                          dwi.data_ptr(), dwo.data_ptr(), workspace.data_ptr(), _bytes(workspace), sp)
     _raise(code, "triattn_transition_bwd")
     return dz, dlw, dlb, dwi, dwo
 
 
 GRAD_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+_dtype_of = operator.attrgetter("dtype")
+_TENSOR = np.dtype([("data", np.uint64), ("numel", np.int64), ("dtype", np.int32)], align=True)  # Tensor
 
 
 def _dense(t) -> bool:
@@ -737,14 +770,25 @@ def _dense(t) -> bool:
 
 
 def _tensor_table(tensors, name, device):
-    table = (Tensor * len(tensors))()
-    for i, t in enumerate(tensors):
-        if t.dtype not in GRAD_DTYPES or t.device != device or t.layout != torch.strided:
-            raise ValueError(f"{name}[{i}] must be a strided bfloat16 or float32 tensor on {device}")
-        if not t.is_contiguous() and t.numel() and not _dense(t):
-            raise ValueError(f"{name}[{i}] must fill one block of memory")
-        table[i] = (t.data_ptr(), t.numel(), GRAD_DTYPES[t.dtype])
-    return table
+    """The triattn_tensor array of a list, column by column: a model has
+    thousands of gradients, and the host's time per tensor is what counts."""
+    n = len(tensors)
+    table = np.empty(n, dtype=_TENSOR)
+    try:
+        table["data"] = np.fromiter(map(torch.Tensor.data_ptr, tensors), np.uint64, n)
+        table["numel"] = np.fromiter(map(torch.Tensor.numel, tensors), np.int64, n)
+        table["dtype"] = np.fromiter(map(GRAD_DTYPES.__getitem__, map(_dtype_of, tensors)), np.int32, n)
+        plain = (all(map(torch.Tensor.is_contiguous, tensors))
+                 and set(map(torch.Tensor.get_device, tensors)) <= {device.index})
+    except (KeyError, RuntimeError):
+        plain = False
+    if not plain:
+        for i, t in enumerate(tensors):
+            if t.dtype not in GRAD_DTYPES or t.device != device or t.layout != torch.strided:
+                raise ValueError(f"{name}[{i}] must be a strided bfloat16 or float32 tensor on {device}")
+            if not t.is_contiguous() and t.numel() and not _dense(t):
+                raise ValueError(f"{name}[{i}] must fill one block of memory")
+    return table, plain
 
 
 def _grad_call(tensors, norm_type):
@@ -763,11 +807,12 @@ def triattn_grad_norm(tensors, norm_type: float = 2.0, *, stream=None):
     2 or inf.  Returns a 0-dim FP32 tensor; nothing waits for the device."""
     tensors, kind, device = _grad_call(tensors, norm_type)
     n = len(tensors)
-    table = _tensor_table(tensors, "tensors", device)
-    with _on_stream(device, stream):
+    table, _ = _tensor_table(tensors, "tensors", device)
+    here, sp = _on_stream(device, stream)
+    with here:
         norm = torch.empty((), dtype=torch.float32, device=device)
         ws = torch.empty(max(int(load().triattn_grad_norm_workspace_bytes(n)), 16), dtype=torch.uint8, device=device)
-        code = load().triattn_grad_norm(table, n, kind, _ptr(norm), _ptr(ws), _bytes(ws), _stream_ptr(stream))
+        code = load().triattn_grad_norm(ctypes.c_void_p(table.ctypes.data), n, kind, _ptr(norm), _ptr(ws), _bytes(ws), sp)
     _raise(code, "triattn_grad_norm")
     return norm
 
@@ -775,26 +820,30 @@ def triattn_grad_norm(tensors, norm_type: float = 2.0, *, stream=None):
 def triattn_clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, *, out=None, stream=None):
     """Scale ``tensors`` (BF16 and FP32 CUDA tensors, mixed) by
     min(1, max_norm / (norm + 1e-6)), in place, or into ``out`` (a list of
-    tensors of the same shapes, strides and dtypes).  Returns the norm before
+    tensors of the same dtypes and sizes, in the same memory order).  Returns the norm before
     clipping as a 0-dim FP32 tensor; nothing waits for the device.  A tensor
     may not be listed twice."""
     tensors, kind, device = _grad_call(tensors, norm_type)
     n = len(tensors)
-    table = _tensor_table(tensors, "tensors", device)
+    table, plain = _tensor_table(tensors, "tensors", device)
     into = None
     if out is not None:
         out = [out] if isinstance(out, torch.Tensor) else list(out)
         if len(out) != n:
             raise ValueError(f"out has {len(out)} tensors, expected {n}")
-        into = _tensor_table(out, "out", device)
-        for i, (a, b) in enumerate(zip(tensors, out)):
-            if a.dtype != b.dtype or a.shape != b.shape or a.stride() != b.stride():
-                raise ValueError(f"out[{i}] must have the shape, strides and dtype of tensors[{i}]")
-    with _on_stream(device, stream):
+        into, plain_out = _tensor_table(out, "out", device)
+        same = (table["numel"] == into["numel"]) & (table["dtype"] == into["dtype"])
+        if not (plain and plain_out):
+            same &= [a.shape == b.shape and a.stride() == b.stride() for a, b in zip(tensors, out)]
+        if not same.all():
+            raise ValueError(f"out[{int(same.argmin())}] does not match tensors[{int(same.argmin())}]")
+    here, sp = _on_stream(device, stream)
+    with here:
         norm = torch.empty((), dtype=torch.float32, device=device)
         ws = torch.empty(max(int(load().triattn_grad_norm_workspace_bytes(n)), 16), dtype=torch.uint8, device=device)
-        code = load().triattn_clip_grad_norm(table, into, n, kind, float(max_norm), _ptr(norm), _ptr(ws), _bytes(ws),
-                                             _stream_ptr(stream))
+        code = load().triattn_clip_grad_norm(ctypes.c_void_p(table.ctypes.data),
+                                             None if into is None else ctypes.c_void_p(into.ctypes.data), n, kind,
+                                             float(max_norm), _ptr(norm), _ptr(ws), _bytes(ws), sp)
     _raise(code, "triattn_clip_grad_norm")
     return norm
 
