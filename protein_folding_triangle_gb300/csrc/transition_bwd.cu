@@ -26,8 +26,8 @@
 //
 // Warps: 0 loads weights, 2 tells CTA 0 that this CTA's are in; 1 and 3 (of
 // CTA 0) issue the MMAs, one [a | b] and dh, one dx; 4-7 write x = LayerNorm(z)
-// and g, 8-11 take dx through the LayerNorm's backward (thread = row for
-// both); 12-19 the activation.
+// and g (thread = row), 8-11 take dx through the LayerNorm's backward; 12-19 the
+// activation.
 #include <algorithm>
 #include <cstring>
 
@@ -39,12 +39,12 @@ namespace {
 
 constexpr int kTbThreads = 20 * 32;
 // Registers per thread of the warpgroups (setmaxnreg): five shares of what the
-// block was launched with (96 each).  The LayerNorm's warps hold a row of dx.
-constexpr int kRegsIssue = 40, kRegsRow = 64, kRegsLn = 168, kRegsAct = 104;
+// block was launched with (96 each).
+constexpr int kRegsIssue = 40, kRegsRow = 104, kRegsLn = 128, kRegsAct = 104;
 constexpr int kRegsSum = kRegsIssue + kRegsRow + kRegsLn + 2 * kRegsAct;
 constexpr int kTbMaxSlots = 4;
 constexpr int kTbBarBytes = 1024 + 1024;  // barriers, ln_w and ln_b
-constexpr int kTbStg = 8 * 3 * 2048;      // per activation warp: h, da, db of 32 rows x 32 features
+constexpr int kTbStg = 4 * 3 * 4096;      // per 32 rows (a pair of activation warps): h, da, db of 64 features
 constexpr int kTbSmemMax = 232448;
 
 struct TbBars {
@@ -83,18 +83,16 @@ struct TbSmem {
   static constexpr int bytes(int slots) { return slots * (kA + kB) + 3 * kRows + kTbStg + kTbBarBytes + 1024; }
 };
 
-// v[j] summed over the 32 lanes for every j, lane l ending with the sum of
-// v[l mod 16] (lane exchange, then halving; fixed order).
-__device__ __forceinline__ float lane_scatter_sum(float (&v)[16], int lane) {
+// v[j] summed over the 8 threads t mod 4 + 4 q for every j, the thread of
+// index q ending with the sum of v[q] (halving exchange, fixed order).
+__device__ __forceinline__ float rows_scatter_sum(float (&v)[8], int lane) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], 16);
-#pragma unroll
-  for (int n = 8; n > 0; n >>= 1) {
-    const bool up = (lane & n) != 0;
+  for (int n = 4; n > 0; n >>= 1) {
+    const bool up = (lane & (4 * n)) != 0;
 #pragma unroll
     for (int j = 0; j < n; ++j) {
       const float keep = up ? v[j + n] : v[j], send = up ? v[j] : v[j + n];
-      v[j] = keep + __shfl_xor_sync(0xffffffffu, send, n);
+      v[j] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * n);
     }
   }
   return v[0];
@@ -296,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTbThreads, 1)
     }
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ x = LayerNorm(z), g = m d_out
-    regs_dec<kRegsRow>();
+    regs_inc<kRegsRow>();
     const bool first = warp == 4 && lane == 0;
     auto write = [&](int u) -> bool {
       const long long row = tile_row(u) + r;
@@ -308,9 +306,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTbThreads, 1)
       auto z16 = [&](int c) { return reinterpret_cast<const uint4*>(zt + (c >> 3) * 16384 + sw128(r, c & 7)); };
       const float2 st = row_stats<C>(z16);
       const float2 nm = make_float2(-st.x, -st.x), rs = make_float2(st.y, st.y);
+      // x in registers before the previous tile's has been read
+      uint32_t x[C / 2];
+#pragma unroll
+      for (int c = 0; c < C / 8; ++c) {
+        const uint4 w = *z16(c);
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        const float4* gm = reinterpret_cast<const float4*>(s_gam + 8 * c);
+        const float4* bt = reinterpret_cast<const float4*>(s_bet + 8 * c);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 ga = gm[e], be = bt[e];
+          const float2 x0 = ffma2(fmul2(fadd2(bf16x2_to_f32x2(ws[2 * e]), nm), rs), make_float2(ga.x, ga.y),
+                                  make_float2(be.x, be.y));
+          const float2 x1 = ffma2(fmul2(fadd2(bf16x2_to_f32x2(ws[2 * e + 1]), nm), rs), make_float2(ga.z, ga.w),
+                                  make_float2(be.z, be.w));
+          x[4 * c + 2 * e] = live ? pack_bf16x2(x0.x, x0.y) : 0u;
+          x[4 * c + 2 * e + 1] = live ? pack_bf16x2(x1.x, x1.y) : 0u;
+        }
+        if (c % 2 == 1) asm volatile("" ::: "memory");  // no more rows unpacked at a time than fit
+      }
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->g_full, u & 1, wc, abort))) return false;
       if (u > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->xg_free, (u - 1) & 1, wc, abort))) return false;
       tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < C / 16; ++c) {
+        uint32_t v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = x[8 * c + e];
+        tmem_st8(tmem + lane_addr + kX + 8 * c, v);
+      }
 #pragma unroll 1
       for (int c = 0; c < C / 8; c += 4) {  // g: 32 features = 16 columns at a time
         uint32_t v[16];
@@ -339,33 +364,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTbThreads, 1)
           st_global_v8(p.g + row * C + 8 * c + 16, hi);
         }
       }
-#pragma unroll 2
-      for (int c = 0; c < C / 8; c += 2) {  // x: 16 features = 8 columns at a time
-        uint32_t v[8];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint4 w = *z16(c + j);
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-          const float4* gm = reinterpret_cast<const float4*>(s_gam + 8 * (c + j));
-          const float4* bt = reinterpret_cast<const float4*>(s_bet + 8 * (c + j));
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float4 ga = gm[e], be = bt[e];
-            const float2 x0 = ffma2(fmul2(fadd2(bf16x2_to_f32x2(ws[2 * e]), nm), rs), make_float2(ga.x, ga.y),
-                                    make_float2(be.x, be.y));
-            const float2 x1 = ffma2(fmul2(fadd2(bf16x2_to_f32x2(ws[2 * e + 1]), nm), rs), make_float2(ga.z, ga.w),
-                                    make_float2(be.z, be.w));
-            v[4 * j + 2 * e] = live ? pack_bf16x2(x0.x, x0.y) : 0u;
-            v[4 * j + 2 * e + 1] = live ? pack_bf16x2(x1.x, x1.y) : 0u;
-          }
-        }
-        tmem_st8(tmem + lane_addr + kX + 4 * c, v);
-        if (in) st_global_v8(p.x + row * C + 8 * c, v);
-      }
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(&bars->xg_full, 0);
+      if (in) {
+#pragma unroll
+        for (int c = 0; c < C / 16; ++c) {
+          uint32_t v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = x[8 * c + e];
+          st_global_v8(p.x + row * C + 16 * c, v);
+        }
+      }
       return true;
     };
     if (first && mine > 0) {
@@ -382,86 +393,117 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTbThreads, 1)
     }
   } else if (warp >= 8 && warp < 12) {
     // ------------------------------------------------------------ LayerNorm backward
-    // dz = rstd (t - mean(t) - xhat mean(t xhat)), t = dx ln_w, over the row of
-    // dx, taken out of TMEM at once (the next tile's first dx MMA waits for
-    // it).  The sums over the rows for d_ln_w and d_ln_b: 16 features at a time
-    // across the lanes, one feature per lane pair, added up over the tiles.
+    // dz = rstd (t - mean(t) - xhat mean(t xhat)), t = dx ln_w, over the rows of
+    // dx, taken out of TMEM as matrix fragments of 16 rows: a thread holds 2 of
+    // every 8 features of 2 of them, so a row's sums take two exchanges and a
+    // feature's sum over the rows (for d_ln_w and d_ln_b) three; with a whole
+    // row per thread that sum alone took 1500 instructions per tile.  Two
+    // fragments at once would free TMEM earlier, but not fit the registers.
     regs_inc<kRegsLn>();
     const bool first = warp == 8 && lane == 0;
-    float accg[C / 16], accb[C / 16];
+    const int q = lane >> 2, cl = 2 * (lane & 3);
+    float accg[C / 32], accb[C / 32];
 #pragma unroll
-    for (int b = 0; b < C / 16; ++b) accg[b] = accb[b] = 0.f;
+    for (int b = 0; b < C / 32; ++b) accg[b] = accb[b] = 0.f;
     auto ln_bwd = [&](int u) -> bool {
-      const long long row = tile_row(u) + r;
-      const bool live = row < p.M && (p.mask == nullptr || (p.mask[row] & 0x7FFFu) != 0);
       uint8_t* const zt = s_z + (u & 1) * L::kRows;
-      auto z16 = [&](int c) { return reinterpret_cast<uint4*>(zt + (c >> 3) * 16384 + sw128(r, c & 7)); };
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->z_full[u & 1], (u >> 1) & 1, wc, abort))) return false;
-      float2 st = row_stats<C>(z16);
+      // the statistics of row r, and whether it takes part, by its own thread
+      const float2 st = row_stats<C>(
+          [&](int c) { return reinterpret_cast<const uint4*>(zt + (c >> 3) * 16384 + sw128(r, c & 7)); });
+      const long long row = tile_row(u) + r;
+      const uint32_t lives =
+          __ballot_sync(0xffffffffu, row < p.M && (p.mask == nullptr || (p.mask[row] & 0x7FFFu) != 0));
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->dx_full, u & 1, wc, abort))) return false;
       tc_fence_after();
-      float d[C];
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {  // rows 16 h + q and 16 h + q + 8 of the warp's 32
+        uint32_t d[C / 2];
+        const uint32_t at = tmem + lane_addr + (static_cast<uint32_t>(16 * h) << 16) + kDx;
 #pragma unroll
-      for (int c = 0; c < C; c += 32) {
-        uint32_t v[32];
-        tmem_ld32_wait(tmem + lane_addr + kDx + c, v);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) d[c + e] = __uint_as_float(v[e]);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cta(&bars->dx_free, 0);
-      // a row left out has dx = 0; xhat = 0 whatever z holds there
-      auto xhat8 = [&](int c, float (&xh)[8]) {
-        const uint4 w = *z16(c);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 v = fmul2(fadd2(bf16x2_to_f32x2(ws[e]), make_float2(-st.x, -st.x)), make_float2(st.y, st.y));
-          xh[2 * e] = live ? v.x : 0.f;
-          xh[2 * e + 1] = live ? v.y : 0.f;
+        for (int c = 0; c + 64 <= C; c += 64) tmem_ld_frag_wait<32>(at + c, &d[c / 2]);
+        if constexpr (C % 64 != 0) tmem_ld_frag_wait<16>(at + C - 32, &d[(C - 32) / 2]);
+        if (h == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cta(&bars->dx_free, 0);
         }
-      };
-      float sg = 0.f, sgx = 0.f;
-#pragma unroll
-      for (int c = 0; c < C / 8; ++c) {
-        float xh[8];
-        if (c % 2 == 0) asm volatile("" ::: "memory");
-        xhat8(c, xh);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float t = d[8 * c + e] * s_gam[8 * c + e];
-          sg += t;
-          sgx = fmaf(t, xh[e], sgx);
-        }
-      }
-      const float m1 = sg * (1.f / C), m2 = sgx * (1.f / C);
-      // z and ln_w are read again below: kept from above they would not fit
-      asm volatile("" ::: "memory");
-#pragma unroll
-      for (int b = 0; b < C / 16; ++b) {
-        float v[16];
+        float2 nm[2], rs[2];
+        bool live[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int c = 2 * b + k;
-          float xh[8];
-          xhat8(c, xh);
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 gm = *reinterpret_cast<const float2*>(s_gam + 8 * c + 2 * e);
-            const float o0 = st.y * (d[8 * c + 2 * e] * gm.x - m1 - xh[2 * e] * m2);
-            const float o1 = st.y * (d[8 * c + 2 * e + 1] * gm.y - m1 - xh[2 * e + 1] * m2);
-            o[e] = live ? pack_bf16x2(o0, o1) : 0u;
-          }
-          *z16(c) = make_uint4(o[0], o[1], o[2], o[3]);  // dz in z's place: the row is this thread's
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[8 * k + e] = d[8 * c + e] * xh[e];
+          const int src = 16 * h + 8 * k + q;
+          const float mean = __shfl_sync(0xffffffffu, st.x, src), rstd = __shfl_sync(0xffffffffu, st.y, src);
+          nm[k] = make_float2(-mean, -mean);
+          rs[k] = make_float2(rstd, rstd);
+          live[k] = ((lives >> src) & 1u) != 0;
         }
-        accg[b] += lane_scatter_sum(v, lane);
+        // z of row k's features 8 j + cl, + 1: one word of shared memory
+        uint8_t* const zr = zt + (quarter * 32 + 16 * h + q) * 128 + 2 * cl;
+        auto zw = [&](int k, int j) {
+          return reinterpret_cast<uint32_t*>(zr + (j >> 3) * 16384 + k * 1024 + (((j & 7) ^ (q & 7)) << 4));
+        };
+        auto xhat = [&](int k, int j) {
+          const float2 v = fmul2(fadd2(bf16x2_to_f32x2(*zw(k, j)), nm[k]), rs[k]);
+          // a row left out has dx = 0; xhat = 0 whatever z holds there
+          return live[k] ? v : make_float2(0.f, 0.f);
+        };
+        auto dx = [&](int k, int j) {  // as zw
+          return make_float2(__uint_as_float(d[4 * j + 2 * k]), __uint_as_float(d[4 * j + 2 * k + 1]));
+        };
+        float2 s1[2], s2[2];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = d[16 * b + e];
-        accb[b] += lane_scatter_sum(v, lane);
+        for (int k = 0; k < 2; ++k) s1[k] = s2[k] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < C / 8; ++j) {
+          const float2 gm = *reinterpret_cast<const float2*>(s_gam + 8 * j + cl);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 t = fmul2(dx(k, j), gm);
+            s1[k] = fadd2(s1[k], t);
+            s2[k] = ffma2(t, xhat(k, j), s2[k]);
+          }
+          // z and ln_w are read again below: kept from here they would not fit
+          if (j % 4 == 3) asm volatile("" ::: "memory");
+        }
+        float2 m1[2], m2[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float a = s1[k].x + s1[k].y, b = s2[k].x + s2[k].y;
+#pragma unroll
+          for (int off = 1; off < 4; off <<= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, off);
+            b += __shfl_xor_sync(0xffffffffu, b, off);
+          }
+          a *= -rs[k].x * (1.f / C);
+          b *= -rs[k].x * (1.f / C);
+          m1[k] = make_float2(a, a);
+          m2[k] = make_float2(b, b);
+        }
+#pragma unroll
+        for (int b = 0; b < C / 32; ++b) {
+          float vg[8], vb[8];
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) {
+            const int j = 4 * b + jj;
+            const float2 gm = *reinterpret_cast<const float2*>(s_gam + 8 * j + cl);
+            float2 cg = make_float2(0.f, 0.f), cb = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float2 xh = xhat(k, j), dv = dx(k, j);
+              const float2 o = ffma2(xh, m2[k], ffma2(fmul2(dv, gm), rs[k], m1[k]));
+              *zw(k, j) = live[k] ? pack_bf16x2(o.x, o.y) : 0u;  // dz in z's place: the word is this thread's
+              cg = ffma2(dv, xh, cg);
+              cb = fadd2(cb, dv);
+            }
+            vg[2 * jj] = cg.x;
+            vg[2 * jj + 1] = cg.y;
+            vb[2 * jj] = cb.x;
+            vb[2 * jj + 1] = cb.y;
+          }
+          accg[b] += rows_scatter_sum(vg, lane);
+          accb[b] += rows_scatter_sum(vb, lane);
+        }
       }
       return true;
     };
@@ -487,72 +529,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTbThreads, 1)
     if (first) bulk_wait_all();
     __syncwarp();
     const size_t part = static_cast<size_t>(blockIdx.x) * 4 + quarter;
-    if (lane < 16) {
 #pragma unroll
-      for (int b = 0; b < C / 16; ++b) {
-        p.part_g[part * C + 16 * b + lane] = accg[b];
-        p.part_b[part * C + 16 * b + lane] = accb[b];
-      }
+    for (int b = 0; b < C / 32; ++b) {
+      const int c = 32 * b + 8 * (q >> 1) + cl + (q & 1);
+      p.part_g[part * C + c] = accg[b];
+      p.part_b[part * C + c] = accb[b];
     }
   } else if (warp >= 12) {
     // ------------------------------------------------------------ activation
-    // Warp = 32 rows x 32 of the chunk's 64 hidden features, 16 at a time.
+    // Warp = 32 rows x 32 of the chunk's 64 hidden features, 16 at a time.  The
+    // two warps of the same rows share a staging buffer, so that a store's
+    // rows are whole 128-byte lines (64-byte rows: see above).
     regs_inc<kRegsAct>();
     const int hf = (warp - 12) >> 2;
     const uint32_t abd = tmem + lane_addr + kABD + 32 * hf, dab = tmem + lane_addr + kDAB + 16 * hf;
-    uint8_t* const stg = s_stg + (warp - 12) * (3 * 2048);
+    uint8_t* const stg = s_stg + quarter * (3 * 4096);
+    bool ok = true;
     int u = 0, i = 0;
-    for (long long g = 0; g < total; ++g) {
-      const int hid = 64 * i + 32 * hf;
+    for (long long g = 0; g < total; ++g) {  // no warp leaves the loop early: pairs meet at their barrier
       const long long row0 = tile_row(u) + quarter * 32;  // the warp's first row
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars->abd_full, static_cast<uint32_t>(g) & 1, wc, abort))) break;
+      // the chunk before's stores have read the staging buffer
+      if (hf == 0 && lane == 0) bulk_wait_read();
+      __syncwarp();
+      named_bar_sync(3 + quarter, 64);
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->abd_full, static_cast<uint32_t>(g) & 1, wc, abort));
       tc_fence_after();
-      uint32_t ho[16], ao[16], bo[16];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        uint32_t a[16], b[16], d[16];
+        uint32_t a[16], b[16], d[16], h[8];
         tmem_ld16x3_wait(abd + 16 * j, a, abd + 64 + 16 * j, b, abd + 128 + 16 * j, d);
         if (j == 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cta(&bars->abd_free, 0);
         }
+        uint32_t da[8], db[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float2 hv, av, bv;
           gate_bwd2<ACT>(make_float2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1])),
                          make_float2(__uint_as_float(b[2 * e]), __uint_as_float(b[2 * e + 1])),
                          make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])), hv, av, bv);
-          ho[8 * j + e] = pack_bf16x2(hv.x, hv.y);
-          ao[8 * j + e] = pack_bf16x2(av.x, av.y);
-          bo[8 * j + e] = pack_bf16x2(bv.x, bv.y);
+          h[e] = pack_bf16x2(hv.x, hv.y);
+          da[e] = pack_bf16x2(av.x, av.y);
+          db[e] = pack_bf16x2(bv.x, bv.y);
+        }
+        if (j == 0) {
+          // the previous chunk's dx has read [da | db]
+          if (g > 0)
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->dab_free, static_cast<uint32_t>(g - 1) & 1, wc, abort));
+          tc_fence_after();
+        }
+        tmem_st8(dab + 8 * j, da);
+        tmem_st8(dab + 32 + 8 * j, db);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint8_t* const at = stg + sw128(lane, 4 * hf + 2 * j + k);
+          *reinterpret_cast<uint4*>(at) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+          *reinterpret_cast<uint4*>(at + 4096) = make_uint4(da[4 * k], da[4 * k + 1], da[4 * k + 2], da[4 * k + 3]);
+          *reinterpret_cast<uint4*>(at + 8192) = make_uint4(db[4 * k], db[4 * k + 1], db[4 * k + 2], db[4 * k + 3]);
         }
       }
-      // the previous chunk's dx has read [da | db]
-      if (g > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->dab_free, static_cast<uint32_t>(g - 1) & 1, wc, abort)))
-        break;
-      tc_fence_after();
-      tmem_st16(dab, ao);
-      tmem_st16(dab + 32, bo);
       tc_wait_st();
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cta(&bars->dab_full, 0);
-      if (lane == 0) bulk_wait_read();  // the chunk before's stores have read the staging buffers
-      __syncwarp();
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {  // 64-byte swizzled rows
-        uint8_t* const at = stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
-        *reinterpret_cast<uint4*>(at) = make_uint4(ho[4 * j], ho[4 * j + 1], ho[4 * j + 2], ho[4 * j + 3]);
-        *reinterpret_cast<uint4*>(at + 2048) = make_uint4(ao[4 * j], ao[4 * j + 1], ao[4 * j + 2], ao[4 * j + 3]);
-        *reinterpret_cast<uint4*>(at + 4096) = make_uint4(bo[4 * j], bo[4 * j + 1], bo[4 * j + 2], bo[4 * j + 3]);
-      }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0 && hid < p.H && row0 < p.M) {
-        tma_store_3d(&tm_h, stg, hid, static_cast<int>(row0), 0);
-        tma_store_3d(&tm_dab, stg + 2048, hid, static_cast<int>(row0), 0);
-        tma_store_3d(&tm_dab, stg + 4096, p.H + hid, static_cast<int>(row0), 0);
+      if (lane == 0) mbar_arrive_cta(&bars->dab_full, 0);
+      named_bar_sync(3 + quarter, 64);
+      if (hf == 0 && lane == 0 && ok && row0 < p.M) {
+        tma_store_3d(&tm_h, stg, 64 * i, static_cast<int>(row0), 0);
+        tma_store_3d(&tm_dab, stg + 4096, 64 * i, 0, static_cast<int>(row0));
+        tma_store_3d(&tm_dab, stg + 8192, 64 * i, 1, static_cast<int>(row0));
       }
       if (++i == p.chunks) {
         i = 0;
@@ -611,11 +658,11 @@ cudaError_t launch_transition_bwd(long long M, int C, int H, int act, const void
   const cuuint64_t c = static_cast<cuuint64_t>(C), hh = static_cast<cuuint64_t>(H), mm = static_cast<cuuint64_t>(M);
   const cuuint64_t zd[3] = {c, mm, 1}, zs[2] = {2 * c, 2 * c * mm};
   const cuuint64_t hd[3] = {hh, mm, 1}, hs[2] = {2 * hh, 2 * hh * mm};
-  const cuuint64_t ad[3] = {2 * hh, mm, 1}, as[2] = {4 * hh, 4 * hh * mm};
+  const cuuint64_t ad[3] = {hh, 2, mm}, as[2] = {2 * hh, 4 * hh};  // the a and b columns apart: past H is left out
   const cuuint64_t wd[3] = {hh, 2, c}, ws[2] = {2 * hh, 4 * hh};  // the a and b columns apart: past H reads 0
   const cuuint64_t od[3] = {c, hh, 1}, os[2] = {2 * c, 2 * c * hh};
   if (!tf_map(&m.z, z, zd, zs, 128, 1) || !tf_map(&m.dout, d_out, zd, zs, 128, 1) ||
-      !tf_map(&m.dz, dz, zd, zs, 128, 1) || !tf_map32(&m.h, h, hd, hs) || !tf_map32(&m.dab, dab, ad, as) ||
+      !tf_map(&m.dz, dz, zd, zs, 128, 1) || !tf_map(&m.h, h, hd, hs, 32, 1) || !tf_map(&m.dab, dab, ad, as, 1, 32) ||
       !tf_map(&m.win, w_in, wd, ws, 1, static_cast<cuuint32_t>(C)) || !tf_map(&m.wo, w_o, od, os, 32, 1) ||
       !tf_map(&m.wx, w_in, wd, ws, 1, static_cast<cuuint32_t>(C / 2)))
     return cudaErrorInvalidValue;
