@@ -151,9 +151,7 @@ cudaError_t launch_gate_bwd_proj(int B, long long NN, int Cz, int Ch, const void
                                  const WaitCtl& wc, cudaStream_t s);
 // The driver's cuTensorMapEncodeTiled (PFN_cuTensorMapEncodeTiled_v12000), or null.
 void* tensor_map_encoder();
-// The transition's fused forward (transition_fwd.cu): whether its rule takes
-// this width, and the launch (arguments as in triattn_transition_fwd).
-bool transition_fwd_fused(int C, int H);
+// The transition's forward (transition_fwd.cu; arguments as in triattn_transition_fwd).
 cudaError_t launch_transition_fwd(long long M, int C, int H, int act, const void* z, const void* mask,
                                   const float* ln_w, const float* ln_b, const void* w_in, const void* w_o, void* out,
                                   const WaitCtl& wc, cudaStream_t s);
@@ -162,7 +160,7 @@ cudaError_t launch_transition_fwd(long long M, int C, int H, int act, const void
 // (written only with a mask), h [M, H] and [da | db] [M, 2H], all BF16;
 // *parts (at most kTbPartRows) partial rows of d_ln_w and d_ln_b.
 constexpr int kTbPartRows = 152 * 4;
-bool transition_bwd_fused(int C, int H);
+bool transition_bwd_fused(int C);
 cudaError_t launch_transition_bwd(long long M, int C, int H, int act, const void* z, const void* mask,
                                   const float* ln_w, const float* ln_b, const void* w_in, const void* w_o,
                                   const void* d_out, void* dz, void* x, void* g, void* h, void* dab, float* part_g,

@@ -456,6 +456,12 @@ __device__ __forceinline__ void mma_ts_pair(uint32_t d_tmem, uint32_t a_tmem, ui
           d_tmem),
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(accum));
 }
+__device__ __forceinline__ void mma_ss_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+          d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accum));
+}
 // Arrival on the barrier at this offset in both CTAs once every MMA issued so
 // far has completed.
 __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {

@@ -43,26 +43,6 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 __device__ __forceinline__ uint4 ld16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ void st16(uint16_t* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
 
-// h = act(a) b m, 8 features per thread (P [M, 2H] = a | b, h [M, H]).
-template <int ACT>
-__global__ void __launch_bounds__(256) gate_fwd_kernel(const uint16_t* __restrict__ P,
-                                                       const uint16_t* __restrict__ mask, uint16_t* __restrict__ h,
-                                                       int H, size_t M) {
-  const size_t chunks = H / 8;
-  for (size_t t = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < M * chunks;
-       t += static_cast<size_t>(gridDim.x) * blockDim.x) {
-    const size_t m = t / chunks;
-    const int c0 = 8 * static_cast<int>(t % chunks);
-    float a[8], b[8];
-    unpack8(ld16(P + m * 2 * H + c0), a);
-    unpack8(ld16(P + m * 2 * H + H + c0), b);
-    const float mk = mask != nullptr ? bf16lo_to_f32(mask[m]) : 1.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a[e] = act_fwd<ACT>(a[e]) * b[e] * mk;
-    st16(h + m * H + c0, pack8(a));
-  }
-}
-
 // h = act(a) b, and [da | db] over P in place, from dh [M, H].
 template <int ACT>
 __global__ void __launch_bounds__(256) gate_bwd_kernel(uint16_t* __restrict__ P, const uint16_t* __restrict__ dh,
@@ -148,14 +128,14 @@ struct TrWs {
 TrWs tr_ws(const TrDims& d, bool bwd) {
   TrWs w;
   size_t o = 0;
-  if (!bwd && transition_fwd_fused(d.C, d.H)) {  // the fused forward keeps everything on the chip
+  if (!bwd) {  // the forward keeps everything on the chip
     w.gemm = w.x = w.mean = w.rstd = w.P = w.h = w.g = w.dh = w.dx = w.pg = w.pb = 0;
     w.total = 256;
     return w;
   }
   w.gemm = o; o += rup(kGemmWorkspace);
   w.x = o;    o += rup(d.M * d.C * 2);
-  if (bwd && transition_bwd_fused(d.C, d.H)) {
+  if (transition_bwd_fused(d.C)) {
     w.P = o;  o += rup(d.M * d.H * 4);
     w.h = o;  o += rup(d.M * d.H * 2);
     w.g = o;  o += rup(d.M * d.C * 2);
@@ -168,14 +148,11 @@ TrWs tr_ws(const TrDims& d, bool bwd) {
   w.rstd = o; o += rup(d.M * 4);
   w.P = o;    o += rup(d.M * d.H * 4);
   w.h = o;    o += rup(d.M * d.H * 2);
-  w.g = w.dh = w.dx = w.pg = w.pb = o;
-  if (bwd) {
-    w.g = o;  o += rup(d.M * d.C * 2);
-    w.dh = o; o += rup(d.M * d.H * 2);
-    w.dx = o; o += rup(d.M * d.C * 2);
-    w.pg = o; o += rup(static_cast<size_t>(kLnBlocks) * d.C * 4);
-    w.pb = o; o += rup(static_cast<size_t>(kLnBlocks) * d.C * 4);
-  }
+  w.g = o;    o += rup(d.M * d.C * 2);
+  w.dh = o;   o += rup(d.M * d.H * 2);
+  w.dx = o;   o += rup(d.M * d.C * 2);
+  w.pg = o;   o += rup(static_cast<size_t>(kLnBlocks) * d.C * 4);
+  w.pb = o;   o += rup(static_cast<size_t>(kLnBlocks) * d.C * 4);
   w.total = o;
   return w;
 }
@@ -248,32 +225,11 @@ triattn_status triattn_transition_fwd(const triattn_transition_shape* shape, con
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < w.total)
     return TRIATTN_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (transition_fwd_fused(d.C, d.H)) {
-    const cudaError_t e = trace_call(kKTrFwd, s, [&] {
-      return launch_transition_fwd(shape->M, d.C, d.H, d.act, z, mask, ln_w, ln_b, w_in, w_o, out, current_wait_ctl(),
-                                   s);
-    });
-    return e == cudaSuccess ? TRIATTN_OK : TRIATTN_ERR_CUDA;
-  }
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  void* const gws = ws + w.gemm;
-  const int M = static_cast<int>(d.M);
-  uint16_t* P = reinterpret_cast<uint16_t*>(ws + w.P);
-  uint16_t* h = reinterpret_cast<uint16_t*>(ws + w.h);
-  if (trace_call(kKTrLn, s, [&] { return ln_fwd_rows(d, z, mask, ln_w, ln_b, ws, w, s); }) != cudaSuccess)
-    return TRIATTN_ERR_CUDA;
-  if (gemm_traced(kKTrGemm, gws, s, false, false, M, 2 * d.H, d.C, ws + w.x, d.C, w_in, 2 * d.H, P, 2 * d.H, false) !=
-      TRIATTN_OK)
-    return TRIATTN_ERR_CUDA;
-  if (trace_call(kKTrGate, s, [&] {
-        return by_act(d.act, [&](auto ic) {
-          gate_fwd_kernel<decltype(ic)::value><<<grid_for(d.M * d.H / 8), 256, 0, s>>>(
-              P, static_cast<const uint16_t*>(mask), h, d.H, d.M);
-          return cudaGetLastError();
-        });
-      }) != cudaSuccess)
-    return TRIATTN_ERR_CUDA;
-  return gemm_traced(kKTrGemm, gws, s, false, false, M, d.C, d.H, h, d.H, w_o, d.C, out, d.C, false);
+  const cudaError_t e = trace_call(kKTrFwd, s, [&] {
+    return launch_transition_fwd(shape->M, d.C, d.H, d.act, z, mask, ln_w, ln_b, w_in, w_o, out, current_wait_ctl(),
+                                 s);
+  });
+  return e == cudaSuccess ? TRIATTN_OK : TRIATTN_ERR_CUDA;
 }
 
 triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, const void* z, const void* mask,
@@ -329,7 +285,7 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
              return cudaGetLastError();
            }) == cudaSuccess;
   };
-  if (transition_bwd_fused(C, H)) {
+  if (transition_bwd_fused(C)) {
     if (mk != nullptr) g = ws + w.g;
     if (trace_call(kKTrBwd, s, [&] {
           return launch_transition_bwd(shape->M, C, H, d.act, z, mask, ln_w, ln_b, w_in, w_o, d_out, dz, ws + w.x,

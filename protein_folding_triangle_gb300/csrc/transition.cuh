@@ -13,17 +13,6 @@ namespace {
 // act(a) and act'(a).  Each takes one hardware tanh (absolute error about
 // 2^-11, below the BF16 rounding of h): sigmoid(a) = (1 + tanh(a / 2)) / 2.
 template <int ACT>
-__device__ __forceinline__ float act_fwd(float a) {
-  if constexpr (ACT == TRIATTN_ACT_GELU) {
-    const float u = a * fmaf(0.0356774081f * a, a, 0.7978845608f);  // sqrt(2/pi) (a + 0.044715 a^3)
-    const float ha = 0.5f * a;
-    return fmaf(ha, tanh_approx(u), ha);
-  } else {
-    const float s = fmaf(0.5f, tanh_approx(0.5f * a), 0.5f);
-    return ACT == TRIATTN_ACT_SILU ? a * s : s;
-  }
-}
-template <int ACT>
 __device__ __forceinline__ void act_both(float a, float& f, float& df) {
   if constexpr (ACT == TRIATTN_ACT_GELU) {
     const float a2 = a * a;
@@ -94,9 +83,9 @@ __device__ __forceinline__ float2 bf16x2_to_f32x2(uint32_t w) {
 
 // Mean and 1 / sqrt(variance + eps) of a row of C features held as C / 8
 // chunks of 16 bytes at z16(c), in one pass about the mean k of its first 8
-// features: |k - mean| is at most sqrt((C - 8) / 8) < 4 standard deviations
+// features: |k - mean| is at most sqrt((C - 8) / 8) < 6 standard deviations
 // whatever the row holds, so that the difference below loses less than a
-// factor of 17 of the FP32 precision.
+// factor of 37 of the FP32 precision.
 template <int C, typename F>
 __device__ __forceinline__ float2 row_stats(F&& z16) {
   float k;

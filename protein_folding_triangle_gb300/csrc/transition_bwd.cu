@@ -648,7 +648,7 @@ cudaError_t tb_launch(const TbMaps& m, TbParams p, int grid, cudaStream_t s) {
 
 }  // namespace
 
-bool transition_bwd_fused(int C, int) { return C <= 128; }
+bool transition_bwd_fused(int C) { return C <= 128; }
 
 cudaError_t launch_transition_bwd(long long M, int C, int H, int act, const void* z, const void* mask,
                                   const float* ln_w, const float* ln_b, const void* w_in, const void* w_o,

@@ -366,3 +366,11 @@ def test_tensors_on_16_byte_boundaries(C, H):
     torch.cuda.synchronize()
     for a, b in zip(ref, (out,) + tuple(grads)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("C,H", [(32, 2112), (64, 1504), (128, 1024), (128, 4096), (160, 2048), (224, 96), (256, 1536)])
+@pytest.mark.parametrize("M", [1, 300, 2600])
+def test_hidden_widths_past_shared_memory(C, H, M):
+    """Hidden widths whose weights do not stay in shared memory, with fewer and
+    more row tiles than a cluster pair takes at once."""
+    check(S.make_transition_inputs((M,), C, H, seed=C + H + M, drop=0.1 if M > 1 else 0.0), case=[C, H, M])
