@@ -482,8 +482,8 @@ triattn_status triattn_trimul_bwd(const triattn_trimul_shape* shape, const void*
  *   w_in [C, 2H] bf16, w_o [H, C] bf16
  *   d_ln_w, d_ln_b [C], d_w_in [C, 2H], d_w_o [H, C]  fp32 or bf16 (flags);
  *                      overwritten, not accumulated
- *   workspace  triattn_transition_workspace_bytes(shape, backward) bytes,
- *              256-byte aligned, contents ignored.
+ *   workspace  of the backward: triattn_transition_workspace_bytes(shape)
+ *              bytes, 256-byte aligned, contents ignored.
  *
  * Bitwise reproducible for a fixed shape and device.  Argument errors
  * return before anything is launched; a failed launch returns
@@ -502,12 +502,12 @@ typedef struct {
   unsigned flags; /* 0 or TRIATTN_FLAG_GRADS_BF16 */
 } triattn_transition_shape;
 
-size_t triattn_transition_workspace_bytes(const triattn_transition_shape* shape, int backward);
+size_t triattn_transition_workspace_bytes(const triattn_transition_shape* shape);
 
-/* Forward: writes out. */
+/* Forward: writes out.  It needs no workspace. */
 triattn_status triattn_transition_fwd(const triattn_transition_shape* shape, const void* z, const void* mask,
                                       const float* ln_w, const float* ln_b, const void* w_in, const void* w_o,
-                                      void* out, void* workspace, size_t workspace_bytes, void* stream);
+                                      void* out, void* stream);
 
 /* Backward of <out, d_out>: dz (bf16) and the parameter gradients. */
 triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, const void* z, const void* mask,

@@ -125,14 +125,9 @@ TrDims tr_dims(const triattn_transition_shape* s) {
 struct TrWs {
   size_t gemm, x, mean, rstd, P, h, g, dh, dx, pg, pb, total;
 };
-TrWs tr_ws(const TrDims& d, bool bwd) {
+TrWs tr_ws(const TrDims& d) {
   TrWs w;
   size_t o = 0;
-  if (!bwd) {  // the forward keeps everything on the chip
-    w.gemm = w.x = w.mean = w.rstd = w.P = w.h = w.g = w.dh = w.dx = w.pg = w.pb = 0;
-    w.total = 256;
-    return w;
-  }
   w.gemm = o; o += rup(kGemmWorkspace);
   w.x = o;    o += rup(d.M * d.C * 2);
   if (transition_bwd_fused(d.C)) {
@@ -205,14 +200,14 @@ using namespace triattn;
 
 extern "C" {
 
-size_t triattn_transition_workspace_bytes(const triattn_transition_shape* shape, int backward) {
+size_t triattn_transition_workspace_bytes(const triattn_transition_shape* shape) {
   if (check_transition(shape) != TRIATTN_OK) return 0;
-  return tr_ws(tr_dims(shape), backward != 0).total;
+  return tr_ws(tr_dims(shape)).total;
 }
 
 triattn_status triattn_transition_fwd(const triattn_transition_shape* shape, const void* z, const void* mask,
                                       const float* ln_w, const float* ln_b, const void* w_in, const void* w_o,
-                                      void* out, void* workspace, size_t workspace_bytes, void* stream) {
+                                      void* out, void* stream) {
   const triattn_status st = check_transition(shape);
   if (st != TRIATTN_OK) return st;
   if (shape->M == 0) return TRIATTN_OK;
@@ -221,9 +216,6 @@ triattn_status triattn_transition_fwd(const triattn_transition_shape* shape, con
     if (q == nullptr || !al16(q)) return TRIATTN_ERR_INVALID_ARG;
   if (mask != nullptr && !al2(mask)) return TRIATTN_ERR_INVALID_ARG;
   const TrDims d = tr_dims(shape);
-  const TrWs w = tr_ws(d, false);
-  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < w.total)
-    return TRIATTN_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = trace_call(kKTrFwd, s, [&] {
     return launch_transition_fwd(shape->M, d.C, d.H, d.act, z, mask, ln_w, ln_b, w_in, w_o, out, current_wait_ctl(),
@@ -255,7 +247,7 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
   for (const void* q : req)
     if (q == nullptr || !al16(q)) return TRIATTN_ERR_INVALID_ARG;
   if (mask != nullptr && !al2(mask)) return TRIATTN_ERR_INVALID_ARG;
-  const TrWs w = tr_ws(d, true);
+  const TrWs w = tr_ws(d);
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < w.total)
     return TRIATTN_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

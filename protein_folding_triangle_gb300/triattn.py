@@ -152,9 +152,9 @@ def _declare(lib):
     lib.triattn_trimul_bwd.argtypes = [tp] + [vp] * 16 + [ctypes.c_size_t, vp]
     lib.triattn_trimul_bwd.restype = ctypes.c_int
     rp, gp = ctypes.POINTER(TransitionShape), ctypes.POINTER(Tensor)
-    lib.triattn_transition_workspace_bytes.argtypes = [rp, ctypes.c_int]
+    lib.triattn_transition_workspace_bytes.argtypes = [rp]
     lib.triattn_transition_workspace_bytes.restype = ctypes.c_size_t
-    lib.triattn_transition_fwd.argtypes = [rp] + [vp] * 8 + [ctypes.c_size_t, vp]
+    lib.triattn_transition_fwd.argtypes = [rp] + [vp] * 8
     lib.triattn_transition_fwd.restype = ctypes.c_int
     lib.triattn_transition_bwd.argtypes = [rp] + [vp] * 13 + [ctypes.c_size_t, vp]
     lib.triattn_transition_bwd.restype = ctypes.c_int
@@ -630,6 +630,14 @@ def triattn_trimul_bwd(z, mask, ln_in_w, w_p, ln_out_w, w_o, ctx, d_out, directi
     return out
 
 
+def _current_stream_ptr(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the stream's address without a Stream object around it, where torch has that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream_ptr)
+
+
 class _Here:
     """A context that changes nothing."""
 
@@ -649,10 +657,10 @@ def _on_stream(device, stream):
     on, so that a workspace freed at the end of the call is not handed to
     another stream while its kernels still run."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
         if torch.cuda.current_device() == device.index:
-            return _HERE, ctypes.c_void_p(stream.cuda_stream)
-    return torch.cuda.stream(stream), ctypes.c_void_p(stream.cuda_stream)
+            return _HERE, _raw_stream(device.index)
+        stream = torch.cuda.current_stream(device)
+    return torch.cuda.stream(stream), stream.cuda_stream
 
 
 def _same_device(device, **tensors):
@@ -667,10 +675,10 @@ def transition_shape(rows: int, C: int, H: int, activation: str = "silu", grads_
     return TransitionShape(rows, C, H, ACTIVATIONS[activation], FLAG_GRADS_BF16 if grads_bf16 else 0)
 
 
-def transition_workspace_bytes(rows: int, C: int, H: int, backward: bool = False) -> int:
-    """Workspace of the transition's forward or backward; 0 for an unsupported shape."""
+def transition_workspace_bytes(rows: int, C: int, H: int) -> int:
+    """Workspace of the transition's backward; 0 for an unsupported shape."""
     s = transition_shape(rows, C, H)
-    return int(load().triattn_transition_workspace_bytes(ctypes.byref(s), int(backward)))
+    return int(load().triattn_transition_workspace_bytes(ctypes.byref(s)))
 
 
 def _transition_check(z, mask, ln_w, ln_b, w_in, w_o):
@@ -688,30 +696,23 @@ def _transition_check(z, mask, ln_w, ln_b, w_in, w_o):
     return z.numel() // C if C else 0, C, H
 
 
-def triattn_transition_fwd(z, mask, ln_w, ln_b, w_in, w_o, activation: str = "silu", *, workspace=None, out=None,
-                           stream=None):
+def triattn_transition_fwd(z, mask, ln_w, ln_b, w_in, w_o, activation: str = "silu", *, out=None, stream=None):
     """Transition (gated feed-forward block) forward over the rows of z
     [..., C] bf16: out = mask * ((act(a) * b) w_o), [a | b] = LayerNorm(z) w_in.
     ``mask`` [...] bf16 (1 keeps a row, 0 leaves it out) or None; ``activation``
     "silu", "sigmoid" or "gelu" (tanh form).  Returns out [..., C] bf16."""
     M, C, H = _transition_check(z, mask, ln_w, ln_b, w_in, w_o)
     s = transition_shape(M, C, H, activation)
-    lib = load()
-    need = lib.triattn_transition_workspace_bytes(ctypes.byref(s), 0)
-    if need == 0:
-        raise TriAttnError(ERR_UNSUPPORTED, "triattn_transition_fwd")
     here, sp = _on_stream(z.device, stream)
     with here:
-        workspace = torch.empty(need, dtype=torch.uint8, device=z.device) if workspace is None else workspace
         if out is None:
             out = torch.empty_like(z)
         else:
             _check(out, "out", z.shape)
             _same_device(z.device, out=out)
-        _same_device(z.device, workspace=workspace)
-        code = lib.triattn_transition_fwd(ctypes.byref(s), z.data_ptr(), None if mask is None else mask.data_ptr(),
-                                          ln_w.data_ptr(), ln_b.data_ptr(), w_in.data_ptr(), w_o.data_ptr(),
-                                          out.data_ptr(), workspace.data_ptr(), _bytes(workspace), sp)
+        code = load().triattn_transition_fwd(ctypes.byref(s), z.data_ptr(), None if mask is None else mask.data_ptr(),
+                                             ln_w.data_ptr(), ln_b.data_ptr(), w_in.data_ptr(), w_o.data_ptr(),
+                                             out.data_ptr(), sp)
     _raise(code, "triattn_transition_fwd")
     return out
 
@@ -725,7 +726,7 @@ def triattn_transition_bwd(z, mask, ln_w, ln_b, w_in, w_o, d_out, activation: st
     _check(d_out, "d_out", z.shape)
     s = transition_shape(M, C, H, activation, grads_bf16)
     lib = load()
-    need = lib.triattn_transition_workspace_bytes(ctypes.byref(s), 1)
+    need = lib.triattn_transition_workspace_bytes(ctypes.byref(s))
     if need == 0:
         raise TriAttnError(ERR_UNSUPPORTED, "triattn_transition_bwd")
     dt = torch.bfloat16 if grads_bf16 else torch.float32

@@ -337,7 +337,8 @@ def test_refusals_on_device():
     with pytest.raises(ValueError):
         T.triattn_transition_bwd(z, None, lw, lb, wi, wo, x["d_out"][:4])
     with pytest.raises(T.TriAttnError):
-        T.triattn_transition_fwd(z, None, lw, lb, wi, wo, workspace=torch.empty(128, dtype=torch.uint8, device="cuda"))
+        T.triattn_transition_bwd(z, None, lw, lb, wi, wo, x["d_out"],
+                                 workspace=torch.empty(128, dtype=torch.uint8, device="cuda"))
     odd = torch.empty(8 * 64 + 4, dtype=torch.bfloat16, device="cuda")[4:].view(8, 64)  # 8-byte aligned
     with pytest.raises(T.TriAttnError):
         T.triattn_transition_fwd(odd, None, lw, lb, wi, wo)

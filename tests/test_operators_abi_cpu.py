@@ -18,13 +18,13 @@ def lib():
     return T.load()
 
 
-def fwd(lib, shape, nbytes, ws=FAKE, **kw):
+def fwd(lib, shape, **kw):
     names = ("z", "ln_w", "ln_b", "w_in", "w_o", "out")
     p = {n: ctypes.c_void_p(FAKE) for n in names}
     p["mask"] = None
     p.update(kw)
     return lib.triattn_transition_fwd(ctypes.byref(shape), p["z"], p["mask"], p["ln_w"], p["ln_b"], p["w_in"],
-                                      p["w_o"], p["out"], ctypes.c_void_p(ws), ctypes.c_size_t(nbytes), None)
+                                      p["w_o"], p["out"], None)
 
 
 def bwd(lib, shape, nbytes, ws=FAKE, **kw):
@@ -43,38 +43,36 @@ UNSUPPORTED = [(10, 48, 64), (10, 288, 64), (10, 16, 64), (10, 64, 40), (10, 64,
 def test_transition_shapes(lib):
     for M, C, H in [(1, 32, 32), (0, 128, 512), (589824, 128, 512), ((1 << 31) - 1, 256, 4096)]:
         assert T.transition_workspace_bytes(M, C, H) > 0
-        assert T.transition_workspace_bytes(M, C, H, True) > 0
     for bad in UNSUPPORTED:
         s = T.TransitionShape(*bad, 0, 0)
         assert T.transition_workspace_bytes(*bad) == 0, bad
-        assert fwd(lib, s, 1 << 40) == T.ERR_UNSUPPORTED and bwd(lib, s, 1 << 40) == T.ERR_UNSUPPORTED, bad
+        assert fwd(lib, s) == T.ERR_UNSUPPORTED and bwd(lib, s, 1 << 40) == T.ERR_UNSUPPORTED, bad
     for bad in [(-1, 64, 64, 0, 0), (1, 0, 64, 0, 0), (1, 64, 0, 0, 0), (1, 64, 64, 3, 0), (1, 64, 64, -1, 0),
                 (1, 64, 64, 0, 1)]:
         s = T.TransitionShape(*bad)
-        assert lib.triattn_transition_workspace_bytes(ctypes.byref(s), 0) == 0
-        assert fwd(lib, s, 1 << 40) == T.ERR_INVALID_ARG and bwd(lib, s, 1 << 40) == T.ERR_INVALID_ARG, bad
+        assert lib.triattn_transition_workspace_bytes(ctypes.byref(s)) == 0
+        assert fwd(lib, s) == T.ERR_INVALID_ARG and bwd(lib, s, 1 << 40) == T.ERR_INVALID_ARG, bad
     with pytest.raises(ValueError):
         T.transition_shape(1, 64, 64, "tanh")
 
 
 def test_transition_pointers_and_workspace(lib):
     s = T.TransitionShape(10, 64, 64, 0, 0)
-    nf, nb = T.transition_workspace_bytes(10, 64, 64), T.transition_workspace_bytes(10, 64, 64, True)
+    nb = T.transition_workspace_bytes(10, 64, 64)
     for n in ("z", "ln_w", "ln_b", "w_in", "w_o", "out"):
-        assert fwd(lib, s, nf, **{n: None}) == T.ERR_INVALID_ARG, n
-        assert fwd(lib, s, nf, **{n: ctypes.c_void_p(FAKE + 8)}) == T.ERR_INVALID_ARG, n
+        assert fwd(lib, s, **{n: None}) == T.ERR_INVALID_ARG, n
+        assert fwd(lib, s, **{n: ctypes.c_void_p(FAKE + 8)}) == T.ERR_INVALID_ARG, n
     for n in ("z", "ln_w", "ln_b", "w_in", "w_o", "d_out", "dz", "d_ln_w", "d_ln_b", "d_w_in", "d_w_o"):
         assert bwd(lib, s, nb, **{n: None}) == T.ERR_INVALID_ARG, n
         assert bwd(lib, s, nb, **{n: ctypes.c_void_p(FAKE + 8)}) == T.ERR_INVALID_ARG, n
-    assert fwd(lib, s, nf, mask=ctypes.c_void_p(FAKE + 1)) == T.ERR_INVALID_ARG
+    assert fwd(lib, s, mask=ctypes.c_void_p(FAKE + 1)) == T.ERR_INVALID_ARG
     assert bwd(lib, s, nb, mask=ctypes.c_void_p(FAKE + 1)) == T.ERR_INVALID_ARG
-    for call, n in ((fwd, nf), (bwd, nb)):
-        assert call(lib, s, n - 1) == T.ERR_WORKSPACE
-        assert call(lib, s, n, ws=FAKE + 16) == T.ERR_WORKSPACE
-        assert call(lib, s, n, ws=0) == T.ERR_WORKSPACE
+    assert bwd(lib, s, nb - 1) == T.ERR_WORKSPACE
+    assert bwd(lib, s, nb, ws=FAKE + 16) == T.ERR_WORKSPACE
+    assert bwd(lib, s, nb, ws=0) == T.ERR_WORKSPACE
     # no rows: nothing to launch, and nothing to point at
     empty = T.TransitionShape(0, 64, 64, 0, 0)
-    assert fwd(lib, empty, 0, ws=0, z=None, out=None) == T.OK
+    assert fwd(lib, empty, z=None, out=None) == T.OK
 
 
 def table(*entries):
