@@ -528,9 +528,10 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
  * `tensors` and `out` are HOST arrays, read before the call returns; their
  * data are contiguous DEVICE arrays, BF16 or FP32, aligned to their element.
  * Tensors of 0 elements are skipped (their data may be NULL); n = 0 gives
- * norm 0.  An element below 2^40 per tensor.  `norm` is one device float,
+ * norm 0.  Fewer than 2^40 elements per tensor, 2^24 tensors.  `norm` is one device float,
  * 4-byte aligned; no call waits for the device.  Squares are added in FP32
- * per thread and in FP64 above that, in a fixed order: bitwise reproducible.
+ * per block of threads and in FP64 above that, in a fixed order: bitwise
+ * reproducible.
  * A NaN element makes norm NaN; a norm that is not finite makes coef NaN or
  * 0, and the gradients are multiplied by it like any other.  Destinations may
  * share no byte with one another or with a gradient, nor, in place, the

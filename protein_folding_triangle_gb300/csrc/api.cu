@@ -207,7 +207,7 @@ const char* const kKernelName[kKinds] = {"tri_attn_fwd",     "bwd_preprocess",  
                                          "trimul_colsum",   "gemm",            "trimul_proj_gate",
                                          "transition_ln",   "transition_fwd",  "transition_bwd",
                                          "transition_gemm", "transition_gate",
-                                         "transition_ln_bwd", "transition_colsum", "grad_sum",
+                                         "transition_ln_bwd", "transition_colsum", "grad_table", "grad_sum",
                                          "grad_scale",      "grad_norm"};
 struct TraceRec {
   int kind;

@@ -7,10 +7,14 @@
 //
 // Every tensor is cut into chunks of 32 KB on 16-byte boundaries of the
 // address space (the first and last chunk of a tensor may be partly outside
-// it); a fixed grid walks the chunks of all tensors, so a list of many small
-// tensors and a few large ones balance the same way.  The tensor table
-// travels in the kernel's parameters: no copy to the device, nothing kept
-// between calls, and a captured graph holds its own table.
+// it); each block of a fixed grid takes a run of consecutive chunks, so a list
+// of many small tensors and a few large ones balance the same way, and looks a
+// tensor up once, then steps.  The table of a short list travels in the
+// kernels' parameters, that of a long one is put into the workspace by a
+// one-block kernel that has it in its parameters (with 32 KB of parameters
+// every block of a grid costs 35 ns more: 22 us for a grid that does nothing);
+// either way nothing is copied from the host, nothing is kept between calls,
+// and a captured graph holds its own table.
 //
 // Pass 1 reads every gradient once: a thread adds squares in FP32 (at most a
 // few thousand, eight chains), everything above it (warp, block, the sum of
@@ -37,20 +41,26 @@ namespace {
 constexpr int kGnThreads = 256;
 constexpr int kGnUnits = 8;                                   // 16-byte units per thread and chunk
 constexpr long long kGnChunk = 16ll * kGnThreads * kGnUnits;  // 32 KB
+static_assert(152 * 4 % 32 == 0, "the partials by one warp");
 constexpr int kGnGrid = 152 * 4;  // largest grid; the partials (and so the order of the sum) depend on it
-// Table entries of one launch.  The large table nearly fills the 32,764 bytes
-// of kernel parameters; the small one keeps the launch of a short list cheap.
-constexpr int kGnSmall = 96, kGnLarge = 1152;
+// Longest list whose table is a parameter, and entries that one upload carries.
+constexpr int kGnSmall = 96, kGnUpload = 1000;
 
 template <int K>
 struct GnTable {
   uint64_t ptr[K];    // gradient
   uint64_t out[K];    // destination of the scaled gradient
   uint64_t numel[K];  // elements; bit 63: FP32
-  uint32_t end[K];    // chunks of tensors 0 .. k
+  uint64_t end[K];    // chunks of tensors 0 .. k
   int n;
 };
-static_assert(sizeof(GnTable<kGnLarge>) + 64 <= 32764, "kernel parameter limit");
+static_assert(sizeof(GnTable<kGnUpload>) + 64 <= 32764, "kernel parameter limit");
+
+// The same arrays in the workspace.
+struct GnView {
+  uint64_t *ptr, *out, *numel, *end;
+  int n;
+};
 
 struct GnChunk {
   const uint8_t* p;   // 16-byte aligned start of the chunk
@@ -59,27 +69,61 @@ struct GnChunk {
   bool f32;
 };
 
-template <int K>
-__device__ __forceinline__ GnChunk gn_chunk(const GnTable<K>& t, uint32_t c) {
-  int lo = 0, hi = t.n - 1;  // first tensor whose end is above c
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (t.end[mid] > c) hi = mid;
-    else lo = mid + 1;
+__global__ void __launch_bounds__(256) grad_table_kernel(const __grid_constant__ GnTable<kGnUpload> t, GnView v,
+                                                         int at) {
+  for (int i = threadIdx.x; i < t.n; i += 256) {
+    v.ptr[at + i] = t.ptr[i];
+    v.out[at + i] = t.out[i];
+    v.numel[at + i] = t.numel[i];
+    v.end[at + i] = t.end[i];
   }
-  const uint32_t first = lo > 0 ? t.end[lo - 1] : 0u;
-  const uint64_t ne = t.numel[lo];
+}
+
+// First tensor whose end is above chunk c, by all lanes of a warp together.
+__device__ __forceinline__ int gn_find(const GnView& t, uint64_t c) {
+  int lo = 0, n = t.n;  // it is one of [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = static_cast<int>(threadIdx.x & 31) * step;  // the last entry of lane's part, or the last of all
+    const int at = lo + min(i + step, n) - 1;
+    const uint32_t above = __ballot_sync(0xffffffffu, i >= n || t.end[at] > c);
+    const int part = __ffs(above) - 1;
+    lo += part * step;
+    n = min(step, n - part * step);
+  }
+  return lo;
+}
+
+// The run of chunks [c0, c1) of this block.
+__device__ __forceinline__ void gn_run(uint64_t chunks, uint64_t& c0, uint64_t& c1) {
+  const uint64_t per = chunks / gridDim.x, more = chunks % gridDim.x, b = blockIdx.x;
+  c0 = b * per + (b < more ? b : more);
+  c1 = c0 + per + (b < more ? 1 : 0);
+}
+
+// Chunk c of tensor k (k the one it belongs to).
+__device__ __forceinline__ GnChunk gn_chunk(const GnView& t, int k, uint64_t c) {
+  const uint64_t first = k > 0 ? t.end[k - 1] : 0u;
+  const uint64_t ne = t.numel[k], ptr = t.ptr[k];
   GnChunk r;
   r.f32 = (ne >> 63) != 0;
   const long long bytes = static_cast<long long>(ne & ~(1ull << 63)) * (r.f32 ? 4 : 2);
-  const uint64_t base = t.ptr[lo] & ~uint64_t(15);
-  const long long head = static_cast<long long>(t.ptr[lo] - base);
+  const uint64_t base = ptr & ~uint64_t(15);
+  const long long head = static_cast<long long>(ptr - base);
   const long long off = static_cast<long long>(c - first) * kGnChunk;
   r.p = reinterpret_cast<const uint8_t*>(base + off);
   r.lo = max(head - off, 0ll);
   r.hi = min(head + bytes - off, kGnChunk);
-  r.shift = static_cast<long long>(t.out[lo] - t.ptr[lo]);
+  r.shift = static_cast<long long>(t.out[k] - ptr);
   return r;
+}
+template <bool SMALL>
+__device__ __forceinline__ GnView gn_view(const GnTable<kGnSmall>& s, const GnView& v) {
+  if constexpr (SMALL)
+    return GnView{const_cast<uint64_t*>(s.ptr), const_cast<uint64_t*>(s.out), const_cast<uint64_t*>(s.numel),
+                  const_cast<uint64_t*>(s.end), s.n};
+  else
+    return v;
 }
 
 // Values of a 16-byte unit: 4 FP32 or 8 BF16.
@@ -119,41 +163,53 @@ __device__ __forceinline__ uint4 gn_edge(const uint8_t* p, long long lo, long lo
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The combined value of all lanes / warps / blocks: a sum of squares, or a
-// maximum of |g| (NaN above everything).
-__device__ __forceinline__ double gn_join(double a, double b, bool inf) {
+// Two partial values joined: a sum of squares, or a maximum of |g| (NaN above
+// everything).
+template <typename V>
+__device__ __forceinline__ V gn_join(V a, V b, bool inf) {
   if (!inf) return a + b;
-  return (isnan(a) || isnan(b)) ? nan("") : fmax(a, b);
+  return (a != a || b != b) ? a + b : (a > b ? a : b);
 }
-__device__ double gn_block(double v, bool inf, double* red) {
+template <typename V>
+__device__ __forceinline__ V gn_warp(V v, bool inf) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v = gn_join(v, __shfl_xor_sync(0xffffffffu, v, off), inf);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double s = red[0];
-#pragma unroll
-  for (int w = 1; w < kGnThreads / 32; ++w) s = gn_join(s, red[w], inf);
-  return s;
+  return v;
 }
 
-template <int K>
-__global__ void __launch_bounds__(kGnThreads) grad_sum_kernel(const __grid_constant__ GnTable<K> t, int inf,
-                                                              double* __restrict__ part) {
-  __shared__ double red[kGnThreads / 32];
-  const uint32_t chunks = t.n > 0 ? t.end[t.n - 1] : 0u;
+template <bool SMALL>
+__global__ void __launch_bounds__(kGnThreads) grad_sum_kernel(const __grid_constant__ GnTable<kGnSmall> small,
+                                                              const __grid_constant__ GnView big, uint64_t chunks,
+                                                              int inf, float* __restrict__ part) {
+  __shared__ float red[kGnThreads / 32];
+  const GnView t = gn_view<SMALL>(small, big);
   float acc[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const GnChunk k = gn_chunk(t, c);
+  uint64_t c0, c1;
+  gn_run(chunks, c0, c1);
+  int i = c0 < c1 ? gn_find(t, c0) : 0;
+  GnChunk k;
+  if (c0 < c1) k = gn_chunk(t, i, c0);
+  for (uint64_t c = c0; c < c1; ++c) {
+    // the next chunk is looked up while this one's loads are under way
+    GnChunk next = k;
     if (k.lo == 0 && k.hi == kGnChunk) {
       uint4 w[kGnUnits];
 #pragma unroll
       for (int u = 0; u < kGnUnits; ++u)
         w[u] = __ldg(reinterpret_cast<const uint4*>(k.p) + threadIdx.x + u * kGnThreads);
+      if (c + 1 < c1) {
+        while (t.end[i] <= c + 1) ++i;
+        next = gn_chunk(t, i, c + 1);
+      }
 #pragma unroll
       for (int u = 0; u < kGnUnits; ++u) gn_add(w[u], k.f32, inf != 0, acc);
     } else {
+      if (c + 1 < c1) {
+        while (t.end[i] <= c + 1) ++i;
+        next = gn_chunk(t, i, c + 1);
+      }
 #pragma unroll
       for (int u = 0; u < kGnUnits; ++u) {
         const long long at = 16ll * (threadIdx.x + u * kGnThreads);
@@ -163,26 +219,47 @@ __global__ void __launch_bounds__(kGnThreads) grad_sum_kernel(const __grid_const
         gn_add(w, k.f32, inf != 0, acc);
       }
     }
+    k = next;
   }
-  double v = acc[0];
+  // the block's 256 threads pairwise in FP32 (at most 11 roundings more)
 #pragma unroll
-  for (int e = 1; e < 8; ++e) v = gn_join(v, acc[e], inf != 0);
-  v = gn_block(v, inf != 0, red);
-  if (threadIdx.x == 0) part[blockIdx.x] = v;
+  for (int n = 4; n > 0; n >>= 1)
+#pragma unroll
+    for (int e = 0; e < n; ++e) acc[e] = gn_join(acc[e], acc[e + n], inf != 0);
+  const float v = gn_warp(acc[0], inf != 0);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const float s = gn_warp(threadIdx.x < kGnThreads / 32 ? red[threadIdx.x] : 0.f, inf != 0);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
+  }
 }
 
-// The norm from the partials of every launch, the same in every block.
-__device__ float gn_norm(const double* __restrict__ part, int n, bool inf, double* red) {
-  double v = 0.0;
-  for (int i = threadIdx.x; i < n; i += kGnThreads) v = gn_join(v, part[i], inf);
-  v = gn_block(v, inf, red);
-  return static_cast<float>(inf ? v : sqrt(v));
+// The norm from the blocks' partials, the same in every block: by one warp,
+// in FP64 (two adds per clock and SM: with every thread of every block taking
+// part, this alone took 20 us).
+__device__ float gn_norm(const float* __restrict__ part, int n, bool inf, float* red) {
+  if (threadIdx.x < 32) {
+    float p[kGnGrid / 32];  // every load under way before the first sum
+#pragma unroll
+    for (int k = 0; k < kGnGrid / 32; ++k) {
+      const int i = threadIdx.x + 32 * k;
+      p[k] = i < n ? part[i] : 0.f;
+    }
+    double v = 0.0;
+#pragma unroll
+    for (int k = 0; k < kGnGrid / 32; ++k) v = gn_join(v, static_cast<double>(p[k]), inf);
+    v = gn_warp(v, inf);
+    if (threadIdx.x == 0) *red = static_cast<float>(inf ? v : sqrt(v));
+  }
+  __syncthreads();
+  return *red;
 }
 
-__global__ void __launch_bounds__(kGnThreads) grad_norm_kernel(const double* __restrict__ part, int n, int inf,
-                                                               float* __restrict__ norm) {
-  __shared__ double red[kGnThreads / 32];
-  const float v = gn_norm(part, n, inf != 0, red);
+__global__ void __launch_bounds__(32) grad_norm_kernel(const float* __restrict__ part, int n, int inf,
+                                                       float* __restrict__ norm) {
+  __shared__ float red;
+  const float v = gn_norm(part, n, inf != 0, &red);
   if (threadIdx.x == 0) *norm = v;
 }
 
@@ -210,20 +287,25 @@ __device__ __forceinline__ void gn_store_edge(uint8_t* p, uint4 w, long long lo,
   }
 }
 
-template <int K>
-__global__ void __launch_bounds__(kGnThreads) grad_scale_kernel(const __grid_constant__ GnTable<K> t,
-                                                                const double* __restrict__ part, int nparts, int inf,
+template <bool SMALL>
+__global__ void __launch_bounds__(kGnThreads) grad_scale_kernel(const __grid_constant__ GnTable<kGnSmall> small,
+                                                                const __grid_constant__ GnView big, uint64_t chunks,
+                                                                const float* __restrict__ part, int inf,
                                                                 float max_norm, int in_place,
                                                                 float* __restrict__ norm) {
-  __shared__ double red[kGnThreads / 32];
-  const float nv = gn_norm(part, nparts, inf != 0, red);
-  if (blockIdx.x == 0 && threadIdx.x == 0 && norm != nullptr) *norm = nv;
+  __shared__ float red;
+  const float nv = gn_norm(part, gridDim.x, inf != 0, &red);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = nv;
   const float q = max_norm / (nv + 1e-6f);
   const float coef = q > 1.f ? 1.f : q;  // NaN stays NaN
   if (in_place && coef == 1.f) return;
-  const uint32_t chunks = t.n > 0 ? t.end[t.n - 1] : 0u;
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const GnChunk k = gn_chunk(t, chunks - 1 - c);
+  const GnView t = gn_view<SMALL>(small, big);
+  uint64_t c0, c1;
+  gn_run(chunks, c0, c1);
+  int i = c0 < c1 ? gn_find(t, c1 - 1) : 0;
+  for (uint64_t c = c1; c-- > c0;) {  // the block's last chunk first: it was read last
+    while (i > 0 && t.end[i - 1] > c) --i;
+    const GnChunk k = gn_chunk(t, i, c);
     const bool vec = (k.shift & 15) == 0;  // source and destination units coincide
     uint8_t* dst = const_cast<uint8_t*>(k.p) + k.shift;
     if (vec && k.lo == 0 && k.hi == kGnChunk) {
@@ -251,8 +333,6 @@ __global__ void __launch_bounds__(kGnThreads) grad_scale_kernel(const __grid_con
 }
 
 // ---------------------------------------------------------------- host side
-int gn_launches(long long n) { return static_cast<int>((n + kGnLarge - 1) / kGnLarge); }
-
 long long gn_bytes(const triattn_tensor& t) { return t.numel * (t.dtype == TRIATTN_DTYPE_FP32 ? 4 : 2); }
 
 triattn_status gn_check(const triattn_tensor* ts, long long n) {
@@ -264,7 +344,6 @@ triattn_status gn_check(const triattn_tensor* ts, long long n) {
     if (t.numel == 0) continue;
     const uintptr_t es = t.dtype == TRIATTN_DTYPE_FP32 ? 4 : 2;
     if (t.data == nullptr || (reinterpret_cast<uintptr_t>(t.data) & (es - 1)) != 0) return TRIATTN_ERR_INVALID_ARG;
-    // chunks are counted in 32 bits over one launch's tensors
     if (t.numel >= (1ll << 40)) return TRIATTN_ERR_UNSUPPORTED;
   }
   return TRIATTN_OK;
@@ -287,74 +366,82 @@ std::vector<Span> gn_spans(const triattn_tensor* ts, long long n) {
   return v;
 }
 
-// Table of tensors [i0, i1); false if their chunks exceed 32 bits.
+// Where a call's parts lie in the workspace: the blocks' partials, then the
+// table's four columns (long lists).
+struct GnWs {
+  size_t part, table, total;
+};
+GnWs gn_ws(long long n) {
+  GnWs w;
+  w.part = 0;
+  w.table = (kGnGrid * sizeof(float) + 255) / 256 * 256;
+  w.total = w.table + (n > kGnSmall ? static_cast<size_t>(n) * 4 * sizeof(uint64_t) : 0);
+  return w;
+}
+
 template <int K>
-bool gn_fill(GnTable<K>* t, const triattn_tensor* ts, const triattn_tensor* out, long long i0, long long i1) {
-  t->n = 0;
-  uint64_t end = 0;
-  for (long long i = i0; i < i1; ++i) {
-    if (ts[i].numel == 0) continue;
-    const uint64_t p = reinterpret_cast<uint64_t>(ts[i].data);
-    const int k = t->n++;
-    t->ptr[k] = p;
-    t->out[k] = out != nullptr ? reinterpret_cast<uint64_t>(out[i].data) : p;
-    t->numel[k] = static_cast<uint64_t>(ts[i].numel) | (ts[i].dtype == TRIATTN_DTYPE_FP32 ? 1ull << 63 : 0ull);
-    end += ((p & 15) + gn_bytes(ts[i]) + kGnChunk - 1) / kGnChunk;
-    if (end > 0x7fffffffull) return false;
-    t->end[k] = static_cast<uint32_t>(end);
+void gn_entry(GnTable<K>* t, const triattn_tensor& g, const triattn_tensor* out, uint64_t* end) {
+  const uint64_t p = reinterpret_cast<uint64_t>(g.data);
+  const int k = t->n++;
+  t->ptr[k] = p;
+  t->out[k] = out != nullptr ? reinterpret_cast<uint64_t>(out->data) : p;
+  t->numel[k] = static_cast<uint64_t>(g.numel) | (g.dtype == TRIATTN_DTYPE_FP32 ? 1ull << 63 : 0ull);
+  *end += ((p & 15) + gn_bytes(g) + kGnChunk - 1) / kGnChunk;
+  t->end[k] = *end;
+}
+
+// One call's tables: the list without its empty tensors, in `small` or uploaded.
+struct GnCall {
+  GnTable<kGnSmall> small;
+  GnView big;
+  uint64_t chunks;
+  bool is_small;
+  unsigned grid;  // one block per chunk up to the full grid
+  float* part;
+};
+triattn_status gn_prepare(GnCall* c, const triattn_tensor* ts, const triattn_tensor* out, long long n, void* workspace,
+                          cudaStream_t s) {
+  const GnWs w = gn_ws(n);
+  c->part = static_cast<float*>(workspace);
+  c->is_small = n <= kGnSmall;
+  c->chunks = 0;
+  c->small.n = 0;
+  c->big.n = 0;
+  if (c->is_small) {
+    for (long long i = 0; i < n; ++i)
+      if (ts[i].numel > 0) gn_entry(&c->small, ts[i], out != nullptr ? &out[i] : nullptr, &c->chunks);
+  } else {
+    uint64_t* col = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(workspace) + w.table);
+    c->big.ptr = col;
+    c->big.out = col + n;
+    c->big.numel = col + 2 * n;
+    c->big.end = col + 3 * n;
+    GnTable<kGnUpload> t;
+    for (long long i = 0; i < n;) {
+      t.n = 0;
+      for (; i < n && t.n < kGnUpload; ++i)
+        if (ts[i].numel > 0) gn_entry(&t, ts[i], out != nullptr ? &out[i] : nullptr, &c->chunks);
+      if (t.n == 0) break;
+      const int at = c->big.n;
+      const cudaError_t e = trace_call(kKGradTable, s, [&] {
+        grad_table_kernel<<<1, 256, 0, s>>>(t, c->big, at);
+        return cudaGetLastError();
+      });
+      if (e != cudaSuccess) return TRIATTN_ERR_CUDA;
+      c->big.n += t.n;
+    }
   }
-  return true;
-}
-
-// Blocks of a launch: one per chunk up to the full grid.  Several launches
-// leave kGnGrid partials each, a single one as many as it has blocks.
-template <int K>
-unsigned gn_blocks(const GnTable<K>& t) {
-  const uint32_t chunks = t.n > 0 ? t.end[t.n - 1] : 1u;
-  return std::min<uint32_t>(chunks, kGnGrid);
-}
-
-template <int K, bool SCALE>
-triattn_status gn_launch(const triattn_tensor* ts, const triattn_tensor* out, long long i0, long long i1, int inf,
-                         double* part, int launches, float max_norm, float* norm, cudaStream_t s) {
-  GnTable<K> t;
-  if (!gn_fill(&t, ts, out, i0, i1)) return TRIATTN_ERR_UNSUPPORTED;
-  const unsigned grid = gn_blocks(t);
-  const cudaError_t e = trace_call(SCALE ? kKGradScale : kKGradSum, s, [&] {
-    if constexpr (SCALE)
-      grad_scale_kernel<K><<<grid, kGnThreads, 0, s>>>(t, part, launches > 1 ? launches * kGnGrid : grid, inf, max_norm,
-                                                       out == nullptr ? 1 : 0, norm);
-    else
-      grad_sum_kernel<K><<<launches > 1 ? kGnGrid : grid, kGnThreads, 0, s>>>(t, inf, part);
-    return cudaGetLastError();
-  });
-  return e == cudaSuccess ? TRIATTN_OK : TRIATTN_ERR_CUDA;
-}
-
-template <bool SCALE>
-triattn_status gn_pass(const triattn_tensor* ts, const triattn_tensor* out, long long n, int inf, double* part,
-                       float max_norm, float* norm, cudaStream_t s) {
-  const int L = gn_launches(n);
-  for (int j = 0; j < L; ++j) {
-    const int l = SCALE ? L - 1 - j : j;  // the last tensors read first: they are in L2
-    const long long i0 = static_cast<long long>(l) * kGnLarge, i1 = std::min<long long>(n, i0 + kGnLarge);
-    double* p = SCALE ? part : part + static_cast<size_t>(l) * kGnGrid;
-    float* nm = j == 0 ? norm : nullptr;
-    const triattn_status st = i1 - i0 <= kGnSmall
-                                  ? gn_launch<kGnSmall, SCALE>(ts, out, i0, i1, inf, p, L, max_norm, nm, s)
-                                  : gn_launch<kGnLarge, SCALE>(ts, out, i0, i1, inf, p, L, max_norm, nm, s);
-    if (st != TRIATTN_OK) return st;
-  }
+  c->grid = static_cast<unsigned>(std::min<uint64_t>(std::max<uint64_t>(c->chunks, 1), kGnGrid));
   return TRIATTN_OK;
 }
 
-// Partials that a single launch over these tensors leaves.
-int gn_single_parts(const triattn_tensor* ts, long long n) {
-  uint64_t chunks = 0;
-  for (long long i = 0; i < n; ++i)
-    if (ts[i].numel > 0)
-      chunks += ((reinterpret_cast<uint64_t>(ts[i].data) & 15) + gn_bytes(ts[i]) + kGnChunk - 1) / kGnChunk;
-  return static_cast<int>(std::min<uint64_t>(std::max<uint64_t>(chunks, 1), kGnGrid));
+triattn_status gn_sum(const GnCall& c, int inf, cudaStream_t s) {
+  const cudaError_t e = trace_call(kKGradSum, s, [&] {
+    if (c.is_small) grad_sum_kernel<true><<<c.grid, kGnThreads, 0, s>>>(c.small, c.big, c.chunks, inf, c.part);
+    else grad_sum_kernel<false><<<c.grid, kGnThreads, 0, s>>>(c.small, c.big, c.chunks, inf, c.part);
+    return cudaGetLastError();
+  });
+  return e == cudaSuccess ? TRIATTN_OK : TRIATTN_ERR_CUDA;
 }
 
 triattn_status gn_check_call(const triattn_tensor* ts, long long n, int norm_type, const float* norm,
@@ -363,16 +450,8 @@ triattn_status gn_check_call(const triattn_tensor* ts, long long n, int norm_typ
   if (st != TRIATTN_OK) return st;
   if (norm_type != TRIATTN_NORM_L2 && norm_type != TRIATTN_NORM_MAX) return TRIATTN_ERR_INVALID_ARG;
   if (norm == nullptr || (reinterpret_cast<uintptr_t>(norm) & 3u) != 0) return TRIATTN_ERR_INVALID_ARG;
-  if (n > 0 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-                workspace_bytes < triattn_grad_norm_workspace_bytes(n)))
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < gn_ws(n).total)
     return TRIATTN_ERR_WORKSPACE;
-  // every launch's chunk count fits before the first launch
-  for (long long i0 = 0; i0 < n; i0 += kGnLarge) {
-    uint64_t chunks = 0;
-    for (long long i = i0; i < std::min<long long>(n, i0 + kGnLarge); ++i)
-      chunks += (static_cast<uint64_t>(gn_bytes(ts[i])) + 15) / kGnChunk + 1;
-    if (chunks > 0x7fffffffull) return TRIATTN_ERR_UNSUPPORTED;
-  }
   return TRIATTN_OK;
 }
 
@@ -385,7 +464,7 @@ extern "C" {
 
 size_t triattn_grad_norm_workspace_bytes(long long n) {
   if (n < 0 || n > (1ll << 24)) return 0;
-  return static_cast<size_t>(gn_launches(n)) * kGnGrid * sizeof(double);
+  return gn_ws(n).total;
 }
 
 triattn_status triattn_grad_norm(const triattn_tensor* tensors, long long n, int norm_type, float* norm,
@@ -393,12 +472,12 @@ triattn_status triattn_grad_norm(const triattn_tensor* tensors, long long n, int
   triattn_status st = gn_check_call(tensors, n, norm_type, norm, workspace, workspace_bytes);
   if (st != TRIATTN_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  double* part = static_cast<double*>(workspace);
   const int inf = norm_type == TRIATTN_NORM_MAX;
-  if ((st = gn_pass<false>(tensors, nullptr, n, inf, part, 0.f, nullptr, s)) != TRIATTN_OK) return st;
-  const int nparts = gn_launches(n) == 1 ? gn_single_parts(tensors, n) : gn_launches(n) * kGnGrid;
+  GnCall c;
+  if ((st = gn_prepare(&c, tensors, nullptr, n, workspace, s)) != TRIATTN_OK) return st;
+  if ((st = gn_sum(c, inf, s)) != TRIATTN_OK) return st;
   const cudaError_t e = trace_call(kKGradNorm, s, [&] {
-    grad_norm_kernel<<<1, kGnThreads, 0, s>>>(part, nparts, inf, norm);
+    grad_norm_kernel<<<1, 32, 0, s>>>(c.part, static_cast<int>(c.grid), inf, norm);
     return cudaGetLastError();
   });
   return e == cudaSuccess ? TRIATTN_OK : TRIATTN_ERR_CUDA;
@@ -434,17 +513,21 @@ triattn_status triattn_clip_grad_norm(const triattn_tensor* tensors, const triat
     return TRIATTN_ERR_WORKSPACE;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  double* part = static_cast<double*>(workspace);
   const int inf = norm_type == TRIATTN_NORM_MAX;
-  if (n == 0) {
-    const cudaError_t e = trace_call(kKGradNorm, s, [&] {
-      grad_norm_kernel<<<1, kGnThreads, 0, s>>>(part, 0, inf, norm);
-      return cudaGetLastError();
-    });
-    return e == cudaSuccess ? TRIATTN_OK : TRIATTN_ERR_CUDA;
-  }
-  if ((st = gn_pass<false>(tensors, nullptr, n, inf, part, 0.f, nullptr, s)) != TRIATTN_OK) return st;
-  return gn_pass<true>(tensors, out, n, inf, part, max_norm, norm, s);
+  GnCall c;
+  if ((st = gn_prepare(&c, tensors, out, n, workspace, s)) != TRIATTN_OK) return st;
+  if ((st = gn_sum(c, inf, s)) != TRIATTN_OK) return st;
+  const cudaError_t e = trace_call(kKGradScale, s, [&] {
+    const int in_place = out == nullptr ? 1 : 0;
+    if (c.is_small)
+      grad_scale_kernel<true><<<c.grid, kGnThreads, 0, s>>>(c.small, c.big, c.chunks, c.part, inf, max_norm, in_place,
+                                                            norm);
+    else
+      grad_scale_kernel<false><<<c.grid, kGnThreads, 0, s>>>(c.small, c.big, c.chunks, c.part, inf, max_norm, in_place,
+                                                             norm);
+    return cudaGetLastError();
+  });
+  return e == cudaSuccess ? TRIATTN_OK : TRIATTN_ERR_CUDA;
 }
 
 }  // extern "C"

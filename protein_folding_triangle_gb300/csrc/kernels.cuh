@@ -173,7 +173,7 @@ enum KernelKind {
   kKFwd = 0, kKPre, kKTrans, kKMain, kKRedDq, kKRedDb, kKMainAtomic, kKFinDq, kKFinDb, kKCombine, kKFwdPrep,
   kKModLnFwd, kKModLayout, kKModGemm, kKModLnBwd, kKModColSum,
   kKTmLnIn, kKTmProj, kKTmGate, kKTmContract, kKTmLnOut, kKTmOutGate, kKTmColSum, kKGemm, kKTmProjGate,
-  kKTrLn, kKTrFwd, kKTrBwd, kKTrGemm, kKTrGate, kKTrLnBwd, kKTrColSum, kKGradSum, kKGradScale, kKGradNorm,
+  kKTrLn, kKTrFwd, kKTrBwd, kKTrGemm, kKTrGate, kKTrLnBwd, kKTrColSum, kKGradTable, kKGradSum, kKGradScale, kKGradNorm,
   kKinds
 };
 // Runs `launch` on stream `s`, bracketed by a pair of trace events while
