@@ -40,7 +40,7 @@ namespace {
 constexpr int kTbThreads = 20 * 32;
 // Registers per thread of the warpgroups (setmaxnreg): five shares of what the
 // block was launched with (96 each).
-constexpr int kRegsIssue = 40, kRegsRow = 104, kRegsLn = 128, kRegsAct = 104;
+constexpr int kRegsIssue = 40, kRegsRow = 88, kRegsLn = 144, kRegsAct = 104;
 constexpr int kRegsSum = kRegsIssue + kRegsRow + kRegsLn + 2 * kRegsAct;
 constexpr int kTbMaxSlots = 4;
 constexpr int kTbBarBytes = 1024 + 1024;  // barriers, ln_w and ln_b
@@ -66,7 +66,7 @@ struct TbParams {
   int H, chunks, slots, tiles;
   const uint16_t* mask;
   const float *ln_w, *ln_b;
-  uint16_t *x, *g;
+  uint16_t* g;
   float *part_g, *part_b;
   WaitCtl wc;
 };
@@ -101,7 +101,8 @@ __device__ __forceinline__ float rows_scatter_sum(float (&v)[8], int lane) {
 template <int C, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTbThreads, 1)
     transition_bwd_kernel(const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_do,
-                          const __grid_constant__ CUtensorMap tm_dz, const __grid_constant__ CUtensorMap tm_h,
+                          const __grid_constant__ CUtensorMap tm_dz, const __grid_constant__ CUtensorMap tm_x,
+                          const __grid_constant__ CUtensorMap tm_h,
                           const __grid_constant__ CUtensorMap tm_dab, const __grid_constant__ CUtensorMap tm_win,
                           const __grid_constant__ CUtensorMap tm_wo, const __grid_constant__ CUtensorMap tm_wx,
                           const TbParams p) {
@@ -294,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTbThreads, 1)
     }
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ x = LayerNorm(z), g = m d_out
-    regs_inc<kRegsRow>();
+    regs_dec<kRegsRow>();
     const bool first = warp == 4 && lane == 0;
     auto write = [&](int u) -> bool {
       const long long row = tile_row(u) + r;
@@ -368,15 +369,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTbThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(&bars->xg_full, 0);
-      if (in) {
+      // x for the weight gradients takes d_out's place in shared memory (the row
+      // is this thread's) and goes out by TMA: stored from here, 32 bytes per
+      // row and instruction, it cost 80 us at 768 x 768 rows
 #pragma unroll
-        for (int c = 0; c < C / 16; ++c) {
-          uint32_t v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = x[8 * c + e];
-          st_global_v8(p.x + row * C + 16 * c, v);
-        }
-      }
+      for (int c = 0; c < C / 8; ++c)
+        *reinterpret_cast<uint4*>(s_g + (c >> 3) * 16384 + sw128(r, c & 7)) =
+            make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
       return true;
     };
     if (first && mine > 0) {
@@ -387,10 +386,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTbThreads, 1)
     bool ok = true;
     for (int u = 0; u < mine; ++u) {  // no warp leaves the loop early: they meet at its barrier
       ok = ok && write(u);
+      fence_proxy_async_smem();
       __syncwarp();
-      named_bar_sync(1, 128);  // every row of the d_out tile is read
-      if (first && ok && u + 1 < mine) load_rows(s_g, &tm_do, &bars->g_full, u + 1);
+      named_bar_sync(1, 128);  // every row of the d_out tile is read, and x in its place
+      if (first && ok) {
+        if (tile_row(u) < p.M) {
+#pragma unroll
+          for (int b = 0; b < L::kKb; ++b)
+            tma_store_3d(&tm_x, s_g + b * 16384, 64 * b, static_cast<int>(tile_row(u)), 0);
+        }
+        if (u + 1 < mine) {
+          bulk_wait_read();
+          load_rows(s_g, &tm_do, &bars->g_full, u + 1);
+        }
+      }
     }
+    if (first) bulk_wait_all();
+    __syncwarp();
   } else if (warp >= 8 && warp < 12) {
     // ------------------------------------------------------------ LayerNorm backward
     // dz = rstd (t - mean(t) - xhat mean(t xhat)), t = dx ln_w, over the rows of
@@ -628,7 +640,7 @@ int tb_slots() {
 }
 
 struct TbMaps {
-  CUtensorMap z, dout, dz, h, dab, win, wo, wx;
+  CUtensorMap z, dout, dz, x, h, dab, win, wo, wx;
 };
 
 template <int C, int ACT>
@@ -642,7 +654,8 @@ cudaError_t tb_launch(const TbMaps& m, TbParams p, int grid, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // a split above the launch's registers would wait for ever
   if (at.numRegs * (kTbThreads / 128) < kRegsSum) return cudaErrorInvalidConfiguration;
-  transition_bwd_kernel<C, ACT><<<grid, kTbThreads, bytes, s>>>(m.z, m.dout, m.dz, m.h, m.dab, m.win, m.wo, m.wx, p);
+  transition_bwd_kernel<C, ACT><<<grid, kTbThreads, bytes, s>>>(m.z, m.dout, m.dz, m.x, m.h, m.dab, m.win, m.wo,
+                                                                         m.wx, p);
   return cudaGetLastError();
 }
 
@@ -662,7 +675,7 @@ cudaError_t launch_transition_bwd(long long M, int C, int H, int act, const void
   const cuuint64_t wd[3] = {hh, 2, c}, ws[2] = {2 * hh, 4 * hh};  // the a and b columns apart: past H reads 0
   const cuuint64_t od[3] = {c, hh, 1}, os[2] = {2 * c, 2 * c * hh};
   if (!tf_map(&m.z, z, zd, zs, 128, 1) || !tf_map(&m.dout, d_out, zd, zs, 128, 1) ||
-      !tf_map(&m.dz, dz, zd, zs, 128, 1) || !tf_map(&m.h, h, hd, hs, 32, 1) || !tf_map(&m.dab, dab, ad, as, 1, 32) ||
+      !tf_map(&m.dz, dz, zd, zs, 128, 1) || !tf_map(&m.x, x, zd, zs, 128, 1) || !tf_map(&m.h, h, hd, hs, 32, 1) || !tf_map(&m.dab, dab, ad, as, 1, 32) ||
       !tf_map(&m.win, w_in, wd, ws, 1, static_cast<cuuint32_t>(C)) || !tf_map(&m.wo, w_o, od, os, 32, 1) ||
       !tf_map(&m.wx, w_in, wd, ws, 1, static_cast<cuuint32_t>(C / 2)))
     return cudaErrorInvalidValue;
@@ -675,7 +688,6 @@ cudaError_t launch_transition_bwd(long long M, int C, int H, int act, const void
   p.mask = static_cast<const uint16_t*>(mask);
   p.ln_w = ln_w;
   p.ln_b = ln_b;
-  p.x = static_cast<uint16_t*>(x);
   p.g = static_cast<uint16_t*>(g);
   p.part_g = part_g;
   p.part_b = part_b;
