@@ -45,6 +45,11 @@
 //              the core's layout [nblk][B, N, H, N, D] (5-D tensor map), and
 //              the bias columns as 32-element rows into the planes
 //              [B, H, N, N] (4-D map); padding columns are dropped.
+// A fifth serves the transition's backward at widths whose rows do not fit its
+// own kernel:
+//   transition bwd  tile n holds hidden features [128n, 128n + 128) of both
+//              projections, [a | b]; the epilogue reads dh (row-major) and
+//              writes h = act(a) b, da = dh b act'(a) and db = dh act(a).
 // Every mbarrier wait is bounded (WaitCtl): a wait that runs out records a
 // timeout in the device status word and the CTA stops.
 #include <cudaTypedefs.h>
@@ -54,6 +59,7 @@
 #include <mutex>
 
 #include "kernels.cuh"
+#include "transition.cuh"
 
 namespace triattn {
 namespace {
@@ -86,7 +92,8 @@ struct GemmParams {
   WaitCtl wc;
 };
 
-enum GemmMode { kPlain = 0, kGated = 1, kGateBwd = 2, kHeads = 3 };
+// kTrBwd + TRIATTN_ACT_*: the transition's backward
+enum GemmMode { kPlain = 0, kGated = 1, kGateBwd = 2, kHeads = 3, kTrBwd = 4 };
 
 
 
@@ -120,7 +127,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE>::kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_x,
                 const __grid_constant__ CUtensorMap tm_y, GemmParams p) {
-  static_assert(MODE == kPlain || MODE == kHeads || (BN == 256 && !A_MN && B_MN), "gated tiles: K-major x, N-major W_p");
+  static_assert(MODE == kPlain || MODE == kHeads || MODE >= kTrBwd || (BN == 256 && !A_MN && B_MN), "gated tiles: K-major x, N-major W_p");
   static_assert(MODE != kHeads || !A_MN, "heads epilogue: K-major A");
   using L = GemmSmem<BN, MODE>;
   constexpr int GB_S = GemmCfg<MODE>::kS;
@@ -187,7 +194,11 @@ __global__ void __launch_bounds__(GemmCfg<MODE>::kThreads, 1)
           } else {
             tma_load_3d(sa, &tm_a, &bars->full[stage], k0, m0, bt);
           }
-          if constexpr (MODE == kGated || MODE == kGateBwd) {  // the four branch blocks of channels [64 nt, 64 nt + 64), or g
+          if constexpr (MODE >= kTrBwd) {  // hidden features [128 nt, 128 nt + 128) of a and of b
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              tma_load_3d(sb + j * 64 * 128, &tm_b, &bars->full[stage], (j >> 1) * p.Ch + 128 * nt + 64 * (j & 1), k0, bt);
+          } else if constexpr (MODE == kGated || MODE == kGateBwd) {  // the four branch blocks of channels [64 nt, 64 nt + 64), or g
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int col = nt < p.gated_tiles ? j * p.Ch + 64 * nt : 4 * p.Ch + 256 * (nt - p.gated_tiles) + 64 * j;
@@ -431,6 +442,55 @@ __global__ void __launch_bounds__(GemmCfg<MODE>::kThreads, 1)
         issue(&tm_c, bgate, (2 * unit_br + 1) * p.Ch + ch, static_cast<int>(mq), 0);
       }
     };
+    // transition bwd: this lane's row of 32 hidden features, unit `part` of the
+    // tile's 128; dh loaded before the accumulator wait
+    auto load_dh = [&](int mt, int nt, uint32_t (&d)[16]) {
+      const long long m = unit_rows(mt) + lane;
+      const int hid = 128 * nt + 32 * part;
+      if (m >= p.M || hid >= p.Ch) return;
+      const uint4* src = reinterpret_cast<const uint4*>(p.dA + m * p.Ch + hid);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 w = src[c];
+        d[4 * c] = w.x;
+        d[4 * c + 1] = w.y;
+        d[4 * c + 2] = w.z;
+        d[4 * c + 3] = w.w;
+      }
+    };
+    auto transition_tile = [&](int mt, int nt, int ab, const uint32_t (&d)[16]) {
+      const long long mq = unit_rows(mt);
+      const int hid = 128 * nt + 32 * part;
+      if (mq >= p.M || hid >= p.Ch) return;
+      const uint32_t ta = tmem + lane_addr + ab * BN + 32 * part;
+      uint32_t h[16], da[16], db[16];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t a[16], b[16];
+        tmem_ld16x2_wait(ta + 16 * hf, a, ta + 128 + 16 * hf, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float2 hv, av, bv;
+          gate_bwd2<MODE - kTrBwd>(make_float2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1])),
+                                   make_float2(__uint_as_float(b[2 * e]), __uint_as_float(b[2 * e + 1])),
+                                   bf16x2_to_f32x2(d[8 * hf + e]), hv, av, bv);
+          h[8 * hf + e] = pack_bf16x2(hv.x, hv.y);
+          da[8 * hf + e] = pack_bf16x2(av.x, av.y);
+          db[8 * hf + e] = pack_bf16x2(bv.x, bv.y);
+        }
+      }
+      auto put = [&](const uint32_t (&w)[16]) -> uint8_t* {
+        uint8_t* buf = next_buf();
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        return buf;
+      };
+      issue(&tm_x, put(h), hid, static_cast<int>(mq), 0);
+      issue(&tm_c, put(da), hid, 0, static_cast<int>(mq));
+      issue(&tm_c, put(db), hid, 1, static_cast<int>(mq));
+    };
     int local = 0;
     for (long long t = blockIdx.x; t < total; t += gridDim.x, ++local) {
       int mt, nt, bt, ks;
@@ -438,8 +498,15 @@ __global__ void __launch_bounds__(GemmCfg<MODE>::kThreads, 1)
       const int ab = local & 1;
       uint32_t dpre[16];
       if constexpr (MODE == kGateBwd) load_d(mt, nt, dpre);
+      if constexpr (MODE >= kTrBwd) load_dh(mt, nt, dpre);
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->acc_full[ab], (local >> 1) & 1, wc, abort))) break;
       tc_fence_after();
+      if constexpr (MODE >= kTrBwd) {
+        transition_tile(mt, nt, ab, dpre);
+        tc_fence_before();
+        mbar_arrive(&bars->acc_empty[ab]);
+        continue;
+      }
       if constexpr (MODE == kGated || MODE == kGateBwd) {
         if (nt < p.gated_tiles) {
           gated_tile(mt, nt, ab, dpre);
@@ -755,6 +822,38 @@ cudaError_t launch_gate_bwd_proj(int B, long long NN, int Cz, int Ch, const void
   const long long total = static_cast<long long>(p.tiles_m) * p.tiles_n;
   const int grid = static_cast<int>(std::min<long long>(total, gemm_sms()));
   return gemm_launch_t<256, false, true, kGateBwd>(tma, tmb, tmc, tmc, tmc, p, grid, s);
+}
+
+cudaError_t launch_transition_gate(long long M, int C, int H, int act, const void* x, const void* w_in, const void* dh,
+                                   void* h, void* dab, const WaitCtl& wc, cudaStream_t s) {
+  CUtensorMap tma, tmb, tmc, tmx;
+  const cuuint64_t hh = static_cast<cuuint64_t>(H), m = static_cast<cuuint64_t>(M);
+  const cuuint64_t hd[3] = {hh, m, 1}, hs[2] = {2 * hh, 2 * hh * m};
+  const cuuint64_t ad[3] = {hh, 2, m}, as[2] = {2 * hh, 4 * hh};  // the a and b columns apart: past H is left out
+  if (!al16p(x) || !al16p(w_in) || !al16p(dh) || !al16p(h) || !al16p(dab) || M > 0x7fffffffLL ||
+      !gemm_map(&tma, x, C, M, 1, C, 0, 64, 128) || !gemm_map(&tmb, w_in, 2 * H, C, 1, 2 * H, 0, 64, 64) ||
+      !tf_map32(&tmx, h, hd, hs) ||
+      !tf_map_box(&tmc, dab, ad, as, 32u, 1u, 32u, CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
+  GemmParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.M = static_cast<int>(M);
+  p.N = 2 * H;
+  p.K = C;
+  p.batch = 1;
+  p.ksplit = 1;
+  p.kchunk = (C + GB_K - 1) / GB_K * GB_K;
+  p.tiles_m = static_cast<int>((M + GB_M - 1) / GB_M);
+  p.tiles_n = (H + 127) / 128;
+  p.Ch = H;
+  p.NN = 1;
+  p.dA = static_cast<const uint16_t*>(dh);
+  p.wc = wc;
+  const long long total = static_cast<long long>(p.tiles_m) * p.tiles_n;
+  const int grid = static_cast<int>(std::min<long long>(total, gemm_sms()));
+  return by_act(act, [&](auto ic) {
+    return gemm_launch_t<256, false, true, kTrBwd + decltype(ic)::value>(tma, tmb, tmc, tmx, tmx, p, grid, s);
+  });
 }
 
 cudaError_t launch_gemm_heads(bool tb, int M, int N, int K, const void* A, long long lda, const void* B, long long ldb,

@@ -151,6 +151,11 @@ cudaError_t launch_gate_bwd_proj(int B, long long NN, int Cz, int Ch, const void
                                  const WaitCtl& wc, cudaStream_t s);
 // The driver's cuTensorMapEncodeTiled (PFN_cuTensorMapEncodeTiled_v12000), or null.
 void* tensor_map_encoder();
+// The transition's backward through its gating, [a | b] = x W_in computed
+// again (x [M, C], W_in [C, 2H]): h = act(a) b [M, H] and [da | db] [M, 2H] from
+// dh [M, H], all BF16.
+cudaError_t launch_transition_gate(long long M, int C, int H, int act, const void* x, const void* w_in, const void* dh,
+                                   void* h, void* dab, const WaitCtl& wc, cudaStream_t s);
 // The transition's forward (transition_fwd.cu; arguments as in triattn_transition_fwd).
 cudaError_t launch_transition_fwd(long long M, int C, int H, int act, const void* z, const void* mask,
                                   const float* ln_w, const float* ln_b, const void* w_in, const void* w_o, void* out,

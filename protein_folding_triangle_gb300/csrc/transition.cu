@@ -43,33 +43,6 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 __device__ __forceinline__ uint4 ld16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ void st16(uint16_t* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
 
-// h = act(a) b, and [da | db] over P in place, from dh [M, H].
-template <int ACT>
-__global__ void __launch_bounds__(256) gate_bwd_kernel(uint16_t* __restrict__ P, const uint16_t* __restrict__ dh,
-                                                       uint16_t* __restrict__ h, int H, size_t M) {
-  const size_t chunks = H / 8;
-  for (size_t t = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < M * chunks;
-       t += static_cast<size_t>(gridDim.x) * blockDim.x) {
-    const size_t m = t / chunks;
-    const int c0 = 8 * static_cast<int>(t % chunks);
-    float a[8], b[8], d[8], o[8];
-    unpack8(ld16(P + m * 2 * H + c0), a);
-    unpack8(ld16(P + m * 2 * H + H + c0), b);
-    unpack8(ld16(dh + m * H + c0), d);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float f, df;
-      act_both<ACT>(a[e], f, df);
-      o[e] = f * b[e];
-      a[e] = d[e] * b[e] * df;
-      b[e] = d[e] * f;
-    }
-    st16(h + m * H + c0, pack8(o));
-    st16(P + m * 2 * H + c0, pack8(a));
-    st16(P + m * 2 * H + H + c0, pack8(b));
-  }
-}
-
 // g = m d_out, exactly 0 where m is 0 (8 features per thread).
 __global__ void __launch_bounds__(256) mask_rows_kernel(const uint16_t* __restrict__ d_out,
                                                         const uint16_t* __restrict__ mask, uint16_t* __restrict__ g,
@@ -297,14 +270,9 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
         }) != cudaSuccess)
       return TRIATTN_ERR_CUDA;
   }
-  if (!gemm(false, false, M, 2 * H, C, ws + w.x, C, w_in, 2 * H, P, 2 * H, false) ||
-      !gemm(false, true, M, H, C, g, C, w_o, C, dh, H, false))
-    return TRIATTN_ERR_CUDA;
-  if (trace_call(kKTrGate, s, [&] {
-        return by_act(d.act, [&](auto ic) {
-          gate_bwd_kernel<decltype(ic)::value><<<grid_for(d.M * H / 8), 256, 0, s>>>(P, dh, h, H, d.M);
-          return cudaGetLastError();
-        });
+  if (!gemm(false, true, M, H, C, g, C, w_o, C, dh, H, false) ||
+      trace_call(kKTrGate, s, [&] {
+        return launch_transition_gate(shape->M, C, H, d.act, ws + w.x, w_in, dh, h, P, current_wait_ctl(), s);
       }) != cudaSuccess)
     return TRIATTN_ERR_CUDA;
   if (!weight_grads() || !gemm(false, true, M, C, 2 * H, P, 2 * H, w_in, 2 * H, ws + w.dx, C, false))

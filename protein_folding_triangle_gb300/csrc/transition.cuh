@@ -10,30 +10,10 @@
 namespace triattn {
 namespace {
 
-// act(a) and act'(a).  Each takes one hardware tanh (absolute error about
-// 2^-11, below the BF16 rounding of h): sigmoid(a) = (1 + tanh(a / 2)) / 2.
-template <int ACT>
-__device__ __forceinline__ void act_both(float a, float& f, float& df) {
-  if constexpr (ACT == TRIATTN_ACT_GELU) {
-    const float a2 = a * a;
-    const float t = tanh_approx(a * fmaf(0.0356774081f, a2, 0.7978845608f));
-    const float ht = fmaf(0.5f, t, 0.5f);
-    f = a * ht;
-    df = fmaf(0.5f * a * fmaf(-t, t, 1.f), fmaf(0.1070322243f, a2, 0.7978845608f), ht);
-  } else {
-    const float s = fmaf(0.5f, tanh_approx(0.5f * a), 0.5f);
-    if constexpr (ACT == TRIATTN_ACT_SILU) {
-      f = a * s;
-      df = fmaf(f, 1.f - s, s);
-    } else {
-      f = s;
-      df = s * (1.f - s);
-    }
-  }
-}
-
-// The same for two features at once on packed FP32 pairs, with the product:
-// h = act(a) b.
+// h = act(a) b, two features at once on packed FP32 pairs.  An activation
+// takes one hardware tanh (absolute error about 2^-11, below the BF16 rounding
+// of h; an exponential and a reciprocal would take twice the special-function
+// unit): sigmoid(a) = (1 + tanh(a / 2)) / 2.
 template <int ACT>
 __device__ __forceinline__ float2 gate_fwd2(float2 a, float2 b) {
   const float2 half = make_float2(0.5f, 0.5f);
