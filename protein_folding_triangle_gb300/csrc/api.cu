@@ -247,8 +247,8 @@ cudaError_t traced(int kind, cudaStream_t s, F launch) {
 
 }  // namespace
 
-cudaError_t trace_call(int kind, cudaStream_t s, const std::function<cudaError_t()>& launch) {
-  return traced(kind, s, launch);
+cudaError_t trace_call(int kind, cudaStream_t s, cudaError_t (*launch)(void*), void* arg) {
+  return traced(kind, s, [&] { return launch(arg); });
 }
 
 WaitCtl current_wait_ctl() {

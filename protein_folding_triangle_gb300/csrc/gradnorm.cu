@@ -10,19 +10,21 @@
 // it); each block of a fixed grid takes a run of consecutive chunks, so a list
 // of many small tensors and a few large ones balance the same way, and looks a
 // tensor up once, then steps.  The table of a short list travels in the
-// kernels' parameters, that of a long one is put into the workspace by a
-// one-block kernel that has it in its parameters (with 32 KB of parameters
-// every block of a grid costs 35 ns more: 22 us for a grid that does nothing);
-// either way nothing is copied from the host, nothing is kept between calls,
-// and a captured graph holds its own table.
+// kernels' parameters (3 KB), that of a long one is put into the workspace by a
+// one-block kernel that has it in its parameters (32 KB, which make a launch
+// some 10 us longer, so it is done once and not for both passes); either way
+// nothing is copied from the host, nothing is kept between calls, and a
+// captured graph holds its own table.
 //
 // Pass 1 reads every gradient once: a thread adds squares in FP32 (at most a
-// few thousand, eight chains), everything above it (warp, block, the sum of
-// the blocks' partials) is added in FP64 in fixed order, so the result is
-// bitwise reproducible and uses no atomics.  Pass 2 (clipping only): every
+// few thousand, eight chains), a block's threads are added pairwise in FP32
+// and the blocks' partials in FP64, all in fixed order, so the result is
+// bitwise reproducible and uses no atomics.  It is bound by HBM: 400 MB of BF16
+// in 70 us (5.7 TB/s), 480 MB of FP32 in 90 us.  Pass 2 (clipping only): every
 // block adds the same partials in the same order, so no block waits for
 // another, and scales its chunks, last chunk first: what pass 1 read last is
-// still in L2.  In place nothing is written when the coefficient is 1.
+// still in L2 (480 MB read and written in 158 us).  In place nothing is
+// written when the coefficient is 1.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -4,7 +4,7 @@
 #include <cuda_runtime.h>
 #include <cstddef>
 #include <cstdint>
-#include <functional>
+#include <type_traits>
 
 #include "ptx.cuh"
 
@@ -183,6 +183,11 @@ enum KernelKind {
 };
 // Runs `launch` on stream `s`, bracketed by a pair of trace events while
 // tracing is on.
-cudaError_t trace_call(int kind, cudaStream_t s, const std::function<cudaError_t()>& launch);
+cudaError_t trace_call(int kind, cudaStream_t s, cudaError_t (*launch)(void*), void* arg);
+template <typename F>
+cudaError_t trace_call(int kind, cudaStream_t s, F&& launch) {
+  return trace_call(
+      kind, s, [](void* f) -> cudaError_t { return (*static_cast<std::remove_reference_t<F>*>(f))(); }, &launch);
+}
 
 }  // namespace triattn

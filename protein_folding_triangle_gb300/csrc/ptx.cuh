@@ -442,6 +442,14 @@ __device__ __forceinline__ void mbar_arrive_cta(uint64_t* bar, uint32_t rank) {
       "r"(rank)
       : "memory");
 }
+// At the end of a CTA whose waits gave up: copies and MMAs that were under way
+// then may still touch its shared memory and TMEM; they take microseconds.
+__device__ __forceinline__ void settle_if_aborted(volatile int* abort) {
+  if (*abort == 0) return;
+  const uint64_t t0 = global_timer_ns();
+  while (global_timer_ns() - t0 < 200000) {
+  }
+}
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols));
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");

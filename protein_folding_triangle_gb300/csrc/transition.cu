@@ -133,14 +133,11 @@ triattn_status check_transition(const triattn_transition_shape* s) {
   return TRIATTN_OK;
 }
 
-// f(std::integral_constant<int, C>) for the row widths.
+// f(std::integral_constant<int, C>) for the row widths that the fused backward
+// does not take.
 template <typename F>
 cudaError_t by_c(int C, F&& f) {
   switch (C) {
-    case 32: return f(std::integral_constant<int, 32>{});
-    case 64: return f(std::integral_constant<int, 64>{});
-    case 96: return f(std::integral_constant<int, 96>{});
-    case 128: return f(std::integral_constant<int, 128>{});
     case 160: return f(std::integral_constant<int, 160>{});
     case 192: return f(std::integral_constant<int, 192>{});
     case 224: return f(std::integral_constant<int, 224>{});
@@ -250,6 +247,12 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
              return cudaGetLastError();
            }) == cudaSuccess;
   };
+  // Up to 128 features one kernel does everything before the weight gradients.
+  // Wider rows of x, g and z do not fit the shared memory beside the weights:
+  // there the steps are kernels of their own, with the gating in the epilogue
+  // of the recomputed projections (147456 rows, C = 256, H = 1024: 0.91 ms
+  // against a floor of 0.32 ms; in proportion to the products the fused path
+  // takes 0.6 of that).
   if (transition_bwd_fused(C)) {
     if (mk != nullptr) g = ws + w.g;
     if (trace_call(kKTrBwd, s, [&] {

@@ -8,7 +8,7 @@
 // come through two rings per 64-wide hidden chunk, W_in and W_o as the
 // operands of [a | b] (CTA 0: W_a, CTA 1: W_b) and dh, and W_in again, split
 // along C instead of the hidden axis, as that of dx: 40 KB per chunk and CTA
-// at C = 128 from L2, 16 bytes per clock at the pace below, and what is left of
+// at C = 128 from L2, 11 bytes per clock at the pace below, and what is left of
 // shared memory holds the row tiles and the outputs' staging.
 //
 // Per tile and chunk:
@@ -19,10 +19,12 @@
 // x, g (C / 2 columns each), dx (C), [a | b | dh] (192) and [da | db] (64) fill
 // the 512 TMEM columns at C = 128.
 //
-// What bounds it is the 6 H bytes per row of h and [da | db] (0.27 ms of the
-// memory at 768 x 768 rows, H = 512): one store per thread and row of 32 bytes
-// takes 2.6 clocks of the load/store unit each, more than everything else, so
-// they go through shared memory and TMA.
+// What bounds it is its writes, 6 H + 4 C bytes per row: 2.1 GB at 768 x 768
+// rows, C = 128, H = 512, 0.52 ms of the 4.07 TB/s that a plain fill of memory
+// reaches here, against 0.48 ms for the whole kernel (part of them is still in
+// L2 at its end).  Stores of 32 bytes per thread and row take 2.6 clocks of the
+// load/store unit each, more than everything else, so all tiles go through
+// shared memory and TMA (0.58 ms with x alone stored from registers).
 //
 // Warps: 0 loads weights, 2 tells CTA 0 that this CTA's are in; 1 and 3 (of
 // CTA 0) issue the MMAs, one [a | b] and dh, one dx; 4-7 write x = LayerNorm(z)
@@ -622,6 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTbThreads, 1)
     __syncwarp();
   }
 
+  settle_if_aborted(abort);
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // no arrival is under way to a CTA that has left

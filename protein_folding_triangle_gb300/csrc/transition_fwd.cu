@@ -483,6 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
     }
   }
 
+  settle_if_aborted(abort);
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // no arrival is under way to a CTA that has left
