@@ -162,14 +162,20 @@ cudaError_t launch_transition_fwd(long long M, int C, int H, int act, const void
                                   const WaitCtl& wc, cudaStream_t s);
 // The transition's fused backward up to the weight gradients' operands
 // (transition_bwd.cu): dz, and for every row x [M, C], g = m d_out [M, C]
-// (written only with a mask), h [M, H] and [da | db] [M, 2H], all BF16;
-// *parts (at most kTbPartRows) partial rows of d_ln_w and d_ln_b.
+// (written only with a mask), both BF16; *parts (at most kTbPartRows) partial
+// rows of d_ln_w and d_ln_b.
 constexpr int kTbPartRows = 152 * 4;
 bool transition_bwd_fused(int C);
 cudaError_t launch_transition_bwd(long long M, int C, int H, int act, const void* z, const void* mask,
                                   const float* ln_w, const float* ln_b, const void* w_in, const void* w_o,
-                                  const void* d_out, void* dz, void* x, void* g, void* h, void* dab, float* part_g,
-                                  float* part_b, int* parts, const WaitCtl& wc, cudaStream_t s);
+                                  const void* d_out, void* dz, void* x, void* g, float* part_g, float* part_b,
+                                  int* parts, const WaitCtl& wc, cudaStream_t s);
+// The weight gradients from x and g (transition_wgrad.cu) as *parts FP32
+// partial sums in `part` (transition_wgrad_bytes()), each dW_in [C, 2H] and
+// dW_o [H, C].
+size_t transition_wgrad_bytes(long long M, int C, int H);
+cudaError_t launch_transition_wgrad(long long M, int C, int H, int act, const void* x, const void* g, const void* w_in,
+                                    const void* w_o, float* part, int* parts, const WaitCtl& wc, cudaStream_t s);
 // The bounded-wait control of the current device (status word, time limit).
 WaitCtl current_wait_ctl();
 
@@ -178,7 +184,7 @@ enum KernelKind {
   kKFwd = 0, kKPre, kKTrans, kKMain, kKRedDq, kKRedDb, kKMainAtomic, kKFinDq, kKFinDb, kKCombine, kKFwdPrep,
   kKModLnFwd, kKModLayout, kKModGemm, kKModLnBwd, kKModColSum,
   kKTmLnIn, kKTmProj, kKTmGate, kKTmContract, kKTmLnOut, kKTmOutGate, kKTmColSum, kKGemm, kKTmProjGate,
-  kKTrLn, kKTrFwd, kKTrBwd, kKTrGemm, kKTrGate, kKTrLnBwd, kKTrColSum, kKGradTable, kKGradSum, kKGradScale, kKGradNorm,
+  kKTrLn, kKTrFwd, kKTrBwd, kKTrWgrad, kKTrGemm, kKTrGate, kKTrLnBwd, kKTrColSum, kKGradTable, kKGradSum, kKGradScale, kKGradNorm,
   kKinds
 };
 // Runs `launch` on stream `s`, bracketed by a pair of trace events while

@@ -64,20 +64,49 @@ __global__ void __launch_bounds__(256) mask_rows_kernel(const uint16_t* __restri
   }
 }
 
-// One warp per output column, as column_sum_kernel, the result FP32 or BF16.
-__global__ void __launch_bounds__(256) ln_param_sum_kernel(const float* __restrict__ pg, const float* __restrict__ pb,
-                                                           int rows, int C, int bf16, void* __restrict__ dgamma,
-                                                           void* __restrict__ dbeta) {
-  const int col = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x & 31;
-  if (col >= 2 * C) return;
-  const float* part = col < C ? pg : pb;
-  void* dst = col < C ? dgamma : dbeta;
-  const int c = col < C ? col : col - C;
+// The backward's partial sums in ascending order, the results FP32 or BF16 (one
+// rounding): the first wblocks blocks take those of the weight gradients (n
+// float4 each, dW_in's n_in first), a thread per four elements; the others the
+// rows of d_ln_w's and d_ln_b's, a warp per column.
+struct SumParams {
+  const float4* w;
+  size_t n_in, n;
+  int wparts;
+  unsigned wblocks;
+  const float *pg, *pb;
+  int rows, C, bf16;
+  void *d_w_in, *d_w_o, *d_ln_w, *d_ln_b;
+};
+__global__ void __launch_bounds__(256) transition_sum_kernel(const SumParams p) {
+  if (blockIdx.x < p.wblocks) {
+    const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= p.n) return;
+    float4 s = p.w[i];
+#pragma unroll 8
+    for (int g = 1; g < p.wparts; ++g) {
+      const float4 v = p.w[g * p.n + i];
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    void* const dst = i < p.n_in ? p.d_w_in : p.d_w_o;
+    const size_t at = i < p.n_in ? i : i - p.n_in;
+    if (p.bf16) static_cast<uint2*>(dst)[at] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    else static_cast<float4*>(dst)[at] = s;
+    return;
+  }
+  const int col = static_cast<int>(blockIdx.x - p.wblocks) * 8 + threadIdx.x / 32, lane = threadIdx.x & 31;
+  if (col >= 2 * p.C) return;
+  const float* part = col < p.C ? p.pg : p.pb;
+  void* dst = col < p.C ? p.d_ln_w : p.d_ln_b;
+  const int c = col < p.C ? col : col - p.C;
   float s = 0.f;
-  for (int r = lane; r < rows; r += 32) s += part[static_cast<size_t>(r) * C + c];
+#pragma unroll 8
+  for (int r = lane; r < p.rows; r += 32) s += part[static_cast<size_t>(r) * p.C + c];
   s = warp_sum(s);
   if (lane != 0) return;
-  if (bf16) static_cast<uint16_t*>(dst)[c] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFFu);
+  if (p.bf16) static_cast<uint16_t*>(dst)[c] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFFu);
   else static_cast<float*>(dst)[c] = s;
 }
 
@@ -96,22 +125,23 @@ TrDims tr_dims(const triattn_transition_shape* s) {
 }
 
 struct TrWs {
-  size_t gemm, x, mean, rstd, P, h, g, dh, dx, pg, pb, total;
+  size_t gemm, x, mean, rstd, P, h, g, dh, dx, wg, pg, pb, total;
 };
 TrWs tr_ws(const TrDims& d) {
   TrWs w;
   size_t o = 0;
-  w.gemm = o; o += rup(kGemmWorkspace);
-  w.x = o;    o += rup(d.M * d.C * 2);
+  w.gemm = w.wg = o;
   if (transition_bwd_fused(d.C)) {
-    w.P = o;  o += rup(d.M * d.H * 4);
-    w.h = o;  o += rup(d.M * d.H * 2);
+    w.x = o;  o += rup(d.M * d.C * 2);
     w.g = o;  o += rup(d.M * d.C * 2);
+    w.wg = o; o += rup(transition_wgrad_bytes(static_cast<long long>(d.M), d.C, d.H));
     w.pg = o; o += rup(static_cast<size_t>(kTbPartRows) * d.C * 4);
     w.pb = o; o += rup(static_cast<size_t>(kTbPartRows) * d.C * 4);
-    w.mean = w.rstd = w.dh = w.dx = w.total = o;
+    w.mean = w.rstd = w.P = w.h = w.dh = w.dx = w.total = o;
     return w;
   }
+  o += rup(kGemmWorkspace);
+  w.x = o;    o += rup(d.M * d.C * 2);
   w.mean = o; o += rup(d.M * 4);
   w.rstd = o; o += rup(d.M * 4);
   w.P = o;    o += rup(d.M * d.H * 4);
@@ -232,35 +262,38 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
                   int ldc, bool f32) {
     return gemm_traced(kKTrGemm, gws, s, ta, tb, m, n, k, A, lda, B, ldb, Cp, ldc, f32) == TRIATTN_OK;
   };
+  SumParams sum = {nullptr, 0, 0, 0, 0u, reinterpret_cast<float*>(ws + w.pg), reinterpret_cast<float*>(ws + w.pb),
+                   kLnBlocks, C, d.bf16 ? 1 : 0, d_w_in, d_w_o, d_ln_w, d_ln_b};
   float* pg = reinterpret_cast<float*>(ws + w.pg);
   float* pb = reinterpret_cast<float*>(ws + w.pb);
-  int parts = kLnBlocks;
-  // dW_o = h^T g, dW_in = x^T [da | db], and the sums of the LayerNorm's partial rows
-  auto weight_grads = [&]() -> bool {
-    return gemm(true, false, H, C, M, h, H, g, C, d_w_o, C, !d.bf16) &&
-           gemm(true, false, C, 2 * H, M, ws + w.x, C, P, 2 * H, d_w_in, 2 * H, !d.bf16);
-  };
-  auto ln_grads = [&] {
+  auto sums = [&] {
     return trace_call(kKTrColSum, s, [&] {
-             ln_param_sum_kernel<<<static_cast<unsigned>((2 * C + 7) / 8), 256, 0, s>>>(pg, pb, parts, C,
-                                                                                        d.bf16 ? 1 : 0, d_ln_w, d_ln_b);
+             transition_sum_kernel<<<sum.wblocks + static_cast<unsigned>((2 * C + 7) / 8), 256, 0, s>>>(sum);
              return cudaGetLastError();
            }) == cudaSuccess;
   };
   // Up to 128 features one kernel does everything before the weight gradients.
   // Wider rows of x, g and z do not fit the shared memory beside the weights:
   // there the steps are kernels of their own, with the gating in the epilogue
-  // of the recomputed projections (147456 rows, C = 256, H = 1024: 0.91 ms
-  // against a floor of 0.32 ms; in proportion to the products the fused path
-  // takes 0.6 of that).
+  // of the recomputed projections (147456 rows, C = 256, H = 1024: 0.91 ms,
+  // 2.8 times the floor of its products; the fused path takes 2.2 times its own).
   if (transition_bwd_fused(C)) {
     if (mk != nullptr) g = ws + w.g;
+    float* const part = reinterpret_cast<float*>(ws + w.wg);
     if (trace_call(kKTrBwd, s, [&] {
           return launch_transition_bwd(shape->M, C, H, d.act, z, mask, ln_w, ln_b, w_in, w_o, d_out, dz, ws + w.x,
-                                       ws + w.g, h, P, pg, pb, &parts, current_wait_ctl(), s);
+                                       ws + w.g, pg, pb, &sum.rows, current_wait_ctl(), s);
+        }) != cudaSuccess ||
+        trace_call(kKTrWgrad, s, [&] {
+          return launch_transition_wgrad(shape->M, C, H, d.act, ws + w.x, g, w_in, w_o, part, &sum.wparts,
+                                         current_wait_ctl(), s);
         }) != cudaSuccess)
       return TRIATTN_ERR_CUDA;
-    return weight_grads() && ln_grads() ? TRIATTN_OK : TRIATTN_ERR_CUDA;
+    sum.w = reinterpret_cast<const float4*>(part);
+    sum.n_in = static_cast<size_t>(2) * C * H / 4;
+    sum.n = static_cast<size_t>(3) * C * H / 4;
+    sum.wblocks = static_cast<unsigned>((sum.n + 255) / 256);
+    return sums() ? TRIATTN_OK : TRIATTN_ERR_CUDA;
   }
   if (trace_call(kKTrLn, s, [&] { return ln_fwd_rows(d, z, mask, ln_w, ln_b, ws, w, s); }) != cudaSuccess)
     return TRIATTN_ERR_CUDA;
@@ -278,7 +311,9 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
         return launch_transition_gate(shape->M, C, H, d.act, ws + w.x, w_in, dh, h, P, current_wait_ctl(), s);
       }) != cudaSuccess)
     return TRIATTN_ERR_CUDA;
-  if (!weight_grads() || !gemm(false, true, M, C, 2 * H, P, 2 * H, w_in, 2 * H, ws + w.dx, C, false))
+  if (!gemm(true, false, H, C, M, h, H, g, C, d_w_o, C, !d.bf16) ||
+      !gemm(true, false, C, 2 * H, M, ws + w.x, C, P, 2 * H, d_w_in, 2 * H, !d.bf16) ||
+      !gemm(false, true, M, C, 2 * H, P, 2 * H, w_in, 2 * H, ws + w.dx, C, false))
     return TRIATTN_ERR_CUDA;
   if (trace_call(kKTrLnBwd, s, [&] {
         return by_c(C, [&](auto ic) {
@@ -296,7 +331,7 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
         });
       }) != cudaSuccess)
     return TRIATTN_ERR_CUDA;
-  return ln_grads() ? TRIATTN_OK : TRIATTN_ERR_CUDA;
+  return sums() ? TRIATTN_OK : TRIATTN_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,30 +1,34 @@
 // The transition's backward up to the weight gradients, in one kernel: per
 // row tile it computes x, a and b again, dh = g W_o^T, the activation's
 // backward, dx = [da | db] W_in^T and the LayerNorm's backward, and leaves
-// x, g, h and [da | db] in memory for the weight-gradient GEMMs.
+// x and g in memory for the weight gradients (transition_wgrad.cu).
 //
 // A pair of CTAs (tcgen05 cta_group::2) takes tiles of 256 rows, 128 per CTA;
 // each CTA holds one half of the N columns of every B operand.  The weights
 // come through two rings per 64-wide hidden chunk, W_in and W_o as the
 // operands of [a | b] (CTA 0: W_a, CTA 1: W_b) and dh, and W_in again, split
 // along C instead of the hidden axis, as that of dx: 40 KB per chunk and CTA
-// at C = 128 from L2, 11 bytes per clock at the pace below, and what is left of
-// shared memory holds the row tiles and the outputs' staging.
+// at C = 128 from L2, 15 bytes per clock at the pace below, and what is left of
+// shared memory holds the row tiles.
 //
 // Per tile and chunk:
 //   [a | b] = x [W_a | W_b]    M = 256, N = 128, K = C, A = x in TMEM
 //   dh      = g W_o^T          M = 256, N = 64,  K = C, A = g in TMEM
-//   h = act(a) b, da = dh b act'(a), db = dh act(a)   (registers; BF16 out)
+//   da = dh b act'(a), db = dh act(a)                 (registers)
 //   dx     += [da | db] W_in^T M = 256, N = C, K = 128, A in TMEM
 // x, g (C / 2 columns each), dx (C), [a | b | dh] (192) and [da | db] (64) fill
 // the 512 TMEM columns at C = 128.
 //
-// What bounds it is its writes, 6 H + 4 C bytes per row: 2.1 GB at 768 x 768
-// rows, C = 128, H = 512, 0.52 ms of the 4.07 TB/s that a plain fill of memory
-// reaches here, against 0.48 ms for the whole kernel (part of them is still in
-// L2 at its end).  Stores of 32 bytes per thread and row take 2.6 clocks of the
-// load/store unit each, more than everything else, so all tiles go through
-// shared memory and TMA (0.58 ms with x alone stored from registers).
+// What bounds it is the chain of a chunk: the next [a | b] and dh are computed
+// while the activation runs, but into the columns that it reads (TMEM has no
+// second set), so products and activation overlap by half: 0.355 ms at 768 x 768
+// rows, C = 128, H = 512, against 0.198 ms of products.  Loading a chunk's 96
+// columns at once, to free them sooner, spills (0.41 ms).  Storing h, da and db
+// here for library-shaped weight-gradient products cost 0.125 ms of writes (1.8 GB),
+// and their products, bound by reading them, took 0.342 ms: computing them again
+// (transition_wgrad.cu) takes 0.405 ms, 0.06 ms less in all and no workspace of
+// 6 H bytes per row.  Row tiles leave by TMA: x stored from registers, 32 bytes per
+// row and instruction, took 0.08 ms more.
 //
 // Warps: 0 loads weights, 2 tells CTA 0 that this CTA's are in; 1 and 3 (of
 // CTA 0) issue the MMAs, one [a | b] and dh, one dx; 4-7 write x = LayerNorm(z)
@@ -46,7 +50,6 @@ constexpr int kRegsIssue = 40, kRegsRow = 88, kRegsLn = 144, kRegsAct = 104;
 constexpr int kRegsSum = kRegsIssue + kRegsRow + kRegsLn + 2 * kRegsAct;
 constexpr int kTbMaxSlots = 4;
 constexpr int kTbBarBytes = 1024 + 1024;  // barriers, ln_w and ln_b
-constexpr int kTbStg = 4 * 3 * 4096;      // per 32 rows (a pair of activation warps): h, da, db of 64 features
 constexpr int kTbSmemMax = 232448;
 
 struct TbBars {
@@ -82,7 +85,7 @@ struct TbSmem {
   static constexpr int kWx = (C / 2) * 128;   // ring B: C / 2 rows (N) of 64 hidden columns (K), for a and for b
   static constexpr int kB = 2 * kWx;
   static constexpr int kRows = kKb * 16384;   // a tile of 128 rows
-  static constexpr int bytes(int slots) { return slots * (kA + kB) + 3 * kRows + kTbStg + kTbBarBytes + 1024; }
+  static constexpr int bytes(int slots) { return slots * (kA + kB) + 3 * kRows + kTbBarBytes + 1024; }
 };
 
 // v[j] summed over the 8 threads t mod 4 + 4 q for every j, the thread of
@@ -104,10 +107,8 @@ template <int C, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTbThreads, 1)
     transition_bwd_kernel(const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_do,
                           const __grid_constant__ CUtensorMap tm_dz, const __grid_constant__ CUtensorMap tm_x,
-                          const __grid_constant__ CUtensorMap tm_h,
-                          const __grid_constant__ CUtensorMap tm_dab, const __grid_constant__ CUtensorMap tm_win,
-                          const __grid_constant__ CUtensorMap tm_wo, const __grid_constant__ CUtensorMap tm_wx,
-                          const TbParams p) {
+                          const __grid_constant__ CUtensorMap tm_win, const __grid_constant__ CUtensorMap tm_wo,
+                          const __grid_constant__ CUtensorMap tm_wx, const TbParams p) {
   using L = TbSmem<C>;
   constexpr uint32_t kX = 0, kG = C / 2, kDx = C, kABD = 256, kDAB = 448;  // TMEM columns
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -115,9 +116,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTbThreads, 1)
   uint8_t* const s_b = s_a + p.slots * L::kA;
   uint8_t* const s_z = s_b + p.slots * L::kB;  // two z tiles
   uint8_t* const s_g = s_z + 2 * L::kRows;
-  uint8_t* const s_stg = s_g + L::kRows;
-  TbBars* const bars = reinterpret_cast<TbBars*>(s_stg + kTbStg);
-  float* const s_gam = reinterpret_cast<float*>(s_stg + kTbStg + 1024);
+  TbBars* const bars = reinterpret_cast<TbBars*>(s_g + L::kRows);
+  float* const s_gam = reinterpret_cast<float*>(s_g + L::kRows + 1024);
   float* const s_bet = s_gam + C;
   volatile int* abort = &bars->abort;
   const WaitCtl& wc = p.wc;
@@ -551,26 +551,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTbThreads, 1)
     }
   } else if (warp >= 12) {
     // ------------------------------------------------------------ activation
-    // Warp = 32 rows x 32 of the chunk's 64 hidden features, 16 at a time.  The
-    // two warps of the same rows share a staging buffer, so that a store's
-    // rows are whole 128-byte lines (64-byte rows: see above).
+    // Warp = 32 rows x 32 of the chunk's 64 hidden features, 16 at a time
     regs_inc<kRegsAct>();
     const int hf = (warp - 12) >> 2;
     const uint32_t abd = tmem + lane_addr + kABD + 32 * hf, dab = tmem + lane_addr + kDAB + 16 * hf;
-    uint8_t* const stg = s_stg + quarter * (3 * 4096);
-    bool ok = true;
-    int u = 0, i = 0;
-    for (long long g = 0; g < total; ++g) {  // no warp leaves the loop early: pairs meet at their barrier
-      const long long row0 = tile_row(u) + quarter * 32;  // the warp's first row
-      // the chunk before's stores have read the staging buffer
-      if (hf == 0 && lane == 0) bulk_wait_read();
-      __syncwarp();
-      named_bar_sync(3 + quarter, 64);
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->abd_full, static_cast<uint32_t>(g) & 1, wc, abort));
+    for (long long g = 0; g < total; ++g) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->abd_full, static_cast<uint32_t>(g) & 1, wc, abort))) break;
       tc_fence_after();
+      bool ok = true;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        uint32_t a[16], b[16], d[16], h[8];
+        uint32_t a[16], b[16], d[16];
         tmem_ld16x3_wait(abd + 16 * j, a, abd + 64 + 16 * j, b, abd + 128 + 16 * j, d);
         if (j == 1) {
           tc_fence_before();
@@ -584,44 +575,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTbThreads, 1)
           gate_bwd2<ACT>(make_float2(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1])),
                          make_float2(__uint_as_float(b[2 * e]), __uint_as_float(b[2 * e + 1])),
                          make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])), hv, av, bv);
-          h[e] = pack_bf16x2(hv.x, hv.y);
           da[e] = pack_bf16x2(av.x, av.y);
           db[e] = pack_bf16x2(bv.x, bv.y);
         }
-        if (j == 0) {
-          // the previous chunk's dx has read [da | db]
-          if (g > 0)
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->dab_free, static_cast<uint32_t>(g - 1) & 1, wc, abort));
+        if (j == 0 && g > 0) {  // the previous chunk's dx has read [da | db]
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->dab_free, static_cast<uint32_t>(g - 1) & 1, wc, abort));
           tc_fence_after();
         }
         tmem_st8(dab + 8 * j, da);
         tmem_st8(dab + 32 + 8 * j, db);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint8_t* const at = stg + sw128(lane, 4 * hf + 2 * j + k);
-          *reinterpret_cast<uint4*>(at) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
-          *reinterpret_cast<uint4*>(at + 4096) = make_uint4(da[4 * k], da[4 * k + 1], da[4 * k + 2], da[4 * k + 3]);
-          *reinterpret_cast<uint4*>(at + 8192) = make_uint4(db[4 * k], db[4 * k + 1], db[4 * k + 2], db[4 * k + 3]);
-        }
       }
       tc_wait_st();
+      if (!ok) break;
       tc_fence_before();
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(&bars->dab_full, 0);
-      named_bar_sync(3 + quarter, 64);
-      if (hf == 0 && lane == 0 && ok && row0 < p.M) {
-        tma_store_3d(&tm_h, stg, 64 * i, static_cast<int>(row0), 0);
-        tma_store_3d(&tm_dab, stg + 4096, 64 * i, 0, static_cast<int>(row0));
-        tma_store_3d(&tm_dab, stg + 8192, 64 * i, 1, static_cast<int>(row0));
-      }
-      if (++i == p.chunks) {
-        i = 0;
-        ++u;
-      }
     }
-    if (lane == 0) bulk_wait_all();
-    __syncwarp();
   }
 
   settle_if_aborted(abort);
@@ -643,7 +612,7 @@ int tb_slots() {
 }
 
 struct TbMaps {
-  CUtensorMap z, dout, dz, x, h, dab, win, wo, wx;
+  CUtensorMap z, dout, dz, x, win, wo, wx;
 };
 
 template <int C, int ACT>
@@ -657,8 +626,7 @@ cudaError_t tb_launch(const TbMaps& m, TbParams p, int grid, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // a split above the launch's registers would wait for ever
   if (at.numRegs * (kTbThreads / 128) < kRegsSum) return cudaErrorInvalidConfiguration;
-  transition_bwd_kernel<C, ACT><<<grid, kTbThreads, bytes, s>>>(m.z, m.dout, m.dz, m.x, m.h, m.dab, m.win, m.wo,
-                                                                         m.wx, p);
+  transition_bwd_kernel<C, ACT><<<grid, kTbThreads, bytes, s>>>(m.z, m.dout, m.dz, m.x, m.win, m.wo, m.wx, p);
   return cudaGetLastError();
 }
 
@@ -668,17 +636,15 @@ bool transition_bwd_fused(int C) { return C <= 128; }
 
 cudaError_t launch_transition_bwd(long long M, int C, int H, int act, const void* z, const void* mask,
                                   const float* ln_w, const float* ln_b, const void* w_in, const void* w_o,
-                                  const void* d_out, void* dz, void* x, void* g, void* h, void* dab, float* part_g,
-                                  float* part_b, int* parts, const WaitCtl& wc, cudaStream_t s) {
+                                  const void* d_out, void* dz, void* x, void* g, float* part_g, float* part_b,
+                                  int* parts, const WaitCtl& wc, cudaStream_t s) {
   TbMaps m;
   const cuuint64_t c = static_cast<cuuint64_t>(C), hh = static_cast<cuuint64_t>(H), mm = static_cast<cuuint64_t>(M);
   const cuuint64_t zd[3] = {c, mm, 1}, zs[2] = {2 * c, 2 * c * mm};
-  const cuuint64_t hd[3] = {hh, mm, 1}, hs[2] = {2 * hh, 2 * hh * mm};
-  const cuuint64_t ad[3] = {hh, 2, mm}, as[2] = {2 * hh, 4 * hh};  // the a and b columns apart: past H is left out
   const cuuint64_t wd[3] = {hh, 2, c}, ws[2] = {2 * hh, 4 * hh};  // the a and b columns apart: past H reads 0
   const cuuint64_t od[3] = {c, hh, 1}, os[2] = {2 * c, 2 * c * hh};
   if (!tf_map(&m.z, z, zd, zs, 128, 1) || !tf_map(&m.dout, d_out, zd, zs, 128, 1) ||
-      !tf_map(&m.dz, dz, zd, zs, 128, 1) || !tf_map(&m.x, x, zd, zs, 128, 1) || !tf_map(&m.h, h, hd, hs, 32, 1) || !tf_map(&m.dab, dab, ad, as, 1, 32) ||
+      !tf_map(&m.dz, dz, zd, zs, 128, 1) || !tf_map(&m.x, x, zd, zs, 128, 1) ||
       !tf_map(&m.win, w_in, wd, ws, 1, static_cast<cuuint32_t>(C)) || !tf_map(&m.wo, w_o, od, os, 32, 1) ||
       !tf_map(&m.wx, w_in, wd, ws, 1, static_cast<cuuint32_t>(C / 2)))
     return cudaErrorInvalidValue;
