@@ -64,10 +64,13 @@ __global__ void __launch_bounds__(256) mask_rows_kernel(const uint16_t* __restri
   }
 }
 
-// The backward's partial sums in ascending order, the results FP32 or BF16 (one
+// The backward's partial sums in a fixed order, the results FP32 or BF16 (one
 // rounding): the first wblocks blocks take those of the weight gradients (n
-// float4 each, dW_in's n_in first), a thread per four elements; the others the
-// rows of d_ln_w's and d_ln_b's, a warp per column.
+// float4 each, dW_in's n_in first), four threads per four elements, each a
+// quarter of the parts; the others the rows of d_ln_w's and d_ln_b's, eight
+// columns each.  A thread has its loads under way at once: what the launch
+// takes is their latency.
+constexpr int kSumRows = kTbPartRows / 32, kSumParts = 10;
 struct SumParams {
   const float4* w;
   size_t n_in, n;
@@ -79,33 +82,58 @@ struct SumParams {
 };
 __global__ void __launch_bounds__(256) transition_sum_kernel(const SumParams p) {
   if (blockIdx.x < p.wblocks) {
-    const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= p.n) return;
-    float4 s = p.w[i];
-#pragma unroll 8
-    for (int g = 1; g < p.wparts; ++g) {
-      const float4 v = p.w[g * p.n + i];
+    __shared__ float4 quarter[3][64];
+    const int q = threadIdx.x / 64, per = (p.wparts + 3) / 4;
+    const size_t i = static_cast<size_t>(blockIdx.x) * 64 + threadIdx.x % 64;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4 v) {
       s.x += v.x;
       s.y += v.y;
       s.z += v.z;
       s.w += v.w;
+    };
+    if (i < p.n) {
+      const int end = min((q + 1) * per, p.wparts);
+      for (int g = q * per; g < end; g += kSumParts) {
+        float4 v[kSumParts];
+#pragma unroll
+        for (int k = 0; k < kSumParts; ++k)
+          v[k] = g + k < end ? p.w[(g + k) * p.n + i] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kSumParts; ++k) add(v[k]);
+      }
     }
+    if (q > 0) quarter[q - 1][threadIdx.x % 64] = s;
+    __syncthreads();
+    if (q > 0 || i >= p.n) return;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) add(quarter[k][threadIdx.x]);
     void* const dst = i < p.n_in ? p.d_w_in : p.d_w_o;
     const size_t at = i < p.n_in ? i : i - p.n_in;
     if (p.bf16) static_cast<uint2*>(dst)[at] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
     else static_cast<float4*>(dst)[at] = s;
     return;
   }
-  const int col = static_cast<int>(blockIdx.x - p.wblocks) * 8 + threadIdx.x / 32, lane = threadIdx.x & 31;
-  if (col >= 2 * p.C) return;
-  const float* part = col < p.C ? p.pg : p.pb;
-  void* dst = col < p.C ? p.d_ln_w : p.d_ln_b;
-  const int c = col < p.C ? col : col - p.C;
+  __shared__ float row[32][8];
+  const int k8 = threadIdx.x & 7, rg = threadIdx.x >> 3;
+  const int c0 = static_cast<int>(blockIdx.x - p.wblocks) * 8;  // of the 2 C columns
+  const float* part = c0 < p.C ? p.pg : p.pb;
+  void* dst = c0 < p.C ? p.d_ln_w : p.d_ln_b;
+  const int c = (c0 < p.C ? c0 : c0 - p.C) + k8;
   float s = 0.f;
-#pragma unroll 8
-  for (int r = lane; r < p.rows; r += 32) s += part[static_cast<size_t>(r) * p.C + c];
-  s = warp_sum(s);
-  if (lane != 0) return;
+  for (int r0 = rg; r0 < p.rows; r0 += 32 * kSumRows) {
+    float v[kSumRows];
+#pragma unroll
+    for (int k = 0; k < kSumRows; ++k)
+      v[k] = r0 + 32 * k < p.rows ? part[static_cast<size_t>(r0 + 32 * k) * p.C + c] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kSumRows; ++k) s += v[k];
+  }
+  row[rg][k8] = s;
+  __syncthreads();
+  if (rg > 0) return;
+#pragma unroll
+  for (int k = 1; k < 32; ++k) s += row[k][k8];
   if (p.bf16) static_cast<uint16_t*>(dst)[c] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFFu);
   else static_cast<float*>(dst)[c] = s;
 }
@@ -268,7 +296,7 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
   float* pb = reinterpret_cast<float*>(ws + w.pb);
   auto sums = [&] {
     return trace_call(kKTrColSum, s, [&] {
-             transition_sum_kernel<<<sum.wblocks + static_cast<unsigned>((2 * C + 7) / 8), 256, 0, s>>>(sum);
+             transition_sum_kernel<<<sum.wblocks + static_cast<unsigned>(2 * C / 8), 256, 0, s>>>(sum);
              return cudaGetLastError();
            }) == cudaSuccess;
   };
@@ -292,7 +320,7 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
     sum.w = reinterpret_cast<const float4*>(part);
     sum.n_in = static_cast<size_t>(2) * C * H / 4;
     sum.n = static_cast<size_t>(3) * C * H / 4;
-    sum.wblocks = static_cast<unsigned>((sum.n + 255) / 256);
+    sum.wblocks = static_cast<unsigned>((sum.n + 63) / 64);
     return sums() ? TRIATTN_OK : TRIATTN_ERR_CUDA;
   }
   if (trace_call(kKTrLn, s, [&] { return ln_fwd_rows(d, z, mask, ln_w, ln_b, ws, w, s); }) != cudaSuccess)

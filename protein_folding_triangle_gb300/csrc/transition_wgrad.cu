@@ -16,13 +16,14 @@
 // The same shared-memory tiles of x and g are the row-major A operand of the
 // first two and the feature-major one of the last two.  The groups of CTAs
 // that share the rows out leave one FP32 partial of the gradients each, added
-// in ascending order by transition_sum_kernel (transition.cu).  TMEM:
-// [a | b | dh] 192 columns, the gradients 192.
+// in a fixed order by transition_sum_kernel (transition.cu).  TMEM: [a | b | dh]
+// 192 columns, the gradients 192.
 //
-// What bounds it is the pace of MMAs with both operands in shared memory, about
-// 95 clocks each where the tensor pipe alone takes 64: 0.405 ms at 768 x 768 rows,
-// C = 128, H = 512 (0.24 ms of products; the same chain without MMAs 0.27 ms;
-// without its loads, or with the row tiles brought to L2 ahead, no less).
+// What bounds it is shared memory: per row tile and slice the MMAs read 208 KB of
+// operands, the loads write 64 KB and the activation 48 KB.  0.403 ms at 768 x 768
+// rows, C = 128, H = 512, 100 bytes per clock, the tensor pipe active for 48 % of
+// it (0.24 ms of products); without the activation 0.397 ms, without that and the
+// loads 0.326 ms.  Row tiles brought to L2 ahead change nothing.
 // With C <= 64 x and g share the A operand of the gradients and four stages
 // fit: 0.098 ms at 640 x 640 rows, C = 64, H = 256 (0.143 ms without both).
 // Eight activation warps instead of sixteen: 0.43 ms.

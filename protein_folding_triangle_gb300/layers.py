@@ -16,6 +16,12 @@ parameter's dtype (BF16 projection matrices, FP32 LayerNorm parameters).
   the update; its forward keeps only its inputs for the backward.
 - ``clip_grad_norm_``: clips the gradients of a model's parameters by their
   global norm, in place.
+
+Forward and backward may be captured into a CUDA graph.  Before a backward is
+captured, drop what holds an eager autograd graph of the same parameters (a
+loss that is still referenced, say): torch ties the accumulation of a leaf to
+the stream of the graph that used it first, and a capture that reaches another
+stream fails.
 """
 from __future__ import annotations
 
@@ -149,6 +155,7 @@ def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0) -> torc
     """Scale the gradients of ``parameters`` (BF16 and FP32) in place so that
     their global norm (2 or inf) is at most ``max_norm``.  Parameters without a
     gradient are skipped.  Returns the norm before clipping (0-dim FP32 on the
-    gradients' device; nothing waits for it)."""
+    gradients' device; nothing waits for it).  Captured into a graph, it keeps
+    the gradients' addresses: zero them between replays, do not free them."""
     parameters = [parameters] if isinstance(parameters, torch.Tensor) else parameters
     return T.triattn_clip_grad_norm([p.grad for p in parameters if p.grad is not None], max_norm, norm_type)

@@ -660,6 +660,8 @@ def _on_stream(device, stream):
         if torch.cuda.current_device() == device.index:
             return _HERE, _raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, expected {device}")
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
@@ -821,9 +823,10 @@ def triattn_grad_norm(tensors, norm_type: float = 2.0, *, stream=None):
 def triattn_clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, *, out=None, stream=None):
     """Scale ``tensors`` (BF16 and FP32 CUDA tensors, mixed) by
     min(1, max_norm / (norm + 1e-6)), in place, or into ``out`` (a list of
-    tensors of the same dtypes and sizes, in the same memory order).  Returns the norm before
-    clipping as a 0-dim FP32 tensor; nothing waits for the device.  A tensor
-    may not be listed twice."""
+    tensors of the same dtypes and sizes, in the same memory order, that share
+    no memory with ``tensors``).  Returns the norm before clipping as a 0-dim
+    FP32 tensor; nothing waits for the device.  A tensor may not be listed
+    twice.  A captured call keeps the tensors' addresses."""
     tensors, kind, device = _grad_call(tensors, norm_type)
     n = len(tensors)
     table, plain = _tensor_table(tensors, "tensors", device)

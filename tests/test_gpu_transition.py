@@ -160,6 +160,31 @@ def test_rows_without_spread():
         assert rel_rmse(cpu64(out[r]), TR.run(*params(x))["out"][r]) <= 4 * TOL_OUT, r
 
 
+@pytest.mark.parametrize("C,H", [(128, 512), (96, 64), (256, 64)])
+def test_rows_far_from_zero(C, H):
+    """Rows with a common offset of many standard deviations, and rows whose
+    first features lie far from the others.  z is what the oracle has too, so
+    only the FP32 statistics differ: the mean of C values within 2^12 standard
+    deviations is off by at most log2(C) + 2 half steps of 2^12, 10 * 2^-12 =
+    2.5e-3 standard deviations, that of the other rows by far less; both add
+    in quadrature to the tolerance of an ordinary row."""
+    x = S.make_transition_inputs((640,), C, H, seed=16)
+    z = x["z"].float()
+    z[0:128] += 8.0
+    z[128:256] -= 40.0
+    z[256:384, :8] += 300.0  # the features that the one-pass statistics start from
+    z[384:512, -8:] -= 300.0
+    z[512:576] = 4096.0 + 32.0 * (z[512:576] > 0)  # two values, a step of BF16 apart
+    z[576:640] *= 1e-3
+    x["z"] = z.to(torch.bfloat16)
+    ref = run_oracle(x)
+    got = run_gpu(x)
+    for i in range(0, 640, 64):
+        r = slice(i, i + 64)
+        assert rel_rmse(cpu64(got[0][r]), ref[0][r]) <= (TOL_OUT**2 + 2.5e-3**2) ** 0.5, i
+        assert rel_rmse(cpu64(got[1][r]), ref[1][r]) <= (TOL_GRADS**2 + 2.5e-3**2) ** 0.5, i
+
+
 def test_no_rows():
     x = S.make_transition_inputs((0,), 64, 128, seed=1)
     got = run_gpu(x)

@@ -56,6 +56,15 @@ def test_transition_shapes(lib):
         T.transition_shape(1, 64, 64, "tanh")
 
 
+def test_stream_of_another_device():
+    class Stream:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        T._on_stream(torch.device("cuda", 0), Stream())
+
+
 def test_transition_pointers_and_workspace(lib):
     s = T.TransitionShape(10, 64, 64, 0, 0)
     nb = T.transition_workspace_bytes(10, 64, 64)
