@@ -205,7 +205,7 @@ const char* const kKernelName[kKinds] = {"tri_attn_fwd",     "bwd_preprocess",  
                                          "trimul_ln_in",     "trimul_proj_gemm", "trimul_gate",
                                          "trimul_contract_gemm", "trimul_ln_out", "trimul_out_gate",
                                          "trimul_colsum",   "gemm",            "trimul_proj_gate",
-                                         "transition_ln",   "transition_fwd",  "transition_bwd", "transition_wgrad",
+                                         "transition_ln",   "transition_fwd",  "transition_rows", "transition_bwd", "transition_wgrad",
                                          "transition_gemm", "transition_gate",
                                          "transition_ln_bwd", "transition_colsum", "grad_table", "grad_sum",
                                          "grad_scale",      "grad_norm"};

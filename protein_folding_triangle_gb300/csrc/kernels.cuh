@@ -160,6 +160,14 @@ cudaError_t launch_transition_gate(long long M, int C, int H, int act, const voi
 cudaError_t launch_transition_fwd(long long M, int C, int H, int act, const void* z, const void* mask,
                                   const float* ln_w, const float* ln_b, const void* w_in, const void* w_o, void* out,
                                   const WaitCtl& wc, cudaStream_t s);
+// The same for at most kTrRowsMax rows (transition_rows.cu): up to there all
+// clusters of four rows run in three waves at most, and it is the faster of the
+// two for every width (us at C / H, 192 and 256 rows, against a tile of 256 rows:
+// 128 / 512 9.6 and 14.9, 12.6; 64 / 256 6.8 and 11.0, 7.9; 256 / 1024 21.3 and
+// 31.5, 32.4; 128 / 4096 36.6 and 51.3, 40.3).
+constexpr int kTrRowsMax = 192;
+cudaError_t launch_transition_rows(int M, int C, int H, int act, const void* z, const void* mask, const float* ln_w,
+                                   const float* ln_b, const void* w_in, const void* w_o, void* out, cudaStream_t s);
 // The transition's fused backward up to the weight gradients' operands
 // (transition_bwd.cu): dz, and for every row x [M, C], g = m d_out [M, C]
 // (written only with a mask), both BF16; *parts (at most kTbPartRows) partial
@@ -184,7 +192,7 @@ enum KernelKind {
   kKFwd = 0, kKPre, kKTrans, kKMain, kKRedDq, kKRedDb, kKMainAtomic, kKFinDq, kKFinDb, kKCombine, kKFwdPrep,
   kKModLnFwd, kKModLayout, kKModGemm, kKModLnBwd, kKModColSum,
   kKTmLnIn, kKTmProj, kKTmGate, kKTmContract, kKTmLnOut, kKTmOutGate, kKTmColSum, kKGemm, kKTmProjGate,
-  kKTrLn, kKTrFwd, kKTrBwd, kKTrWgrad, kKTrGemm, kKTrGate, kKTrLnBwd, kKTrColSum, kKGradTable, kKGradSum, kKGradScale, kKGradNorm,
+  kKTrLn, kKTrFwd, kKTrRows, kKTrBwd, kKTrWgrad, kKTrGemm, kKTrGate, kKTrLnBwd, kKTrColSum, kKGradTable, kKGradSum, kKGradScale, kKGradNorm,
   kKinds
 };
 // Runs `launch` on stream `s`, bracketed by a pair of trace events while

@@ -442,6 +442,16 @@ __device__ __forceinline__ void mbar_arrive_cta(uint64_t* bar, uint32_t rank) {
       "r"(rank)
       : "memory");
 }
+// Two floats at the same shared-memory offset in CTA `rank`.
+__device__ __forceinline__ float2 ld_cluster_f32x2(const float* p, uint32_t rank) {
+  float2 v;
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %2, %3;\n ld.shared::cluster.v2.f32 {%0, %1}, [a];\n}\n"
+      : "=f"(v.x), "=f"(v.y)
+      : "r"(smem_u32(p)), "r"(rank)
+      : "memory");
+  return v;
+}
 // At the end of a CTA whose waits gave up: copies and MMAs that were under way
 // then may still touch its shared memory and TMEM; they take microseconds.
 __device__ __forceinline__ void settle_if_aborted(volatile int* abort) {

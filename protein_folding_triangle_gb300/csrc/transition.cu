@@ -245,6 +245,13 @@ triattn_status triattn_transition_fwd(const triattn_transition_shape* shape, con
   if (mask != nullptr && !al2(mask)) return TRIATTN_ERR_INVALID_ARG;
   const TrDims d = tr_dims(shape);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (shape->M <= kTrRowsMax) {
+    const cudaError_t e = trace_call(kKTrRows, s, [&] {
+      return launch_transition_rows(static_cast<int>(shape->M), d.C, d.H, d.act, z, mask, ln_w, ln_b, w_in, w_o, out,
+                                    s);
+    });
+    return e == cudaSuccess ? TRIATTN_OK : TRIATTN_ERR_CUDA;
+  }
   const cudaError_t e = trace_call(kKTrFwd, s, [&] {
     return launch_transition_fwd(shape->M, d.C, d.H, d.act, z, mask, ln_w, ln_b, w_in, w_o, out, current_wait_ctl(),
                                  s);

@@ -683,19 +683,29 @@ def transition_workspace_bytes(rows: int, C: int, H: int) -> int:
     return int(load().triattn_transition_workspace_bytes(ctypes.byref(s)))
 
 
+def _fits(t, device: int, shape, dtype) -> bool:
+    return t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous()
+
+
 def _transition_check(z, mask, ln_w, ln_b, w_in, w_o):
     if z.dim() < 1 or w_o.dim() != 2:
         raise ValueError("z must be [..., C] and w_o [H, C]")
-    C, H = z.shape[-1], w_o.shape[0]
-    _check(z, "z", z.shape)
-    _check(ln_w, "ln_w", (C,), torch.float32)
-    _check(ln_b, "ln_b", (C,), torch.float32)
-    _check(w_in, "w_in", (C, 2 * H))
-    _check(w_o, "w_o", (H, C))
-    if mask is not None:
-        _check(mask, "mask", z.shape[:-1])
-    _same_device(z.device, mask=mask, ln_w=ln_w, ln_b=ln_b, w_in=w_in, w_o=w_o)
-    return z.numel() // C if C else 0, C, H
+    lead, C, H = z.shape[:-1], z.shape[-1], w_o.shape[0]
+    # one look at every tensor, what is wrong is found out below: a call on a few
+    # rows takes the GPU 5 us, so the host's 12 are what counts there
+    dev, bf16, f32 = z.get_device(), torch.bfloat16, torch.float32
+    if not (dev >= 0 and z.dtype is bf16 and z.is_contiguous() and _fits(ln_w, dev, (C,), f32)
+            and _fits(ln_b, dev, (C,), f32) and _fits(w_in, dev, (C, 2 * H), bf16) and _fits(w_o, dev, (H, C), bf16)
+            and (mask is None or _fits(mask, dev, lead, bf16))):
+        _check(z, "z", z.shape)
+        _check(ln_w, "ln_w", (C,), torch.float32)
+        _check(ln_b, "ln_b", (C,), torch.float32)
+        _check(w_in, "w_in", (C, 2 * H))
+        _check(w_o, "w_o", (H, C))
+        if mask is not None:
+            _check(mask, "mask", lead)
+        _same_device(z.device, mask=mask, ln_w=ln_w, ln_b=ln_b, w_in=w_in, w_o=w_o)
+    return lead.numel(), C, H
 
 
 def triattn_transition_fwd(z, mask, ln_w, ln_b, w_in, w_o, activation: str = "silu", *, out=None, stream=None):

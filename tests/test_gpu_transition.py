@@ -92,6 +92,9 @@ CASES = [
     ((515,), 192, 352, 0.2),
     ((300,), 224, 896, 0.0),
     ((1031,), 256, 1024, 0.1),
+    ((193,), 128, 512, 0.2),
+    ((255,), 64, 96, 0.0),
+    ((256,), 256, 512, 0.2),
     ((5000,), 128, 160, 0.0),
     ((70, 257), 128, 480, 0.1),
 ]
@@ -183,6 +186,29 @@ def test_rows_far_from_zero(C, H):
         r = slice(i, i + 64)
         assert rel_rmse(cpu64(got[0][r]), ref[0][r]) <= (TOL_OUT**2 + 2.5e-3**2) ** 0.5, i
         assert rel_rmse(cpu64(got[1][r]), ref[1][r]) <= (TOL_GRADS**2 + 2.5e-3**2) ** 0.5, i
+
+
+@pytest.mark.parametrize("kind", TR.ACTIVATIONS)
+@pytest.mark.parametrize("C,H", [(32, 32), (64, 4096), (96, 288), (128, 512), (160, 64), (192, 352), (224, 96), (256, 1024)])
+@pytest.mark.parametrize("M", [1, 2, 5, 48, 191, 192])
+def test_forward_of_a_few_rows(C, H, M, kind):
+    """Few rows are computed in FP32 and rounded once: an element is off by at
+    most half a step of BF16, 2^-8 of its value, and by the FP32 sums' errors, at
+    most about (C + H) 2^-24 = 2.6e-4 of the root sum of squares of the terms,
+    which is the size of the value itself for these inputs.  Masked rows hold
+    NaN."""
+    x = S.make_transition_inputs((M,), C, H, seed=C + H + M, drop=0.3 if M > 2 else 0.0)
+    ref = TR.run(*params(x), x["d_out"], kind)["out"]
+    if x["mask"] is not None:
+        x["z"][x["mask"] == 0] = float("nan")
+    d = to_dev(x)
+    out = T.triattn_transition_fwd(*params(d), kind)
+    assert rel_rmse(cpu64(out), ref) <= 2.0**-8 + 3e-4
+    if x["mask"] is not None:
+        assert torch.count_nonzero(out[d["mask"] == 0]) == 0
+    again = torch.full((M + 2, C), 7.0, dtype=torch.bfloat16, device="cuda")
+    T.triattn_transition_fwd(*params(d), kind, out=again[1:M + 1])
+    assert torch.equal(again[1:M + 1], out) and bool((again[0] == 7.0).all()) and bool((again[M + 1] == 7.0).all())
 
 
 def test_no_rows():
