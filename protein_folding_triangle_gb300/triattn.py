@@ -11,10 +11,10 @@ from __future__ import annotations
 import ctypes
 import operator
 import os
+import struct
 import threading
 from typing import Optional
 
-import numpy as np
 import torch
 
 from . import build as _build
@@ -768,7 +768,6 @@ def triattn_transition_bwd(z, mask, ln_w, ln_b, w_in, w_o, d_out, activation: st
 
 GRAD_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 _dtype_of = operator.attrgetter("dtype")
-_TENSOR = np.dtype([("data", np.uint64), ("numel", np.int64), ("dtype", np.int32)], align=True)  # Tensor
 
 
 def _dense(t) -> bool:
@@ -783,17 +782,21 @@ def _dense(t) -> bool:
 
 
 def _tensor_table(tensors, name, device):
-    """The triattn_tensor array of a list, column by column: a model has
-    thousands of gradients, and the host's time per tensor is what counts."""
+    """The triattn_tensor array of a list as bytes (address, elements and dtype,
+    eight each), its elements and dtypes, and whether all are contiguous.
+    Column by column: a model has thousands of gradients, and the host's time
+    per tensor is what counts."""
     n = len(tensors)
-    table = np.empty(n, dtype=_TENSOR)
     try:
-        table["data"] = np.fromiter(map(torch.Tensor.data_ptr, tensors), np.uint64, n)
-        table["numel"] = np.fromiter(map(torch.Tensor.numel, tensors), np.int64, n)
-        table["dtype"] = np.fromiter(map(GRAD_DTYPES.__getitem__, map(_dtype_of, tensors)), np.int32, n)
+        numel = list(map(torch.Tensor.numel, tensors))
+        kinds = list(map(GRAD_DTYPES.__getitem__, map(_dtype_of, tensors)))
+        rows = [0] * (3 * n)
+        rows[0::3], rows[1::3], rows[2::3] = map(torch.Tensor.data_ptr, tensors), numel, kinds
+        table = struct.pack(f"{3 * n}q", *rows)
         plain = (all(map(torch.Tensor.is_contiguous, tensors))
                  and set(map(torch.Tensor.get_device, tensors)) <= {device.index})
     except (KeyError, RuntimeError):
+        table = numel = kinds = None
         plain = False
     if not plain:
         for i, t in enumerate(tensors):
@@ -801,7 +804,9 @@ def _tensor_table(tensors, name, device):
                 raise ValueError(f"{name}[{i}] must be a strided bfloat16 or float32 tensor on {device}")
             if not t.is_contiguous() and t.numel() and not _dense(t):
                 raise ValueError(f"{name}[{i}] must fill one block of memory")
-    return table, plain
+        if table is None:
+            raise ValueError(f"{name} holds a tensor without an address")
+    return table, numel, kinds, plain
 
 
 def _grad_call(tensors, norm_type):
@@ -820,12 +825,13 @@ def triattn_grad_norm(tensors, norm_type: float = 2.0, *, stream=None):
     2 or inf.  Returns a 0-dim FP32 tensor; nothing waits for the device."""
     tensors, kind, device = _grad_call(tensors, norm_type)
     n = len(tensors)
-    table, _ = _tensor_table(tensors, "tensors", device)
+    table, _, _, _ = _tensor_table(tensors, "tensors", device)
     here, sp = _on_stream(device, stream)
+    lib = load()
     with here:
         norm = torch.empty((), dtype=torch.float32, device=device)
-        ws = torch.empty(max(int(load().triattn_grad_norm_workspace_bytes(n)), 16), dtype=torch.uint8, device=device)
-        code = load().triattn_grad_norm(ctypes.c_void_p(table.ctypes.data), n, kind, _ptr(norm), _ptr(ws), _bytes(ws), sp)
+        ws = torch.empty(lib.triattn_grad_norm_workspace_bytes(n), dtype=torch.uint8, device=device)
+        code = lib.triattn_grad_norm(table, n, kind, norm.data_ptr(), ws.data_ptr(), ws.numel(), sp)
     _raise(code, "triattn_grad_norm")
     return norm
 
@@ -839,25 +845,25 @@ def triattn_clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, *, 
     twice.  A captured call keeps the tensors' addresses."""
     tensors, kind, device = _grad_call(tensors, norm_type)
     n = len(tensors)
-    table, plain = _tensor_table(tensors, "tensors", device)
+    table, numel, kinds, plain = _tensor_table(tensors, "tensors", device)
     into = None
     if out is not None:
         out = [out] if isinstance(out, torch.Tensor) else list(out)
         if len(out) != n:
             raise ValueError(f"out has {len(out)} tensors, expected {n}")
-        into, plain_out = _tensor_table(out, "out", device)
-        same = (table["numel"] == into["numel"]) & (table["dtype"] == into["dtype"])
-        if not (plain and plain_out):
-            same &= [a.shape == b.shape and a.stride() == b.stride() for a, b in zip(tensors, out)]
-        if not same.all():
-            raise ValueError(f"out[{int(same.argmin())}] does not match tensors[{int(same.argmin())}]")
+        into, numel_out, kinds_out, plain_out = _tensor_table(out, "out", device)
+        if not (numel == numel_out and kinds == kinds_out and plain and plain_out):
+            for i, (a, b) in enumerate(zip(tensors, out)):
+                if (a.numel() != b.numel() or a.dtype != b.dtype
+                        or not (plain and plain_out) and (a.shape != b.shape or a.stride() != b.stride())):
+                    raise ValueError(f"out[{i}] does not match tensors[{i}]")
     here, sp = _on_stream(device, stream)
+    lib = load()
     with here:
         norm = torch.empty((), dtype=torch.float32, device=device)
-        ws = torch.empty(max(int(load().triattn_grad_norm_workspace_bytes(n)), 16), dtype=torch.uint8, device=device)
-        code = load().triattn_clip_grad_norm(ctypes.c_void_p(table.ctypes.data),
-                                             None if into is None else ctypes.c_void_p(into.ctypes.data), n, kind,
-                                             float(max_norm), _ptr(norm), _ptr(ws), _bytes(ws), sp)
+        ws = torch.empty(lib.triattn_grad_norm_workspace_bytes(n), dtype=torch.uint8, device=device)
+        code = lib.triattn_clip_grad_norm(table, into, n, kind, float(max_norm), norm.data_ptr(), ws.data_ptr(),
+                                          ws.numel(), sp)
     _raise(code, "triattn_clip_grad_norm")
     return norm
 
