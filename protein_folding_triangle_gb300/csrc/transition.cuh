@@ -95,6 +95,20 @@ __device__ __forceinline__ float2 row_stats(F&& z16) {
   return make_float2(k + ds, rsqrtf(fmaxf(fmaf(-ds, ds, (qq.x + qq.y) * (1.f / C)), 0.f) + 1e-5f));
 }
 
+// Gives a kernel its dynamic shared memory.  `regs` is what its warpgroups'
+// register split adds up to: a split above what the launch of `warpgroups` has
+// would wait for ever.  One query per call, and a setting only where it is
+// missing (the first call on a device, or after its reset).
+template <typename K>
+cudaError_t tf_allow(K* kernel, int bytes, int warpgroups = 0, int regs = 0) {
+  cudaFuncAttributes at;
+  const cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+  if (e != cudaSuccess) return e;
+  if (at.numRegs * warpgroups < regs) return cudaErrorInvalidConfiguration;
+  if (at.maxDynamicSharedSizeBytes >= bytes) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 // f(std::integral_constant<int, ACT>) for the activations.
 template <typename F>
 cudaError_t by_act(int act, F&& f) {

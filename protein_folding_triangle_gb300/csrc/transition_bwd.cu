@@ -619,13 +619,8 @@ template <int C, int ACT>
 cudaError_t tb_launch(const TbMaps& m, TbParams p, int grid, cudaStream_t s) {
   p.slots = tb_slots<C>();
   const int bytes = TbSmem<C>::bytes(p.slots);
-  cudaError_t e = cudaFuncSetAttribute(transition_bwd_kernel<C, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       bytes);
-  cudaFuncAttributes at;
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, transition_bwd_kernel<C, ACT>);
+  const cudaError_t e = tf_allow(transition_bwd_kernel<C, ACT>, bytes, kTbThreads / 128, kRegsSum);
   if (e != cudaSuccess) return e;
-  // a split above the launch's registers would wait for ever
-  if (at.numRegs * (kTbThreads / 128) < kRegsSum) return cudaErrorInvalidConfiguration;
   transition_bwd_kernel<C, ACT><<<grid, kTbThreads, bytes, s>>>(m.z, m.dout, m.dz, m.x, m.win, m.wo, m.wx, p);
   return cudaGetLastError();
 }

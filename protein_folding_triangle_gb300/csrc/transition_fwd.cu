@@ -21,14 +21,20 @@
 // memory instead (a third longer per MMA); a chunk's [a | b] then takes 16
 // MMAs against the activation's reading it, so one stage is enough.
 //
-// Warps: 0 loads the weights, 3 tells CTA 0 that this CTA's are in; 1 and 2 (of CTA 0) issue the MMAs of both CTAs,
-// one the input projections, one the output projection: a wait costs an
-// issuer some 200 clocks even when the phase is complete, and the tensor
-// cores' queue is shorter than that (one issuer for both kept them busy for
-// 60% of the time); 4-7 normalise the next tile's rows, 8-11 drain out
-// (thread = row for both; one group for both took 10,000 clocks a tile,
-// more than its MMAs); 12-27 the activation, eight warps per stage, so that a
-// chunk's arithmetic may take the time of two chunks' MMAs.
+// Warps: 0 loads the weights, 3 tells CTA 0 that this CTA's are in; 1 and 2 (of
+// CTA 0) issue the MMAs of both CTAs, one the input projections, one the output
+// projection: a wait costs an issuer some 200 clocks even when the phase is
+// complete, and the tensor cores' queue is shorter than that (one issuer for
+// both kept them busy for 60% of the time); 4-7 normalise the next tile's rows,
+// 8-11 drain out (thread = row for both; one group for both took 10,000 clocks
+// a tile, more than its MMAs); 12-27 the activation, eight warps per stage, so
+// that a chunk's arithmetic may take the time of two chunks' MMAs.
+//
+// What bounds it is the MMAs' pace and the waits between them: 0.161 ms at
+// 768 x 768 rows, C = 128, H = 512, against 0.118 ms of products and 0.045 ms of
+// memory; the tensor pipe is active for 61 % of it (an MMA with A in TMEM takes
+// 87 clocks where the pipe needs 64).  384 x 384 rows, C = 256, H = 1024: 0.232 ms
+// against 0.118 (A in shared memory: 125 clocks).
 #include <algorithm>
 #include <cstring>
 
@@ -498,13 +504,8 @@ cudaError_t tf_launch(const CUtensorMap& tz, const CUtensorMap& to, const CUtens
                       TfParams p, int grid, cudaStream_t s) {
   p.slots = std::min(p.chunks, TfSmem<C>::kFit);
   const int bytes = TfSmem<C>::bytes(p.slots);
-  cudaError_t e = cudaFuncSetAttribute(transition_fwd_kernel<C, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       bytes);
-  cudaFuncAttributes at;
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, transition_fwd_kernel<C, ACT>);
+  const cudaError_t e = tf_allow(transition_fwd_kernel<C, ACT>, bytes, kTfThreads / 128, kTfRegsSum);
   if (e != cudaSuccess) return e;
-  // a split above the launch's registers would wait for ever
-  if (at.numRegs * (kTfThreads / 128) < kTfRegsSum) return cudaErrorInvalidConfiguration;
   transition_fwd_kernel<C, ACT><<<grid, kTfThreads, bytes, s>>>(tz, to, twi, two, p);
   return cudaGetLastError();
 }

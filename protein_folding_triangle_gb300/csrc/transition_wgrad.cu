@@ -266,8 +266,7 @@ __global__ void __launch_bounds__(kTwThreads, 1)
 template <int C, int ACT>
 cudaError_t tw_launch(const CUtensorMap& tx, const CUtensorMap& tg, const CUtensorMap& ti, const CUtensorMap& to,
                       const TwParams& p, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(transition_wgrad_kernel<C, ACT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, TwSmem<C>::kBytes);
+  const cudaError_t e = tf_allow(transition_wgrad_kernel<C, ACT>, TwSmem<C>::kBytes);
   if (e != cudaSuccess) return e;
   transition_wgrad_kernel<C, ACT><<<p.slices * p.groups, kTwThreads, TwSmem<C>::kBytes, s>>>(tx, tg, ti, to, p);
   return cudaGetLastError();

@@ -684,7 +684,7 @@ def transition_workspace_bytes(rows: int, C: int, H: int) -> int:
 
 
 def _fits(t, device: int, shape, dtype) -> bool:
-    return t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous()
+    return t is not None and t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous()
 
 
 def _transition_check(z, mask, ln_w, ln_b, w_in, w_o):
@@ -735,7 +735,9 @@ def triattn_transition_bwd(z, mask, ln_w, ln_b, w_in, w_o, d_out, activation: st
     again.  Returns (dz bf16, d_ln_w, d_ln_b, d_w_in, d_w_o), the parameter
     gradients FP32, or with ``grads_bf16`` BF16 (one rounding of the FP32 sums)."""
     M, C, H = _transition_check(z, mask, ln_w, ln_b, w_in, w_o)
-    _check(d_out, "d_out", z.shape)
+    if not _fits(d_out, z.get_device(), z.shape, torch.bfloat16):
+        _check(d_out, "d_out", z.shape)
+        _same_device(z.device, d_out=d_out)
     s = transition_shape(M, C, H, activation, grads_bf16)
     lib = load()
     need = lib.triattn_transition_workspace_bytes(ctypes.byref(s))
@@ -744,11 +746,12 @@ def triattn_transition_bwd(z, mask, ln_w, ln_b, w_in, w_o, d_out, activation: st
     dt = torch.bfloat16 if grads_bf16 else torch.float32
     here, sp = _on_stream(z.device, stream)
     with here:
-        workspace = torch.empty(need, dtype=torch.uint8, device=z.device) if workspace is None else workspace
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=z.device)
+        else:
+            _same_device(z.device, workspace=workspace)
         if out is None:
-            kw = dict(dtype=dt, device=z.device)
-            out = (torch.empty_like(z), torch.empty(C, **kw), torch.empty(C, **kw), torch.empty((C, 2 * H), **kw),
-                   torch.empty((H, C), **kw))
+            out = (torch.empty_like(z),) + tuple(torch.empty_like(t, dtype=dt) for t in (ln_w, ln_b, w_in, w_o))
             dz, dlw, dlb, dwi, dwo = out
         else:
             dz, dlw, dlb, dwi, dwo = out
@@ -757,7 +760,6 @@ def triattn_transition_bwd(z, mask, ln_w, ln_b, w_in, w_o, d_out, activation: st
                                    ("d_w_o", dwo, (H, C))):
                 _check(t, name, shape, dt)
             _same_device(z.device, dz=dz, d_ln_w=dlw, d_ln_b=dlb, d_w_in=dwi, d_w_o=dwo)
-        _same_device(z.device, d_out=d_out, workspace=workspace)
         code = lib.triattn_transition_bwd(ctypes.byref(s), z.data_ptr(), None if mask is None else mask.data_ptr(),
                                           ln_w.data_ptr(), ln_b.data_ptr(), w_in.data_ptr(), w_o.data_ptr(),
                                           d_out.data_ptr(), dz.data_ptr(), dlw.data_ptr(), dlb.data_ptr(),
