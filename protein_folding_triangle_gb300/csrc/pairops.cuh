@@ -4,6 +4,8 @@
 // fixed-order sums of the LayerNorm parameter gradients, and the traced call
 // of the library's tensor-core GEMM in row-major terms.
 #pragma once
+#include <type_traits>
+
 #include <cuda_runtime.h>
 
 #include <cstddef>
@@ -155,6 +157,22 @@ __device__ __forceinline__ void unpack(const Packed<K>& r, float (&f)[K]) {
 #pragma unroll
   for (int e = 0; e < K; ++e) f[e] = (e & 1) ? bf16hi_to_f32(r.w[e >> 1]) : bf16lo_to_f32(r.w[e >> 1]);
 }
+// The same of FP32 features, for kernels that take either.
+template <int K>
+struct Plain {
+  float v[K];
+};
+template <int K>
+__device__ __forceinline__ void ld_packed(const float* p, Plain<K>& r) {
+  ld_f32<K>(p, r.v);
+}
+template <int K>
+__device__ __forceinline__ void unpack(const Plain<K>& r, float (&f)[K]) {
+#pragma unroll
+  for (int e = 0; e < K; ++e) f[e] = r.v[e];
+}
+template <int K, typename T>
+using RowOf = std::conditional_t<std::is_same<T, float>::value, Plain<K>, Packed<K>>;
 
 // One warp per pair: x = (z - mean) * rstd * gamma + beta (BF16), mean and
 // rstd saved in FP32.  Lane l holds the C / 32 consecutive features from
@@ -222,9 +240,9 @@ __global__ void __launch_bounds__(256, kLnFwdPerSm) ln_fwd_kernel(const uint16_t
 // l holds the C / 32 consecutive features from l C / 32; the loads of
 // several pairs are in flight together.  MASKED: a row whose mask is 0 gives
 // dz = 0 and no part of dgamma and dbeta, whatever z and dx hold there.
-template <int C, bool MASKED = false>
+template <int C, bool MASKED = false, typename DX = uint16_t>
 __global__ void __launch_bounds__(256, kLnBwdPerSm) ln_bwd_kernel(const uint16_t* __restrict__ z,
-                                                                  const uint16_t* __restrict__ dx,
+                                                                  const DX* __restrict__ dx,
                                                                   const float* __restrict__ gamma,
                                                                   const float* __restrict__ mean_in,
                                                                   const float* __restrict__ rstd_in,
@@ -244,7 +262,8 @@ __global__ void __launch_bounds__(256, kLnBwdPerSm) ln_bwd_kernel(const uint16_t
 #pragma unroll
   for (int e = 0; e < kPer; ++e) accg[e] = accb[e] = 0.f;
   for (size_t m0 = static_cast<size_t>(blockIdx.x) * 8 + warp; m0 < M; m0 += kRows * warps) {
-    Packed<kPer> zr[kRows], dr[kRows];
+    Packed<kPer> zr[kRows];
+    RowOf<kPer, DX> dr[kRows];
     float mu[kRows], rs[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r)

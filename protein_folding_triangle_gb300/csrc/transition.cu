@@ -176,7 +176,7 @@ TrWs tr_ws(const TrDims& d) {
   w.h = o;    o += rup(d.M * d.H * 2);
   w.g = o;    o += rup(d.M * d.C * 2);
   w.dh = o;   o += rup(d.M * d.H * 2);
-  w.dx = o;   o += rup(d.M * d.C * 2);
+  w.dx = o;   o += rup(d.M * d.C * 4);  // FP32: BF16 would save 25 us of 940 and add a seventh to the error of dz
   w.pg = o;   o += rup(static_cast<size_t>(kLnBlocks) * d.C * 4);
   w.pb = o;   o += rup(static_cast<size_t>(kLnBlocks) * d.C * 4);
   w.total = o;
@@ -310,8 +310,9 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
   // Up to 128 features one kernel does everything before the weight gradients.
   // Wider rows of x, g and z do not fit the shared memory beside the weights:
   // there the steps are kernels of their own, with the gating in the epilogue
-  // of the recomputed projections (147456 rows, C = 256, H = 1024: 0.91 ms,
-  // 2.8 times the floor of its products; the fused path takes 2.2 times its own).
+  // of the recomputed projections (147456 rows, C = 256, H = 1024, masked:
+  // 0.94 ms, 4.0 times what the formula's products take at the tensor cores'
+  // rate; the fused path takes 3.2 times that).
   if (transition_bwd_fused(C)) {
     if (mk != nullptr) g = ws + w.g;
     float* const part = reinterpret_cast<float*>(ws + w.wg);
@@ -348,20 +349,20 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
     return TRIATTN_ERR_CUDA;
   if (!gemm(true, false, H, C, M, h, H, g, C, d_w_o, C, !d.bf16) ||
       !gemm(true, false, C, 2 * H, M, ws + w.x, C, P, 2 * H, d_w_in, 2 * H, !d.bf16) ||
-      !gemm(false, true, M, C, 2 * H, P, 2 * H, w_in, 2 * H, ws + w.dx, C, false))
+      !gemm(false, true, M, C, 2 * H, P, 2 * H, w_in, 2 * H, ws + w.dx, C, true))
     return TRIATTN_ERR_CUDA;
   if (trace_call(kKTrLnBwd, s, [&] {
         return by_c(C, [&](auto ic) {
           constexpr int kC = decltype(ic)::value;
           const uint16_t* zp = static_cast<const uint16_t*>(z);
-          const uint16_t* dx = reinterpret_cast<const uint16_t*>(ws + w.dx);
+          const float* dx = reinterpret_cast<const float*>(ws + w.dx);  // not rounded, as in the fused kernel
           const float* mean = reinterpret_cast<const float*>(ws + w.mean);
           const float* rstd = reinterpret_cast<const float*>(ws + w.rstd);
           uint16_t* dzp = static_cast<uint16_t*>(dz);
           if (mk != nullptr)
-            ln_bwd_kernel<kC, true><<<kLnBlocks, 256, 0, s>>>(zp, dx, ln_w, mean, rstd, dzp, pg, pb, d.M, mk);
+            ln_bwd_kernel<kC, true, float><<<kLnBlocks, 256, 0, s>>>(zp, dx, ln_w, mean, rstd, dzp, pg, pb, d.M, mk);
           else
-            ln_bwd_kernel<kC><<<kLnBlocks, 256, 0, s>>>(zp, dx, ln_w, mean, rstd, dzp, pg, pb, d.M);
+            ln_bwd_kernel<kC, false, float><<<kLnBlocks, 256, 0, s>>>(zp, dx, ln_w, mean, rstd, dzp, pg, pb, d.M);
           return cudaGetLastError();
         });
       }) != cudaSuccess)
