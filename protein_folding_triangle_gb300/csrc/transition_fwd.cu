@@ -343,6 +343,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
         *z16(c) = make_uint4(ws[0], ws[1], ws[2], ws[3]);
       }
       if constexpr (kXs) {
+        // Before the arrival: as long as this tile's products cannot start, x_free
+        // cannot pass the phase waited for; nor can x_full pass the one that the
+        // issuer waits for, since it takes each x_full before it issues the
+        // products that x_free stands for.
+        if (u > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->x_free, (u - 1) & 1, wc, abort))) return false;
         fence_proxy_async_smem();
       } else {
         if (u > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->x_free, (u - 1) & 1, wc, abort))) return false;
@@ -372,9 +377,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
     if constexpr (kXs) {
       for (int u = 0; u < mine && ok; ++u) {
         ok = normalise(u);
-        // the next tile's z takes the place of an x that the MMAs have read
-        const int v = u + 1 - L::kZt;
-        if (first && ok && u + 1 < mine && (v < 0 || mbar_wait(&bars->x_free, v & 1, wc, abort))) load_z(u + 1);
+        // the next tile's z takes the place of an x that the MMAs have read: the
+        // previous tile's, waited for above, or, with one z tile, this one's (whose
+        // next phase needs the very z that is loaded here)
+        if (first && ok && u + 1 < mine && (L::kZt == 2 || mbar_wait(&bars->x_free, u & 1, wc, abort))) load_z(u + 1);
         __syncwarp();
       }
     } else {
