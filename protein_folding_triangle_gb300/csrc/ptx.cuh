@@ -63,14 +63,30 @@ __device__ __forceinline__ bool mbar_try_wait_suspend(uint64_t* bar, uint32_t pa
 }
 constexpr uint32_t kSuspendHintNs = 20000;
 
+// The same with an acquire of cluster scope: it also orders what another CTA wrote
+// before an arrival that released at cluster scope (mbar_arrive_cluster).
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+
 // Bounded wait for the phase with the given parity.  `abort` is a CTA-shared
 // flag: once any thread of the CTA has given up, the others stop waiting.
+template <bool CLUSTER = false>
 static __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const WaitCtl& wc,
                                        volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (CLUSTER ? mbar_try_wait_cluster(bar, parity, kSuspendHintNs) : mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (;;) {
-    if (mbar_try_wait_suspend(bar, parity, kSuspendHintNs)) return true;
+    if (CLUSTER ? mbar_try_wait_cluster(bar, parity, kSuspendHintNs)
+                : mbar_try_wait_suspend(bar, parity, kSuspendHintNs))
+      return true;
     if (*abort) return false;
     if (global_timer_ns() - t0 > wc.limit_ns) {
       atomicOr(wc.status, kDevTimeout);
@@ -431,14 +447,24 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrival on the barrier at the same shared-memory offset in CTA `rank`.  What
-// it hands over lies in TMEM (ordered by the tcgen05 fences on both sides) or
-// was written by TMA; at cluster scope the release would also wait for every
+// Arrival on the barrier at the same shared-memory offset in CTA `rank`, for
+// what lies in TMEM (ordered by the tcgen05 fences on both sides) or was
+// written by TMA; at cluster scope the release would also wait for every
 // global store of the thread, and the acquire would drop the L1 cache.
 __device__ __forceinline__ void mbar_arrive_cta(uint64_t* bar, uint32_t rank) {
   asm volatile(
       "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n"
       " mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(rank)
+      : "memory");
+}
+// The same with a release of cluster scope, for what this thread (and those
+// that it has synchronised with) stored into this CTA's shared memory; the
+// waiting side takes mbar_wait<true>.
+__device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n"
+      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar)),
       "r"(rank)
       : "memory");
 }

@@ -232,7 +232,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
         } else {
           if (g >= 2) wait(&bars->ab_free[st], static_cast<uint32_t>((g >> 1) - 1) & 1);
         }
-        if (i == 0) wait(&bars->x_full, t & 1);
+        if (i == 0) ok = ok && __all_sync(0xffffffffu, mbar_wait<kXs>(&bars->x_full, t & 1, wc, abort));
         if (!stays || t == 0) wait(&bars->w_ready[ws], wphase);
         if (!ok) break;
         tc_fence_after();
@@ -369,7 +369,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTfThreads, 1)
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive_cta(&bars->x_full, 0);
+      if (lane == 0) {
+        // x in shared memory was stored by this CTA and is read for the MMAs that CTA
+        // 0's issuer starts: release and acquire have to reach across the pair
+        if constexpr (kXs) mbar_arrive_cluster(&bars->x_full, 0);
+        else mbar_arrive_cta(&bars->x_full, 0);
+      }
       return true;
     };
     bool ok = true;

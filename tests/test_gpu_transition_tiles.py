@@ -85,3 +85,25 @@ def test_forward_at_the_edge_of_a_wave(C, M):
     # one row is C elements, not 256 C: every rounding at its largest gives 1.06e-2
     assert np.sqrt((last ** 2).mean()) <= 2 * TOL_OUT * np.sqrt((got[-1] ** 2).mean())
     assert bool((buf[0] == 7.0).all()) and bool((buf[M + 1] == 7.0).all())
+
+
+@pytest.mark.parametrize("C,H", [(160, 32), (192, 128), (224, 64), (256, 96)])
+def test_wide_rows_under_load(C, H):
+    """At C > 128 both CTAs of a pair write x to their shared memory and one of
+    them starts the products on both: the same bits in every one of many calls,
+    with a second stream's calls and memory traffic beside them."""
+    x = S.make_transition_inputs((ROWS,), C, H, seed=C, drop=0.1)
+    d = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in x.items()}
+    ref = T.triattn_transition_fwd(*params(d))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    noise = torch.zeros(64 << 20, device="cuda")
+    torch.cuda.synchronize()
+    outs = [[torch.full_like(ref, 9.0) for _ in range(12)] for _ in streams]
+    torch.cuda.synchronize()
+    for k in range(12):
+        for s, o in zip(streams, outs):
+            T.triattn_transition_fwd(*params(d), out=o[k], stream=s)
+        noise.add_(1.0)
+    torch.cuda.synchronize()
+    assert T.device_status() == T.OK
+    assert all(torch.equal(o, ref) for os in outs for o in os)
