@@ -466,10 +466,11 @@ triattn_status triattn_trimul_bwd(const triattn_trimul_shape* shape, const void*
  * included).  The forward keeps nothing for the backward, which computes x, a
  * and b again.
  *
- * Operands of the products (x, h, m d_out, dh's parts) are rounded to BF16, sums
- * are FP32 and outputs are rounded once.  Up to 192 rows the forward rounds
- * nothing but out: a row may differ by those roundings between a small call and
- * a large one.
+ * Operands of the products (x, h, m d_out, [da | db], and dh above 128 features)
+ * are rounded to BF16, sums are FP32 and outputs are rounded once; act and act'
+ * are right to FP32 relative to their own value, however closed the gate.  Up to
+ * 192 rows the forward rounds nothing but out: a row may differ by those
+ * roundings between a small call and a large one.
  *
  * Shape: 0 <= M < 2^31; C a multiple of 32 up to 256; H a multiple of 32 up
  * to 4096; flags 0 or TRIATTN_FLAG_GRADS_BF16 (the backward's parameter

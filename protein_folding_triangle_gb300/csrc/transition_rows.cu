@@ -37,9 +37,10 @@ __device__ __forceinline__ float rw_sum(float v) {
   return v;
 }
 __device__ __forceinline__ float rw_act(float a, int act) {
-  if (act == TRIATTN_ACT_GELU) return 0.5f * a * (1.f + tanhf(a * fmaf(a * a, 0.0356774081f, 0.7978845608f)));
-  const float s = 1.f / (1.f + __expf(-a));
-  return act == TRIATTN_ACT_SILU ? a * s : s;
+  // GELU as a sigmoid too: 1 + tanh(u) would leave nothing of a closed gate
+  const float v = act == TRIATTN_ACT_GELU ? a * fmaf(a * a, 0.0713548163f, 1.5957691216f) : a;
+  const float s = 1.f / (1.f + __expf(-v));
+  return act == TRIATTN_ACT_SIGMOID ? s : a * s;
 }
 
 template <int R>
