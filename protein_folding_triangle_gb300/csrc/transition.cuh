@@ -98,7 +98,9 @@ __device__ __forceinline__ float2 row_stats(F&& z16) {
   return make_float2(k + ds, rsqrtf(fmaxf(fmaf(-ds, ds, (qq.x + qq.y) * (1.f / C)), 0.f) + 1e-5f));
 }
 
-// Gives a kernel its dynamic shared memory.  `regs` is what its warpgroups'
+// Allows a kernel `bytes` of dynamic shared memory: the most that any launch of it
+// takes, the same in every call, so that a thread that sets it never takes away
+// what another one is about to launch with.  `regs` is what its warpgroups'
 // register split adds up to: a split above what the launch of `warpgroups` has
 // would wait for ever.  One query per call, and a setting only where it is
 // missing (the first call on a device, or after its reset).

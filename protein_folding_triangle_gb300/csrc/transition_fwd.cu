@@ -515,7 +515,8 @@ cudaError_t tf_launch(const CUtensorMap& tz, const CUtensorMap& to, const CUtens
                       TfParams p, int grid, cudaStream_t s) {
   p.slots = std::min(p.chunks, TfSmem<C>::kFit);
   const int bytes = TfSmem<C>::bytes(p.slots);
-  const cudaError_t e = tf_allow(transition_fwd_kernel<C, ACT>, bytes, kTfThreads / 128, kTfRegsSum);
+  const cudaError_t e =
+      tf_allow(transition_fwd_kernel<C, ACT>, TfSmem<C>::bytes(TfSmem<C>::kFit), kTfThreads / 128, kTfRegsSum);
   if (e != cudaSuccess) return e;
   transition_fwd_kernel<C, ACT><<<grid, kTfThreads, bytes, s>>>(tz, to, twi, two, p);
   return cudaGetLastError();
