@@ -671,6 +671,11 @@ def _same_device(device, **tensors):
             raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+# After a call that wrote tensors of the caller's through their addresses: autograd
+# has to see that one it saved is no longer what it was (a list costs 50 ns per tensor).
+_written = torch.autograd.graph.increment_version
+
+
 def transition_shape(rows: int, C: int, H: int, activation: str = "silu", grads_bf16: bool = False) -> TransitionShape:
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {tuple(ACTIVATIONS)}")
@@ -716,6 +721,7 @@ def triattn_transition_fwd(z, mask, ln_w, ln_b, w_in, w_o, activation: str = "si
     M, C, H = _transition_check(z, mask, ln_w, ln_b, w_in, w_o)
     s = transition_shape(M, C, H, activation)
     here, sp = _on_stream(z.device, stream)
+    given = out
     with here:
         if out is None:
             out = torch.empty_like(z)
@@ -726,6 +732,8 @@ def triattn_transition_fwd(z, mask, ln_w, ln_b, w_in, w_o, activation: str = "si
                                              ln_w.data_ptr(), ln_b.data_ptr(), w_in.data_ptr(), w_o.data_ptr(),
                                              out.data_ptr(), sp)
     _raise(code, "triattn_transition_fwd")
+    if given is not None:
+        _written(out)
     return out
 
 
@@ -745,6 +753,7 @@ def triattn_transition_bwd(z, mask, ln_w, ln_b, w_in, w_o, d_out, activation: st
         raise TriAttnError(ERR_UNSUPPORTED, "triattn_transition_bwd")
     dt = torch.bfloat16 if grads_bf16 else torch.float32
     here, sp = _on_stream(z.device, stream)
+    given = out
     with here:
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=z.device)
@@ -765,6 +774,8 @@ def triattn_transition_bwd(z, mask, ln_w, ln_b, w_in, w_o, d_out, activation: st
                                           d_out.data_ptr(), dz.data_ptr(), dlw.data_ptr(), dlb.data_ptr(),
                                           dwi.data_ptr(), dwo.data_ptr(), workspace.data_ptr(), _bytes(workspace), sp)
     _raise(code, "triattn_transition_bwd")
+    if given is not None:
+        _written([dz, dlw, dlb, dwi, dwo])
     return dz, dlw, dlb, dwi, dwo
 
 
@@ -867,6 +878,7 @@ def triattn_clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, *, 
         code = lib.triattn_clip_grad_norm(table, into, n, kind, float(max_norm), norm.data_ptr(), ws.data_ptr(),
                                           ws.numel(), sp)
     _raise(code, "triattn_clip_grad_norm")
+    _written(tensors if out is None else out)
     return norm
 
 
