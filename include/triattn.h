@@ -539,7 +539,8 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
  * per block of threads and in FP64 above that, in a fixed order: bitwise
  * reproducible.
  * A NaN element makes norm NaN; a norm that is not finite makes coef NaN or
- * 0, and the gradients are multiplied by it like any other.  Destinations may
+ * 0, and the gradients are multiplied by it like any other.  `norm` and the
+ * workspace must not overlap a tensor or each other.  Destinations may
  * share no byte with one another or with a gradient, nor, in place, the
  * gradients with one another: TRIATTN_ERR_INVALID_ARG, as for a NULL or
  * misaligned pointer, a negative count, a norm type that is neither, a

@@ -21,11 +21,11 @@
 // chain, it joins the chains pairwise and adds them to a total, so that no sum is
 // long however large the list (as one chain, 34 GB lose up to 2e-4 of it).  A
 // block's threads are added pairwise in FP32 and the blocks' partials in FP64, all
-// in fixed order, so the result is bitwise reproducible and uses no atomics.  It is bound by HBM: 400 MB of BF16
-// in 70 us (5.7 TB/s), 480 MB of FP32 in 90 us.  Pass 2 (clipping only): every
+// in fixed order, so the result is bitwise reproducible and uses no atomics.  It is bound by HBM: 480 MB of FP32
+// in 72 us (6.7 TB/s).  Pass 2 (clipping only): every
 // block adds the same partials in the same order, so no block waits for
 // another, and scales its chunks, last chunk first: what pass 1 read last is
-// still in L2 (480 MB read and written in 158 us).  In place nothing is
+// still in L2 (480 MB read and written in 149 us).  In place nothing is
 // written when the coefficient is 1.
 #include <cuda_runtime.h>
 

@@ -163,8 +163,8 @@ cudaError_t launch_transition_fwd(long long M, int C, int H, int act, const void
 // The same for at most kTrRowsMax rows (transition_rows.cu): up to there all
 // clusters of four rows run at once (three CTAs fit an SM), and it is the faster
 // of the two for every width (us at C / H, 192 and 256 rows, against a tile of 256 rows:
-// 128 / 512 9.6 and 14.9, 12.6; 64 / 256 6.8 and 11.0, 7.9; 256 / 1024 21.3 and
-// 31.5, 32.4; 128 / 4096 36.6 and 51.3, 40.3).
+// 128 / 512 9.6 and 14.9, 13.5; 64 / 256 7.2 and 11.0, 8.7; 256 / 1024 21.4 and
+// 31.5, 34.8; 128 / 4096 36.7 and 51.3, 44.8).
 constexpr int kTrRowsMax = 192;
 cudaError_t launch_transition_rows(int M, int C, int H, int act, const void* z, const void* mask, const float* ln_w,
                                    const float* ln_b, const void* w_in, const void* w_o, void* out, cudaStream_t s);

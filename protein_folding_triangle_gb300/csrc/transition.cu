@@ -176,7 +176,7 @@ TrWs tr_ws(const TrDims& d) {
   w.h = o;    o += rup(d.M * d.H * 2);
   w.g = o;    o += rup(d.M * d.C * 2);
   w.dh = o;   o += rup(d.M * d.H * 2);
-  w.dx = o;   o += rup(d.M * d.C * 4);  // FP32: BF16 would save 25 us of 940 and add a seventh to the error of dz
+  w.dx = o;   o += rup(d.M * d.C * 4);  // FP32: BF16 would save 25 us of 950 and add a seventh to the error of dz
   w.pg = o;   o += rup(static_cast<size_t>(kLnBlocks) * d.C * 4);
   w.pb = o;   o += rup(static_cast<size_t>(kLnBlocks) * d.C * 4);
   w.total = o;
@@ -310,9 +310,11 @@ triattn_status triattn_transition_bwd(const triattn_transition_shape* shape, con
   // Up to 128 features one kernel does everything before the weight gradients.
   // Wider rows of x, g and z do not fit the shared memory beside the weights:
   // there the steps are kernels of their own, with the gating in the epilogue
-  // of the recomputed projections (147456 rows, C = 256, H = 1024, masked:
-  // 0.94 ms, 4.0 times what the formula's products take at the tensor cores'
-  // rate; the fused path takes 3.2 times that).
+  // of the recomputed projections.  147456 masked rows, C / H 256 / 1024: 0.95 ms,
+  // 4.0 times what the formula's products take at the tensor cores' rate;
+  // 192 / 768 0.76 ms, 5.7 times; 160 / 320 0.49 ms, 10 times (the fused path: 3.5
+  // times at 128 / 512, 5.6 at 64 / 256).  dh is rounded to BF16 on its way through
+  // memory, as an operand of the gating's kernel.
   if (transition_bwd_fused(C)) {
     if (mk != nullptr) g = ws + w.g;
     float* const part = reinterpret_cast<float*>(ws + w.wg);

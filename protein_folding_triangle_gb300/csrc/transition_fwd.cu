@@ -30,11 +30,19 @@
 // a tile, more than its MMAs); 12-27 the activation, eight warps per stage, so
 // that a chunk's arithmetic may take the time of two chunks' MMAs.
 //
-// What bounds it is the MMAs' pace and the waits between them: 0.161 ms at
+// What bounds it is the MMAs' pace and the waits between them: 0.160 ms at
 // 768 x 768 rows, C = 128, H = 512, against 0.118 ms of products and 0.045 ms of
-// memory; the tensor pipe is active for 61 % of it (an MMA with A in TMEM takes
-// 87 clocks where the pipe needs 64).  384 x 384 rows, C = 256, H = 1024: 0.232 ms
-// against 0.118 (A in shared memory: 125 clocks).
+// memory; the tensor pipe is active for 61 % of it (103 clocks per MMA, all told,
+// where the pipe needs 64).  384 x 384 rows, C = 256, H = 1024, GELU: 0.254 ms
+// against 0.118, the pipe active for 38 %: with one stage of [a | b] the products of
+// a chunk wait until the activation has read the chunk before.  640 x 640 rows,
+// C = 64, H = 256: 0.056 ms against 0.021, 30 %: at K = 64 the LayerNorm and the
+// activation take longer than the products.
+//
+// Roundings: x and h are BF16 because they are operands of the tensor cores (TF32
+// runs at half the rate, and twice the bytes do not fit TMEM and shared memory
+// beside the weights); a, b, the statistics and every sum are FP32.  The relative
+// error of out is 3.4e-3, of which one rounding of the result is 1.7e-3.
 #include <algorithm>
 #include <cstring>
 

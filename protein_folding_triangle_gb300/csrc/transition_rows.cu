@@ -10,8 +10,8 @@
 // only out is rounded.
 //
 // What bounds it is latency: a launch, the loads of z and of the weights, and
-// the exchange.  5.4 us per call for one row at C = 128, H = 512, 6.7 for 2 to 48
-// (a CTA per SM) in a captured graph, where the tile kernel takes 11.9.  One to four
+// the exchange.  5.2 us per call for one row at C = 128, H = 512, 6.1 to 6.5 for 2 to
+// 48 (a CTA per SM) in a captured graph, where the tile kernel takes 13.  One to four
 // rows at a time: the weights' loads are shared, and four sums per column stay in
 // registers.
 #include "kernels.cuh"

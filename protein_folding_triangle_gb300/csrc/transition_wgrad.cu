@@ -20,13 +20,14 @@
 // 192 columns, the gradients 192.
 //
 // What bounds it is shared memory: per row tile and slice the MMAs read 208 KB of
-// operands, the loads write 64 KB and the activation 48 KB.  0.403 ms at 768 x 768
-// rows, C = 128, H = 512, 100 bytes per clock, the tensor pipe active for 48 % of
-// it (0.24 ms of products); without the activation 0.397 ms, without that and the
-// loads 0.326 ms.  Row tiles brought to L2 ahead change nothing.
+// operands, the loads write 64 KB and the activation 48 KB.  0.422 ms at 768 x 768
+// rows, C = 128, H = 512, 95 bytes per clock, the tensor pipe active for 46 % of
+// it (0.24 ms of products).  With the hardware tanh in the gates it was 0.403 ms,
+// without the activation 0.397 ms, without that and the loads 0.326 ms.  Row tiles
+// brought to L2 ahead change nothing.
 // With C <= 64 x and g share the A operand of the gradients and four stages
 // fit: 0.098 ms at 640 x 640 rows, C = 64, H = 256 (0.143 ms without both).
-// Eight activation warps instead of sixteen: 0.43 ms.
+// Eight activation warps instead of sixteen: 0.43 ms (0.403 then).
 //
 // Warps: 0 loads, 1 issues the first two products, 2 the last two, 4-19 the
 // activation (warp = 32 rows x 16 features) and, at the end, the partials.

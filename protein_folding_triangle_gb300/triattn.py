@@ -151,7 +151,7 @@ def _declare(lib):
     lib.triattn_trimul_fwd.restype = ctypes.c_int
     lib.triattn_trimul_bwd.argtypes = [tp] + [vp] * 16 + [ctypes.c_size_t, vp]
     lib.triattn_trimul_bwd.restype = ctypes.c_int
-    rp, gp = ctypes.POINTER(TransitionShape), ctypes.POINTER(Tensor)
+    rp = ctypes.POINTER(TransitionShape)
     lib.triattn_transition_workspace_bytes.argtypes = [rp]
     lib.triattn_transition_workspace_bytes.restype = ctypes.c_size_t
     lib.triattn_transition_fwd.argtypes = [rp] + [vp] * 8
