@@ -568,6 +568,134 @@ triattn_status triattn_clip_grad_norm(const triattn_tensor* tensors, const triat
                                       size_t workspace_bytes, void* stream);
 
 /*
+ * Norms of queries and keys for each head, with the position rotation in the
+ * same pass: what stands between the projections and the core.  For every row
+ * x [D] of q and of k (example b, slice o, head h, token n):
+ *
+ *   y = R(pos) (w[h] * x / sqrt(mean_d x^2 + eps))
+ *
+ * R turns the D / 2 pairs of features by pos * theta^(-2 i / D), i the pair:
+ * (y_a, y_b) = (u_a cos - u_b sin, u_a sin + u_b cos).  TRIATTN_ROTARY_HALF:
+ * pairs (i, i + D/2); TRIATTN_ROTARY_INTERLEAVED: pairs (2i, 2i + 1);
+ * TRIATTN_ROTARY_NONE: no rotation.  pos is positions[b, n], or n where
+ * positions is NULL; angles are right to 3e-7 for every 32-bit position.
+ * Statistics and sums are FP32, each output is rounded once.  The backward
+ * computes everything again from q and k.
+ *
+ * Shape: B, N_o, N, H >= 1, D 16 or 32, B <= 65535, B*N_o < 2^31, H*N < 2^30;
+ * w_heads H (w_q, w_k [H, D]) or 1 ([D], the same for all heads); eps and theta
+ * positive and finite; flags 0.  Otherwise TRIATTN_ERR_INVALID_ARG or
+ * TRIATTN_ERR_UNSUPPORTED (D, sizes); the size query returns 0.
+ *
+ * q, k share a layout, so do the outputs, the incoming gradients and dq, dk
+ * (each NULL: the core's contiguous layout; otherwise the rules of
+ * tri_attn_fwd_strided), BF16, 16-byte aligned.  Weights and their gradients
+ * are FP32, positions [B, N] int32, 4-byte aligned.  Outputs must not overlap
+ * inputs, but for dq and dk, which may be d_q_out and d_k_out (same pointers
+ * and layout).  d_w_q, d_w_k are overwritten.  q and k have to be finite: a row
+ * that is not makes its own outputs and the weights' gradients NaN.
+ * workspace (backward): triattn_qk_norm_workspace_bytes(shape) bytes,
+ * 256-byte aligned, contents ignored.  Bitwise reproducible.
+ */
+#define TRIATTN_ROTARY_NONE 0
+#define TRIATTN_ROTARY_HALF 1
+#define TRIATTN_ROTARY_INTERLEAVED 2
+
+typedef struct {
+  int B;          /* examples */
+  int N_o;        /* outer slices */
+  int N;          /* tokens */
+  int H;          /* heads */
+  int D;          /* features per head: 16 or 32 */
+  int w_heads;    /* rows of the weights: H, or 1 */
+  int rotary;     /* TRIATTN_ROTARY_* */
+  float eps;      /* added to the mean square */
+  double theta;   /* base of the rotation's frequencies */
+  unsigned flags; /* 0 */
+} triattn_qk_norm_shape;
+
+size_t triattn_qk_norm_workspace_bytes(const triattn_qk_norm_shape* shape);
+
+triattn_status triattn_qk_norm_fwd(const triattn_qk_norm_shape* shape, const void* q, const void* k,
+                                   const triattn_layout* in_layout, const float* w_q, const float* w_k,
+                                   const int* positions, void* q_out, void* k_out, const triattn_layout* out_layout,
+                                   void* stream);
+
+/* Backward of <q_out, d_q_out> + <k_out, d_k_out>. */
+triattn_status triattn_qk_norm_bwd(const triattn_qk_norm_shape* shape, const void* q, const void* k,
+                                   const triattn_layout* in_layout, const float* w_q, const float* w_k,
+                                   const int* positions, const void* d_q_out, const void* d_k_out,
+                                   const triattn_layout* d_out_layout, void* dq, void* dk,
+                                   const triattn_layout* grad_layout, float* d_w_q, float* d_w_k, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * Learned relative position bias by buckets:
+ *
+ *   out[pair, :] = base[pair, :] + table[bucket(b, i, j), :]
+ *   d_table[k, :] = sum of d_out[pair, :] over the pairs of bucket k
+ *
+ * over the pairs (b, i, j) of N tokens, F values each: the planes that the
+ * core takes as bias, [B, F, N, N] (TRIATTN_RELPOS_HEADS, F heads), or pair
+ * features [B, N, N, F] (TRIATTN_RELPOS_PAIRS).  With d = positions[b, i] -
+ * positions[b, j] (the token's index where positions is NULL) and R =
+ * max_distance:
+ *
+ *   TRIATTN_BUCKETS_CLIP  min(max(d, -R), R) + R; 2 R + 1 rows
+ *   TRIATTN_BUCKETS_LOG   n rows (even, at least 4, R > n / 4), half of them for
+ *                         d >= 0, half for d < 0; with e = n / 4 (rounded down)
+ *                         and m = min(|d|, R), row m for m < e, else
+ *                         min(n / 2 - 1, e + floor((n / 2 - e) log(m / e) / log(R / e)));
+ *                         the rows of d < 0 follow those of d >= 0
+ *
+ * With chains [B, N] (ids, int32) the table has one more row, its last, for
+ * all pairs of different chains.  buckets is the number of all rows.
+ *
+ * Shape: B, F >= 1, 1 <= N <= 16384, B*N*N < 2^31, at most 256 buckets, R 1 to
+ * 1024; heads: B*F <= 65535; pairs: F a multiple of 8 up to 256.  flags 0, or
+ * TRIATTN_FLAG_DOUT_FP32 (heads only; the backward's d_out is FP32, as the
+ * core writes dbias with TRIATTN_FLAG_DBIAS_FP32; the forward ignores it).
+ * Otherwise TRIATTN_ERR_INVALID_ARG (also for a number of buckets that does not
+ * fit the rule) or TRIATTN_ERR_UNSUPPORTED; the size query returns 0.
+ *
+ * table and d_table [buckets, F] FP32; base (optional, NULL = zero) and out
+ * BF16, rounded once; d_out BF16 or FP32; positions, chains optional.  All
+ * contiguous, 16-byte aligned; positions, chains and d_table 4-byte aligned.
+ * out may be base; otherwise outputs must not overlap inputs.  The gradient of
+ * base is d_out.  d_out has to be finite (a value that is not may make other
+ * buckets of its column NaN).  Sums are FP32, joined in FP64, in a fixed order:
+ * bitwise reproducible.  workspace (backward):
+ * triattn_relpos_workspace_bytes(shape) bytes, 256-byte aligned, contents
+ * ignored.
+ */
+#define TRIATTN_RELPOS_HEADS 0
+#define TRIATTN_RELPOS_PAIRS 1
+#define TRIATTN_BUCKETS_CLIP 0
+#define TRIATTN_BUCKETS_LOG 1
+#define TRIATTN_FLAG_DOUT_FP32 4u
+
+typedef struct {
+  int B;            /* examples */
+  int N;            /* tokens */
+  int F;            /* heads, or pair features */
+  int layout;       /* TRIATTN_RELPOS_* */
+  int kind;         /* TRIATTN_BUCKETS_* */
+  int buckets;      /* rows of the table */
+  int max_distance; /* R */
+  unsigned flags;   /* 0 or TRIATTN_FLAG_DOUT_FP32 */
+} triattn_relpos_shape;
+
+size_t triattn_relpos_workspace_bytes(const triattn_relpos_shape* shape);
+
+triattn_status triattn_relpos_fwd(const triattn_relpos_shape* shape, const float* table, const void* base,
+                                  const int* positions, const int* chains, void* out, void* stream);
+
+/* Backward of <out, d_out>: d_table (overwritten). */
+triattn_status triattn_relpos_bwd(const triattn_relpos_shape* shape, const void* d_out, const int* positions,
+                                  const int* chains, float* d_table, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
  * The library's tensor-core GEMM, as used by the multiplicative update and
  * the module (exported so that it can be tested and reused; not one of the
  * method's operations).  Row-major C[M, N] = op(A) op(B): A is [M, K] with

@@ -208,7 +208,9 @@ const char* const kKernelName[kKinds] = {"tri_attn_fwd",     "bwd_preprocess",  
                                          "transition_ln",   "transition_fwd",  "transition_rows", "transition_bwd", "transition_wgrad",
                                          "transition_gemm", "transition_gate",
                                          "transition_ln_bwd", "transition_colsum", "grad_table", "grad_sum",
-                                         "grad_scale",      "grad_norm"};
+                                         "grad_scale",      "grad_norm",
+                                         "qk_norm_fwd",     "qk_norm_bwd",     "qk_norm_dw",
+                                         "relpos_fwd",      "relpos_bwd",      "relpos_sum"};
 struct TraceRec {
   int kind;
   cudaEvent_t a, b;
@@ -246,6 +248,8 @@ cudaError_t traced(int kind, cudaStream_t s, F launch) {
 }
 
 }  // namespace
+
+bool row_layout_from(const triattn_layout* u, const triattn_shape* s, RowLayout* out) { return layout_from(u, s, out); }
 
 cudaError_t trace_call(int kind, cudaStream_t s, cudaError_t (*launch)(void*), void* arg) {
   return traced(kind, s, [&] { return launch(arg); });

@@ -7,6 +7,7 @@
 #include <type_traits>
 
 #include "ptx.cuh"
+#include "triattn.h"
 
 namespace triattn {
 
@@ -39,6 +40,9 @@ struct RowLayout {
 inline RowLayout contiguous_layout(int N, int H, int D) {
   return RowLayout{static_cast<long long>(H) * N * D, static_cast<long long>(N) * D, D, 0};
 }
+// A caller's layout by the rules of the strided entry points (null: the
+// library's own); false when it breaks one.
+bool row_layout_from(const triattn_layout* u, const triattn_shape* s, RowLayout* out);
 // Rows [n0, n0 + box) of slice bo, head h through a map of the layout above.
 __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, uint64_t* bar, bool hn, int n0, int h,
                                               int bo, int H) {
@@ -193,6 +197,7 @@ enum KernelKind {
   kKModLnFwd, kKModLayout, kKModGemm, kKModLnBwd, kKModColSum,
   kKTmLnIn, kKTmProj, kKTmGate, kKTmContract, kKTmLnOut, kKTmOutGate, kKTmColSum, kKGemm, kKTmProjGate,
   kKTrLn, kKTrFwd, kKTrRows, kKTrBwd, kKTrWgrad, kKTrGemm, kKTrGate, kKTrLnBwd, kKTrColSum, kKGradTable, kKGradSum, kKGradScale, kKGradNorm,
+  kKQkFwd, kKQkBwd, kKQkDw, kKRelFwd, kKRelBwd, kKRelSum,
   kKinds
 };
 // Runs `launch` on stream `s`, bracketed by a pair of trace events while

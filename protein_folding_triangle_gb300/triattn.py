@@ -42,10 +42,12 @@ EXPORTED = ("triattn_status_string", "triattn_fwd_workspace_bytes", "triattn_bwd
             "triattn_trimul_bwd", "triattn_gemm_workspace_bytes", "triattn_gemm", "tri_attn_fwd_strided",
             "tri_attn_bwd_strided", "triattn_transition_workspace_bytes", "triattn_transition_fwd",
             "triattn_transition_bwd", "triattn_grad_norm_workspace_bytes", "triattn_grad_norm",
-            "triattn_clip_grad_norm")
+            "triattn_clip_grad_norm", "triattn_qk_norm_workspace_bytes", "triattn_qk_norm_fwd", "triattn_qk_norm_bwd",
+            "triattn_relpos_workspace_bytes", "triattn_relpos_fwd", "triattn_relpos_bwd")
 
 FLAG_DBIAS_FP32 = 1
 FLAG_GRADS_BF16 = 2
+FLAG_DOUT_FP32 = 4
 
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -87,6 +89,18 @@ class TransitionShape(ctypes.Structure):
                 ("flags", ctypes.c_uint)]
 
 
+class QKNormShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("N_o", ctypes.c_int), ("N", ctypes.c_int), ("H", ctypes.c_int),
+                ("D", ctypes.c_int), ("w_heads", ctypes.c_int), ("rotary", ctypes.c_int), ("eps", ctypes.c_float),
+                ("theta", ctypes.c_double), ("flags", ctypes.c_uint)]
+
+
+class RelposShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("F", ctypes.c_int), ("layout", ctypes.c_int),
+                ("kind", ctypes.c_int), ("buckets", ctypes.c_int), ("max_distance", ctypes.c_int),
+                ("flags", ctypes.c_uint)]
+
+
 class Tensor(ctypes.Structure):
     """triattn_tensor: one gradient of a list (device pointer, elements, dtype)."""
     _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_longlong), ("dtype", ctypes.c_int)]
@@ -94,6 +108,9 @@ class Tensor(ctypes.Structure):
 
 ACTIVATIONS = {"silu": 0, "sigmoid": 1, "gelu": 2}
 TRIMUL_DIRECTIONS = {"outgoing": 0, "incoming": 1}
+ROTARY = {"none": 0, "half": 1, "interleaved": 2}
+RELPOS_LAYOUTS = {"heads": 0, "pairs": 1}
+BUCKETS = {"clip": 0, "log": 1}
 
 
 def _declare(lib):
@@ -165,6 +182,21 @@ def _declare(lib):
     lib.triattn_grad_norm.restype = ctypes.c_int
     lib.triattn_clip_grad_norm.argtypes = [vp, vp, ll, ctypes.c_int, ctypes.c_float, vp, vp, ctypes.c_size_t, vp]
     lib.triattn_clip_grad_norm.restype = ctypes.c_int
+    qp = ctypes.POINTER(QKNormShape)
+    lib.triattn_qk_norm_workspace_bytes.argtypes = [qp]
+    lib.triattn_qk_norm_workspace_bytes.restype = ctypes.c_size_t
+    lib.triattn_qk_norm_fwd.argtypes = [qp, vp, vp, lp, vp, vp, vp, vp, vp, lp, vp]
+    lib.triattn_qk_norm_fwd.restype = ctypes.c_int
+    lib.triattn_qk_norm_bwd.argtypes = ([qp, vp, vp, lp, vp, vp, vp, vp, vp, lp, vp, vp, lp, vp, vp, vp,
+                                         ctypes.c_size_t, vp])
+    lib.triattn_qk_norm_bwd.restype = ctypes.c_int
+    bp = ctypes.POINTER(RelposShape)
+    lib.triattn_relpos_workspace_bytes.argtypes = [bp]
+    lib.triattn_relpos_workspace_bytes.restype = ctypes.c_size_t
+    lib.triattn_relpos_fwd.argtypes = [bp] + [vp] * 6
+    lib.triattn_relpos_fwd.restype = ctypes.c_int
+    lib.triattn_relpos_bwd.argtypes = [bp] + [vp] * 5 + [ctypes.c_size_t, vp]
+    lib.triattn_relpos_bwd.restype = ctypes.c_int
     lib.triattn_gemm_workspace_bytes.argtypes = [ctypes.c_int] * 4
     lib.triattn_gemm_workspace_bytes.restype = ctypes.c_size_t
     lib.triattn_gemm.argtypes = ([ctypes.c_int] * 5 + [vp, ll, vp, ll, vp, ll, ctypes.c_int, ctypes.c_int, ll, ll, ll,
@@ -777,6 +809,217 @@ def triattn_transition_bwd(z, mask, ln_w, ln_b, w_in, w_o, d_out, activation: st
     if given is not None:
         _written([dz, dlw, dlb, dwi, dwo])
     return dz, dlw, dlb, dwi, dwo
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows_pair(a, b, names, shape, device):
+    """The layout that two [B, N_o, H, N, D] views share, None where both are contiguous."""
+    if a.is_contiguous() and b.is_contiguous():
+        for name, t in zip(names, (a, b)):
+            _check(t, name, shape)
+        lay = None
+    else:
+        lay = layout_of(a)
+        for name, t in zip(names, (a, b)):
+            _check_view(t, name, shape, lay)
+    _same_device(device, **dict(zip(names, (a, b))))
+    return lay
+
+
+def qk_norm_shape(shape, w, rotary: str = "half", theta: float = 10000.0, eps: float = 1e-6) -> QKNormShape:
+    """Of q's shape and its weight, [H, D] or [D]."""
+    if len(shape) != 5:
+        raise ValueError("q must be [B, N_o, H, N, D]")
+    if rotary not in ROTARY:
+        raise ValueError(f"rotary must be one of {tuple(ROTARY)}")
+    B, No, H, N, D = shape
+    return QKNormShape(B, No, N, H, D, 1 if w.dim() == 1 else H, ROTARY[rotary], eps, theta, 0)
+
+
+def _qk_norm_check(q, k, w_q, w_k, positions, rotary, theta, eps):
+    s = qk_norm_shape(q.shape, w_q, rotary, theta, eps)
+    lay = _rows_pair(q, k, ("q", "k"), q.shape, q.device)
+    w_shape = (s.D,) if w_q.dim() == 1 else (s.H, s.D)
+    _check(w_q, "w_q", w_shape, torch.float32)
+    _check(w_k, "w_k", w_shape, torch.float32)
+    if positions is not None:
+        _check(positions, "positions", (s.B, s.N), torch.int32)
+    _same_device(q.device, w_q=w_q, w_k=w_k, positions=positions)
+    return s, lay
+
+
+def _ref(lay):
+    return None if lay is None else ctypes.byref(lay)
+
+
+def triattn_qk_norm_fwd(q, k, w_q, w_k, positions=None, rotary: str = "half", *, theta: float = 10000.0,
+                        eps: float = 1e-6, out=None, stream=None):
+    """Norms of queries and keys for each head with the position rotation:
+    y = R(pos) (w[h] * x rsqrt(mean x^2 + eps)) for every row of q and k
+    [B, N_o, H, N, D] bf16 (contiguous, or views as tri_attn_fwd_strided takes
+    them).  ``w_q``, ``w_k`` [H, D] or [D] fp32; ``positions`` [B, N] int32 (the
+    token's index if None); ``rotary`` "half", "interleaved" or "none".  Returns
+    (q, k) normed, contiguous, or written into the views ``out``."""
+    s, lay = _qk_norm_check(q, k, w_q, w_k, positions, rotary, theta, eps)
+    here, sp = _on_stream(q.device, stream)
+    given, lo = out, None
+    with here:
+        if out is None:
+            out = tuple(torch.empty(q.shape, dtype=q.dtype, device=q.device) for _ in range(2))
+        else:
+            lo = _rows_pair(*out, ("q_out", "k_out"), q.shape, q.device)
+        qo, ko = out
+        code = load().triattn_qk_norm_fwd(ctypes.byref(s), q.data_ptr(), k.data_ptr(), _ref(lay), w_q.data_ptr(),
+                                          w_k.data_ptr(), _address(positions), qo.data_ptr(), ko.data_ptr(), _ref(lo),
+                                          sp)
+    _raise(code, "triattn_qk_norm_fwd")
+    if given is not None:
+        _written([qo, ko])
+    return qo, ko
+
+
+def triattn_qk_norm_bwd(q, k, w_q, w_k, d_q_out, d_k_out, positions=None, rotary: str = "half", *,
+                        theta: float = 10000.0, eps: float = 1e-6, workspace=None, out=None, stream=None):
+    """Backward of <q_out, d_q_out> + <k_out, d_k_out>; the norms are computed
+    again from q and k.  Returns (dq, dk bf16, d_w_q, d_w_k fp32); ``out`` may
+    pass them preallocated, dq and dk also as views, or d_q_out and d_k_out
+    themselves."""
+    s, lay = _qk_norm_check(q, k, w_q, w_k, positions, rotary, theta, eps)
+    ld = _rows_pair(d_q_out, d_k_out, ("d_q_out", "d_k_out"), q.shape, q.device)
+    lib = load()
+    need = lib.triattn_qk_norm_workspace_bytes(ctypes.byref(s))
+    if need == 0:
+        raise TriAttnError(ERR_UNSUPPORTED, "triattn_qk_norm_bwd")
+    here, sp = _on_stream(q.device, stream)
+    given, lg = out, None
+    with here:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            _same_device(q.device, workspace=workspace)
+        if out is None:
+            out = tuple(torch.empty(q.shape, dtype=q.dtype, device=q.device) for _ in range(2))
+            out += (torch.empty_like(w_q), torch.empty_like(w_k))
+            dq, dk, dwq, dwk = out
+        else:
+            dq, dk, dwq, dwk = out
+            lg = _rows_pair(dq, dk, ("dq", "dk"), q.shape, q.device)
+            _check(dwq, "d_w_q", w_q.shape, torch.float32)
+            _check(dwk, "d_w_k", w_k.shape, torch.float32)
+            _same_device(q.device, d_w_q=dwq, d_w_k=dwk)
+        code = lib.triattn_qk_norm_bwd(ctypes.byref(s), q.data_ptr(), k.data_ptr(), _ref(lay), w_q.data_ptr(),
+                                       w_k.data_ptr(), _address(positions), d_q_out.data_ptr(), d_k_out.data_ptr(),
+                                       _ref(ld), dq.data_ptr(), dk.data_ptr(), _ref(lg), dwq.data_ptr(),
+                                       dwk.data_ptr(), workspace.data_ptr(), _bytes(workspace), sp)
+    _raise(code, "triattn_qk_norm_bwd")
+    if given is not None:
+        _written([dq, dk, dwq, dwk])
+    return dq, dk, dwq, dwk
+
+
+def relpos_shape(B: int, N: int, F: int, buckets: int, layout: str = "heads", kind: str = "clip",
+                 max_distance: int = 32, dout_fp32: bool = False) -> RelposShape:
+    if layout not in RELPOS_LAYOUTS:
+        raise ValueError(f"layout must be one of {tuple(RELPOS_LAYOUTS)}")
+    if kind not in BUCKETS:
+        raise ValueError(f"kind must be one of {tuple(BUCKETS)}")
+    return RelposShape(B, N, F, RELPOS_LAYOUTS[layout], BUCKETS[kind], buckets, max_distance,
+                       FLAG_DOUT_FP32 if dout_fp32 else 0)
+
+
+def _relpos_ids(positions, chains, B, N, device):
+    for name, t in (("positions", positions), ("chains", chains)):
+        if t is not None:
+            _check(t, name, (B, N), torch.int32)
+    _same_device(device, positions=positions, chains=chains)
+
+
+def triattn_relpos_fwd(table, base=None, positions=None, chains=None, *, layout: str = "heads", kind: str = "clip",
+                       max_distance: int = 32, out=None, stream=None):
+    """Learned relative position bias: out = base + table[bucket(i, j)], planes
+    [B, F, N, N] ("heads": the core's bias) or pair features [B, N, N, F]
+    ("pairs"), bf16.  ``table`` [buckets, F] fp32; ``base`` of out's shape or
+    None (then positions or out give B and N); ``positions`` [B, N] int32 (the
+    token's index if None); ``chains`` [B, N] int32 or None: pairs of different
+    chains take the table's last row, which it has for them.  ``kind`` "clip":
+    2 max_distance + 1 rows; "log": an even number of rows, logarithmic from a
+    quarter of them to max_distance.  ``out`` may be base."""
+    if table.dim() != 2:
+        raise ValueError("table must be [buckets, F]")
+    K, F = table.shape
+    device = table.device
+    like = base if base is not None else out
+    if like is not None:
+        if like.dim() != 4:
+            raise ValueError("base must be [B, F, N, N] or [B, N, N, F]")
+        B, N = like.shape[0], like.shape[2]
+    elif positions is not None and positions.dim() == 2:
+        B, N = positions.shape
+    else:
+        raise ValueError("base, out or positions [B, N] must be given")
+    s = relpos_shape(B, N, F, K, layout, kind, max_distance)
+    shape = (B, F, N, N) if layout == "heads" else (B, N, N, F)
+    _check(table, "table", (K, F), torch.float32)
+    if base is not None:
+        _check(base, "base", shape)
+        _same_device(device, base=base)
+    _relpos_ids(positions, chains, B, N, device)
+    here, sp = _on_stream(device, stream)
+    given = out
+    with here:
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        else:
+            _check(out, "out", shape)
+            _same_device(device, out=out)
+        code = load().triattn_relpos_fwd(ctypes.byref(s), table.data_ptr(), _address(base), _address(positions),
+                                         _address(chains), out.data_ptr(), sp)
+    _raise(code, "triattn_relpos_fwd")
+    if given is not None:
+        _written(out)
+    return out
+
+
+def triattn_relpos_bwd(d_out, buckets: int, positions=None, chains=None, *, layout: str = "heads", kind: str = "clip",
+                       max_distance: int = 32, workspace=None, out=None, stream=None):
+    """Gradient of the table of ``buckets`` rows: d_table [buckets, F] fp32 from
+    d_out [B, F, N, N] (bf16, or fp32 as tri_attn_bwd(..., dbias_fp32=True)
+    gives it) or [B, N, N, F] (bf16).  The gradient of base is d_out itself."""
+    if d_out.dim() != 4:
+        raise ValueError("d_out must be [B, F, N, N] or [B, N, N, F]")
+    B, N = d_out.shape[0], d_out.shape[2]
+    F = d_out.shape[1] if layout == "heads" else d_out.shape[3]
+    f32 = d_out.dtype is torch.float32 and layout == "heads"
+    s = relpos_shape(B, N, F, buckets, layout, kind, max_distance, f32)
+    _check(d_out, "d_out", (B, F, N, N) if layout == "heads" else (B, N, N, F),
+           torch.float32 if f32 else torch.bfloat16)
+    device = d_out.device
+    _relpos_ids(positions, chains, B, N, device)
+    lib = load()
+    need = lib.triattn_relpos_workspace_bytes(ctypes.byref(s))
+    if need == 0:
+        raise TriAttnError(ERR_UNSUPPORTED, "triattn_relpos_bwd")
+    here, sp = _on_stream(device, stream)
+    given = out
+    with here:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        else:
+            _same_device(device, workspace=workspace)
+        if out is None:
+            out = torch.empty((buckets, F), dtype=torch.float32, device=device)
+        else:
+            _check(out, "d_table", (buckets, F), torch.float32)
+            _same_device(device, d_table=out)
+        code = lib.triattn_relpos_bwd(ctypes.byref(s), d_out.data_ptr(), _address(positions), _address(chains),
+                                      out.data_ptr(), workspace.data_ptr(), _bytes(workspace), sp)
+    _raise(code, "triattn_relpos_bwd")
+    if given is not None:
+        _written(out)
+    return out
 
 
 GRAD_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
