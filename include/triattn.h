@@ -696,6 +696,48 @@ triattn_status triattn_relpos_bwd(const triattn_relpos_shape* shape, const void*
                                   void* stream);
 
 /*
+ * Orthogonalising a list of n matrices (the updates of a model's projection
+ * matrices) by Newton-Schulz products.  For every matrix G, with
+ * X = G / (|G|_F + eps), `steps` times
+ *
+ *   A = X X^T,  B = b A + c A^2,  X <- a X + B X   (a, b, c: coefficients)
+ *
+ * (X^T X and X B for a matrix of more rows than columns), then out = X: G's
+ * singular vectors with singular values near 1 for coefficients such as 3.4445,
+ * -4.7750, 2.0315 and five steps.  The products' operands are pairs of FP16
+ * values (22 bits, down to 2^-33), sums are FP32, those of the norm's squares FP64
+ * above a run of rows; out is rounded once.  Every matrix depends on itself alone, bit
+ * for bit.  Coefficients have to keep every element of X, A, c A + b I and
+ * B + a I below 255; a matrix that is not finite gives an out that is not.
+ *
+ * `matrices` and `out` are HOST arrays, read before the call returns: row-major
+ * DEVICE matrices, `stride` elements between rows, BF16 or FP32 (out: BF16),
+ * aligned to their element; out[i] has the sizes of matrices[i] and may share
+ * memory with any of `matrices` (all are read before the first is written), not
+ * with another out.  Matrices without elements are skipped.  Sides up to 65536,
+ * 1 to 64 steps, at most 2^20 matrices, and tiles of 2^31 in all.
+ * TRIATTN_ERR_INVALID_ARG: a NULL or misaligned pointer, a negative size, a stride
+ * below cols, outputs that overlap or do not match, steps < 1, eps or a
+ * coefficient that is not finite, eps <= 0.  TRIATTN_ERR_UNSUPPORTED: another
+ * dtype, larger sizes, more steps.  workspace:
+ * triattn_orthogonalize_workspace_bytes(matrices, n) bytes (it depends on the
+ * sizes alone), 256-byte aligned, contents ignored.  Nothing waits for the
+ * device.  Bitwise reproducible.
+ */
+typedef struct {
+  void* data;       /* device pointer */
+  long long rows;
+  long long cols;
+  long long stride; /* elements between rows, >= cols */
+  int dtype;        /* TRIATTN_DTYPE_* */
+} triattn_matrix;
+
+size_t triattn_orthogonalize_workspace_bytes(const triattn_matrix* matrices, long long n);
+triattn_status triattn_orthogonalize(const triattn_matrix* matrices, const triattn_matrix* out, long long n, int steps,
+                                     const float* coefficients, float eps, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/*
  * The library's tensor-core GEMM, as used by the multiplicative update and
  * the module (exported so that it can be tested and reused; not one of the
  * method's operations).  Row-major C[M, N] = op(A) op(B): A is [M, K] with

@@ -210,7 +210,8 @@ const char* const kKernelName[kKinds] = {"tri_attn_fwd",     "bwd_preprocess",  
                                          "transition_ln_bwd", "transition_colsum", "grad_table", "grad_sum",
                                          "grad_scale",      "grad_norm",
                                          "qk_norm_fwd",     "qk_norm_bwd",     "qk_norm_dw",
-                                         "relpos_fwd",      "relpos_bwd",      "relpos_sum"};
+                                         "relpos_fwd",      "relpos_bwd",      "relpos_sum",
+                                         "orth_load",       "orth_gemm"};
 struct TraceRec {
   int kind;
   cudaEvent_t a, b;

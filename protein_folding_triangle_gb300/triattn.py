@@ -43,7 +43,8 @@ EXPORTED = ("triattn_status_string", "triattn_fwd_workspace_bytes", "triattn_bwd
             "tri_attn_bwd_strided", "triattn_transition_workspace_bytes", "triattn_transition_fwd",
             "triattn_transition_bwd", "triattn_grad_norm_workspace_bytes", "triattn_grad_norm",
             "triattn_clip_grad_norm", "triattn_qk_norm_workspace_bytes", "triattn_qk_norm_fwd", "triattn_qk_norm_bwd",
-            "triattn_relpos_workspace_bytes", "triattn_relpos_fwd", "triattn_relpos_bwd")
+            "triattn_relpos_workspace_bytes", "triattn_relpos_fwd", "triattn_relpos_bwd",
+            "triattn_orthogonalize_workspace_bytes", "triattn_orthogonalize")
 
 FLAG_DBIAS_FP32 = 1
 FLAG_GRADS_BF16 = 2
@@ -197,6 +198,10 @@ def _declare(lib):
     lib.triattn_relpos_fwd.restype = ctypes.c_int
     lib.triattn_relpos_bwd.argtypes = [bp] + [vp] * 5 + [ctypes.c_size_t, vp]
     lib.triattn_relpos_bwd.restype = ctypes.c_int
+    lib.triattn_orthogonalize_workspace_bytes.argtypes = [vp, ll]
+    lib.triattn_orthogonalize_workspace_bytes.restype = ctypes.c_size_t
+    lib.triattn_orthogonalize.argtypes = [vp, vp, ll, ctypes.c_int, vp, ctypes.c_float, vp, ctypes.c_size_t, vp]
+    lib.triattn_orthogonalize.restype = ctypes.c_int
     lib.triattn_gemm_workspace_bytes.argtypes = [ctypes.c_int] * 4
     lib.triattn_gemm_workspace_bytes.restype = ctypes.c_size_t
     lib.triattn_gemm.argtypes = ([ctypes.c_int] * 5 + [vp, ll, vp, ll, vp, ll, ctypes.c_int, ctypes.c_int, ll, ll, ll,
@@ -1123,6 +1128,68 @@ def triattn_clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, *, 
     _raise(code, "triattn_clip_grad_norm")
     _written(tensors if out is None else out)
     return norm
+
+
+def _matrix_table(tensors, name, device):
+    """The triattn_matrix array of a list of 2-D tensors, five words each."""
+    rows = []
+    for i, t in enumerate(tensors):
+        if t.dim() != 2 or t.dtype not in GRAD_DTYPES or t.device != device or t.layout != torch.strided:
+            raise ValueError(f"{name}[{i}] must be a 2-D bfloat16 or float32 tensor on {device}")
+        m, n = t.shape
+        stride = t.stride(0) if m > 1 else n
+        if (n > 1 and t.stride(1) != 1) or (stride < n and t.numel()):
+            raise ValueError(f"{name}[{i}] must have contiguous rows")
+        rows += (t.data_ptr(), m, n, stride, GRAD_DTYPES[t.dtype])
+    return struct.pack(f"{len(rows)}q", *rows)
+
+
+ORTHOGONALIZE = (3.4445, -4.7750, 2.0315)
+
+
+def triattn_orthogonalize(tensors, steps: int = 5, *, coefficients=ORTHOGONALIZE, eps: float = 1e-7, out=None,
+                          workspace=None, stream=None):
+    """Orthogonalise a list of matrices (2-D BF16 or FP32 CUDA tensors, mixed,
+    with contiguous rows) by Newton-Schulz products: X = G / (|G| + eps), then
+    ``steps`` times X <- a X + (b A + c A^2) X, A = X X^T.  Returns the list of
+    results (BF16, of the same shapes), or writes them into ``out``, whose tensors
+    may be those of ``tensors``; nothing waits for the device.  A captured call
+    keeps the tensors' addresses."""
+    tensors = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
+    if len(coefficients) != 3:
+        raise ValueError("coefficients must be three numbers")
+    device = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
+    if device.type != "cuda":
+        raise ValueError("the matrices must be CUDA tensors")
+    n = len(tensors)
+    table = _matrix_table(tensors, "tensors", device)
+    here, sp = _on_stream(device, stream)
+    given = out
+    lib = load()
+    with here:
+        if out is None:
+            out = [torch.empty(t.shape, dtype=torch.bfloat16, device=device) for t in tensors]
+        else:
+            out = [out] if isinstance(out, torch.Tensor) else list(out)
+            if len(out) != n:
+                raise ValueError(f"out has {len(out)} tensors, expected {n}")
+            for i, (a, b) in enumerate(zip(tensors, out)):
+                if a.shape != b.shape or b.dtype is not torch.bfloat16:
+                    raise ValueError(f"out[{i}] must be a bfloat16 tensor of the shape of tensors[{i}]")
+        into = _matrix_table(out, "out", device)
+        need = lib.triattn_orthogonalize_workspace_bytes(table, n)
+        if need == 0:
+            raise TriAttnError(ERR_UNSUPPORTED, "triattn_orthogonalize")
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        else:
+            _same_device(device, workspace=workspace)
+        code = lib.triattn_orthogonalize(table, into, n, int(steps), struct.pack("3f", *map(float, coefficients)),
+                                         float(eps), workspace.data_ptr(), _bytes(workspace), sp)
+    _raise(code, "triattn_orthogonalize")
+    if given is not None:
+        _written(out)
+    return out
 
 
 def gemm(a, b, *, ta: bool = False, tb: bool = False, out_f32: bool = False, out=None, stream=None):
