@@ -706,8 +706,7 @@ triattn_status triattn_relpos_bwd(const triattn_relpos_shape* shape, const void*
  * singular vectors with singular values near 1 for coefficients such as 3.4445,
  * -4.7750, 2.0315 and five steps.  The products' operands are pairs of FP16
  * values (22 bits, down to 2^-33), sums are FP32, those of the norm's squares FP64
- * above a run of rows; out is rounded once.  Every matrix depends on itself alone, bit
- * for bit.  Coefficients have to keep every element of X, A, c A + b I and
+ * above a run of rows; out is rounded once.  Coefficients have to keep every element of X, A, c A + b I and
  * B + a I below 255; a matrix that is not finite gives an out that is not.
  *
  * `matrices` and `out` are HOST arrays, read before the call returns: row-major
@@ -722,7 +721,8 @@ triattn_status triattn_relpos_bwd(const triattn_relpos_shape* shape, const void*
  * dtype, larger sizes, more steps.  workspace:
  * triattn_orthogonalize_workspace_bytes(matrices, n) bytes (it depends on the
  * sizes alone), 256-byte aligned, contents ignored.  Nothing waits for the
- * device.  Bitwise reproducible.
+ * device.  Bitwise reproducible for the same list of sizes; in another list a
+ * matrix may be shared out otherwise, and its sums added in another order.
  */
 typedef struct {
   void* data;       /* device pointer */

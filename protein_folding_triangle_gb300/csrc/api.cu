@@ -211,7 +211,7 @@ const char* const kKernelName[kKinds] = {"tri_attn_fwd",     "bwd_preprocess",  
                                          "grad_scale",      "grad_norm",
                                          "qk_norm_fwd",     "qk_norm_bwd",     "qk_norm_dw",
                                          "relpos_fwd",      "relpos_bwd",      "relpos_sum",
-                                         "orth_load",       "orth_gemm"};
+                                         "orth_load",       "orth_gemm",       "orth_solo"};
 struct TraceRec {
   int kind;
   cudaEvent_t a, b;

@@ -197,7 +197,7 @@ enum KernelKind {
   kKModLnFwd, kKModLayout, kKModGemm, kKModLnBwd, kKModColSum,
   kKTmLnIn, kKTmProj, kKTmGate, kKTmContract, kKTmLnOut, kKTmOutGate, kKTmColSum, kKGemm, kKTmProjGate,
   kKTrLn, kKTrFwd, kKTrRows, kKTrBwd, kKTrWgrad, kKTrGemm, kKTrGate, kKTrLnBwd, kKTrColSum, kKGradTable, kKGradSum, kKGradScale, kKGradNorm,
-  kKQkFwd, kKQkBwd, kKQkDw, kKRelFwd, kKRelBwd, kKRelSum, kKOrthLoad, kKOrthGemm,
+  kKQkFwd, kKQkBwd, kKQkDw, kKRelFwd, kKRelBwd, kKRelSum, kKOrthLoad, kKOrthGemm, kKOrthSolo,
   kKinds
 };
 // Runs `launch` on stream `s`, bracketed by a pair of trace events while

@@ -32,39 +32,11 @@
 #include <vector>
 
 #include "kernels.cuh"
+#include "orthogonalize.cuh"
 #include "triattn.h"
 
 namespace triattn {
 namespace {
-
-constexpr int kTile = 32768;     // bytes of a tile, hi and lo
-constexpr int kPlane = 16384;
-constexpr float kScale = 256.f;  // what is stored of a value
-
-// One matrix of the list, as the kernels see it.
-struct OrthMat {
-  const void* src;
-  void* dst;
-  long long ld_src, ld_dst;  // elements between rows
-  int m, n;                  // X
-  int flags;                 // kFp32: the source is FP32; kTall: X is the transposed matrix
-  int mt, nt;                // 128-row and 128-column tiles of X
-  int x[2], a, a2, b;        // tiles of X (two copies), A, A', B'
-  int parts, part0;          // partial sums of squares
-  int part_rows;             // rows of the source per partial sum
-  int tiles0, sq0, mn0;      // tiles (128 x 64) of X, 128 x 128 tiles of A and of X before this matrix
-};
-constexpr int kFp32 = 1, kTall = 2;
-
-struct OrthView {
-  const OrthMat* mat;
-  float* part;
-  uint8_t* tiles;
-  int n;
-};
-__device__ __forceinline__ uint8_t* tile_at(const OrthView& v, int t) {
-  return v.tiles + static_cast<size_t>(t) * kTile;
-}
 
 constexpr int kUpload = 256;
 struct OrthTable {
@@ -92,7 +64,7 @@ __device__ __forceinline__ int find(const OrthView& v, int at) {
 }
 
 __device__ __forceinline__ float element(const OrthMat& q, long long at) {
-  return (q.flags & kFp32) ? __ldg(static_cast<const float*>(q.src) + at)
+  return (q.flags & kOrthFp32) ? __ldg(static_cast<const float*>(q.src) + at)
                            : bf16lo_to_f32(__ldg(static_cast<const uint16_t*>(q.src) + at));
 }
 
@@ -101,7 +73,7 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(OrthView v) {
   __shared__ float sh[8];
   const int k = find<&OrthMat::part0>(v, blockIdx.x);
   const OrthMat q = v.mat[k];
-  const int rows = (q.flags & kTall) ? q.n : q.m, cols = (q.flags & kTall) ? q.m : q.n;
+  const int rows = (q.flags & kOrthTall) ? q.n : q.m, cols = (q.flags & kOrthTall) ? q.m : q.n;
   const int r0 = (blockIdx.x - q.part0) * q.part_rows, r1 = min(r0 + q.part_rows, rows);
   float s = 0.f;
   const int e = (r1 - r0) * cols;  // part_rows keeps this small unless a row is long
@@ -121,24 +93,6 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(OrthView v) {
   }
 }
 
-__device__ __forceinline__ uint16_t half_bits(float x) { return __half_as_ushort(__float2half_rn(x)); }
-__device__ __forceinline__ float half_value(uint16_t b) { return __half2float(__ushort_as_half(b)); }
-
-// Eight scaled values as FP16 pairs, one 16-byte piece of each plane.
-__device__ __forceinline__ void split8(const float* y, uint4& hi, uint4& lo) {
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __half2 a = __floats2half2_rn(y[2 * e], y[2 * e + 1]);
-    const float2 f = __half22float2(a);
-    const __half2 b = __floats2half2_rn(y[2 * e] - f.x, y[2 * e + 1] - f.y);
-    h[e] = *reinterpret_cast<const uint32_t*>(&a);
-    l[e] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-
 // One tile of X per block: normed, scaled, split, in the image's order.
 __global__ void __launch_bounds__(256) orth_load_kernel(OrthView v, float eps) {
   __shared__ double sh[256];
@@ -152,10 +106,10 @@ __global__ void __launch_bounds__(256) orth_load_kernel(OrthView v, float eps) {
     if (threadIdx.x < o) sh[threadIdx.x] += sh[threadIdx.x + o];
     __syncthreads();
   }
-  const float scale = static_cast<float>(static_cast<double>(kScale) / (sqrt(sh[0]) + eps));
+  const float scale = static_cast<float>(static_cast<double>(kOrthScale) / (sqrt(sh[0]) + eps));
   const int t = blockIdx.x - q.tiles0, i = t / (2 * q.nt), c = t - i * 2 * q.nt;
   uint8_t* out = tile_at(v, q.x[0] + t);
-  const bool tall = (q.flags & kTall) != 0;
+  const bool tall = (q.flags & kOrthTall) != 0;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int e = threadIdx.x + 256 * u;
@@ -172,13 +126,13 @@ __global__ void __launch_bounds__(256) orth_load_kernel(OrthView v, float eps) {
     uint4 hi, lo;
     split8(y, hi, lo);
     *reinterpret_cast<uint4*>(out + sw128(r, p)) = hi;
-    *reinterpret_cast<uint4*>(out + kPlane + sw128(r, p)) = lo;
+    *reinterpret_cast<uint4*>(out + kOrthPlane + sw128(r, p)) = lo;
   }
 }
 
 // ------------------------------------------------------------- products
 constexpr int kStages = 3;
-constexpr int kStage = 2 * kTile;  // the A and the B operand of 64 of K
+constexpr int kStage = 2 * kOrthTile;  // the A and the B operand of 64 of K
 constexpr int kEpiWarps = 4;
 constexpr int kStg = 8192;         // staging of an epilogue warp: 32 rows of a tile, hi and lo
 constexpr int kThreads = (2 + kEpiWarps) * 32;
@@ -253,25 +207,25 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
         if (!__all_sync(0xffffffffu, mbar_wait(&bars.empty[stage], phase ^ 1, st.wc, abort))) { go = false; break; }
         if (lane == 0) {
           uint8_t* sa = sm + stage * kStage;
-          uint8_t* sb = sa + kTile;
+          uint8_t* sb = sa + kOrthTile;
           uint64_t* full = &bars.full[stage];
           const bool same = PHASE == 1 && t.i == t.j;
-          mbar_expect_tx(full, same ? kTile : kStage);
+          mbar_expect_tx(full, same ? kOrthTile : kStage);
           const int x = q.x[st.in];
           if constexpr (PHASE == 1) {
-            bulk_load(sa, tile_at(v, x + t.i * 2 * q.nt + kk), kTile, full);
-            if (!same) bulk_load(sb, tile_at(v, x + t.j * 2 * q.nt + kk), kTile, full);
+            bulk_load(sa, tile_at(v, x + t.i * 2 * q.nt + kk), kOrthTile, full);
+            if (!same) bulk_load(sb, tile_at(v, x + t.j * 2 * q.nt + kk), kOrthTile, full);
           } else if constexpr (PHASE == 2) {
-            bulk_load(sa, tile_at(v, q.a2 + t.i * 2 * q.mt + kk), kTile, full);
-            bulk_load(sb, tile_at(v, q.a + t.j * 2 * q.mt + kk), kTile, full);
+            bulk_load(sa, tile_at(v, q.a2 + t.i * 2 * q.mt + kk), kOrthTile, full);
+            bulk_load(sb, tile_at(v, q.a + t.j * 2 * q.mt + kk), kOrthTile, full);
           } else {
-            bulk_load(sa, tile_at(v, q.b + t.i * 2 * q.mt + kk), kTile, full);
+            bulk_load(sa, tile_at(v, q.b + t.i * 2 * q.mt + kk), kOrthTile, full);
             // 64 rows of two tiles side by side: blocks of 64 columns, hi then lo
             const uint8_t* p = tile_at(v, x + (kk >> 1) * 2 * q.nt + 2 * t.j) + (kk & 1) * 8192;
             bulk_load(sb, p, 8192, full);
-            bulk_load(sb + 8192, p + kTile, 8192, full);
-            bulk_load(sb + 16384, p + kPlane, 8192, full);
-            bulk_load(sb + 24576, p + kTile + kPlane, 8192, full);
+            bulk_load(sb + 8192, p + kOrthTile, 8192, full);
+            bulk_load(sb + 16384, p + kOrthPlane, 8192, full);
+            bulk_load(sb + 24576, p + kOrthTile + kOrthPlane, 8192, full);
           }
         }
         __syncwarp();
@@ -290,16 +244,16 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
       for (int kk = 0; kk < t.ks; ++kk) {
         if (!__all_sync(0xffffffffu, mbar_wait(&bars.full[stage], phase, st.wc, abort))) { go = false; break; }
         tc_fence_after();
-        const uint32_t sa = smem_u32(sm + stage * kStage), sb = PHASE == 1 && t.i == t.j ? sa : sa + kTile;
+        const uint32_t sa = smem_u32(sm + stage * kStage), sb = PHASE == 1 && t.i == t.j ? sa : sa + kOrthTile;
         if (elect_one()) {
 #pragma unroll
           for (int k16 = 0; k16 < 4; ++k16) {
             uint64_t da[2], db[2];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-              da[p] = smem_desc(sa + p * kPlane + k16 * 32, 16, 1024, 2);
-              db[p] = PHASE == 3 ? smem_desc(sb + p * kPlane + k16 * 2048, 8192, 1024, 2)
-                                 : smem_desc(sb + p * kPlane + k16 * 32, 16, 1024, 2);
+              da[p] = smem_desc(sa + p * kOrthPlane + k16 * 32, 16, 1024, 2);
+              db[p] = PHASE == 3 ? smem_desc(sb + p * kOrthPlane + k16 * 2048, 8192, 1024, 2)
+                                 : smem_desc(sb + p * kOrthPlane + k16 * 32, 16, 1024, 2);
             }
             mma_ss(tmem + ab * 128, da[0], db[0], idesc, (kk > 0 || k16 > 0) ? 1u : 0u);
             mma_ss(tmem + ab * 128, da[0], db[1], idesc, 1u);
@@ -336,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
       __syncwarp();
       if (lane == 0) {
         bulk_store_nc(tile + quarter * 4096, stg, 4096);
-        bulk_store_nc(tile + kPlane + quarter * 4096, stg + 4096, 4096);
+        bulk_store_nc(tile + kOrthPlane + quarter * 4096, stg + 4096, 4096);
         bulk_commit();
       }
     };
@@ -357,16 +311,16 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
           mbar_arrive(&bars.acc_empty[ab]);
         }
         const int diag = t.i * 128 + r - (t.j * 128 + 64 * h);  // the column of this row's diagonal element
-        constexpr float kBack = 1.f / kScale;                   // products carry the scale twice
+        constexpr float kBack = 1.f / kOrthScale;                   // products carry the scale twice
         if constexpr (PHASE == 1) {
           const int tt = t.i * 2 * q.mt + 2 * t.j + h;
           store(tile_at(v, q.a + tt), u, w, [&](int, float x) { return x * kBack; });
           store(tile_at(v, q.a2 + tt), u, w, [&](int col, float x) {
-            return st.c * (x * kBack) + (col == diag ? st.b * kScale : 0.f);
+            return st.c * (x * kBack) + (col == diag ? st.b * kOrthScale : 0.f);
           });
         } else if constexpr (PHASE == 2) {
           store(tile_at(v, q.b + t.i * 2 * q.mt + 2 * t.j + h), u, w,
-                [&](int col, float x) { return x * kBack + (col == diag ? st.a * kScale : 0.f); });
+                [&](int col, float x) { return x * kBack + (col == diag ? st.a * kOrthScale : 0.f); });
         } else if (!st.last) {
           store(tile_at(v, q.x[st.in ^ 1] + t.i * 2 * q.nt + 2 * t.j + h), u, w,
                 [&](int, float x) { return x * kBack; });
@@ -378,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
             for (int e = 0; e < 64; ++e) {
               if (col0 + e >= q.n) break;
               const float x = __uint_as_float(e < 32 ? u[e & 31] : w[e & 31]) * (kBack * kBack);
-              const long long o = (q.flags & kTall) ? (col0 + e) * q.ld_dst + row : row * q.ld_dst + col0 + e;
+              const long long o = (q.flags & kOrthTall) ? (col0 + e) * q.ld_dst + row : row * q.ld_dst + col0 + e;
               dst[o] = static_cast<uint16_t>(pack_bf16x2(x, 0.f) & 0xFFFFu);
             }
           }
@@ -399,8 +353,12 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
 }
 
 // ------------------------------------------------------------------ host
+// The list as the kernels take it: the matrices of one row of tiles (m <= 128)
+// first, the widest in front, then the others, and where their parts lie in the
+// workspace.
 struct Plan {
   std::vector<OrthMat> mats;
+  int solo = 0;
   long long parts = 0, load_tiles = 0, sq = 0, mn = 0, tiles = 0;
   size_t part_off = 0, tiles_off = 0, total = 0;
 };
@@ -420,40 +378,68 @@ bool plan_of(const triattn_matrix* in, const triattn_matrix* out, long long n, P
       q.dst = out[k].data;
       q.ld_dst = out[k].stride;
     }
-    q.flags = (in[k].dtype == TRIATTN_DTYPE_FP32 ? kFp32 : 0) | (rows > cols ? kTall : 0);
+    q.flags = (in[k].dtype == TRIATTN_DTYPE_FP32 ? kOrthFp32 : 0) | (rows > cols ? kOrthTall : 0);
     q.m = std::min(rows, cols);
     q.n = std::max(rows, cols);
     q.mt = (q.m + 127) / 128;
     q.nt = (q.n + 127) / 128;
     q.part_rows = std::max(1, 16384 / cols);
     q.parts = (rows + q.part_rows - 1) / q.part_rows;
+    p->mats.push_back(q);
+  }
+  const auto others = std::stable_partition(p->mats.begin(), p->mats.end(), [](const OrthMat& q) { return q.mt == 1; });
+  p->solo = static_cast<int>(others - p->mats.begin());
+  std::stable_sort(p->mats.begin(), others, [](const OrthMat& x, const OrthMat& y) { return x.n > y.n; });
+  for (OrthMat& q : p->mats) {
+    const long long xt = 2ll * q.mt * q.nt, at = 2ll * q.mt * q.mt;
     q.part0 = static_cast<int>(p->parts);
     q.tiles0 = static_cast<int>(p->load_tiles);
-    q.sq0 = static_cast<int>(p->sq);
-    q.mn0 = static_cast<int>(p->mn);
-    const long long xt = 2ll * q.mt * q.nt, at = 2ll * q.mt * q.mt;
-    long long t = p->tiles;
-    for (int* s : {&q.x[0], &q.x[1]}) {
-      *s = static_cast<int>(t);
-      t += xt;
-    }
-    for (int* s : {&q.a, &q.a2, &q.b}) {
-      *s = static_cast<int>(t);
-      t += at;
-    }
-    p->tiles = t;
     p->parts += q.parts;
     p->load_tiles += xt;
-    p->sq += at / 2;
-    p->mn += xt / 2;
+    q.x[0] = static_cast<int>(p->tiles);
+    p->tiles += xt;
+    if (q.mt > 1) {
+      q.sq0 = static_cast<int>(p->sq);
+      q.mn0 = static_cast<int>(p->mn);
+      p->sq += at / 2;
+      p->mn += xt / 2;
+      q.x[1] = static_cast<int>(p->tiles);
+      q.a = static_cast<int>(p->tiles + xt);
+      q.a2 = static_cast<int>(p->tiles + xt + at);
+      q.b = static_cast<int>(p->tiles + xt + 2 * at);
+      p->tiles += xt + 3 * at;
+    }
     if (p->tiles >= (1ll << 31) || p->parts >= (1ll << 31)) return false;
-    p->mats.push_back(q);
   }
   auto up = [](size_t x) { return (x + 1023) / 1024 * 1024; };
   p->part_off = up(p->mats.size() * sizeof(OrthMat));
   p->tiles_off = up(p->part_off + static_cast<size_t>(p->parts) * 4);
-  p->total = p->tiles_off + static_cast<size_t>(p->tiles) * kTile;
+  p->total = p->tiles_off + static_cast<size_t>(p->tiles) * kOrthTile;
   return true;
+}
+
+// CTAs per matrix of one row of tiles.  A CTA takes about 1.7 k cycles per chunk
+// of 64 columns and step, and 4 k (alone) or 7 k (in a team, which adds its parts
+// of A) between two passes; the list takes as long as its widest matrix or as its
+// sum spread over the SMs (clusters of eight leave some of a GPC's idle).
+int team_of(const OrthMat* q, int n) {
+  int best = 1;
+  double least = 0.0;
+  for (int t = 1; t <= 8; t *= 2) {
+    double widest = 0.0, sum = 0.0;
+    for (int k = 0; k < n; ++k) {
+      const int chunks = (q[k].n + 63) / 64;
+      const double c = 1.7 * ((chunks + t - 1) / t) + (t > 1 ? 7.0 : 4.0);
+      widest = std::max(widest, c);
+      sum += c * t;
+    }
+    const double time = std::max(widest, sum / (t == 8 ? 128 : 152));
+    if (t == 1 || time < least) {
+      best = t;
+      least = time;
+    }
+  }
+  return best;
 }
 
 constexpr long long kMaxSide = 65536;
@@ -507,8 +493,15 @@ cudaError_t run(const Plan& p, int steps, const float* co, float eps, uint8_t* w
       orth_load_kernel<<<static_cast<unsigned>(p.load_tiles), 256, 0, s>>>(v, eps);
       return cudaGetLastError();
     });
+  if (p.solo > 0 && e == cudaSuccess)
+    e = trace_call(kKOrthSolo, s, [&] {
+      return launch_orth_solo(mats, p.solo, v.tiles, steps, OrthCoef{co[0], co[1], co[2]},
+                              team_of(p.mats.data(), p.solo), wc, s);
+    });
+  v.mat += p.solo;
+  v.n -= p.solo;
   OrthStep st{co[0], co[1], co[2], 0, 0, 0, wc};
-  for (int k = 0; k < steps && e == cudaSuccess; ++k) {
+  for (int k = 0; k < steps && v.n > 0 && e == cudaSuccess; ++k) {
     st.in = k & 1;
     st.last = k == steps - 1;
     st.items = static_cast<int>(p.sq);

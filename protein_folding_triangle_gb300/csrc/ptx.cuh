@@ -259,6 +259,9 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// The same for shared memory of the whole cluster and for global memory.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
 // One lane of a converged warp returns true (elect.sync); the warp stays
 // converged around the guarded region, so values every lane computed can
 // live in uniform registers.
@@ -499,6 +502,16 @@ __device__ __forceinline__ float2 ld_cluster_f32x2(const float* p, uint32_t rank
       : "r"(smem_u32(p)), "r"(rank)
       : "memory");
   return v;
+}
+// Address of p's place in CTA `rank` of the cluster, and a 16-byte store there.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t a, const uint4& v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
 }
 // At the end of a CTA whose waits gave up: copies and MMAs that were under way
 // then may still touch its shared memory and TMEM; they take microseconds.
