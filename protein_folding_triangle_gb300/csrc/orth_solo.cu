@@ -2,20 +2,27 @@
 // projection of a pair stack of 128 features): one kernel for all steps, a CTA
 // or a cluster ("team") of 2, 4 or 8 per matrix, X cut along its columns.
 //
-// B' [128, 128] stays in shared memory and A in TMEM, and a step is one pass over
-// the CTA's columns, 64 at a time: D = B' X_c, the epilogue turns D into the new
-// X_c in the place of the old one, and A += X_c X_c^T for the next step follows at
-// once, so a chunk is touched once per step and not once per product.  Up to five
-// chunks per CTA stay in shared memory for all steps; more go through L2 (the
-// working set of all CTAs, 64 KB a chunk, fits it).  Between two passes the team
-// adds its parts of A through distributed shared memory, every CTA one band of
-// rows, in the order of the ranks, and every CTA then makes all of B' = b A + c A^2
-// + a I.
+// A step is one pass over the CTA's columns, 64 at a time: D = B' X_c, the
+// epilogue turns D into the new X_c in the place of the old one, and
+// A += X_c X_c^T for the next step follows at once, so a chunk is touched once per
+// step and not once per product.  Up to five chunks per CTA stay in shared memory
+// for all steps; more go through L2 (the working set of all CTAs, 64 KB a chunk,
+// fits it).  The left operands B' and the new X_c are in TMEM: from shared memory
+// both operands of an MMA of 64 columns take 68 cycles to read, 34 to multiply.
 //
-//   warp 0     loads of X's chunks (ring of five)
-//   warp 1     MMAs: 24 of N = 64 for D and 12 of N = m for A per chunk, each three
-//              products of FP16 pairs; 24 of N = m for A^2 per step
-//   warps 2-9  D to X, A and A^2 to B': thread = row, 32 or 64 columns
+// Between two passes the team adds its parts of A, every CTA one band of rows in
+// the order of the ranks, and every CTA then makes all of B' = b A + c A^2 + a I.
+// The parts go through L2 (distributed shared memory took 20 us a step for a team
+// of eight) and the bands of the sum from there by multicast.
+//
+//   warp 0      loads of X's chunks (ring of five)
+//   warp 1      MMAs: 24 of N = 64 for D and 12 of N = m for A per chunk, each three
+//               products of FP16 pairs; 24 of N = m for A^2 per step.  D runs two
+//               chunks ahead of A, so that the epilogue's time is hidden
+//   warps 2-17  D to X, A and A^2 to B': thread = row, 16 or 32 columns
+//
+// A and B' are held without the scale (their norms are near 1 and what matters is
+// the error beside that), so the products' results need no factor.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -29,11 +36,13 @@ namespace triattn {
 namespace {
 
 constexpr int kRing = 5;
-constexpr int kB = 2 * kOrthTile;  // A, then B', as two tiles of 64 columns
+constexpr int kB = 2 * kOrthTile;  // A as two tiles of 64 columns
 constexpr int kSmem = kB + kRing * kOrthTile + 1024;
-constexpr int kWarps = 8;  // epilogue
+constexpr int kWarps = 16;  // epilogue
+constexpr int kAhead = 2;    // chunks that D is ahead of A
 constexpr int kThreads = (2 + kWarps) * 32;
-constexpr uint32_t kColA = 0, kColA2 = 128, kColD = 256;
+// TMEM: A, A^2 or two D, B' (hi, lo), two X_c (hi, lo)
+constexpr uint32_t kColA = 0, kColA2 = 128, kColD = 128, kColB = 256, kColX = 384;
 
 struct SoloBars {
   uint64_t full[kRing];    // a chunk has been loaded
@@ -41,10 +50,12 @@ struct SoloBars {
   uint64_t used[kRing];    // the last product that reads the slot is done
   uint64_t stored[kRing];  // the slot has been copied out
   uint64_t dfull[2], dfree[2];
+  uint64_t xfree[2];       // the product that reads X_c in TMEM is done
   uint64_t afull, aready, a2full, bready;
+  uint64_t aimage;         // the team's A has been loaded
   uint64_t saved;          // a pass's chunks are in memory
-  uint64_t team;
-  uint64_t pair[4];        // the two warps of a quarter of the rows
+  uint64_t team, band;     // the team's CTAs; this CTA's band of the sum is in memory
+  uint64_t quad[4];        // the four warps of a quarter of the rows
   uint32_t tmem_slot;
   int abort;
 };
@@ -71,6 +82,7 @@ __global__ void __launch_bounds__(kThreads, 1) orth_solo_kernel(const OrthMat* m
       mbar_init(&bars.stored[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.xfree[i], 1);
       mbar_init(&bars.dfull[i], 1);
       mbar_init(&bars.dfree[i], kWarps);
     }
@@ -80,7 +92,9 @@ __global__ void __launch_bounds__(kThreads, 1) orth_solo_kernel(const OrthMat* m
     mbar_init(&bars.bready, kWarps);
     mbar_init(&bars.saved, 4);
     mbar_init(&bars.team, T * kWarps);
-    for (int i = 0; i < 4; ++i) mbar_init(&bars.pair[i], 2);
+    mbar_init(&bars.band, kWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars.quad[i], 4);
+    mbar_init(&bars.aimage, 1);
     bars.abort = 0;
     fence_mbar_init();
   }
@@ -118,50 +132,55 @@ __global__ void __launch_bounds__(kThreads, 1) orth_solo_kernel(const OrthMat* m
   } else if (warp == 1) {
     const int k16 = (q.m + 15) / 16;  // K = m and N = m, to 16
     const uint32_t ia = idesc_f16_f32(128, 16 * k16, 0, 0), id = idesc_f16_f32(128, 64, 0, 1);
-    const uint32_t sB = smem_u32(sm), sR = smem_u32(ring);
+    // operands by the low words of their descriptors (address and leading offset in
+    // 16 bytes; the high word is the same for all): one thread issues 36 MMAs a
+    // chunk, and what it computes for each counts
+    constexpr uint32_t kPlaneW = kOrthPlane / 16, kTileW = kOrthTile / 16;
+    const uint32_t sB = (smem_u32(sm) >> 4) | (1u << 16), sR = (smem_u32(ring) >> 4) | (1u << 16),
+                   sN = (smem_u32(ring) >> 4) | (512u << 16);  // MN-major: 8192 bytes between blocks of 64 columns
     uint32_t full = 0, ready = 0;
-    int dn = 0;  // accumulators D used
+    int dn = 0, xn = 0;  // accumulators D and operands X_c used
     bool go = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       go = go && __all_sync(0xffffffffu, mbar_wait(bar, parity, wc, abort));
       tc_fence_after();
       return go;
     };
-    // the three products of 16 of K; descriptors by plane
-    auto products = [&](uint32_t d, uint32_t a, uint32_t b, bool b_mn, uint32_t idesc, bool first) {
-      const uint64_t a0 = smem_desc(a, 16, 1024, 2), a1 = smem_desc(a + kOrthPlane, 16, 1024, 2);
-      const uint64_t b0 = b_mn ? smem_desc(b, 8192, 1024, 2) : smem_desc(b, 16, 1024, 2);
-      const uint64_t b1 = b_mn ? smem_desc(b + kOrthPlane, 8192, 1024, 2) : smem_desc(b + kOrthPlane, 16, 1024, 2);
-      mma_ss(d, a0, b0, idesc, first ? 0u : 1u);
-      mma_ss(d, a0, b1, idesc, 1u);
-      mma_ss(d, a1, b0, idesc, 1u);
+    auto products = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool first) {  // of 16 of K
+      mma_ss_w(d, a, b, idesc, first ? 0u : 1u);
+      mma_ss_w(d, a, b + kPlaneW, idesc, 1u);
+      mma_ss_w(d, a + kPlaneW, b, idesc, 1u);
     };
-    auto add_chunk = [&](int slot, bool first, bool last) {  // A += X_c X_c^T
-      if (elect_one()) {
-        const uint32_t x = sR + slot * kOrthTile;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) products(tmem + kColA, x + k * 32, x + k * 32, false, ia, first && k == 0);
-        mma_commit(&bars.used[slot]);
-        if (last) mma_commit(&bars.afull);
-      }
-      __syncwarp();
+    auto products_t = [&](uint32_t d, uint32_t a, uint32_t lo, uint32_t b, uint32_t idesc, bool first) {  // a in TMEM
+      mma_ts_w(d, a, b, idesc, first ? 0u : 1u);
+      mma_ts_w(d, a, b + kPlaneW, idesc, 1u);
+      mma_ts_w(d, a + lo, b, idesc, 1u);
     };
     int g = 0;
     for (int c = 0; c < nloc && go; ++c, ++g) {
       const int slot = g % kRing;
       if (!wait(&bars.full[slot], (full >> slot) & 1)) break;
       full ^= 1u << slot;
-      add_chunk(slot, c == 0, c == nloc - 1);
+      const uint32_t x = sR + slot * kTileW;
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) products(tmem + kColA, x + 2 * k, x + 2 * k, ia, c == 0 && k == 0);
+        mma_commit(&bars.used[slot]);
+        if (c == nloc - 1) mma_commit(&bars.afull);
+      }
+      __syncwarp();
     }
     if (nloc == 0 && elect_one()) mma_commit(&bars.afull);
     __syncwarp();
     for (int p = 1; p <= steps && go; ++p) {
-      if (!wait(&bars.aready, (p - 1) & 1)) break;
+      if (!wait(T > 1 ? &bars.aimage : &bars.aready, (p - 1) & 1)) break;
       if (elect_one()) {  // A^2: A is its own transposed
-        for (int k = 0; k < k16; ++k) {
-          const uint32_t at = sB + (k >> 2) * kOrthTile + (k & 3) * 32;
-          products(tmem + kColA2, at, at, false, ia, k == 0);
-        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < k16) {
+            const uint32_t at = sB + (k >> 2) * kTileW + (k & 3) * 2;
+            products(tmem + kColA2, at, at, ia, k == 0);
+          }
         mma_commit(&bars.a2full);
       }
       __syncwarp();
@@ -173,39 +192,49 @@ __global__ void __launch_bounds__(kThreads, 1) orth_solo_kernel(const OrthMat* m
         const int slot = slot_of(c);
         if (!wait(&bars.ready[slot], (ready >> slot) & 1)) return;
         ready ^= 1u << slot;
-        add_chunk(slot, c == 0, c == nloc - 1);
+        const uint32_t x = sR + slot * kTileW, at = tmem + kColX + 64 * (xn & 1);
+        if (elect_one()) {  // A += X_c X_c^T
+#pragma unroll
+          for (int k = 0; k < 4; ++k) products_t(tmem + kColA, at + 8 * k, 32, x + 2 * k, ia, c == 0 && k == 0);
+          mma_commit(&bars.used[slot]);
+          mma_commit(&bars.xfree[xn & 1]);
+          if (c == nloc - 1) mma_commit(&bars.afull);
+        }
+        __syncwarp();
+        ++xn;
       };
-      for (int c = 0; c < nloc && go; ++c, ++g) {
-        const int slot = slot_of(c), db = dn & 1;
-        if (!resident) {
-          if (!wait(&bars.full[slot], (full >> slot) & 1)) break;
-          full ^= 1u << slot;
+      for (int c = 0; c < nloc + (last ? 0 : kAhead) && go; ++c) {
+        if (c < nloc) {
+          const int slot = slot_of(c), db = dn & 1;
+          if (!resident) {
+            if (!wait(&bars.full[slot], (full >> slot) & 1)) break;
+            full ^= 1u << slot;
+          }
+          if (!wait(&bars.dfree[db], ((dn >> 1) & 1) ^ 1)) break;
+          const uint32_t x = sN + slot * kTileW, d = tmem + kColD + 64 * db;
+          if (elect_one()) {  // D = B' X_c, X_c [rows of K, 64 columns] as it lies
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k < k16) products_t(d, tmem + kColB + 8 * k, 64, x + k * 128, id, k == 0);
+            mma_commit(&bars.dfull[db]);
+            if (last) mma_commit(&bars.used[slot]);
+          }
+          __syncwarp();
+          ++dn;
+          ++g;
         }
-        if (!wait(&bars.dfree[db], ((dn >> 1) & 1) ^ 1)) break;
-        if (elect_one()) {  // D = B' X_c, X_c [rows of K, 64 columns] as it lies
-          const uint32_t x = sR + slot * kOrthTile;
-          for (int k = 0; k < k16; ++k)
-            products(tmem + kColD + 64 * db, sB + (k >> 2) * kOrthTile + (k & 3) * 32, x + k * 2048, true, id, k == 0);
-          mma_commit(&bars.dfull[db]);
-          if (last) mma_commit(&bars.used[slot]);
-        }
-        __syncwarp();
-        ++dn;
-        if (!last && c > 0) add_ready(c - 1);
+        if (!last && c >= kAhead) add_ready(c - kAhead);
       }
-      if (!last && go) {
-        if (nloc > 0) add_ready(nloc - 1);
-        else if (elect_one()) mma_commit(&bars.afull);
-        __syncwarp();
-      }
+      if (!last && go && nloc == 0 && elect_one()) mma_commit(&bars.afull);
+      __syncwarp();
     }
   } else {
-    const int quarter = warp & 3, half = (warp - 2) >> 2, r = quarter * 32 + lane;
+    const int quarter = warp & 3, part = (warp - 2) >> 2, r = quarter * 32 + lane;
     const int te = threadIdx.x - 64;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    constexpr float kBack = 1.f / kOrthScale;  // products carry the scale twice
+    constexpr float kBack = 1.f / kOrthScale, kBackA = kBack * kBack;  // A carries the scale twice
     uint32_t tphase = 0, pphase = 0;
-    int dn = 0, g = resident ? 0 : nloc, last_slot = -1;
+    int dn = 0, xn = 0, g = resident ? 0 : nloc, last_slot = -1;
     bool go = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       go = go && __all_sync(0xffffffffu, mbar_wait(bar, parity, wc, abort));
@@ -223,146 +252,178 @@ __global__ void __launch_bounds__(kThreads, 1) orth_solo_kernel(const OrthMat* m
       tphase ^= 1;
       return go;
     };
-    auto pair_sync = [&]() {
-      arrive(&bars.pair[quarter]);
-      go = go && __all_sync(0xffffffffu, mbar_wait(&bars.pair[quarter], pphase, wc, abort));
+    auto quad_sync = [&]() {
+      arrive(&bars.quad[quarter]);
+      go = go && __all_sync(0xffffffffu, mbar_wait(&bars.quad[quarter], pphase, wc, abort));
       pphase ^= 1;
       return go;
     };
-    uint8_t* const mine = sm + half * kOrthTile;  // this thread's 64 columns of A and B'
+    // this thread's 32 columns of A and B': half a tile
+    uint8_t* const mine = sm + (part >> 1) * kOrthTile;
+    const int ch0 = 4 * (part & 1);
+    // the team's exchange: [T] parts [32][128] of four columns, then A's image
+    uint8_t* const ex = tiles + static_cast<size_t>(q.a) * kOrthTile;
+    uint8_t* const image = ex + static_cast<size_t>(T) * kB;
     for (int p = 1; p <= steps; ++p) {
       const bool last = p == steps;
       // ---- A to shared memory: the CTA's own, or the team's sum
       if (!wait(&bars.afull, (p - 1) & 1)) break;
-      if (T == 1) {
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t v[32];
-          tmem_ld32_wait(lane_addr + kColA + 64 * half + 32 * h, v);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(v[8 * c + e]) * kBack;
-            uint4 hi, lo;
-            split8(y, hi, lo);
-            *reinterpret_cast<uint4*>(mine + sw128(r, 4 * h + c)) = hi;
-            *reinterpret_cast<uint4*>(mine + kOrthPlane + sw128(r, 4 * h + c)) = lo;
-          }
-        }
+      uint32_t v[32];
+      if (nloc > 0) {
+        tmem_ld32_wait(lane_addr + kColA + 32 * part, v);
       } else {
-        const int RL = 128 / T, band = kB / T;
-        if (!team_sync()) break;  // nobody reads its B' any more
-        const uint32_t to = cluster_addr(sm + rank * band, r / RL);
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t v[32];
-          if (nloc > 0) {
-            tmem_ld32_wait(lane_addr + kColA + 64 * half + 32 * h, v);
-          } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = 0u;
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            st_cluster_v4(to + ((half * 16 + h * 8 + k) * RL + r % RL) * 16,
-                          make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
-        }
-        if (!team_sync()) break;  // the band's parts are here
-        const int units = RL * 16;  // of eight columns
-        float y[4][8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int u = te + 256 * k;
-          if (u >= units) break;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[k][e] = 0.f;
-          for (int t = 0; t < T; ++t) {
-            const float4* f = reinterpret_cast<const float4*>(sm + t * band) + 2 * (u / RL) * RL + u % RL;
-            const float4 f0 = f[0], f1 = f[RL];
-            y[k][0] += f0.x;
-            y[k][1] += f0.y;
-            y[k][2] += f0.z;
-            y[k][3] += f0.w;
-            y[k][4] += f1.x;
-            y[k][5] += f1.y;
-            y[k][6] += f1.z;
-            y[k][7] += f1.w;
-          }
-        }
-        if (!team_sync()) break;  // and have been read: A takes their place
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int u = te + 256 * k;
-          if (u >= units) break;
-          const int row = rank * RL + u % RL, ch = u / RL;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[k][e] *= kBack;
-          uint4 hi, lo;
-          split8(y[k], hi, lo);
-          uint8_t* at = sm + (ch >> 3) * kOrthTile + sw128(row, ch & 7);
-          for (int t = 0; t < T; ++t) {
-            st_cluster_v4(cluster_addr(at, t), hi);
-            st_cluster_v4(cluster_addr(at + kOrthPlane, t), lo);
-          }
-        }
-        fence_proxy_async_all();
-        if (!team_sync()) break;
+        for (int e = 0; e < 32; ++e) v[e] = 0u;
       }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      arrive(&bars.aready);
-      // ---- B' = b A + c A^2 + a I over A
-      if (!wait(&bars.a2full, (p - 1) & 1)) break;
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        uint32_t v[32];
-        tmem_ld32_wait(lane_addr + kColA2 + 64 * half + 32 * h, v);
+      if (T == 1) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint4* ph = reinterpret_cast<uint4*>(mine + sw128(r, 4 * h + c));
-          uint4* pl = reinterpret_cast<uint4*>(mine + kOrthPlane + sw128(r, 4 * h + c));
           float y[8];
-          join8(*ph, *pl, y);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            y[e] = co.b * y[e] + co.c * (__uint_as_float(v[8 * c + e]) * kBack);
-            if (64 * half + 32 * h + 8 * c + e == r) y[e] += co.a * kOrthScale;
+          for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(v[8 * c + e]) * kBackA;
+          uint4 hi, lo;
+          split8(y, hi, lo);
+          *reinterpret_cast<uint4*>(mine + sw128(r, ch0 + c)) = hi;
+          *reinterpret_cast<uint4*>(mine + kOrthPlane + sw128(r, ch0 + c)) = lo;
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        arrive(&bars.aready);
+      } else {
+        uint4* out = reinterpret_cast<uint4*>(ex + static_cast<size_t>(rank) * kB);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          __stcg(out + (part * 8 + k) * 128 + r, make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+        tc_fence_before();
+        if (!team_sync()) break;  // the parts are there
+        const int RL = 128 / T;   // rows of the band
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int u = te + 32 * kWarps * k, row = rank * RL + u % RL, ch = u / RL;  // eight columns of a row
+          if (u >= RL * 16) break;
+          const float4* f = reinterpret_cast<const float4*>(ex) + 2 * ch * 128 + row;
+          float y[8];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // four columns, the parts' loads together
+            float4 part_of[8], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+              if (t < T) part_of[t] = __ldcg(f + t * (kB / 16) + h * 128);
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+              if (t < T) {
+                sum.x += part_of[t].x;
+                sum.y += part_of[t].y;
+                sum.z += part_of[t].z;
+                sum.w += part_of[t].w;
+              }
+            y[4 * h] = sum.x * kBackA;
+            y[4 * h + 1] = sum.y * kBackA;
+            y[4 * h + 2] = sum.z * kBackA;
+            y[4 * h + 3] = sum.w * kBackA;
           }
           uint4 hi, lo;
           split8(y, hi, lo);
-          *ph = hi;
-          *pl = lo;
+          uint8_t* at = image + (ch >> 3) * kOrthTile + sw128(row, ch & 7);
+          *reinterpret_cast<uint4*>(at) = hi;
+          *reinterpret_cast<uint4*>(at + kOrthPlane) = lo;
         }
+        fence_proxy_async_all();  // the band is read by bulk copies
+        arrive(&bars.band);
+        if (te == 0) {
+          mbar_expect_tx(&bars.aimage, kB);
+          if (mbar_wait(&bars.band, (p - 1) & 1, wc, abort)) {
+            fence_proxy_async_all();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // hi and lo of both tiles, to every CTA of the team
+              const int at = k * kOrthPlane + rank * RL * 128;
+              bulk_load_multicast(sm + at, image + at, RL * 128, &bars.aimage, (1u << T) - 1u);
+            }
+          }
+        }
+        __syncwarp();
+        if (!wait(&bars.aimage, (p - 1) & 1)) break;
       }
-      fence_proxy_async_smem();
+      // ---- B' = b A + c A^2 + a I
+      if (!wait(&bars.a2full, (p - 1) & 1)) break;
+#pragma unroll
+      for (int c2 = 0; c2 < 2; ++c2) {  // 16 columns
+        // A: this CTA's own is still in TMEM, the team's sum only in its image
+        uint32_t a2[16], a1[16], hi[8], lo[8];
+        tmem_ld16x2_wait(lane_addr + kColA2 + 32 * part + 16 * c2, a2, lane_addr + kColA + 32 * part + 16 * c2, a1);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float y[8];
+          if (T == 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(a1[8 * c + e]) * kBackA;
+          } else {
+            const uint8_t* at = mine + sw128(r, ch0 + 2 * c2 + c);
+            join8(*reinterpret_cast<const uint4*>(at), *reinterpret_cast<const uint4*>(at + kOrthPlane), y);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            y[e] = co.b * y[e] + co.c * __uint_as_float(a2[8 * c + e]);
+            if (32 * part + 16 * c2 + 8 * c + e == r) y[e] += co.a;
+          }
+          uint4 h, l;
+          split8(y, h, l);
+          hi[4 * c] = h.x;
+          hi[4 * c + 1] = h.y;
+          hi[4 * c + 2] = h.z;
+          hi[4 * c + 3] = h.w;
+          lo[4 * c] = l.x;
+          lo[4 * c + 1] = l.y;
+          lo[4 * c + 2] = l.z;
+          lo[4 * c + 3] = l.w;
+        }
+        tmem_st8(lane_addr + kColB + 16 * part + 8 * c2, hi);
+        tmem_st8(lane_addr + kColB + 64 + 16 * part + 8 * c2, lo);
+      }
+      tc_wait_st();
       tc_fence_before();
       arrive(&bars.bready);
       // ---- the chunks
       for (int c = 0; c < nloc; ++c, ++dn) {
         const int db = dn & 1, slot = resident ? c : (g + c) % kRing;
         if (!wait(&bars.dfull[db], (dn >> 1) & 1)) break;
-        uint32_t v[32];
-        tmem_ld32_wait(lane_addr + kColD + 64 * db + 32 * half, v);
+        uint32_t d[16];
+        tmem_ld16_wait(lane_addr + kColD + 64 * db + 16 * part, d);
         tc_fence_before();
         arrive(&bars.dfree[db]);
         uint8_t* x = ring + slot * kOrthTile;
         if (!last) {
+          uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 2; ++k) {
             float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(v[8 * k + e]) * kBack;
-            uint4 hi, lo;
-            split8(y, hi, lo);
-            *reinterpret_cast<uint4*>(x + sw128(r, 4 * half + k)) = hi;
-            *reinterpret_cast<uint4*>(x + kOrthPlane + sw128(r, 4 * half + k)) = lo;
+            for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(d[8 * k + e]);
+            uint4 h, l;
+            split8(y, h, l);
+            *reinterpret_cast<uint4*>(x + sw128(r, 2 * part + k)) = h;
+            *reinterpret_cast<uint4*>(x + kOrthPlane + sw128(r, 2 * part + k)) = l;
+            hi[4 * k] = h.x;
+            hi[4 * k + 1] = h.y;
+            hi[4 * k + 2] = h.z;
+            hi[4 * k + 3] = h.w;
+            lo[4 * k] = l.x;
+            lo[4 * k + 1] = l.y;
+            lo[4 * k + 2] = l.z;
+            lo[4 * k + 3] = l.w;
           }
+          if (!wait(&bars.xfree[xn & 1], ((xn >> 1) & 1) ^ 1)) break;
+          const uint32_t at = lane_addr + kColX + 64 * (xn & 1) + 8 * part;
+          tmem_st8(at, hi);
+          tmem_st8(at + 32, lo);
+          ++xn;
+          tc_wait_st();
           fence_proxy_async_smem();
+          tc_fence_before();
           arrive(&bars.ready[slot]);
           if (!resident) {
-            if (!pair_sync()) break;  // both halves of the quarter's rows
-            if (half == 0 && lane == 0) {
+            if (!quad_sync()) break;  // all columns of the quarter's rows
+            if (part == 0 && lane == 0) {
               if (last_slot >= 0) {
                 bulk_wait_read();
                 mbar_arrive(&bars.stored[last_slot]);
@@ -382,24 +443,24 @@ __global__ void __launch_bounds__(kThreads, 1) orth_solo_kernel(const OrthMat* m
         const int col0 = (c0 + c) * 64;
         if (q.flags & kOrthTall) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int col = col0 + 32 * half + e;
+          for (int e = 0; e < 16; ++e) {
+            const int col = col0 + 16 * part + e;
             if (r < q.m && col < q.n)
               dst[col * q.ld_dst + r] =
-                  static_cast<uint16_t>(pack_bf16x2(__uint_as_float(v[e]) * (kBack * kBack), 0.f) & 0xFFFFu);
+                  static_cast<uint16_t>(pack_bf16x2(__uint_as_float(d[e]) * kBack, 0.f) & 0xFFFFu);
           }
         } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 2; ++k) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16x2(__uint_as_float(v[8 * k + 2 * e]) * (kBack * kBack),
-                                 __uint_as_float(v[8 * k + 2 * e + 1]) * (kBack * kBack));
-            *reinterpret_cast<uint4*>(x + sw128(r, 4 * half + k)) = make_uint4(w[0], w[1], w[2], w[3]);
+              w[e] = pack_bf16x2(__uint_as_float(d[8 * k + 2 * e]) * kBack,
+                                 __uint_as_float(d[8 * k + 2 * e + 1]) * kBack);
+            *reinterpret_cast<uint4*>(x + sw128(r, 2 * part + k)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          if (!pair_sync()) break;
-          const int row0 = quarter * 32 + half * 16, rows = min(16, q.m - row0), cols = min(64, q.n - col0);
+          if (!quad_sync()) break;
+          const int row0 = quarter * 32 + part * 8, rows = min(8, q.m - row0), cols = min(64, q.n - col0);
           uint16_t* to = dst + row0 * q.ld_dst + col0;
           if (cols == 64 && (reinterpret_cast<uintptr_t>(to) & 15) == 0 && q.ld_dst % 8 == 0) {
             for (int e = lane; e < rows * 8; e += 32)
@@ -413,14 +474,14 @@ __global__ void __launch_bounds__(kThreads, 1) orth_solo_kernel(const OrthMat* m
         }
         if (!resident) {
           fence_proxy_async_smem();  // read before the next load writes it
-          if (!pair_sync()) break;
-          if (half == 0 && lane == 0) mbar_arrive(&bars.stored[slot]);
+          if (!quad_sync()) break;
+          if (part == 0 && lane == 0) mbar_arrive(&bars.stored[slot]);
         }
       }
       if (!go) break;
       if (!resident) {
         g += nloc;
-        if (!last && half == 0 && lane == 0) {
+        if (!last && part == 0 && lane == 0) {
           bulk_wait_all();
           fence_proxy_async_all();
           mbar_arrive(&bars.stored[last_slot]);

@@ -358,12 +358,36 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
 // workspace.
 struct Plan {
   std::vector<OrthMat> mats;
-  int solo = 0;
+  int solo = 0, team = 1;
   long long parts = 0, load_tiles = 0, sq = 0, mn = 0, tiles = 0;
   size_t part_off = 0, tiles_off = 0, total = 0;
 };
 
 bool dims_ok(const triattn_matrix& g) { return g.rows > 0 && g.cols > 0; }
+
+// CTAs per matrix of one row of tiles.  A CTA takes about 1.7 k cycles per chunk
+// of 64 columns and step, and 4 k (alone) or 7 k (in a team, which adds its parts
+// of A) between two passes; the list takes as long as its widest matrix or as its
+// sum spread over the SMs (clusters of eight leave some of a GPC's idle).
+int team_of(const OrthMat* q, int n) {
+  int best = 1;
+  double least = 0.0;
+  for (int t = 1; t <= 8; t *= 2) {
+    double widest = 0.0, sum = 0.0;
+    for (int k = 0; k < n; ++k) {
+      const int chunks = (q[k].n + 63) / 64;
+      const double c = 1.7 * ((chunks + t - 1) / t) + (t > 1 ? 7.0 : 4.0);
+      widest = std::max(widest, c);
+      sum += c * t;
+    }
+    const double time = std::max(widest, sum / (t == 8 ? 128 : 152));
+    if (t == 1 || time < least) {
+      best = t;
+      least = time;
+    }
+  }
+  return best;
+}
 
 // false: more than the kernels' 32-bit counts hold
 bool plan_of(const triattn_matrix* in, const triattn_matrix* out, long long n, Plan* p) {
@@ -390,6 +414,7 @@ bool plan_of(const triattn_matrix* in, const triattn_matrix* out, long long n, P
   const auto others = std::stable_partition(p->mats.begin(), p->mats.end(), [](const OrthMat& q) { return q.mt == 1; });
   p->solo = static_cast<int>(others - p->mats.begin());
   std::stable_sort(p->mats.begin(), others, [](const OrthMat& x, const OrthMat& y) { return x.n > y.n; });
+  p->team = team_of(p->mats.data(), p->solo);
   for (OrthMat& q : p->mats) {
     const long long xt = 2ll * q.mt * q.nt, at = 2ll * q.mt * q.mt;
     q.part0 = static_cast<int>(p->parts);
@@ -408,6 +433,9 @@ bool plan_of(const triattn_matrix* in, const triattn_matrix* out, long long n, P
       q.a2 = static_cast<int>(p->tiles + xt + at);
       q.b = static_cast<int>(p->tiles + xt + 2 * at);
       p->tiles += xt + 3 * at;
+    } else if (p->team > 1) {
+      q.a = static_cast<int>(p->tiles);
+      p->tiles += 2 * (p->team + 1);
     }
     if (p->tiles >= (1ll << 31) || p->parts >= (1ll << 31)) return false;
   }
@@ -416,30 +444,6 @@ bool plan_of(const triattn_matrix* in, const triattn_matrix* out, long long n, P
   p->tiles_off = up(p->part_off + static_cast<size_t>(p->parts) * 4);
   p->total = p->tiles_off + static_cast<size_t>(p->tiles) * kOrthTile;
   return true;
-}
-
-// CTAs per matrix of one row of tiles.  A CTA takes about 1.7 k cycles per chunk
-// of 64 columns and step, and 4 k (alone) or 7 k (in a team, which adds its parts
-// of A) between two passes; the list takes as long as its widest matrix or as its
-// sum spread over the SMs (clusters of eight leave some of a GPC's idle).
-int team_of(const OrthMat* q, int n) {
-  int best = 1;
-  double least = 0.0;
-  for (int t = 1; t <= 8; t *= 2) {
-    double widest = 0.0, sum = 0.0;
-    for (int k = 0; k < n; ++k) {
-      const int chunks = (q[k].n + 63) / 64;
-      const double c = 1.7 * ((chunks + t - 1) / t) + (t > 1 ? 7.0 : 4.0);
-      widest = std::max(widest, c);
-      sum += c * t;
-    }
-    const double time = std::max(widest, sum / (t == 8 ? 128 : 152));
-    if (t == 1 || time < least) {
-      best = t;
-      least = time;
-    }
-  }
-  return best;
 }
 
 constexpr long long kMaxSide = 65536;
@@ -496,7 +500,7 @@ cudaError_t run(const Plan& p, int steps, const float* co, float eps, uint8_t* w
   if (p.solo > 0 && e == cudaSuccess)
     e = trace_call(kKOrthSolo, s, [&] {
       return launch_orth_solo(mats, p.solo, v.tiles, steps, OrthCoef{co[0], co[1], co[2]},
-                              team_of(p.mats.data(), p.solo), wc, s);
+                              p.team, wc, s);
     });
   v.mat += p.solo;
   v.n -= p.solo;

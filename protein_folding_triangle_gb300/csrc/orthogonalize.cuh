@@ -21,7 +21,7 @@ struct OrthMat {
   int m, n;                  // X
   int flags;                 // kOrthFp32: the source is FP32; kOrthTall: X is the transposed matrix
   int mt, nt;                // 128-row and 128-column tiles of X
-  int x[2], a, a2, b;        // tiles of X (two copies), A, A', B'
+  int x[2], a, a2, b;        // tiles of X (two copies), A, A', B'; a team's: X, and 2 (team + 1) at a
   int parts, part0;          // partial sums of squares
   int part_rows;             // rows of the source per partial sum
   int tiles0, sq0, mn0;      // tiles (128 x 64) of X, 128 x 128 tiles of A and of X before this matrix
@@ -38,16 +38,17 @@ __device__ __forceinline__ uint8_t* tile_at(const OrthView& v, int t) {
   return v.tiles + static_cast<size_t>(t) * kOrthTile;
 }
 
-// Eight scaled values as FP16 pairs, one 16-byte piece of each plane.
+// Eight scaled values as FP16 pairs, one 16-byte piece of each plane: hi is the
+// value's leading 11 bits (cut off, so that no conversion back is needed), lo the
+// rest rounded.
 __device__ __forceinline__ void split8(const float* y, uint4& hi, uint4& lo) {
   uint32_t h[4], l[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const __half2 a = __floats2half2_rn(y[2 * e], y[2 * e + 1]);
-    const float2 f = __half22float2(a);
-    const __half2 b = __floats2half2_rn(y[2 * e] - f.x, y[2 * e + 1] - f.y);
-    h[e] = *reinterpret_cast<const uint32_t*>(&a);
-    l[e] = *reinterpret_cast<const uint32_t*>(&b);
+    const float a = __uint_as_float(__float_as_uint(y[2 * e]) & 0xFFFFE000u);
+    const float b = __uint_as_float(__float_as_uint(y[2 * e + 1]) & 0xFFFFE000u);
+    h[e] = pack_f16x2(a, b);
+    l[e] = pack_f16x2(y[2 * e] - a, y[2 * e + 1] - b);
   }
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
