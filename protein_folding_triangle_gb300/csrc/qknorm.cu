@@ -26,7 +26,6 @@ namespace triattn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPairs = 8;  // pairs of features per thread
 
 struct QkArgs {
   const uint16_t* x[2];   // q, k
@@ -56,43 +55,43 @@ __device__ __forceinline__ void row_of(const QkArgs& a, int j, int& h, int& n) {
   }
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// The thread's two 16-byte pieces as four pairs of (a, b) values, two pairs to a
+// packed operation: a[i] holds the first features of pairs 2 i and 2 i + 1, b[i]
+// the second ones.  SPLIT: the pieces are the same place of both halves of the
+// row; otherwise they are neighbours and a pair's features too.
+template <bool SPLIT>
+__device__ __forceinline__ void to_pairs(const uint4& lo, const uint4& hi, float2 (&a)[4], float2 (&b)[4]) {
+  const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16lo_to_f32(w[i]);
-    f[2 * i + 1] = bf16hi_to_f32(w[i]);
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
-}
-
-// The thread's two 16-byte pieces as pairs (a, b): the same place of both
-// halves of the row (HALF), or neighbours.
-template <bool SPLIT>
-__device__ __forceinline__ void to_pairs(const uint4& lo, const uint4& hi, float (&a)[kPairs], float (&b)[kPairs]) {
-  float f0[8], f1[8];
-  unpack8(lo, f0);
-  unpack8(hi, f1);
-#pragma unroll
-  for (int i = 0; i < kPairs; ++i) {
-    a[i] = SPLIT ? f0[i] : (i < 4 ? f0[(2 * i) & 7] : f1[(2 * i) & 7]);
-    b[i] = SPLIT ? f1[i] : (i < 4 ? f0[(2 * i + 1) & 7] : f1[(2 * i + 1) & 7]);
+    if constexpr (SPLIT) {
+      a[i] = make_float2(bf16lo_to_f32(l[i]), bf16hi_to_f32(l[i]));
+      b[i] = make_float2(bf16lo_to_f32(h[i]), bf16hi_to_f32(h[i]));
+    } else {
+      const uint32_t u = i < 2 ? l[(2 * i) & 3] : h[(2 * i) & 3], v = i < 2 ? l[(2 * i + 1) & 3] : h[(2 * i + 1) & 3];
+      a[i] = make_float2(bf16lo_to_f32(u), bf16lo_to_f32(v));
+      b[i] = make_float2(bf16hi_to_f32(u), bf16hi_to_f32(v));
+    }
   }
 }
 template <bool SPLIT>
-__device__ __forceinline__ void from_pairs(const float (&a)[kPairs], const float (&b)[kPairs], uint4& lo, uint4& hi) {
-  float f0[8], f1[8];
+__device__ __forceinline__ void from_pairs(const float2 (&a)[4], const float2 (&b)[4], uint4& lo, uint4& hi) {
+  uint32_t l[4], h[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    f0[i] = SPLIT ? a[i] : ((i & 1) ? b[i / 2] : a[i / 2]);
-    f1[i] = SPLIT ? b[i] : ((i & 1) ? b[4 + i / 2] : a[4 + i / 2]);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (SPLIT) {
+      l[i] = pack_bf16x2(a[i].x, a[i].y);
+      h[i] = pack_bf16x2(b[i].x, b[i].y);
+    } else {
+      (i < 2 ? l : h)[(2 * i) & 3] = pack_bf16x2(a[i].x, b[i].x);
+      (i < 2 ? l : h)[(2 * i + 1) & 3] = pack_bf16x2(a[i].y, b[i].y);
+    }
   }
-  lo = pack8(f0);
-  hi = pack8(f1);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
 }
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 neg(float2 x) { return make_float2(-x.x, -x.y); }
 
 // cos and sin of position times frequency.  The angle is a whole number of
 // 2^-64 turns, so the product wraps to the turn's fraction exactly and a far
@@ -115,7 +114,7 @@ struct Place {
   int h, n, b, lo, hi;                            // head, token, example, elements of the two pieces
   bool live;
   __device__ __forceinline__ Place(const QkArgs& a) {
-    const int j = blockIdx.x * kRows + threadIdx.x / kPer, part = threadIdx.x % kPer;
+    const int j = (blockIdx.x >> 1) * kRows + threadIdx.x / kPer, part = threadIdx.x % kPer;
     live = j < a.HN;
     row_of(a, live ? j : 0, h, n);
     b = blockIdx.y / a.cpb;
@@ -123,42 +122,49 @@ struct Place {
     hi = kSplit ? D / 2 + 8 * part : lo + 8;
   }
   __device__ __forceinline__ int pair(int i) const { return (kSplit ? lo : lo / 2) + i; }
-  __device__ __forceinline__ void weights(const QkArgs& a, const float* w, float (&wa)[kPairs],
-                                          float (&wb)[kPairs]) const {
+  // features of pair i of the thread's eight
+  __device__ __forceinline__ int first(int i) const { return kSplit ? lo + i : lo + 2 * i; }
+  __device__ __forceinline__ int second(int i) const { return kSplit ? hi + i : lo + 2 * i + 1; }
+  __device__ __forceinline__ void weights(const QkArgs& a, const float* w, float2 (&wa)[4], float2 (&wb)[4]) const {
     const float* p = w + (a.w_heads > 1 ? static_cast<size_t>(h) * D : 0);
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      wa[i] = __ldg(p + (kSplit ? lo + i : lo + 2 * i));
-      wb[i] = __ldg(p + (kSplit ? hi + i : lo + 2 * i + 1));
+    for (int i = 0; i < 4; ++i) {
+      wa[i] = make_float2(__ldg(p + first(2 * i)), __ldg(p + first(2 * i + 1)));
+      wb[i] = make_float2(__ldg(p + second(2 * i)), __ldg(p + second(2 * i + 1)));
     }
   }
-  __device__ __forceinline__ void turns(const QkArgs& a, float (&c)[kPairs], float (&s)[kPairs]) const {
+  __device__ __forceinline__ void turns(const QkArgs& a, float2 (&c)[4], float2 (&s)[4]) const {
     const int p = a.pos != nullptr ? __ldg(a.pos + static_cast<size_t>(b) * a.N + n) : n;
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) angle(p, a.freq[pair(i)], c[i], s[i]);
+    for (int i = 0; i < 4; ++i) {
+      angle(p, a.freq[pair(2 * i)], c[i].x, s[i].x);
+      angle(p, a.freq[pair(2 * i + 1)], c[i].y, s[i].y);
+    }
   }
 };
 
+// Blocks of q and k alternate, so that both parts of a pair row are read at
+// about the same time.
 template <int D, int ROT>
 __global__ void __launch_bounds__(kThreads, 2) qk_norm_fwd_kernel(const QkArgs a) {
   constexpr int U = 4;  // slices in flight
   using P = Place<D, ROT>;
   const P at(a);
-  const int m = blockIdx.z;
+  const int m = blockIdx.x & 1;
   const uint16_t* x = m ? a.x[1] : a.x[0];
   uint16_t* y = m ? a.y[1] : a.y[0];
   // y_a = r (x_a ac - x_b bs),  y_b = r (x_a as + x_b bc): weights and rotation in one
-  float ac[kPairs], bs[kPairs], as[kPairs], bc[kPairs];
+  float2 ac[4], bs[4], as[4], bc[4];
   at.weights(a, m ? a.w[1] : a.w[0], ac, bc);
   if constexpr (ROT != TRIATTN_ROTARY_NONE) {
-    float c[kPairs], s[kPairs];
+    float2 c[4], s[4];
     at.turns(a, c, s);
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      as[i] = ac[i] * s[i];
-      bs[i] = bc[i] * s[i];
-      ac[i] *= c[i];
-      bc[i] *= c[i];
+    for (int i = 0; i < 4; ++i) {
+      as[i] = fmul2(ac[i], s[i]);
+      bs[i] = neg(fmul2(bc[i], s[i]));
+      ac[i] = fmul2(ac[i], c[i]);
+      bc[i] = fmul2(bc[i], c[i]);
     }
   }
   const int o0 = (blockIdx.y % a.cpb) * a.per, o1 = min(o0 + a.per, a.N_o);
@@ -173,16 +179,16 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_fwd_kernel(const QkArgs a
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      float xa[kPairs], xb[kPairs], ss = 0.f;
+      float2 xa[4], xb[4], ss = splat(0.f);
       to_pairs<P::kSplit>(lo[k], hi[k], xa, xb);
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
-      const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
+      for (int i = 0; i < 4; ++i) ss = ffma2(xa[i], xa[i], ffma2(xb[i], xb[i], ss));
+      const float2 r = splat(rsqrtf(row_sum<D>(ss.x + ss.y) * (1.f / D) + a.eps));
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        const float ra = r * xa[i], rb = r * xb[i];
-        xa[i] = ROT != TRIATTN_ROTARY_NONE ? ra * ac[i] - rb * bs[i] : ra * ac[i];
-        xb[i] = ROT != TRIATTN_ROTARY_NONE ? ra * as[i] + rb * bc[i] : rb * bc[i];
+      for (int i = 0; i < 4; ++i) {
+        const float2 ra = fmul2(r, xa[i]), rb = fmul2(r, xb[i]);
+        xa[i] = ROT != TRIATTN_ROTARY_NONE ? ffma2(ra, ac[i], fmul2(rb, bs[i])) : fmul2(ra, ac[i]);
+        xb[i] = ROT != TRIATTN_ROTARY_NONE ? ffma2(ra, as[i], fmul2(rb, bc[i])) : fmul2(rb, bc[i]);
       }
       if (at.live && o + k < o1) {
         uint16_t* p = y + (static_cast<long long>(at.b) * a.N_o + o + k) * a.ly.slice + ys;
@@ -202,15 +208,15 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_bwd_kernel(const QkArgs a
   __shared__ float sums[P::kRows][D + 1];
   __shared__ float parts[kThreads];
   const P at(a);
-  const int m = blockIdx.z;
+  const int m = blockIdx.x & 1, tile = blockIdx.x >> 1;
   const uint16_t* x = m ? a.x[1] : a.x[0];
   const uint16_t* dy = m ? a.dy[1] : a.dy[0];  // may be dx: read by plain loads, a piece before it is written
   uint16_t* dx = m ? a.y[1] : a.y[0];
-  float wa[kPairs], wb[kPairs], c[kPairs], s[kPairs], da[kPairs], db[kPairs];
+  float2 wa[4], wb[4], c[4], s[4], da[4], db[4];
   at.weights(a, m ? a.w[1] : a.w[0], wa, wb);
   if constexpr (ROT != TRIATTN_ROTARY_NONE) at.turns(a, c, s);
 #pragma unroll
-  for (int i = 0; i < kPairs; ++i) da[i] = db[i] = 0.f;
+  for (int i = 0; i < 4; ++i) da[i] = db[i] = splat(0.f);
   const int o0 = (blockIdx.y % a.cpb) * a.per, o1 = min(o0 + a.per, a.N_o);
   const long long xs = at.h * a.lx.head + at.n * a.lx.row, gs = at.h * a.ldy.head + at.n * a.ldy.row,
                   ys = at.h * a.ly.head + at.n * a.ly.row;
@@ -228,35 +234,34 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_bwd_kernel(const QkArgs a
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      float xa[kPairs], xb[kPairs], ga[kPairs], gb[kPairs], ss = 0.f, dot = 0.f;
+      float2 xa[4], xb[4], ga[4], gb[4], ss = splat(0.f), dot = splat(0.f);
       to_pairs<P::kSplit>(lo[k], hi[k], xa, xb);
       to_pairs<P::kSplit>(gl[k], gh[k], ga, gb);
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
-      const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
+      for (int i = 0; i < 4; ++i) ss = ffma2(xa[i], xa[i], ffma2(xb[i], xb[i], ss));
+      const float r = rsqrtf(row_sum<D>(ss.x + ss.y) * (1.f / D) + a.eps);
       const bool live = at.live && o + k < o1;
+      const float2 rl = splat(live ? r : 0.f);  // a row that is not there adds nothing to dw
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
+      for (int i = 0; i < 4; ++i) {
         if constexpr (ROT != TRIATTN_ROTARY_NONE) {  // back by the angle
-          const float t = ga[i];
-          ga[i] = t * c[i] + gb[i] * s[i];
-          gb[i] = gb[i] * c[i] - t * s[i];
+          const float2 t = ga[i];
+          ga[i] = ffma2(gb[i], s[i], fmul2(t, c[i]));
+          gb[i] = ffma2(neg(t), s[i], fmul2(gb[i], c[i]));
         }
-        xa[i] *= r;  // n
-        xb[i] *= r;
-        if (live) {
-          da[i] += ga[i] * xa[i];
-          db[i] += gb[i] * xb[i];
-        }
-        ga[i] *= wa[i];
-        gb[i] *= wb[i];
-        dot += ga[i] * xa[i] + gb[i] * xb[i];
+        const float2 ua = fmul2(ga[i], xa[i]), ub = fmul2(gb[i], xb[i]);
+        da[i] = ffma2(ua, rl, da[i]);
+        db[i] = ffma2(ub, rl, db[i]);
+        dot = ffma2(ua, wa[i], ffma2(ub, wb[i], dot));
+        ga[i] = fmul2(ga[i], wa[i]);
+        gb[i] = fmul2(gb[i], wb[i]);
       }
-      dot = row_sum<D>(dot) * (1.f / D);
+      // dx = r (a - n mean(a n)) = r a - x r^3 mean(a x)
+      const float2 f = splat(-(r * r) * (r * (1.f / D) * row_sum<D>(dot.x + dot.y))), rr = splat(r);
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        xa[i] = r * (ga[i] - xa[i] * dot);
-        xb[i] = r * (gb[i] - xb[i] * dot);
+      for (int i = 0; i < 4; ++i) {
+        xa[i] = ffma2(xa[i], f, fmul2(ga[i], rr));
+        xb[i] = ffma2(xb[i], f, fmul2(gb[i], rr));
       }
       if (live) {
         uint16_t* p = dx + (static_cast<long long>(at.b) * a.N_o + o + k) * a.ly.slice + ys;
@@ -267,71 +272,83 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_bwd_kernel(const QkArgs a
       }
     }
   }
-  // the block's sums by head, rows added in a fixed order
+  // the block's sums by head, rows added in a fixed order: thread (part, slot, feature)
   const int row = threadIdx.x / P::kPer;
 #pragma unroll
-  for (int i = 0; i < kPairs; ++i) {
-    sums[row][P::kSplit ? at.lo + i : at.lo + 2 * i] = da[i];
-    sums[row][P::kSplit ? at.hi + i : at.lo + 2 * i + 1] = db[i];
+  for (int i = 0; i < 4; ++i) {
+    sums[row][at.first(2 * i)] = da[i].x;
+    sums[row][at.first(2 * i + 1)] = da[i].y;
+    sums[row][at.second(2 * i)] = db[i].x;
+    sums[row][at.second(2 * i + 1)] = db[i].y;
   }
-  const int j0 = blockIdx.x * P::kRows, last = static_cast<int>(min(static_cast<long long>(P::kRows), a.HN - j0));
-  const int d = threadIdx.x % D, part = threadIdx.x / D;
-  constexpr int kParts = kThreads / D;
-  float* out = a.part + ((static_cast<size_t>(m) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * a.slots * D;
-  for (int sl = 0; sl < a.slots; ++sl) {
+  __syncthreads();
+  const long long j0 = static_cast<long long>(tile) * P::kRows;
+  const int last = static_cast<int>(min(static_cast<long long>(P::kRows), a.HN - j0));
+  const int cells = a.slots * D, np = max(1, kThreads / cells);
+  float* out = a.part + ((static_cast<size_t>(m) * gridDim.y + blockIdx.y) * (gridDim.x >> 1) + tile) * cells;
+  for (int e = threadIdx.x; e < np * cells; e += np > 1 ? np * cells : kThreads) {
+    const int part = e / cells, cell = e - part * cells, sl = cell / D, d = cell - sl * D;
     // rows of the slot: every H-th (heads in a row), or those of one head in sequence
     int first, end, step;
     if (a.lx.hn) {
-      first = sl;
+      first = a.slots == a.H ? static_cast<int>((sl + a.H - j0 % a.H) % a.H) : sl;
       end = last;
       step = a.H;
     } else {
-      const int head = j0 / a.N + sl;
-      first = static_cast<int>(max(0ll, static_cast<long long>(head) * a.N - j0));
-      end = static_cast<int>(min(static_cast<long long>(last), (head + 1ll) * a.N - j0));
+      const long long h0 = (j0 / a.N + sl) * a.N - j0;
+      first = static_cast<int>(max(0ll, h0));
+      end = static_cast<int>(min(static_cast<long long>(last), h0 + a.N));
       step = 1;
     }
-    __syncthreads();
     float v = 0.f;
-    for (int rr = first + part * step; rr < end; rr += kParts * step) v += sums[rr][d];
-    parts[threadIdx.x] = v;
+    for (int rr = first + part * step; rr < end; rr += np * step) v += sums[rr][d];
+    if (np > 1) parts[e] = v;
+    else out[cell] = v;
+  }
+  if (np > 1) {
     __syncthreads();
-    if (threadIdx.x < D) {
-      v = 0.f;
-#pragma unroll
-      for (int p = 0; p < kParts; ++p) v += parts[p * D + threadIdx.x];
-      out[sl * D + threadIdx.x] = v;
+    if (threadIdx.x < cells) {
+      float v = 0.f;
+      for (int p = 0; p < np; ++p) v += parts[p * cells + threadIdx.x];
+      out[threadIdx.x] = v;
     }
   }
 }
 
 // dw[h][d] (or dw[d], all heads) from the blocks' partial sums, in a fixed order.
+// Partials [chunks][tiles][slots][D]: with the heads in a row a slot is a head
+// (the j0 + slot-th where a tile does not hold all of them), otherwise the
+// slot-th head of the tile.
 __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* __restrict__ part, float* __restrict__ dwq,
                                                           float* __restrict__ dwk, int D, int rows, int tiles,
                                                           int chunks, int slots, int H, int N, int w_heads, int hn) {
   __shared__ double sh[1024];
   const int d = threadIdx.x % D, lane = threadIdx.x / D, lanes = 1024 / D;
-  const float* p = part + static_cast<size_t>(blockIdx.y) * chunks * tiles * slots * D;
-  const int h0 = w_heads > 1 ? blockIdx.x : 0, h1 = w_heads > 1 ? h0 + 1 : H;
+  const float* p = part + static_cast<size_t>(blockIdx.y) * chunks * tiles * slots * D + d;
+  const int h = blockIdx.x;
   double v = 0.0;
-  for (int h = h0; h < h1; ++h) {
+  if (w_heads == 1) {  // everything
+    const int n = chunks * tiles * slots;
+#pragma unroll 4
+    for (int e = lane; e < n; e += lanes) v += p[static_cast<size_t>(e) * D];
+  } else {
     const int t0 = hn ? 0 : static_cast<int>(static_cast<long long>(h) * N / rows);
-    const int t1 = hn ? tiles : static_cast<int>(((h + 1ll) * N - 1) / rows) + 1;
-    const int nt = t1 - t0;
+    const int nt = (hn ? tiles : static_cast<int>(((h + 1ll) * N - 1) / rows) + 1) - t0;
+#pragma unroll 4
     for (int e = lane; e < nt * chunks; e += lanes) {
-      const int t = t0 + e % nt, ch = e / nt;
-      const long long j0 = static_cast<long long>(t) * rows;
-      const int sl = hn ? static_cast<int>((h + H - j0 % H) % H) : h - static_cast<int>(j0 / N);
-      if (sl < slots) v += p[((static_cast<size_t>(ch) * tiles + t) * slots + sl) * D + d];
+      const int ch = e / nt, t = t0 + e - ch * nt;
+      int sl = h;
+      if (!hn) sl = h - static_cast<int>(static_cast<long long>(t) * rows / N);
+      else if (slots < H) sl = static_cast<int>((h + H - static_cast<long long>(t) * rows % H) % H);
+      if (sl < slots) v += p[((static_cast<size_t>(ch) * tiles + t) * slots + sl) * D];
     }
   }
   sh[threadIdx.x] = v;
-  __syncthreads();
-  if (threadIdx.x < D) {
-    v = 0.0;
-    for (int l = 0; l < lanes; ++l) v += sh[l * D + threadIdx.x];
-    (blockIdx.y ? dwk : dwq)[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] = static_cast<float>(v);
+  for (int o = lanes / 2; o > 0; o /= 2) {
+    __syncthreads();
+    if (lane < o) sh[threadIdx.x] += sh[threadIdx.x + o * D];
   }
+  if (lane == 0) (blockIdx.y ? dwk : dwq)[static_cast<size_t>(h) * D + d] = static_cast<float>(sh[threadIdx.x]);
 }
 
 struct Plan {
@@ -340,14 +357,15 @@ struct Plan {
 };
 
 // Blocks: a tile of rows of a slice times a run of slices, about `waves` times
-// what the GPU holds at once (two blocks an SM).
-Plan plan_of(const triattn_qk_norm_shape* s, bool hn, int waves) {
+// what the GPU holds at once (two blocks an SM), but runs of at least `least`
+// slices: what a block does before and after them takes as long as about that many.
+Plan plan_of(const triattn_qk_norm_shape* s, bool hn, int waves, int least) {
   Plan p;
   p.rows = kThreads / (s->D / 16);
   const long long HN = static_cast<long long>(s->H) * s->N;
   p.tiles = static_cast<int>((HN + p.rows - 1) / p.rows);
   const long long base = 2ll * p.tiles * s->B, want = 152ll * 2 * waves;
-  long long cpb = std::max(1ll, std::min<long long>(want / base, s->N_o));
+  long long cpb = std::max(1ll, std::min<long long>(want / base, s->N_o / least));
   cpb = std::min(cpb, 65535ll / s->B);
   p.per = static_cast<int>((s->N_o + cpb - 1) / cpb);
   p.cpb = (s->N_o + p.per - 1) / p.per;
@@ -356,7 +374,8 @@ Plan plan_of(const triattn_qk_norm_shape* s, bool hn, int waves) {
   p.part_bytes = 2ull * p.chunks * p.tiles * p.slots * s->D * 4;
   return p;
 }
-constexpr int kFwdWaves = 4, kBwdWaves = 2;
+Plan fwd_plan(const triattn_qk_norm_shape* s, bool hn) { return plan_of(s, hn, 4, 4); }
+Plan bwd_plan(const triattn_qk_norm_shape* s, bool hn) { return plan_of(s, hn, 2, 8); }
 
 triattn_status check(const triattn_qk_norm_shape* s, triattn_shape* core) {
   if (s == nullptr || s->B < 1 || s->N_o < 1 || s->N < 1 || s->H < 1 || s->D < 1 || s->flags != 0)
@@ -432,7 +451,7 @@ size_t triattn_qk_norm_workspace_bytes(const triattn_qk_norm_shape* shape) {
   triattn_shape core;
   if (check(shape, &core) != TRIATTN_OK) return 0;
   // the larger of the two orders of rows
-  return (std::max(plan_of(shape, true, kBwdWaves).part_bytes, plan_of(shape, false, kBwdWaves).part_bytes) + 255) /
+  return (std::max(bwd_plan(shape, true).part_bytes, bwd_plan(shape, false).part_bytes) + 255) /
          256 * 256;
 }
 
@@ -449,14 +468,14 @@ triattn_status triattn_qk_norm_fwd(const triattn_qk_norm_shape* shape, const voi
   for (const void* p : {q, k, static_cast<const void*>(q_out), static_cast<const void*>(k_out)})
     if (!al(p, 16)) return TRIATTN_ERR_INVALID_ARG;
   if (!al(w_q, 4) || !al(w_k, 4) || (positions != nullptr && !al(positions, 4))) return TRIATTN_ERR_INVALID_ARG;
-  const Plan p = plan_of(shape, lx.hn != 0, kFwdWaves);
+  const Plan p = fwd_plan(shape, lx.hn != 0);
   QkArgs a = args_of(shape, p, lx, ly, w_q, w_k, positions);
   a.x[0] = static_cast<const uint16_t*>(q);
   a.x[1] = static_cast<const uint16_t*>(k);
   a.y[0] = static_cast<uint16_t*>(q_out);
   a.y[1] = static_cast<uint16_t*>(k_out);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid(p.tiles, p.chunks, 2);
+  const dim3 grid(2 * p.tiles, p.chunks);
   return trace_call(kKQkFwd, s, [&] { return dispatch(shape, a, grid, false, s); }) == cudaSuccess ? TRIATTN_OK
                                                                                                     : TRIATTN_ERR_CUDA;
 }
@@ -480,7 +499,7 @@ triattn_status triattn_qk_norm_bwd(const triattn_qk_norm_shape* shape, const voi
     if (!al(p, 4)) return TRIATTN_ERR_INVALID_ARG;
   if (positions != nullptr && !al(positions, 4)) return TRIATTN_ERR_INVALID_ARG;
   if (!al(workspace, 256) || workspace_bytes < triattn_qk_norm_workspace_bytes(shape)) return TRIATTN_ERR_WORKSPACE;
-  const Plan p = plan_of(shape, lx.hn != 0, kBwdWaves);
+  const Plan p = bwd_plan(shape, lx.hn != 0);
   QkArgs a = args_of(shape, p, lx, ly, w_q, w_k, positions);
   a.ldy = ldy;
   a.x[0] = static_cast<const uint16_t*>(q);
@@ -491,7 +510,7 @@ triattn_status triattn_qk_norm_bwd(const triattn_qk_norm_shape* shape, const voi
   a.y[1] = static_cast<uint16_t*>(dk);
   a.part = static_cast<float*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid(p.tiles, p.chunks, 2);
+  const dim3 grid(2 * p.tiles, p.chunks);
   cudaError_t e = trace_call(kKQkBwd, s, [&] { return dispatch(shape, a, grid, true, s); });
   if (e == cudaSuccess)
     e = trace_call(kKQkDw, s, [&] {

@@ -123,50 +123,59 @@ __global__ void __launch_bounds__(kThreads) relpos_heads_fwd_kernel(const __grid
 }
 
 // ------------------------------------------------ pair features, forward
-// Block: a run of rows (b, i); thread: eight features of every (blockDim /
-// (F / 8))-th pair of the row, four in flight.  The table comes from L1.
-__global__ void __launch_bounds__(kThreads) relpos_pairs_fwd_kernel(const __grid_constant__ RelposArgs a, int rows) {
-  constexpr int U = 4;
+// Block: a run of segments of a row (b, i), as many as any other block's or one
+// more; thread: eight features of four pairs of a segment, all four in flight.
+// The table comes from L1.
+constexpr int kPairsU = 4;
+int pairs_threads(int F) { return kThreads / (F / 8) * (F / 8); }
+int pairs_segment(int F) { return kPairsU * (kThreads / (F / 8)); }
+__global__ void __launch_bounds__(kThreads) relpos_pairs_fwd_kernel(const __grid_constant__ RelposArgs a) {
+  constexpr int U = kPairsU;
   __shared__ uint8_t lut[2 * kRelposMaxDistance + 1];
   for (int d = threadIdx.x; d <= 2 * a.R; d += blockDim.x) lut[d] = a.lut[d];
   __syncthreads();
-  const int per = a.F / 8, f = (threadIdx.x % per) * 8, j0 = threadIdx.x / per, step = blockDim.x / per;
-  const long long r0 = static_cast<long long>(blockIdx.x) * rows;
-  const long long r1 = min(r0 + rows, static_cast<long long>(a.B) * a.N);
-  for (long long r = r0; r < r1; ++r) {
+  const int per = a.F / 8, f = (threadIdx.x % per) * 8, jt = threadIdx.x / per, step = blockDim.x / per;
+  const int len = U * step, segs = (a.N + len - 1) / len;
+  const long long all = static_cast<long long>(a.B) * a.N * segs;
+  const long long s0 = all * blockIdx.x / gridDim.x, s1 = all * (blockIdx.x + 1) / gridDim.x;
+  long long r = s0 / segs;
+  int seg = static_cast<int>(s0 - r * segs);
+  for (long long s = s0; s < s1; ++s) {
     const int b = static_cast<int>(r / a.N), i = static_cast<int>(r - static_cast<long long>(b) * a.N);
     const int pi = a.position(b, i);
     const int* chain = a.chain != nullptr ? a.chain + static_cast<size_t>(b) * a.N : nullptr;
     const int ci = chain != nullptr ? __ldg(chain + i) : 0;
     const size_t row = static_cast<size_t>(r) * a.N;
-    for (int j = j0; j < a.N; j += U * step) {
-      uint4 in[U];
-      int k[U];
+    uint4 in[U];
+    int k[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int ju = min(j + u * step, a.N - 1);
-        if (a.base != nullptr) in[u] = *reinterpret_cast<const uint4*>(a.base + (row + ju) * a.F + f);
-        k[u] = chain != nullptr && __ldg(chain + ju) != ci ? a.buckets - 1
-                                                           : lut[distance(pi, a.position(b, ju), a.R)];
-      }
+    for (int u = 0; u < U; ++u) {
+      const int j = seg * len + u * step + jt;
+      if (j >= a.N) break;
+      if (a.base != nullptr) in[u] = *reinterpret_cast<const uint4*>(a.base + (row + j) * a.F + f);
+      k[u] = chain != nullptr && __ldg(chain + j) != ci ? a.buckets - 1 : lut[distance(pi, a.position(b, j), a.R)];
+    }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int ju = j + u * step;
-        if (ju >= a.N) break;
-        const float4* e = reinterpret_cast<const float4*>(a.table + static_cast<size_t>(k[u]) * a.F + f);
-        const float4 e0 = __ldg(e), e1 = __ldg(e + 1);
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (a.base != nullptr) unpack8(in[u], v);
-        v[0] += e0.x;
-        v[1] += e0.y;
-        v[2] += e0.z;
-        v[3] += e0.w;
-        v[4] += e1.x;
-        v[5] += e1.y;
-        v[6] += e1.z;
-        v[7] += e1.w;
-        *reinterpret_cast<uint4*>(a.out + (row + ju) * a.F + f) = pack8(v);
-      }
+    for (int u = 0; u < U; ++u) {
+      const int j = seg * len + u * step + jt;
+      if (j >= a.N) break;
+      const float4* e = reinterpret_cast<const float4*>(a.table + static_cast<size_t>(k[u]) * a.F + f);
+      const float4 e0 = __ldg(e), e1 = __ldg(e + 1);
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (a.base != nullptr) unpack8(in[u], v);
+      v[0] += e0.x;
+      v[1] += e0.y;
+      v[2] += e0.z;
+      v[3] += e0.w;
+      v[4] += e1.x;
+      v[5] += e1.y;
+      v[6] += e1.z;
+      v[7] += e1.w;
+      *reinterpret_cast<uint4*>(a.out + (row + j) * a.F + f) = pack8(v);
+    }
+    if (++seg == segs) {
+      seg = 0;
+      ++r;
     }
   }
 }
@@ -190,106 +199,101 @@ __device__ __forceinline__ void values(const uint4 (&v)[2], float (&f)[8]) {
 __device__ __forceinline__ float value(uint16_t v) { return bf16lo_to_f32(v); }
 __device__ __forceinline__ float value(float v) { return v; }
 
-// Block: a run of rows of one plane; thread: one chunk of eight columns, row
-// after row, four rows in flight.  A thread adds elements of one bucket in a
-// register and, when the bucket changes, adds the register to a place of its
-// own (bucket by lane of its warp) in shared memory: no two threads share a
-// sum, so the order is fixed.  The positions of a chunk are known by their
-// smallest and largest: where both give one bucket (all but the pairs near the
-// diagonal), the eight elements are added at once.
+// Block: a run of rows of one plane, a row per warp; lane: every 32nd chunk of
+// eight columns, four in flight.  A chunk's positions are known by their smallest
+// and largest (kept per chunk in shared memory): where both give one bucket (all
+// but the pairs near the diagonal), the eight elements are added at once, the
+// buckets of the far ends and of other chains in registers.  Everything else
+// goes to a place of the lane's own (bucket by lane of its warp) in shared memory:
+// no two threads share a sum, so the order is fixed.  The diagonal crosses a
+// different chunk in every row, and every warp meets it as often as the others.
+struct Window {
+  int lo, hi, chain;  // positions of the chunk's columns; its chain
+  int one;            // all of one chain
+};
 template <typename T>
 __global__ void __launch_bounds__(kThreads) relpos_heads_bwd_kernel(const __grid_constant__ RelposArgs a, const T* d_out,
                                                                     int rows) {
-  constexpr int U = 4;                  // rows in flight
+  constexpr int U = 4;                  // chunks in flight
   constexpr int V = sizeof(T) / 2;      // 16-byte pieces of a chunk
-  extern __shared__ float hist[];       // [warps][buckets][32]
+  extern __shared__ float sh[];         // windows [chunks], sums [warps][buckets][32]
   __shared__ uint8_t lut[2 * kRelposMaxDistance + 1];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, T0 = blockDim.x, nw = blockDim.x / 32;
-  for (int d = threadIdx.x; d <= 2 * a.R; d += T0) lut[d] = a.lut[d];
-  for (int e = threadIdx.x; e < nw * a.buckets * 32; e += T0) hist[e] = 0.f;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, nw = blockDim.x / 32;
+  const int nt = chunks_of(a.N), b = blockIdx.y / a.F;
+  Window* win = reinterpret_cast<Window*>(sh);
+  float* hist = sh + 4 * nt;
+  const int* chain = a.chain != nullptr ? a.chain + static_cast<size_t>(b) * a.N : nullptr;
+  for (int d = threadIdx.x; d <= 2 * a.R; d += blockDim.x) lut[d] = a.lut[d];
+  for (int e = threadIdx.x; e < nw * a.buckets * 32; e += blockDim.x) hist[e] = 0.f;
+  for (int t = threadIdx.x; t < nt; t += blockDim.x) {
+    // all columns that the chunk can hold, whatever its rows' alignment
+    const int ja = max(0, a.N % 8 == 0 ? 8 * t : 8 * t - 7), jb = min(a.N, 8 * t + 8);
+    Window w{0x7fffffff, -0x7fffffff - 1, chain != nullptr ? __ldg(chain + ja) : 0, 1};
+    for (int j = ja; j < jb; ++j) {
+      const int p = a.position(b, j);
+      w.lo = min(w.lo, p);
+      w.hi = max(w.hi, p);
+      if (chain != nullptr && __ldg(chain + j) != w.chain) w.one = 0;
+    }
+    win[t] = w;
+  }
   __syncthreads();
   float* mine = hist + warp * a.buckets * 32 + lane;
-  const int b = blockIdx.y / a.F;
   const size_t plane = static_cast<size_t>(a.N) * a.N, p0 = blockIdx.y * plane;
   const size_t total = static_cast<size_t>(a.B) * a.F * plane;
-  const int* chain = a.chain != nullptr ? a.chain + static_cast<size_t>(b) * a.N : nullptr;
-  const int nt = chunks_of(a.N), i0 = blockIdx.x * rows, i1 = min(i0 + rows, a.N);
-  const int rp = max(1, T0 / nt), rr = threadIdx.x / min(nt, T0), t0 = threadIdx.x - rr * min(nt, T0);
-  int cur = 0;
-  float acc = 0.f;
-  auto add = [&](int bucket, float v) {
-    if (bucket != cur) {
-      mine[cur * 32] += acc;
-      cur = bucket;
-      acc = 0.f;
-    }
-    acc += v;
-  };
-  for (int t = t0; t < nt && rr < rp; t += T0) {
-    // positions and chains of all columns that the chunk can hold
-    int lo = 0x7fffffff, hi = -0x7fffffff - 1, cw = 0;
-    bool one = true;  // of one chain
-    {
-      const int ja = max(0, a.N % 8 == 0 ? 8 * t : 8 * t - 7), jb = min(a.N, 8 * t + 8);
-      cw = chain != nullptr ? __ldg(chain + ja) : 0;
-      for (int j = ja; j < jb; ++j) {
-        const int p = a.position(b, j);
-        lo = min(lo, p);
-        hi = max(hi, p);
-        if (chain != nullptr) one = one && __ldg(chain + j) == cw;
-      }
-    }
-    for (int i = i0 + rr; i < i1; i += U * rp) {
+  const int kl = lut[0], kh = lut[2 * a.R], ko = a.buckets - 1;  // far on either side, other chains
+  float sl = 0.f, sh_ = 0.f, so = 0.f;
+  const int i1 = min((static_cast<int>(blockIdx.x) + 1) * rows, a.N);
+  for (int i = blockIdx.x * rows + warp; i < i1; i += nw) {
+    const size_t s = p0 + static_cast<size_t>(i) * a.N;
+    const int off = static_cast<int>(s & 7);
+    const int pi = a.position(b, i), ci = chain != nullptr ? __ldg(chain + i) : 0;
+    for (int t = lane; t < nt; t += U * 32) {
       uint4 raw[U][V];
-      int off[U], pi[U], ci[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int iu = min(i + u * rp, i1 - 1);
-        const size_t s = p0 + static_cast<size_t>(iu) * a.N;
-        off[u] = static_cast<int>(s & 7);
-        const size_t e = s - off[u] + 8 * static_cast<size_t>(t);
-        if (e + 8 <= total) load8(d_out + e, raw[u]);
-        pi[u] = a.position(b, iu);
-        ci[u] = chain != nullptr ? __ldg(chain + iu) : 0;
+        const size_t e = s - off + 8 * static_cast<size_t>(t + 32 * u);
+        if (t + 32 * u < nt && e + 8 <= total) load8(d_out + e, raw[u]);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int iu = i + u * rp;
-        if (iu >= i1) break;
-        const int j0 = 8 * t - off[u];
-        if (j0 >= a.N) continue;  // rows end in their last chunk or in the one before
+        const int tu = t + 32 * u, j0 = 8 * tu - off;
+        if (tu >= nt || j0 >= a.N) break;
         float v[8];
-        const size_t s = p0 + static_cast<size_t>(iu) * a.N;
         if (j0 >= 0 && j0 + 8 <= a.N) {
           values(raw[u], v);
         } else {  // the ends of a row: what lies outside it counts as zero
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[k] = j0 + k >= 0 && j0 + k < a.N ? value(d_out[s + j0 + k]) : 0.f;
         }
-        int k0 = -1;  // the chunk's bucket, if it is one
-        if (one) {
-          if (ci[u] != cw) {
-            k0 = a.buckets - 1;
-          } else {
-            const int ka = lut[distance(pi[u], hi, a.R)], kb = lut[distance(pi[u], lo, a.R)];
-            k0 = ka == kb ? ka : -1;
-          }
+        const Window w = win[tu];
+        int ka = ko, kb = ko;
+        if (w.chain == ci || !w.one) {
+          ka = lut[distance(pi, w.hi, a.R)];
+          kb = lut[distance(pi, w.lo, a.R)];
         }
-        if (k0 >= 0) {
-          add(k0, ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])));
+        if (w.one && ka == kb) {
+          const float x = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+          if (ka == kl) sl += x;
+          else if (ka == kh) sh_ += x;
+          else if (ka == ko) so += x;
+          else mine[ka * 32] += x;
         } else {
+          int kk[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int j = min(max(j0 + k, 0), a.N - 1);
-            const int kk = chain != nullptr && __ldg(chain + j) != ci[u] ? a.buckets - 1
-                                                                         : lut[distance(pi[u], a.position(b, j), a.R)];
-            add(kk, v[k]);
+            kk[k] = chain != nullptr && __ldg(chain + j) != ci ? ko : lut[distance(pi, a.position(b, j), a.R)];
           }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mine[kk[k] * 32] += v[k];
         }
       }
     }
   }
-  mine[cur * 32] += acc;
+  mine[kl * 32] += sl;
+  mine[kh * 32] += sh_;
+  mine[ko * 32] += so;
   __syncthreads();
   float* out = a.part + (static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x) * a.buckets;
   for (int k = warp; k < a.buckets; k += nw) {
@@ -387,19 +391,28 @@ int rows_per_block(int N, long long planes, int want) {
   return static_cast<int>((N + blocks - 1) / blocks);
 }
 
-// Planes' gradient: as many warps as two blocks an SM have room for.
-int bwd_warps(int buckets) {
-  int w = kThreads / 32;
-  while (w > 1 && w * buckets * 128 > 112000) w /= 2;
-  return w;
+// Planes' gradient: as many warps as three, two or one blocks an SM have room
+// for, at least four if they can be had.
+struct BwdPlan {
+  int warps, rows, splits;
+  size_t smem;
+};
+BwdPlan bwd_plan(int B, int N, int F, int buckets) {
+  BwdPlan p;
+  const size_t win = static_cast<size_t>(chunks_of(N)) * sizeof(Window);
+  p.warps = kThreads / 32;
+  while (p.warps > 1 && win + static_cast<size_t>(p.warps) * buckets * 128 > (p.warps > 4 ? 72000u : 216000u)) p.warps /= 2;
+  p.smem = win + static_cast<size_t>(p.warps) * buckets * 128;
+  const int per_sm = std::max(1, std::min<int>(2048 / (32 * p.warps), static_cast<int>(220000 / (p.smem + 3200))));
+  p.rows = rows_per_block(N, static_cast<long long>(B) * F, 152 * per_sm * 2);
+  p.splits = (N + p.rows - 1) / p.rows;
+  return p;
 }
-constexpr int kBwdBlocks = 152 * 3;
 
 size_t part_bytes(const triattn_relpos_shape* s) {
   if (s->layout == TRIATTN_RELPOS_PAIRS)
     return static_cast<size_t>(relpos_pairs_parts(s->B, s->N)) * s->buckets * s->F * 4;
-  const int rows = rows_per_block(s->N, static_cast<long long>(s->B) * s->F, kBwdBlocks);
-  return static_cast<size_t>(s->B) * s->F * ((s->N + rows - 1) / rows) * s->buckets * 4;
+  return static_cast<size_t>(s->B) * s->F * bwd_plan(s->B, s->N, s->F, s->buckets).splits * s->buckets * 4;
 }
 
 // One limit per kernel whatever the call asks for: calls of other threads in
@@ -423,21 +436,18 @@ cudaError_t launch_heads_fwd(const RelposArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_pairs_fwd(const RelposArgs& a, cudaStream_t s) {
-  const int per = a.F / 8, threads = kThreads / per * per;
-  const long long all = static_cast<long long>(a.B) * a.N;
-  const int rows = static_cast<int>((all + 152 * 8 - 1) / (152 * 8));
-  relpos_pairs_fwd_kernel<<<static_cast<unsigned>((all + rows - 1) / rows), threads, 0, s>>>(a, rows);
+  const int len = pairs_segment(a.F);
+  const long long all = static_cast<long long>(a.B) * a.N * ((a.N + len - 1) / len);
+  relpos_pairs_fwd_kernel<<<static_cast<unsigned>(std::min(all, 152ll * 4)), pairs_threads(a.F), 0, s>>>(a);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_heads_bwd(const RelposArgs& a, const void* d_out, int rows, cudaStream_t s) {
-  const int warps = bwd_warps(a.buckets);
-  const size_t smem = static_cast<size_t>(warps) * a.buckets * 128;
-  cudaError_t e = allow_smem(relpos_heads_bwd_kernel<T>, smem);
+cudaError_t launch_heads_bwd(const RelposArgs& a, const void* d_out, const BwdPlan& p, cudaStream_t s) {
+  cudaError_t e = allow_smem(relpos_heads_bwd_kernel<T>, p.smem);
   if (e != cudaSuccess) return e;
-  relpos_heads_bwd_kernel<T><<<dim3((a.N + rows - 1) / rows, a.B * a.F), warps * 32, smem, s>>>(
-      a, static_cast<const T*>(d_out), rows);
+  relpos_heads_bwd_kernel<T><<<dim3(p.splits, a.B * a.F), p.warps * 32, p.smem, s>>>(
+      a, static_cast<const T*>(d_out), p.rows);
   return cudaGetLastError();
 }
 
@@ -498,17 +508,16 @@ triattn_status triattn_relpos_bwd(const triattn_relpos_shape* shape, const void*
         return cudaGetLastError();
       });
   } else {
-    const int rows = rows_per_block(a.N, static_cast<long long>(a.B) * a.F, kBwdBlocks);
-    const int splits = (a.N + rows - 1) / rows;
+    const BwdPlan p = bwd_plan(a.B, a.N, a.F, a.buckets);
     e = trace_call(kKRelBwd, s, [&] {
-      return (shape->flags & TRIATTN_FLAG_DOUT_FP32) ? launch_heads_bwd<float>(a, d_out, rows, s)
-                                                     : launch_heads_bwd<uint16_t>(a, d_out, rows, s);
+      return (shape->flags & TRIATTN_FLAG_DOUT_FP32) ? launch_heads_bwd<float>(a, d_out, p, s)
+                                                     : launch_heads_bwd<uint16_t>(a, d_out, p, s);
     });
     if (e == cudaSuccess)
       e = trace_call(kKRelSum, s, [&] {  // partials [B][F][splits][buckets]
-        const size_t per = static_cast<size_t>(splits) * a.buckets;
+        const size_t per = static_cast<size_t>(p.splits) * a.buckets;
         relpos_sum_kernel<<<dim3((a.buckets + 31) / 32, a.F), 1024, 0, s>>>(a.part, d_table, a.buckets, a.F, 1, a.B,
-                                                                           splits, a.F * per, a.buckets, per);
+                                                                           p.splits, a.F * per, a.buckets, per);
         return cudaGetLastError();
       });
   }

@@ -10,7 +10,7 @@
 // pairs, 128 features and 66 buckets, against 22 us for the bytes of d_out,
 // which bound it.
 //
-// One CTA per run of pairs, 128 threads:
+// One CTA per run of pairs, 6 warps:
 //   warp 0     TMA: per 64 pairs the rows of d_out as 64-feature boxes (128-byte
 //              swizzle), which are A, features contiguous (MN-major).
 //   warp 1     MMA issuer: per 64 pairs and 128 features four M = 128,
@@ -18,10 +18,12 @@
 //              turns, and a run is at most kRun blocks of 64 pairs, so that no
 //              accumulator adds more than 4 kRun products of 16: the tensor
 //              cores cut off what an FP32 accumulator cannot hold.
-//   warps 2-3  one pair per thread: its bucket, then the two bytes of its one
-//              in B [buckets, 64 pairs] (K-major, swizzled), after the one that
-//              the stage held before is put out.
-// At the end all warps add the accumulators and write the run's partial table.
+//   warps 2-5  one pair per thread, two warps for the even and two for the odd
+//              stages: its bucket (of the next stage while they wait for this
+//              one), then the two bytes of its one in B [buckets, 64 pairs]
+//              (K-major, swizzled), after the one that the stage held before is
+//              put out.
+// At the end four warps add the accumulators and write the run's partial table.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -51,7 +53,9 @@ struct PairsBwd {
   WaitCtl wc;
 };
 
-__global__ void __launch_bounds__(128, 1) relpos_pairs_bwd_kernel(const __grid_constant__ CUtensorMap tm,
+constexpr int kPairThreads = 192;
+
+__global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const __grid_constant__ CUtensorMap tm,
                                                                   const __grid_constant__ RelposArgs a, PairsBwd p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Bars bars;
@@ -60,10 +64,10 @@ __global__ void __launch_bounds__(128, 1) relpos_pairs_bwd_kernel(const __grid_c
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abort = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int d = threadIdx.x; d <= 2 * a.R; d += 128) lut[d] = a.lut[d];
+  for (int d = threadIdx.x; d <= 2 * a.R; d += kPairThreads) lut[d] = a.lut[d];
   for (int s = 0; s < p.stages; ++s) {
     uint4* e = reinterpret_cast<uint4*>(sm + s * p.stage_bytes + p.a_bytes);
-    for (int k = threadIdx.x; k < p.nb * 8; k += 128) e[k] = make_uint4(0u, 0u, 0u, 0u);
+    for (int k = threadIdx.x; k < p.nb * 8; k += kPairThreads) e[k] = make_uint4(0u, 0u, 0u, 0u);
     if (threadIdx.x < kBlk) held[s][threadIdx.x] = kNone;
   }
   if (threadIdx.x == 0) {
@@ -121,29 +125,20 @@ __global__ void __launch_bounds__(128, 1) relpos_pairs_bwd_kernel(const __grid_c
       if (++stage == p.stages) { stage = 0; phase ^= 1; }
     }
   } else {
-    const int c = threadIdx.x - 64;  // the pair of the block
-    long long q = b0 * kBlk + c;
+    const int c = threadIdx.x & 63, odd = warp >= 4;  // the pair of the block
+    long long q = (b0 + odd) * kBlk + c;
     const long long NN = static_cast<long long>(a.N) * a.N;
     int b = static_cast<int>(q / NN), i = static_cast<int>((q - b * NN) / a.N);
     int j = static_cast<int>(q - b * NN - static_cast<long long>(i) * a.N);
-    int stage = 0, phase = 0;
-    for (int k = 0; k < n; ++k, q += kBlk) {
-      int row = -1;
-      if (q < p.P) {
-        const bool other = a.chain != nullptr && __ldg(a.chain + static_cast<size_t>(b) * a.N + i) !=
-                                                     __ldg(a.chain + static_cast<size_t>(b) * a.N + j);
-        row = other ? a.buckets - 1 : lut[distance(a.position(b, i), a.position(b, j), a.R)];
-      }
-      if (!mbar_wait(&bars.empty[stage], phase ^ 1, p.wc, abort)) break;
-      uint16_t* e = reinterpret_cast<uint16_t*>(sm + stage * p.stage_bytes + p.a_bytes);
-      if (held[stage][c] != kNone) e[held[stage][c]] = 0;
-      const uint16_t at = row >= 0 ? static_cast<uint16_t>(sw128(row, c >> 3) / 2 + (c & 7)) : kNone;
-      if (at != kNone) e[at] = 0x3F80;  // 1
-      held[stage][c] = at;
-      fence_proxy_async_smem();
-      mbar_arrive(&bars.full[stage]);
-      if (++stage == p.stages) { stage = 0; phase ^= 1; }
-      j += kBlk;
+    auto bucket = [&]() {  // of pair (b, i, j); none past the last
+      if (q >= p.P) return -1;
+      const size_t at = static_cast<size_t>(b) * a.N;
+      const bool other = a.chain != nullptr && __ldg(a.chain + at + i) != __ldg(a.chain + at + j);
+      return other ? a.buckets - 1 : static_cast<int>(lut[distance(a.position(b, i), a.position(b, j), a.R)]);
+    };
+    auto next = [&]() {  // two blocks on
+      q += 2 * kBlk;
+      j += 2 * kBlk;
       if (j >= a.N) {
         const int w = j / a.N;
         j -= w * a.N;
@@ -154,12 +149,27 @@ __global__ void __launch_bounds__(128, 1) relpos_pairs_bwd_kernel(const __grid_c
           b += v;
         }
       }
+    };
+    int row = bucket();
+    for (int k = odd; k < n; k += 2) {
+      const int stage = k % p.stages, phase = (k / p.stages) & 1;
+      next();
+      const int row_next = k + 2 < n ? bucket() : -1;
+      if (!mbar_wait(&bars.empty[stage], phase ^ 1, p.wc, abort)) break;
+      uint16_t* e = reinterpret_cast<uint16_t*>(sm + stage * p.stage_bytes + p.a_bytes);
+      if (held[stage][c] != kNone) e[held[stage][c]] = 0;
+      const uint16_t at = row >= 0 ? static_cast<uint16_t>(sw128(row, c >> 3) / 2 + (c & 7)) : kNone;
+      if (at != kNone) e[at] = 0x3F80;  // 1
+      held[stage][c] = at;
+      fence_proxy_async_smem();
+      mbar_arrive(&bars.full[stage]);
+      row = row_next;
     }
   }
   __syncwarp();
   const bool ok = __all_sync(0xffffffffu, mbar_wait(&bars.done, 0, p.wc, abort));
   tc_fence_after();
-  if (ok) {
+  if (ok && warp < 4) {
     float* out = a.part + static_cast<size_t>(blockIdx.x) * a.buckets * a.F;
     const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
     const int used = min(n, p.sets);
@@ -212,7 +222,7 @@ cudaError_t launch_relpos_pairs_bwd(const RelposArgs& a, const void* d_out, int 
   p.a_bytes = p.mt * 2 * kBlk * 128;
   p.stage_bytes = p.a_bytes + p.nb * 128;
   p.stage_bytes = (p.stage_bytes + 1023) / 1024 * 1024;
-  p.stages = std::min(kStagesMax, (kSmemMax - 1024) / p.stage_bytes);
+  p.stages = std::min(kStagesMax, (kSmemMax - 1024) / p.stage_bytes) & ~1;  // even: a stage's ones are always one warp's
   p.wc = wc;
   CUtensorMap tm;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.F), static_cast<cuuint64_t>(p.P), 1};
@@ -226,7 +236,7 @@ cudaError_t launch_relpos_pairs_bwd(const RelposArgs& a, const void* d_out, int 
       cudaFuncSetAttribute(relpos_pairs_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
   if (e != cudaSuccess) return e;
   // all of an SM's shared memory, so that one CTA runs on it: it takes all of TMEM
-  relpos_pairs_bwd_kernel<<<parts, 128, kSmemMax, s>>>(tm, a, p);
+  relpos_pairs_bwd_kernel<<<parts, kPairThreads, kSmemMax, s>>>(tm, a, p);
   return cudaGetLastError();
 }
 
