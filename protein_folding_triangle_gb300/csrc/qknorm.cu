@@ -356,26 +356,35 @@ struct Plan {
   size_t part_bytes;
 };
 
-// Blocks: a tile of rows of a slice times a run of slices, about `waves` times
-// what the GPU holds at once (two blocks an SM), but runs of at least `least`
-// slices: what a block does before and after them takes as long as about that many.
-Plan plan_of(const triattn_qk_norm_shape* s, bool hn, int waves, int least) {
+// Blocks: a tile of rows of a slice times a run of slices.  Of one to six waves of
+// what the GPU holds at once (two blocks an SM) the one with the shortest run of
+// a SM's blocks, where what a block does before and after its slices takes as
+// long as `extra` of them.
+Plan plan_of(const triattn_qk_norm_shape* s, bool hn, int extra) {
   Plan p;
   p.rows = kThreads / (s->D / 16);
   const long long HN = static_cast<long long>(s->H) * s->N;
   p.tiles = static_cast<int>((HN + p.rows - 1) / p.rows);
-  const long long base = 2ll * p.tiles * s->B, want = 152ll * 2 * waves;
-  long long cpb = std::max(1ll, std::min<long long>(want / base, s->N_o / least));
-  cpb = std::min(cpb, 65535ll / s->B);
-  p.per = static_cast<int>((s->N_o + cpb - 1) / cpb);
+  const long long base = 2ll * p.tiles * s->B, slots = 152 * 2;
+  long long best = 1, least = -1;
+  for (int w = 1; w <= 6; ++w) {
+    const long long cpb = std::max(1ll, std::min<long long>({slots * w / base, s->N_o, 65535ll / s->B}));
+    const long long per = (s->N_o + cpb - 1) / cpb, blocks = base * ((s->N_o + per - 1) / per);
+    const long long time = (blocks + slots - 1) / slots * (per + extra);
+    if (least < 0 || time < least) {
+      best = cpb;
+      least = time;
+    }
+  }
+  p.per = static_cast<int>((s->N_o + best - 1) / best);
   p.cpb = (s->N_o + p.per - 1) / p.per;
   p.chunks = p.cpb * s->B;
   p.slots = hn ? std::min(s->H, p.rows) : static_cast<int>(std::min<long long>(s->H, (p.rows - 1) / s->N + 2));
   p.part_bytes = 2ull * p.chunks * p.tiles * p.slots * s->D * 4;
   return p;
 }
-Plan fwd_plan(const triattn_qk_norm_shape* s, bool hn) { return plan_of(s, hn, 4, 4); }
-Plan bwd_plan(const triattn_qk_norm_shape* s, bool hn) { return plan_of(s, hn, 2, 8); }
+Plan fwd_plan(const triattn_qk_norm_shape* s, bool hn) { return plan_of(s, hn, 3); }
+Plan bwd_plan(const triattn_qk_norm_shape* s, bool hn) { return plan_of(s, hn, 8); }
 
 triattn_status check(const triattn_qk_norm_shape* s, triattn_shape* core) {
   if (s == nullptr || s->B < 1 || s->N_o < 1 || s->N < 1 || s->H < 1 || s->D < 1 || s->flags != 0)

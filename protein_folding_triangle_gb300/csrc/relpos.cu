@@ -50,73 +50,197 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 }
 
 // The planes' rows need not start on 16 bytes: chunk t of a row is the t-th
-// aligned group of eight elements that holds elements of the row, [8 t - off,
-// 8 t - off + 8) of it, off the place of the row's start in its group.
-__host__ __device__ constexpr int chunks_of(int N) { return N % 8 == 0 ? N / 8 : (N + 14) / 8; }
+// aligned group of W elements that holds elements of the row, [W t - off,
+// W t - off + W) of it, off the place of the row's start in its group.
+__host__ __device__ constexpr int chunks_of(int N, int W) { return N % W == 0 ? N / W : (N + 2 * W - 2) / W; }
+
+// What the columns that chunk t can hold (whatever its rows' off) have in common.
+struct Window {
+  int lo, hi;            // smallest and largest position
+  int chain, chain_max;  // smallest and largest chain
+  int run;               // the positions are lo, lo + 1, ..., in order
+};
+// First column of chunk t's window: of its aligned W columns, and where rows start
+// anywhere of the W before them too.
+template <int W>
+__device__ __forceinline__ int first_column(int N, int t) { return N % W == 0 ? W * t : max(0, W * (t - 1)); }
+// All windows, by all threads of the block (a multiple of W, W lanes to a group of
+// columns); the caller waits for them.
+template <int W>
+__device__ __forceinline__ void make_windows(const RelposArgs& a, int b, int nt, Window* win) {
+  constexpr int U = 4;  // groups of columns whose loads are under way together
+  const int l = threadIdx.x % W, step = blockDim.x / W;
+  const bool two = a.N % W != 0;
+  const int* pos = a.pos != nullptr ? a.pos + static_cast<size_t>(b) * a.N : nullptr;
+  const int* chain = a.chain != nullptr ? a.chain + static_cast<size_t>(b) * a.N : nullptr;
+  for (int t0 = threadIdx.x / W; t0 - threadIdx.x / W < nt; t0 += U * step) {
+    int p[U][2], c[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {  // its own columns, and the W before
+        const int j = min(max(W * (t0 + u * step - g) + l, 0), a.N - 1);
+        p[u][g] = j;
+        c[u][g] = 0;
+        if (pos != nullptr && (g == 0 || two)) p[u][g] = __ldg(pos + j);
+        if (chain != nullptr && (g == 0 || two)) c[u][g] = __ldg(chain + j);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u * step;
+      Window w{0x7fffffff, -0x7fffffff - 1, 0x7fffffff, -0x7fffffff - 1, 1};
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int j = W * (t - g) + l;
+        if ((g == 1 && !two) || j < 0 || j >= a.N) continue;
+        w.lo = min(w.lo, p[u][g]);
+        w.hi = max(w.hi, p[u][g]);
+        w.chain = min(w.chain, c[u][g]);
+        w.chain_max = max(w.chain_max, c[u][g]);
+      }
+#pragma unroll
+      for (int o = W / 2; o > 0; o /= 2) {
+        w.lo = min(w.lo, __shfl_xor_sync(0xffffffffu, w.lo, o));
+        w.hi = max(w.hi, __shfl_xor_sync(0xffffffffu, w.hi, o));
+        w.chain = min(w.chain, __shfl_xor_sync(0xffffffffu, w.chain, o));
+        w.chain_max = max(w.chain_max, __shfl_xor_sync(0xffffffffu, w.chain_max, o));
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int j = W * (t - g) + l;
+        if ((g == 1 && !two) || j < 0 || j >= a.N) continue;
+        if (static_cast<long long>(p[u][g]) - w.lo != j - first_column<W>(a.N, t)) w.run = 0;
+      }
+#pragma unroll
+      for (int o = W / 2; o > 0; o /= 2) w.run &= __shfl_xor_sync(0xffffffffu, w.run, o);
+      if (l == 0 && t < nt) win[t] = w;
+    }
+  }
+}
+
+// The planes' kernels.  A block has a run of units of one example: a unit is a row
+// i and a segment of its chunks (of one or four heads), a warp's work, the lanes
+// along the chunks.
+constexpr int kSegChunks = 64;
+struct Units {
+  int segs, len;  // segments of a row, chunks of a segment
+  __host__ __device__ Units(int nt) {
+    segs = (nt + kSegChunks - 1) / kSegChunks;
+    len = ((nt + segs - 1) / segs + 31) / 32 * 32;
+    segs = (nt + len - 1) / len;
+  }
+};
 
 // ------------------------------------------------------- planes, forward
-// Block: a run of rows i of one example and G heads; thread: a chunk of eight
-// columns.  The values of every bucket lie in shared memory by distance.
-template <int G>
-__global__ void __launch_bounds__(kThreads) relpos_heads_fwd_kernel(const __grid_constant__ RelposArgs a, int rows) {
+// Four heads at a time: the buckets are found once for all.  The values of every
+// bucket lie in shared memory by distance.  Chunks inside the row and of one chain
+// are taken as a whole; the others of a warp (the ends of rows that do not start
+// on a chunk, and where chains meet) go element by element, four chunks at a time,
+// a lane to an element.  ALIGNED: all rows start on 16 bytes.
+constexpr int kFwdBlocks = 4;  // an SM
+template <bool ALIGNED>
+__global__ void __launch_bounds__(kThreads, kFwdBlocks) relpos_heads_fwd_kernel(const __grid_constant__ RelposArgs a) {
+  constexpr int G = kHeadGroup, W = 8;
   extern __shared__ float sh[];
-  const int W = spread(2 * a.R + 1) + 1, NP = spread(a.N - 1) + 1;
-  float* val = sh;                                   // [G][W]: distance + R, then the other chains' value
-  int* pos = reinterpret_cast<int*>(val + G * W);    // [NP]
-  int* chain = pos + NP;                             // [NP], with chains
-  const int groups = (a.F + G - 1) / G, b = blockIdx.y / groups, h0 = (blockIdx.y % groups) * G;
+  const int nt = chunks_of(a.N, W), VW = spread(2 * a.R + 1) + 1;
+  Window* win = reinterpret_cast<Window*>(sh);                        // [chunks]
+  float* val = sh + 5 * nt;                                           // [G][VW]: distance + R, then other chains
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int groups = (a.F + G - 1) / G, b = blockIdx.y / groups, h0 = (blockIdx.y % groups) * G, ng = min(G, a.F - h0);
+  const int* chain = a.chain != nullptr ? a.chain + static_cast<size_t>(b) * a.N : nullptr;
   for (int d = threadIdx.x; d <= 2 * a.R + 1; d += kThreads) {
     const int k = d <= 2 * a.R ? a.lut[d] : a.buckets - 1;
 #pragma unroll
     for (int g = 0; g < G; ++g)
-      if (h0 + g < a.F) val[g * W + spread(d)] = a.table[static_cast<size_t>(k) * a.F + h0 + g];
+      if (g < ng) val[g * VW + spread(d)] = a.table[static_cast<size_t>(k) * a.F + h0 + g];
   }
-  for (int n = threadIdx.x; n < a.N; n += kThreads) {
-    pos[spread(n)] = a.position(b, n);
-    if (a.chain != nullptr) chain[spread(n)] = __ldg(a.chain + static_cast<size_t>(b) * a.N + n);
-  }
+  make_windows<W>(a, b, nt, win);
   __syncthreads();
-  const int nt = chunks_of(a.N);
-  const int i0 = blockIdx.x * rows, items = (min(i0 + rows, a.N) - i0) * nt;
+  const int other = spread(2 * a.R + 1);
   const size_t plane = static_cast<size_t>(a.N) * a.N;
-  for (int it = threadIdx.x; it < items; it += kThreads) {
-    const int r = it / nt, i = i0 + r, t = it - r * nt;
+  const Units un(nt);
+  const int units = a.N * un.segs;
+  const int u0 = static_cast<int>(static_cast<long long>(units) * blockIdx.x / gridDim.x);
+  const int u1 = static_cast<int>(static_cast<long long>(units) * (blockIdx.x + 1) / gridDim.x);
+  for (int u = u0 + warp; u < u1; u += kThreads / 32) {
+    const int i = u / un.segs, seg = u - i * un.segs;
+    const int pi = a.position(b, i), ci = chain != nullptr ? __ldg(chain + i) : 0;
     const size_t row = ((static_cast<size_t>(b) * a.F + h0) * a.N + i) * a.N;
-    const int off = G == 1 ? static_cast<int>(row & 7) : 0;  // G > 1: rows start on 16 bytes
-    const int j0 = 8 * t - off;
-    const int pi = pos[spread(i)], ci = a.chain != nullptr ? chain[spread(i)] : 0;
-    const bool whole = j0 >= 0 && j0 + 8 <= a.N;
-    uint4 in[G];
-    if (a.base != nullptr && whole) {
+    int off[G];
 #pragma unroll
-      for (int g = 0; g < G; ++g)
-        if (h0 + g < a.F) in[g] = *reinterpret_cast<const uint4*>(a.base + row + g * plane + j0);
-    }
-    int at[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int j = min(max(j0 + k, 0), a.N - 1);
-      at[k] = distance(pi, pos[spread(j)], a.R);
-      if (a.chain != nullptr && chain[spread(j)] != ci) at[k] = 2 * a.R + 1;
-      at[k] = spread(at[k]);
-    }
-    if (whole) {
+    for (int g = 0; g < G; ++g) off[g] = ALIGNED ? 0 : static_cast<int>((row + g * plane) & (W - 1));
+    auto place = [&](int j) {  // of column j, any chain
+      return chain != nullptr && __ldg(chain + j) != ci ? other : spread(distance(pi, a.position(b, j), a.R));
+    };
+    const int t1 = min((seg + 1) * un.len, nt);
+    for (int t0 = seg * un.len; t0 < t1; t0 += 32) {
+      const int t = t0 + lane;
+      const Window w = win[min(t, nt - 1)];
+      const bool apart = ci < w.chain || ci > w.chain_max;  // no column of the row's chain
+      const bool one_chain = (apart || w.chain == w.chain_max) && t < t1;
+      uint4 in[G];
+      bool whole[G];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        if (h0 + g >= a.F) break;
-        float v[8];
-        if (a.base != nullptr) unpack8(in[g], v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = (a.base != nullptr ? v[k] : 0.f) + val[g * W + at[k]];
-        *reinterpret_cast<uint4*>(a.out + row + g * plane + j0) = pack8(v);
+        const int j0 = W * t - off[g];
+        whole[g] = g < ng && one_chain && (ALIGNED || (j0 >= 0 && j0 + W <= a.N));
+        in[g] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.base != nullptr && whole[g]) in[g] = *reinterpret_cast<const uint4*>(a.base + row + g * plane + j0);
       }
-    } else {  // the ends of a row (G == 1), element by element
+      const int far = distance(pi, w.hi, a.R), near = distance(pi, w.lo, a.R);
+      const bool single = one_chain && (apart || far == near);
+      const int one = apart ? other : spread(far);
+      if (single) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int j = j0 + k;
-        if (j < 0 || j >= a.N) continue;
-        const float v = (a.base != nullptr ? bf16lo_to_f32(a.base[row + j]) : 0.f) + val[at[k]];
-        a.out[row + j] = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xFFFFu);
+        for (int g = 0; g < G; ++g) {
+          if (!whole[g]) continue;
+          const float2 x = make_float2(val[g * VW + one], val[g * VW + one]);
+          const uint32_t p[4] = {in[g].x, in[g].y, in[g].z, in[g].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 v = fadd2(make_float2(bf16lo_to_f32(p[k]), bf16hi_to_f32(p[k])), x);
+            o[k] = pack_bf16x2(v.x, v.y);
+          }
+          *reinterpret_cast<uint4*>(a.out + row + g * plane + W * t - off[g]) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      } else if (one_chain) {
+        int at[W];
+        const bool run = w.run != 0;
+        const int p0 = w.lo - first_column<W>(a.N, t);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const int j0 = W * t - off[g];
+          if (!whole[g]) continue;
+          if (g == 0 || !ALIGNED) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) at[k] = run ? spread(distance(pi, p0 + j0 + k, a.R)) : place(j0 + k);
+          }
+          float v[8];
+          unpack8(in[g], v);
+#pragma unroll
+          for (int k = 0; k < W; ++k) v[k] += val[g * VW + at[k]];
+          *reinterpret_cast<uint4*>(a.out + row + g * plane + j0) = pack8(v);
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        if (g >= ng) break;
+        uint32_t left = __ballot_sync(0xffffffffu, t < t1 && !whole[g] && W * t - off[g] < a.N);
+        while (left != 0) {
+          int q = -1;
+#pragma unroll
+          for (int k = 0; k < 32 / W; ++k) {
+            if (left != 0 && lane / W == k) q = __ffs(left) - 1;
+            left &= left - 1;
+          }
+          const int j = W * (t0 + q) - off[g] + lane % W;
+          if (q >= 0 && j >= 0 && j < a.N) {
+            const size_t e = row + g * plane + j;
+            const float v = (a.base != nullptr ? bf16lo_to_f32(a.base[e]) : 0.f) + val[g * VW + place(j)];
+            a.out[e] = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xFFFFu);
+          }
+        }
       }
     }
   }
@@ -181,127 +305,204 @@ __global__ void __launch_bounds__(kThreads) relpos_pairs_fwd_kernel(const __grid
 }
 
 // ------------------------------------------------------ planes, gradient
-__device__ __forceinline__ void load8(const uint16_t* p, uint4 (&v)[1]) { v[0] = __ldg(reinterpret_cast<const uint4*>(p)); }
-__device__ __forceinline__ void load8(const float* p, uint4 (&v)[2]) {
-  v[0] = __ldg(reinterpret_cast<const uint4*>(p));
-  v[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+// An element (zero where `in` does not hold) as it is loaded, a register to itself;
+// volatile, so that the loads stay together in front of what uses them.
+__device__ __forceinline__ uint32_t load1(const uint16_t* p, bool in) {
+  uint32_t v;
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.u32 %0, 0;\n @p ld.global.nc.u16 %0, [%1];\n}\n"
+               : "=r"(v)
+               : "l"(p), "r"(static_cast<uint32_t>(in)));
+  return v;
 }
-__device__ __forceinline__ void values(const uint4 (&v)[1], float (&f)[8]) { unpack8(v[0], f); }
-__device__ __forceinline__ void values(const uint4 (&v)[2], float (&f)[8]) {
+__device__ __forceinline__ uint32_t load1(const float* p, bool in) {
+  uint32_t v;
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.u32 %0, 0;\n @p ld.global.nc.u32 %0, [%1];\n}\n"
+               : "=r"(v)
+               : "l"(p), "r"(static_cast<uint32_t>(in)));
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ float value1(uint32_t v) { return sizeof(T) == 2 ? bf16lo_to_f32(v) : __uint_as_float(v); }
+// 16 consecutive elements: their 16-byte pieces, and the values of the pieces.
+template <int V>
+__device__ __forceinline__ void load16(const void* p, uint4 (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = __ldg(static_cast<const uint4*>(p) + i);
+}
+__device__ __forceinline__ void values(const uint4 (&v)[2], float (&f)[16]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[8 * i + 2 * k] = bf16lo_to_f32(w[k]);
+      f[8 * i + 2 * k + 1] = bf16hi_to_f32(w[k]);
+    }
+  }
+}
+__device__ __forceinline__ void values(const uint4 (&v)[4], float (&f)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
     f[4 * i] = __uint_as_float(v[i].x);
     f[4 * i + 1] = __uint_as_float(v[i].y);
     f[4 * i + 2] = __uint_as_float(v[i].z);
     f[4 * i + 3] = __uint_as_float(v[i].w);
   }
 }
-__device__ __forceinline__ float value(uint16_t v) { return bf16lo_to_f32(v); }
-__device__ __forceinline__ float value(float v) { return v; }
 
-// Block: a run of rows of one plane, a row per warp; lane: every 32nd chunk of
-// eight columns, four in flight.  A chunk's positions are known by their smallest
-// and largest (kept per chunk in shared memory): where both give one bucket (all
-// but the pairs near the diagonal), the eight elements are added at once, the
-// buckets of the far ends and of other chains in registers.  Everything else
-// goes to a place of the lane's own (bucket by lane of its warp) in shared memory:
-// no two threads share a sum, so the order is fixed.  The diagonal crosses a
-// different chunk in every row, and every warp meets it as often as the others.
-struct Window {
-  int lo, hi, chain;  // positions of the chunk's columns; its chain
-  int one;            // all of one chain
-};
+// A warp's work is a block of eight rows and 32 chunks of 16 columns of a plane, a
+// chunk to a lane, and what its elements are is asked once for the block:
+//   of other chains, or all of one bucket: all elements are added, in registers for
+//     the buckets of the far ends and of other chains;
+//   on the diagonal: where the positions count up along rows and columns, column j is
+//     at distance i - j from row i in every row, and a lane adds the elements of six
+//     distances of its own, in registers (where the table's distances fit them);
+//   mixed (chains that meet, gaps, other buckets, the ends of rows that do not start
+//     on a chunk): element by element, two rows at a time, a lane to an element, to
+//     a place of the lane's own (bucket by lane of its warp) in shared memory.
+// No two threads share a sum, so the order is fixed.
+// Distances that the lanes hold, [-kNear, kNear), and those of a table that fit: a
+// chunk with one of them in one of the rows has no other's distance above
+// kNearMax + 2 (W - 1) + kRows - 1.
+constexpr int kBwdW = 16, kRows = 8, kNear = 96, kNearMax = 47;
+static_assert(kNearMax + 2 * (kBwdW - 1) + kRows - 1 < kNear, "distances of a chunk on the diagonal");
 template <typename T>
-__global__ void __launch_bounds__(kThreads) relpos_heads_bwd_kernel(const __grid_constant__ RelposArgs a, const T* d_out,
-                                                                    int rows) {
-  constexpr int U = 4;                  // chunks in flight
-  constexpr int V = sizeof(T) / 2;      // 16-byte pieces of a chunk
-  extern __shared__ float sh[];         // windows [chunks], sums [warps][buckets][32]
+__global__ void __launch_bounds__(kThreads, 2) relpos_heads_bwd_kernel(const __grid_constant__ RelposArgs a, const T* d_out) {
+  constexpr int W = kBwdW;
+  constexpr int V = sizeof(T);  // 16-byte pieces of a chunk
+  constexpr int U = 16 / V;     // rows in flight
+  extern __shared__ float sh[];
   __shared__ uint8_t lut[2 * kRelposMaxDistance + 1];
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, nw = blockDim.x / 32;
-  const int nt = chunks_of(a.N), b = blockIdx.y / a.F;
-  Window* win = reinterpret_cast<Window*>(sh);
-  float* hist = sh + 4 * nt;
+  const int nt = chunks_of(a.N, W), b = blockIdx.y / a.F;
+  Window* win = reinterpret_cast<Window*>(sh);  // [chunks]
+  float* hist = sh + (5 * nt + 3) / 4 * 4;      // [warps][buckets][32]
   const int* chain = a.chain != nullptr ? a.chain + static_cast<size_t>(b) * a.N : nullptr;
   for (int d = threadIdx.x; d <= 2 * a.R; d += blockDim.x) lut[d] = a.lut[d];
-  for (int e = threadIdx.x; e < nw * a.buckets * 32; e += blockDim.x) hist[e] = 0.f;
-  for (int t = threadIdx.x; t < nt; t += blockDim.x) {
-    // all columns that the chunk can hold, whatever its rows' alignment
-    const int ja = max(0, a.N % 8 == 0 ? 8 * t : 8 * t - 7), jb = min(a.N, 8 * t + 8);
-    Window w{0x7fffffff, -0x7fffffff - 1, chain != nullptr ? __ldg(chain + ja) : 0, 1};
-    for (int j = ja; j < jb; ++j) {
-      const int p = a.position(b, j);
-      w.lo = min(w.lo, p);
-      w.hi = max(w.hi, p);
-      if (chain != nullptr && __ldg(chain + j) != w.chain) w.one = 0;
-    }
-    win[t] = w;
-  }
+  for (int e = threadIdx.x; e < nw * a.buckets * 8; e += blockDim.x)
+    reinterpret_cast<float4*>(hist)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  make_windows<W>(a, b, nt, win);
   __syncthreads();
   float* mine = hist + warp * a.buckets * 32 + lane;
-  const size_t plane = static_cast<size_t>(a.N) * a.N, p0 = blockIdx.y * plane;
-  const size_t total = static_cast<size_t>(a.B) * a.F * plane;
+  const size_t p0 = static_cast<size_t>(blockIdx.y) * a.N * a.N;
   const int kl = lut[0], kh = lut[2 * a.R], ko = a.buckets - 1;  // far on either side, other chains
-  float sl = 0.f, sh_ = 0.f, so = 0.f;
-  const int i1 = min((static_cast<int>(blockIdx.x) + 1) * rows, a.N);
-  for (int i = blockIdx.x * rows + warp; i < i1; i += nw) {
-    const size_t s = p0 + static_cast<size_t>(i) * a.N;
-    const int off = static_cast<int>(s & 7);
-    const int pi = a.position(b, i), ci = chain != nullptr ? __ldg(chain + i) : 0;
-    for (int t = lane; t < nt; t += U * 32) {
-      uint4 raw[U][V];
+  float sl = 0.f, sh_ = 0.f, so = 0.f, near[kNear / 16];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const size_t e = s - off + 8 * static_cast<size_t>(t + 32 * u);
-        if (t + 32 * u < nt && e + 8 <= total) load8(d_out + e, raw[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int tu = t + 32 * u, j0 = 8 * tu - off;
-        if (tu >= nt || j0 >= a.N) break;
-        float v[8];
-        if (j0 >= 0 && j0 + 8 <= a.N) {
-          values(raw[u], v);
-        } else {  // the ends of a row: what lies outside it counts as zero
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = j0 + k >= 0 && j0 + k < a.N ? value(d_out[s + j0 + k]) : 0.f;
-        }
-        const Window w = win[tu];
-        int ka = ko, kb = ko;
-        if (w.chain == ci || !w.one) {
-          ka = lut[distance(pi, w.hi, a.R)];
-          kb = lut[distance(pi, w.lo, a.R)];
-        }
-        if (w.one && ka == kb) {
-          const float x = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-          if (ka == kl) sl += x;
-          else if (ka == kh) sh_ += x;
-          else if (ka == ko) so += x;
-          else mine[ka * 32] += x;
-        } else {
-          int kk[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int j = min(max(j0 + k, 0), a.N - 1);
-            kk[k] = chain != nullptr && __ldg(chain + j) != ci ? ko : lut[distance(pi, a.position(b, j), a.R)];
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) mine[kk[k] * 32] += v[k];
-        }
+  for (int m = 0; m < kNear / 16; ++m) near[m] = 0.f;
+  const int cols = (nt + 31) / 32, units = (a.N + kRows - 1) / kRows * cols;
+  const int u0 = static_cast<int>(static_cast<long long>(units) * blockIdx.x / gridDim.x);
+  const int u1 = static_cast<int>(static_cast<long long>(units) * (blockIdx.x + 1) / gridDim.x);
+  for (int u = u0 + warp; u < u1; u += nw) {
+    // the rows' diagonals come to all warps in turn
+    const int rb = u / cols, cb = (u - rb * cols + rb * cols / nw) % cols;
+    const int i0 = rb * kRows, nr = min(kRows, a.N - i0), t = 32 * cb + lane;
+    const size_t s0 = p0 + static_cast<size_t>(i0) * a.N;
+    auto off_of = [&](int r) { return static_cast<int>((s0 + static_cast<size_t>(r) * a.N) & (W - 1)); };
+    // the rows' positions and chains
+    const int pi = a.position(b, i0 + min(lane, nr - 1)), ci = chain != nullptr ? __ldg(chain + i0 + min(lane, nr - 1)) : 0;
+    const int rlo = __reduce_min_sync(0xffffffffu, pi), rhi = __reduce_max_sync(0xffffffffu, pi);
+    const int rc = __reduce_min_sync(0xffffffffu, ci), rc1 = __reduce_max_sync(0xffffffffu, ci);
+    const bool rrun = __all_sync(0xffffffffu, static_cast<long long>(pi) - rlo == min(lane, nr - 1));
+    // what the lane's chunk is in all of them
+    enum { kNone, kAll, kDiagonal, kMixed };
+    int kind = kNone, k = ko;
+    if (t < nt) {
+      const Window w = win[t];
+      if (a.N % W != 0 && (t == 0 || W * t + W > a.N)) {
+        kind = kMixed;  // the ends of rows
+      } else if (rc1 < w.chain || rc > w.chain_max) {
+        kind = kAll;
+      } else if (rc != rc1 || w.chain != w.chain_max) {
+        kind = kMixed;
+      } else {
+        k = lut[distance(rhi, w.lo, a.R)];
+        const bool diagonal = rrun && w.run && a.R <= kNearMax &&
+                              static_cast<long long>(rlo) - w.lo == i0 - first_column<W>(a.N, t);
+        kind = k == lut[distance(rlo, w.hi, a.R)] ? kAll : diagonal ? kDiagonal : kMixed;
       }
     }
+    if (kind == kAll) {
+      float x = 0.f;
+      for (int r0 = 0; r0 < nr; r0 += U) {
+        uint4 raw[U][V];
+#pragma unroll
+        for (int q = 0; q < U; ++q)
+          if (r0 + q < nr) load16(d_out + (s0 + static_cast<size_t>(r0 + q) * a.N - off_of(r0 + q) + W * t), raw[q]);
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+          if (r0 + q >= nr) break;
+          float v[W];
+          values(raw[q], v);
+#pragma unroll
+          for (int e = 0; e < W; e += 4) x += (v[e] + v[e + 1]) + (v[e + 2] + v[e + 3]);
+        }
+      }
+      if (k == kl) sl += x;
+      else if (k == kh) sh_ += x;
+      else if (k == ko) so += x;
+      else mine[k * 32] += x;
+    }
+    __syncwarp();
+    const uint32_t diagonals = __ballot_sync(0xffffffffu, kind == kDiagonal);
+    if (diagonals != 0) {
+      for (int r0 = 0; r0 < nr; r0 += 4) {
+        uint32_t x[4][kNear / 16];  // all loads before the first sum
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = r0 + q, j0 = i0 + r + kNear - lane, c0 = j0 + off_of(r) - 32 * W * cb;  // from the chunks' first column
+          const T* row = d_out + s0 + static_cast<size_t>(r) * a.N;
+#pragma unroll
+          for (int m = 0; m < kNear / 16; ++m) {
+            const int j = j0 - 32 * m, c = c0 - 32 * m;
+            const bool in = (r < nr) & (j >= 0) & (j < a.N) & (c >= 0) & (c < 32 * W) & ((diagonals >> ((c / W) & 31)) & 1u);
+            x[q][m] = load1(row + j, in);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int m = 0; m < kNear / 16; ++m) near[m] += value1<T>(x[q][m]);
+      }
+    }
+    for (uint32_t left = __ballot_sync(0xffffffffu, kind == kMixed); left != 0; left &= left - 1) {
+      const int tq = 32 * cb + __ffs(left) - 1;
+      int kk[kRows / 2];
+      uint32_t x[kRows / 2];
+#pragma unroll
+      for (int q = 0; q < kRows / 2; ++q) {
+        const int r = 2 * q + lane / W, i = i0 + min(r, nr - 1), j = W * tq - off_of(r) + lane % W;
+        const bool in = r < nr && j >= 0 && j < a.N;
+        const int jc = min(max(j, 0), a.N - 1);
+        const bool apart = chain != nullptr && __ldg(chain + jc) != __ldg(chain + i);
+        const int d = distance(a.position(b, i), a.position(b, jc), a.R);
+        kk[q] = in ? (apart ? ko : lut[d]) : -1;
+        x[q] = load1(d_out + s0 + static_cast<size_t>(r) * a.N + j, in);
+      }
+#pragma unroll
+      for (int q = 0; q < kRows / 2; ++q)
+        if (kk[q] >= 0) mine[kk[q] * 32] += value1<T>(x[q]);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < kNear / 16; ++m) {
+    const int d = 32 * m + lane - kNear;
+    mine[lut[min(max(d, -a.R), a.R) + a.R] * 32] += near[m];
   }
   mine[kl * 32] += sl;
   mine[kh * 32] += sh_;
   mine[ko * 32] += so;
   __syncthreads();
   float* out = a.part + (static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x) * a.buckets;
-  for (int k = warp; k < a.buckets; k += nw) {
+  for (int k0 = 4 * warp; k0 < a.buckets; k0 += 4 * nw) {  // four buckets, eight lanes to a bucket's 32 places
+    const int k = min(k0 + lane / 8, a.buckets - 1);
     float v = 0.f;
-    for (int w = 0; w < nw; ++w) v += hist[(w * a.buckets + k) * 32 + lane];
+    for (int w = 0; w < nw; ++w) {
+      const float4 x = reinterpret_cast<const float4*>(hist)[(w * a.buckets + k) * 8 + lane % 8];
+      v += (x.x + x.y) + (x.z + x.w);
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0) out[k] = v;
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane % 8 == 0 && k0 + lane / 8 < a.buckets) out[k] = v;
   }
 }
 
@@ -385,27 +586,21 @@ RelposArgs args_of(const triattn_relpos_shape* s, const int* positions, const in
   return a;
 }
 
-// Rows per block of `planes` planes of N rows, so that about `want` blocks run.
-int rows_per_block(int N, long long planes, int want) {
-  const long long blocks = std::max(1ll, std::min<long long>(N, want / planes));
-  return static_cast<int>((N + blocks - 1) / blocks);
-}
-
 // Planes' gradient: as many warps as three, two or one blocks an SM have room
 // for, at least four if they can be had.
 struct BwdPlan {
-  int warps, rows, splits;
+  int warps, splits;
   size_t smem;
 };
 BwdPlan bwd_plan(int B, int N, int F, int buckets) {
   BwdPlan p;
-  const size_t win = static_cast<size_t>(chunks_of(N)) * sizeof(Window);
+  const size_t win = (static_cast<size_t>(chunks_of(N, kBwdW)) * sizeof(Window) + 15) / 16 * 16;
   p.warps = kThreads / 32;
   while (p.warps > 1 && win + static_cast<size_t>(p.warps) * buckets * 128 > (p.warps > 4 ? 72000u : 216000u)) p.warps /= 2;
   p.smem = win + static_cast<size_t>(p.warps) * buckets * 128;
-  const int per_sm = std::max(1, std::min<int>(2048 / (32 * p.warps), static_cast<int>(220000 / (p.smem + 3200))));
-  p.rows = rows_per_block(N, static_cast<long long>(B) * F, 152 * per_sm * 2);
-  p.splits = (N + p.rows - 1) / p.rows;
+  const int per_sm = std::max(1, std::min<int>(16 / p.warps, static_cast<int>(232448 / (p.smem + 3200))));
+  const int units = (N + kRows - 1) / kRows * ((chunks_of(N, kBwdW) + 31) / 32);
+  p.splits = std::max(1, std::min((units + p.warps - 1) / p.warps, static_cast<int>(152ll * per_sm / (static_cast<long long>(B) * F))));
   return p;
 }
 
@@ -424,14 +619,16 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic);
 }
 
-template <int G>
+template <bool ALIGNED>
 cudaError_t launch_heads_fwd(const RelposArgs& a, cudaStream_t s) {
-  const int groups = (a.F + G - 1) / G;
-  const size_t smem = 4ull * (G * (spread(2 * a.R + 1) + 1) + (a.chain != nullptr ? 2 : 1) * (spread(a.N - 1) + 1));
-  cudaError_t e = allow_smem(relpos_heads_fwd_kernel<G>, smem);
+  const int groups = (a.F + kHeadGroup - 1) / kHeadGroup;
+  const int nt = chunks_of(a.N, 8);
+  const size_t smem = sizeof(Window) * nt + 4ull * kHeadGroup * (spread(2 * a.R + 1) + 1);
+  cudaError_t e = allow_smem(relpos_heads_fwd_kernel<ALIGNED>, smem);
   if (e != cudaSuccess) return e;
-  const int rows = rows_per_block(a.N, static_cast<long long>(a.B) * groups, 152 * 6);
-  relpos_heads_fwd_kernel<G><<<dim3((a.N + rows - 1) / rows, a.B * groups), kThreads, smem, s>>>(a, rows);
+  const int units = a.N * Units(nt).segs, blocks = 152 * kFwdBlocks / (a.B * groups);
+  relpos_heads_fwd_kernel<ALIGNED><<<dim3(std::max(1, std::min((units + 7) / 8, blocks)), a.B * groups), kThreads, smem,
+                                     s>>>(a);
   return cudaGetLastError();
 }
 
@@ -447,7 +644,7 @@ cudaError_t launch_heads_bwd(const RelposArgs& a, const void* d_out, const BwdPl
   cudaError_t e = allow_smem(relpos_heads_bwd_kernel<T>, p.smem);
   if (e != cudaSuccess) return e;
   relpos_heads_bwd_kernel<T><<<dim3(p.splits, a.B * a.F), p.warps * 32, p.smem, s>>>(
-      a, static_cast<const T*>(d_out), p.rows);
+      a, static_cast<const T*>(d_out));
   return cudaGetLastError();
 }
 
@@ -478,8 +675,7 @@ triattn_status triattn_relpos_fwd(const triattn_relpos_shape* shape, const float
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = trace_call(kKRelFwd, s, [&] {
     if (shape->layout == TRIATTN_RELPOS_PAIRS) return launch_pairs_fwd(a, s);
-    // rows off 16 bytes start elsewhere in every plane: one head at a time
-    return shape->N % 8 == 0 ? launch_heads_fwd<kHeadGroup>(a, s) : launch_heads_fwd<1>(a, s);
+    return shape->N % 8 == 0 ? launch_heads_fwd<true>(a, s) : launch_heads_fwd<false>(a, s);
   });
   return e == cudaSuccess ? TRIATTN_OK : TRIATTN_ERR_CUDA;
 }

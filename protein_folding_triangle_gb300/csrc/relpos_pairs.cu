@@ -18,8 +18,7 @@
 //              turns, and a run is at most kRun blocks of 64 pairs, so that no
 //              accumulator adds more than 4 kRun products of 16: the tensor
 //              cores cut off what an FP32 accumulator cannot hold.
-//   warps 2-5  one pair per thread, two warps for the even and two for the odd
-//              stages: its bucket (of the next stage while they wait for this
+//   warps 2-9  one pair per thread, two warps per stage, in turn: its bucket (of the next stage while they wait for this
 //              one), then the two bytes of its one in B [buckets, 64 pairs]
 //              (K-major, swizzled), after the one that the stage held before is
 //              put out.
@@ -49,11 +48,13 @@ struct Bars {
 struct PairsBwd {
   long long P;                  // pairs
   int nb, mt, sets, stages;     // buckets to 16, 128-feature tiles, accumulators per tile, ring stages
+  int groups;                   // that place the ones, a divisor of the stages: a stage's ones are always one group's
   int stage_bytes, a_bytes;
   WaitCtl wc;
 };
 
-constexpr int kPairThreads = 192;
+constexpr int kGroups = 4;  // of two warps that place the ones
+constexpr int kPairThreads = 64 + 64 * kGroups;
 
 __global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const __grid_constant__ CUtensorMap tm,
                                                                   const __grid_constant__ RelposArgs a, PairsBwd p) {
@@ -65,14 +66,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const
   volatile int* abort = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int d = threadIdx.x; d <= 2 * a.R; d += kPairThreads) lut[d] = a.lut[d];
-  for (int s = 0; s < p.stages; ++s) {
-    uint4* e = reinterpret_cast<uint4*>(sm + s * p.stage_bytes + p.a_bytes);
-    for (int k = threadIdx.x; k < p.nb * 8; k += kPairThreads) e[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (threadIdx.x < kBlk) held[s][threadIdx.x] = kNone;
-  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&bars.full[s], 1 + kBlk);
+      mbar_init(&bars.full[s], 1 + 2);
       mbar_init(&bars.empty[s], 1);
     }
     mbar_init(&bars.done, 1);
@@ -80,7 +76,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&bars.tmem_slot, 512);
-  fence_proxy_async_smem();  // the cleared stages
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -105,28 +100,35 @@ __global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const
     }
   } else if (warp == 1) {
     const uint32_t idesc = idesc_bf16_f32(128, p.nb, 1, 0);
-    int stage = 0, phase = 0;
+    // operands by the low words of their descriptors: what the one issuing thread
+    // computes per stage has to stay below the 700 cycles that a stage's bytes take
+    const uint32_t s0 = smem_u32(sm) >> 4, stage_w = p.stage_bytes / 16;
+    const uint32_t a0 = s0 | (kBlk * 128 / 16) << 16, e0 = (s0 + p.a_bytes / 16) | (1u << 16);
+    const uint32_t set_cols = p.mt * p.nb;
+    int stage = 0, phase = 0, set = 0;
     for (int k = 0; k < n; ++k) {
       if (!__all_sync(0xffffffffu, mbar_wait(&bars.full[stage], phase, p.wc, abort))) break;
       tc_fence_after();
-      const uint32_t sa = smem_u32(sm + stage * p.stage_bytes), sb = sa + p.a_bytes;
+      const uint32_t xa = a0 + stage * stage_w, xe = e0 + stage * stage_w, d = tmem + set * set_cols;
+      const uint32_t more = k >= p.sets ? 1u : 0u;
       if (elect_one()) {
-        const int set = k % p.sets;
-        for (int m = 0; m < p.mt; ++m)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          if (m == p.mt) break;
 #pragma unroll
           for (int k16 = 0; k16 < kBlk / 16; ++k16)
-            mma_ss(tmem + (set * p.mt + m) * p.nb,
-                   smem_desc(sa + m * 2 * kBlk * 128 + k16 * 2048, kBlk * 128, 1024, 2),
-                   smem_desc(sb + k16 * 32, 16, 1024, 2), idesc, (k >= p.sets || k16 > 0) ? 1u : 0u);
+            mma_ss_w(d + m * p.nb, xa + m * (2 * kBlk * 128 / 16) + k16 * 128, xe + k16 * 2, idesc, k16 > 0 ? 1u : more);
+        }
         mma_commit(&bars.empty[stage]);
         if (k == n - 1) mma_commit(&bars.done);
       }
       __syncwarp();
+      if (++set == p.sets) set = 0;
       if (++stage == p.stages) { stage = 0; phase ^= 1; }
     }
   } else {
-    const int c = threadIdx.x & 63, odd = warp >= 4;  // the pair of the block
-    long long q = (b0 + odd) * kBlk + c;
+    const int c = threadIdx.x & 63, group = (warp - 2) >> 1;  // the pair of the block
+    long long q = (b0 + group) * kBlk + c;
     const long long NN = static_cast<long long>(a.N) * a.N;
     int b = static_cast<int>(q / NN), i = static_cast<int>((q - b * NN) / a.N);
     int j = static_cast<int>(q - b * NN - static_cast<long long>(i) * a.N);
@@ -136,9 +138,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const
       const bool other = a.chain != nullptr && __ldg(a.chain + at + i) != __ldg(a.chain + at + j);
       return other ? a.buckets - 1 : static_cast<int>(lut[distance(a.position(b, i), a.position(b, j), a.R)]);
     };
-    auto next = [&]() {  // two blocks on
-      q += 2 * kBlk;
-      j += 2 * kBlk;
+    auto next = [&]() {  // to the group's next block
+      q += p.groups * kBlk;
+      j += p.groups * kBlk;
       if (j >= a.N) {
         const int w = j / a.N;
         j -= w * a.N;
@@ -151,18 +153,23 @@ __global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const
       }
     };
     int row = bucket();
-    for (int k = odd; k < n; k += 2) {
+    for (int k = group; k < n && group < p.groups; k += p.groups) {
       const int stage = k % p.stages, phase = (k / p.stages) & 1;
       next();
-      const int row_next = k + 2 < n ? bucket() : -1;
-      if (!mbar_wait(&bars.empty[stage], phase ^ 1, p.wc, abort)) break;
+      const int row_next = k + p.groups < n ? bucket() : -1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars.empty[stage], phase ^ 1, p.wc, abort))) break;
       uint16_t* e = reinterpret_cast<uint16_t*>(sm + stage * p.stage_bytes + p.a_bytes);
-      if (held[stage][c] != kNone) e[held[stage][c]] = 0;
+      if (k < p.stages) {  // a fresh stage: the pair's column of zeros
+        for (int r = 0; r < p.nb; ++r) e[sw128(r, c >> 3) / 2 + (c & 7)] = 0;
+      } else if (held[stage][c] != kNone) {
+        e[held[stage][c]] = 0;
+      }
       const uint16_t at = row >= 0 ? static_cast<uint16_t>(sw128(row, c >> 3) / 2 + (c & 7)) : kNone;
       if (at != kNone) e[at] = 0x3F80;  // 1
       held[stage][c] = at;
       fence_proxy_async_smem();
-      mbar_arrive(&bars.full[stage]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.full[stage]);
       row = row_next;
     }
   }
@@ -222,7 +229,9 @@ cudaError_t launch_relpos_pairs_bwd(const RelposArgs& a, const void* d_out, int 
   p.a_bytes = p.mt * 2 * kBlk * 128;
   p.stage_bytes = p.a_bytes + p.nb * 128;
   p.stage_bytes = (p.stage_bytes + 1023) / 1024 * 1024;
-  p.stages = std::min(kStagesMax, (kSmemMax - 1024) / p.stage_bytes) & ~1;  // even: a stage's ones are always one warp's
+  p.stages = std::min(kStagesMax, (kSmemMax - 1024) / p.stage_bytes);
+  p.groups = p.stages >= kGroups ? kGroups : 2;
+  p.stages -= p.stages % p.groups;
   p.wc = wc;
   CUtensorMap tm;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.F), static_cast<cuuint64_t>(p.P), 1};

@@ -820,17 +820,19 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _rows_pair(a, b, names, shape, device):
+def _rows_pair(a, b, names, shape, dev: int):
     """The layout that two [B, N_o, H, N, D] views share, None where both are contiguous."""
-    if a.is_contiguous() and b.is_contiguous():
-        for name, t in zip(names, (a, b)):
-            _check(t, name, shape)
-        lay = None
-    else:
-        lay = layout_of(a)
-        for name, t in zip(names, (a, b)):
-            _check_view(t, name, shape, lay)
-    _same_device(device, **dict(zip(names, (a, b))))
+    bf16 = torch.bfloat16
+    if (a.dtype is bf16 and b.dtype is bf16 and a.shape == shape and b.shape == shape and dev >= 0
+            and a.get_device() == dev and b.get_device() == dev):
+        if a.is_contiguous() and b.is_contiguous():
+            return None
+        if a.stride() == b.stride():
+            return layout_of(a)
+    lay = layout_of(a)
+    for name, t in zip(names, (a, b)):
+        _check_view(t, name, shape, lay)
+    _same_device(torch.device("cuda", dev), **dict(zip(names, (a, b))))
     return lay
 
 
@@ -845,15 +847,23 @@ def qk_norm_shape(shape, w, rotary: str = "half", theta: float = 10000.0, eps: f
 
 
 def _qk_norm_check(q, k, w_q, w_k, positions, rotary, theta, eps):
-    s = qk_norm_shape(q.shape, w_q, rotary, theta, eps)
-    lay = _rows_pair(q, k, ("q", "k"), q.shape, q.device)
-    w_shape = (s.D,) if w_q.dim() == 1 else (s.H, s.D)
-    _check(w_q, "w_q", w_shape, torch.float32)
-    _check(w_k, "w_k", w_shape, torch.float32)
-    if positions is not None:
-        _check(positions, "positions", (s.B, s.N), torch.int32)
-    _same_device(q.device, w_q=w_q, w_k=w_k, positions=positions)
+    shape, dev, f32 = q.shape, q.get_device(), torch.float32
+    s = qk_norm_shape(shape, w_q, rotary, theta, eps)
+    lay = _rows_pair(q, k, ("q", "k"), shape, dev)
+    w_shape = (s.D,) if s.w_heads == 1 and w_q.dim() == 1 else (s.H, s.D)
+    if not (_fits(w_q, dev, w_shape, f32) and _fits(w_k, dev, w_shape, f32)
+            and (positions is None or _fits(positions, dev, (s.B, s.N), torch.int32))):
+        _check(w_q, "w_q", w_shape, f32)
+        _check(w_k, "w_k", w_shape, f32)
+        if positions is not None:
+            _check(positions, "positions", (s.B, s.N), torch.int32)
+        _same_device(q.device, w_q=w_q, w_k=w_k, positions=positions)
     return s, lay
+
+
+def _rows_like(q, lay):
+    """A contiguous tensor of q's shape."""
+    return torch.empty_like(q) if lay is None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
 
 
 def _ref(lay):
@@ -873,9 +883,9 @@ def triattn_qk_norm_fwd(q, k, w_q, w_k, positions=None, rotary: str = "half", *,
     given, lo = out, None
     with here:
         if out is None:
-            out = tuple(torch.empty(q.shape, dtype=q.dtype, device=q.device) for _ in range(2))
+            out = _rows_like(q, lay), _rows_like(q, lay)
         else:
-            lo = _rows_pair(*out, ("q_out", "k_out"), q.shape, q.device)
+            lo = _rows_pair(*out, ("q_out", "k_out"), q.shape, q.get_device())
         qo, ko = out
         code = load().triattn_qk_norm_fwd(ctypes.byref(s), q.data_ptr(), k.data_ptr(), _ref(lay), w_q.data_ptr(),
                                           w_k.data_ptr(), _address(positions), qo.data_ptr(), ko.data_ptr(), _ref(lo),
@@ -893,7 +903,7 @@ def triattn_qk_norm_bwd(q, k, w_q, w_k, d_q_out, d_k_out, positions=None, rotary
     pass them preallocated, dq and dk also as views, or d_q_out and d_k_out
     themselves."""
     s, lay = _qk_norm_check(q, k, w_q, w_k, positions, rotary, theta, eps)
-    ld = _rows_pair(d_q_out, d_k_out, ("d_q_out", "d_k_out"), q.shape, q.device)
+    ld = _rows_pair(d_q_out, d_k_out, ("d_q_out", "d_k_out"), q.shape, q.get_device())
     lib = load()
     need = lib.triattn_qk_norm_workspace_bytes(ctypes.byref(s))
     if need == 0:
@@ -906,12 +916,10 @@ def triattn_qk_norm_bwd(q, k, w_q, w_k, d_q_out, d_k_out, positions=None, rotary
         else:
             _same_device(q.device, workspace=workspace)
         if out is None:
-            out = tuple(torch.empty(q.shape, dtype=q.dtype, device=q.device) for _ in range(2))
-            out += (torch.empty_like(w_q), torch.empty_like(w_k))
-            dq, dk, dwq, dwk = out
+            dq, dk, dwq, dwk = (_rows_like(q, lay), _rows_like(q, lay), torch.empty_like(w_q), torch.empty_like(w_k))
         else:
             dq, dk, dwq, dwk = out
-            lg = _rows_pair(dq, dk, ("dq", "dk"), q.shape, q.device)
+            lg = _rows_pair(dq, dk, ("dq", "dk"), q.shape, q.get_device())
             _check(dwq, "d_w_q", w_q.shape, torch.float32)
             _check(dwk, "d_w_k", w_k.shape, torch.float32)
             _same_device(q.device, d_w_q=dwq, d_w_k=dwk)
@@ -936,6 +944,9 @@ def relpos_shape(B: int, N: int, F: int, buckets: int, layout: str = "heads", ki
 
 
 def _relpos_ids(positions, chains, B, N, device):
+    dev, i32 = device.index, torch.int32
+    if ((positions is None or _fits(positions, dev, (B, N), i32)) and (chains is None or _fits(chains, dev, (B, N), i32))):
+        return
     for name, t in (("positions", positions), ("chains", chains)):
         if t is not None:
             _check(t, name, (B, N), torch.int32)
@@ -967,10 +978,13 @@ def triattn_relpos_fwd(table, base=None, positions=None, chains=None, *, layout:
         raise ValueError("base, out or positions [B, N] must be given")
     s = relpos_shape(B, N, F, K, layout, kind, max_distance)
     shape = (B, F, N, N) if layout == "heads" else (B, N, N, F)
-    _check(table, "table", (K, F), torch.float32)
-    if base is not None:
-        _check(base, "base", shape)
-        _same_device(device, base=base)
+    dev = table.get_device()
+    if not (_fits(table, dev, (K, F), torch.float32) and dev >= 0
+            and (base is None or _fits(base, dev, shape, torch.bfloat16))):
+        _check(table, "table", (K, F), torch.float32)
+        if base is not None:
+            _check(base, "base", shape)
+            _same_device(device, base=base)
     _relpos_ids(positions, chains, B, N, device)
     here, sp = _on_stream(device, stream)
     given = out
@@ -1130,18 +1144,36 @@ def triattn_clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, *, 
     return norm
 
 
+_shape_of = operator.attrgetter("shape")
+
+
 def _matrix_table(tensors, name, device):
-    """The triattn_matrix array of a list of 2-D tensors, five words each."""
-    rows = []
-    for i, t in enumerate(tensors):
-        if t.dim() != 2 or t.dtype not in GRAD_DTYPES or t.device != device or t.layout != torch.strided:
-            raise ValueError(f"{name}[{i}] must be a 2-D bfloat16 or float32 tensor on {device}")
-        m, n = t.shape
-        stride = t.stride(0) if m > 1 else n
-        if (n > 1 and t.stride(1) != 1) or (stride < n and t.numel()):
-            raise ValueError(f"{name}[{i}] must have contiguous rows")
-        rows += (t.data_ptr(), m, n, stride, GRAD_DTYPES[t.dtype])
-    return struct.pack(f"{len(rows)}q", *rows)
+    """The triattn_matrix array of a list of 2-D tensors as bytes (address, rows,
+    columns, stride and dtype, eight each), and their shapes.  Column by column,
+    like _tensor_table."""
+    n = len(tensors)
+    shapes = list(map(_shape_of, tensors))
+    rows = [0] * (5 * n)
+    try:
+        plain = (set(map(len, shapes)) <= {2} and all(map(torch.Tensor.is_contiguous, tensors))
+                 and set(map(torch.Tensor.get_device, tensors)) <= {device.index})
+        rows[4::5] = map(GRAD_DTYPES.__getitem__, map(_dtype_of, tensors))
+        rows[0::5] = map(torch.Tensor.data_ptr, tensors)
+        if plain and n:
+            rows[1::5], cols = zip(*shapes)
+            rows[2::5] = rows[3::5] = cols
+    except (KeyError, RuntimeError):
+        plain = False
+    if not plain:
+        for i, t in enumerate(tensors):
+            if t.dim() != 2 or t.dtype not in GRAD_DTYPES or t.device != device or t.layout != torch.strided:
+                raise ValueError(f"{name}[{i}] must be a 2-D bfloat16 or float32 tensor on {device}")
+            r, c = t.shape
+            stride = t.stride(0) if r > 1 else c
+            if (c > 1 and t.stride(1) != 1) or (stride < c and t.numel()):
+                raise ValueError(f"{name}[{i}] must have contiguous rows")
+            rows[5 * i:5 * i + 5] = (t.data_ptr(), r, c, stride, GRAD_DTYPES[t.dtype])
+    return struct.pack(f"{5 * n}q", *rows), shapes
 
 
 ORTHOGONALIZE = (3.4445, -4.7750, 2.0315)
@@ -1162,21 +1194,22 @@ def triattn_orthogonalize(tensors, steps: int = 5, *, coefficients=ORTHOGONALIZE
     if device.type != "cuda":
         raise ValueError("the matrices must be CUDA tensors")
     n = len(tensors)
-    table = _matrix_table(tensors, "tensors", device)
+    table, shapes = _matrix_table(tensors, "tensors", device)
     here, sp = _on_stream(device, stream)
     given = out
     lib = load()
     with here:
         if out is None:
-            out = [torch.empty(t.shape, dtype=torch.bfloat16, device=device) for t in tensors]
+            out = [torch.empty(shape, dtype=torch.bfloat16, device=device) for shape in shapes]
         else:
             out = [out] if isinstance(out, torch.Tensor) else list(out)
             if len(out) != n:
                 raise ValueError(f"out has {len(out)} tensors, expected {n}")
+        into, shapes_out = _matrix_table(out, "out", device)
+        if shapes != shapes_out or set(map(_dtype_of, out)) - {torch.bfloat16}:
             for i, (a, b) in enumerate(zip(tensors, out)):
                 if a.shape != b.shape or b.dtype is not torch.bfloat16:
                     raise ValueError(f"out[{i}] must be a bfloat16 tensor of the shape of tensors[{i}]")
-        into = _matrix_table(out, "out", device)
         need = lib.triattn_orthogonalize_workspace_bytes(table, n)
         if need == 0:
             raise TriAttnError(ERR_UNSUPPORTED, "triattn_orthogonalize")

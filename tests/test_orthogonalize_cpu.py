@@ -85,7 +85,7 @@ def test_python_refusals(lib):
         with pytest.raises(ValueError):
             T._matrix_table([bad], "tensors", dev)
     for good in (t, t[:, 1:3], t[:1], t[:, :1], t[::2]):
-        assert len(T._matrix_table([good], "tensors", dev)) == 40
+        assert len(T._matrix_table([good], "tensors", dev)[0]) == 40
     with pytest.raises(ValueError):
         T.triattn_orthogonalize([t])
     with pytest.raises(ValueError):
