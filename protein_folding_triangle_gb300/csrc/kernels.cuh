@@ -209,4 +209,25 @@ cudaError_t trace_call(int kind, cudaStream_t s, F&& launch) {
       kind, s, [](void* f) -> cudaError_t { return (*static_cast<std::remove_reference_t<F>*>(f))(); }, &launch);
 }
 
+// Launch of a kernel that starts with after_previous(): its blocks may come up
+// while the kernel before it in the stream still runs, as soon as each of that
+// one's blocks has let_next_start() or ended, and wait there for its results.  The
+// first kernel of a call is not launched so (`alone`): what stands before it in the
+// stream is not ours.
+template <typename... P, typename... A>
+cudaError_t launch_after(bool alone, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
+                         A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = alone ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 }  // namespace triattn

@@ -69,6 +69,8 @@ __global__ void __launch_bounds__(kThreads, 1) orth_solo_kernel(const OrthMat* m
   volatile int* abort = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = T > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  let_next_start();
+  after_previous();
   const OrthMat q = mats[blockIdx.x / T];
   const int chunks = (q.n + 63) / 64;
   const int c0 = chunks * rank / T, nloc = chunks * (rank + 1) / T - c0;
@@ -515,12 +517,14 @@ cudaError_t launch_orth_solo(const OrthMat* mats, int n, uint8_t* tiles, int ste
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = team;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = team;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, orth_solo_kernel, mats, tiles, steps, co, team, wc);
 }
 

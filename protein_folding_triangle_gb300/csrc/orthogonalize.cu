@@ -46,16 +46,18 @@ struct OrthTable {
 static_assert(sizeof(OrthTable) + 32 <= 32764, "kernel parameter limit");
 
 __global__ void __launch_bounds__(256) orth_table_kernel(const __grid_constant__ OrthTable t, OrthMat* to) {
+  let_next_start();
+  after_previous();  // what last used the workspace
   if (threadIdx.x < t.n) to[threadIdx.x] = t.mat[threadIdx.x];
 }
 
 // The matrix that item `at` belongs to (the last whose first item is not above it), by a whole warp.
 template <int OrthMat::* FIRST>
-__device__ __forceinline__ int find(const OrthView& v, int at) {
-  int lo = 0, n = v.n;  // it is one of [lo, lo + n)
+__device__ __forceinline__ int find(const OrthMat* mat, int count, int at) {
+  int lo = 0, n = count;  // it is one of [lo, lo + n)
   while (n > 1) {
     const int step = (n + 31) / 32, i = static_cast<int>(threadIdx.x & 31) * step;
-    const uint32_t below = __ballot_sync(0xffffffffu, i < n && v.mat[lo + i].*FIRST <= at);
+    const uint32_t below = __ballot_sync(0xffffffffu, i < n && mat[lo + i].*FIRST <= at);
     const int part = 31 - __clz(below);
     lo += part * step;
     n = min(step, n - part * step);
@@ -67,20 +69,65 @@ __device__ __forceinline__ float element(const OrthMat& q, long long at) {
   return (q.flags & kOrthFp32) ? __ldg(static_cast<const float*>(q.src) + at)
                            : bf16lo_to_f32(__ldg(static_cast<const uint16_t*>(q.src) + at));
 }
+// Eight consecutive elements from `at`, a multiple of eight from an address on 16 bytes.
+__device__ __forceinline__ void elements8(const OrthMat& q, long long at, float (&y)[8]) {
+  if (q.flags & kOrthFp32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(q.src) + at);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    y[0] = a.x;
+    y[1] = a.y;
+    y[2] = a.z;
+    y[3] = a.w;
+    y[4] = b.x;
+    y[5] = b.y;
+    y[6] = b.z;
+    y[7] = b.w;
+  } else {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(q.src) + at));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[2 * i] = bf16lo_to_f32(w[i]);
+      y[2 * i + 1] = bf16hi_to_f32(w[i]);
+    }
+  }
+}
+__device__ __forceinline__ bool on16(const OrthMat& q) { return (reinterpret_cast<uintptr_t>(q.src) & 15) == 0; }
 
-// Sums of squares, one partial per run of rows of the source.
-__global__ void __launch_bounds__(256) orth_norm_kernel(OrthView v) {
+// Sums of squares, one partial per kNormPart elements of the source in the order of
+// its rows.  A short list's table is a parameter, which the first block puts where
+// the later kernels look for it.
+constexpr int kNormPart = 4096;
+template <bool PARAM>
+__global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ OrthTable t, OrthView v, OrthMat* to) {
   __shared__ float sh[8];
-  const int k = find<&OrthMat::part0>(v, blockIdx.x);
-  const OrthMat q = v.mat[k];
+  let_next_start();
+  after_previous();  // the table, or what last used the workspace
+  if (PARAM && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < t.n; i += 256) to[i] = t.mat[i];
+  const OrthMat* mat = PARAM ? t.mat : v.mat;
+  const OrthMat q = mat[find<&OrthMat::part0>(mat, PARAM ? t.n : v.n, blockIdx.x)];
   const int rows = (q.flags & kOrthTall) ? q.n : q.m, cols = (q.flags & kOrthTall) ? q.m : q.n;
-  const int r0 = (blockIdx.x - q.part0) * q.part_rows, r1 = min(r0 + q.part_rows, rows);
+  const long long n = static_cast<long long>(rows) * cols, e0 = static_cast<long long>(blockIdx.x - q.part0) * kNormPart;
   float s = 0.f;
-  const int e = (r1 - r0) * cols;  // part_rows keeps this small unless a row is long
-  for (int i = threadIdx.x; i < e; i += 256) {
-    const int r = i / cols;
-    const float x = element(q, (r0 + r) * q.ld_src + (i - r * cols));
-    s += x * x;
+  if (q.ld_src == cols && on16(q) && e0 + kNormPart <= n) {
+#pragma unroll
+    for (int u = 0; u < kNormPart / 2048; ++u) {
+      float y[8];
+      elements8(q, e0 + 2048 * u + 8 * threadIdx.x, y);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += y[k] * y[k];
+    }
+  } else {
+    const int m = static_cast<int>(min(static_cast<long long>(kNormPart), n - e0));
+    const long long r0 = e0 / cols;
+    const int c0 = static_cast<int>(e0 - r0 * cols);
+#pragma unroll 8
+    for (int i = threadIdx.x; i < m; i += 256) {
+      const int r = (c0 + i) / cols;
+      const float x = element(q, (r0 + r) * q.ld_src + (c0 + i - r * cols));
+      s += x * x;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -95,51 +142,62 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(OrthView v) {
 
 // One tile of X per block: normed, scaled, split, in the image's order.
 __global__ void __launch_bounds__(256) orth_load_kernel(OrthView v, float eps) {
-  __shared__ double sh[256];
-  const int k = find<&OrthMat::tiles0>(v, blockIdx.x);
-  const OrthMat q = v.mat[k];
-  double s = 0.0;
-  for (int i = threadIdx.x; i < q.parts; i += 256) s += v.part[q.part0 + i];
-  sh[threadIdx.x] = s;
-  __syncthreads();
-  for (int o = 128; o > 0; o >>= 1) {
-    if (threadIdx.x < o) sh[threadIdx.x] += sh[threadIdx.x + o];
-    __syncthreads();
-  }
-  const float scale = static_cast<float>(static_cast<double>(kOrthScale) / (sqrt(sh[0]) + eps));
+  __shared__ double sh[8];
+  let_next_start();
+  after_previous();
+  const OrthMat q = v.mat[find<&OrthMat::tiles0>(v.mat, v.n, blockIdx.x)];
   const int t = blockIdx.x - q.tiles0, i = t / (2 * q.nt), c = t - i * 2 * q.nt;
-  uint8_t* out = tile_at(v, q.x[0] + t);
   const bool tall = (q.flags & kOrthTall) != 0;
+  const bool wide = !tall && on16(q) && q.ld_src % 8 == 0;
+  float y[4][8];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int e = threadIdx.x + 256 * u;
     // lanes along what is contiguous in memory: columns, or rows of a transposed matrix
     const int r = tall ? e & 127 : e >> 3, p = tall ? e >> 7 : e & 7;
     const int row = i * 128 + r, col = c * 64 + p * 8;
-    float y[8];
+    if (wide && row < q.m && col + 8 <= q.n) {
+      elements8(q, row * q.ld_src + col, y[u]);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const bool in = row < q.m && col + j < q.n;
-      const long long at = tall ? (col + j) * q.ld_src + row : row * q.ld_src + col + j;
-      y[j] = in ? element(q, at) * scale : 0.f;
+      for (int j = 0; j < 8; ++j) {
+        const bool in = row < q.m && col + j < q.n;
+        y[u][j] = in ? element(q, tall ? (col + j) * q.ld_src + row : row * q.ld_src + col + j) : 0.f;
+      }
     }
+  }
+  double s = 0.0;
+  for (int k = threadIdx.x; k < q.parts; k += 256) s += v.part[q.part0 + k];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = ((sh[0] + sh[1]) + (sh[2] + sh[3])) + ((sh[4] + sh[5]) + (sh[6] + sh[7]));
+  const float scale = static_cast<float>(static_cast<double>(kOrthScale) / (sqrt(s) + eps));
+  uint8_t* out = tile_at(v, q.x[0] + t);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int e = threadIdx.x + 256 * u, r = tall ? e & 127 : e >> 3, p = tall ? e >> 7 : e & 7;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[u][j] *= scale;
     uint4 hi, lo;
-    split8(y, hi, lo);
+    split8(y[u], hi, lo);
     *reinterpret_cast<uint4*>(out + sw128(r, p)) = hi;
     *reinterpret_cast<uint4*>(out + kOrthPlane + sw128(r, p)) = lo;
   }
 }
 
 // ------------------------------------------------------------- products
-constexpr int kStages = 3;
-constexpr int kStage = 2 * kOrthTile;  // the A and the B operand of 64 of K
-constexpr int kEpiWarps = 4;
-constexpr int kStg = 8192;         // staging of an epilogue warp: 32 rows of a tile, hi and lo
+constexpr int kStages = 4;
+constexpr int kStage = kOrthTile + kOrthTile / 2;  // 64 of K: 128 rows of A, 64 columns of B, hi and lo
+constexpr int kEpiWarps = 8;
+constexpr int kStg = 8192;  // staging of 32 rows of a tile, hi and lo
 constexpr int kThreads = (2 + kEpiWarps) * 32;
-constexpr int kSmem = kStages * kStage + kEpiWarps * kStg + 1024;
+constexpr int kSmem = kStages * kStage + 4 * kStg + 1024;
 
 struct GemmBars {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+  uint64_t pair[4];  // the two warps of a quarter of the rows
   uint32_t tmem_slot;
   int abort;
 };
@@ -152,11 +210,13 @@ struct OrthStep {
   WaitCtl wc;
 };
 
-// Operand pairs of one 128 x 128 tile of phase PHASE's product.  One CTA per SM,
-// tiles in turn: warp 0 loads (64 of K per stage, 64 KB), warp 1 issues twelve
-// MMAs per stage (four of K by three products), warps 2-5 take the accumulator
-// (one of two) out, scale it, split it and store it through shared memory as bulk
-// copies of 4 KB.
+// 128 x 64 tiles of phase PHASE's product.  One CTA per SM, tiles in turn: warp 0
+// loads (64 of K per stage, 48 KB), warp 1 issues twelve MMAs per stage (four of K
+// by three products), warps 2-9 take the accumulator (one of two) out, split it and
+// store it through shared memory as bulk copies of 4 KB.  Tiles of 128 columns need
+// a third fewer bytes per product, but the lists that come here are a few matrices,
+// half of whose tiles would leave most SMs without one (twelve of 256 x 1037 have
+// 48 such tiles of A).  A and B' are held without the scale.
 template <int PHASE>
 __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, OrthStep st) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -164,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abort = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  let_next_start();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars.full[i], 1);
@@ -171,15 +232,17 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.acc_full[i], 1);
-      mbar_init(&bars.acc_empty[i], kEpiWarps * 32);
+      mbar_init(&bars.acc_empty[i], kEpiWarps);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&bars.pair[i], 2);
     bars.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(&bars.tmem_slot, 256);
+  if (warp == 1) tmem_alloc(&bars.tmem_slot, 128);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  after_previous();
   const uint32_t tmem = bars.tmem_slot;
 
   struct Item {
@@ -188,9 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
   };
   auto item = [&](int at) {
     Item t;
-    const int k = PHASE == 3 ? find<&OrthMat::mn0>(v, at) : find<&OrthMat::sq0>(v, at);
+    const int k = PHASE == 3 ? find<&OrthMat::mn0>(v.mat, v.n, at) : find<&OrthMat::sq0>(v.mat, v.n, at);
     t.q = v.mat[k];
-    const int r = at - (PHASE == 3 ? t.q.mn0 : t.q.sq0), w = PHASE == 3 ? t.q.nt : t.q.mt;
+    const int r = at - (PHASE == 3 ? t.q.mn0 : t.q.sq0), w = 2 * (PHASE == 3 ? t.q.nt : t.q.mt);
     t.i = r / w;
     t.j = r - t.i * w;
     t.ks = ((PHASE == 1 ? t.q.n : t.q.m) + 63) / 64;
@@ -203,29 +266,30 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
     for (int at = blockIdx.x; at < st.items && go; at += gridDim.x) {
       const Item t = item(at);
       const OrthMat& q = t.q;
+      const bool same = PHASE == 1 && t.i == t.j / 2;  // B's columns are among A's rows
+      const uint8_t *pa, *pb;  // of the first stage; both go on by a tile, B of phase 3 by half a tile's rows
+      if constexpr (PHASE == 1) {
+        pa = tile_at(v, q.x[st.in] + t.i * 2 * q.nt);
+        pb = tile_at(v, q.x[st.in] + (t.j / 2) * 2 * q.nt) + (t.j & 1) * 8192;
+      } else if constexpr (PHASE == 2) {
+        pa = tile_at(v, q.a2 + t.i * 2 * q.mt);
+        pb = tile_at(v, q.a + (t.j / 2) * 2 * q.mt) + (t.j & 1) * 8192;
+      } else {
+        pa = tile_at(v, q.b + t.i * 2 * q.mt);
+        pb = tile_at(v, q.x[st.in] + t.j);
+      }
       for (int kk = 0; kk < t.ks; ++kk) {
         if (!__all_sync(0xffffffffu, mbar_wait(&bars.empty[stage], phase ^ 1, st.wc, abort))) { go = false; break; }
         if (lane == 0) {
           uint8_t* sa = sm + stage * kStage;
-          uint8_t* sb = sa + kOrthTile;
           uint64_t* full = &bars.full[stage];
-          const bool same = PHASE == 1 && t.i == t.j;
           mbar_expect_tx(full, same ? kOrthTile : kStage);
-          const int x = q.x[st.in];
-          if constexpr (PHASE == 1) {
-            bulk_load(sa, tile_at(v, x + t.i * 2 * q.nt + kk), kOrthTile, full);
-            if (!same) bulk_load(sb, tile_at(v, x + t.j * 2 * q.nt + kk), kOrthTile, full);
-          } else if constexpr (PHASE == 2) {
-            bulk_load(sa, tile_at(v, q.a2 + t.i * 2 * q.mt + kk), kOrthTile, full);
-            bulk_load(sb, tile_at(v, q.a + t.j * 2 * q.mt + kk), kOrthTile, full);
-          } else {
-            bulk_load(sa, tile_at(v, q.b + t.i * 2 * q.mt + kk), kOrthTile, full);
-            // 64 rows of two tiles side by side: blocks of 64 columns, hi then lo
-            const uint8_t* p = tile_at(v, x + (kk >> 1) * 2 * q.nt + 2 * t.j) + (kk & 1) * 8192;
-            bulk_load(sb, p, 8192, full);
-            bulk_load(sb + 8192, p + kOrthTile, 8192, full);
-            bulk_load(sb + 16384, p + kOrthPlane, 8192, full);
-            bulk_load(sb + 24576, p + kOrthTile + kOrthPlane, 8192, full);
+          bulk_load(sa, pa + static_cast<size_t>(kk) * kOrthTile, kOrthTile, full);
+          if (!same) {
+            const uint8_t* p = PHASE == 3 ? pb + static_cast<size_t>(kk >> 1) * 2 * q.nt * kOrthTile + (kk & 1) * 8192
+                                          : pb + static_cast<size_t>(kk) * kOrthTile;
+            bulk_load(sa + kOrthTile, p, 8192, full);
+            bulk_load(sa + kOrthTile + 8192, p + kOrthPlane, 8192, full);
           }
         }
         __syncwarp();
@@ -233,31 +297,30 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
       }
     }
   } else if (warp == 1) {
-    const uint32_t idesc = idesc_f16_f32(128, 128, 0, PHASE == 3 ? 1 : 0);
+    constexpr uint32_t kPlaneW = kOrthPlane / 16, kStageW = kStage / 16;
+    const uint32_t idesc = idesc_f16_f32(128, 64, 0, PHASE == 3 ? 1 : 0);
+    const uint32_t s0 = smem_u32(sm) >> 4, a0 = s0 | (1u << 16), b0 = s0 | ((PHASE == 3 ? 512u : 1u) << 16);
     int stage = 0, phase = 0, local = 0;
     bool go = true;
     for (int at = blockIdx.x; at < st.items && go; at += gridDim.x, ++local) {
       const Item t = item(at);
       const int ab = local & 1;
+      const bool same = PHASE == 1 && t.i == t.j / 2;
+      // B's low plane behind its high one, a tile's plane away where it is part of A
+      const uint32_t b_at = same ? (t.j & 1) * 512u : kOrthTile / 16, b_lo = same ? kPlaneW : 512u;
       if (!__all_sync(0xffffffffu, mbar_wait(&bars.acc_empty[ab], ((local >> 1) & 1) ^ 1, st.wc, abort))) break;
       tc_fence_after();
       for (int kk = 0; kk < t.ks; ++kk) {
         if (!__all_sync(0xffffffffu, mbar_wait(&bars.full[stage], phase, st.wc, abort))) { go = false; break; }
         tc_fence_after();
-        const uint32_t sa = smem_u32(sm + stage * kStage), sb = PHASE == 1 && t.i == t.j ? sa : sa + kOrthTile;
+        const uint32_t xa = a0 + stage * kStageW, xb = b0 + stage * kStageW + b_at, d = tmem + ab * 64;
         if (elect_one()) {
 #pragma unroll
-          for (int k16 = 0; k16 < 4; ++k16) {
-            uint64_t da[2], db[2];
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              da[p] = smem_desc(sa + p * kOrthPlane + k16 * 32, 16, 1024, 2);
-              db[p] = PHASE == 3 ? smem_desc(sb + p * kOrthPlane + k16 * 2048, 8192, 1024, 2)
-                                 : smem_desc(sb + p * kOrthPlane + k16 * 32, 16, 1024, 2);
-            }
-            mma_ss(tmem + ab * 128, da[0], db[0], idesc, (kk > 0 || k16 > 0) ? 1u : 0u);
-            mma_ss(tmem + ab * 128, da[0], db[1], idesc, 1u);
-            mma_ss(tmem + ab * 128, da[1], db[0], idesc, 1u);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t ka = xa + 2 * k, kb = xb + (PHASE == 3 ? 128 * k : 2 * k);
+            mma_ss_w(d, ka, kb, idesc, (kk > 0 || k > 0) ? 1u : 0u);
+            mma_ss_w(d, ka, kb + b_lo, idesc, 1u);
+            mma_ss_w(d, ka + kPlaneW, kb, idesc, 1u);
           }
           mma_commit(&bars.empty[stage]);
           if (kk == t.ks - 1) mma_commit(&bars.acc_full[ab]);
@@ -267,79 +330,106 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
       }
     }
   } else {
-    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const int quarter = warp & 3, half = (warp - 2) >> 2, r = quarter * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-    uint8_t* stg = sm + kStages * kStage + (warp - 2) * kStg;
-    // 64 columns of this warp's rows, f(column, accumulator) times the scale, into a tile
-    auto store = [&](uint8_t* tile, const uint32_t (&lo)[32], const uint32_t (&hi)[32], auto&& f) {
-      if (lane == 0) bulk_wait_read();  // the staging has been read
+    uint8_t* stg = sm + kStages * kStage + quarter * kStg;  // this quarter's rows
+    uint32_t pphase = 0;
+    bool go = true;
+    auto pair_sync = [&]() {
       __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.pair[quarter]);
+      go = go && __all_sync(0xffffffffu, mbar_wait(&bars.pair[quarter], pphase, st.wc, abort));
+      pphase ^= 1;
+      return go;
+    };
+    // this warp's 32 of a tile's columns, f(column, accumulator), and the quarter's rows out
+    auto store = [&](uint8_t* tile, const uint32_t (&acc)[32], auto&& f) {
+      if (half == 0 && lane == 0) bulk_wait_read();  // the staging has been read
+      if (!pair_sync()) return;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < 4; ++c) {
         float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          y[e] = f(8 * c + e, __uint_as_float(c < 4 ? lo[(8 * c + e) & 31] : hi[(8 * c + e) & 31]));
+        for (int e = 0; e < 8; ++e) y[e] = f(32 * half + 8 * c + e, __uint_as_float(acc[8 * c + e]));
         uint4 h, l;
         split8(y, h, l);
-        const uint32_t o = lane * 128 + ((c ^ (lane & 7)) << 4);
+        const uint32_t o = lane * 128 + (((4 * half + c) ^ (lane & 7)) << 4);
         *reinterpret_cast<uint4*>(stg + o) = h;
         *reinterpret_cast<uint4*>(stg + 4096 + o) = l;
       }
       fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
+      if (!pair_sync()) return;
+      if (half == 0 && lane == 0) {
         bulk_store_nc(tile + quarter * 4096, stg, 4096);
         bulk_store_nc(tile + kOrthPlane + quarter * 4096, stg + 4096, 4096);
         bulk_commit();
       }
     };
+    constexpr float kBack = 1.f / kOrthScale;
     int local = 0;
-    for (int at = blockIdx.x; at < st.items; at += gridDim.x, ++local) {
+    for (int at = blockIdx.x; at < st.items && go; at += gridDim.x, ++local) {
       const Item t = item(at);
       const OrthMat& q = t.q;
       const int ab = local & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars.acc_full[ab], (local >> 1) & 1, st.wc, abort))) break;
+      go = __all_sync(0xffffffffu, mbar_wait(&bars.acc_full[ab], (local >> 1) & 1, st.wc, abort));
+      if (!go) break;
       tc_fence_after();
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        uint32_t u[32], w[32];
-        const uint32_t ta = tmem + lane_addr + ab * 128 + 64 * h;
-        tmem_ld32x2_wait(ta, u, ta + 32, w);
-        if (h == 1) {
-          tc_fence_before();
-          mbar_arrive(&bars.acc_empty[ab]);
-        }
-        const int diag = t.i * 128 + r - (t.j * 128 + 64 * h);  // the column of this row's diagonal element
-        constexpr float kBack = 1.f / kOrthScale;                   // products carry the scale twice
-        if constexpr (PHASE == 1) {
-          const int tt = t.i * 2 * q.mt + 2 * t.j + h;
-          store(tile_at(v, q.a + tt), u, w, [&](int, float x) { return x * kBack; });
-          store(tile_at(v, q.a2 + tt), u, w, [&](int col, float x) {
-            return st.c * (x * kBack) + (col == diag ? st.b * kOrthScale : 0.f);
-          });
-        } else if constexpr (PHASE == 2) {
-          store(tile_at(v, q.b + t.i * 2 * q.mt + 2 * t.j + h), u, w,
-                [&](int col, float x) { return x * kBack + (col == diag ? st.a * kOrthScale : 0.f); });
-        } else if (!st.last) {
-          store(tile_at(v, q.x[st.in ^ 1] + t.i * 2 * q.nt + 2 * t.j + h), u, w,
-                [&](int, float x) { return x * kBack; });
-        } else {
-          const int row = t.i * 128 + r, col0 = t.j * 128 + 64 * h;
-          uint16_t* dst = static_cast<uint16_t*>(q.dst);
-          if (row < q.m) {
+      uint32_t u[32];
+      tmem_ld32_wait(tmem + lane_addr + ab * 64 + 32 * half, u);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.acc_empty[ab]);
+      const int diag = t.i * 128 + r - t.j * 64;  // the column of this row's diagonal element
+      if constexpr (PHASE == 1) {
+        const int tt = t.i * 2 * q.mt + t.j;
+        store(tile_at(v, q.a + tt), u, [&](int, float x) { return x * (kBack * kBack); });
+        store(tile_at(v, q.a2 + tt), u, [&](int col, float x) {
+          return st.c * (x * (kBack * kBack)) + (col == diag ? st.b : 0.f);
+        });
+      } else if constexpr (PHASE == 2) {
+        store(tile_at(v, q.b + t.i * 2 * q.mt + t.j), u,
+              [&](int col, float x) { return x + (col == diag ? st.a : 0.f); });
+      } else if (!st.last) {
+        store(tile_at(v, q.x[st.in ^ 1] + t.i * 2 * q.nt + t.j), u, [&](int, float x) { return x; });
+      } else {
+        // a transposed matrix's rows are contiguous across lanes, an ordinary one's go
+        // through the staging (64 columns of BF16, swizzled)
+        const int row0 = t.i * 128 + quarter * 32, col0 = t.j * 64;
+        uint16_t* dst = static_cast<uint16_t*>(q.dst);
+        if (q.flags & kOrthTall) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e) {
-              if (col0 + e >= q.n) break;
-              const float x = __uint_as_float(e < 32 ? u[e & 31] : w[e & 31]) * (kBack * kBack);
-              const long long o = (q.flags & kOrthTall) ? (col0 + e) * q.ld_dst + row : row * q.ld_dst + col0 + e;
-              dst[o] = static_cast<uint16_t>(pack_bf16x2(x, 0.f) & 0xFFFFu);
-            }
+          for (int e = 0; e < 32; ++e) {
+            const int col = col0 + 32 * half + e;
+            if (row0 + lane < q.m && col < q.n)
+              dst[col * q.ld_dst + row0 + lane] =
+                  static_cast<uint16_t>(pack_bf16x2(__uint_as_float(u[e]) * kBack, 0.f) & 0xFFFFu);
           }
+          continue;
+        }
+        if (!pair_sync()) break;  // the staging has been read
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(u[8 * c + 2 * e]) * kBack, __uint_as_float(u[8 * c + 2 * e + 1]) * kBack);
+          *reinterpret_cast<uint4*>(stg + sw128(lane, 4 * half + c)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (!pair_sync()) break;
+        const int r0 = 16 * half, rows = min(16, q.m - row0 - r0), cols = min(64, q.n - col0);
+        uint16_t* to = dst + (row0 + r0) * q.ld_dst + col0;
+        if (cols == 64 && (reinterpret_cast<uintptr_t>(to) & 15) == 0 && q.ld_dst % 8 == 0) {
+          for (int e = lane; e < rows * 8; e += 32)
+            *reinterpret_cast<uint4*>(to + (e >> 3) * q.ld_dst + (e & 7) * 8) =
+                *reinterpret_cast<const uint4*>(stg + sw128(r0 + (e >> 3), e & 7));
+        } else {
+          for (int rr = 0; rr < rows; ++rr)
+            for (int e = lane; e < cols; e += 32)
+              to[rr * q.ld_dst + e] = reinterpret_cast<const uint16_t*>(stg + sw128(r0 + rr, e >> 3))[e & 7];
         }
       }
     }
-    if (lane == 0) bulk_wait_all();
+    if (half == 0 && lane == 0) bulk_wait_all();
     __syncwarp();
   }
   tc_fence_before();
@@ -348,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 128);
   }
 }
 
@@ -407,8 +497,8 @@ bool plan_of(const triattn_matrix* in, const triattn_matrix* out, long long n, P
     q.n = std::max(rows, cols);
     q.mt = (q.m + 127) / 128;
     q.nt = (q.n + 127) / 128;
-    q.part_rows = std::max(1, 16384 / cols);
-    q.parts = (rows + q.part_rows - 1) / q.part_rows;
+    const long long parts = (in[k].rows * in[k].cols + kNormPart - 1) / kNormPart;
+    q.parts = static_cast<int>(parts);
     p->mats.push_back(q);
   }
   const auto others = std::stable_partition(p->mats.begin(), p->mats.end(), [](const OrthMat& q) { return q.mt == 1; });
@@ -426,8 +516,8 @@ bool plan_of(const triattn_matrix* in, const triattn_matrix* out, long long n, P
     if (q.mt > 1) {
       q.sq0 = static_cast<int>(p->sq);
       q.mn0 = static_cast<int>(p->mn);
-      p->sq += at / 2;
-      p->mn += xt / 2;
+      p->sq += at;
+      p->mn += xt;
       q.x[1] = static_cast<int>(p->tiles);
       q.a = static_cast<int>(p->tiles + xt);
       q.a2 = static_cast<int>(p->tiles + xt + at);
@@ -465,12 +555,11 @@ triattn_status check_list(const triattn_matrix* ms, long long n, bool output) {
 }
 
 template <int PHASE>
-cudaError_t launch_phase(const OrthView& v, const OrthStep& st, int sms, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(orth_gemm_kernel<PHASE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+cudaError_t launch_phase(const OrthView& v, const OrthStep& st, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(orth_gemm_kernel<PHASE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   return trace_call(kKOrthGemm, s, [&] {
-    orth_gemm_kernel<PHASE><<<std::min(st.items, sms), kThreads, kSmem, s>>>(v, st);
-    return cudaGetLastError();
+    return launch_after(false, orth_gemm_kernel<PHASE>, std::min(st.items, 152), kThreads, kSmem, s, v, st);
   });
 }
 
@@ -478,29 +567,26 @@ cudaError_t run(const Plan& p, int steps, const float* co, float eps, uint8_t* w
   OrthMat* mats = reinterpret_cast<OrthMat*>(ws);
   OrthView v{mats, reinterpret_cast<float*>(ws + p.part_off), ws + p.tiles_off, static_cast<int>(p.mats.size())};
   OrthTable t;
+  const bool small = p.mats.size() <= static_cast<size_t>(kUpload);
   cudaError_t e = cudaSuccess;
   for (size_t k = 0; k < p.mats.size() && e == cudaSuccess; k += kUpload) {
     t.n = static_cast<int>(std::min<size_t>(kUpload, p.mats.size() - k));
     std::copy_n(p.mats.data() + k, t.n, t.mat);
-    e = trace_call(kKOrthLoad, s, [&] {
-      orth_table_kernel<<<1, 256, 0, s>>>(t, mats + k);
-      return cudaGetLastError();
-    });
+    if (!small)
+      e = trace_call(kKOrthLoad, s, [&] { return launch_after(k == 0, orth_table_kernel, 1, 256, 0, s, t, mats + k); });
   }
   if (e == cudaSuccess)
     e = trace_call(kKOrthLoad, s, [&] {
-      orth_norm_kernel<<<static_cast<unsigned>(p.parts), 256, 0, s>>>(v);
-      return cudaGetLastError();
+      return launch_after(small, small ? orth_norm_kernel<true> : orth_norm_kernel<false>, static_cast<unsigned>(p.parts),
+                          256, 0, s, t, v, mats);
     });
   if (e == cudaSuccess)
     e = trace_call(kKOrthLoad, s, [&] {
-      orth_load_kernel<<<static_cast<unsigned>(p.load_tiles), 256, 0, s>>>(v, eps);
-      return cudaGetLastError();
+      return launch_after(false, orth_load_kernel, static_cast<unsigned>(p.load_tiles), 256, 0, s, v, eps);
     });
   if (p.solo > 0 && e == cudaSuccess)
     e = trace_call(kKOrthSolo, s, [&] {
-      return launch_orth_solo(mats, p.solo, v.tiles, steps, OrthCoef{co[0], co[1], co[2]},
-                              p.team, wc, s);
+      return launch_orth_solo(mats, p.solo, v.tiles, steps, OrthCoef{co[0], co[1], co[2]}, p.team, wc, s);
     });
   v.mat += p.solo;
   v.n -= p.solo;
@@ -509,10 +595,10 @@ cudaError_t run(const Plan& p, int steps, const float* co, float eps, uint8_t* w
     st.in = k & 1;
     st.last = k == steps - 1;
     st.items = static_cast<int>(p.sq);
-    e = launch_phase<1>(v, st, 152, s);
-    if (e == cudaSuccess) e = launch_phase<2>(v, st, 152, s);
+    e = launch_phase<1>(v, st, s);
+    if (e == cudaSuccess) e = launch_phase<2>(v, st, s);
     st.items = static_cast<int>(p.mn);
-    if (e == cudaSuccess) e = launch_phase<3>(v, st, 152, s);
+    if (e == cudaSuccess) e = launch_phase<3>(v, st, s);
   }
   return e;
 }

@@ -23,8 +23,7 @@ struct OrthMat {
   int mt, nt;                // 128-row and 128-column tiles of X
   int x[2], a, a2, b;        // tiles of X (two copies), A, A', B'; a team's: X, and 2 (team + 1) at a
   int parts, part0;          // partial sums of squares
-  int part_rows;             // rows of the source per partial sum
-  int tiles0, sq0, mn0;      // tiles (128 x 64) of X, 128 x 128 tiles of A and of X before this matrix
+  int tiles0, sq0, mn0;      // 128 x 64 tiles of X (all matrices), of A and of X (several rows of tiles) before it
 };
 constexpr int kOrthFp32 = 1, kOrthTall = 2;
 
