@@ -9,6 +9,7 @@ if the shared library is missing or cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import operator
 import os
 import struct
@@ -838,27 +839,35 @@ def _rows_pair(a, b, names, shape, dev: int):
 
 def qk_norm_shape(shape, w, rotary: str = "half", theta: float = 10000.0, eps: float = 1e-6) -> QKNormShape:
     """Of q's shape and its weight, [H, D] or [D]."""
+    return QKNormShape.from_buffer_copy(_qk_norm_plan(tuple(shape), w.dim() == 1, rotary, theta, eps)[0])
+
+
+@functools.lru_cache(maxsize=256)
+def _qk_norm_plan(shape, shared, rotary, theta, eps):
+    """(struct, its reference, the weights' shape, the positions' shape, the
+    backward's workspace) of a call of these sizes."""
     if len(shape) != 5:
         raise ValueError("q must be [B, N_o, H, N, D]")
     if rotary not in ROTARY:
         raise ValueError(f"rotary must be one of {tuple(ROTARY)}")
     B, No, H, N, D = shape
-    return QKNormShape(B, No, N, H, D, 1 if w.dim() == 1 else H, ROTARY[rotary], eps, theta, 0)
+    s = QKNormShape(B, No, N, H, D, 1 if shared else H, ROTARY[rotary], eps, theta, 0)
+    ref = ctypes.byref(s)
+    return s, ref, (D,) if shared else (H, D), (B, N), load().triattn_qk_norm_workspace_bytes(ref)
 
 
 def _qk_norm_check(q, k, w_q, w_k, positions, rotary, theta, eps):
     shape, dev, f32 = q.shape, q.get_device(), torch.float32
-    s = qk_norm_shape(shape, w_q, rotary, theta, eps)
+    _, ref, w_shape, p_shape, need = _qk_norm_plan(shape, w_q.dim() == 1, rotary, theta, eps)
     lay = _rows_pair(q, k, ("q", "k"), shape, dev)
-    w_shape = (s.D,) if s.w_heads == 1 and w_q.dim() == 1 else (s.H, s.D)
     if not (_fits(w_q, dev, w_shape, f32) and _fits(w_k, dev, w_shape, f32)
-            and (positions is None or _fits(positions, dev, (s.B, s.N), torch.int32))):
+            and (positions is None or _fits(positions, dev, p_shape, torch.int32))):
         _check(w_q, "w_q", w_shape, f32)
         _check(w_k, "w_k", w_shape, f32)
         if positions is not None:
-            _check(positions, "positions", (s.B, s.N), torch.int32)
+            _check(positions, "positions", p_shape, torch.int32)
         _same_device(q.device, w_q=w_q, w_k=w_k, positions=positions)
-    return s, lay
+    return ref, need, lay
 
 
 def _rows_like(q, lay):
@@ -878,7 +887,7 @@ def triattn_qk_norm_fwd(q, k, w_q, w_k, positions=None, rotary: str = "half", *,
     them).  ``w_q``, ``w_k`` [H, D] or [D] fp32; ``positions`` [B, N] int32 (the
     token's index if None); ``rotary`` "half", "interleaved" or "none".  Returns
     (q, k) normed, contiguous, or written into the views ``out``."""
-    s, lay = _qk_norm_check(q, k, w_q, w_k, positions, rotary, theta, eps)
+    ref, _, lay = _qk_norm_check(q, k, w_q, w_k, positions, rotary, theta, eps)
     here, sp = _on_stream(q.device, stream)
     given, lo = out, None
     with here:
@@ -887,7 +896,7 @@ def triattn_qk_norm_fwd(q, k, w_q, w_k, positions=None, rotary: str = "half", *,
         else:
             lo = _rows_pair(*out, ("q_out", "k_out"), q.shape, q.get_device())
         qo, ko = out
-        code = load().triattn_qk_norm_fwd(ctypes.byref(s), q.data_ptr(), k.data_ptr(), _ref(lay), w_q.data_ptr(),
+        code = load().triattn_qk_norm_fwd(ref, q.data_ptr(), k.data_ptr(), _ref(lay), w_q.data_ptr(),
                                           w_k.data_ptr(), _address(positions), qo.data_ptr(), ko.data_ptr(), _ref(lo),
                                           sp)
     _raise(code, "triattn_qk_norm_fwd")
@@ -902,10 +911,8 @@ def triattn_qk_norm_bwd(q, k, w_q, w_k, d_q_out, d_k_out, positions=None, rotary
     again from q and k.  Returns (dq, dk bf16, d_w_q, d_w_k fp32); ``out`` may
     pass them preallocated, dq and dk also as views, or d_q_out and d_k_out
     themselves."""
-    s, lay = _qk_norm_check(q, k, w_q, w_k, positions, rotary, theta, eps)
+    ref, need, lay = _qk_norm_check(q, k, w_q, w_k, positions, rotary, theta, eps)
     ld = _rows_pair(d_q_out, d_k_out, ("d_q_out", "d_k_out"), q.shape, q.get_device())
-    lib = load()
-    need = lib.triattn_qk_norm_workspace_bytes(ctypes.byref(s))
     if need == 0:
         raise TriAttnError(ERR_UNSUPPORTED, "triattn_qk_norm_bwd")
     here, sp = _on_stream(q.device, stream)
@@ -923,7 +930,7 @@ def triattn_qk_norm_bwd(q, k, w_q, w_k, d_q_out, d_k_out, positions=None, rotary
             _check(dwq, "d_w_q", w_q.shape, torch.float32)
             _check(dwk, "d_w_k", w_k.shape, torch.float32)
             _same_device(q.device, d_w_q=dwq, d_w_k=dwk)
-        code = lib.triattn_qk_norm_bwd(ctypes.byref(s), q.data_ptr(), k.data_ptr(), _ref(lay), w_q.data_ptr(),
+        code = load().triattn_qk_norm_bwd(ref, q.data_ptr(), k.data_ptr(), _ref(lay), w_q.data_ptr(),
                                        w_k.data_ptr(), _address(positions), d_q_out.data_ptr(), d_k_out.data_ptr(),
                                        _ref(ld), dq.data_ptr(), dk.data_ptr(), _ref(lg), dwq.data_ptr(),
                                        dwk.data_ptr(), workspace.data_ptr(), _bytes(workspace), sp)
@@ -935,12 +942,22 @@ def triattn_qk_norm_bwd(q, k, w_q, w_k, d_q_out, d_k_out, positions=None, rotary
 
 def relpos_shape(B: int, N: int, F: int, buckets: int, layout: str = "heads", kind: str = "clip",
                  max_distance: int = 32, dout_fp32: bool = False) -> RelposShape:
+    return RelposShape.from_buffer_copy(_relpos_plan(B, N, F, buckets, layout, kind, max_distance, dout_fp32)[0])
+
+
+@functools.lru_cache(maxsize=256)
+def _relpos_plan(B, N, F, buckets, layout, kind, max_distance, dout_fp32):
+    """(struct, its reference, the planes' or features' shape, the backward's
+    workspace) of a call of these sizes."""
     if layout not in RELPOS_LAYOUTS:
         raise ValueError(f"layout must be one of {tuple(RELPOS_LAYOUTS)}")
     if kind not in BUCKETS:
         raise ValueError(f"kind must be one of {tuple(BUCKETS)}")
-    return RelposShape(B, N, F, RELPOS_LAYOUTS[layout], BUCKETS[kind], buckets, max_distance,
-                       FLAG_DOUT_FP32 if dout_fp32 else 0)
+    s = RelposShape(B, N, F, RELPOS_LAYOUTS[layout], BUCKETS[kind], buckets, max_distance,
+                    FLAG_DOUT_FP32 if dout_fp32 else 0)
+    ref = ctypes.byref(s)
+    shape = (B, F, N, N) if layout == "heads" else (B, N, N, F)
+    return s, ref, shape, load().triattn_relpos_workspace_bytes(ref)
 
 
 def _relpos_ids(positions, chains, B, N, device):
@@ -976,8 +993,7 @@ def triattn_relpos_fwd(table, base=None, positions=None, chains=None, *, layout:
         B, N = positions.shape
     else:
         raise ValueError("base, out or positions [B, N] must be given")
-    s = relpos_shape(B, N, F, K, layout, kind, max_distance)
-    shape = (B, F, N, N) if layout == "heads" else (B, N, N, F)
+    _, ref, shape, _ = _relpos_plan(B, N, F, K, layout, kind, max_distance, False)
     dev = table.get_device()
     if not (_fits(table, dev, (K, F), torch.float32) and dev >= 0
             and (base is None or _fits(base, dev, shape, torch.bfloat16))):
@@ -994,7 +1010,7 @@ def triattn_relpos_fwd(table, base=None, positions=None, chains=None, *, layout:
         else:
             _check(out, "out", shape)
             _same_device(device, out=out)
-        code = load().triattn_relpos_fwd(ctypes.byref(s), table.data_ptr(), _address(base), _address(positions),
+        code = load().triattn_relpos_fwd(ref, table.data_ptr(), _address(base), _address(positions),
                                          _address(chains), out.data_ptr(), sp)
     _raise(code, "triattn_relpos_fwd")
     if given is not None:
@@ -1012,13 +1028,10 @@ def triattn_relpos_bwd(d_out, buckets: int, positions=None, chains=None, *, layo
     B, N = d_out.shape[0], d_out.shape[2]
     F = d_out.shape[1] if layout == "heads" else d_out.shape[3]
     f32 = d_out.dtype is torch.float32 and layout == "heads"
-    s = relpos_shape(B, N, F, buckets, layout, kind, max_distance, f32)
-    _check(d_out, "d_out", (B, F, N, N) if layout == "heads" else (B, N, N, F),
-           torch.float32 if f32 else torch.bfloat16)
+    _, ref, shape, need = _relpos_plan(B, N, F, buckets, layout, kind, max_distance, f32)
+    _check(d_out, "d_out", shape, torch.float32 if f32 else torch.bfloat16)
     device = d_out.device
     _relpos_ids(positions, chains, B, N, device)
-    lib = load()
-    need = lib.triattn_relpos_workspace_bytes(ctypes.byref(s))
     if need == 0:
         raise TriAttnError(ERR_UNSUPPORTED, "triattn_relpos_bwd")
     here, sp = _on_stream(device, stream)
@@ -1033,7 +1046,7 @@ def triattn_relpos_bwd(d_out, buckets: int, positions=None, chains=None, *, layo
         else:
             _check(out, "d_table", (buckets, F), torch.float32)
             _same_device(device, d_table=out)
-        code = lib.triattn_relpos_bwd(ctypes.byref(s), d_out.data_ptr(), _address(positions), _address(chains),
+        code = load().triattn_relpos_bwd(ref, d_out.data_ptr(), _address(positions), _address(chains),
                                       out.data_ptr(), workspace.data_ptr(), _bytes(workspace), sp)
     _raise(code, "triattn_relpos_bwd")
     if given is not None:
@@ -1145,23 +1158,32 @@ def triattn_clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, *, 
 
 
 _shape_of = operator.attrgetter("shape")
+_contiguous, _device_index, _data_ptr = torch.Tensor.is_contiguous, torch.Tensor.get_device, torch.Tensor.data_ptr
 
 
-def _matrix_table(tensors, name, device):
+def _matrix_table(tensors, name, device, of=None):
     """The triattn_matrix array of a list of 2-D tensors as bytes (address, rows,
-    columns, stride and dtype, eight each), and their shapes.  Column by column,
-    like _tensor_table."""
+    columns, stride and dtype, eight each), with what an array of outputs of the
+    same shapes takes over (``of``).  Column by column, like _tensor_table."""
     n = len(tensors)
+    bf16 = torch.bfloat16
     shapes = list(map(_shape_of, tensors))
-    rows = [0] * (5 * n)
+    kinds = list(map(_dtype_of, tensors))
+    all_bf16 = kinds.count(bf16) == n
+    if of is not None and not (all_bf16 and shapes == of[0]):
+        for i, (shape, b) in enumerate(zip(of[0], tensors)):
+            if b.shape != shape or b.dtype is not bf16:
+                raise ValueError(f"{name}[{i}] must be a bfloat16 tensor of the shape of tensors[{i}]")
+    rows = [0] * (5 * n) if of is None or not of[2] else of[1].copy()
     try:
-        plain = (set(map(len, shapes)) <= {2} and all(map(torch.Tensor.is_contiguous, tensors))
-                 and set(map(torch.Tensor.get_device, tensors)) <= {device.index})
-        rows[4::5] = map(GRAD_DTYPES.__getitem__, map(_dtype_of, tensors))
-        rows[0::5] = map(torch.Tensor.data_ptr, tensors)
-        if plain and n:
-            rows[1::5], cols = zip(*shapes)
-            rows[2::5] = rows[3::5] = cols
+        plain = all(map(_contiguous, tensors)) and set(map(_device_index, tensors)) <= {device.index}
+        if plain and (of is None or not of[2]):
+            plain = set(map(len, shapes)) <= {2}
+            if plain and n:
+                rows[1::5], cols = zip(*shapes)
+                rows[2::5] = rows[3::5] = cols
+        rows[4::5] = [0] * n if all_bf16 else list(map(GRAD_DTYPES.__getitem__, kinds))
+        rows[0::5] = map(_data_ptr, tensors)
     except (KeyError, RuntimeError):
         plain = False
     if not plain:
@@ -1173,7 +1195,7 @@ def _matrix_table(tensors, name, device):
             if (c > 1 and t.stride(1) != 1) or (stride < c and t.numel()):
                 raise ValueError(f"{name}[{i}] must have contiguous rows")
             rows[5 * i:5 * i + 5] = (t.data_ptr(), r, c, stride, GRAD_DTYPES[t.dtype])
-    return struct.pack(f"{5 * n}q", *rows), shapes
+    return struct.pack(f"{5 * n}q", *rows), (shapes, rows, plain)
 
 
 ORTHOGONALIZE = (3.4445, -4.7750, 2.0315)
@@ -1194,22 +1216,18 @@ def triattn_orthogonalize(tensors, steps: int = 5, *, coefficients=ORTHOGONALIZE
     if device.type != "cuda":
         raise ValueError("the matrices must be CUDA tensors")
     n = len(tensors)
-    table, shapes = _matrix_table(tensors, "tensors", device)
+    table, of = _matrix_table(tensors, "tensors", device)
     here, sp = _on_stream(device, stream)
     given = out
     lib = load()
     with here:
         if out is None:
-            out = [torch.empty(shape, dtype=torch.bfloat16, device=device) for shape in shapes]
+            out = [torch.empty(shape, dtype=torch.bfloat16, device=device) for shape in of[0]]
         else:
             out = [out] if isinstance(out, torch.Tensor) else list(out)
             if len(out) != n:
                 raise ValueError(f"out has {len(out)} tensors, expected {n}")
-        into, shapes_out = _matrix_table(out, "out", device)
-        if shapes != shapes_out or set(map(_dtype_of, out)) - {torch.bfloat16}:
-            for i, (a, b) in enumerate(zip(tensors, out)):
-                if a.shape != b.shape or b.dtype is not torch.bfloat16:
-                    raise ValueError(f"out[{i}] must be a bfloat16 tensor of the shape of tensors[{i}]")
+        into, _ = _matrix_table(out, "out", device, of)
         need = lib.triattn_orthogonalize_workspace_bytes(table, n)
         if need == 0:
             raise TriAttnError(ERR_UNSUPPORTED, "triattn_orthogonalize")
