@@ -14,8 +14,14 @@ parameter's dtype (BF16 projection matrices, FP32 LayerNorm parameters).
   incoming ("TurboPairFormer", Figure 12).  Returns the update.
 - ``Transition``: the gated feed-forward block over the pair rows.  Returns
   the update; its forward keeps only its inputs for the backward.
+- ``QKNorm``: norms of queries and keys for each head with the position
+  rotation, in front of the core (``triattn.triangle_attention``).
+- ``RelativePosition``: a learned relative position bias by buckets, added to
+  the core's bias planes or to the pair features.
 - ``clip_grad_norm_``: clips the gradients of a model's parameters by their
   global norm, in place.
+- ``orthogonalize_grads_``: orthogonalises the gradients of its matrices, in
+  place.
 
 Forward and backward may be captured into a CUDA graph.  Before a backward is
 captured, drop what holds an eager autograd graph of the same parameters (a
@@ -82,6 +88,44 @@ class TransitionFunction(torch.autograd.Function):
         dz, dlw, dlb, dwi, dwo = T.triattn_transition_bwd(z, mask, ln_w, ln_b, w_in, w_o, d_out.contiguous(),
                                                           ctx.activation)
         return dz, dlw, dlb, dwi, dwo, None, None
+
+
+class QKNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, w_q, w_k, positions, rotary: str, theta: float, eps: float):
+        if q.stride() != k.stride():
+            q, k = q.contiguous(), k.contiguous()
+        out = T.triattn_qk_norm_fwd(q, k, w_q, w_k, positions, rotary, theta=theta, eps=eps)
+        ctx.save_for_backward(q, k, w_q, w_k, positions)
+        ctx.rotary, ctx.theta, ctx.eps = rotary, theta, eps
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_q, d_k):
+        q, k, w_q, w_k, positions = ctx.saved_tensors
+        return (*T.triattn_qk_norm_bwd(q, k, w_q, w_k, d_q.contiguous(), d_k.contiguous(), positions, ctx.rotary,
+                                       theta=ctx.theta, eps=ctx.eps), None, None, None, None)
+
+
+class RelativePositionFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, table, base, positions, chains, layout: str, kind: str, max_distance: int):
+        if base is not None:
+            base = base.contiguous()
+        out = T.triattn_relpos_fwd(table, base, positions, chains, layout=layout, kind=kind, max_distance=max_distance)
+        ctx.save_for_backward(positions, chains)
+        ctx.buckets, ctx.how = table.shape[0], dict(layout=layout, kind=kind, max_distance=max_distance)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_out):
+        positions, chains = ctx.saved_tensors
+        d_table = None
+        if ctx.needs_input_grad[0]:
+            d_table = T.triattn_relpos_bwd(d_out.contiguous(), ctx.buckets, positions, chains, **ctx.how)
+        return d_table, d_out if ctx.needs_input_grad[1] else None, None, None, None, None, None
 
 
 class TriangleAttention(torch.nn.Module):
@@ -151,6 +195,62 @@ class Transition(torch.nn.Module):
         return TransitionFunction.apply(z, self.ln_w, self.ln_b, self.w_in, self.w_o, mask, self.activation)
 
 
+class QKNorm(torch.nn.Module):
+    """Norms of queries and keys [B, N_o, H, N, D] (BF16; contiguous, or views of
+    one layout with contiguous features, as in a projection's rows) for each head,
+    y = w[h] * x rsqrt(mean x^2 + eps), turned by the position's angles: pairs
+    (i, i + D/2) with ``rotary`` "half", (2 i, 2 i + 1) with "interleaved", none
+    with "none".  ``shared``: one weight [D] for all heads.  ``positions``
+    (optional) [B, N] int32, the token's index if None.  Returns (q, k)."""
+
+    def __init__(self, n_heads: int, head_dim: int, rotary: str = "half", theta: float = 10000.0, eps: float = 1e-6,
+                 shared: bool = False, device=None):
+        super().__init__()
+        if rotary not in T.ROTARY:
+            raise ValueError(f"rotary must be one of {tuple(T.ROTARY)}")
+        self.rotary, self.theta, self.eps = rotary, theta, eps
+        shape = (head_dim,) if shared else (n_heads, head_dim)
+        self.w_q = torch.nn.Parameter(torch.ones(shape, dtype=torch.float32, device=device))
+        self.w_k = torch.nn.Parameter(torch.ones(shape, dtype=torch.float32, device=device))
+
+    def forward(self, q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor] = None):
+        return QKNormFunction.apply(q, k, self.w_q, self.w_k, positions, self.rotary, self.theta, self.eps)
+
+
+class RelativePosition(torch.nn.Module):
+    """Learned relative position bias: adds a row of the table (FP32, zeros at
+    first) by the bucket of pos[i] - pos[j] to ``base`` (BF16), the bias planes
+    [B, features, N, N] of the core (``layout`` "heads": features are heads) or
+    pair features [B, N, N, features] ("pairs").  ``kind`` "clip" has
+    2 max_distance + 1 buckets; "log" ``buckets``, an even number, half of them
+    for each sign, logarithmic up to max_distance.  ``chains``: one row more, for
+    pairs of different chains, whose indices [B, N] int32 each call then takes.
+    ``positions`` (optional) [B, N] int32, the token's index if None.  Without
+    ``base`` the bias alone, for the B and N of ``positions``."""
+
+    def __init__(self, features: int, layout: str = "heads", kind: str = "clip", max_distance: int = 32,
+                 buckets: Optional[int] = None, chains: bool = False, device=None):
+        super().__init__()
+        if layout not in T.RELPOS_LAYOUTS:
+            raise ValueError(f"layout must be one of {tuple(T.RELPOS_LAYOUTS)}")
+        if kind not in T.BUCKETS:
+            raise ValueError(f"kind must be one of {tuple(T.BUCKETS)}")
+        if buckets is None:
+            if kind != "clip":
+                raise ValueError("buckets must be given")
+            buckets = 2 * max_distance + 1
+        self.layout, self.kind, self.max_distance, self.chains = layout, kind, max_distance, chains
+        self.table = torch.nn.Parameter(
+            torch.zeros(buckets + (1 if chains else 0), features, dtype=torch.float32, device=device))
+
+    def forward(self, base: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                chains: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if (chains is not None) != self.chains:
+            raise ValueError("chains must be given" if self.chains else "this bias has no row for other chains")
+        return RelativePositionFunction.apply(self.table, base, positions, chains, self.layout, self.kind,
+                                              self.max_distance)
+
+
 def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0) -> torch.Tensor:
     """Scale the gradients of ``parameters`` (BF16 and FP32) in place so that
     their global norm (2 or inf) is at most ``max_norm``.  Parameters without a
@@ -159,3 +259,23 @@ def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0) -> torc
     the gradients' addresses: zero them between replays, do not free them."""
     parameters = [parameters] if isinstance(parameters, torch.Tensor) else parameters
     return T.triattn_clip_grad_norm([p.grad for p in parameters if p.grad is not None], max_norm, norm_type)
+
+
+def orthogonalize_grads_(parameters, steps: int = 5, *, coefficients=T.ORTHOGONALIZE, eps: float = 1e-7) -> None:
+    """Replace the gradients of the matrices among ``parameters`` (2-D, BF16 and
+    FP32) by their orthogonalised ones (Newton-Schulz products, rounded to BF16),
+    in place.  Parameters of other dimensions or without a gradient stay as they
+    are.  Captured into a graph, it keeps the gradients' addresses, as
+    clip_grad_norm_ does.  To orthogonalise running means of gradients, hand
+    those to ``triattn.triattn_orthogonalize``."""
+    parameters = [parameters] if isinstance(parameters, torch.Tensor) else parameters
+    grads = [p.grad for p in parameters if p.grad is not None and p.dim() == 2]
+    if not grads:
+        return
+    wide = [g for g in grads if g.dtype != torch.bfloat16]
+    narrow = [torch.empty(g.shape, dtype=torch.bfloat16, device=g.device) for g in wide]
+    it = iter(narrow)
+    T.triattn_orthogonalize(grads, steps, coefficients=coefficients, eps=eps,
+                            out=[g if g.dtype == torch.bfloat16 else next(it) for g in grads])
+    for g, o in zip(wide, narrow):
+        g.copy_(o)
