@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_bwd_kernel(const QkArgs a
   using P = Place<D, ROT>;
   __shared__ float sums[P::kRows][D + 1];
   __shared__ float parts[kThreads];
+  let_next_start();
   const P at(a);
   const int m = blockIdx.x & 1, tile = blockIdx.x >> 1;
   const uint16_t* x = m ? a.x[1] : a.x[0];
@@ -319,10 +320,10 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_bwd_kernel(const QkArgs a
 // Partials [chunks][tiles][slots][D]: with the heads in a row a slot is a head
 // (the j0 + slot-th where a tile does not hold all of them), otherwise the
 // slot-th head of the tile.
-__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* __restrict__ part, float* __restrict__ dwq,
-                                                          float* __restrict__ dwk, int D, int rows, int tiles,
+__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* part, float* dwq, float* dwk, int D, int rows, int tiles,
                                                           int chunks, int slots, int H, int N, int w_heads, int hn) {
   __shared__ double sh[1024];
+  after_previous();
   const int d = threadIdx.x % D, lane = threadIdx.x / D, lanes = 1024 / D;
   const float* p = part + static_cast<size_t>(blockIdx.y) * chunks * tiles * slots * D + d;
   const int h = blockIdx.x;
@@ -523,10 +524,8 @@ triattn_status triattn_qk_norm_bwd(const triattn_qk_norm_shape* shape, const voi
   cudaError_t e = trace_call(kKQkBwd, s, [&] { return dispatch(shape, a, grid, true, s); });
   if (e == cudaSuccess)
     e = trace_call(kKQkDw, s, [&] {
-      qk_norm_dw_kernel<<<dim3(shape->w_heads, 2), 1024, 0, s>>>(a.part, d_w_q, d_w_k, shape->D, p.rows, p.tiles,
-                                                                p.chunks, p.slots, shape->H, shape->N, shape->w_heads,
-                                                                lx.hn);
-      return cudaGetLastError();
+      return launch_after(false, qk_norm_dw_kernel, dim3(shape->w_heads, 2), 1024, 0, s, a.part, d_w_q, d_w_k, shape->D,
+                          p.rows, p.tiles, p.chunks, p.slots, shape->H, shape->N, shape->w_heads, lx.hn);
     });
   return e == cudaSuccess ? TRIATTN_OK : TRIATTN_ERR_CUDA;
 }

@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 2) relpos_heads_bwd_kernel(const __g
   constexpr int U = 16 / V;     // rows in flight
   extern __shared__ float sh[];
   __shared__ uint8_t lut[2 * kRelposMaxDistance + 1];
+  let_next_start();
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, nw = blockDim.x / 32;
   const int nt = chunks_of(a.N, W), b = blockIdx.y / a.F;
   Window* win = reinterpret_cast<Window*>(sh);  // [chunks]
@@ -508,17 +509,19 @@ __global__ void __launch_bounds__(kThreads, 2) relpos_heads_bwd_kernel(const __g
 
 // out[y * oy + x * ox] = sum over (b, s) of part[b * pb + s * ps + y * py + x], 32 x by 32 slices
 // of the sum per block, joined in a fixed order.
-__global__ void __launch_bounds__(1024) relpos_sum_kernel(const float* __restrict__ part, float* __restrict__ out,
-                                                          int nx, int ox, int oy, int nb, int ns, size_t pb, size_t ps,
+__global__ void __launch_bounds__(1024) relpos_sum_kernel(const float* part, float* out, int nx, int ox, int oy, int nb, int ns, size_t pb, size_t ps,
                                                           size_t py) {
   __shared__ double sh[32][33];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, x = blockIdx.x * 32 + lane;
   double v = 0.0;
-  if (x < nx)
+  after_previous();
+  if (x < nx) {
+#pragma unroll 8
     for (int e = slice; e < nb * ns; e += 32) {
       const int b = e / ns, s = e - b * ns;
       v += part[b * pb + s * ps + blockIdx.y * py + x];
     }
+  }
   sh[slice][lane] = v;
   __syncthreads();
   if (slice == 0 && x < nx) {
@@ -699,9 +702,8 @@ triattn_status triattn_relpos_bwd(const triattn_relpos_shape* shape, const void*
     e = trace_call(kKRelBwd, s, [&] { return launch_relpos_pairs_bwd(a, d_out, parts, current_wait_ctl(), s); });
     if (e == cudaSuccess)
       e = trace_call(kKRelSum, s, [&] {  // partials [parts][buckets][F]
-        relpos_sum_kernel<<<dim3((a.F + 31) / 32, a.buckets), 1024, 0, s>>>(
-            a.part, d_table, a.F, 1, a.F, 1, parts, 0, static_cast<size_t>(a.buckets) * a.F, a.F);
-        return cudaGetLastError();
+        return launch_after(false, relpos_sum_kernel, dim3((a.F + 31) / 32, a.buckets), 1024, 0, s, a.part, d_table, a.F,
+                            1, a.F, 1, parts, 0, static_cast<size_t>(a.buckets) * a.F, a.F);
       });
   } else {
     const BwdPlan p = bwd_plan(a.B, a.N, a.F, a.buckets);
@@ -712,9 +714,8 @@ triattn_status triattn_relpos_bwd(const triattn_relpos_shape* shape, const void*
     if (e == cudaSuccess)
       e = trace_call(kKRelSum, s, [&] {  // partials [B][F][splits][buckets]
         const size_t per = static_cast<size_t>(p.splits) * a.buckets;
-        relpos_sum_kernel<<<dim3((a.buckets + 31) / 32, a.F), 1024, 0, s>>>(a.part, d_table, a.buckets, a.F, 1, a.B,
-                                                                           p.splits, a.F * per, a.buckets, per);
-        return cudaGetLastError();
+        return launch_after(false, relpos_sum_kernel, dim3((a.buckets + 31) / 32, a.F), 1024, 0, s, a.part, d_table,
+                            a.buckets, a.F, 1, a.B, p.splits, a.F * per, a.buckets, per);
       });
   }
   return e == cudaSuccess ? TRIATTN_OK : TRIATTN_ERR_CUDA;

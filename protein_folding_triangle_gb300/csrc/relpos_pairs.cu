@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const
   __shared__ Bars bars;
   __shared__ uint8_t lut[2 * kRelposMaxDistance + 1];
   __shared__ uint16_t held[kStagesMax][kBlk];  // where the stage's ones lie (element of B)
+  let_next_start();
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abort = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
