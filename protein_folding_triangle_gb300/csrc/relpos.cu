@@ -249,11 +249,14 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks) relpos_heads_fwd_kernel(
 // ------------------------------------------------ pair features, forward
 // Block: a run of segments of a row (b, i), as many as any other block's or one
 // more; thread: eight features of four pairs of a segment, all four in flight.
-// The table comes from L1.
-constexpr int kPairsU = 4;
+// The table comes from L1.  768^2 pairs of 128 features (302 MB) take 52 us, 1920^2
+// 299 us (6.4 TB/s).  Five blocks per SM were the fastest of three to six (at 1920^2 of
+// 128 features: 331 us with three and six pairs, 321, 299, 338); loads of the next
+// segment ahead of a segment's stores cost a tenth.
+constexpr int kPairsU = 4, kPairsBlocks = 5;
 int pairs_threads(int F) { return kThreads / (F / 8) * (F / 8); }
 int pairs_segment(int F) { return kPairsU * (kThreads / (F / 8)); }
-__global__ void __launch_bounds__(kThreads) relpos_pairs_fwd_kernel(const __grid_constant__ RelposArgs a) {
+__global__ void __launch_bounds__(kThreads, kPairsBlocks) relpos_pairs_fwd_kernel(const __grid_constant__ RelposArgs a) {
   constexpr int U = kPairsU;
   __shared__ uint8_t lut[2 * kRelposMaxDistance + 1];
   for (int d = threadIdx.x; d <= 2 * a.R; d += blockDim.x) lut[d] = a.lut[d];
@@ -638,7 +641,7 @@ cudaError_t launch_heads_fwd(const RelposArgs& a, cudaStream_t s) {
 cudaError_t launch_pairs_fwd(const RelposArgs& a, cudaStream_t s) {
   const int len = pairs_segment(a.F);
   const long long all = static_cast<long long>(a.B) * a.N * ((a.N + len - 1) / len);
-  relpos_pairs_fwd_kernel<<<static_cast<unsigned>(std::min(all, 152ll * 4)), pairs_threads(a.F), 0, s>>>(a);
+  relpos_pairs_fwd_kernel<<<static_cast<unsigned>(std::min(all, 152ll * kPairsBlocks)), pairs_threads(a.F), 0, s>>>(a);
   return cudaGetLastError();
 }
 
