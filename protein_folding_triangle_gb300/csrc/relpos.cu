@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 2) relpos_heads_bwd_kernel(const __g
       }
     }
     if (kind == kAll) {
-      float x = 0.f;
+      float2 x2 = {0.f, 0.f}, y2 = {0.f, 0.f};
       for (int r0 = 0; r0 < nr; r0 += U) {
         uint4 raw[U][V];
 #pragma unroll
@@ -438,9 +438,13 @@ __global__ void __launch_bounds__(kThreads, 2) relpos_heads_bwd_kernel(const __g
           float v[W];
           values(raw[q], v);
 #pragma unroll
-          for (int e = 0; e < W; e += 4) x += (v[e] + v[e + 1]) + (v[e + 2] + v[e + 3]);
+          for (int e = 0; e < W; e += 4) {
+            x2 = fadd2(x2, make_float2(v[e], v[e + 1]));
+            y2 = fadd2(y2, make_float2(v[e + 2], v[e + 3]));
+          }
         }
       }
+      const float x = (x2.x + x2.y) + (y2.x + y2.y);
       if (k == kl) sl += x;
       else if (k == kh) sh_ += x;
       else if (k == ko) so += x;
