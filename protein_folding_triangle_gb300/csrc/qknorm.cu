@@ -478,6 +478,7 @@ triattn_status triattn_qk_norm_fwd(const triattn_qk_norm_shape* shape, const voi
   for (const void* p : {q, k, static_cast<const void*>(q_out), static_cast<const void*>(k_out)})
     if (!al(p, 16)) return TRIATTN_ERR_INVALID_ARG;
   if (!al(w_q, 4) || !al(w_k, 4) || (positions != nullptr && !al(positions, 4))) return TRIATTN_ERR_INVALID_ARG;
+  if (q_out == k_out || q_out == q || q_out == k || k_out == q || k_out == k) return TRIATTN_ERR_INVALID_ARG;
   const Plan p = fwd_plan(shape, lx.hn != 0);
   QkArgs a = args_of(shape, p, lx, ly, w_q, w_k, positions);
   a.x[0] = static_cast<const uint16_t*>(q);
@@ -509,6 +510,12 @@ triattn_status triattn_qk_norm_bwd(const triattn_qk_norm_shape* shape, const voi
     if (!al(p, 4)) return TRIATTN_ERR_INVALID_ARG;
   if (positions != nullptr && !al(positions, 4)) return TRIATTN_ERR_INVALID_ARG;
   if (!al(workspace, 256) || workspace_bytes < triattn_qk_norm_workspace_bytes(shape)) return TRIATTN_ERR_WORKSPACE;
+  auto same = [](const RowLayout& a, const RowLayout& b) {
+    return a.slice == b.slice && a.head == b.head && a.row == b.row;
+  };
+  if (dq == dk || d_w_q == d_w_k || dq == q || dq == k || dk == q || dk == k || dq == d_k_out || dk == d_q_out ||
+      ((dq == d_q_out || dk == d_k_out) && !same(ldy, ly)))
+    return TRIATTN_ERR_INVALID_ARG;
   const Plan p = bwd_plan(shape, lx.hn != 0);
   QkArgs a = args_of(shape, p, lx, ly, w_q, w_k, positions);
   a.ldy = ldy;

@@ -90,10 +90,16 @@ class TransitionFunction(torch.autograd.Function):
         return dz, dlw, dlb, dwi, dwo, None, None
 
 
+def _rows(t: torch.Tensor) -> bool:
+    """Whether a [B, N_o, H, N, D] view is one of rows that the kernels take as it is."""
+    return (t.dim() == 5 and t.stride(4) == 1 and (t.shape[0] == 1 or t.stride(0) == t.shape[1] * t.stride(1))
+            and all(s > 0 and s % 8 == 0 for s in t.stride()[1:4]) and t.data_ptr() % 16 == 0)
+
+
 class QKNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, w_q, w_k, positions, rotary: str, theta: float, eps: float):
-        if q.stride() != k.stride():
+        if q.stride() != k.stride() or not (_rows(q) and _rows(k)):
             q, k = q.contiguous(), k.contiguous()
         out = T.triattn_qk_norm_fwd(q, k, w_q, w_k, positions, rotary, theta=theta, eps=eps)
         ctx.save_for_backward(q, k, w_q, w_k, positions)

@@ -77,6 +77,22 @@ def test_qk_norm_pointers(lib):
         assert qk(lib, s, lays, bwd=True) == T.ERR_INVALID_ARG
 
 
+def test_qk_norm_outputs_of_their_own(lib):
+    """Outputs that are each other or an input; dq, dk over d_q_out, d_k_out want
+    their layout."""
+    s, at = shape(), [FAKE + (i << 24) for i in range(12)]
+    names = ("q", "k", "w_q", "w_k", "positions", "d_q_out", "d_k_out", "q_out", "k_out", "d_w_q", "d_w_k")
+    apart = dict(zip(names, at))
+    for a, b in (("q_out", "k_out"), ("q_out", "q"), ("q_out", "k"), ("k_out", "q"), ("k_out", "k")):
+        for bwd in (False, True):
+            assert qk(lib, s, bwd=bwd, **{**apart, a: apart[b]}) == T.ERR_INVALID_ARG, (a, b)
+    for a, b in (("d_w_q", "d_w_k"), ("q_out", "d_k_out"), ("k_out", "d_q_out")):
+        assert qk(lib, s, bwd=True, **{**apart, a: apart[b]}) == T.ERR_INVALID_ARG, (a, b)
+    rows = (7 * 96, 16, 96)
+    for a, b in (("q_out", "d_q_out"), ("k_out", "d_k_out")):
+        assert qk(lib, s, (None, rows, None), bwd=True, **{**apart, a: apart[b]}) == T.ERR_INVALID_ARG, (a, b)
+
+
 def rel(lib, s, table=FAKE, base=FAKE, positions=FAKE, chains=None, out=FAKE):
     return lib.triattn_relpos_fwd(ctypes.byref(s), V(table), V(base), V(positions), V(chains), V(out), None)
 
