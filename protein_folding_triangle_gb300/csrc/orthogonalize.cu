@@ -29,6 +29,7 @@
 #include <cmath>
 #include <cstdint>
 #include <new>
+#include <type_traits>
 #include <vector>
 
 #include "kernels.cuh"
@@ -38,6 +39,9 @@
 namespace triattn {
 namespace {
 
+constexpr int kMaxSteps = 64;
+constexpr int kDoneBytes = 4 * 3 * kMaxSteps;  // a count for every phase
+static_assert(kDoneBytes / 4 <= 256 && kDoneBytes % 16 == 0, "cleared by one block");
 constexpr int kUpload = 256;
 struct OrthTable {
   OrthMat mat[kUpload];
@@ -103,6 +107,7 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ 
   __shared__ float sh[8];
   let_next_start();
   after_previous();  // the table, or what last used the workspace
+  if (blockIdx.x == 0 && threadIdx.x < kDoneBytes / 4) v.done[threadIdx.x] = 0;
   if (PARAM && blockIdx.x == 0)
     for (int i = threadIdx.x; i < t.n; i += 256) to[i] = t.mat[i];
   const OrthMat* mat = PARAM ? t.mat : v.mat;
@@ -202,29 +207,51 @@ struct GemmBars {
   int abort;
 };
 
-struct OrthStep {
+struct OrthRun {
   float a, b, c;
-  int in;    // which copy of X is read
-  int last;  // the last step: X goes to the destinations
-  int items;
+  int steps, sq, mn;  // items of the phases of A and A', and of X
+  uint32_t* done;     // [3 steps] rows of warps that have stored all of a phase's tiles
   WaitCtl wc;
 };
 
-// 128 x 64 tiles of phase PHASE's product.  One CTA per SM, tiles in turn: warp 0
-// loads (64 of K per stage, 48 KB), warp 1 issues twelve MMAs per stage (four of K
-// by three products), warps 2-9 take the accumulator (one of two) out, split it and
-// store it through shared memory as bulk copies of 4 KB.  Tiles of 128 columns need
-// a third fewer bytes per product, but the lists that come here are a few matrices,
-// half of whose tiles would leave most SMs without one (twelve of 256 x 1037 have
-// 48 such tiles of A).  A and B' are held without the scale.
-template <int PHASE>
-__global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, OrthStep st) {
+template <int P>
+using Phase = std::integral_constant<int, P>;
+
+// Bounded wait of a whole warp until what `n` others have stored before they added
+// themselves to *p can be loaded by bulk copies.
+__device__ __forceinline__ bool count_wait(const uint32_t* p, uint32_t n, const WaitCtl& wc, volatile int* abort) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) {
+    const uint64_t t0 = global_timer_ns();
+    while (ld_acquire_gpu(p) < n) {
+      if (*abort != 0) ok = false;
+      if (ok && global_timer_ns() - t0 > wc.limit_ns) {
+        atomicOr(wc.status, kDevTimeout);
+        *abort = 1;
+        ok = false;
+      }
+      if (!ok) break;
+    }
+    fence_proxy_async_all();
+  }
+  return __shfl_sync(0xffffffffu, ok, 0);
+}
+
+// All steps of the matrices of more than 128 rows.  A phase is its product's tiles of
+// 128 x 64, shared out over one CTA per SM; warp 0 loads (64 of K per stage, 48 KB),
+// warp 1 issues twelve MMAs per stage (four of K by three products), warps 2-9 take
+// the accumulator (one of two) out, split it and store it through shared memory as
+// bulk copies of 4 KB.  A phase's loads wait until all CTAs that had tiles of the one
+// before have counted themselves (a cooperative launch: all of them run).  Tiles of
+// 128 columns need a third fewer bytes per product, but the lists that come here are
+// a few matrices, half of whose tiles would leave most SMs without one (twelve of
+// 256 x 1037 have 48 such tiles of A).  A and B' are held without the scale.
+__global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, OrthRun st) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ GemmBars bars;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abort = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  let_next_start();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars.full[i], 1);
@@ -242,14 +269,14 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  after_previous();
   const uint32_t tmem = bars.tmem_slot;
 
   struct Item {
     OrthMat q;
     int i, j, ks;  // tile (i, j) of the product, stages of K
   };
-  auto item = [&](int at) {
+  auto item = [&](auto which, int at) {
+    constexpr int PHASE = decltype(which)::value;
     Item t;
     const int k = PHASE == 3 ? find<&OrthMat::mn0>(v.mat, v.n, at) : find<&OrthMat::sq0>(v.mat, v.n, at);
     t.q = v.mat[k];
@@ -263,71 +290,98 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
   if (warp == 0) {
     int stage = 0, phase = 0;
     bool go = true;
-    for (int at = blockIdx.x; at < st.items && go; at += gridDim.x) {
-      const Item t = item(at);
-      const OrthMat& q = t.q;
-      const bool same = PHASE == 1 && t.i == t.j / 2;  // B's columns are among A's rows
-      const uint8_t *pa, *pb;  // of the first stage; both go on by a tile, B of phase 3 by half a tile's rows
-      if constexpr (PHASE == 1) {
-        pa = tile_at(v, q.x[st.in] + t.i * 2 * q.nt);
-        pb = tile_at(v, q.x[st.in] + (t.j / 2) * 2 * q.nt) + (t.j & 1) * 8192;
-      } else if constexpr (PHASE == 2) {
-        pa = tile_at(v, q.a2 + t.i * 2 * q.mt);
-        pb = tile_at(v, q.a + (t.j / 2) * 2 * q.mt) + (t.j & 1) * 8192;
-      } else {
-        pa = tile_at(v, q.b + t.i * 2 * q.mt);
-        pb = tile_at(v, q.x[st.in] + t.j);
-      }
-      for (int kk = 0; kk < t.ks; ++kk) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars.empty[stage], phase ^ 1, st.wc, abort))) { go = false; break; }
-        if (lane == 0) {
-          uint8_t* sa = sm + stage * kStage;
-          uint64_t* full = &bars.full[stage];
-          mbar_expect_tx(full, same ? kOrthTile : kStage);
-          bulk_load(sa, pa + static_cast<size_t>(kk) * kOrthTile, kOrthTile, full);
-          if (!same) {
-            const uint8_t* p = PHASE == 3 ? pb + static_cast<size_t>(kk >> 1) * 2 * q.nt * kOrthTile + (kk & 1) * 8192
-                                          : pb + static_cast<size_t>(kk) * kOrthTile;
-            bulk_load(sa + kOrthTile, p, 8192, full);
-            bulk_load(sa + kOrthTile + 8192, p + kOrthPlane, 8192, full);
-          }
+    auto load = [&](auto which, int k) {
+      constexpr int PHASE = decltype(which)::value;
+      const int items = PHASE == 3 ? st.mn : st.sq, in = k & 1, e = 3 * k + PHASE - 1;
+      bool ready = e == 0;
+      for (int at = blockIdx.x; at < items && go; at += gridDim.x) {
+        const Item t = item(which, at);
+        const OrthMat& q = t.q;
+        const bool same = PHASE == 1 && t.i == t.j / 2;  // B's columns are among A's rows
+        const uint8_t *pa, *pb;  // of the first stage; both go on by a tile, B of phase 3 by half a tile's rows
+        if constexpr (PHASE == 1) {
+          pa = tile_at(v, q.x[in] + t.i * 2 * q.nt);
+          pb = tile_at(v, q.x[in] + (t.j / 2) * 2 * q.nt) + (t.j & 1) * 8192;
+        } else if constexpr (PHASE == 2) {
+          pa = tile_at(v, q.a2 + t.i * 2 * q.mt);
+          pb = tile_at(v, q.a + (t.j / 2) * 2 * q.mt) + (t.j & 1) * 8192;
+        } else {
+          pa = tile_at(v, q.b + t.i * 2 * q.mt);
+          pb = tile_at(v, q.x[in] + t.j);
         }
-        __syncwarp();
-        if (++stage == kStages) { stage = 0; phase ^= 1; }
+        if (!ready) {
+          go = count_wait(st.done + e - 1, 4u * min(static_cast<int>(gridDim.x), PHASE == 1 ? st.mn : st.sq), st.wc, abort);
+          if (!go) break;
+          ready = true;
+        }
+        for (int kk = 0; kk < t.ks; ++kk) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars.empty[stage], phase ^ 1, st.wc, abort))) { go = false; break; }
+          if (lane == 0) {
+            uint8_t* sa = sm + stage * kStage;
+            uint64_t* full = &bars.full[stage];
+            mbar_expect_tx(full, same ? kOrthTile : kStage);
+            bulk_load(sa, pa + static_cast<size_t>(kk) * kOrthTile, kOrthTile, full);
+            if (!same) {
+              const uint8_t* p = PHASE == 3 ? pb + static_cast<size_t>(kk >> 1) * 2 * q.nt * kOrthTile + (kk & 1) * 8192
+                                            : pb + static_cast<size_t>(kk) * kOrthTile;
+              bulk_load(sa + kOrthTile, p, 8192, full);
+              bulk_load(sa + kOrthTile + 8192, p + kOrthPlane, 8192, full);
+            }
+          }
+          __syncwarp();
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        }
       }
+    };
+    for (int k = 0; k < st.steps && go; ++k) {
+      load(Phase<1>{}, k);
+      load(Phase<2>{}, k);
+      load(Phase<3>{}, k);
     }
   } else if (warp == 1) {
     constexpr uint32_t kPlaneW = kOrthPlane / 16, kStageW = kStage / 16;
-    const uint32_t idesc = idesc_f16_f32(128, 64, 0, PHASE == 3 ? 1 : 0);
-    const uint32_t s0 = smem_u32(sm) >> 4, a0 = s0 | (1u << 16), b0 = s0 | ((PHASE == 3 ? 512u : 1u) << 16);
     int stage = 0, phase = 0, local = 0;
     bool go = true;
-    for (int at = blockIdx.x; at < st.items && go; at += gridDim.x, ++local) {
-      const Item t = item(at);
-      const int ab = local & 1;
-      const bool same = PHASE == 1 && t.i == t.j / 2;
-      // B's low plane behind its high one, a tile's plane away where it is part of A
-      const uint32_t b_at = same ? (t.j & 1) * 512u : kOrthTile / 16, b_lo = same ? kPlaneW : 512u;
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars.acc_empty[ab], ((local >> 1) & 1) ^ 1, st.wc, abort))) break;
-      tc_fence_after();
-      for (int kk = 0; kk < t.ks; ++kk) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars.full[stage], phase, st.wc, abort))) { go = false; break; }
-        tc_fence_after();
-        const uint32_t xa = a0 + stage * kStageW, xb = b0 + stage * kStageW + b_at, d = tmem + ab * 64;
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t ka = xa + 2 * k, kb = xb + (PHASE == 3 ? 128 * k : 2 * k);
-            mma_ss_w(d, ka, kb, idesc, (kk > 0 || k > 0) ? 1u : 0u);
-            mma_ss_w(d, ka, kb + b_lo, idesc, 1u);
-            mma_ss_w(d, ka + kPlaneW, kb, idesc, 1u);
-          }
-          mma_commit(&bars.empty[stage]);
-          if (kk == t.ks - 1) mma_commit(&bars.acc_full[ab]);
+    auto multiply = [&](auto which) {
+      constexpr int PHASE = decltype(which)::value;
+      const uint32_t idesc = idesc_f16_f32(128, 64, 0, PHASE == 3 ? 1 : 0);
+      const uint32_t s0 = smem_u32(sm) >> 4, a0 = s0 | (1u << 16), b0 = s0 | ((PHASE == 3 ? 512u : 1u) << 16);
+      const int items = PHASE == 3 ? st.mn : st.sq;
+      for (int at = blockIdx.x; at < items && go; at += gridDim.x, ++local) {
+        const Item t = item(which, at);
+        const int ab = local & 1;
+        const bool same = PHASE == 1 && t.i == t.j / 2;
+        // B's low plane behind its high one, a tile's plane away where it is part of A
+        const uint32_t b_at = same ? (t.j & 1) * 512u : kOrthTile / 16, b_lo = same ? kPlaneW : 512u;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars.acc_empty[ab], ((local >> 1) & 1) ^ 1, st.wc, abort))) {
+          go = false;
+          break;
         }
-        __syncwarp();
-        if (++stage == kStages) { stage = 0; phase ^= 1; }
+        tc_fence_after();
+        for (int kk = 0; kk < t.ks; ++kk) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars.full[stage], phase, st.wc, abort))) { go = false; break; }
+          tc_fence_after();
+          const uint32_t xa = a0 + stage * kStageW, xb = b0 + stage * kStageW + b_at, d = tmem + ab * 64;
+          if (elect_one()) {
+  #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t ka = xa + 2 * k, kb = xb + (PHASE == 3 ? 128 * k : 2 * k);
+              mma_ss_w(d, ka, kb, idesc, (kk > 0 || k > 0) ? 1u : 0u);
+              mma_ss_w(d, ka, kb + b_lo, idesc, 1u);
+              mma_ss_w(d, ka + kPlaneW, kb, idesc, 1u);
+            }
+            mma_commit(&bars.empty[stage]);
+            if (kk == t.ks - 1) mma_commit(&bars.acc_full[ab]);
+          }
+          __syncwarp();
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        }
       }
+    };
+    for (int k = 0; k < st.steps && go; ++k) {
+      multiply(Phase<1>{});
+      multiply(Phase<2>{});
+      multiply(Phase<3>{});
     }
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2, r = quarter * 32 + lane;
@@ -367,67 +421,83 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
     };
     constexpr float kBack = 1.f / kOrthScale;
     int local = 0;
-    for (int at = blockIdx.x; at < st.items && go; at += gridDim.x, ++local) {
-      const Item t = item(at);
-      const OrthMat& q = t.q;
-      const int ab = local & 1;
-      go = __all_sync(0xffffffffu, mbar_wait(&bars.acc_full[ab], (local >> 1) & 1, st.wc, abort));
-      if (!go) break;
-      tc_fence_after();
-      uint32_t u[32];
-      tmem_ld32_wait(tmem + lane_addr + ab * 64 + 32 * half, u);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.acc_empty[ab]);
-      const int diag = t.i * 128 + r - t.j * 64;  // the column of this row's diagonal element
-      if constexpr (PHASE == 1) {
-        const int tt = t.i * 2 * q.mt + t.j;
-        store(tile_at(v, q.a + tt), u, [&](int, float x) { return x * (kBack * kBack); });
-        store(tile_at(v, q.a2 + tt), u, [&](int col, float x) {
-          return st.c * (x * (kBack * kBack)) + (col == diag ? st.b : 0.f);
-        });
-      } else if constexpr (PHASE == 2) {
-        store(tile_at(v, q.b + t.i * 2 * q.mt + t.j), u,
-              [&](int col, float x) { return x + (col == diag ? st.a : 0.f); });
-      } else if (!st.last) {
-        store(tile_at(v, q.x[st.in ^ 1] + t.i * 2 * q.nt + t.j), u, [&](int, float x) { return x; });
-      } else {
-        // a transposed matrix's rows are contiguous across lanes, an ordinary one's go
-        // through the staging (64 columns of BF16, swizzled)
-        const int row0 = t.i * 128 + quarter * 32, col0 = t.j * 64;
-        uint16_t* dst = static_cast<uint16_t*>(q.dst);
-        if (q.flags & kOrthTall) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int col = col0 + 32 * half + e;
-            if (row0 + lane < q.m && col < q.n)
-              dst[col * q.ld_dst + row0 + lane] =
-                  static_cast<uint16_t>(pack_bf16x2(__uint_as_float(u[e]) * kBack, 0.f) & 0xFFFFu);
-          }
-          continue;
-        }
-        if (!pair_sync()) break;  // the staging has been read
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(u[8 * c + 2 * e]) * kBack, __uint_as_float(u[8 * c + 2 * e + 1]) * kBack);
-          *reinterpret_cast<uint4*>(stg + sw128(lane, 4 * half + c)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        if (!pair_sync()) break;
-        const int r0 = 16 * half, rows = min(16, q.m - row0 - r0), cols = min(64, q.n - col0);
-        uint16_t* to = dst + (row0 + r0) * q.ld_dst + col0;
-        if (cols == 64 && (reinterpret_cast<uintptr_t>(to) & 15) == 0 && q.ld_dst % 8 == 0) {
-          for (int e = lane; e < rows * 8; e += 32)
-            *reinterpret_cast<uint4*>(to + (e >> 3) * q.ld_dst + (e & 7) * 8) =
-                *reinterpret_cast<const uint4*>(stg + sw128(r0 + (e >> 3), e & 7));
+    auto take = [&](auto which, int step) {
+      constexpr int PHASE = decltype(which)::value;
+      const int items = PHASE == 3 ? st.mn : st.sq, in = step & 1;
+      const bool last = PHASE == 3 && step == st.steps - 1;  // X goes to the destinations
+      for (int at = blockIdx.x; at < items && go; at += gridDim.x, ++local) {
+        const Item t = item(which, at);
+        const OrthMat& q = t.q;
+        const int ab = local & 1;
+        go = __all_sync(0xffffffffu, mbar_wait(&bars.acc_full[ab], (local >> 1) & 1, st.wc, abort));
+        if (!go) break;
+        tc_fence_after();
+        uint32_t u[32];
+        tmem_ld32_wait(tmem + lane_addr + ab * 64 + 32 * half, u);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.acc_empty[ab]);
+        const int diag = t.i * 128 + r - t.j * 64;  // the column of this row's diagonal element
+        if constexpr (PHASE == 1) {
+          const int tt = t.i * 2 * q.mt + t.j;
+          store(tile_at(v, q.a + tt), u, [&](int, float x) { return x * (kBack * kBack); });
+          store(tile_at(v, q.a2 + tt), u, [&](int col, float x) {
+            return st.c * (x * (kBack * kBack)) + (col == diag ? st.b : 0.f);
+          });
+        } else if constexpr (PHASE == 2) {
+          store(tile_at(v, q.b + t.i * 2 * q.mt + t.j), u,
+                [&](int col, float x) { return x + (col == diag ? st.a : 0.f); });
+        } else if (!last) {
+          store(tile_at(v, q.x[in ^ 1] + t.i * 2 * q.nt + t.j), u, [&](int, float x) { return x; });
         } else {
-          for (int rr = 0; rr < rows; ++rr)
-            for (int e = lane; e < cols; e += 32)
-              to[rr * q.ld_dst + e] = reinterpret_cast<const uint16_t*>(stg + sw128(r0 + rr, e >> 3))[e & 7];
+          // a transposed matrix's rows are contiguous across lanes, an ordinary one's go
+          // through the staging (64 columns of BF16, swizzled)
+          const int row0 = t.i * 128 + quarter * 32, col0 = t.j * 64;
+          uint16_t* dst = static_cast<uint16_t*>(q.dst);
+          if (q.flags & kOrthTall) {
+  #pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int col = col0 + 32 * half + e;
+              if (row0 + lane < q.m && col < q.n)
+                dst[col * q.ld_dst + row0 + lane] =
+                    static_cast<uint16_t>(pack_bf16x2(__uint_as_float(u[e]) * kBack, 0.f) & 0xFFFFu);
+            }
+            continue;
+          }
+          if (!pair_sync()) break;  // the staging has been read
+  #pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[4];
+  #pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_bf16x2(__uint_as_float(u[8 * c + 2 * e]) * kBack, __uint_as_float(u[8 * c + 2 * e + 1]) * kBack);
+            *reinterpret_cast<uint4*>(stg + sw128(lane, 4 * half + c)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (!pair_sync()) break;
+          const int r0 = 16 * half, rows = min(16, q.m - row0 - r0), cols = min(64, q.n - col0);
+          uint16_t* to = dst + (row0 + r0) * q.ld_dst + col0;
+          if (cols == 64 && (reinterpret_cast<uintptr_t>(to) & 15) == 0 && q.ld_dst % 8 == 0) {
+            for (int e = lane; e < rows * 8; e += 32)
+              *reinterpret_cast<uint4*>(to + (e >> 3) * q.ld_dst + (e & 7) * 8) =
+                  *reinterpret_cast<const uint4*>(stg + sw128(r0 + (e >> 3), e & 7));
+          } else {
+            for (int rr = 0; rr < rows; ++rr)
+              for (int e = lane; e < cols; e += 32)
+                to[rr * q.ld_dst + e] = reinterpret_cast<const uint16_t*>(stg + sw128(r0 + rr, e >> 3))[e & 7];
+          }
         }
       }
+      if (go && !last && static_cast<int>(blockIdx.x) < items && half == 0 && lane == 0) {
+        bulk_wait_all();  // this thread's stores, the quarter's, are in memory
+        fence_proxy_async_all();
+        red_release_gpu(st.done + 3 * step + PHASE - 1, 1u);
+      }
+      __syncwarp();
+    };
+    for (int k = 0; k < st.steps && go; ++k) {
+      take(Phase<1>{}, k);
+      take(Phase<2>{}, k);
+      take(Phase<3>{}, k);
     }
     if (half == 0 && lane == 0) bulk_wait_all();
     __syncwarp();
@@ -530,7 +600,7 @@ bool plan_of(const triattn_matrix* in, const triattn_matrix* out, long long n, P
     if (p->tiles >= (1ll << 31) || p->parts >= (1ll << 31)) return false;
   }
   auto up = [](size_t x) { return (x + 1023) / 1024 * 1024; };
-  p->part_off = up(p->mats.size() * sizeof(OrthMat));
+  p->part_off = up(kDoneBytes + p->mats.size() * sizeof(OrthMat));
   p->tiles_off = up(p->part_off + static_cast<size_t>(p->parts) * 4);
   p->total = p->tiles_off + static_cast<size_t>(p->tiles) * kOrthTile;
   return true;
@@ -554,18 +624,30 @@ triattn_status check_list(const triattn_matrix* ms, long long n, bool output) {
   return TRIATTN_OK;
 }
 
-template <int PHASE>
-cudaError_t launch_phase(const OrthView& v, const OrthStep& st, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(orth_gemm_kernel<PHASE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+cudaError_t launch_gemm(const OrthView& v, const OrthRun& st, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(orth_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  return trace_call(kKOrthGemm, s, [&] {
-    return launch_after(false, orth_gemm_kernel<PHASE>, std::min(st.items, 152), kThreads, kSmem, s, v, st);
-  });
+  int device = 0, sms = 0;
+  if (cudaGetDevice(&device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+    return cudaErrorInvalidDevice;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(std::min(st.mn, sms));  // m <= n: no phase has more tiles
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeCooperative;
+  at.val.cooperative = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, orth_gemm_kernel, v, st);
 }
 
 cudaError_t run(const Plan& p, int steps, const float* co, float eps, uint8_t* ws, const WaitCtl& wc, cudaStream_t s) {
-  OrthMat* mats = reinterpret_cast<OrthMat*>(ws);
-  OrthView v{mats, reinterpret_cast<float*>(ws + p.part_off), ws + p.tiles_off, static_cast<int>(p.mats.size())};
+  OrthMat* mats = reinterpret_cast<OrthMat*>(ws + kDoneBytes);
+  OrthView v{mats, reinterpret_cast<float*>(ws + p.part_off), ws + p.tiles_off, reinterpret_cast<uint32_t*>(ws),
+             static_cast<int>(p.mats.size())};
   OrthTable t;
   const bool small = p.mats.size() <= static_cast<size_t>(kUpload);
   cudaError_t e = cudaSuccess;
@@ -590,16 +672,8 @@ cudaError_t run(const Plan& p, int steps, const float* co, float eps, uint8_t* w
     });
   v.mat += p.solo;
   v.n -= p.solo;
-  OrthStep st{co[0], co[1], co[2], 0, 0, 0, wc};
-  for (int k = 0; k < steps && v.n > 0 && e == cudaSuccess; ++k) {
-    st.in = k & 1;
-    st.last = k == steps - 1;
-    st.items = static_cast<int>(p.sq);
-    e = launch_phase<1>(v, st, s);
-    if (e == cudaSuccess) e = launch_phase<2>(v, st, s);
-    st.items = static_cast<int>(p.mn);
-    if (e == cudaSuccess) e = launch_phase<3>(v, st, s);
-  }
+  const OrthRun st{co[0], co[1], co[2], steps, static_cast<int>(p.sq), static_cast<int>(p.mn), v.done, wc};
+  if (v.n > 0 && e == cudaSuccess) e = trace_call(kKOrthGemm, s, [&] { return launch_gemm(v, st, s); });
   return e;
 }
 
@@ -629,7 +703,7 @@ triattn_status triattn_orthogonalize(const triattn_matrix* matrices, const triat
   if (coefficients == nullptr || steps < 1 || !(eps > 0.f) || !std::isfinite(eps)) return TRIATTN_ERR_INVALID_ARG;
   for (int i = 0; i < 3; ++i)
     if (!std::isfinite(coefficients[i])) return TRIATTN_ERR_INVALID_ARG;
-  if (steps > 64) return TRIATTN_ERR_UNSUPPORTED;
+  if (steps > kMaxSteps) return TRIATTN_ERR_UNSUPPORTED;
   for (long long i = 0; i < n; ++i)
     if (out[i].rows != matrices[i].rows || out[i].cols != matrices[i].cols) return TRIATTN_ERR_INVALID_ARG;
   try {

@@ -31,6 +31,7 @@ struct OrthView {
   const OrthMat* mat;
   float* part;
   uint8_t* tiles;
+  uint32_t* done;  // counts of the larger matrices' phases
   int n;
 };
 __device__ __forceinline__ uint8_t* tile_at(const OrthView& v, int t) {
