@@ -39,9 +39,6 @@
 namespace triattn {
 namespace {
 
-constexpr int kMaxSteps = 64;
-constexpr int kDoneBytes = 4 * 3 * kMaxSteps;  // a count for every phase
-static_assert(kDoneBytes / 4 <= 256 && kDoneBytes % 16 == 0, "cleared by one block");
 constexpr int kUpload = 256;
 struct OrthTable {
   OrthMat mat[kUpload];
@@ -107,7 +104,7 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ 
   __shared__ float sh[8];
   let_next_start();
   after_previous();  // the table, or what last used the workspace
-  if (blockIdx.x == 0 && threadIdx.x < kDoneBytes / 4) v.done[threadIdx.x] = 0;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < v.n; i += gridDim.x * 256) v.done[i] = 0;
   if (PARAM && blockIdx.x == 0)
     for (int i = threadIdx.x; i < t.n; i += 256) to[i] = t.mat[i];
   const OrthMat* mat = PARAM ? t.mat : v.mat;
@@ -196,7 +193,7 @@ __global__ void __launch_bounds__(256) orth_load_kernel(OrthView v, float eps) {
 constexpr int kStages = 4;
 constexpr int kStage = kOrthTile + kOrthTile / 2;  // 64 of K: 128 rows of A, 64 columns of B, hi and lo
 constexpr int kEpiWarps = 8;
-constexpr int kStg = 8192;  // staging of 32 rows of a tile, hi and lo
+constexpr int kStg = 4096;  // staging of 32 rows of a tile, BF16
 constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr int kSmem = kStages * kStage + 4 * kStg + 1024;
 
@@ -210,7 +207,6 @@ struct GemmBars {
 struct OrthRun {
   float a, b, c;
   int steps, sq, mn;  // items of the phases of A and A', and of X
-  uint32_t* done;     // [3 steps] rows of warps that have stored all of a phase's tiles
   WaitCtl wc;
 };
 
@@ -240,9 +236,9 @@ __device__ __forceinline__ bool count_wait(const uint32_t* p, uint32_t n, const 
 // All steps of the matrices of more than 128 rows.  A phase is its product's tiles of
 // 128 x 64, shared out over one CTA per SM; warp 0 loads (64 of K per stage, 48 KB),
 // warp 1 issues twelve MMAs per stage (four of K by three products), warps 2-9 take
-// the accumulator (one of two) out, split it and store it through shared memory as
-// bulk copies of 4 KB.  A phase's loads wait until all CTAs that had tiles of the one
-// before have counted themselves (a cooperative launch: all of them run).  Tiles of
+// the accumulator (one of two) out, split it and store it.  The loads of a matrix's
+// tiles wait until all of its tiles of the phase before have been counted (a
+// cooperative launch: all CTAs run; each has its tiles phase by phase).  Tiles of
 // 128 columns need a third fewer bytes per product, but the lists that come here are
 // a few matrices, half of whose tiles would leave most SMs without one (twelve of
 // 256 x 1037 have 48 such tiles of A).  A and B' are held without the scale.
@@ -273,13 +269,14 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
 
   struct Item {
     OrthMat q;
+    int k;         // the matrix
     int i, j, ks;  // tile (i, j) of the product, stages of K
   };
   auto item = [&](auto which, int at) {
     constexpr int PHASE = decltype(which)::value;
     Item t;
-    const int k = PHASE == 3 ? find<&OrthMat::mn0>(v.mat, v.n, at) : find<&OrthMat::sq0>(v.mat, v.n, at);
-    t.q = v.mat[k];
+    t.k = PHASE == 3 ? find<&OrthMat::mn0>(v.mat, v.n, at) : find<&OrthMat::sq0>(v.mat, v.n, at);
+    t.q = v.mat[t.k];
     const int r = at - (PHASE == 3 ? t.q.mn0 : t.q.sq0), w = 2 * (PHASE == 3 ? t.q.nt : t.q.mt);
     t.i = r / w;
     t.j = r - t.i * w;
@@ -292,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
     bool go = true;
     auto load = [&](auto which, int k) {
       constexpr int PHASE = decltype(which)::value;
-      const int items = PHASE == 3 ? st.mn : st.sq, in = k & 1, e = 3 * k + PHASE - 1;
-      bool ready = e == 0;
+      const int items = PHASE == 3 ? st.mn : st.sq, in = k & 1;
+      int ready = -1;  // the matrix whose operands are
       for (int at = blockIdx.x; at < items && go; at += gridDim.x) {
         const Item t = item(which, at);
         const OrthMat& q = t.q;
@@ -309,10 +306,11 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
           pa = tile_at(v, q.b + t.i * 2 * q.mt);
           pb = tile_at(v, q.x[in] + t.j);
         }
-        if (!ready) {
-          go = count_wait(st.done + e - 1, 4u * min(static_cast<int>(gridDim.x), PHASE == 1 ? st.mn : st.sq), st.wc, abort);
+        if (t.k != ready) {
+          const uint32_t sq = 2 * q.mt * q.mt, before = k * (2 * sq + 2 * q.mt * q.nt) + (PHASE - 1) * sq;
+          go = before == 0 || count_wait(v.done + t.k, kEpiWarps * before, st.wc, abort);
           if (!go) break;
-          ready = true;
+          ready = t.k;
         }
         for (int kk = 0; kk < t.ks; ++kk) {
           if (!__all_sync(0xffffffffu, mbar_wait(&bars.empty[stage], phase ^ 1, st.wc, abort))) { go = false; break; }
@@ -363,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
           tc_fence_after();
           const uint32_t xa = a0 + stage * kStageW, xb = b0 + stage * kStageW + b_at, d = tmem + ab * 64;
           if (elect_one()) {
-  #pragma unroll
+#pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t ka = xa + 2 * k, kb = xb + (PHASE == 3 ? 128 * k : 2 * k);
               mma_ss_w(d, ka, kb, idesc, (kk > 0 || k > 0) ? 1u : 0u);
@@ -386,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2, r = quarter * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-    uint8_t* stg = sm + kStages * kStage + quarter * kStg;  // this quarter's rows
+    uint8_t* stg = sm + kStages * kStage + quarter * kStg;  // this quarter's rows of the result
     uint32_t pphase = 0;
     bool go = true;
     auto pair_sync = [&]() {
@@ -396,27 +394,24 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
       pphase ^= 1;
       return go;
     };
-    // this warp's 32 of a tile's columns, f(column, accumulator), and the quarter's rows out
+    // this warp's 32 rows and columns of a tile, f(column, accumulator), to its image:
+    // two pieces of eight columns lie side by side, in the order of the swizzle
     auto store = [&](uint8_t* tile, const uint32_t (&acc)[32], auto&& f) {
-      if (half == 0 && lane == 0) bulk_wait_read();  // the staging has been read
-      if (!pair_sync()) return;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float y[8];
+      for (int c = 0; c < 4; c += 2) {
+        uint4 h[2], l[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = f(32 * half + 8 * c + e, __uint_as_float(acc[8 * c + e]));
-        uint4 h, l;
-        split8(y, h, l);
-        const uint32_t o = lane * 128 + (((4 * half + c) ^ (lane & 7)) << 4);
-        *reinterpret_cast<uint4*>(stg + o) = h;
-        *reinterpret_cast<uint4*>(stg + 4096 + o) = l;
-      }
-      fence_proxy_async_smem();
-      if (!pair_sync()) return;
-      if (half == 0 && lane == 0) {
-        bulk_store_nc(tile + quarter * 4096, stg, 4096);
-        bulk_store_nc(tile + kOrthPlane + quarter * 4096, stg + 4096, 4096);
-        bulk_commit();
+        for (int p = 0; p < 2; ++p) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            y[e] = f(32 * half + 8 * (c + p) + e, __uint_as_float(acc[8 * (c + p) + e]));
+          split8(y, h[p], l[p]);
+        }
+        const bool odd = (lane & 1) != 0;
+        uint8_t* to = tile + r * 128 + (((4 * half + c) ^ (lane & 6)) << 4);
+        st_global_32(to, odd ? h[1] : h[0], odd ? h[0] : h[1]);
+        st_global_32(to + kOrthPlane, odd ? l[1] : l[0], odd ? l[0] : l[1]);
       }
     };
     constexpr float kBack = 1.f / kOrthScale;
@@ -455,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
           const int row0 = t.i * 128 + quarter * 32, col0 = t.j * 64;
           uint16_t* dst = static_cast<uint16_t*>(q.dst);
           if (q.flags & kOrthTall) {
-  #pragma unroll
+#pragma unroll
             for (int e = 0; e < 32; ++e) {
               const int col = col0 + 32 * half + e;
               if (row0 + lane < q.m && col < q.n)
@@ -465,10 +460,10 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
             continue;
           }
           if (!pair_sync()) break;  // the staging has been read
-  #pragma unroll
+#pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t w[4];
-  #pragma unroll
+#pragma unroll
             for (int e = 0; e < 4; ++e)
               w[e] = pack_bf16x2(__uint_as_float(u[8 * c + 2 * e]) * kBack, __uint_as_float(u[8 * c + 2 * e + 1]) * kBack);
             *reinterpret_cast<uint4*>(stg + sw128(lane, 4 * half + c)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -486,21 +481,20 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
                 to[rr * q.ld_dst + e] = reinterpret_cast<const uint16_t*>(stg + sw128(r0 + rr, e >> 3))[e & 7];
           }
         }
+        if (!last) {
+          __syncwarp();
+          if (lane == 0) {
+            fence_proxy_async_all();
+            red_release_gpu(v.done + t.k, 1u);
+          }
+        }
       }
-      if (go && !last && static_cast<int>(blockIdx.x) < items && half == 0 && lane == 0) {
-        bulk_wait_all();  // this thread's stores, the quarter's, are in memory
-        fence_proxy_async_all();
-        red_release_gpu(st.done + 3 * step + PHASE - 1, 1u);
-      }
-      __syncwarp();
     };
     for (int k = 0; k < st.steps && go; ++k) {
       take(Phase<1>{}, k);
       take(Phase<2>{}, k);
       take(Phase<3>{}, k);
     }
-    if (half == 0 && lane == 0) bulk_wait_all();
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -520,7 +514,7 @@ struct Plan {
   std::vector<OrthMat> mats;
   int solo = 0, team = 1;
   long long parts = 0, load_tiles = 0, sq = 0, mn = 0, tiles = 0;
-  size_t part_off = 0, tiles_off = 0, total = 0;
+  size_t done_off = 0, part_off = 0, tiles_off = 0, total = 0;
 };
 
 bool dims_ok(const triattn_matrix& g) { return g.rows > 0 && g.cols > 0; }
@@ -600,7 +594,8 @@ bool plan_of(const triattn_matrix* in, const triattn_matrix* out, long long n, P
     if (p->tiles >= (1ll << 31) || p->parts >= (1ll << 31)) return false;
   }
   auto up = [](size_t x) { return (x + 1023) / 1024 * 1024; };
-  p->part_off = up(kDoneBytes + p->mats.size() * sizeof(OrthMat));
+  p->done_off = up(p->mats.size() * sizeof(OrthMat));
+  p->part_off = up(p->done_off + p->mats.size() * 4);
   p->tiles_off = up(p->part_off + static_cast<size_t>(p->parts) * 4);
   p->total = p->tiles_off + static_cast<size_t>(p->tiles) * kOrthTile;
   return true;
@@ -645,8 +640,9 @@ cudaError_t launch_gemm(const OrthView& v, const OrthRun& st, cudaStream_t s) {
 }
 
 cudaError_t run(const Plan& p, int steps, const float* co, float eps, uint8_t* ws, const WaitCtl& wc, cudaStream_t s) {
-  OrthMat* mats = reinterpret_cast<OrthMat*>(ws + kDoneBytes);
-  OrthView v{mats, reinterpret_cast<float*>(ws + p.part_off), ws + p.tiles_off, reinterpret_cast<uint32_t*>(ws),
+  OrthMat* mats = reinterpret_cast<OrthMat*>(ws);
+  OrthView v{mats, reinterpret_cast<float*>(ws + p.part_off), ws + p.tiles_off,
+             reinterpret_cast<uint32_t*>(ws + p.done_off),
              static_cast<int>(p.mats.size())};
   OrthTable t;
   const bool small = p.mats.size() <= static_cast<size_t>(kUpload);
@@ -671,8 +667,9 @@ cudaError_t run(const Plan& p, int steps, const float* co, float eps, uint8_t* w
       return launch_orth_solo(mats, p.solo, v.tiles, steps, OrthCoef{co[0], co[1], co[2]}, p.team, wc, s);
     });
   v.mat += p.solo;
+  v.done += p.solo;
   v.n -= p.solo;
-  const OrthRun st{co[0], co[1], co[2], steps, static_cast<int>(p.sq), static_cast<int>(p.mn), v.done, wc};
+  const OrthRun st{co[0], co[1], co[2], steps, static_cast<int>(p.sq), static_cast<int>(p.mn), wc};
   if (v.n > 0 && e == cudaSuccess) e = trace_call(kKOrthGemm, s, [&] { return launch_gemm(v, st, s); });
   return e;
 }
@@ -703,7 +700,7 @@ triattn_status triattn_orthogonalize(const triattn_matrix* matrices, const triat
   if (coefficients == nullptr || steps < 1 || !(eps > 0.f) || !std::isfinite(eps)) return TRIATTN_ERR_INVALID_ARG;
   for (int i = 0; i < 3; ++i)
     if (!std::isfinite(coefficients[i])) return TRIATTN_ERR_INVALID_ARG;
-  if (steps > kMaxSteps) return TRIATTN_ERR_UNSUPPORTED;
+  if (steps > 64) return TRIATTN_ERR_UNSUPPORTED;
   for (long long i = 0; i < n; ++i)
     if (out[i].rows != matrices[i].rows || out[i].cols != matrices[i].cols) return TRIATTN_ERR_INVALID_ARG;
   try {

@@ -31,7 +31,7 @@ struct OrthView {
   const OrthMat* mat;
   float* part;
   uint8_t* tiles;
-  uint32_t* done;  // counts of the larger matrices' phases
+  uint32_t* done;  // tiles (by warps) that have been stored, of every larger matrix
   int n;
 };
 __device__ __forceinline__ uint8_t* tile_at(const OrthView& v, int t) {
