@@ -483,10 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
         }
         if (!last) {
           __syncwarp();
-          if (lane == 0) {
-            fence_proxy_async_all();
-            red_release_gpu(v.done + t.k, 1u);
-          }
+          if (lane == 0) red_release_gpu(v.done + t.k, 1u);
         }
       }
     };
