@@ -190,18 +190,20 @@ __global__ void __launch_bounds__(256) orth_load_kernel(OrthView v, float eps) {
 }
 
 // ------------------------------------------------------------- products
-constexpr int kStages = 4;
-constexpr int kStage = kOrthTile + kOrthTile / 2;  // 64 of K: 128 rows of A, 64 columns of B, hi and lo
 constexpr int kEpiWarps = 8;
-constexpr int kStg = 4096;  // staging of 32 rows of a tile, BF16
 constexpr int kThreads = (2 + kEpiWarps) * 32;
-constexpr int kSmem = kStages * kStage + 4 * kStg + 1024;
-
-struct GemmBars {
-  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
-  uint64_t pair[4];  // the two warps of a quarter of the rows
-  uint32_t tmem_slot;
-  int abort;
+template <int W>  // columns of a product's tile, 64 or 128
+struct Gemm {
+  static constexpr int kStages = W == 64 ? 4 : 3;
+  static constexpr int kStage = kOrthTile + W * 256;  // 64 of K: 128 rows of A, W columns of B, hi and lo
+  static constexpr int kStg = 32 * W * 2;             // staging of 32 rows of a tile of the result, BF16
+  static constexpr int kSmem = kStages * kStage + 4 * kStg + 1024;
+  struct Bars {
+    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+    uint64_t pair[4];  // the two warps of a quarter of the rows
+    uint32_t tmem_slot;
+    int abort;
+  };
 };
 
 struct OrthRun {
@@ -212,6 +214,18 @@ struct OrthRun {
 
 template <int P>
 using Phase = std::integral_constant<int, P>;
+
+// A matrix's row of the table, which no kernel that takes it so writes.
+__device__ __forceinline__ OrthMat constant(const OrthMat* p) {
+  static_assert(sizeof(OrthMat) == 96, "six pieces");
+  union {
+    uint4 raw[6];
+    OrthMat mat;
+  } u;
+#pragma unroll
+  for (int i = 0; i < 6; ++i) u.raw[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  return u.mat;
+}
 
 // Bounded wait of a whole warp until what `n` others have stored before they added
 // themselves to *p can be loaded by bulk copies.
@@ -234,17 +248,19 @@ __device__ __forceinline__ bool count_wait(const uint32_t* p, uint32_t n, const 
 }
 
 // All steps of the matrices of more than 128 rows.  A phase is its product's tiles of
-// 128 x 64, shared out over one CTA per SM; warp 0 loads (64 of K per stage, 48 KB),
-// warp 1 issues twelve MMAs per stage (four of K by three products), warps 2-9 take
-// the accumulator (one of two) out, split it and store it.  The loads of a matrix's
-// tiles wait until all of its tiles of the phase before have been counted (a
-// cooperative launch: all CTAs run; each has its tiles phase by phase).  Tiles of
-// 128 columns need a third fewer bytes per product, but the lists that come here are
-// a few matrices, half of whose tiles would leave most SMs without one (twelve of
-// 256 x 1037 have 48 such tiles of A).  A and B' are held without the scale.
+// 128 x W, shared out over one CTA per SM; warp 0 loads (64 of K per stage, 48 or
+// 64 KB), warp 1 issues twelve MMAs per stage (four of K by three products), warps
+// 2-9 take the accumulator (one of two) out, split it and store it.  The loads of a
+// matrix's tiles wait until all of its tiles of the phase before have been counted (a
+// cooperative launch: all CTAs run; each has its tiles phase by phase).  Where a
+// CTA's tiles lie is looked up for 32 of them at once, a lane to a tile, before the
+// wait.  A and B' are held without the scale.
+template <int W>
 __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, OrthRun st) {
+  using G = Gemm<W>;
+  constexpr int kStages = G::kStages, kStage = G::kStage, T = 128 / W;  // W-column tiles of 128 columns
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ GemmBars bars;
+  __shared__ typename G::Bars bars;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abort = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -261,75 +277,105 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
     bars.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(&bars.tmem_slot, 128);
+  if (warp == 1) tmem_alloc(&bars.tmem_slot, 2 * W);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem_slot;
 
-  struct Item {
-    OrthMat q;
-    int k;         // the matrix
-    int i, j, ks;  // tile (i, j) of the product, stages of K
-  };
-  auto item = [&](auto which, int at) {
+  bool go = true;
+  // body(matrix, tile row, tile column, stages of K) for this CTA's tiles of a phase
+  auto tiles = [&](auto which, auto&& body) {
     constexpr int PHASE = decltype(which)::value;
-    Item t;
-    t.k = PHASE == 3 ? find<&OrthMat::mn0>(v.mat, v.n, at) : find<&OrthMat::sq0>(v.mat, v.n, at);
-    t.q = v.mat[t.k];
-    const int r = at - (PHASE == 3 ? t.q.mn0 : t.q.sq0), w = 2 * (PHASE == 3 ? t.q.nt : t.q.mt);
-    t.i = r / w;
-    t.j = r - t.i * w;
-    t.ks = ((PHASE == 1 ? t.q.n : t.q.m) + 63) / 64;
-    return t;
+    const int items = PHASE == 3 ? st.mn : st.sq, grid = gridDim.x;
+    for (long long first = blockIdx.x; first < items && go; first += 32ll * grid) {
+      const long long at = first + static_cast<long long>(lane) * grid;
+      int k = 0, i = 0, j = 0, ks = 0;
+      if (at < items) {
+        int n = v.n;
+        while (n > 1) {  // the last matrix whose first tile is not above it
+          const int h = n / 2;
+          const OrthMat* mid = v.mat + k + h;
+          if (__ldg(PHASE == 3 ? &mid->mn0 : &mid->sq0) <= at) {
+            k += h;
+            n -= h;
+          } else {
+            n = h;
+          }
+        }
+        const OrthMat* q = v.mat + k;
+        const int r = static_cast<int>(at) - __ldg(PHASE == 3 ? &q->mn0 : &q->sq0);
+        const int w = T * __ldg(PHASE == 3 ? &q->nt : &q->mt);
+        i = r / w;
+        j = r - i * w;
+        ks = (__ldg(PHASE == 1 ? &q->n : &q->m) + 63) / 64;
+      }
+      const int count = static_cast<int>(min(32ll, (items - first + grid - 1) / grid));
+      for (int l = 0; l < count && go; ++l)
+        body(__shfl_sync(0xffffffffu, k, l), __shfl_sync(0xffffffffu, i, l), __shfl_sync(0xffffffffu, j, l),
+             __shfl_sync(0xffffffffu, ks, l));
+    }
   };
 
   if (warp == 0) {
     int stage = 0, phase = 0;
-    bool go = true;
-    auto load = [&](auto which, int k) {
+    auto load = [&](auto which, int step) {
       constexpr int PHASE = decltype(which)::value;
-      const int items = PHASE == 3 ? st.mn : st.sq, in = k & 1;
+      const int in = step & 1;
       int ready = -1;  // the matrix whose operands are
-      for (int at = blockIdx.x; at < items && go; at += gridDim.x) {
-        const Item t = item(which, at);
-        const OrthMat& q = t.q;
-        const bool same = PHASE == 1 && t.i == t.j / 2;  // B's columns are among A's rows
+      tiles(which, [&](int k, int i, int j, int ks) {
+        const OrthMat q = constant(v.mat + k);
+        const bool same = PHASE == 1 && i == j / T;  // B's columns are among A's rows
+        const int x = in != 0 ? q.x[1] : q.x[0];
         const uint8_t *pa, *pb;  // of the first stage; both go on by a tile, B of phase 3 by half a tile's rows
         if constexpr (PHASE == 1) {
-          pa = tile_at(v, q.x[in] + t.i * 2 * q.nt);
-          pb = tile_at(v, q.x[in] + (t.j / 2) * 2 * q.nt) + (t.j & 1) * 8192;
+          pa = tile_at(v, x + i * 2 * q.nt);
+          pb = tile_at(v, x + (j / T) * 2 * q.nt) + (j % T) * 8192;
         } else if constexpr (PHASE == 2) {
-          pa = tile_at(v, q.a2 + t.i * 2 * q.mt);
-          pb = tile_at(v, q.a + (t.j / 2) * 2 * q.mt) + (t.j & 1) * 8192;
+          pa = tile_at(v, q.a2 + i * 2 * q.mt);
+          pb = tile_at(v, q.a + (j / T) * 2 * q.mt) + (j % T) * 8192;
         } else {
-          pa = tile_at(v, q.b + t.i * 2 * q.mt);
-          pb = tile_at(v, q.x[in] + t.j);
+          pa = tile_at(v, q.b + i * 2 * q.mt);
+          pb = tile_at(v, x + j * (W / 64));
         }
-        if (t.k != ready) {
-          const uint32_t sq = 2 * q.mt * q.mt, before = k * (2 * sq + 2 * q.mt * q.nt) + (PHASE - 1) * sq;
-          go = before == 0 || count_wait(v.done + t.k, kEpiWarps * before, st.wc, abort);
-          if (!go) break;
-          ready = t.k;
+        if (k != ready) {
+          const uint32_t sq = T * q.mt * q.mt, before = step * (2 * sq + T * q.mt * q.nt) + (PHASE - 1) * sq;
+          go = before == 0 || count_wait(v.done + k, kEpiWarps * before, st.wc, abort);
+          if (!go) return;
+          ready = k;
         }
-        for (int kk = 0; kk < t.ks; ++kk) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&bars.empty[stage], phase ^ 1, st.wc, abort))) { go = false; break; }
+        for (int kk = 0; kk < ks; ++kk) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars.empty[stage], phase ^ 1, st.wc, abort))) {
+            go = false;
+            return;
+          }
           if (lane == 0) {
             uint8_t* sa = sm + stage * kStage;
+            uint8_t* sb = sa + kOrthTile;
             uint64_t* full = &bars.full[stage];
             mbar_expect_tx(full, same ? kOrthTile : kStage);
             bulk_load(sa, pa + static_cast<size_t>(kk) * kOrthTile, kOrthTile, full);
-            if (!same) {
-              const uint8_t* p = PHASE == 3 ? pb + static_cast<size_t>(kk >> 1) * 2 * q.nt * kOrthTile + (kk & 1) * 8192
-                                            : pb + static_cast<size_t>(kk) * kOrthTile;
-              bulk_load(sa + kOrthTile, p, 8192, full);
-              bulk_load(sa + kOrthTile + 8192, p + kOrthPlane, 8192, full);
+            if constexpr (PHASE == 3) {  // blocks of 64 columns, hi of all before lo
+              const uint8_t* p = pb + static_cast<size_t>(kk >> 1) * 2 * q.nt * kOrthTile + (kk & 1) * 8192;
+#pragma unroll
+              for (int c = 0; c < W / 64; ++c) {
+                bulk_load(sb + c * 8192, p + c * kOrthTile, 8192, full);
+                bulk_load(sb + W * 128 + c * 8192, p + c * kOrthTile + kOrthPlane, 8192, full);
+              }
+            } else if (!same) {
+              const uint8_t* p = pb + static_cast<size_t>(kk) * kOrthTile;
+              if constexpr (W == 128) {
+                bulk_load(sb, p, kOrthTile, full);
+              } else {
+                bulk_load(sb, p, 8192, full);
+                bulk_load(sb + 8192, p + kOrthPlane, 8192, full);
+              }
             }
           }
           __syncwarp();
           if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
-      }
+      });
     };
     for (int k = 0; k < st.steps && go; ++k) {
       load(Phase<1>{}, k);
@@ -339,27 +385,27 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
   } else if (warp == 1) {
     constexpr uint32_t kPlaneW = kOrthPlane / 16, kStageW = kStage / 16;
     int stage = 0, phase = 0, local = 0;
-    bool go = true;
     auto multiply = [&](auto which) {
       constexpr int PHASE = decltype(which)::value;
-      const uint32_t idesc = idesc_f16_f32(128, 64, 0, PHASE == 3 ? 1 : 0);
+      const uint32_t idesc = idesc_f16_f32(128, W, 0, PHASE == 3 ? 1 : 0);
       const uint32_t s0 = smem_u32(sm) >> 4, a0 = s0 | (1u << 16), b0 = s0 | ((PHASE == 3 ? 512u : 1u) << 16);
-      const int items = PHASE == 3 ? st.mn : st.sq;
-      for (int at = blockIdx.x; at < items && go; at += gridDim.x, ++local) {
-        const Item t = item(which, at);
+      tiles(which, [&](int, int i, int j, int ks) {
         const int ab = local & 1;
-        const bool same = PHASE == 1 && t.i == t.j / 2;
+        const bool same = PHASE == 1 && i == j / T;
         // B's low plane behind its high one, a tile's plane away where it is part of A
-        const uint32_t b_at = same ? (t.j & 1) * 512u : kOrthTile / 16, b_lo = same ? kPlaneW : 512u;
+        const uint32_t b_at = same ? (j % T) * 512u : kOrthTile / 16, b_lo = same ? kPlaneW : W * 8u;
         if (!__all_sync(0xffffffffu, mbar_wait(&bars.acc_empty[ab], ((local >> 1) & 1) ^ 1, st.wc, abort))) {
           go = false;
-          break;
+          return;
         }
         tc_fence_after();
-        for (int kk = 0; kk < t.ks; ++kk) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&bars.full[stage], phase, st.wc, abort))) { go = false; break; }
+        for (int kk = 0; kk < ks; ++kk) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars.full[stage], phase, st.wc, abort))) {
+            go = false;
+            return;
+          }
           tc_fence_after();
-          const uint32_t xa = a0 + stage * kStageW, xb = b0 + stage * kStageW + b_at, d = tmem + ab * 64;
+          const uint32_t xa = a0 + stage * kStageW, xb = b0 + stage * kStageW + b_at, d = tmem + ab * W;
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -369,12 +415,13 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
               mma_ss_w(d, ka + kPlaneW, kb, idesc, 1u);
             }
             mma_commit(&bars.empty[stage]);
-            if (kk == t.ks - 1) mma_commit(&bars.acc_full[ab]);
+            if (kk == ks - 1) mma_commit(&bars.acc_full[ab]);
           }
           __syncwarp();
           if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
-      }
+        ++local;
+      });
     };
     for (int k = 0; k < st.steps && go; ++k) {
       multiply(Phase<1>{});
@@ -382,11 +429,11 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
       multiply(Phase<3>{});
     }
   } else {
+    constexpr int H = W / 2;  // columns of a warp
     const int quarter = warp & 3, half = (warp - 2) >> 2, r = quarter * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-    uint8_t* stg = sm + kStages * kStage + quarter * kStg;  // this quarter's rows of the result
+    uint8_t* stg = sm + kStages * kStage + quarter * G::kStg;  // this quarter's rows of the result
     uint32_t pphase = 0;
-    bool go = true;
     auto pair_sync = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.pair[quarter]);
@@ -394,9 +441,11 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
       pphase ^= 1;
       return go;
     };
-    // this warp's 32 rows and columns of a tile, f(column, accumulator), to its image:
-    // two pieces of eight columns lie side by side, in the order of the swizzle
-    auto store = [&](uint8_t* tile, const uint32_t (&acc)[32], auto&& f) {
+    // 32 rows and columns, from c0 on, of a product's tile, f(column, accumulator), to
+    // the images from `tile` on: two pieces of eight columns lie side by side, in the
+    // order of the swizzle
+    auto store = [&](uint8_t* tile, int c0, const uint32_t (&acc)[32], auto&& f) {
+      tile += (c0 / 64) * kOrthTile + r * 128;
 #pragma unroll
       for (int c = 0; c < 4; c += 2) {
         uint4 h[2], l[2];
@@ -404,12 +453,11 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
         for (int p = 0; p < 2; ++p) {
           float y[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            y[e] = f(32 * half + 8 * (c + p) + e, __uint_as_float(acc[8 * (c + p) + e]));
+          for (int e = 0; e < 8; ++e) y[e] = f(c0 + 8 * (c + p) + e, __uint_as_float(acc[8 * (c + p) + e]));
           split8(y, h[p], l[p]);
         }
         const bool odd = (lane & 1) != 0;
-        uint8_t* to = tile + r * 128 + (((4 * half + c) ^ (lane & 6)) << 4);
+        uint8_t* to = tile + (((c0 % 64 / 8 + c) ^ (lane & 6)) << 4);
         st_global_32(to, odd ? h[1] : h[0], odd ? h[0] : h[1]);
         st_global_32(to + kOrthPlane, odd ? l[1] : l[0], odd ? l[0] : l[1]);
       }
@@ -418,74 +466,87 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
     int local = 0;
     auto take = [&](auto which, int step) {
       constexpr int PHASE = decltype(which)::value;
-      const int items = PHASE == 3 ? st.mn : st.sq, in = step & 1;
+      const int in = step & 1;
       const bool last = PHASE == 3 && step == st.steps - 1;  // X goes to the destinations
-      for (int at = blockIdx.x; at < items && go; at += gridDim.x, ++local) {
-        const Item t = item(which, at);
-        const OrthMat& q = t.q;
+      tiles(which, [&](int k, int i, int j, int) {
+        const OrthMat q = constant(v.mat + k);
         const int ab = local & 1;
         go = __all_sync(0xffffffffu, mbar_wait(&bars.acc_full[ab], (local >> 1) & 1, st.wc, abort));
-        if (!go) break;
+        if (!go) return;
+        ++local;
         tc_fence_after();
-        uint32_t u[32];
-        tmem_ld32_wait(tmem + lane_addr + ab * 64 + 32 * half, u);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.acc_empty[ab]);
-        const int diag = t.i * 128 + r - t.j * 64;  // the column of this row's diagonal element
-        if constexpr (PHASE == 1) {
-          const int tt = t.i * 2 * q.mt + t.j;
-          store(tile_at(v, q.a + tt), u, [&](int, float x) { return x * (kBack * kBack); });
-          store(tile_at(v, q.a2 + tt), u, [&](int col, float x) {
-            return st.c * (x * (kBack * kBack)) + (col == diag ? st.b : 0.f);
-          });
-        } else if constexpr (PHASE == 2) {
-          store(tile_at(v, q.b + t.i * 2 * q.mt + t.j), u,
-                [&](int col, float x) { return x + (col == diag ? st.a : 0.f); });
-        } else if (!last) {
-          store(tile_at(v, q.x[in ^ 1] + t.i * 2 * q.nt + t.j), u, [&](int, float x) { return x; });
-        } else {
-          // a transposed matrix's rows are contiguous across lanes, an ordinary one's go
-          // through the staging (64 columns of BF16, swizzled)
-          const int row0 = t.i * 128 + quarter * 32, col0 = t.j * 64;
-          uint16_t* dst = static_cast<uint16_t*>(q.dst);
-          if (q.flags & kOrthTall) {
+        const int row0 = i * 128 + quarter * 32, col0 = j * W;
+        if (PHASE == 3 && last && !(q.flags & kOrthTall) && !pair_sync()) return;  // the staging has been read
+        const int diag = i * 128 + r - col0;  // the column of this row's diagonal element
+#pragma unroll
+        for (int g = 0; g < H; g += 32) {
+          const int c0 = H * half + g;
+          uint32_t u[32];
+          tmem_ld32_wait(tmem + lane_addr + ab * W + c0, u);
+          if (g + 32 == H) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.acc_empty[ab]);
+          }
+          if constexpr (PHASE == 1) {
+            const int t = i * 2 * q.mt + j * (W / 64);
+            store(tile_at(v, q.a + t), c0, u, [&](int, float x) { return x * (kBack * kBack); });
+            store(tile_at(v, q.a2 + t), c0, u, [&](int col, float x) {
+              return st.c * (x * (kBack * kBack)) + (col == diag ? st.b : 0.f);
+            });
+          } else if constexpr (PHASE == 2) {
+            store(tile_at(v, q.b + i * 2 * q.mt + j * (W / 64)), c0, u,
+                  [&](int col, float x) { return x + (col == diag ? st.a : 0.f); });
+          } else if (!last) {
+            store(tile_at(v, (in != 0 ? q.x[0] : q.x[1]) + i * 2 * q.nt + j * (W / 64)), c0, u,
+                  [&](int, float x) { return x; });
+          } else if (q.flags & kOrthTall) {
+            // a transposed matrix's rows are contiguous across lanes
+            uint16_t* dst = static_cast<uint16_t*>(q.dst);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const int col = col0 + 32 * half + e;
+              const int col = col0 + c0 + e;
               if (row0 + lane < q.m && col < q.n)
                 dst[col * q.ld_dst + row0 + lane] =
                     static_cast<uint16_t>(pack_bf16x2(__uint_as_float(u[e]) * kBack, 0.f) & 0xFFFFu);
             }
-            continue;
-          }
-          if (!pair_sync()) break;  // the staging has been read
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16x2(__uint_as_float(u[8 * c + 2 * e]) * kBack, __uint_as_float(u[8 * c + 2 * e + 1]) * kBack);
-            *reinterpret_cast<uint4*>(stg + sw128(lane, 4 * half + c)) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          if (!pair_sync()) break;
-          const int r0 = 16 * half, rows = min(16, q.m - row0 - r0), cols = min(64, q.n - col0);
-          uint16_t* to = dst + (row0 + r0) * q.ld_dst + col0;
-          if (cols == 64 && (reinterpret_cast<uintptr_t>(to) & 15) == 0 && q.ld_dst % 8 == 0) {
-            for (int e = lane; e < rows * 8; e += 32)
-              *reinterpret_cast<uint4*>(to + (e >> 3) * q.ld_dst + (e & 7) * 8) =
-                  *reinterpret_cast<const uint4*>(stg + sw128(r0 + (e >> 3), e & 7));
           } else {
-            for (int rr = 0; rr < rows; ++rr)
-              for (int e = lane; e < cols; e += 32)
-                to[rr * q.ld_dst + e] = reinterpret_cast<const uint16_t*>(stg + sw128(r0 + rr, e >> 3))[e & 7];
+            // the others go through the staging, blocks of 64 columns of BF16, swizzled
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16x2(__uint_as_float(u[8 * c + 2 * e]) * kBack,
+                                   __uint_as_float(u[8 * c + 2 * e + 1]) * kBack);
+              *reinterpret_cast<uint4*>(stg + (c0 / 64) * 4096 + sw128(lane, c0 % 64 / 8 + c)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
         }
         if (!last) {
           __syncwarp();
-          if (lane == 0) red_release_gpu(v.done + t.k, 1u);
+          if (lane == 0) red_release_gpu(v.done + k, 1u);
+        } else if (!(q.flags & kOrthTall)) {
+          if (!pair_sync()) return;
+          uint16_t* dst = static_cast<uint16_t*>(q.dst);
+#pragma unroll 1
+          for (int blk = 0; blk < W / 64; ++blk) {
+            const int r0 = 16 * half, rows = min(16, q.m - row0 - r0), cols = min(64, q.n - col0 - 64 * blk);
+            const uint8_t* from = stg + blk * 4096;
+            uint16_t* to = dst + (row0 + r0) * q.ld_dst + col0 + 64 * blk;
+            if (cols == 64 && (reinterpret_cast<uintptr_t>(to) & 15) == 0 && q.ld_dst % 8 == 0) {
+              for (int e = lane; e < rows * 8; e += 32)
+                *reinterpret_cast<uint4*>(to + (e >> 3) * q.ld_dst + (e & 7) * 8) =
+                    *reinterpret_cast<const uint4*>(from + sw128(r0 + (e >> 3), e & 7));
+            } else {
+              for (int rr = 0; rr < rows; ++rr)
+                for (int e = lane; e < cols; e += 32)
+                  to[rr * q.ld_dst + e] = reinterpret_cast<const uint16_t*>(from + sw128(r0 + rr, e >> 3))[e & 7];
+            }
+          }
         }
-      }
+      });
     };
     for (int k = 0; k < st.steps && go; ++k) {
       take(Phase<1>{}, k);
@@ -499,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, 2 * W);
   }
 }
 
@@ -509,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) orth_gemm_kernel(OrthView v, Orth
 // workspace.
 struct Plan {
   std::vector<OrthMat> mats;
-  int solo = 0, team = 1;
+  int solo = 0, team = 1, width = 64;  // width: of the products' tiles of the larger matrices
   long long parts = 0, load_tiles = 0, sq = 0, mn = 0, tiles = 0;
   size_t done_off = 0, part_off = 0, tiles_off = 0, total = 0;
 };
@@ -534,6 +595,38 @@ int team_of(const OrthMat* q, int n) {
     const double time = std::max(widest, sum / (t == 8 ? 128 : 152));
     if (t == 1 || time < least) {
       best = t;
+      least = time;
+    }
+  }
+  return best;
+}
+
+// Columns of the larger matrices' tiles.  A stage of 64 columns takes about 0.7 of a
+// unit, one of 128 about 0.9 (the MMAs read A from shared memory for half as many
+// columns), a tile about one stage more; narrow tiles give a short list's products to
+// twice the SMs.  Both measured, five steps, us with 64 and with 128: one 300 x 300 93
+// and 112, 8 of them 101 and 117, 64 of them 418 and 299; 4 of 256 x 1037 117 and 139,
+// 12 143 and 158, 40 334 and 272; 512 x 1100 135 and 164, 12 of them 338 and 274, 40
+// 1007 and 752 (378 TFLOP/s); 4 of 1024 x 4096 1223 and 790 (489 TFLOP/s).
+int width_of(const OrthMat* q, int n) {
+  double least = 0.0;
+  int best = 64;
+  for (int w = 64; w <= 128; w *= 2) {
+    const double stage = w == 64 ? 0.7 : 0.9;
+    double tiles[3] = {}, stages[3] = {}, widest[3] = {}, time = 0.0;
+    for (int k = 0; k < n; ++k) {
+      const double sq = 128.0 / w * q[k].mt * q[k].mt, mn = 128.0 / w * q[k].mt * q[k].nt;
+      const double ks[3] = {(q[k].n + 63) / 64 + 1.0, (q[k].m + 63) / 64 + 1.0, (q[k].m + 63) / 64 + 1.0};
+      for (int p = 0; p < 3; ++p) {
+        const double t = p < 2 ? sq : mn;
+        tiles[p] += t;
+        stages[p] += t * ks[p];
+        widest[p] = std::max(widest[p], ks[p]);
+      }
+    }
+    for (int p = 0; p < 3 && n > 0; ++p) time += stage * std::max(widest[p], stages[p] / tiles[p] * std::ceil(tiles[p] / 152));
+    if (w == 64 || time < least) {
+      best = w;
       least = time;
     }
   }
@@ -566,6 +659,7 @@ bool plan_of(const triattn_matrix* in, const triattn_matrix* out, long long n, P
   p->solo = static_cast<int>(others - p->mats.begin());
   std::stable_sort(p->mats.begin(), others, [](const OrthMat& x, const OrthMat& y) { return x.n > y.n; });
   p->team = team_of(p->mats.data(), p->solo);
+  p->width = width_of(p->mats.data() + p->solo, static_cast<int>(p->mats.size()) - p->solo);
   for (OrthMat& q : p->mats) {
     const long long xt = 2ll * q.mt * q.nt, at = 2ll * q.mt * q.mt;
     q.part0 = static_cast<int>(p->parts);
@@ -577,8 +671,8 @@ bool plan_of(const triattn_matrix* in, const triattn_matrix* out, long long n, P
     if (q.mt > 1) {
       q.sq0 = static_cast<int>(p->sq);
       q.mn0 = static_cast<int>(p->mn);
-      p->sq += at;
-      p->mn += xt;
+      p->sq += at * 64 / p->width;
+      p->mn += xt * 64 / p->width;
       q.x[1] = static_cast<int>(p->tiles);
       q.a = static_cast<int>(p->tiles + xt);
       q.a2 = static_cast<int>(p->tiles + xt + at);
@@ -616,8 +710,10 @@ triattn_status check_list(const triattn_matrix* ms, long long n, bool output) {
   return TRIATTN_OK;
 }
 
+template <int W>
 cudaError_t launch_gemm(const OrthView& v, const OrthRun& st, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(orth_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  constexpr int kSmem = Gemm<W>::kSmem;
+  const cudaError_t e = cudaFuncSetAttribute(orth_gemm_kernel<W>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   int device = 0, sms = 0;
   if (cudaGetDevice(&device) != cudaSuccess ||
@@ -633,7 +729,7 @@ cudaError_t launch_gemm(const OrthView& v, const OrthRun& st, cudaStream_t s) {
   at.val.cooperative = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, orth_gemm_kernel, v, st);
+  return cudaLaunchKernelEx(&cfg, orth_gemm_kernel<W>, v, st);
 }
 
 cudaError_t run(const Plan& p, int steps, const float* co, float eps, uint8_t* ws, const WaitCtl& wc, cudaStream_t s) {
@@ -667,7 +763,8 @@ cudaError_t run(const Plan& p, int steps, const float* co, float eps, uint8_t* w
   v.done += p.solo;
   v.n -= p.solo;
   const OrthRun st{co[0], co[1], co[2], steps, static_cast<int>(p.sq), static_cast<int>(p.mn), wc};
-  if (v.n > 0 && e == cudaSuccess) e = trace_call(kKOrthGemm, s, [&] { return launch_gemm(v, st, s); });
+  if (v.n > 0 && e == cudaSuccess)
+    e = trace_call(kKOrthGemm, s, [&] { return p.width == 64 ? launch_gemm<64>(v, st, s) : launch_gemm<128>(v, st, s); });
   return e;
 }
 
