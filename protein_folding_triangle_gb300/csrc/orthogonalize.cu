@@ -142,6 +142,26 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ 
   }
 }
 
+// Eight elements of X from (row, col) on, zero outside it: loaded from the nearest
+// places inside, so that no load waits for a condition.
+template <typename S>
+__device__ __forceinline__ void gather8(const OrthMat& q, int row, int col, float (&y)[8]) {
+  const bool tall = (q.flags & kOrthTall) != 0;
+  const S* p = static_cast<const S*>(q.src) + (tall ? min(row, q.m - 1) : min(row, q.m - 1) * q.ld_src);
+  S x[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int c = min(col + j, q.n - 1);
+    x[j] = __ldg(p + (tall ? c * q.ld_src : c));
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const bool in = row < q.m && col + j < q.n;
+    if constexpr (sizeof(S) == 4) y[j] = in ? x[j] : 0.f;
+    else y[j] = in ? bf16lo_to_f32(x[j]) : 0.f;
+  }
+}
+
 // One tile of X per block: normed, scaled, split, in the image's order.
 __global__ void __launch_bounds__(256) orth_load_kernel(OrthView v, float eps) {
   __shared__ double sh[8];
@@ -158,15 +178,9 @@ __global__ void __launch_bounds__(256) orth_load_kernel(OrthView v, float eps) {
     // lanes along what is contiguous in memory: columns, or rows of a transposed matrix
     const int r = tall ? e & 127 : e >> 3, p = tall ? e >> 7 : e & 7;
     const int row = i * 128 + r, col = c * 64 + p * 8;
-    if (wide && row < q.m && col + 8 <= q.n) {
-      elements8(q, row * q.ld_src + col, y[u]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bool in = row < q.m && col + j < q.n;
-        y[u][j] = in ? element(q, tall ? (col + j) * q.ld_src + row : row * q.ld_src + col + j) : 0.f;
-      }
-    }
+    if (wide && row < q.m && col + 8 <= q.n) elements8(q, row * q.ld_src + col, y[u]);
+    else if (q.flags & kOrthFp32) gather8<float>(q, row, col, y[u]);
+    else gather8<uint16_t>(q, row, col, y[u]);
   }
   double s = 0.0;
   for (int k = threadIdx.x; k < q.parts; k += 256) s += v.part[q.part0 + k];
