@@ -578,7 +578,7 @@ triattn_status triattn_clip_grad_norm(const triattn_tensor* tensors, const triat
  * (y_a, y_b) = (u_a cos - u_b sin, u_a sin + u_b cos).  TRIATTN_ROTARY_HALF:
  * pairs (i, i + D/2); TRIATTN_ROTARY_INTERLEAVED: pairs (2i, 2i + 1);
  * TRIATTN_ROTARY_NONE: no rotation.  pos is positions[b, n], or n where
- * positions is NULL; angles are right to 3e-7 for every 32-bit position.
+ * positions is NULL; angles are right to 5e-7 for every 32-bit position.
  * Statistics and sums are FP32, each output is rounded once.  The backward
  * computes everything again from q and k.
  *
@@ -591,9 +591,11 @@ triattn_status triattn_clip_grad_norm(const triattn_tensor* tensors, const triat
  * (each NULL: the core's contiguous layout; otherwise the rules of
  * tri_attn_fwd_strided), BF16, 16-byte aligned.  Weights and their gradients
  * are FP32, positions [B, N] int32, 4-byte aligned.  Outputs must not overlap
- * inputs, but for dq and dk, which may be d_q_out and d_k_out (same pointers
- * and layout).  d_w_q, d_w_k are overwritten.  q and k have to be finite: a row
- * that is not makes its own outputs and the weights' gradients NaN.
+ * inputs or one another, but for dq and dk, which may be d_q_out and d_k_out
+ * (same pointers and layout); equal pointers are TRIATTN_ERR_INVALID_ARG.
+ * d_w_q, d_w_k are overwritten.  q and k have to be finite, with squares that
+ * FP32 holds: a row that is not makes its own outputs and the weights' gradients
+ * NaN, one of larger values gives zeros.
  * workspace (backward): triattn_qk_norm_workspace_bytes(shape) bytes,
  * 256-byte aligned, contents ignored.  Bitwise reproducible.
  */
@@ -706,8 +708,9 @@ triattn_status triattn_relpos_bwd(const triattn_relpos_shape* shape, const void*
  * singular vectors with singular values near 1 for coefficients such as 3.4445,
  * -4.7750, 2.0315 and five steps.  The products' operands are pairs of FP16
  * values (22 bits, down to 2^-33), sums are FP32, those of the norm's squares FP64
- * above a run of rows; out is rounded once.  Coefficients have to keep every element of X, A, c A + b I and
- * B + a I below 255; a matrix that is not finite gives an out that is not.
+ * above runs of 4096 elements; out is rounded once.  Coefficients have to keep
+ * every element of X, A, c A + b I and B + a I below 255; a matrix that is not
+ * finite gives an out that is not.
  *
  * `matrices` and `out` are HOST arrays, read before the call returns: row-major
  * DEVICE matrices, `stride` elements between rows, BF16 or FP32 (out: BF16),

@@ -15,6 +15,9 @@
 // The parts go through L2 (distributed shared memory took 20 us a step for a team
 // of eight) and the bands of the sum from there by multicast.
 //
+// 480 matrices of 48 blocks of 128 features: 223 us, tensor pipe active 43 %; the ten
+// of one block, teams of eight: 58 us, 11 us a step, most of it the team's sum.
+//
 //   warp 0      loads of X's chunks (ring of five)
 //   warp 1      MMAs: 24 of N = 64 for D and 12 of N = m for A per chunk, each three
 //               products of FP16 pairs; 24 of N = m for A^2 per step.  D runs two
