@@ -218,6 +218,8 @@ def library_path() -> str:
 def load(path: Optional[str] = None):
     """Load libtriattn (built in-tree by ``build.build()``); raises if absent."""
     global _LIB
+    if _LIB is not None and path is None:
+        return _LIB
     with _LOCK:
         if _LIB is None:
             p = path or library_path()
@@ -676,6 +678,9 @@ def _current_stream_ptr(index: int) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream_ptr)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 class _Here:
     """A context that changes nothing."""
 
@@ -695,8 +700,9 @@ def _on_stream(device, stream):
     on, so that a workspace freed at the end of the call is not handed to
     another stream while its kernels still run."""
     if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return _HERE, _raw_stream(device.index)
+        index = device.index
+        if _current_device() == index:
+            return _HERE, _raw_stream(index)
         stream = torch.cuda.current_stream(device)
     elif stream.device != device:
         raise ValueError(f"stream is on {stream.device}, expected {device}")
@@ -857,10 +863,18 @@ def _qk_norm_plan(shape, shared, rotary, theta, eps):
 
 
 def _qk_norm_check(q, k, w_q, w_k, positions, rotary, theta, eps):
-    shape, dev, f32 = q.shape, q.get_device(), torch.float32
+    """(shape's reference, the backward's workspace, q's layout) of valid arguments.
+    The tests of a usual call stand in one line each: the host's time is what a
+    small call takes."""
+    shape, dev, f32, bf16 = q.shape, q.get_device(), torch.float32, torch.bfloat16
     _, ref, w_shape, p_shape, need = _qk_norm_plan(shape, w_q.dim() == 1, rotary, theta, eps)
-    lay = _rows_pair(q, k, ("q", "k"), shape, dev)
-    if not (_fits(w_q, dev, w_shape, f32) and _fits(w_k, dev, w_shape, f32)
+    if (q.dtype is bf16 and k.dtype is bf16 and k.shape == shape and dev >= 0 and k.get_device() == dev
+            and q.is_contiguous() and k.is_contiguous()):
+        lay = None
+    else:
+        lay = _rows_pair(q, k, ("q", "k"), shape, dev)
+    if not (w_q.dtype is f32 and w_k.dtype is f32 and w_q.shape == w_shape and w_k.shape == w_shape
+            and w_q.get_device() == dev and w_k.get_device() == dev and w_q.is_contiguous() and w_k.is_contiguous()
             and (positions is None or _fits(positions, dev, p_shape, torch.int32))):
         _check(w_q, "w_q", w_shape, f32)
         _check(w_k, "w_k", w_shape, f32)
