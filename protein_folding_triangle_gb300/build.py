@@ -1,10 +1,14 @@
-"""In-tree build of libtriattn (nvcc, sm_103a only).
+"""In-tree build of libtriattn (nvcc, sm_103a only) and of the Python binding's
+native part.
 
 Each translation unit is compiled in parallel with
 ``nvcc -gencode arch=compute_103a,code=sm_103a -lineinfo -O3`` and linked
 into ``_build/libtriattn_<machine>.so`` next to this file.  No cmake, no
 torch extension machinery: the library exports a plain C ABI
-(include/triattn.h).
+(include/triattn.h).  ``csrc/host.cpp``, which reads torch tensors for the
+binding, is compiled with g++ against the installed torch's headers into
+``_build/triattn_host_<machine>_<torch version>.so``; the library does not
+depend on it.
 """
 from __future__ import annotations
 
@@ -13,6 +17,7 @@ import os
 import platform
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -38,6 +43,11 @@ def lib_path() -> str:
     return os.path.join(BUILD, f"libtriattn_{platform.machine()}.so")
 
 
+def host_path() -> str:
+    import torch
+    return os.path.join(BUILD, f"triattn_host_{platform.machine()}_{torch.__version__}.so")
+
+
 def _stale(out: str, deps) -> bool:
     if not os.path.exists(out):
         return True
@@ -46,13 +56,45 @@ def _stale(out: str, deps) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libtriattn if any source is newer than the library."""
+    """Compile libtriattn and the binding's native part where a source is newer;
+    the library's path."""
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        host = ex.submit(_build_host, force, verbose)
+        out = _build_lib(force, verbose)
+        host.result()
+    return out
+
+
+def _build_host(force: bool, verbose: bool) -> None:
+    import torch
+    out, src = host_path(), os.path.join(CSRC, "host.cpp")
+    if not force and not _stale(out, [src, os.path.join(INCLUDE, "triattn.h"), __file__]):
+        return
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(root, "include"),
+               os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    lib = os.path.join(root, "lib")
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", src, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [x for d in include for x in ("-I", d)]
+    cmd += ["-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    if verbose:
+        print(r.stdout, r.stderr)
+    os.replace(tmp, out)
+
+
+def _build_lib(force: bool, verbose: bool) -> str:
     out = lib_path()
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     deps = srcs + [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "triattn.h"), __file__]
     if not force and not _stale(out, deps):
         return out
-    os.makedirs(BUILD, exist_ok=True)
     exe = nvcc()
     objs = [os.path.join(BUILD, f"{os.path.splitext(s)[0]}_{platform.machine()}.o") for s in SOURCES]
 

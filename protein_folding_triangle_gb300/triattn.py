@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import operator
 import os
 import struct
@@ -21,6 +23,7 @@ import torch
 from . import build as _build
 
 _LIB = None
+_HOST = None
 _LOCK = threading.Lock()
 
 STATUS = {
@@ -225,8 +228,33 @@ def load(path: Optional[str] = None):
             p = path or library_path()
             if not os.path.exists(p):
                 raise RuntimeError(f"libtriattn is not built ({p} missing): run __graft_entry__.build()")
-            _LIB = _declare(ctypes.CDLL(p))
+            lib = _declare(ctypes.CDLL(p))
+            _load_host(lib)
+            _LIB = lib
     return _LIB
+
+
+def _load_host(lib):
+    """The binding's native part (csrc/host.cpp), which takes the library's functions
+    by address: usual calls of some entry points and the tables of long lists."""
+    global _HOST
+    from . import build
+    p = build.host_path()
+    if not os.path.exists(p):
+        raise RuntimeError(f"the binding's native part is not built ({p} missing): run __graft_entry__.build()")
+    loader = importlib.machinery.ExtensionFileLoader("triattn_host", p)
+    host = importlib.util.module_from_spec(importlib.util.spec_from_loader("triattn_host", loader))
+    loader.exec_module(host)
+    names = ("qk_norm_workspace_bytes", "qk_norm_fwd", "qk_norm_bwd", "relpos_workspace_bytes", "relpos_fwd",
+             "relpos_bwd")
+    host.bind(*(ctypes.cast(getattr(lib, f"triattn_{n}"), ctypes.c_void_p).value for n in names))
+    _HOST = host
+
+
+def _host():
+    if _HOST is None:
+        load()
+    return _HOST
 
 
 def shape_of(q: torch.Tensor) -> Shape:
@@ -901,6 +929,10 @@ def triattn_qk_norm_fwd(q, k, w_q, w_k, positions=None, rotary: str = "half", *,
     them).  ``w_q``, ``w_k`` [H, D] or [D] fp32; ``positions`` [B, N] int32 (the
     token's index if None); ``rotary`` "half", "interleaved" or "none".  Returns
     (q, k) normed, contiguous, or written into the views ``out``."""
+    if out is None and stream is None:
+        done = _host().qk_norm_fwd(q, k, w_q, w_k, positions, ROTARY.get(rotary, -1), theta, eps)
+        if done is not None:
+            return done
     ref, _, lay = _qk_norm_check(q, k, w_q, w_k, positions, rotary, theta, eps)
     here, sp = _on_stream(q.device, stream)
     given, lo = out, None
@@ -925,6 +957,10 @@ def triattn_qk_norm_bwd(q, k, w_q, w_k, d_q_out, d_k_out, positions=None, rotary
     again from q and k.  Returns (dq, dk bf16, d_w_q, d_w_k fp32); ``out`` may
     pass them preallocated, dq and dk also as views, or d_q_out and d_k_out
     themselves."""
+    if out is None and stream is None and workspace is None:
+        done = _host().qk_norm_bwd(q, k, w_q, w_k, d_q_out, d_k_out, positions, ROTARY.get(rotary, -1), theta, eps)
+        if done is not None:
+            return done
     ref, need, lay = _qk_norm_check(q, k, w_q, w_k, positions, rotary, theta, eps)
     ld = _rows_pair(d_q_out, d_k_out, ("d_q_out", "d_k_out"), q.shape, q.get_device())
     if need == 0:
@@ -994,6 +1030,11 @@ def triattn_relpos_fwd(table, base=None, positions=None, chains=None, *, layout:
     chains take the table's last row, which it has for them.  ``kind`` "clip":
     2 max_distance + 1 rows; "log": an even number of rows, logarithmic from a
     quarter of them to max_distance.  ``out`` may be base."""
+    if out is None and stream is None:
+        done = _host().relpos_fwd(table, base, positions, chains, RELPOS_LAYOUTS.get(layout, -1), BUCKETS.get(kind, -1),
+                                  max_distance)
+        if done is not None:
+            return done
     if table.dim() != 2:
         raise ValueError("table must be [buckets, F]")
     K, F = table.shape
@@ -1037,6 +1078,11 @@ def triattn_relpos_bwd(d_out, buckets: int, positions=None, chains=None, *, layo
     """Gradient of the table of ``buckets`` rows: d_table [buckets, F] fp32 from
     d_out [B, F, N, N] (bf16, or fp32 as tri_attn_bwd(..., dbias_fp32=True)
     gives it) or [B, N, N, F] (bf16).  The gradient of base is d_out itself."""
+    if out is None and stream is None and workspace is None:
+        done = _host().relpos_bwd(d_out, buckets, positions, chains, RELPOS_LAYOUTS.get(layout, -1),
+                                  BUCKETS.get(kind, -1), max_distance)
+        if done is not None:
+            return done
     if d_out.dim() != 4:
         raise ValueError("d_out must be [B, F, N, N] or [B, N, N, F]")
     B, N = d_out.shape[0], d_out.shape[2]
@@ -1171,45 +1217,22 @@ def triattn_clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, *, 
     return norm
 
 
-_shape_of = operator.attrgetter("shape")
-_contiguous, _device_index, _data_ptr = torch.Tensor.is_contiguous, torch.Tensor.get_device, torch.Tensor.data_ptr
-
-
 def _matrix_table(tensors, name, device, of=None):
     """The triattn_matrix array of a list of 2-D tensors as bytes (address, rows,
-    columns, stride and dtype, eight each), with what an array of outputs of the
-    same shapes takes over (``of``).  Column by column, like _tensor_table."""
-    n = len(tensors)
-    bf16 = torch.bfloat16
-    shapes = list(map(_shape_of, tensors))
-    kinds = list(map(_dtype_of, tensors))
-    all_bf16 = kinds.count(bf16) == n
-    if of is not None and not (all_bf16 and shapes == of[0]):
-        for i, (shape, b) in enumerate(zip(of[0], tensors)):
-            if b.shape != shape or b.dtype is not bf16:
-                raise ValueError(f"{name}[{i}] must be a bfloat16 tensor of the shape of tensors[{i}]")
-    rows = [0] * (5 * n) if of is None or not of[2] else of[1].copy()
-    try:
-        plain = all(map(_contiguous, tensors)) and set(map(_device_index, tensors)) <= {device.index}
-        if plain and (of is None or not of[2]):
-            plain = set(map(len, shapes)) <= {2}
-            if plain and n:
-                rows[1::5], cols = zip(*shapes)
-                rows[2::5] = rows[3::5] = cols
-        rows[4::5] = [0] * n if all_bf16 else list(map(GRAD_DTYPES.__getitem__, kinds))
-        rows[0::5] = map(_data_ptr, tensors)
-    except (KeyError, RuntimeError):
-        plain = False
-    if not plain:
-        for i, t in enumerate(tensors):
-            if t.dim() != 2 or t.dtype not in GRAD_DTYPES or t.device != device or t.layout != torch.strided:
-                raise ValueError(f"{name}[{i}] must be a 2-D bfloat16 or float32 tensor on {device}")
-            r, c = t.shape
-            stride = t.stride(0) if r > 1 else c
-            if (c > 1 and t.stride(1) != 1) or (stride < c and t.numel()):
-                raise ValueError(f"{name}[{i}] must have contiguous rows")
-            rows[5 * i:5 * i + 5] = (t.data_ptr(), r, c, stride, GRAD_DTYPES[t.dtype])
-    return struct.pack(f"{5 * n}q", *rows), (shapes, rows, plain)
+    columns, stride and dtype, eight each), and their shapes; as outputs, of the
+    shapes ``of``.  For the lists that the native part does not take."""
+    rows = []
+    for i, t in enumerate(tensors):
+        if of is not None and (t.shape != of[i] or t.dtype is not torch.bfloat16):
+            raise ValueError(f"{name}[{i}] must be a bfloat16 tensor of the shape of tensors[{i}]")
+        if t.dim() != 2 or t.dtype not in GRAD_DTYPES or t.device != device or t.layout != torch.strided:
+            raise ValueError(f"{name}[{i}] must be a 2-D bfloat16 or float32 tensor on {device}")
+        r, c = t.shape
+        stride = t.stride(0) if r > 1 else c
+        if (c > 1 and t.stride(1) != 1) or (stride < c and t.numel()):
+            raise ValueError(f"{name}[{i}] must have contiguous rows")
+        rows += (t.data_ptr(), r, c, stride, GRAD_DTYPES[t.dtype])
+    return struct.pack(f"{len(rows)}q", *rows), [t.shape for t in tensors]
 
 
 ORTHOGONALIZE = (3.4445, -4.7750, 2.0315)
@@ -1230,18 +1253,20 @@ def triattn_orthogonalize(tensors, steps: int = 5, *, coefficients=ORTHOGONALIZE
     if device.type != "cuda":
         raise ValueError("the matrices must be CUDA tensors")
     n = len(tensors)
-    table, of = _matrix_table(tensors, "tensors", device)
     here, sp = _on_stream(device, stream)
     given = out
     lib = load()
     with here:
-        if out is None:
-            out = [torch.empty(shape, dtype=torch.bfloat16, device=device) for shape in of[0]]
-        else:
+        if out is not None:
             out = [out] if isinstance(out, torch.Tensor) else list(out)
             if len(out) != n:
                 raise ValueError(f"out has {len(out)} tensors, expected {n}")
-        into, _ = _matrix_table(out, "out", device, of)
+        tables = _host().matrix_tables(tensors, out, device.index)
+        table, into = tables if tables is not None else (_matrix_table(tensors, "tensors", device)[0], None)
+        if out is None:
+            out = [torch.empty(t.shape, dtype=torch.bfloat16, device=device) for t in tensors]
+        if into is None:
+            into, _ = _matrix_table(out, "out", device, [t.shape for t in tensors])
         need = lib.triattn_orthogonalize_workspace_bytes(table, n)
         if need == 0:
             raise TriAttnError(ERR_UNSUPPORTED, "triattn_orthogonalize")
