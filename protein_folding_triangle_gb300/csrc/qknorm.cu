@@ -297,7 +297,11 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_bwd_kernel(const QkArgs a
     const int part = e / cells, cell = e - part * cells, sl = cell / D, d = cell - sl * D;
     // rows of the slot: every H-th (heads in a row), or those of one head in sequence
     int first, end, step;
-    if (a.lx.hn) {
+    if (a.w_heads == 1) {  // all of them
+      first = 0;
+      end = last;
+      step = 1;
+    } else if (a.lx.hn) {
       first = a.slots == a.H ? static_cast<int>((sl + a.H - j0 % a.H) % a.H) : sl;
       end = last;
       step = a.H;
@@ -323,7 +327,8 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_bwd_kernel(const QkArgs a
 }
 
 // dw[h][d] (or dw[d], all heads) from the blocks' partial sums, in a fixed order.
-// Partials [chunks][tiles][slots][D]: with the heads in a row a slot is a head
+// Partials [chunks][tiles][slots][D]: a slot is all of a tile where the heads share a
+// weight (2 x 131 tokens of six heads: 11 -> 3 us); with the heads in a row it is a head
 // (the j0 + slot-th where a tile does not hold all of them), otherwise the
 // slot-th head of the tile.
 __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* part, float* dwq, float* dwk, int D, int rows, int tiles,
@@ -386,7 +391,9 @@ Plan plan_of(const triattn_qk_norm_shape* s, bool hn, int extra) {
   p.per = static_cast<int>((s->N_o + best - 1) / best);
   p.cpb = (s->N_o + p.per - 1) / p.per;
   p.chunks = p.cpb * s->B;
-  p.slots = hn ? std::min(s->H, p.rows) : static_cast<int>(std::min<long long>(s->H, (p.rows - 1) / s->N + 2));
+  p.slots = s->w_heads == 1 ? 1
+            : hn ? std::min(s->H, p.rows)
+                 : static_cast<int>(std::min<long long>(s->H, (p.rows - 1) / s->N + 2));
   p.part_bytes = 2ull * p.chunks * p.tiles * p.slots * s->D * 4;
   return p;
 }

@@ -49,6 +49,18 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
+// An element (zero where `in` does not hold) of memory that the kernel may write,
+// loaded on the spot: under a condition of the compiler's the loads would wait for one
+// another.
+__device__ __forceinline__ uint32_t load1_written(const uint16_t* p, bool in) {
+  uint32_t v;
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.u32 %0, 0;\n @p ld.global.u16 %0, [%1];\n}\n"
+               : "=r"(v)
+               : "l"(p), "r"(static_cast<uint32_t>(in))
+               : "memory");
+  return v;
+}
+
 // The planes' rows need not start on 16 bytes: chunk t of a row is the t-th
 // aligned group of W elements that holds elements of the row, [W t - off,
 // W t - off + W) of it, off the place of the row's start in its group.
@@ -118,29 +130,18 @@ __device__ __forceinline__ void make_windows(const RelposArgs& a, int b, int nt,
   }
 }
 
-// The planes' kernels.  A block has a run of units of one example: a unit is a row
-// i and a segment of its chunks (of one or four heads), a warp's work, the lanes
-// along the chunks.
-constexpr int kSegChunks = 64;
-struct Units {
-  int segs, len;  // segments of a row, chunks of a segment
-  __host__ __device__ Units(int nt) {
-    segs = (nt + kSegChunks - 1) / kSegChunks;
-    len = ((nt + segs - 1) / segs + 31) / 32 * 32;
-    segs = (nt + len - 1) / len;
-  }
-};
-
 // ------------------------------------------------------- planes, forward
-// Four heads at a time: the buckets are found once for all.  The values of every
-// bucket lie in shared memory by distance.  Chunks inside the row and of one chain
-// are taken as a whole; the others of a warp (the ends of rows that do not start
-// on a chunk, and where chains meet) go element by element, four chunks at a time,
-// a lane to an element.  ALIGNED: all rows start on 16 bytes.  2048 tokens, 16
-// heads, four chains (268 MB): 54 us, 4.9 TB/s; 2049 tokens 75 us (taking the four
-// heads' different offsets in one pass over the chunks: 145 us).  DRAM is busy half of
-// the time: between a warp's loads and its stores lie the buckets.  Three, five, six
-// or eight blocks an SM: 55, 56, 58 and 73 us; loads of 32 bytes: the same.
+// Four heads at a time: the buckets are found once for all.  A warp takes 32
+// consecutive chunks of the example's rows, a lane to a chunk, and the warps of a block
+// take turns at the same columns, as the ends of rows, gaps and meeting chains cost
+// more.  The values of every bucket lie in shared memory by distance.  Chunks inside
+// the row and of one chain are taken as a whole; the others of a warp (the ends of rows
+// that do not start on a chunk, and where chains meet) go element by element, four
+// chunks of every head at a time, a lane to an element.  ALIGNED: all rows start on 16
+// bytes.  2048 tokens, 16 heads, four chains (268 MB): 51 us, 5.3 TB/s; 2049 tokens 68
+// (without the turns 55 and 90; the four heads' different offsets in one pass over the
+// chunks: 145).  Between a warp's loads and its stores lie the buckets.  Five, six or
+// eight blocks an SM: a few us more; loads of 32 bytes: the same.
 constexpr int kFwdBlocks = 4;  // an SM
 template <bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, kFwdBlocks) relpos_heads_fwd_kernel(const __grid_constant__ RelposArgs a) {
@@ -162,90 +163,109 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks) relpos_heads_fwd_kernel(
   __syncthreads();
   const int other = spread(2 * a.R + 1);
   const size_t plane = static_cast<size_t>(a.N) * a.N;
-  const Units un(nt);
-  const int units = a.N * un.segs;
-  const int u0 = static_cast<int>(static_cast<long long>(units) * blockIdx.x / gridDim.x);
-  const int u1 = static_cast<int>(static_cast<long long>(units) * (blockIdx.x + 1) / gridDim.x);
-  for (int u = u0 + warp; u < u1; u += kThreads / 32) {
-    const int i = u / un.segs, seg = u - i * un.segs;
+  const int items = a.N * nt, pieces = (items + 31) / 32;
+  const int u0 = static_cast<int>(static_cast<long long>(pieces) * blockIdx.x / gridDim.x);
+  const int u1 = static_cast<int>(static_cast<long long>(pieces) * (blockIdx.x + 1) / gridDim.x);
+  const size_t first = (static_cast<size_t>(b) * a.F + h0) * plane;
+  auto place = [&](int pi, int ci, int j) {  // of column j, any chain
+    return chain != nullptr && __ldg(chain + j) != ci ? other : spread(distance(pi, a.position(b, j), a.R));
+  };
+  constexpr int kWarps = kThreads / 32;
+  for (int v0 = u0, turn = warp; v0 < u1; v0 += kWarps, ++turn) {
+    const int u = v0 + turn % kWarps;  // what lies in the same columns comes to all warps in turn
+    if (u >= u1) continue;
+    const int e = min(32 * u + lane, items - 1), i = e / nt, t = e - i * nt;
+    const bool mine = 32 * u + lane < items;
     const int pi = a.position(b, i), ci = chain != nullptr ? __ldg(chain + i) : 0;
-    const size_t row = ((static_cast<size_t>(b) * a.F + h0) * a.N + i) * a.N;
+    const size_t row = first + static_cast<size_t>(i) * a.N;
     int off[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) off[g] = ALIGNED ? 0 : static_cast<int>((row + g * plane) & (W - 1));
-    auto place = [&](int j) {  // of column j, any chain
-      return chain != nullptr && __ldg(chain + j) != ci ? other : spread(distance(pi, a.position(b, j), a.R));
-    };
-    const int t1 = min((seg + 1) * un.len, nt);
-    for (int t0 = seg * un.len; t0 < t1; t0 += 32) {
-      const int t = t0 + lane;
-      const Window w = win[min(t, nt - 1)];
-      const bool apart = ci < w.chain || ci > w.chain_max;  // no column of the row's chain
-      const bool one_chain = (apart || w.chain == w.chain_max) && t < t1;
-      uint4 in[G];
-      bool whole[G];
+    const Window w = win[t];
+    const bool apart = ci < w.chain || ci > w.chain_max;  // no column of the row's chain
+    const bool one_chain = (apart || w.chain == w.chain_max) && mine;
+    uint4 in[G];
+    bool whole[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int j0 = W * t - off[g];
+      whole[g] = g < ng && one_chain && (ALIGNED || (j0 >= 0 && j0 + W <= a.N));
+      in[g] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.base != nullptr && whole[g]) in[g] = *reinterpret_cast<const uint4*>(a.base + row + g * plane + j0);
+    }
+    const int far = distance(pi, w.hi, a.R), near = distance(pi, w.lo, a.R);
+    const bool single = one_chain && (apart || far == near);
+    const int one = apart ? other : spread(far);
+    if (single) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        if (!whole[g]) continue;
+        const float2 x = make_float2(val[g * VW + one], val[g * VW + one]);
+        const uint32_t p[4] = {in[g].x, in[g].y, in[g].z, in[g].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = fadd2(make_float2(bf16lo_to_f32(p[k]), bf16hi_to_f32(p[k])), x);
+          o[k] = pack_bf16x2(v.x, v.y);
+        }
+        *reinterpret_cast<uint4*>(a.out + row + g * plane + W * t - off[g]) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    } else if (one_chain) {
+      int at[W];
+      const bool run = w.run != 0;
+      const int p0 = w.lo - first_column<W>(a.N, t);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const int j0 = W * t - off[g];
-        whole[g] = g < ng && one_chain && (ALIGNED || (j0 >= 0 && j0 + W <= a.N));
-        in[g] = make_uint4(0u, 0u, 0u, 0u);
-        if (a.base != nullptr && whole[g]) in[g] = *reinterpret_cast<const uint4*>(a.base + row + g * plane + j0);
-      }
-      const int far = distance(pi, w.hi, a.R), near = distance(pi, w.lo, a.R);
-      const bool single = one_chain && (apart || far == near);
-      const int one = apart ? other : spread(far);
-      if (single) {
+        if (!whole[g]) continue;
+        if (g == 0 || !ALIGNED) {
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          if (!whole[g]) continue;
-          const float2 x = make_float2(val[g * VW + one], val[g * VW + one]);
-          const uint32_t p[4] = {in[g].x, in[g].y, in[g].z, in[g].w};
-          uint32_t o[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 v = fadd2(make_float2(bf16lo_to_f32(p[k]), bf16hi_to_f32(p[k])), x);
-            o[k] = pack_bf16x2(v.x, v.y);
-          }
-          *reinterpret_cast<uint4*>(a.out + row + g * plane + W * t - off[g]) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int k = 0; k < W; ++k) at[k] = run ? spread(distance(pi, p0 + j0 + k, a.R)) : place(pi, ci, j0 + k);
         }
-      } else if (one_chain) {
-        int at[W];
-        const bool run = w.run != 0;
-        const int p0 = w.lo - first_column<W>(a.N, t);
+        float v[8];
+        unpack8(in[g], v);
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const int j0 = W * t - off[g];
-          if (!whole[g]) continue;
-          if (g == 0 || !ALIGNED) {
-#pragma unroll
-            for (int k = 0; k < W; ++k) at[k] = run ? spread(distance(pi, p0 + j0 + k, a.R)) : place(j0 + k);
-          }
-          float v[8];
-          unpack8(in[g], v);
-#pragma unroll
-          for (int k = 0; k < W; ++k) v[k] += val[g * VW + at[k]];
-          *reinterpret_cast<uint4*>(a.out + row + g * plane + j0) = pack8(v);
-        }
+        for (int k = 0; k < W; ++k) v[k] += val[g * VW + at[k]];
+        *reinterpret_cast<uint4*>(a.out + row + g * plane + j0) = pack8(v);
       }
+    }
+    uint32_t left[G], any = 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      left[g] = __ballot_sync(0xffffffffu, g < ng && mine && !whole[g] && W * t - off[g] < a.N);
+      any |= left[g];
+    }
+    while (any != 0) {  // all heads' loads before the stores
+      size_t at[G];
+      uint32_t x[G], in_ = 0;
+      float v[G];
+      any = 0;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        if (g >= ng) break;
-        uint32_t left = __ballot_sync(0xffffffffu, t < t1 && !whole[g] && W * t - off[g] < a.N);
-        while (left != 0) {
-          int q = -1;
+        int q = 0;
+        bool has = false;
 #pragma unroll
-          for (int k = 0; k < 32 / W; ++k) {
-            if (left != 0 && lane / W == k) q = __ffs(left) - 1;
-            left &= left - 1;
+        for (int k = 0; k < 32 / W; ++k) {
+          if (left[g] != 0 && lane / W == k) {
+            q = __ffs(left[g]) - 1;
+            has = true;
           }
-          const int j = W * (t0 + q) - off[g] + lane % W;
-          if (q >= 0 && j >= 0 && j < a.N) {
-            const size_t e = row + g * plane + j;
-            const float v = (a.base != nullptr ? bf16lo_to_f32(a.base[e]) : 0.f) + val[g * VW + place(j)];
-            a.out[e] = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xFFFFu);
-          }
+          left[g] &= left[g] - 1;
         }
+        any |= left[g];
+        const int iq = __shfl_sync(0xffffffffu, i, q), tq = __shfl_sync(0xffffffffu, t, q);
+        const int pq = __shfl_sync(0xffffffffu, pi, q), cq = __shfl_sync(0xffffffffu, ci, q);
+        const size_t start = first + g * plane + static_cast<size_t>(iq) * a.N;
+        const int j = W * tq - (ALIGNED ? 0 : static_cast<int>(start & (W - 1))) + lane % W;
+        has = has && j >= 0 && j < a.N;
+        in_ |= has ? 1u << g : 0u;
+        at[g] = start + j;
+        x[g] = load1_written(a.base + at[g], has && a.base != nullptr);
+        v[g] = val[min(g, ng - 1) * VW + place(pq, cq, min(max(j, 0), a.N - 1))];
       }
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if ((in_ >> g) & 1u) a.out[at[g]] = static_cast<uint16_t>(pack_bf16x2(bf16lo_to_f32(x[g]) + v[g], 0.f) & 0xFFFFu);
     }
   }
 }
@@ -375,14 +395,14 @@ __device__ __forceinline__ void values(const uint4 (&v)[4], float (&f)[16]) {
 // as many loads in flight 45.
 // Distances that the lanes hold, [-kNear, kNear), and those of a table that fit: a
 // chunk with one of them in one of the rows has no other's distance above
-// kNearMax + 2 (W - 1) + kRows - 1.
-constexpr int kBwdW = 16, kRows = 8, kNear = 96, kNearMax = 47;
-static_assert(kNearMax + 2 * (kBwdW - 1) + kRows - 1 < kNear, "distances of a chunk on the diagonal");
-template <typename T>
+// kNearMax + 2 (W - 1) + kRowsMax - 1.
+constexpr int kBwdW = 16, kRowsMax = 8, kNear = 96, kNearMax = 47;
+static_assert(kNearMax + 2 * (kBwdW - 1) + kRowsMax - 1 < kNear, "distances of a chunk on the diagonal");
+template <typename T, int kRows>
 __global__ void __launch_bounds__(kThreads, 2) relpos_heads_bwd_kernel(const __grid_constant__ RelposArgs a, const T* d_out) {
   constexpr int W = kBwdW;
   constexpr int V = sizeof(T);  // 16-byte pieces of a chunk
-  constexpr int U = 16 / V;     // rows in flight
+  constexpr int U = 16 / V < kRows ? 16 / V : kRows;  // rows in flight
   extern __shared__ float sh[];
   __shared__ uint8_t lut[2 * kRelposMaxDistance + 1];
   let_next_start();
@@ -481,23 +501,43 @@ __global__ void __launch_bounds__(kThreads, 2) relpos_heads_bwd_kernel(const __g
           for (int m = 0; m < kNear / 16; ++m) near[m] += value1<T>(x[q][m]);
       }
     }
-    for (uint32_t left = __ballot_sync(0xffffffffu, kind == kMixed); left != 0; left &= left - 1) {
-      const int tq = 32 * cb + __ffs(left) - 1;
-      int kk[kRows / 2];
-      uint32_t x[kRows / 2];
+    uint32_t left = __ballot_sync(0xffffffffu, kind == kMixed);
+    auto gather = [&](int tq, bool some, int (&kk)[kRows / 2], uint32_t (&x)[kRows / 2]) {
 #pragma unroll
       for (int q = 0; q < kRows / 2; ++q) {
         const int r = 2 * q + lane / W, i = i0 + min(r, nr - 1), j = W * tq - off_of(r) + lane % W;
-        const bool in = r < nr && j >= 0 && j < a.N;
+        const bool in = some && r < nr && j >= 0 && j < a.N;
         const int jc = min(max(j, 0), a.N - 1);
         const bool apart = chain != nullptr && __ldg(chain + jc) != __ldg(chain + i);
         const int d = distance(a.position(b, i), a.position(b, jc), a.R);
         kk[q] = in ? (apart ? ko : lut[d]) : -1;
         x[q] = load1(d_out + s0 + static_cast<size_t>(r) * a.N + j, in);
       }
+    };
+    auto add = [&](const int (&kk)[kRows / 2], const uint32_t (&x)[kRows / 2]) {
 #pragma unroll
       for (int q = 0; q < kRows / 2; ++q)
         if (kk[q] >= 0) mine[kk[q] * 32] += value1<T>(x[q]);
+    };
+    if constexpr (kRows == kRowsMax) {
+      for (; left != 0; left &= left - 1) {
+        int kk[kRows / 2];
+        uint32_t x[kRows / 2];
+        gather(32 * cb + __ffs(left) - 1, true, kk, x);
+        add(kk, x);
+      }
+    } else {  // a few units a warp: the loads of four chunks together
+      while (left != 0) {
+        int kk[4][kRows / 2];
+        uint32_t x[4][kRows / 2];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          gather(32 * cb + __ffs(left) - 1, left != 0, kk[m], x[m]);
+          left &= left - 1;
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) add(kk[m], x[m]);
+      }
     }
   }
 #pragma unroll
@@ -524,7 +564,8 @@ __global__ void __launch_bounds__(kThreads, 2) relpos_heads_bwd_kernel(const __g
 }
 
 // out[y * oy + x * ox] = sum over (b, s) of part[b * pb + s * ps + y * py + x], 32 x by 32 slices
-// of the sum per block, joined in a fixed order.
+// of the sum per block, joined in a fixed order, by one warp: FP64 adds are two a clock
+// and SM, and a tree of all warps' lanes takes five times as many.
 __global__ void __launch_bounds__(1024) relpos_sum_kernel(const float* part, float* out, int nx, int ox, int oy, int nb, int ns, size_t pb, size_t ps,
                                                           size_t py) {
   __shared__ double sh[32][33];
@@ -606,9 +647,11 @@ RelposArgs args_of(const triattn_relpos_shape* s, const int* positions, const in
 }
 
 // Planes' gradient: two blocks of eight warps an SM where their sums fit, otherwise
-// fewer warps in a block, and fewer blocks.
+// fewer warps in a block, and fewer blocks.  Units of four rows where those of eight
+// would leave warps without one (3 x 301 tokens, eight heads, FP32: 16.5 and 12 us; 2048
+// tokens, sixteen heads: 33 us with eight, 37 with four).
 struct BwdPlan {
-  int warps, splits;
+  int warps, splits, rows;
   size_t smem;
 };
 BwdPlan bwd_plan(int B, int N, int F, int buckets) {
@@ -618,8 +661,11 @@ BwdPlan bwd_plan(int B, int N, int F, int buckets) {
   while (p.warps > 1 && win + static_cast<size_t>(p.warps) * buckets * 128 > (p.warps > 4 ? 72000u : 216000u)) p.warps /= 2;
   p.smem = win + static_cast<size_t>(p.warps) * buckets * 128;
   const int per_sm = std::max(1, std::min<int>(16 / p.warps, static_cast<int>(232448 / (p.smem + 3200))));
-  const int units = (N + kRows - 1) / kRows * ((chunks_of(N, kBwdW) + 31) / 32);
-  p.splits = std::max(1, std::min((units + p.warps - 1) / p.warps, static_cast<int>(152ll * per_sm / (static_cast<long long>(B) * F))));
+  const int cols = (chunks_of(N, kBwdW) + 31) / 32;
+  const long long planes = static_cast<long long>(B) * F;
+  p.rows = (N + 7) / 8 * cols * planes <= 152ll * per_sm * p.warps ? 4 : 8;
+  const int units = (N + p.rows - 1) / p.rows * cols;
+  p.splits = std::max(1, std::min((units + p.warps - 1) / p.warps, static_cast<int>(152ll * per_sm / planes)));
   return p;
 }
 
@@ -645,7 +691,7 @@ cudaError_t launch_heads_fwd(const RelposArgs& a, cudaStream_t s) {
   const size_t smem = sizeof(Window) * nt + 4ull * kHeadGroup * (spread(2 * a.R + 1) + 1);
   cudaError_t e = allow_smem(relpos_heads_fwd_kernel<ALIGNED>, smem);
   if (e != cudaSuccess) return e;
-  const int units = a.N * Units(nt).segs, blocks = 152 * kFwdBlocks / (a.B * groups);
+  const int units = (a.N * nt + 31) / 32, blocks = 152 * kFwdBlocks / (a.B * groups);
   relpos_heads_fwd_kernel<ALIGNED><<<dim3(std::max(1, std::min((units + 7) / 8, blocks)), a.B * groups), kThreads, smem,
                                      s>>>(a);
   return cudaGetLastError();
@@ -658,13 +704,17 @@ cudaError_t launch_pairs_fwd(const RelposArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t launch_heads_bwd(const RelposArgs& a, const void* d_out, const BwdPlan& p, cudaStream_t s) {
-  cudaError_t e = allow_smem(relpos_heads_bwd_kernel<T>, p.smem);
+template <typename T, int ROWS>
+cudaError_t launch_heads_bwd_rows(const RelposArgs& a, const void* d_out, const BwdPlan& p, cudaStream_t s) {
+  cudaError_t e = allow_smem(relpos_heads_bwd_kernel<T, ROWS>, p.smem);
   if (e != cudaSuccess) return e;
-  relpos_heads_bwd_kernel<T><<<dim3(p.splits, a.B * a.F), p.warps * 32, p.smem, s>>>(
+  relpos_heads_bwd_kernel<T, ROWS><<<dim3(p.splits, a.B * a.F), p.warps * 32, p.smem, s>>>(
       a, static_cast<const T*>(d_out));
   return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_heads_bwd(const RelposArgs& a, const void* d_out, const BwdPlan& p, cudaStream_t s) {
+  return p.rows == 4 ? launch_heads_bwd_rows<T, 4>(a, d_out, p, s) : launch_heads_bwd_rows<T, 8>(a, d_out, p, s);
 }
 
 }  // namespace
