@@ -173,6 +173,7 @@ __device__ __forceinline__ void gather8(const OrthMat& q, int row, int col, floa
 // One tile of X per block: normed, scaled, split, in the image's order.
 __global__ void __launch_bounds__(256) orth_load_kernel(OrthView v, float eps) {
   __shared__ double sh[8];
+  __shared__ float scaled;
   let_next_start();
   after_previous();
   const OrthMat q = v.mat[find<&OrthMat::tiles0>(v.mat, v.n, blockIdx.x)];
@@ -190,14 +191,23 @@ __global__ void __launch_bounds__(256) orth_load_kernel(OrthView v, float eps) {
     else if (q.flags & kOrthFp32) gather8<float>(q, row, col, y[u]);
     else gather8<uint16_t>(q, row, col, y[u]);
   }
-  double s = 0.0;
-  for (int k = threadIdx.x; k < q.parts; k += 256) s += v.part[q.part0 + k];
+  // by one warp where it can be: FP64 has two operations a clock and SM
+  const bool many = q.parts > 256;
+  if (many || threadIdx.x < 32) {
+    double s = 0.0;
+    for (int k = threadIdx.x; k < q.parts; k += many ? 256 : 32) s += v.part[q.part0 + k];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
+  }
+  if (many) __syncthreads();
+  if (threadIdx.x == 0) {
+    double s = sh[0];
+    for (int w = 1; many && w < 8; ++w) s += sh[w];
+    scaled = kOrthScale / (sqrtf(static_cast<float>(s)) + eps);
+  }
   __syncthreads();
-  s = ((sh[0] + sh[1]) + (sh[2] + sh[3])) + ((sh[4] + sh[5]) + (sh[6] + sh[7]));
-  const float scale = static_cast<float>(static_cast<double>(kOrthScale) / (sqrt(s) + eps));
+  const float scale = scaled;
   uint8_t* out = tile_at(v, q.x[0] + t);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {

@@ -564,8 +564,9 @@ __global__ void __launch_bounds__(kThreads, 2) relpos_heads_bwd_kernel(const __g
 }
 
 // out[y * oy + x * ox] = sum over (b, s) of part[b * pb + s * ps + y * py + x], 32 x by 32 slices
-// of the sum per block, joined in a fixed order, by one warp: FP64 adds are two a clock
-// and SM, and a tree of all warps' lanes takes five times as many.
+// of the sum per block, by fours in FP32, joined in a fixed order in FP64 by one warp:
+// FP64 adds are two a clock and SM (every partial in FP64: 2 us more at 152 partials of
+// 66 x 128; a tree over all warps' lanes at the end 1 to 3).
 __global__ void __launch_bounds__(1024) relpos_sum_kernel(const float* part, float* out, int nx, int ox, int oy, int nb, int ns, size_t pb, size_t ps,
                                                           size_t py) {
   __shared__ double sh[32][33];
@@ -573,10 +574,15 @@ __global__ void __launch_bounds__(1024) relpos_sum_kernel(const float* part, flo
   double v = 0.0;
   after_previous();
   if (x < nx) {
-#pragma unroll 8
-    for (int e = slice; e < nb * ns; e += 32) {
-      const int b = e / ns, s = e - b * ns;
-      v += part[b * pb + s * ps + blockIdx.y * py + x];
+#pragma unroll 2
+    for (int e0 = slice; e0 < nb * ns; e0 += 128) {
+      float f = 0.f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int e = e0 + 32 * u, b = e / ns, s = e - b * ns;
+        if (e < nb * ns) f += part[b * pb + s * ps + blockIdx.y * py + x];
+      }
+      v += f;
     }
   }
   sh[slice][lane] = v;
