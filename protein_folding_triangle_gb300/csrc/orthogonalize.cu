@@ -54,10 +54,19 @@ struct OrthTable {
 };
 static_assert(sizeof(OrthTable) + 32 <= 32764, "kernel parameter limit");
 
-__global__ void __launch_bounds__(256) orth_table_kernel(const __grid_constant__ OrthTable t, OrthMat* to) {
+// A row of the table to memory, six lanes to a row.  Parameters that lanes read at
+// places of their own come one after the other, so few of them lie on one SM (a block of
+// 256 rows took 12 us).
+__device__ __forceinline__ void put_row(const OrthTable& t, int k, int piece, OrthMat* to) {
+  static_assert(sizeof(OrthMat) == 96, "six pieces");
+  reinterpret_cast<uint4*>(to + k)[piece] = reinterpret_cast<const uint4*>(t.mat + k)[piece];
+}
+constexpr int kTableRows = 4;  // a block
+__global__ void __launch_bounds__(32) orth_table_kernel(const __grid_constant__ OrthTable t, OrthMat* to) {
   let_next_start();
   after_previous();  // what last used the workspace
-  if (threadIdx.x < t.n) to[threadIdx.x] = t.mat[threadIdx.x];
+  const int k = kTableRows * blockIdx.x + threadIdx.x / 6;
+  if (threadIdx.x < 6 * kTableRows && k < t.n) put_row(t, k, threadIdx.x % 6, to);
 }
 
 // The matrix that item `at` belongs to (the last whose first item is not above it), by a whole warp.
@@ -104,8 +113,8 @@ __device__ __forceinline__ void elements8(const OrthMat& q, long long at, float 
 __device__ __forceinline__ bool on16(const OrthMat& q) { return (reinterpret_cast<uintptr_t>(q.src) & 15) == 0; }
 
 // Sums of squares, one partial per kNormPart elements of the source in the order of
-// its rows.  A short list's table is a parameter, which the first block puts where
-// the later kernels look for it.
+// its rows.  A short list's table is a parameter, whose rows the first blocks put where
+// the later kernels look for them.
 constexpr int kNormPart = 4096;
 template <bool PARAM>
 __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ OrthTable t, OrthView v, OrthMat* to) {
@@ -113,8 +122,7 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ 
   let_next_start();
   after_previous();  // the table, or what last used the workspace
   for (int i = blockIdx.x * 256 + threadIdx.x; i < v.n; i += gridDim.x * 256) v.done[i] = 0;
-  if (PARAM && blockIdx.x == 0)
-    for (int i = threadIdx.x; i < t.n; i += 256) to[i] = t.mat[i];
+  if (PARAM && static_cast<int>(blockIdx.x) < t.n && threadIdx.x < 6) put_row(t, blockIdx.x, threadIdx.x, to);
   const OrthMat* mat = PARAM ? t.mat : v.mat;
   const OrthMat q = mat[find<&OrthMat::part0>(mat, PARAM ? t.n : v.n, blockIdx.x)];
   const int rows = (q.flags & kOrthTall) ? q.n : q.m, cols = (q.flags & kOrthTall) ? q.m : q.n;
@@ -776,7 +784,7 @@ cudaError_t run(const Plan& p, int steps, const float* co, float eps, uint8_t* w
     t.n = static_cast<int>(std::min<size_t>(kUpload, p.mats.size() - k));
     std::copy_n(p.mats.data() + k, t.n, t.mat);
     if (!small)
-      e = trace_call(kKOrthLoad, s, [&] { return launch_after(k == 0, orth_table_kernel, 1, 256, 0, s, t, mats + k); });
+      e = trace_call(kKOrthLoad, s, [&] { return launch_after(k == 0, orth_table_kernel, (t.n + kTableRows - 1) / kTableRows, 32, 0, s, t, mats + k); });
   }
   if (e == cudaSuccess)
     e = trace_call(kKOrthLoad, s, [&] {
