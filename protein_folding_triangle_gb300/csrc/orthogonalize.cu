@@ -26,8 +26,8 @@
 // Kernels: sums of squares, X's tiles, then all steps of the matrices of at most 128
 // rows (orth_solo.cu) and all steps of the others (orth_gemm_kernel); the start of
 // each of the first three lies behind the one before.  The ten matrices of a block of
-// 128 features take 63 us on the device, those of 48 blocks 314 (75 GFLOP by the
-// formula, three times as many run), twelve of 256 x 1037 157, of which the steps' 140
+// 128 features take 62 us on the device, those of 48 blocks 273 (75 GFLOP by the
+// formula, three times as many run), twelve of 256 x 1037 149, of which the steps' 135
 // are 15 dependent phases of two to seven us of loads and products and some five of
 // latency.
 #include <cuda_fp16.h>

@@ -15,7 +15,7 @@
 // the weight gradients are sums in registers until the end.
 //
 // 768^2 tokens and slices, four heads of 32 features, q and k (0.15 GB each): forward
-// 93 us for 0.60 GB, 6.5 TB/s; backward 160 us for 0.91 GB, 5.7 TB/s.  From a
+// 91 us for 0.60 GB, 6.6 TB/s; backward 160 us for 0.91 GB, 5.7 TB/s.  From a
 // projection's pair rows of 392 features, whose 512 bytes of q and k touch a fifth more
 // sectors: 101 and 179 us.  The backward by copies into shared memory six slices
 // ahead (174 and 213 us) and by four pairs a thread (170 and 186) were no faster.
