@@ -33,6 +33,12 @@ decltype(&triattn_relpos_workspace_bytes) rel_bytes = nullptr;
 decltype(&triattn_relpos_fwd) rel_fwd = nullptr;
 decltype(&triattn_relpos_bwd) rel_bwd = nullptr;
 
+// Allocations and calls run without the interpreter's lock, as torch's own do.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // A tensor argument, or null where it is not plainly one.
 const at::Tensor* tensor(PyObject* o) {
   if (!THPVariable_CheckExact(o)) return nullptr;
@@ -147,14 +153,17 @@ PyObject* host_qk_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Args num{a};
   QkNorm c;
   if (n != 8 || !c.read(a, a[4], num, 5)) Py_RETURN_NONE;
-  at::Tensor qo = at::empty(c.q->sizes(), c.q->options()), ko = at::empty(c.q->sizes(), c.q->options());
-  void* s = c10::cuda::getCurrentCUDAStream(c.index).stream();
+  at::Tensor qo, ko;
   triattn_status code;
-  Py_BEGIN_ALLOW_THREADS
-  code = qk_fwd(&c.shape, c.q->const_data_ptr(), c.k->const_data_ptr(), c.rows.at,
-                static_cast<const float*>(c.wq->const_data_ptr()), static_cast<const float*>(c.wk->const_data_ptr()),
-                c.pos, qo.mutable_data_ptr(), ko.mutable_data_ptr(), nullptr, s);
-  Py_END_ALLOW_THREADS
+  {
+    Unlocked unlocked;
+    qo = at::empty(c.q->sizes(), c.q->options());
+    ko = at::empty(c.q->sizes(), c.q->options());
+    code = qk_fwd(&c.shape, c.q->const_data_ptr(), c.k->const_data_ptr(), c.rows.at,
+                  static_cast<const float*>(c.wq->const_data_ptr()),
+                  static_cast<const float*>(c.wk->const_data_ptr()), c.pos, qo.mutable_data_ptr(),
+                  ko.mutable_data_ptr(), nullptr, c10::cuda::getCurrentCUDAStream(c.index).stream());
+  }
   if (code != TRIATTN_OK) Py_RETURN_NONE;
   return Py_BuildValue("(NN)", THPVariable_Wrap(std::move(qo)), THPVariable_Wrap(std::move(ko)));
   END_HANDLE_TH_ERRORS
@@ -170,17 +179,22 @@ PyObject* host_qk_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (dqo == nullptr || dko == nullptr || !out_rows.read(*dqo, *dko, c.q->sizes(), c.index)) Py_RETURN_NONE;
   const size_t need = qk_bytes(&c.shape);
   if (need == 0) Py_RETURN_NONE;
-  at::Tensor ws = bytes(need, *c.q), dq = at::empty(c.q->sizes(), c.q->options()),
-             dk = at::empty(c.q->sizes(), c.q->options()), dwq = at::empty_like(*c.wq), dwk = at::empty_like(*c.wk);
-  void* s = c10::cuda::getCurrentCUDAStream(c.index).stream();
+  at::Tensor dq, dk, dwq, dwk;
   triattn_status code;
-  Py_BEGIN_ALLOW_THREADS
-  code = qk_bwd(&c.shape, c.q->const_data_ptr(), c.k->const_data_ptr(), c.rows.at,
-                static_cast<const float*>(c.wq->const_data_ptr()), static_cast<const float*>(c.wk->const_data_ptr()),
-                c.pos, dqo->const_data_ptr(), dko->const_data_ptr(), out_rows.at, dq.mutable_data_ptr(),
-                dk.mutable_data_ptr(), nullptr, static_cast<float*>(dwq.mutable_data_ptr()),
-                static_cast<float*>(dwk.mutable_data_ptr()), ws.mutable_data_ptr(), need, s);
-  Py_END_ALLOW_THREADS
+  {
+    Unlocked unlocked;
+    const at::Tensor ws = bytes(need, *c.q);
+    dq = at::empty(c.q->sizes(), c.q->options());
+    dk = at::empty(c.q->sizes(), c.q->options());
+    dwq = at::empty_like(*c.wq);
+    dwk = at::empty_like(*c.wk);
+    code = qk_bwd(&c.shape, c.q->const_data_ptr(), c.k->const_data_ptr(), c.rows.at,
+                  static_cast<const float*>(c.wq->const_data_ptr()),
+                  static_cast<const float*>(c.wk->const_data_ptr()), c.pos, dqo->const_data_ptr(),
+                  dko->const_data_ptr(), out_rows.at, dq.mutable_data_ptr(), dk.mutable_data_ptr(), nullptr,
+                  static_cast<float*>(dwq.mutable_data_ptr()), static_cast<float*>(dwk.mutable_data_ptr()),
+                  ws.mutable_data_ptr(), need, c10::cuda::getCurrentCUDAStream(c.index).stream());
+  }
   if (code != TRIATTN_OK) Py_RETURN_NONE;
   return Py_BuildValue("(NNNN)", THPVariable_Wrap(std::move(dq)), THPVariable_Wrap(std::move(dk)),
                        THPVariable_Wrap(std::move(dwq)), THPVariable_Wrap(std::move(dwk)));
@@ -215,13 +229,15 @@ PyObject* host_relpos_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !tokens(a[2], B, N, index, pos) || !tokens(a[3], B, N, index, chain))
     Py_RETURN_NONE;
   if (base == nullptr && rel_bytes(&s) == 0) Py_RETURN_NONE;  // before an output of any size is allocated
-  at::Tensor out = at::empty(sizes, table->options().dtype(at::kBFloat16));
-  void* stream = c10::cuda::getCurrentCUDAStream(index).stream();
+  at::Tensor out;
   triattn_status code;
-  Py_BEGIN_ALLOW_THREADS
-  code = rel_fwd(&s, static_cast<const float*>(table->const_data_ptr()),
-                 base != nullptr ? base->const_data_ptr() : nullptr, pos, chain, out.mutable_data_ptr(), stream);
-  Py_END_ALLOW_THREADS
+  {
+    Unlocked unlocked;
+    out = at::empty(sizes, table->options().dtype(at::kBFloat16));
+    code = rel_fwd(&s, static_cast<const float*>(table->const_data_ptr()),
+                   base != nullptr ? base->const_data_ptr() : nullptr, pos, chain, out.mutable_data_ptr(),
+                   c10::cuda::getCurrentCUDAStream(index).stream());
+  }
   if (code != TRIATTN_OK) Py_RETURN_NONE;
   return THPVariable_Wrap(std::move(out));
   END_HANDLE_TH_ERRORS
@@ -251,13 +267,15 @@ PyObject* host_relpos_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!tokens(a[2], B, N, index, pos) || !tokens(a[3], B, N, index, chain)) Py_RETURN_NONE;
   const size_t need = rel_bytes(&s);
   if (need == 0) Py_RETURN_NONE;
-  at::Tensor ws = bytes(need, *d), out = at::empty({s.buckets, F}, d->options().dtype(at::kFloat));
-  void* stream = c10::cuda::getCurrentCUDAStream(index).stream();
+  at::Tensor out;
   triattn_status code;
-  Py_BEGIN_ALLOW_THREADS
-  code = rel_bwd(&s, d->const_data_ptr(), pos, chain, static_cast<float*>(out.mutable_data_ptr()), ws.mutable_data_ptr(),
-                 need, stream);
-  Py_END_ALLOW_THREADS
+  {
+    Unlocked unlocked;
+    const at::Tensor ws = bytes(need, *d);
+    out = at::empty({s.buckets, F}, d->options().dtype(at::kFloat));
+    code = rel_bwd(&s, d->const_data_ptr(), pos, chain, static_cast<float*>(out.mutable_data_ptr()),
+                   ws.mutable_data_ptr(), need, c10::cuda::getCurrentCUDAStream(index).stream());
+  }
   if (code != TRIATTN_OK) Py_RETURN_NONE;
   return THPVariable_Wrap(std::move(out));
   END_HANDLE_TH_ERRORS

@@ -1048,7 +1048,9 @@ def triattn_relpos_fwd(table, base=None, positions=None, chains=None, *, layout:
         B, N = positions.shape
     else:
         raise ValueError("base, out or positions [B, N] must be given")
-    _, ref, shape, _ = _relpos_plan(B, N, F, K, layout, kind, max_distance, False)
+    _, ref, shape, need = _relpos_plan(B, N, F, K, layout, kind, max_distance, False)
+    if need == 0 and out is None and base is None:  # before an output of any size is allocated
+        raise TriAttnError(ERR_UNSUPPORTED, "triattn_relpos_fwd")
     dev = table.get_device()
     if not (_fits(table, dev, (K, F), torch.float32) and dev >= 0
             and (base is None or _fits(base, dev, shape, torch.bfloat16))):
