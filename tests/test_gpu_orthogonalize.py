@@ -172,3 +172,21 @@ def test_streams_graphs_and_two_at_once():
         assert all(torch.equal(a, b) for a, b in zip(outs[k], want[k:])) and torch.equal(eager[0], want[0])
     for g in got:
         assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+def test_a_wait_that_gives_up_is_reported():
+    """With a limit of a nanosecond the first wait for another CTA's tiles gives up: the
+    call's kernels end by themselves, the status word says so, and the next call, with
+    the limit as it was, is right."""
+    gs = [update(200, 300, 1), update(300, 260, 2, torch.float32)]
+    want = T.triattn_orthogonalize(gs)
+    assert T.device_status() == T.OK
+    T.set_wait_limit_ns(1)
+    try:
+        T.triattn_orthogonalize(gs)
+        status = T.device_status()
+    finally:
+        T.set_wait_limit_ns(0)
+    assert status == T.ERR_TIMEOUT
+    again = T.triattn_orthogonalize(gs)
+    assert T.device_status() == T.OK and all(torch.equal(a, b) for a, b in zip(again, want))
