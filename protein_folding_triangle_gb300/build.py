@@ -25,8 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "noalloc.cu", "module.cu", "trimul.cu", "gemm.cu", "transition.cu",
-           "transition_fwd.cu", "transition_rows.cu", "transition_bwd.cu", "transition_wgrad.cu", "gradnorm.cu", "qknorm.cu",
-           "relpos.cu", "relpos_pairs.cu", "orthogonalize.cu", "orth_solo.cu"]
+           "transition_fwd.cu", "transition_rows.cu", "transition_bwd.cu", "transition_wgrad.cu", "gradnorm.cu",
+           "qknorm.cu", "relpos.cu", "relpos_pairs.cu", "orthogonalize.cu", "orth_solo.cu"]
 HEADERS = ["ptx.cuh", "kernels.cuh", "pairops.cuh", "transition.cuh", "relpos.cuh", "orthogonalize.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]

@@ -664,7 +664,8 @@ int width_of(const OrthMat* q, int n) {
         widest[p] = std::max(widest[p], ks[p]);
       }
     }
-    for (int p = 0; p < 3 && n > 0; ++p) time += stage * std::max(widest[p], stages[p] / tiles[p] * std::ceil(tiles[p] / 152));
+    for (int p = 0; p < 3 && n > 0; ++p)
+      time += stage * std::max(widest[p], stages[p] / tiles[p] * std::ceil(tiles[p] / 152));
     if (w == 64 || time < least) {
       best = w;
       least = time;
@@ -784,12 +785,14 @@ cudaError_t run(const Plan& p, int steps, const float* co, float eps, uint8_t* w
     t.n = static_cast<int>(std::min<size_t>(kUpload, p.mats.size() - k));
     std::copy_n(p.mats.data() + k, t.n, t.mat);
     if (!small)
-      e = trace_call(kKOrthLoad, s, [&] { return launch_after(k == 0, orth_table_kernel, (t.n + kTableRows - 1) / kTableRows, 32, 0, s, t, mats + k); });
+      e = trace_call(kKOrthLoad, s, [&] {
+        return launch_after(k == 0, orth_table_kernel, (t.n + kTableRows - 1) / kTableRows, 32, 0, s, t, mats + k);
+      });
   }
   if (e == cudaSuccess)
     e = trace_call(kKOrthLoad, s, [&] {
-      return launch_after(small, small ? orth_norm_kernel<true> : orth_norm_kernel<false>, static_cast<unsigned>(p.parts),
-                          256, 0, s, t, v, mats);
+      return launch_after(small, small ? orth_norm_kernel<true> : orth_norm_kernel<false>,
+                          static_cast<unsigned>(p.parts), 256, 0, s, t, v, mats);
     });
   if (e == cudaSuccess)
     e = trace_call(kKOrthLoad, s, [&] {
@@ -804,7 +807,9 @@ cudaError_t run(const Plan& p, int steps, const float* co, float eps, uint8_t* w
   v.n -= p.solo;
   const OrthRun st{co[0], co[1], co[2], steps, static_cast<int>(p.sq), static_cast<int>(p.mn), wc};
   if (v.n > 0 && e == cudaSuccess)
-    e = trace_call(kKOrthGemm, s, [&] { return p.width == 64 ? launch_gemm<64>(v, st, s) : launch_gemm<128>(v, st, s); });
+    e = trace_call(kKOrthGemm, s, [&] {
+      return p.width == 64 ? launch_gemm<64>(v, st, s) : launch_gemm<128>(v, st, s);
+    });
   return e;
 }
 

@@ -265,7 +265,8 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks) relpos_heads_fwd_kernel(
       }
 #pragma unroll
       for (int g = 0; g < G; ++g)
-        if ((in_ >> g) & 1u) a.out[at[g]] = static_cast<uint16_t>(pack_bf16x2(bf16lo_to_f32(x[g]) + v[g], 0.f) & 0xFFFFu);
+        if ((in_ >> g) & 1u)
+          a.out[at[g]] = static_cast<uint16_t>(pack_bf16x2(bf16lo_to_f32(x[g]) + v[g], 0.f) & 0xFFFFu);
     }
   }
 }
@@ -280,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks) relpos_heads_fwd_kernel(
 constexpr int kPairsU = 4, kPairsBlocks = 5;
 int pairs_threads(int F) { return kThreads / (F / 8) * (F / 8); }
 int pairs_segment(int F) { return kPairsU * (kThreads / (F / 8)); }
-__global__ void __launch_bounds__(kThreads, kPairsBlocks) relpos_pairs_fwd_kernel(const __grid_constant__ RelposArgs a) {
+__global__ void __launch_bounds__(kThreads, kPairsBlocks)
+    relpos_pairs_fwd_kernel(const __grid_constant__ RelposArgs a) {
   constexpr int U = kPairsU;
   __shared__ uint8_t lut[2 * kRelposMaxDistance + 1];
   for (int d = threadIdx.x; d <= 2 * a.R; d += blockDim.x) lut[d] = a.lut[d];
@@ -399,7 +401,8 @@ __device__ __forceinline__ void values(const uint4 (&v)[4], float (&f)[16]) {
 constexpr int kBwdW = 16, kRowsMax = 8, kNear = 96, kNearMax = 47;
 static_assert(kNearMax + 2 * (kBwdW - 1) + kRowsMax - 1 < kNear, "distances of a chunk on the diagonal");
 template <typename T, int kRows>
-__global__ void __launch_bounds__(kThreads, 2) relpos_heads_bwd_kernel(const __grid_constant__ RelposArgs a, const T* d_out) {
+__global__ void __launch_bounds__(kThreads, 2)
+    relpos_heads_bwd_kernel(const __grid_constant__ RelposArgs a, const T* d_out) {
   constexpr int W = kBwdW;
   constexpr int V = sizeof(T);  // 16-byte pieces of a chunk
   constexpr int U = 16 / V < kRows ? 16 / V : kRows;  // rows in flight
@@ -432,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 2) relpos_heads_bwd_kernel(const __g
     const size_t s0 = p0 + static_cast<size_t>(i0) * a.N;
     auto off_of = [&](int r) { return static_cast<int>((s0 + static_cast<size_t>(r) * a.N) & (W - 1)); };
     // the rows' positions and chains
-    const int pi = a.position(b, i0 + min(lane, nr - 1)), ci = chain != nullptr ? __ldg(chain + i0 + min(lane, nr - 1)) : 0;
+    const int own = i0 + min(lane, nr - 1), pi = a.position(b, own), ci = chain != nullptr ? __ldg(chain + own) : 0;
     const int rlo = __reduce_min_sync(0xffffffffu, pi), rhi = __reduce_max_sync(0xffffffffu, pi);
     const int rc = __reduce_min_sync(0xffffffffu, ci), rc1 = __reduce_max_sync(0xffffffffu, ci);
     const bool rrun = __all_sync(0xffffffffu, static_cast<long long>(pi) - rlo == min(lane, nr - 1));
@@ -486,12 +489,14 @@ __global__ void __launch_bounds__(kThreads, 2) relpos_heads_bwd_kernel(const __g
         uint32_t x[4][kNear / 16];  // all loads before the first sum
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int r = r0 + q, j0 = i0 + r + kNear - lane, c0 = j0 + off_of(r) - 32 * W * cb;  // from the chunks' first column
+          const int r = r0 + q, j0 = i0 + r + kNear - lane;
+          const int c0 = j0 + off_of(r) - 32 * W * cb;  // from the chunks' first column
           const T* row = d_out + s0 + static_cast<size_t>(r) * a.N;
 #pragma unroll
           for (int m = 0; m < kNear / 16; ++m) {
             const int j = j0 - 32 * m, c = c0 - 32 * m;
-            const bool in = (r < nr) & (j >= 0) & (j < a.N) & (c >= 0) & (c < 32 * W) & ((diagonals >> ((c / W) & 31)) & 1u);
+            const bool in = (r < nr) & (j >= 0) & (j < a.N) & (c >= 0) & (c < 32 * W) &
+                            ((diagonals >> ((c / W) & 31)) & 1u);
             x[q][m] = load1(row + j, in);
           }
         }
@@ -567,8 +572,8 @@ __global__ void __launch_bounds__(kThreads, 2) relpos_heads_bwd_kernel(const __g
 // of the sum per block, by fours in FP32, joined in a fixed order in FP64 by one warp:
 // FP64 adds are two a clock and SM (every partial in FP64: 2 us more at 152 partials of
 // 66 x 128; a tree over all warps' lanes at the end 1 to 3).
-__global__ void __launch_bounds__(1024) relpos_sum_kernel(const float* part, float* out, int nx, int ox, int oy, int nb, int ns, size_t pb, size_t ps,
-                                                          size_t py) {
+__global__ void __launch_bounds__(1024) relpos_sum_kernel(const float* part, float* out, int nx, int ox, int oy, int nb,
+                                                          int ns, size_t pb, size_t ps, size_t py) {
   __shared__ double sh[32][33];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, x = blockIdx.x * 32 + lane;
   double v = 0.0;
@@ -664,7 +669,8 @@ BwdPlan bwd_plan(int B, int N, int F, int buckets) {
   BwdPlan p;
   const size_t win = (static_cast<size_t>(chunks_of(N, kBwdW)) * sizeof(Window) + 15) / 16 * 16;
   p.warps = kThreads / 32;
-  while (p.warps > 1 && win + static_cast<size_t>(p.warps) * buckets * 128 > (p.warps > 4 ? 72000u : 216000u)) p.warps /= 2;
+  while (p.warps > 1 && win + static_cast<size_t>(p.warps) * buckets * 128 > (p.warps > 4 ? 72000u : 216000u))
+    p.warps /= 2;
   p.smem = win + static_cast<size_t>(p.warps) * buckets * 128;
   const int per_sm = std::max(1, std::min<int>(16 / p.warps, static_cast<int>(232448 / (p.smem + 3200))));
   const int cols = (chunks_of(N, kBwdW) + 31) / 32;
@@ -740,8 +746,8 @@ triattn_status triattn_relpos_fwd(const triattn_relpos_shape* shape, const float
   triattn_status st = check_shape(shape);
   if (st != TRIATTN_OK) return st;
   if (!rule_ok(shape, chains != nullptr)) return TRIATTN_ERR_INVALID_ARG;
-  if (!al(table, 16) || !al(out, 16) || (base != nullptr && !al(base, 16)) || (positions != nullptr && !al(positions, 4)) ||
-      (chains != nullptr && !al(chains, 4)))
+  if (!al(table, 16) || !al(out, 16) || (base != nullptr && !al(base, 16)) ||
+      (positions != nullptr && !al(positions, 4)) || (chains != nullptr && !al(chains, 4)))
     return TRIATTN_ERR_INVALID_ARG;
   RelposArgs a = args_of(shape, positions, chains);
   a.table = table;
@@ -774,8 +780,8 @@ triattn_status triattn_relpos_bwd(const triattn_relpos_shape* shape, const void*
     e = trace_call(kKRelBwd, s, [&] { return launch_relpos_pairs_bwd(a, d_out, parts, current_wait_ctl(), s); });
     if (e == cudaSuccess)
       e = trace_call(kKRelSum, s, [&] {  // partials [parts][buckets][F]
-        return launch_after(false, relpos_sum_kernel, dim3((a.F + 31) / 32, a.buckets), 1024, 0, s, a.part, d_table, a.F,
-                            1, a.F, 1, parts, 0, static_cast<size_t>(a.buckets) * a.F, a.F);
+        return launch_after(false, relpos_sum_kernel, dim3((a.F + 31) / 32, a.buckets), 1024, 0, s, a.part, d_table,
+                            a.F, 1, a.F, 1, parts, 0, static_cast<size_t>(a.buckets) * a.F, a.F);
       });
   } else {
     const BwdPlan p = bwd_plan(a.B, a.N, a.F, a.buckets);

@@ -1012,7 +1012,8 @@ def _relpos_plan(B, N, F, buckets, layout, kind, max_distance, dout_fp32):
 
 def _relpos_ids(positions, chains, B, N, device):
     dev, i32 = device.index, torch.int32
-    if ((positions is None or _fits(positions, dev, (B, N), i32)) and (chains is None or _fits(chains, dev, (B, N), i32))):
+    if ((positions is None or _fits(positions, dev, (B, N), i32))
+            and (chains is None or _fits(chains, dev, (B, N), i32))):
         return
     for name, t in (("positions", positions), ("chains", chains)):
         if t is not None:

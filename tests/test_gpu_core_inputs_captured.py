@@ -70,7 +70,8 @@ def test_two_graphs_with_their_own_lists():
     """Each holds its own list of matrices (300, past what a launch's parameters
     hold, and a short one); replayed in turn, eager calls of a third between them."""
     g = torch.Generator(device="cuda").manual_seed(5)
-    lists = [[torch.empty(3 + i % 40, 50 + i, device="cuda").normal_(generator=g) for i in range(n)] for n in (300, 9, 20)]
+    lists = [[torch.empty(3 + i % 40, 50 + i, device="cuda").normal_(generator=g) for i in range(n)]
+             for n in (300, 9, 20)]
     outs = [[torch.empty(t.shape, dtype=torch.bfloat16, device="cuda") for t in ts] for ts in lists]
     want = [T.triattn_orthogonalize(ts) for ts in lists]
     torch.cuda.synchronize()

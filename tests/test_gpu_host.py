@@ -100,17 +100,25 @@ def test_on_the_current_stream():
 def test_refusals():
     q, w = randn(1, 3, 2, 9, 16), torch.rand(2, 16, device="cuda")
     table, planes = torch.randn(65, 4, device="cuda"), randn(1, 4, 9, 9)
-    for f in (lambda: T.triattn_qk_norm_fwd(q.float(), q.float(), w, w), lambda: T.triattn_qk_norm_fwd(q, q[:, :2], w, w),
+    for f in (lambda: T.triattn_qk_norm_fwd(q.float(), q.float(), w, w),
+              lambda: T.triattn_qk_norm_fwd(q, q[:, :2], w, w),
               lambda: T.triattn_qk_norm_fwd(q, q, w.bfloat16(), w),
-              lambda: T.triattn_qk_norm_fwd(q, q.cpu(), w, w), lambda: T.triattn_qk_norm_fwd(q, q, w, w, None, "quarter"),
+              lambda: T.triattn_qk_norm_fwd(q, q.cpu(), w, w),
+              lambda: T.triattn_qk_norm_fwd(q, q, w, w, None, "quarter"),
               lambda: T.triattn_qk_norm_fwd(q.transpose(2, 4), q.transpose(2, 4), w, w),
-              lambda: T.triattn_relpos_fwd(table, planes.float()), lambda: T.triattn_relpos_fwd(table, planes, layout="rows"),
-              lambda: T.triattn_relpos_fwd(table.t(), planes), lambda: T.triattn_relpos_bwd(planes[..., :8], 65),
-              lambda: T.triattn_orthogonalize([q]), lambda: T.triattn_orthogonalize([w.double()]),
-              lambda: T.triattn_orthogonalize([w], out=[w]), lambda: T.triattn_orthogonalize([w], out=[w.bfloat16().t()])):
+              lambda: T.triattn_relpos_fwd(table, planes.float()),
+              lambda: T.triattn_relpos_fwd(table, planes, layout="rows"),
+              lambda: T.triattn_relpos_fwd(table.t(), planes),
+              lambda: T.triattn_relpos_bwd(planes[..., :8], 65),
+              lambda: T.triattn_orthogonalize([q]),
+              lambda: T.triattn_orthogonalize([w.double()]),
+              lambda: T.triattn_orthogonalize([w], out=[w]),
+              lambda: T.triattn_orthogonalize([w], out=[w.bfloat16().t()])):
         with pytest.raises(ValueError):
             f()
-    for f in (lambda: T.triattn_qk_norm_fwd(q, q, w, w, eps=-1.0), lambda: T.triattn_relpos_fwd(table, planes, max_distance=31),
-              lambda: T.triattn_relpos_bwd(planes, 66), lambda: T.triattn_relpos_bwd(planes, 1 << 20, max_distance=1 << 19)):
+    for f in (lambda: T.triattn_qk_norm_fwd(q, q, w, w, eps=-1.0),
+              lambda: T.triattn_relpos_fwd(table, planes, max_distance=31),
+              lambda: T.triattn_relpos_bwd(planes, 66),
+              lambda: T.triattn_relpos_bwd(planes, 1 << 20, max_distance=1 << 19)):
         with pytest.raises(T.TriAttnError):
             f()

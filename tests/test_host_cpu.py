@@ -29,8 +29,8 @@ def test_it_takes_no_other_calls(host):
         assert host.relpos_bwd(planes, number, None, None, 0, 0, 32) is None
     assert host.qk_norm_fwd(q) is None and host.qk_norm_bwd() is None
     assert host.relpos_fwd() is None and host.relpos_bwd(planes) is None
-    for lists in (([q],), ([table], [table], 0), ([table], None, -1), ([3], None, 0), (table, None, 0), ([], [table], 0),
-                  ([table], table, 0), ([table], None, "0")):
+    for lists in (([q],), ([table], [table], 0), ([table], None, -1), ([3], None, 0), (table, None, 0),
+                  ([], [table], 0), ([table], table, 0), ([table], None, "0")):
         assert host.matrix_tables(*lists) is None
     assert host.matrix_tables([], None, 0) == (b"", None) and host.matrix_tables([], [], 0) == (b"", b"")
 
