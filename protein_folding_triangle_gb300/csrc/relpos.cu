@@ -435,7 +435,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const size_t s0 = p0 + static_cast<size_t>(i0) * a.N;
     auto off_of = [&](int r) { return static_cast<int>((s0 + static_cast<size_t>(r) * a.N) & (W - 1)); };
     // the rows' positions and chains
-    const int own = i0 + min(lane, nr - 1), pi = a.position(b, own), ci = chain != nullptr ? __ldg(chain + own) : 0;
+    const int pi = a.position(b, i0 + min(lane, nr - 1));
+    const int ci = chain != nullptr ? __ldg(chain + i0 + min(lane, nr - 1)) : 0;
     const int rlo = __reduce_min_sync(0xffffffffu, pi), rhi = __reduce_max_sync(0xffffffffu, pi);
     const int rc = __reduce_min_sync(0xffffffffu, ci), rc1 = __reduce_max_sync(0xffffffffu, ci);
     const bool rrun = __all_sync(0xffffffffu, static_cast<long long>(pi) - rlo == min(lane, nr - 1));
