@@ -665,7 +665,7 @@ triattn_status triattn_qk_norm_bwd(const triattn_qk_norm_shape* shape, const voi
  * contiguous, 16-byte aligned; positions, chains and d_table 4-byte aligned.
  * out may be base; otherwise outputs must not overlap inputs.  The gradient of
  * base is d_out.  d_out has to be finite (a value that is not may make other
- * buckets of its column NaN).  Sums are FP32, joined in FP64, in a fixed order:
+ * buckets of its column NaN).  Sums are FP32, joined in pairs of FP32, in a fixed order:
  * bitwise reproducible.  workspace (backward):
  * triattn_relpos_workspace_bytes(shape) bytes, 256-byte aligned, contents
  * ignored.

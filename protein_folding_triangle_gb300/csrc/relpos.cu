@@ -569,34 +569,81 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// out[y * oy + x * ox] = sum over (b, s) of part[b * pb + s * ps + y * py + x], 32 x by 32 slices
-// of the sum per block, by fours in FP32, joined in a fixed order in FP64 by one warp:
-// FP64 adds are two a clock and SM (every partial in FP64: 2 us more at 152 partials of
-// 66 x 128; a tree over all warps' lanes at the end 1 to 3).
-__global__ void __launch_bounds__(1024) relpos_sum_kernel(const float* part, float* out, int nx, int ox, int oy, int nb,
-                                                          int ns, size_t pb, size_t ps, size_t py) {
-  __shared__ double sh[32][33];
-  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, x = blockIdx.x * 32 + lane;
-  double v = 0.0;
+// A sum in two floats: what an addition rounds off is added apart (Knuth's sum of two
+// numbers).  FP64 has two additions a clock and SM, this some twenty.
+struct Sum2 {
+  float s = 0.f, c = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float t = s + x, z = t - s;
+    c += (s - (t - z)) + (x - z);
+    s = t;
+  }
+  __device__ __forceinline__ void add(float2 x) {
+    add(x.x);
+    c += x.y;
+  }
+  __device__ __forceinline__ float2 pair() const { return make_float2(s, c); }
+};
+
+// Planes: out[k * F + f] = sum over (b, s) of part[b][f][s][k], k along the lanes, 32 slices
+// of the sum per block, joined in a fixed order.
+__global__ void __launch_bounds__(1024) relpos_sum_kernel(const float* part, float* out, int buckets, int nb, int ns) {
+  __shared__ float2 sh[32][33];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, k = blockIdx.x * 32 + lane, F = gridDim.y;
+  const size_t ps = buckets, py = ps * ns, pb = py * F;
+  Sum2 v;
   after_previous();
-  if (x < nx) {
-#pragma unroll 2
-    for (int e0 = slice; e0 < nb * ns; e0 += 128) {
-      float f = 0.f;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int e = e0 + 32 * u, b = e / ns, s = e - b * ns;
-        if (e < nb * ns) f += part[b * pb + s * ps + blockIdx.y * py + x];
-      }
-      v += f;
+  if (k < buckets) {
+#pragma unroll 4
+    for (int e = slice; e < nb * ns; e += 32) {
+      const int b = e / ns, s = e - b * ns;
+      v.add(part[b * pb + blockIdx.y * py + s * ps + k]);
     }
   }
-  sh[slice][lane] = v;
+  sh[slice][lane] = v.pair();
   __syncthreads();
-  if (slice == 0 && x < nx) {
-    v = 0.0;
-    for (int s = 0; s < 32; ++s) v += sh[s][lane];
-    out[static_cast<size_t>(blockIdx.y) * oy + static_cast<size_t>(x) * ox] = static_cast<float>(v);
+  if (slice == 0 && k < buckets) {
+    for (int s = 1; s < 32; ++s) v.add(sh[s][lane]);
+    out[static_cast<size_t>(k) * F + blockIdx.y] = v.s + v.c;
+  }
+}
+
+// Pair features: out[x] = sum over s of part[s][x], x in fours along the lanes, S slices of
+// the sum per block, joined by a warp for each of the four.  32 slices, or eight where there
+// are few partials.  Both measured, the gradient as a whole: 309^2 pairs of 256 features and
+// 201 buckets (152 partials, 31 MB) 27 us with 32 and 31 with eight, 640^2 pairs of 128 and
+// 65 28 and 34; 2 x 30^2 pairs of 256 and 201 (29 partials) 18.5 and 17.
+template <int S>
+__global__ void __launch_bounds__(32 * S) relpos_flat_sum_kernel(const float* part, float* out, int n4, int parts) {
+  constexpr int U = S == 8 ? 8 : 5;  // loads under way together
+  __shared__ float2 sh[S][4][32];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, x = blockIdx.x * 32 + lane;
+  Sum2 v[4];
+  after_previous();
+  if (x < n4) {
+    const float4* p = reinterpret_cast<const float4*>(part) + x;
+    for (int s0 = slice; s0 < parts; s0 += U * S) {
+      float4 f[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        f[u] = s0 + u * S < parts ? p[static_cast<size_t>(s0 + u * S) * n4] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        v[0].add(f[u].x);
+        v[1].add(f[u].y);
+        v[2].add(f[u].z);
+        v[3].add(f[u].w);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sh[slice][i][lane] = v[i].pair();
+  __syncthreads();
+  if (slice < 4 && x < n4) {
+    Sum2 w;
+#pragma unroll
+    for (int s = 0; s < S; ++s) w.add(sh[s][slice][lane]);
+    out[4 * static_cast<size_t>(x) + slice] = w.s + w.c;
   }
 }
 
@@ -781,8 +828,10 @@ triattn_status triattn_relpos_bwd(const triattn_relpos_shape* shape, const void*
     e = trace_call(kKRelBwd, s, [&] { return launch_relpos_pairs_bwd(a, d_out, parts, current_wait_ctl(), s); });
     if (e == cudaSuccess)
       e = trace_call(kKRelSum, s, [&] {  // partials [parts][buckets][F]
-        return launch_after(false, relpos_sum_kernel, dim3((a.F + 31) / 32, a.buckets), 1024, 0, s, a.part, d_table,
-                            a.F, 1, a.F, 1, parts, 0, static_cast<size_t>(a.buckets) * a.F, a.F);
+        const int n4 = a.buckets * a.F / 4;
+        const bool few = parts <= 64;
+        return launch_after(false, few ? relpos_flat_sum_kernel<8> : relpos_flat_sum_kernel<32>, dim3((n4 + 31) / 32),
+                            few ? 256 : 1024, 0, s, a.part, d_table, n4, parts);
       });
   } else {
     const BwdPlan p = bwd_plan(a.B, a.N, a.F, a.buckets);
@@ -792,9 +841,8 @@ triattn_status triattn_relpos_bwd(const triattn_relpos_shape* shape, const void*
     });
     if (e == cudaSuccess)
       e = trace_call(kKRelSum, s, [&] {  // partials [B][F][splits][buckets]
-        const size_t per = static_cast<size_t>(p.splits) * a.buckets;
         return launch_after(false, relpos_sum_kernel, dim3((a.buckets + 31) / 32, a.F), 1024, 0, s, a.part, d_table,
-                            a.buckets, a.F, 1, a.B, p.splits, a.F * per, a.buckets, per);
+                            a.buckets, a.B, p.splits);
       });
   }
   return e == cudaSuccess ? TRIATTN_OK : TRIATTN_ERR_CUDA;

@@ -10,9 +10,9 @@
 // pairs, 128 features and 66 buckets, against 22 us for the bytes of d_out,
 // which bound it.
 //
-// 640^2 pairs, 128 features, 66 buckets (105 MB): 26 us and 13 for the sum of the runs'
-// tables (5 MB); 1920^2 pairs 5.6 TB/s.  Short lists pay the start: barriers, TMEM, the
-// first stages, the last accumulators take 6 us.
+// 640^2 pairs, 128 features, 66 buckets (105 MB): 28 us with the sum of the runs' tables
+// (5 MB); 1920^2 pairs 5.6 TB/s.  Short lists pay the start: barriers, TMEM, the first
+// stages, the last accumulators take 5 us.
 //
 // One CTA per run of pairs, ten warps:
 //   warp 0     TMA: per 64 pairs the rows of d_out as 64-feature boxes (128-byte
@@ -26,7 +26,7 @@
 //              the next stage while they wait for this one), then the two bytes of
 //              its one in B [buckets, 64 pairs] (K-major, swizzled), after the one
 //              that the stage held before is put out.
-// At the end four warps add the accumulators and write the run's partial table.
+// At the end eight warps add the accumulators and write the run's partial table.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -71,6 +71,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const
   volatile int* abort = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int d = threadIdx.x; d <= 2 * a.R; d += kPairThreads) lut[d] = a.lut[d];
+  const long long blocks = (p.P + kBlk - 1) / kBlk;
+  const long long b0 = blocks * blockIdx.x / gridDim.x, b1 = blocks * (blockIdx.x + 1) / gridDim.x;
+  const int n = static_cast<int>(b1 - b0);
+  // the stages' B, of zeros at first
+  const int pieces = p.nb * 8, used_stages = min(n, p.stages);
+  for (int e = threadIdx.x; e < used_stages * pieces; e += kPairThreads) {
+    const int stage = e / pieces;
+    *reinterpret_cast<uint4*>(sm + stage * p.stage_bytes + p.a_bytes + (e - stage * pieces) * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&bars.full[s], 1 + 2);
@@ -85,9 +96,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem_slot;
-  const long long blocks = (p.P + kBlk - 1) / kBlk;
-  const long long b0 = blocks * blockIdx.x / gridDim.x, b1 = blocks * (blockIdx.x + 1) / gridDim.x;
-  const int n = static_cast<int>(b1 - b0);
   const int boxes = (a.F + 63) / 64;
 
   if (warp == 0) {
@@ -164,11 +172,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const
       const int row_next = k + p.groups < n ? bucket() : -1;
       if (!__all_sync(0xffffffffu, mbar_wait(&bars.empty[stage], phase ^ 1, p.wc, abort))) break;
       uint16_t* e = reinterpret_cast<uint16_t*>(sm + stage * p.stage_bytes + p.a_bytes);
-      if (k < p.stages) {  // a fresh stage: the pair's column of zeros
-        for (int r = 0; r < p.nb; ++r) e[sw128(r, c >> 3) / 2 + (c & 7)] = 0;
-      } else if (held[stage][c] != kNone) {
-        e[held[stage][c]] = 0;
-      }
+      if (k >= p.stages && held[stage][c] != kNone) e[held[stage][c]] = 0;
       const uint16_t at = row >= 0 ? static_cast<uint16_t>(sw128(row, c >> 3) / 2 + (c & 7)) : kNone;
       if (at != kNone) e[at] = 0x3F80;  // 1
       held[stage][c] = at;
@@ -181,13 +185,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const
   __syncwarp();
   const bool ok = __all_sync(0xffffffffu, mbar_wait(&bars.done, 0, p.wc, abort));
   tc_fence_after();
-  if (ok && warp < 4) {
+  if (ok && warp < 8) {  // two warps to a quarter of the features, buckets in turn
     float* out = a.part + static_cast<size_t>(blockIdx.x) * a.buckets * a.F;
-    const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int used = min(n, p.sets);
     for (int m = 0; m < p.mt; ++m) {
-      const int f = m * 128 + warp * 32 + lane;
-      for (int k0 = 0; k0 < p.nb; k0 += 16) {
+      const int f = m * 128 + (warp & 3) * 32 + lane;
+      for (int k0 = warp < 4 ? 0 : 16; k0 < p.nb; k0 += 32) {
         float v[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = 0.f;
