@@ -209,6 +209,22 @@ cudaError_t trace_call(int kind, cudaStream_t s, F&& launch) {
       kind, s, [](void* f) -> cudaError_t { return (*static_cast<std::remove_reference_t<F>*>(f))(); }, &launch);
 }
 
+// A sum in two floats: what an addition rounds off is added apart (Knuth's sum of two
+// numbers).  FP64 has two additions a clock and SM, this some twenty.
+struct Sum2 {
+  float s = 0.f, c = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float t = s + x, z = t - s;
+    c += (s - (t - z)) + (x - z);
+    s = t;
+  }
+  __device__ __forceinline__ void add(float2 x) {
+    add(x.x);
+    c += x.y;
+  }
+  __device__ __forceinline__ float2 pair() const { return make_float2(s, c); }
+};
+
 // Launch of a kernel that starts with after_previous(): its blocks may come up
 // while the kernel before it in the stream still runs, as soon as each of that
 // one's blocks has let_next_start() or ended, and wait there for its results.  The

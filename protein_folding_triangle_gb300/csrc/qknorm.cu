@@ -328,51 +328,43 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_bwd_kernel(const QkArgs a
 
 // dw[h][d] (or dw[d], all heads) from the blocks' partial sums, in a fixed order.
 // Partials [chunks][tiles][slots][D]: a slot is all of a tile where the heads share a
-// weight (2 x 131 tokens of six heads: 11 -> 3 us); with the heads in a row it is a head
+// weight (2 x 131 tokens of six heads: 11 -> 2 us); with the heads in a row it is a head
 // (the j0 + slot-th where a tile does not hold all of them), otherwise the
 // slot-th head of the tile.
 __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* part, float* dwq, float* dwk, int D, int rows,
                                                           int tiles, int chunks, int slots, int H, int N, int w_heads,
                                                           int hn) {
-  __shared__ double sh[1024];
+  __shared__ float2 sh[1024];
   after_previous();
   const int d = threadIdx.x % D, lane = threadIdx.x / D, lanes = 1024 / D;
   const float* p = part + static_cast<size_t>(blockIdx.y) * chunks * tiles * slots * D + d;
   const int h = blockIdx.x;
-  double v = 0.0;
+  Sum2 v;
   if (w_heads == 1) {  // everything
     const int n = chunks * tiles * slots;
-#pragma unroll 2
-    for (int e0 = lane; e0 < n; e0 += 4 * lanes) {  // by fours in FP32: FP64 has two adds a clock and SM
-      float f = 0.f;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (e0 + u * lanes < n) f += p[static_cast<size_t>(e0 + u * lanes) * D];
-      v += f;
-    }
+#pragma unroll 4
+    for (int e = lane; e < n; e += lanes) v.add(p[static_cast<size_t>(e) * D]);
   } else {
     const int t0 = hn ? 0 : static_cast<int>(static_cast<long long>(h) * N / rows);
     const int nt = (hn ? tiles : static_cast<int>(((h + 1ll) * N - 1) / rows) + 1) - t0;
-#pragma unroll 2
-    for (int e0 = lane; e0 < nt * chunks; e0 += 4 * lanes) {
-      float f = 0.f;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int e = e0 + u * lanes, ch = e / nt, t = t0 + e - ch * nt;
-        int sl = h;
-        if (!hn) sl = h - static_cast<int>(static_cast<long long>(t) * rows / N);
-        else if (slots < H) sl = static_cast<int>((h + H - static_cast<long long>(t) * rows % H) % H);
-        if (e < nt * chunks && sl < slots) f += p[((static_cast<size_t>(ch) * tiles + t) * slots + sl) * D];
-      }
-      v += f;
+#pragma unroll 4
+    for (int e = lane; e < nt * chunks; e += lanes) {
+      const int ch = e / nt, t = t0 + e - ch * nt;
+      int sl = h;
+      if (!hn) sl = h - static_cast<int>(static_cast<long long>(t) * rows / N);
+      else if (slots < H) sl = static_cast<int>((h + H - static_cast<long long>(t) * rows % H) % H);
+      if (sl < slots) v.add(p[((static_cast<size_t>(ch) * tiles + t) * slots + sl) * D]);
     }
   }
-  sh[threadIdx.x] = v;
+  sh[threadIdx.x] = v.pair();
   for (int o = lanes / 2; o > 0; o /= 2) {
     __syncthreads();
-    if (lane < o) sh[threadIdx.x] += sh[threadIdx.x + o * D];
+    if (lane < o) {
+      v.add(sh[threadIdx.x + o * D]);
+      sh[threadIdx.x] = v.pair();
+    }
   }
-  if (lane == 0) (blockIdx.y ? dwk : dwq)[static_cast<size_t>(h) * D + d] = static_cast<float>(sh[threadIdx.x]);
+  if (lane == 0) (blockIdx.y ? dwk : dwq)[static_cast<size_t>(h) * D + d] = v.s + v.c;
 }
 
 struct Plan {

@@ -569,22 +569,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// A sum in two floats: what an addition rounds off is added apart (Knuth's sum of two
-// numbers).  FP64 has two additions a clock and SM, this some twenty.
-struct Sum2 {
-  float s = 0.f, c = 0.f;
-  __device__ __forceinline__ void add(float x) {
-    const float t = s + x, z = t - s;
-    c += (s - (t - z)) + (x - z);
-    s = t;
-  }
-  __device__ __forceinline__ void add(float2 x) {
-    add(x.x);
-    c += x.y;
-  }
-  __device__ __forceinline__ float2 pair() const { return make_float2(s, c); }
-};
-
 // Planes: out[k * F + f] = sum over (b, s) of part[b][f][s][k], k along the lanes, 32 slices
 // of the sum per block, joined in a fixed order.
 __global__ void __launch_bounds__(1024) relpos_sum_kernel(const float* part, float* out, int buckets, int nb, int ns) {
