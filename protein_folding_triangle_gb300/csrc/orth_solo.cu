@@ -13,7 +13,9 @@
 // Between two passes the team adds its parts of A, every CTA one band of rows in
 // the order of the ranks, and every CTA then makes all of B' = b A + c A^2 + a I.
 // The parts go through L2 (distributed shared memory took 20 us a step for a team
-// of eight) and the bands of the sum from there by multicast.
+// of eight), and every CTA loads the bands of the sum from there, once all have said that
+// theirs are written (one copy of a band to all CTAs of the team: 64 us for the ten
+// matrices of a block, so 65).
 //
 // 480 matrices of 48 blocks of 128 features: 223 us, tensor pipe active 43 %; the ten
 // of one block, teams of eight: 58 us, 11 us a step, most of it the team's sum.
@@ -57,7 +59,7 @@ struct SoloBars {
   uint64_t afull, aready, a2full, bready;
   uint64_t aimage;         // the team's A has been loaded
   uint64_t saved;          // a pass's chunks are in memory
-  uint64_t team, band;     // the team's CTAs; this CTA's band of the sum is in memory
+  uint64_t team, bands;    // the team's CTAs: the parts of A, the bands of their sum are in memory
   uint64_t quad[4];        // the four warps of a quarter of the rows
   uint32_t tmem_slot;
   int abort;
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1) orth_solo_kernel(const OrthMat* m
     mbar_init(&bars.bready, kWarps);
     mbar_init(&bars.saved, 4);
     mbar_init(&bars.team, T * kWarps);
-    mbar_init(&bars.band, kWarps);
+    mbar_init(&bars.bands, T * kWarps);
     for (int i = 0; i < 4; ++i) mbar_init(&bars.quad[i], 4);
     mbar_init(&bars.aimage, 1);
     bars.abort = 0;
@@ -250,9 +252,12 @@ __global__ void __launch_bounds__(kThreads, 1) orth_solo_kernel(const OrthMat* m
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    auto team_sync = [&]() {
+    auto team_arrive = [&](uint64_t* bar) {  // in every CTA of the team
       __syncwarp();
-      if (lane < T) mbar_arrive_cluster(&bars.team, lane);
+      if (lane < T) mbar_arrive_cluster(bar, lane);
+    };
+    auto team_sync = [&]() {
+      team_arrive(&bars.team);
       go = go && __all_sync(0xffffffffu, mbar_wait<true>(&bars.team, tphase, wc, abort));
       tphase ^= 1;
       return go;
@@ -333,18 +338,14 @@ __global__ void __launch_bounds__(kThreads, 1) orth_solo_kernel(const OrthMat* m
           *reinterpret_cast<uint4*>(at) = hi;
           *reinterpret_cast<uint4*>(at + kOrthPlane) = lo;
         }
-        fence_proxy_async_all();  // the band is read by bulk copies
-        arrive(&bars.band);
-        if (te == 0) {
+        fence_proxy_async_all();  // the bands are read by bulk copies
+        team_arrive(&bars.bands);
+        if (te == 0 && mbar_wait<true>(&bars.bands, (p - 1) & 1, wc, abort)) {
+          fence_proxy_async_all();
           mbar_expect_tx(&bars.aimage, kB);
-          if (mbar_wait(&bars.band, (p - 1) & 1, wc, abort)) {
-            fence_proxy_async_all();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {  // hi and lo of both tiles, to every CTA of the team
-              const int at = k * kOrthPlane + rank * RL * 128;
-              bulk_load_multicast(sm + at, image + at, RL * 128, &bars.aimage, (1u << T) - 1u);
-            }
-          }
+          for (int k = 0; k < 4; ++k)  // hi and lo of both tiles
+            bulk_load(sm + k * kOrthPlane, image + k * kOrthPlane, kOrthPlane, &bars.aimage);
         }
         __syncwarp();
         if (!wait(&bars.aimage, (p - 1) & 1)) break;
