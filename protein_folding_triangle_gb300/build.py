@@ -7,8 +7,8 @@ into ``_build/libtriattn_<machine>.so`` next to this file.  No cmake, no
 torch extension machinery: the library exports a plain C ABI
 (include/triattn.h).  ``csrc/host.cpp``, which reads torch tensors for the
 binding, is compiled with g++ against the installed torch's headers into
-``_build/triattn_host_<machine>_<torch version>.so``; the library does not
-depend on it.
+``_build/triattn_host_<torch version>.<Python's ABI tag>.so``; the library does
+not depend on it, and where it cannot be compiled the binding does without.
 """
 from __future__ import annotations
 
@@ -18,6 +18,7 @@ import platform
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -45,7 +46,8 @@ def lib_path() -> str:
 
 def host_path() -> str:
     import torch
-    return os.path.join(BUILD, f"triattn_host_{platform.machine()}_{torch.__version__}.so")
+    # the tag (cpython-312-x86_64-linux-gnu, say) names the interpreter and the machine
+    return os.path.join(BUILD, f"triattn_host_{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")
 
 
 def _stale(out: str, deps) -> bool:
@@ -62,7 +64,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=1) as ex:
         host = ex.submit(_build_host, force, verbose)
         out = _build_lib(force, verbose)
-        host.result()
+        try:
+            host.result()
+        except (RuntimeError, OSError) as e:
+            warnings.warn(f"the binding's native part is not built: {e}", RuntimeWarning)
     return out
 
 
@@ -83,6 +88,8 @@ def _build_host(force: bool, verbose: bool) -> None:
     cmd += ["-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
+        if os.path.exists(out):
+            os.remove(out)  # of an older source
         raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
     if verbose:
         print(r.stdout, r.stderr)

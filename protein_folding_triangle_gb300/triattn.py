@@ -16,6 +16,7 @@ import operator
 import os
 import struct
 import threading
+import warnings
 from typing import Optional
 
 import torch
@@ -234,17 +235,30 @@ def load(path: Optional[str] = None):
     return _LIB
 
 
+class _General:
+    """Stands where the native part is not there: every call goes the general path."""
+
+    @staticmethod
+    def _leave(*args):
+        return None
+
+    qk_norm_fwd = qk_norm_bwd = relpos_fwd = relpos_bwd = matrix_tables = _leave
+
+
 def _load_host(lib):
     """The binding's native part (csrc/host.cpp), which takes the library's functions
-    by address: usual calls of some entry points and the tables of long lists."""
+    by address: usual calls of some entry points and the tables of long lists.  It is
+    built for one torch and one Python; without it these calls take some 10 us more."""
     global _HOST
-    from . import build
-    p = build.host_path()
-    if not os.path.exists(p):
-        raise RuntimeError(f"the binding's native part is not built ({p} missing): run __graft_entry__.build()")
-    loader = importlib.machinery.ExtensionFileLoader("triattn_host", p)
-    host = importlib.util.module_from_spec(importlib.util.spec_from_loader("triattn_host", loader))
-    loader.exec_module(host)
+    p = _build.host_path()
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("triattn_host", p)
+        host = importlib.util.module_from_spec(importlib.util.spec_from_loader("triattn_host", loader))
+        loader.exec_module(host)
+    except ImportError as e:
+        warnings.warn(f"the binding's native part is not used ({e}): run __graft_entry__.build()", RuntimeWarning)
+        _HOST = _General
+        return
     names = ("qk_norm_workspace_bytes", "qk_norm_fwd", "qk_norm_bwd", "relpos_workspace_bytes", "relpos_fwd",
              "relpos_bwd")
     host.bind(*(ctypes.cast(getattr(lib, f"triattn_{n}"), ctypes.c_void_p).value for n in names))
