@@ -21,7 +21,7 @@ parameter's dtype (BF16 projection matrices, FP32 LayerNorm parameters).
 - ``clip_grad_norm_``: clips the gradients of a model's parameters by their
   global norm, in place.
 - ``orthogonalize_grads_``: orthogonalises the gradients of its matrices, in
-  place.
+  place; ``matrix_parameters``: which of a model's parameters those are.
 
 Forward and backward may be captured into a CUDA graph.  Before a backward is
 captured, drop what holds an eager autograd graph of the same parameters (a
@@ -209,6 +209,8 @@ class QKNorm(torch.nn.Module):
     with "none".  ``shared``: one weight [D] for all heads.  ``positions``
     (optional) [B, N] int32, the token's index if None.  Returns (q, k)."""
 
+    NOT_MATRICES = ("w_q", "w_k")  # a vector for each head
+
     def __init__(self, n_heads: int, head_dim: int, rotary: str = "half", theta: float = 10000.0, eps: float = 1e-6,
                  shared: bool = False, device=None):
         super().__init__()
@@ -233,6 +235,8 @@ class RelativePosition(torch.nn.Module):
     pairs of different chains, whose indices [B, N] int32 each call then takes.
     ``positions`` (optional) [B, N] int32, the token's index if None.  Without
     ``base`` the bias alone, for the B and N of ``positions``."""
+
+    NOT_MATRICES = ("table",)  # a vector for each bucket
 
     def __init__(self, features: int, layout: str = "heads", kind: str = "clip", max_distance: int = 32,
                  buckets: Optional[int] = None, chains: bool = False, device=None):
@@ -267,13 +271,30 @@ def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0) -> torc
     return T.triattn_clip_grad_norm([p.grad for p in parameters if p.grad is not None], max_norm, norm_type)
 
 
+def matrix_parameters(module: torch.nn.Module) -> list:
+    """The parameters of ``module`` that are matrices of a product: 2-D, but not the
+    weights of ``QKNorm`` (a vector for each head), the table of
+    ``RelativePosition`` and those of embeddings (a vector for each row), and not
+    what another module names in its ``NOT_MATRICES``."""
+    skip = set()
+    for m in module.modules():
+        rows = ("weight",) if isinstance(m, (torch.nn.Embedding, torch.nn.EmbeddingBag)) else ()
+        names = getattr(m, "NOT_MATRICES", rows)
+        skip.update(id(p) for n, p in m.named_parameters(recurse=False) if n in names)
+    return [p for p in module.parameters() if p.dim() == 2 and id(p) not in skip]
+
+
 def orthogonalize_grads_(parameters, steps: int = 5, *, coefficients=T.ORTHOGONALIZE, eps: float = 1e-7) -> None:
-    """Replace the gradients of the matrices among ``parameters`` (2-D, BF16 and
-    FP32) by their orthogonalised ones (Newton-Schulz products, rounded to BF16),
-    in place.  Parameters of other dimensions or without a gradient stay as they
-    are.  Captured into a graph, it keeps the gradients' addresses, as
+    """Replace gradients of matrices (BF16 and FP32) by their orthogonalised ones
+    (Newton-Schulz products, rounded to BF16), in place.  ``parameters`` is a model,
+    of which the ``matrix_parameters`` are taken, or parameters, of which every 2-D
+    one is, whatever it stands for: the heads' weights of a ``QKNorm``, a bias table
+    and an embedding are 2-D as well, so hand over the model, or the matrices alone.
+    Parameters of other dimensions or without a gradient stay as they are.  Captured into a graph, it keeps the gradients' addresses, as
     clip_grad_norm_ does.  To orthogonalise running means of gradients, hand
     those to ``triattn.triattn_orthogonalize``."""
+    if isinstance(parameters, torch.nn.Module):
+        parameters = matrix_parameters(parameters)
     parameters = [parameters] if isinstance(parameters, torch.Tensor) else parameters
     grads = [p.grad for p in parameters if p.grad is not None and p.dim() == 2]
     if not grads:
