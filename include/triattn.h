@@ -797,7 +797,9 @@ int triattn_trace_read(triattn_trace_entry* out, int max_entries);
 /*
  * Test hook, off by default.  While `on` is nonzero, the forward kernel's
  * producer warp skips its first K-tile load, so nothing ever completes the
- * barrier the MMA warp waits on: the bounded wait runs out, the kernel
+ * barrier the MMA warp waits on, and so does the first CTA of the
+ * orthogonalisation of matrices of at most 128 rows (or columns) and of the
+ * table's gradient from pair features: the bounded wait runs out, the kernel
  * records TRIATTN_ERR_TIMEOUT in the device status word and every CTA
  * returns.  Used only to test timeout reporting (with a short limit set by
  * triattn_set_wait_limit_ns); outputs of such a call are undefined.

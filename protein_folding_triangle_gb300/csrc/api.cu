@@ -260,6 +260,7 @@ WaitCtl current_wait_ctl() {
   int dev = 0;
   WaitCtl wc;
   wc.limit_ns = g_wait_limit_ns.load();
+  wc.starve = g_test_starve.load();
   wc.status = (init_device(&dev) == TRIATTN_OK) ? g_status_ptr[dev] : nullptr;
   return wc;
 }

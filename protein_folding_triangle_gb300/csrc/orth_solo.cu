@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) orth_solo_kernel(const OrthMat* m
           if (!mbar_wait(&bars.saved, (pass - 2) & 1, wc, abort)) break;
           fence_proxy_async_all();
         }
+        if (wc.starve != 0 && blockIdx.x == 0 && g == 0) continue;
         mbar_expect_tx(&bars.full[slot], kOrthTile);
         bulk_load(ring + slot * kOrthTile, xt + static_cast<size_t>(c) * kOrthTile, kOrthTile, &bars.full[slot]);
       }

@@ -16,6 +16,7 @@ constexpr uint32_t kDevTimeout = 1u;
 struct WaitCtl {
   unsigned long long limit_ns;  // per-wait limit
   uint32_t* status;             // device status word (global)
+  int starve = 0;               // test hook: a load that others wait for is left out
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

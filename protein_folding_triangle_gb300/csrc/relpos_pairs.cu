@@ -104,10 +104,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const
       int stage = 0, phase = 0;
       for (int k = 0; k < n; ++k) {
         if (!mbar_wait(&bars.empty[stage], phase ^ 1, p.wc, abort)) break;
-        mbar_expect_tx(&bars.full[stage], boxes * kBlk * 128);
-        for (int x = 0; x < boxes; ++x)
-          tma_load_3d(sm + stage * p.stage_bytes + x * kBlk * 128, &tm, &bars.full[stage], 64 * x,
-                      static_cast<int>((b0 + k) * kBlk), 0);
+        if (p.wc.starve == 0 || blockIdx.x != 0 || k != 0) {
+          mbar_expect_tx(&bars.full[stage], boxes * kBlk * 128);
+          for (int x = 0; x < boxes; ++x)
+            tma_load_3d(sm + stage * p.stage_bytes + x * kBlk * 128, &tm, &bars.full[stage], 64 * x,
+                        static_cast<int>((b0 + k) * kBlk), 0);
+        }
         if (++stage == p.stages) { stage = 0; phase ^= 1; }
       }
     }

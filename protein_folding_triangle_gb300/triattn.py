@@ -546,7 +546,8 @@ def trace_read() -> dict:
 
 
 def test_set_starve(on: bool) -> None:
-    """Test hook: starve the forward's MMA warp so its bounded wait runs out."""
+    """Test hook: starve the MMA warp of the forward, of small matrices' orthogonalisation and of the
+    table's gradient from pair features, so that its bounded wait runs out."""
     load().triattn_test_set_starve(1 if on else 0)
 
 
