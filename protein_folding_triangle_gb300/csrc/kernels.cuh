@@ -223,6 +223,8 @@ struct Sum2 {
     c += x.y;
   }
   __device__ __forceinline__ float2 pair() const { return make_float2(s, c); }
+  // s alone once it is not finite: what is rounded off of that is not a number
+  __device__ __forceinline__ float value() const { return fabsf(s) <= 3.402823466e38f ? s + c : s; }
 };
 
 // Launch of a kernel that starts with after_previous(): its blocks may come up

@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* part, flo
       sh[threadIdx.x] = v.pair();
     }
   }
-  if (lane == 0) (blockIdx.y ? dwk : dwq)[static_cast<size_t>(h) * D + d] = v.s + v.c;
+  if (lane == 0) (blockIdx.y ? dwk : dwq)[static_cast<size_t>(h) * D + d] = v.value();
 }
 
 struct Plan {

@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(1024) relpos_sum_kernel(const float* part, flo
   __syncthreads();
   if (slice == 0 && k < buckets) {
     for (int s = 1; s < 32; ++s) v.add(sh[s][lane]);
-    out[static_cast<size_t>(k) * F + blockIdx.y] = v.s + v.c;
+    out[static_cast<size_t>(k) * F + blockIdx.y] = v.value();
   }
 }
 
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(32 * S) relpos_flat_sum_kernel(const float* pa
     Sum2 w;
 #pragma unroll
     for (int s = 0; s < S; ++s) w.add(sh[s][slice][lane]);
-    out[4 * static_cast<size_t>(x) + slice] = w.s + w.c;
+    out[4 * static_cast<size_t>(x) + slice] = w.value();
   }
 }
 
