@@ -664,8 +664,8 @@ triattn_status triattn_qk_norm_bwd(const triattn_qk_norm_shape* shape, const voi
  * BF16, rounded once; d_out BF16 or FP32; positions, chains optional.  All
  * contiguous, 16-byte aligned; positions, chains and d_table 4-byte aligned.
  * out may be base; otherwise outputs must not overlap inputs.  The gradient of
- * base is d_out.  d_out has to be finite (a value that is not may make other
- * buckets of its column NaN).  Sums are FP32, joined in pairs of FP32, in a fixed order:
+ * base is d_out.  A value of d_out that is not finite is part of its bucket's sum
+ * alone.  Sums are FP32, joined in pairs of FP32, in a fixed order:
  * bitwise reproducible.  workspace (backward):
  * triattn_relpos_workspace_bytes(shape) bytes, 256-byte aligned, contents
  * ignored.

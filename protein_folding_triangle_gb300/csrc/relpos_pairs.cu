@@ -26,7 +26,9 @@
 //              the next stage while they wait for this one), then the two bytes of
 //              its one in B [buckets, 64 pairs] (K-major, swizzled), after the one
 //              that the stage held before is put out.
-// At the end eight warps add the accumulators and write the run's partial table.
+// At the end eight warps add the accumulators and write the run's partial table.  A value
+// that is not finite makes all buckets of its feature NaN in the product (0 x inf); the
+// run's sums of such a feature are then added up one by one.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -54,11 +56,41 @@ struct PairsBwd {
   int nb, mt, sets, stages;     // buckets to 16, 128-feature tiles, accumulators per tile, ring stages
   int groups;                   // that place the ones, a divisor of the stages: a stage's ones are always one group's
   int stage_bytes, a_bytes;
+  const uint16_t* d_out;
   WaitCtl wc;
 };
 
 constexpr int kGroups = 4;  // of two warps that place the ones
 constexpr int kPairThreads = 64 + 64 * kGroups;
+
+// Sums of feature f over the pairs [q0, q1) of the 16 buckets from k0 on, into `out`, by
+// one thread; `cell` is its place in shared memory, sums 128 apart.
+__device__ __noinline__ void add_one_by_one(const RelposArgs& a, const uint16_t* d_out, const uint8_t* lut, long long q0,
+                                            long long q1, int f, int k0, float2* cell, float* out) {
+  for (int e = 0; e < 16; ++e) cell[128 * e] = make_float2(0.f, 0.f);
+  const long long NN = static_cast<long long>(a.N) * a.N;
+  int b = static_cast<int>(q0 / NN), i = static_cast<int>((q0 - b * NN) / a.N);
+  int j = static_cast<int>(q0 - b * NN - static_cast<long long>(i) * a.N);
+  for (long long q = q0; q < q1; ++q) {
+    const size_t at = static_cast<size_t>(b) * a.N;
+    const bool other = a.chain != nullptr && __ldg(a.chain + at + i) != __ldg(a.chain + at + j);
+    const int k = (other ? a.buckets - 1 : lut[distance(a.position(b, i), a.position(b, j), a.R)]) - k0;
+    if (k >= 0 && k < 16) {
+      Sum2 v{cell[128 * k].x, cell[128 * k].y};
+      v.add(bf16lo_to_f32(__ldg(d_out + q * a.F + f)));
+      cell[128 * k] = v.pair();
+    }
+    if (++j == a.N) {
+      j = 0;
+      if (++i == a.N) {
+        i = 0;
+        ++b;
+      }
+    }
+  }
+  for (int e = 0; e < 16 && k0 + e < a.buckets; ++e)
+    out[static_cast<size_t>(k0 + e) * a.F + f] = Sum2{cell[128 * e].x, cell[128 * e].y}.value();
+}
 
 __global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const __grid_constant__ CUtensorMap tm,
                                                                   const __grid_constant__ RelposArgs a, PairsBwd p) {
@@ -193,6 +225,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const
     const int used = min(n, p.sets);
     for (int m = 0; m < p.mt; ++m) {
       const int f = m * 128 + (warp & 3) * 32 + lane;
+      float worst = 0.f;  // not finite where a sum is not
       for (int k0 = warp < 4 ? 0 : 16; k0 < p.nb; k0 += 32) {
         float v[16];
 #pragma unroll
@@ -204,8 +237,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) relpos_pairs_bwd_kernel(const
           for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(r[e]);
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
+        for (int e = 0; e < 16; ++e) {
+          worst += 0.f * v[e];
           if (f < a.F && k0 + e < a.buckets) out[static_cast<size_t>(k0 + e) * a.F + f] = v[e];
+        }
+      }
+      if (f < a.F && worst != 0.f) {  // the ring's memory: all products are done
+        float2* cell = reinterpret_cast<float2*>(sm) + (warp < 4 ? 0 : 16 * 128) + (warp & 3) * 32 + lane;
+        for (int k0 = warp < 4 ? 0 : 16; k0 < a.buckets; k0 += 32)
+          add_one_by_one(a, p.d_out, lut, b0 * kBlk, min(b1 * kBlk, p.P), f, k0, cell, out);
       }
     }
   }
@@ -243,6 +283,7 @@ cudaError_t launch_relpos_pairs_bwd(const RelposArgs& a, const void* d_out, int 
   p.stages = std::min(kStagesMax, (kSmemMax - 1024) / p.stage_bytes);
   p.groups = p.stages >= kGroups ? kGroups : 2;
   p.stages -= p.stages % p.groups;
+  p.d_out = static_cast<const uint16_t*>(d_out);
   p.wc = wc;
   CUtensorMap tm;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.F), static_cast<cuuint64_t>(p.P), 1};

@@ -77,6 +77,37 @@ def test_planes(B, N, F, fp32):
     check_table("heads", d, *ids(B, N), 66, 32)
 
 
+@pytest.mark.parametrize("B,N,F,K", [(1, 9, 8, 18), (2, 40, 64, 66), (1, 131, 136, 66), (1, 75, 256, 202),
+                                     (1, 400, 128, 66)])
+def test_pair_features(B, N, F, K):
+    d = torch.randn(B, N, N, F, generator=torch.Generator().manual_seed(N)).bfloat16()
+    check_table("pairs", scatter(d, "pairs", N).cuda(), *ids(B, N), K, (K - 2) // 2)
+
+
+def test_pair_features_that_are_all_broken():
+    d = torch.full((1, 90, 90, 16), INF, dtype=torch.bfloat16, device="cuda")
+    d[..., 8:] = NAN
+    pos, chain = ids(1, 90)
+    got = T.triattn_relpos_bwd(d, 18, pos, chain, layout="pairs", max_distance=8)
+    assert T.device_status() == T.OK
+    assert bool((got[:, :8] == INF).all()) and bool(torch.isnan(got[:, 8:]).all())
+
+
+def test_pair_features_whose_sum_overflows():
+    """Finite values whose sum FP32 does not hold: an infinity in their bucket, the others as they are."""
+    g = torch.Generator().manual_seed(6)
+    d = torch.randn(1, 70, 70, 24, generator=g).bfloat16()
+    pos, chain = ids(1, 70)
+    k = CI.buckets(1, 70, 18, pos.cpu().numpy(), chain.cpu().numpy(), "clip", 8)[0]
+    i, j = np.argwhere(k == 3)[:2].T
+    d[0, i, j, 5] = 3e38
+    got = cpu64(T.triattn_relpos_bwd(d.cuda(), 18, pos, chain, layout="pairs", max_distance=8))
+    want, size = table_sums(d, k[None], 18, "pairs")
+    assert got[3, 5] == INF
+    got[3, 5] = want[3, 5]
+    assert np.all(np.abs(got - want) <= 528 * 2.0 ** -23 * size)
+
+
 @pytest.mark.parametrize("shared", [False, True])
 def test_norm_weights(shared):
     """An infinite gradient of one element: its feature's sum is not finite, the others are as without it."""
