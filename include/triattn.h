@@ -716,7 +716,8 @@ triattn_status triattn_relpos_bwd(const triattn_relpos_shape* shape, const void*
  * DEVICE matrices, `stride` elements between rows, BF16 or FP32 (out: BF16),
  * aligned to their element; out[i] has the sizes of matrices[i] and may share
  * memory with any of `matrices` (all are read before the first is written), not
- * with another out.  Matrices without elements are skipped.  Sides up to 65536,
+ * with another out, of which it may lie beside in the same rows (blocks of columns
+ * of one matrix, with its stride).  Matrices without elements are skipped.  Sides up to 65536,
  * 1 to 64 steps, at most 2^20 matrices, and tiles of 2^31 in all.
  * TRIATTN_ERR_INVALID_ARG: a NULL or misaligned pointer, a negative size, a stride
  * below cols, outputs that overlap or do not match, steps < 1, eps or a

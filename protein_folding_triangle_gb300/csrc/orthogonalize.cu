@@ -733,6 +733,39 @@ bool plan_of(const triattn_matrix* in, const triattn_matrix* out, long long n, P
   return true;
 }
 
+// Whether no two outputs share an element, as far as it can be told from where they
+// start: ranges of memory that meet are those of blocks of columns of the same rows,
+// apart by their columns (the parts of a fused projection), or they are taken to.
+bool outputs_apart(const triattn_matrix* out, long long n) {
+  struct Span {
+    uintptr_t lo, hi;  // bytes
+    uintptr_t row, step;
+  };
+  std::vector<Span> dst, open;  // open: those that may reach beyond the next one's start
+  dst.reserve(static_cast<size_t>(n));
+  for (long long i = 0; i < n; ++i) {
+    if (!dims_ok(out[i])) continue;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(out[i].data), row = 2 * static_cast<uintptr_t>(out[i].cols);
+    const uintptr_t step = out[i].rows > 1 ? 2 * static_cast<uintptr_t>(out[i].stride) : row;
+    dst.push_back({a, a + static_cast<uintptr_t>(out[i].rows - 1) * step + row, row, out[i].rows > 1 ? step : 0});
+  }
+  std::sort(dst.begin(), dst.end(), [](const Span& x, const Span& y) { return x.lo < y.lo; });
+  for (const Span& y : dst) {
+    size_t kept = 0;
+    for (const Span& x : open) {
+      if (x.hi <= y.lo) continue;
+      const uintptr_t step = std::max(x.step, y.step);
+      if (step == 0 || (x.step != 0 && y.step != 0 && x.step != y.step)) return false;
+      const uintptr_t col = (y.lo - x.lo) % step;  // y's first column, counted from x's, in x's rows
+      if (col < x.row || col + y.row > step) return false;
+      open[kept++] = x;
+    }
+    open.resize(kept);
+    open.push_back(y);
+  }
+  return true;
+}
+
 constexpr long long kMaxSide = 65536;
 
 triattn_status check_list(const triattn_matrix* ms, long long n, bool output) {
@@ -845,19 +878,7 @@ triattn_status triattn_orthogonalize(const triattn_matrix* matrices, const triat
   try {
     // outputs are written without an order between them; every input is read
     // before the first of them
-    struct Span {
-      uintptr_t lo, hi;
-    };
-    std::vector<Span> dst;
-    dst.reserve(static_cast<size_t>(n));
-    for (long long i = 0; i < n; ++i)
-      if (dims_ok(out[i])) {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(out[i].data);
-        dst.push_back({a, a + 2 * static_cast<uintptr_t>((out[i].rows - 1) * out[i].stride + out[i].cols)});
-      }
-    std::sort(dst.begin(), dst.end(), [](const Span& x, const Span& y) { return x.lo < y.lo; });
-    for (size_t i = 1; i < dst.size(); ++i)
-      if (dst[i].lo < dst[i - 1].hi) return TRIATTN_ERR_INVALID_ARG;
+    if (!outputs_apart(out, n)) return TRIATTN_ERR_INVALID_ARG;
     Plan p;
     if (!plan_of(matrices, out, n, &p)) return TRIATTN_ERR_UNSUPPORTED;
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
