@@ -708,7 +708,7 @@ triattn_status triattn_relpos_bwd(const triattn_relpos_shape* shape, const void*
  * singular vectors with singular values near 1 for coefficients such as 3.4445,
  * -4.7750, 2.0315 and five steps.  The products' operands are pairs of FP16
  * values (22 bits, down to 2^-33), sums are FP32, those of the norm's squares FP64
- * above runs of 4096 elements; out is rounded once.  Coefficients have to keep
+ * above runs of 4096 elements (throughout where FP32 does not hold the squares); out is rounded once.  Coefficients have to keep
  * every element of X, A, c A + b I and B + a I below 255; a matrix that is not
  * finite gives an out that is not.
  *

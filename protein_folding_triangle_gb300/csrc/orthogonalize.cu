@@ -113,8 +113,9 @@ __device__ __forceinline__ void elements8(const OrthMat& q, long long at, float 
 __device__ __forceinline__ bool on16(const OrthMat& q) { return (reinterpret_cast<uintptr_t>(q.src) & 15) == 0; }
 
 // Sums of squares, one partial per kNormPart elements of the source in the order of
-// its rows.  A short list's table is a parameter, whose rows the first blocks put where
-// the later kernels look for them.
+// its rows: in FP32, and again in FP64 where FP32 does not hold the squares.  A short
+// list's table is a parameter, whose rows the first blocks put where the later kernels
+// look for them.
 constexpr int kNormPart = 4096;
 template <bool PARAM>
 __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ OrthTable t, OrthView v, OrthMat* to) {
@@ -127,6 +128,16 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ 
   const OrthMat q = mat[find<&OrthMat::part0>(mat, PARAM ? t.n : v.n, blockIdx.x)];
   const int rows = (q.flags & kOrthTall) ? q.n : q.m, cols = (q.flags & kOrthTall) ? q.m : q.n;
   const long long n = static_cast<long long>(rows) * cols, e0 = static_cast<long long>(blockIdx.x - q.part0) * kNormPart;
+  auto each = [&](int first, int step, auto&& f) {  // of the part's elements
+    const int m = static_cast<int>(min(static_cast<long long>(kNormPart), n - e0));
+    const long long r0 = e0 / cols;
+    const int c0 = static_cast<int>(e0 - r0 * cols);
+#pragma unroll 8
+    for (int i = first; i < m; i += step) {
+      const int r = (c0 + i) / cols;
+      f(element(q, (r0 + r) * q.ld_src + (c0 + i - r * cols)));
+    }
+  };
   float s = 0.f;
   if (q.ld_src == cols && on16(q) && e0 + kNormPart <= n) {
 #pragma unroll
@@ -137,25 +148,23 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ 
       for (int k = 0; k < 8; ++k) s += y[k] * y[k];
     }
   } else {
-    const int m = static_cast<int>(min(static_cast<long long>(kNormPart), n - e0));
-    const long long r0 = e0 / cols;
-    const int c0 = static_cast<int>(e0 - r0 * cols);
-#pragma unroll 8
-    for (int i = threadIdx.x; i < m; i += 256) {
-      const int r = (c0 + i) / cols;
-      const float x = element(q, (r0 + r) * q.ld_src + (c0 + i - r * cols));
-      s += x * x;
-    }
+    each(threadIdx.x, 256, [&](float x) { s += x * x; });
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    s = 0.f;
-    for (int w = 0; w < 8; ++w) s += sh[w];
-    v.part[blockIdx.x] = s;
+  if (threadIdx.x >= 32) return;
+  s = 0.f;
+  for (int w = 0; w < 8; ++w) s += sh[w];
+  double d = s;
+  if (!(s >= 0x1p-80f && s <= 0x1p126f)) {  // by one warp: FP32's range ends near it
+    d = 0.0;
+    each(threadIdx.x, 32, [&](float x) { d += static_cast<double>(x) * x; });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
   }
+  if (threadIdx.x == 0) v.part[blockIdx.x] = d;
 }
 
 // Eight elements of X from (row, col) on, zero outside it: loaded from the nearest
@@ -181,7 +190,7 @@ __device__ __forceinline__ void gather8(const OrthMat& q, int row, int col, floa
 // One tile of X per block: normed, scaled, split, in the image's order.
 __global__ void __launch_bounds__(256) orth_load_kernel(OrthView v, float eps) {
   __shared__ double sh[8];
-  __shared__ float scaled;
+  __shared__ float scaled[2];
   let_next_start();
   after_previous();
   const OrthMat q = v.mat[find<&OrthMat::tiles0>(v.mat, v.n, blockIdx.x)];
@@ -212,16 +221,23 @@ __global__ void __launch_bounds__(256) orth_load_kernel(OrthView v, float eps) {
   if (threadIdx.x == 0) {
     double s = sh[0];
     for (int w = 1; many && w < 8; ++w) s += sh[w];
-    scaled = kOrthScale / (sqrtf(static_cast<float>(s)) + eps);
+    if (s >= 0x1p-100 && s <= 0x1p126) {
+      scaled[0] = 1.f;
+      scaled[1] = kOrthScale / (sqrtf(static_cast<float>(s)) + eps);
+    } else {  // in two factors, so that neither leaves FP32's range
+      const double norm = sqrt(s) + eps, first = norm > 0x1p60 ? 0x1p-64 : norm < 0x1p-60 ? 0x1p64 : 1.0;
+      scaled[0] = static_cast<float>(first);
+      scaled[1] = static_cast<float>(kOrthScale / (norm * first));
+    }
   }
   __syncthreads();
-  const float scale = scaled;
+  const float first = scaled[0], scale = scaled[1];
   uint8_t* out = tile_at(v, q.x[0] + t);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int e = threadIdx.x + 256 * u, r = tall ? e & 127 : e >> 3, p = tall ? e >> 7 : e & 7;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[u][j] *= scale;
+    for (int j = 0; j < 8; ++j) y[u][j] = y[u][j] * first * scale;
     uint4 hi, lo;
     split8(y[u], hi, lo);
     *reinterpret_cast<uint4*>(out + sw128(r, p)) = hi;
@@ -728,7 +744,7 @@ bool plan_of(const triattn_matrix* in, const triattn_matrix* out, long long n, P
   auto up = [](size_t x) { return (x + 1023) / 1024 * 1024; };
   p->done_off = up(p->mats.size() * sizeof(OrthMat));
   p->part_off = up(p->done_off + p->mats.size() * 4);
-  p->tiles_off = up(p->part_off + static_cast<size_t>(p->parts) * 4);
+  p->tiles_off = up(p->part_off + static_cast<size_t>(p->parts) * sizeof(double));
   p->total = p->tiles_off + static_cast<size_t>(p->tiles) * kOrthTile;
   return true;
 }
@@ -808,7 +824,7 @@ cudaError_t launch_gemm(const OrthView& v, const OrthRun& st, cudaStream_t s) {
 
 cudaError_t run(const Plan& p, int steps, const float* co, float eps, uint8_t* ws, const WaitCtl& wc, cudaStream_t s) {
   OrthMat* mats = reinterpret_cast<OrthMat*>(ws);
-  OrthView v{mats, reinterpret_cast<float*>(ws + p.part_off), ws + p.tiles_off,
+  OrthView v{mats, reinterpret_cast<double*>(ws + p.part_off), ws + p.tiles_off,
              reinterpret_cast<uint32_t*>(ws + p.done_off),
              static_cast<int>(p.mats.size())};
   OrthTable t;

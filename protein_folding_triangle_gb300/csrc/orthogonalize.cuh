@@ -29,7 +29,7 @@ constexpr int kOrthFp32 = 1, kOrthTall = 2;
 
 struct OrthView {
   const OrthMat* mat;
-  float* part;
+  double* part;
   uint8_t* tiles;
   uint32_t* done;  // tiles (by warps) that have been stored, of every larger matrix
   int n;
