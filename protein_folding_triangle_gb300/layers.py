@@ -114,12 +114,19 @@ class QKNormFunction(torch.autograd.Function):
                                        theta=ctx.theta, eps=ctx.eps), None, None, None, None)
 
 
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """``t``, or a copy that is contiguous and starts on 16 bytes: a part of a batch of
+    planes of an odd number of tokens does not."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class RelativePositionFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, table, base, positions, chains, layout: str, kind: str, max_distance: int):
         if base is not None:
-            base = base.contiguous()
-        out = T.triattn_relpos_fwd(table, base, positions, chains, layout=layout, kind=kind, max_distance=max_distance)
+            base = _aligned(base)
+        out = T.triattn_relpos_fwd(_aligned(table), base, positions, chains, layout=layout, kind=kind, max_distance=max_distance)
         ctx.save_for_backward(positions, chains)
         ctx.buckets, ctx.how = table.shape[0], dict(layout=layout, kind=kind, max_distance=max_distance)
         return out
@@ -130,7 +137,7 @@ class RelativePositionFunction(torch.autograd.Function):
         positions, chains = ctx.saved_tensors
         d_table = None
         if ctx.needs_input_grad[0]:
-            d_table = T.triattn_relpos_bwd(d_out.contiguous(), ctx.buckets, positions, chains, **ctx.how)
+            d_table = T.triattn_relpos_bwd(_aligned(d_out), ctx.buckets, positions, chains, **ctx.how)
         return d_table, d_out if ctx.needs_input_grad[1] else None, None, None, None, None, None
 
 
