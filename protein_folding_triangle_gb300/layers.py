@@ -91,16 +91,36 @@ class TransitionFunction(torch.autograd.Function):
 
 
 def _rows(t: torch.Tensor) -> bool:
-    """Whether a [B, N_o, H, N, D] view is one of rows that the kernels take as it is."""
-    return (t.dim() == 5 and t.stride(4) == 1 and (t.shape[0] == 1 or t.stride(0) == t.shape[1] * t.stride(1))
-            and all(s > 0 and s % 8 == 0 for s in t.stride()[1:4]) and t.data_ptr() % 16 == 0)
+    """Whether a [B, N_o, H, N, D] view is one of rows that the kernels take as it is:
+    the rules of tri_attn_fwd_strided."""
+    if t.dim() != 5 or t.stride(4) != 1 or t.data_ptr() % 16:
+        return False
+    B, No, H, N, D = t.shape
+    example, piece, head, row = t.stride()[:4]
+    if (B > 1 and example != No * piece) or not all(s > 0 and s % 8 == 0 for s in (piece, head, row)):
+        return False
+    if head < row or (head == row and H == 1):  # heads inside a row
+        inner, n_inner, outer, n_outer = head, H, row, N
+    elif piece == H * head and (head != row or N == 1):
+        inner, n_inner, outer, n_outer = row, N, head, H
+    else:
+        return False
+    width = (n_inner - 1) * inner + D
+    return inner >= D and width <= outer and (n_outer - 1) * outer + width <= piece < 1 << 36
+
+
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """``t``, or a copy that is contiguous and starts on 16 bytes: a part of a batch of
+    planes of an odd number of tokens does not."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
 class QKNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, w_q, w_k, positions, rotary: str, theta: float, eps: float):
         if q.stride() != k.stride() or not (_rows(q) and _rows(k)):
-            q, k = q.contiguous(), k.contiguous()
+            q, k = _aligned(q), _aligned(k)
         out = T.triattn_qk_norm_fwd(q, k, w_q, w_k, positions, rotary, theta=theta, eps=eps)
         ctx.save_for_backward(q, k, w_q, w_k, positions)
         ctx.rotary, ctx.theta, ctx.eps = rotary, theta, eps
@@ -110,15 +130,8 @@ class QKNormFunction(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, d_q, d_k):
         q, k, w_q, w_k, positions = ctx.saved_tensors
-        return (*T.triattn_qk_norm_bwd(q, k, w_q, w_k, d_q.contiguous(), d_k.contiguous(), positions, ctx.rotary,
+        return (*T.triattn_qk_norm_bwd(q, k, w_q, w_k, _aligned(d_q), _aligned(d_k), positions, ctx.rotary,
                                        theta=ctx.theta, eps=ctx.eps), None, None, None, None)
-
-
-def _aligned(t: torch.Tensor) -> torch.Tensor:
-    """``t``, or a copy that is contiguous and starts on 16 bytes: a part of a batch of
-    planes of an odd number of tokens does not."""
-    t = t.contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
 class RelativePositionFunction(torch.autograd.Function):
