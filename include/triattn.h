@@ -578,7 +578,8 @@ triattn_status triattn_clip_grad_norm(const triattn_tensor* tensors, const triat
  * (y_a, y_b) = (u_a cos - u_b sin, u_a sin + u_b cos).  TRIATTN_ROTARY_HALF:
  * pairs (i, i + D/2); TRIATTN_ROTARY_INTERLEAVED: pairs (2i, 2i + 1);
  * TRIATTN_ROTARY_NONE: no rotation.  pos is positions[b, n], or n where
- * positions is NULL; angles are right to 5e-7 for every 32-bit position.
+ * positions is NULL; angles are right to 5e-7 for every 32-bit position and theta of
+ * at least 1 (below, the error grows as 1 / theta).
  * Statistics and sums are FP32, each output is rounded once.  The backward
  * computes everything again from q and k.
  *
@@ -707,7 +708,7 @@ triattn_status triattn_relpos_bwd(const triattn_relpos_shape* shape, const void*
  * (X^T X and X B for a matrix of more rows than columns), then out = X: G's
  * singular vectors with singular values near 1 for coefficients such as 3.4445,
  * -4.7750, 2.0315 and five steps.  The products' operands are pairs of FP16
- * values (22 bits, down to 2^-33), sums are FP32, those of the norm's squares FP64
+ * values (22 bits; X down to 2^-33, A and the polynomials in it to 2^-25), sums are FP32, those of the norm's squares FP64
  * above runs of 4096 elements (throughout where FP32 does not hold the squares); out is rounded once.  Coefficients have to keep
  * every element of X, A, c A + b I and B + a I below 255; a matrix that is not
  * finite gives an out that is not.

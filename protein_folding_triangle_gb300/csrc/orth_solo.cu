@@ -17,7 +17,7 @@
 // theirs are written (one copy of a band to all CTAs of the team: 64 us for the ten
 // matrices of a block, so 65).
 //
-// 480 matrices of 48 blocks of 128 features: 223 us, tensor pipe active 43 %; the ten
+// 480 matrices of 48 blocks of 128 features: 221 us, tensor pipe active 44 %; the ten
 // of one block, teams of eight: 58 us, 11 us a step, most of it the team's sum.
 //
 //   warp 0      loads of X's chunks (ring of five)

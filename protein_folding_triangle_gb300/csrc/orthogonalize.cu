@@ -12,9 +12,14 @@
 // is hi hi + hi lo + lo hi in one FP32 accumulator.  Single BF16 operands, as
 // such updates are often computed, are off by 3 % of the result after five steps
 // and by 80 % where a matrix has few directions (what rounding adds beside them
-// is multiplied by a, 3.4, in every step); pairs of BF16 by up to 8e-4, pairs of
-// FP16 by no more than FP32 products (3e-5).  The scale keeps both halves of the
-// small values out of FP16's subnormals; the largest value is 255.
+// is multiplied by a, 3.4, in every step); pairs of BF16 by up to 8e-4.  Pairs of
+// FP16 stay within two to four times the error of FP32 products: with exact sums 2.4e-6
+// against 6e-7 of the result (128 x 388 and 256 x 1037, noise beside a few directions),
+// 4e-5 against 1.6e-5 (90 x 40 of two directions), 8e-5 against 3e-5 (256 x 300 of one);
+// the one rounding to BF16 is 1.6e-3.  X carries the scale, which keeps its small values
+// out of FP16's subnormals (its floor is 2^-33; the largest value is 255).  A, A' and B'
+// do not: their floor is 2^-25, as small beside their diagonals, which are near one or
+// beside b and a, as what FP32 products of norm one round off.
 //
 // With A' = c A + b I and B' = A' A + a I, a step is three plain products:
 //   1  A = X X^T (and A' from the accumulator),  2  B' = A' A,  3  X <- B' X.
@@ -636,7 +641,9 @@ bool dims_ok(const triattn_matrix& g) { return g.rows > 0 && g.cols > 0; }
 // CTAs per matrix of one row of tiles.  A CTA takes about 1.7 k cycles per chunk
 // of 64 columns and step, and 4 k (alone) or 7 k (in a team, which adds its parts
 // of A) between two passes; the list takes as long as its widest matrix or as its
-// sum spread over the SMs (clusters of eight leave some of a GPC's idle).
+// sum spread over the SMs (clusters of eight leave some of a GPC's idle).  A single wide
+// matrix has eight SMs at most: 128 x 4096 takes 99 us, x 16384 251, x 65536 870, and
+// eight of these 1035 together.
 int team_of(const OrthMat* q, int n) {
   int best = 1;
   double least = 0.0;

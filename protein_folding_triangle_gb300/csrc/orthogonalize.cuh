@@ -38,9 +38,10 @@ __device__ __forceinline__ uint8_t* tile_at(const OrthView& v, int t) {
   return v.tiles + static_cast<size_t>(t) * kOrthTile;
 }
 
-// Eight scaled values as FP16 pairs, one 16-byte piece of each plane: hi is the
-// value's leading 11 bits (cut off, so that no conversion back is needed), lo the
-// rest rounded.
+// Eight values as FP16 pairs, one 16-byte piece of each plane: hi is the value's
+// leading 11 bits (cut off, so that no conversion back is needed), lo the rest
+// rounded.  Below 2^-14 FP16 has fewer bits and rounds hi as well, to 2^-25 at most,
+// which lo does not see: the floor of a pair is 2^-25 for hi and as much for lo.
 __device__ __forceinline__ void split8(const float* y, uint4& hi, uint4& lo) {
   uint32_t h[4], l[4];
 #pragma unroll

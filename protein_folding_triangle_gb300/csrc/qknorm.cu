@@ -101,7 +101,8 @@ __device__ __forceinline__ float2 neg(float2 x) { return make_float2(-x.x, -x.y)
 
 // cos and sin of position times frequency.  The angle is a whole number of
 // 2^-64 turns, so the product wraps to the turn's fraction exactly and a far
-// position costs no accuracy; its upper 32 bits are half turns times 2^-31.
+// position costs no accuracy (but what the host's FP64 power is off by, times the
+// position: 3e-7 for theta of at least 1); its upper 32 bits are half turns times 2^-31.
 __device__ __forceinline__ void angle(int pos, unsigned long long freq, float& c, float& s) {
   const long long t = static_cast<long long>(static_cast<unsigned long long>(static_cast<long long>(pos)) * freq);
   sincospif(static_cast<float>(static_cast<int>(t >> 32)) * 0x1p-31f, &s, &c);
