@@ -32,6 +32,7 @@ stream fails.
 from __future__ import annotations
 
 import math
+import warnings
 from typing import Optional
 
 import torch
@@ -240,6 +241,7 @@ class QKNorm(torch.nn.Module):
         shape = (head_dim,) if shared else (n_heads, head_dim)
         self.w_q = torch.nn.Parameter(torch.ones(shape, dtype=torch.float32, device=device))
         self.w_k = torch.nn.Parameter(torch.ones(shape, dtype=torch.float32, device=device))
+        self.w_q.not_matrix = self.w_k.not_matrix = True
 
     def forward(self, q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor] = None):
         return QKNormFunction.apply(q, k, self.w_q, self.w_k, positions, self.rotary, self.theta, self.eps)
@@ -272,6 +274,7 @@ class RelativePosition(torch.nn.Module):
         self.layout, self.kind, self.max_distance, self.chains = layout, kind, max_distance, chains
         self.table = torch.nn.Parameter(
             torch.zeros(buckets + (1 if chains else 0), features, dtype=torch.float32, device=device))
+        self.table.not_matrix = True
 
     def forward(self, base: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
                 chains: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -309,14 +312,19 @@ def orthogonalize_grads_(parameters, steps: int = 5, *, coefficients=T.ORTHOGONA
     (Newton-Schulz products, rounded to BF16), in place.  ``parameters`` is a model,
     of which the ``matrix_parameters`` are taken, or parameters, of which every 2-D
     one is, whatever it stands for: the heads' weights of a ``QKNorm``, a bias table
-    and an embedding are 2-D as well, so hand over the model, or the matrices alone.
+    and an embedding are 2-D as well, so hand over the model, or the matrices alone
+    (a weight or table as a module above made it is warned of).
     Parameters of other dimensions or without a gradient stay as they are.  Captured into a graph, it keeps the gradients' addresses, as
     clip_grad_norm_ does.  To orthogonalise running means of gradients, hand
     those to ``triattn.triattn_orthogonalize``."""
     if isinstance(parameters, torch.nn.Module):
         parameters = matrix_parameters(parameters)
     parameters = [parameters] if isinstance(parameters, torch.Tensor) else parameters
-    grads = [p.grad for p in parameters if p.grad is not None and p.dim() == 2]
+    parameters = [p for p in parameters if p.grad is not None and p.dim() == 2]
+    if any(getattr(p, "not_matrix", False) for p in parameters):
+        warnings.warn("lists of vectors (norm weights, a bias table) are orthogonalised as matrices: hand over the "
+                      "model, or matrix_parameters(model)", stacklevel=2)
+    grads = [p.grad for p in parameters]
     if not grads:
         return
     wide = [g for g in grads if g.dtype != torch.bfloat16]

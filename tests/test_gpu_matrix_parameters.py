@@ -1,4 +1,6 @@
 """GPU test of the orthogonalised gradients of a model: its matrices, and nothing else."""
+import warnings
+
 import numpy as np
 import pytest
 import torch
@@ -39,3 +41,20 @@ def test_a_model_keeps_the_gradients_of_its_vectors():
             assert np.linalg.norm(cpu64(p.grad) - want) <= (2.0 ** -8 + 1e-3) * np.linalg.norm(want)
         else:
             assert torch.equal(p.grad, before[n]), n
+
+
+def test_a_list_with_vectors_is_warned_of():
+    """A list is taken as it is, and the caller is told of the vectors in it."""
+    norm, rel = layers.QKNorm(2, 16, device="cuda"), layers.RelativePosition(4, max_distance=4, device="cuda")
+    w = torch.nn.Parameter(torch.randn(8, 9, device="cuda").bfloat16())
+    for p in (norm.w_q, rel.table, w):
+        p.grad = torch.randn_like(p)
+    for ps in ([norm.w_q, w], [rel.table], list(norm.parameters())):
+        with pytest.warns(UserWarning, match="vectors"):
+            layers.orthogonalize_grads_(ps)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        layers.orthogonalize_grads_([w])
+        layers.orthogonalize_grads_(torch.nn.ModuleList([norm, rel]))
+        layers.orthogonalize_grads_([norm.w_k])  # no gradient
+    assert T.device_status() == T.OK
