@@ -708,18 +708,19 @@ triattn_status triattn_relpos_bwd(const triattn_relpos_shape* shape, const void*
  * (X^T X and X B for a matrix of more rows than columns), then out = X: G's
  * singular vectors with singular values near 1 for coefficients such as 3.4445,
  * -4.7750, 2.0315 and five steps.  The products' operands are pairs of FP16
- * values (22 bits; X down to 2^-33, A and the polynomials in it to 2^-25), sums are FP32, those of the norm's squares FP64
- * above runs of 4096 elements (throughout where FP32 does not hold the squares); out is rounded once.  Coefficients have to keep
- * every element of X, A, c A + b I and B + a I below 255; a matrix that is not
- * finite gives an out that is not.
+ * values (22 bits; X down to 2^-33, A and the polynomials in it to 2^-25), sums
+ * are FP32, those of the norm's squares FP64 above runs of 4096 elements
+ * (throughout where FP32 does not hold the squares); out is rounded once.
+ * Coefficients have to keep every element of X, A, c A + b I and B + a I below
+ * 255; a matrix that is not finite gives an out that is not.
  *
  * `matrices` and `out` are HOST arrays, read before the call returns: row-major
  * DEVICE matrices, `stride` elements between rows, BF16 or FP32 (out: BF16),
  * aligned to their element; out[i] has the sizes of matrices[i] and may share
  * memory with any of `matrices` (all are read before the first is written), not
  * with another out, of which it may lie beside in the same rows (blocks of columns
- * of one matrix, with its stride).  Matrices without elements are skipped.  Sides up to 65536,
- * 1 to 64 steps, at most 2^20 matrices, and tiles of 2^31 in all.
+ * of one matrix, with its stride).  Matrices without elements are skipped.  Sides
+ * up to 65536, 1 to 64 steps, at most 2^20 matrices, and tiles of 2^31 in all.
  * TRIATTN_ERR_INVALID_ARG: a NULL or misaligned pointer, a negative size, a stride
  * below cols, outputs that overlap or do not match, steps < 1, eps or a
  * coefficient that is not finite, eps <= 0.  TRIATTN_ERR_UNSUPPORTED: another

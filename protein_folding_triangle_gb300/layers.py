@@ -140,7 +140,8 @@ class RelativePositionFunction(torch.autograd.Function):
     def forward(ctx, table, base, positions, chains, layout: str, kind: str, max_distance: int):
         if base is not None:
             base = _aligned(base)
-        out = T.triattn_relpos_fwd(_aligned(table), base, positions, chains, layout=layout, kind=kind, max_distance=max_distance)
+        out = T.triattn_relpos_fwd(_aligned(table), base, positions, chains, layout=layout, kind=kind,
+                                   max_distance=max_distance)
         ctx.save_for_backward(positions, chains)
         ctx.buckets, ctx.how = table.shape[0], dict(layout=layout, kind=kind, max_distance=max_distance)
         return out
@@ -314,9 +315,10 @@ def orthogonalize_grads_(parameters, steps: int = 5, *, coefficients=T.ORTHOGONA
     one is, whatever it stands for: the heads' weights of a ``QKNorm``, a bias table
     and an embedding are 2-D as well, so hand over the model, or the matrices alone
     (a weight or table as a module above made it is warned of).
-    Parameters of other dimensions or without a gradient stay as they are.  Captured into a graph, it keeps the gradients' addresses, as
-    clip_grad_norm_ does.  To orthogonalise running means of gradients, hand
-    those to ``triattn.triattn_orthogonalize``."""
+    Parameters of other dimensions or without a gradient stay as they are.  Captured
+    into a graph, it keeps the gradients' addresses, as clip_grad_norm_ does.  To
+    orthogonalise running means of gradients, hand those to
+    ``triattn.triattn_orthogonalize``."""
     if isinstance(parameters, torch.nn.Module):
         parameters = matrix_parameters(parameters)
     parameters = [parameters] if isinstance(parameters, torch.Tensor) else parameters
